@@ -13,4 +13,8 @@ from .ops import (  # noqa: F401
     validate, layout_positions, step_counts, work_items, check_device_status,
     test_wait_timeout, profile_events, profile_split_event, last_error, version,
 )
+from .heads import (  # noqa: F401
+    PagedCache, Rope, kv_cache_append, make_cache, make_rope, paged_attn_decode,
+    paged_workspace_bytes, qk_norm_rope_bwd, qk_norm_rope_fwd,
+)
 from .autograd import RingSelfAttention, ring_attention, shard, unshard  # noqa: F401,E402

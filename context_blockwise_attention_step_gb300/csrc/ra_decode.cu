@@ -1,0 +1,559 @@
+// ra_decode.cu — attention of one new token of every sequence over a paged cache.
+//
+// The visible keys of all (sequence, K/V head) pairs are cut into units of 64 keys and the
+// units, in order, are dealt out evenly to the CTAs: CTA i takes the units [N*i/G, N*(i+1)/G).
+// So every SM gets the same share of the cache whatever the lengths, one long sequence as well
+// as a ragged batch, and the host need not know the lengths. A CTA whose share covers a pair
+// whole writes its result; else it writes its part of the pair (running max m, denominator l,
+// unnormalised sum) to the workspace, at most two parts (the first and the last pair of its
+// share), and a second kernel joins the parts of each pair in the order of the CTAs:
+//
+//   M = max m_i,  l = sum 2^(m_i - M) l_i,  out = sum 2^(m_i - M) o_i / l,
+//   lse = (M + log2 l) ln 2
+//
+// which is the log-sum-exp merge of the ring's blocks (nanotron how-to page, "Numerically-
+// Stable Output Fusion") on unnormalised parts. m counts in units of log2: scores are scaled
+// by scale * log2(e).
+//
+// The keys a query sees: with a window, of the n = seq_lens[b] keys the first
+// min(sinks, n - window) and the last min(window, n); without one all n. Both runs are read as
+// one list of `vis` keys: list index i is key i for i < head, else i + skip.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+#include "ra_internal.h"
+#include "ra_ptx.cuh"
+
+namespace ra {
+
+static __device__ unsigned int g_status_decode;
+
+namespace {
+
+constexpr int kUnit = 64;       // keys of a unit
+constexpr int kMaxCtas = 304;   // two on each of 152 SMs
+constexpr int kThreads = 128;
+constexpr int kJoinThreads = 256;
+
+struct DecodeArgs {
+  const void* q;
+  const void* k_pages;
+  const void* v_pages;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  int64_t table_stride, page_stride, slot_stride, head_stride;
+  int32_t n_seqs, max_pages, page_size, n_pages;
+  int32_t hq, hkv, group, dh;
+  int32_t blocks_per_kv;  // blocks of query heads of one K/V head
+  int32_t block_heads;    // query heads of a block (the last block may have fewer)
+  int32_t window, sinks;
+  float scale_log2;
+  float* parts;  // [CTA][2] parts of block_heads * (dh + 2) floats
+  void* out;
+  float* lse;
+};
+
+struct Visible {
+  int vis, head, skip;  // keys seen; of these the first `head` are keys 0.. , the rest skip + i
+};
+
+__device__ __forceinline__ Visible visible(const DecodeArgs& A, int b, bool flag) {
+  int n = A.seq_lens[b];
+  const int64_t cap = static_cast<int64_t>(A.max_pages) * A.page_size;
+  if (n < 0 || n > cap) {
+    if (flag) atomicOr(&g_status_decode, 1u);
+    n = n < 0 ? 0 : static_cast<int>(cap);
+  }
+  Visible v;
+  v.vis = n;
+  v.head = n;
+  v.skip = 0;
+  if (A.window > 0 && n > A.window) {
+    v.head = min(A.sinks, n - A.window);
+    v.skip = n - A.window - v.head;
+    v.vis = A.window + v.head;
+  }
+  return v;
+}
+
+__device__ __forceinline__ int units_of(const DecodeArgs& A, int b) {
+  return (visible(A, b, false).vis + kUnit - 1) / kUnit;
+}
+
+// Row (token) of key list index i of sequence b: element offset of its K/V head 0.
+__device__ __forceinline__ int64_t key_row(const DecodeArgs& A, int b, const Visible& v, int i) {
+  const int key = i < v.head ? i : i + v.skip;
+  const int page = key / A.page_size;
+  int at = A.block_table[b * A.table_stride + page];
+  if (at < 0 || at >= A.n_pages) {
+    atomicOr(&g_status_decode, 1u);
+    at = 0;
+  }
+  return at * A.page_stride + static_cast<int64_t>(key - page * A.page_size) * A.slot_stride;
+}
+
+__device__ __forceinline__ int64_t block_sum(int64_t x, int64_t* smem) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  if ((threadIdx.x & 31) == 0) smem[threadIdx.x >> 5] = x;
+  __syncthreads();
+  int64_t s = 0;
+  for (int w = 0; w < static_cast<int>(blockDim.x) / 32; ++w) s += smem[w];
+  __syncthreads();
+  return s;
+}
+
+// Units before sequence b and in all, in units per block of query heads and K/V head.
+__device__ __forceinline__ void count_units(const DecodeArgs& A, int b, int64_t* before, int64_t* total,
+                                            int64_t* smem) {
+  int64_t lo = 0, all = 0;
+  for (int i = threadIdx.x; i < A.n_seqs; i += blockDim.x) {
+    const int u = units_of(A, i);
+    all += u;
+    if (i < b) lo += u;
+  }
+  *before = block_sum(lo, smem);
+  *total = block_sum(all, smem);
+}
+
+// CTAs that get work, and the first unit of CTA i.
+__device__ __forceinline__ int active_ctas(int64_t units, int ctas) {
+  return units < ctas ? static_cast<int>(units) : ctas;
+}
+__device__ __forceinline__ int64_t first_unit(int64_t units, int ctas, int i) { return units * i / ctas; }
+// The CTA that has unit u: the largest i with first_unit(i) <= u.
+__device__ __forceinline__ int cta_of(int64_t units, int ctas, int64_t u) {
+  int i = static_cast<int>(((u + 1) * ctas - 1) / units);
+  return i;
+}
+
+// A walk over the pieces of a CTA's share: (sequence, block of query heads) and a range of its
+// units. `u` is the next unit; the sequence is found once and then stepped.
+struct Share {
+  int64_t u, end;       // units of the share left
+  int64_t base;         // first unit of the current pair
+  int b, pair, units;   // sequence, pair within it (hk * blocks_per_kv + block), its units
+};
+
+// Sets up the share of CTA blockIdx.x of gridDim.x; false if it is empty. `scan`: kThreads + 1.
+__device__ __forceinline__ bool share_begin(const DecodeArgs& A, Share& S, int64_t* scan, int64_t* total,
+                                            int* ctas) {
+  const int tid = threadIdx.x;
+  const int per = A.hkv * A.blocks_per_kv;
+  const int chunk = (A.n_seqs + kThreads - 1) / kThreads;
+  const int b0 = min(A.n_seqs, tid * chunk), b1 = min(A.n_seqs, b0 + chunk);
+  int64_t mine = 0;
+  for (int b = b0; b < b1; ++b) mine += units_of(A, b);
+  // inclusive scan over the warp, then over the warps
+  int64_t x = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if ((tid & 31) >= o) x += y;
+  }
+  if ((tid & 31) == 31) scan[tid >> 5] = x;
+  __syncthreads();
+  int64_t before = 0, sum = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < tid >> 5) before += scan[w];
+    sum += scan[w];
+  }
+  before += x - mine;  // units (per pair) before this thread's sequences
+  const int64_t units = sum * per;
+  *total = units;
+  *ctas = active_ctas(units, gridDim.x);
+  __syncthreads();
+  if (static_cast<int>(blockIdx.x) >= *ctas) return false;
+  S.u = first_unit(units, *ctas, blockIdx.x);
+  S.end = first_unit(units, *ctas, blockIdx.x + 1);
+  // the thread whose sequences hold unit S.u finds the pair
+  if (S.u >= before * per && S.u < (before + mine) * per) {
+    int64_t base = before * per;
+    int b = b0, n = units_of(A, b);
+    while (S.u >= base + static_cast<int64_t>(n) * per) {
+      base += static_cast<int64_t>(n) * per;
+      n = units_of(A, ++b);
+    }
+    const int pair = static_cast<int>((S.u - base) / n);
+    scan[0] = base + static_cast<int64_t>(pair) * n;
+    scan[1] = b;
+    scan[2] = pair;
+    scan[3] = n;
+  }
+  __syncthreads();
+  S.base = scan[0];
+  S.b = static_cast<int>(scan[1]);
+  S.pair = static_cast<int>(scan[2]);
+  S.units = static_cast<int>(scan[3]);
+  return true;
+}
+
+// To the next pair with keys (the caller has checked that units are left).
+__device__ __forceinline__ void share_next(const DecodeArgs& A, Share& S) {
+  S.base += S.units;
+  S.u = S.base;
+  if (++S.pair == A.hkv * A.blocks_per_kv) {
+    S.pair = 0;
+    do {
+      S.units = units_of(A, ++S.b);
+    } while (S.units == 0);
+  }
+}
+
+__device__ __forceinline__ float* part_of(const DecodeArgs& A, int cta, int which) {
+  return A.parts + (static_cast<int64_t>(cta) * 2 + which) * A.block_heads * (A.dh + 2);
+}
+
+// ---------------------------------------------------------------- CUDA cores, any head size
+// N sums over the 32 lanes at once: every halving step adds the partner's half and keeps half
+// of the values, so N values cost N - 1 shuffles and 5 - log2(N) more. Lane l ends up with
+// value l / (32 / N).
+template <int N>
+__device__ __forceinline__ float lane_sums(float (&x)[N], int lane) {
+#pragma unroll
+  for (int n = N, o = 16; o > 0; o >>= 1) {
+    if (n > 1) {
+      n >>= 1;
+      const bool hi = (lane & o) != 0;
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        if (i < n) {
+          const float send = hi ? x[i] : x[i + n];
+          const float keep = hi ? x[i + n] : x[i];
+          x[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        }
+      }
+    } else {
+      x[0] += __shfl_xor_sync(0xffffffffu, x[0], o);
+    }
+  }
+  return x[0];
+}
+
+template <typename T> __device__ __forceinline__ float ldv(const T* p);
+template <> __device__ __forceinline__ float ldv<float>(const float* p) { return *p; }
+template <> __device__ __forceinline__ float ldv<__nv_bfloat16>(const __nv_bfloat16* p) {
+  return __bfloat162float(*p);
+}
+template <typename T> __device__ __forceinline__ void stv(T* p, float v);
+template <> __device__ __forceinline__ void stv<float>(float* p, float v) { *p = v; }
+template <> __device__ __forceinline__ void stv<__nv_bfloat16>(__nv_bfloat16* p, float v) {
+  *p = __float2bfloat16_rn(v);
+}
+
+// 1 / l; a query whose every score is -inf has l = 0 and gets out = 0, lse = -inf.
+__device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
+
+__device__ __forceinline__ void store_lse(const DecodeArgs& A, int b, int h, float m, float l) {
+  A.lse[static_cast<int64_t>(b) * A.hq + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+}
+
+// Four warps, each 16 keys of a unit, four keys at a time; lane l holds elements l, l + 32, ...
+// of q, of the keys and of the sums, for HB query heads.
+template <typename T, int HB>
+__global__ void __launch_bounds__(kThreads) decode_simt(const __grid_constant__ DecodeArgs A) {
+  constexpr int NI = 4;  // elements per lane: head_dim <= 128
+  __shared__ int64_t scan[kThreads / 32 < 4 ? 4 : kThreads / 32];
+  __shared__ float sm_m[4][HB], sm_l[4][HB], sm_o[4][HB][128];
+  Share S;
+  int64_t total;
+  int ctas;
+  if (!share_begin(A, S, scan, &total, &ctas)) return;
+  const int64_t share0 = S.u;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, dh = A.dh;
+  const T* kp = static_cast<const T*>(A.k_pages);
+  const T* vp = static_cast<const T*>(A.v_pages);
+  for (;;) {
+    const int hk = S.pair / A.blocks_per_kv, blk = S.pair % A.blocks_per_kv;
+    const int g0 = blk * HB, heads = min(HB, A.group - g0), h0 = hk * A.group + g0;
+    const Visible vis = visible(A, S.b, true);
+    const int u0 = static_cast<int>(S.u - S.base);
+    const int u1 = static_cast<int>(min(static_cast<int64_t>(S.units), S.end - S.base));
+    float qr[HB][NI], o[HB][NI], m[HB], l[HB];
+#pragma unroll
+    for (int h = 0; h < HB; ++h) {
+      m[h] = -INFINITY;
+      l[h] = 0.f;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int d = lane + 32 * i;
+        o[h][i] = 0.f;
+        qr[h][i] = h < heads && d < dh
+                       ? ldv<T>(static_cast<const T*>(A.q) + (static_cast<int64_t>(S.b) * A.hq + h0 + h) * dh + d)
+                       : 0.f;
+      }
+    }
+    for (int u = u0; u < u1; ++u) {
+      for (int t = 0; t < 4; ++t) {
+        const int key0 = u * kUnit + warp * 16 + t * 4;
+        if (key0 >= vis.vis) break;
+        int64_t row = 0;
+        if (lane < 4) row = key_row(A, S.b, vis, min(key0 + lane, vis.vis - 1)) + hk * A.head_stride;
+        float kr[4][NI], vr[4][NI];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int64_t at = __shfl_sync(0xffffffffu, row, j);
+#pragma unroll
+          for (int i = 0; i < NI; ++i) {
+            const int d = lane + 32 * i;
+            kr[j][i] = d < dh ? ldv<T>(kp + at + d) : 0.f;
+            vr[j][i] = d < dh ? ldv<T>(vp + at + d) : 0.f;
+          }
+        }
+        float s[4 * HB];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int h = 0; h < HB; ++h) {
+            float x = 0.f;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) x += qr[h][i] * kr[j][i];
+            s[j * HB + h] = x;
+          }
+        const float mine = lane_sums<4 * HB>(s, lane) * A.scale_log2;
+#pragma unroll
+        for (int h = 0; h < HB; ++h) {
+          float x[4], mx = m[h];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            x[j] = __shfl_sync(0xffffffffu, mine, (j * HB + h) * (32 / (4 * HB)));
+            if (key0 + j >= vis.vis) x[j] = -INFINITY;
+            mx = fmaxf(mx, x[j]);
+          }
+          const float ref = mx == -INFINITY ? 0.f : mx;
+          const float alpha = exp2f(m[h] - ref);
+          m[h] = mx;
+          l[h] *= alpha;
+#pragma unroll
+          for (int i = 0; i < NI; ++i) o[h][i] *= alpha;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float p = exp2f(x[j] - ref);
+            l[h] += p;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) o[h][i] += key0 + j < vis.vis ? p * vr[j][i] : 0.f;
+          }
+        }
+      }
+    }
+    // the four warps' states into one
+#pragma unroll
+    for (int h = 0; h < HB; ++h) {
+      if (lane == 0) {
+        sm_m[warp][h] = m[h];
+        sm_l[warp][h] = l[h];
+      }
+#pragma unroll
+      for (int i = 0; i < NI; ++i) sm_o[warp][h][lane + 32 * i] = o[h][i];
+    }
+    __syncthreads();
+    const bool whole = u0 == 0 && u1 == S.units;
+    float* part = part_of(A, blockIdx.x, S.u == share0 ? 0 : 1);
+    for (int h = warp; h < heads; h += 4) {
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) M = fmaxf(M, sm_m[w][h]);
+      const float ref = M == -INFINITY ? 0.f : M;
+      float f[4], L = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        f[w] = exp2f(sm_m[w][h] - ref);
+        L += f[w] * sm_l[w][h];
+      }
+      const float inv = whole ? inverse(L) : 1.f;
+      for (int d = lane; d < dh; d += 32) {
+        float x = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) x += f[w] * sm_o[w][h][d];
+        if (whole)
+          stv<T>(static_cast<T*>(A.out) + (static_cast<int64_t>(S.b) * A.hq + h0 + h) * dh + d, x * inv);
+        else
+          part[h * (dh + 2) + d] = x;
+      }
+      if (lane == 0) {
+        if (whole) {
+          store_lse(A, S.b, h0 + h, M, L);
+        } else {
+          part[h * (dh + 2) + dh] = M;
+          part[h * (dh + 2) + dh + 1] = L;
+        }
+      }
+    }
+    __syncthreads();
+    if (S.base + S.units >= S.end) break;
+    share_next(A, S);
+  }
+}
+
+// ---------------------------------------------------------------- the join
+// One block per (sequence, query head). Its warps take every eighth part, the lanes four
+// elements each; sums over the warps in a fixed order.
+template <typename T>
+__global__ void __launch_bounds__(kJoinThreads) decode_join(const __grid_constant__ DecodeArgs A, int grid) {
+  __shared__ int64_t scan[kJoinThreads / 32];
+  __shared__ float wt[kMaxCtas + 1];
+  __shared__ float red[kJoinThreads / 32];
+  __shared__ float sums[kJoinThreads / 32][128];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, dh = A.dh;
+  const int b = blockIdx.x / A.hq, h = blockIdx.x % A.hq;
+  const int hk = h / A.group, g = h % A.group, blk = g / A.block_heads, row = g % A.block_heads;
+  int64_t before, sum;
+  count_units(A, b, &before, &sum, scan);
+  // (the main kernel does not come by a sequence whose length is negative: reported here)
+  const int n = (visible(A, b, tid == 0).vis + kUnit - 1) / kUnit, per = A.hkv * A.blocks_per_kv;
+  const int64_t total = sum * per;
+  T* out = static_cast<T*>(A.out) + (static_cast<int64_t>(b) * A.hq + h) * dh;
+  if (n == 0) {
+    for (int d = tid; d < dh; d += kJoinThreads) stv<T>(out + d, 0.f);
+    if (tid == 0) A.lse[static_cast<int64_t>(b) * A.hq + h] = -INFINITY;
+    return;
+  }
+  const int ctas = active_ctas(total, grid);
+  const int64_t u0 = before * per + static_cast<int64_t>(hk * A.blocks_per_kv + blk) * n;
+  const int c0 = cta_of(total, ctas, u0), c1 = cta_of(total, ctas, u0 + n - 1);
+  if (c0 == c1) return;  // one CTA had the whole pair
+  const int parts = c1 - c0 + 1;
+  auto part = [&](int i) {  // the pair is the first of a CTA's share, or its last
+    return part_of(A, c0 + i, u0 <= first_unit(total, ctas, c0 + i) ? 0 : 1) + row * (dh + 2);
+  };
+  float mx = -INFINITY;
+  for (int i = tid; i < parts; i += kJoinThreads) mx = fmaxf(mx, wt[i] = part(i)[dh]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  if (lane == 0) red[warp] = mx;
+  __syncthreads();
+  for (int w = 0; w < kJoinThreads / 32; ++w) mx = fmaxf(mx, red[w]);
+  __syncthreads();
+  const float ref = mx == -INFINITY ? 0.f : mx;
+  float l = 0.f;
+  for (int i = tid; i < parts; i += kJoinThreads) {
+    wt[i] = exp2f(wt[i] - ref);
+    l += wt[i] * part(i)[dh + 1];
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if (lane == 0) red[warp] = l;
+  __syncthreads();
+  l = 0.f;
+  for (int w = 0; w < kJoinThreads / 32; ++w) l += red[w];
+  float x[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int i = warp; i < parts; i += kJoinThreads / 32) {
+    const float* p = part(i);
+    const float f = wt[i];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (lane + 32 * e < dh) x[e] += f * p[lane + 32 * e];
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) sums[warp][lane + 32 * e] = x[e];
+  __syncthreads();
+  for (int d = tid; d < dh; d += kJoinThreads) {
+    float s = 0.f;
+    for (int w = 0; w < kJoinThreads / 32; ++w) s += sums[w][d];
+    stv<T>(out + d, s * inverse(l));
+  }
+  if (tid == 0) store_lse(A, b, h, mx, l);
+}
+
+// Query heads that share one read of a K/V head.
+int heads_of_block(int group) { return group >= 8 ? 8 : group >= 4 ? 4 : group >= 2 ? 2 : 1; }
+
+template <typename T>
+cudaError_t launch(DecodeArgs& A, cudaStream_t st) {
+  int dev = 0, n_sm = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const int grid = 2 * n_sm < kMaxCtas ? 2 * n_sm : kMaxCtas;
+  switch (A.block_heads) {
+    case 1: decode_simt<T, 1><<<grid, kThreads, 0, st>>>(A); break;
+    case 2: decode_simt<T, 2><<<grid, kThreads, 0, st>>>(A); break;
+    case 4: decode_simt<T, 4><<<grid, kThreads, 0, st>>>(A); break;
+    default: decode_simt<T, 8><<<grid, kThreads, 0, st>>>(A); break;
+  }
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  decode_join<T><<<A.n_seqs * A.hq, kJoinThreads, 0, st>>>(A, grid);
+  return cudaGetLastError();
+}
+
+size_t workspace_of(const ra_paged_cache* c, int hq) {
+  const size_t part = heads_of_block(hq / c->hkv) * (c->head_dim + 2) * sizeof(float);
+  return (2 * kMaxCtas * part + 255) & ~size_t(255);
+}
+
+int check_heads(const ra_paged_cache* c, int hq) {
+  if (hq < 1 || hq % c->hkv)
+    return record_error(RA_ERR_UNSUPPORTED, "hq (%d) must be a positive multiple of hkv (%d)", hq, c->hkv);
+  if (static_cast<int64_t>(c->n_seqs) * hq >= (int64_t(1) << 31))
+    return record_error(RA_ERR_UNSUPPORTED, "sequences x query heads must stay below 2^31");
+  return RA_OK;
+}
+
+}  // namespace
+
+cudaError_t decode_status(unsigned int* value, bool reset) {
+  cudaError_t e = cudaMemcpyFromSymbol(value, g_status_decode, sizeof(unsigned int));
+  if (e == cudaSuccess && reset) {
+    const unsigned int zero = 0;
+    e = cudaMemcpyToSymbol(g_status_decode, &zero, sizeof(unsigned int));
+  }
+  return e;
+}
+
+}  // namespace ra
+
+using namespace ra;
+
+extern "C" size_t ra_paged_workspace_bytes(const ra_paged_cache* c, int hq) {
+  if (check_cache(c) != RA_OK || check_heads(c, hq) != RA_OK) return 0;
+  return workspace_of(c, hq);
+}
+
+extern "C" int ra_paged_attn_decode(const ra_paged_cache* c, int hq, float scale, int window, int sinks,
+                                    const void* q, const int32_t* seq_lens, void* out, float* lse,
+                                    void* workspace, size_t workspace_bytes, void* stream) {
+  if (int e = check_cache(c)) return e;
+  if (int e = check_heads(c, hq)) return e;
+  if (c->n_seqs > 0 && (!q || !seq_lens || !out || !lse)) return record_error(RA_ERR_INVALID_ARG, "null tensor pointer");
+  if (std::isnan(scale) || std::isinf(scale)) return record_error(RA_ERR_INVALID_ARG, "scale is not finite");
+  if (window < 0 || sinks < 0) return record_error(RA_ERR_INVALID_ARG, "window and sinks must be >= 0");
+  if (workspace_bytes < workspace_of(c, hq))
+    return record_error(RA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes,
+                        workspace_of(c, hq));
+  if (workspace == nullptr || reinterpret_cast<uintptr_t>(workspace) % 256)
+    return record_error(RA_ERR_INVALID_ARG, "workspace must be a 256-byte aligned device pointer");
+  if (c->n_seqs == 0) return record_error(RA_OK, "%s", "");
+  DecodeArgs A;
+  A.q = q;
+  A.k_pages = c->k_pages;
+  A.v_pages = c->v_pages;
+  A.block_table = c->block_table;
+  A.seq_lens = seq_lens;
+  A.table_stride = c->table_stride;
+  A.page_stride = c->page_stride;
+  A.slot_stride = c->slot_stride;
+  A.head_stride = c->head_stride;
+  A.n_seqs = c->n_seqs;
+  A.max_pages = c->max_pages;
+  A.page_size = c->page_size;
+  A.n_pages = c->n_pages;
+  A.hq = hq;
+  A.hkv = c->hkv;
+  A.group = hq / c->hkv;
+  A.dh = c->head_dim;
+  A.block_heads = heads_of_block(A.group);
+  A.blocks_per_kv = (A.group + A.block_heads - 1) / A.block_heads;
+  A.window = window;
+  A.sinks = sinks;
+  A.scale_log2 = (scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(c->head_dim))) * 1.4426950408889634f;
+  A.parts = static_cast<float*>(workspace);
+  A.out = out;
+  A.lse = lse;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = c->dtype == RA_F32 ? launch<float>(A, st) : launch<__nv_bfloat16>(A, st);
+  if (e != cudaSuccess) return record_error(RA_ERR_CUDA, "decode attention launch: %s", cudaGetErrorString(e));
+  return record_error(RA_OK, "%s", "");
+}

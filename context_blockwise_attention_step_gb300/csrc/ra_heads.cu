@@ -1,0 +1,608 @@
+// ra_heads.cu — per-head norm of queries and keys with the rotation by position in the same
+// pass (forward and backward over a ring problem's rows), and the append of new tokens to a
+// paged cache, which does the same on its way there.
+//
+//   n = x * r,  r = rsqrt(mean(x^2) + eps);   y = R(pos) (n * w)
+//   backward: g = R(pos)^T dy;  dw = sum g * n;  h = g * w;  dx = r * (h - n * mean(h * n))
+//
+// Angles: pair i turns by pos * inv_freq[i]. A float product would lose the angle at far
+// positions (at 2^17 the spacing of floats near pos * 1 rad is 2^-7 rad), so inv_freq / 2pi is
+// kept as a 64-bit fraction of a turn: its product with the position, modulo 2^64, is the
+// angle within the turn, and the top 32 bits go to sincospif.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+#include "ra_internal.h"
+#include "ra_layout.h"
+
+namespace ra {
+
+static __device__ unsigned int g_status_append;
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxPerLane = 4;  // head_dim <= 128
+
+// Rows of a ring problem, in natural order of the sequences (unlike the launch plans' table,
+// which is sorted by length).
+struct RingRows {
+  int32_t layout, D, n_seqs;
+  int32_t seqlen;                     // batch mode: S; varlen mode: 0
+  int32_t shard_rows;                 // varlen mode: rows of one rank's buffer (T / D)
+  int32_t cu_local[RA_MAX_SEQS + 1];  // varlen mode: cu_seqlens / D
+};
+
+// Rows of new tokens of the sequences of a paged cache.
+struct CacheRows {
+  const int32_t* seq_lens;
+  const int32_t* cu_new;  // null: row b is the one new token of sequence b
+  const int32_t* block_table;
+  int64_t table_stride, page_stride, slot_stride, head_stride;
+  int32_t n_seqs, max_pages, page_size, n_pages;
+};
+
+// One token: its position, and where its k and v go.
+struct Token {
+  int64_t pos;
+  int64_t kv;        // element offset of head 0 in k_out / v_out
+  bool absent;       // a row that belongs to no sequence: nothing is written
+  bool idle;         // q_out = 0, no k and v
+};
+
+__device__ __forceinline__ Token locate(const RingRows& R, int row, int64_t kv_row) {
+  Token t;
+  t.absent = t.idle = false;
+  t.kv = static_cast<int64_t>(row) * kv_row;
+  if (R.seqlen > 0) {
+    const int x = row % R.seqlen, L = R.seqlen / R.D;
+    t.pos = layout_pos(R.layout, R.D, L, x / L, x % L);
+  } else {
+    const int r = row / R.shard_rows, x = row % R.shard_rows;
+    int lo = 0, hi = R.n_seqs - 1;  // the last sequence that starts at or before x
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (R.cu_local[mid] <= x) lo = mid; else hi = mid - 1;
+    }
+    const int a0 = R.cu_local[lo];
+    t.pos = layout_pos(R.layout, R.D, R.cu_local[lo + 1] - a0, r, x - a0);
+  }
+  return t;
+}
+
+__device__ __forceinline__ Token locate(const CacheRows& R, int row, int64_t) {
+  Token t;
+  t.kv = 0;
+  t.pos = 0;
+  t.absent = t.idle = false;
+  int b = row;
+  int64_t behind = 0;  // tokens of the sequence after this one
+  if (R.cu_new != nullptr) {
+    if (row < R.cu_new[0] || row >= R.cu_new[R.n_seqs]) {
+      t.absent = true;
+      return t;
+    }
+    int lo = 0, hi = R.n_seqs - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (R.cu_new[mid] <= row) lo = mid; else hi = mid - 1;
+    }
+    b = lo;
+    behind = static_cast<int64_t>(R.cu_new[b + 1]) - 1 - row;
+  }
+  const int len = R.seq_lens[b];
+  t.pos = static_cast<int64_t>(len) - 1 - behind;
+  if (len == 0 && R.cu_new == nullptr) {
+    t.idle = true;
+    return t;
+  }
+  const int64_t page = t.pos / R.page_size;
+  int64_t at = -1;
+  if (t.pos >= 0 && page < R.max_pages) at = R.block_table[b * R.table_stride + page];
+  if (at < 0 || at >= R.n_pages) {
+    t.idle = true;
+    atomicOr(&g_status_append, 1u);
+    return t;
+  }
+  t.kv = at * R.page_stride + (t.pos - page * R.page_size) * R.slot_stride;
+  return t;
+}
+
+
+__device__ __forceinline__ float ldf(const float* p) { return *p; }
+__device__ __forceinline__ float ldf(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ void stf(float* p, float v) { *p = v; }
+__device__ __forceinline__ void stf(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+__device__ __forceinline__ float2 cos_sin(uint64_t turns, int64_t pos) {
+  const int32_t t = static_cast<int32_t>((turns * static_cast<uint64_t>(pos)) >> 32);
+  float s, c;
+  sincospif(static_cast<float>(t) * 4.656612873077393e-10f, &s, &c);  // half turns: t * 2^-31
+  return make_float2(c, s);
+}
+
+// What every kernel here gets by value.
+struct HeadArgs {
+  ra_rope rope;  // rotary_dim 0: none
+  float eps;
+  int hq, hkv, dh, n_rows;
+  int64_t q_stride, k_stride, v_stride;  // elements between the rows of the inputs
+  int64_t kv_head;                       // elements between the heads of k_out and v_out
+};
+
+// The rotated (sign = 1) or back-rotated (sign = -1) element d of a head whose elements lie in
+// `row` (shared memory).
+__device__ __forceinline__ float rotated(const HeadArgs& A, const float* row, int d, int64_t pos,
+                                         float sign) {
+  const int rd = A.rope.rotary_dim;
+  if (d >= rd) return row[d];
+  int i, other;
+  bool second;
+  if (A.rope.interleaved) {
+    i = d >> 1;
+    second = d & 1;
+    other = d ^ 1;
+  } else {
+    second = d >= rd / 2;
+    i = second ? d - rd / 2 : d;
+    other = second ? d - rd / 2 : d + rd / 2;
+  }
+  const float2 cs = cos_sin(A.rope.turns[i], pos);
+  return row[d] * cs.x + (second ? sign : -sign) * row[other] * cs.y;
+}
+
+// ---------------------------------------------------------------- any head size, one warp a head
+// Lane l holds elements l, l + 32, ... of its head; the row goes through shared memory to reach
+// its rotation partners.
+template <typename T, typename Rows, bool CACHE>
+__global__ void __launch_bounds__(kThreads)
+    heads_fwd_any(const __grid_constant__ HeadArgs A, const __grid_constant__ Rows R,
+                  const T* __restrict__ qw, const T* __restrict__ kw, const T* q, const T* k,
+                  const T* v, T* q_out, T* k_out, T* v_out) {
+  __shared__ float rows[kWarps][128];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, dh = A.dh;
+  float* row = rows[warp];
+  const int per = A.hq + A.hkv * (CACHE ? 2 : 1);
+  const int64_t units = static_cast<int64_t>(A.n_rows) * per;
+  for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + warp; u < units;
+       u += static_cast<int64_t>(gridDim.x) * kWarps) {
+    const int t = static_cast<int>(u / per), h = static_cast<int>(u % per);
+    const Token tok = locate(R, t, A.hkv * static_cast<int64_t>(dh));
+    if (tok.absent) continue;
+    const T* src;
+    T* dst;
+    const T* w = nullptr;
+    bool turn = A.rope.rotary_dim > 0;
+    if (h < A.hq) {
+      src = q + t * A.q_stride + h * dh;
+      dst = q_out + (static_cast<int64_t>(t) * A.hq + h) * dh;
+      w = qw;
+    } else if (h < A.hq + A.hkv) {
+      src = k + t * A.k_stride + (h - A.hq) * dh;
+      dst = k_out + tok.kv + (h - A.hq) * A.kv_head;
+      w = kw;
+    } else {
+      src = v + t * A.v_stride + (h - A.hq - A.hkv) * dh;
+      dst = v_out + tok.kv + (h - A.hq - A.hkv) * A.kv_head;
+      turn = false;
+    }
+    if (tok.idle) {
+      if (h < A.hq)
+        for (int d = lane; d < dh; d += 32) stf(dst + d, 0.f);
+      continue;
+    }
+    float x[kMaxPerLane], ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < kMaxPerLane; ++i) {
+      const int d = lane + 32 * i;
+      x[i] = d < dh ? ldf(src + d) : 0.f;
+      ss += x[i] * x[i];
+    }
+    if (w != nullptr) {
+      const float r = rsqrtf(warp_sum(ss) / dh + A.eps);
+#pragma unroll
+      for (int i = 0; i < kMaxPerLane; ++i) {
+        const int d = lane + 32 * i;
+        if (d < dh) x[i] = x[i] * r * ldf(w + d);
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kMaxPerLane; ++i)
+      if (lane + 32 * i < dh) row[lane + 32 * i] = x[i];
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kMaxPerLane; ++i) {
+      const int d = lane + 32 * i;
+      if (d < dh) stf(dst + d, turn ? rotated(A, row, d, tok.pos, 1.f) : x[i]);
+    }
+  }
+}
+
+// A warp takes all heads of its tokens; the weight gradients of its lanes' elements are summed
+// in registers, over the block's warps in shared memory, and written per block.
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+    heads_bwd_any(const __grid_constant__ HeadArgs A, const __grid_constant__ RingRows R,
+                  const T* __restrict__ qw, const T* __restrict__ kw, const T* __restrict__ q,
+                  const T* __restrict__ k, const T* dq_out, const T* dk_out, T* dq, T* dk,
+                  float* __restrict__ partial) {
+  __shared__ float rows[kWarps][128];
+  __shared__ float sums[kWarps][2][128];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, dh = A.dh;
+  float* row = rows[warp];
+  float acc[2][kMaxPerLane] = {};
+  for (int t = blockIdx.x * kWarps + warp; t < A.n_rows; t += gridDim.x * kWarps) {
+    const Token tok = locate(R, t, 0);
+    for (int which = 0; which < 2; ++which) {
+      const int heads = which ? A.hkv : A.hq;
+      const T* w = which ? kw : qw;
+      for (int h = 0; h < heads; ++h) {
+        const int64_t o = (static_cast<int64_t>(t) * heads + h) * dh;
+        const T* dy = (which ? dk_out : dq_out) + o;
+        T* dx = (which ? dk : dq) + o;
+        __syncwarp();
+        for (int d = lane; d < dh; d += 32) row[d] = ldf(dy + d);
+        __syncwarp();
+        float g[kMaxPerLane];
+#pragma unroll
+        for (int i = 0; i < kMaxPerLane; ++i) {
+          const int d = lane + 32 * i;
+          g[i] = d < dh ? (A.rope.rotary_dim > 0 ? rotated(A, row, d, tok.pos, -1.f) : row[d]) : 0.f;
+        }
+        if (w != nullptr) {
+          const T* src = which ? k + t * A.k_stride + h * dh : q + t * A.q_stride + h * dh;
+          float x[kMaxPerLane], ss = 0.f;
+#pragma unroll
+          for (int i = 0; i < kMaxPerLane; ++i) {
+            const int d = lane + 32 * i;
+            x[i] = d < dh ? ldf(src + d) : 0.f;
+            ss += x[i] * x[i];
+          }
+          const float r = rsqrtf(warp_sum(ss) / dh + A.eps);
+          float hn = 0.f;
+#pragma unroll
+          for (int i = 0; i < kMaxPerLane; ++i) {
+            const int d = lane + 32 * i;
+            x[i] *= r;
+            if (which) acc[1][i] += g[i] * x[i]; else acc[0][i] += g[i] * x[i];
+            g[i] *= d < dh ? ldf(w + d) : 0.f;
+            hn += g[i] * x[i];
+          }
+          const float mean = warp_sum(hn) / dh;
+#pragma unroll
+          for (int i = 0; i < kMaxPerLane; ++i) g[i] = r * (g[i] - x[i] * mean);
+        }
+#pragma unroll
+        for (int i = 0; i < kMaxPerLane; ++i) {
+          const int d = lane + 32 * i;
+          if (d < dh) stf(dx + d, g[i]);
+        }
+      }
+    }
+  }
+  if (qw == nullptr) return;
+#pragma unroll
+  for (int i = 0; i < kMaxPerLane; ++i) {
+    sums[warp][0][lane + 32 * i] = acc[0][i];
+    sums[warp][1][lane + 32 * i] = acc[1][i];
+  }
+  __syncthreads();
+  {
+    const int which = threadIdx.x >> 7, d = threadIdx.x & 127;  // kThreads = 2 * 128
+    float s = 0.f;
+    for (int w = 0; w < kWarps; ++w) s += sums[w][which][d];
+    if (d < dh) partial[(static_cast<int64_t>(blockIdx.x) * 2 + which) * dh + d] = s;
+  }
+}
+
+// Sums the blocks' weight gradients: a block for 32 of the 2*dh columns, a warp-row for every
+// 32nd partial.
+__global__ void __launch_bounds__(1024)
+    weight_grad_sum(const float* __restrict__ partial, int n, int dh, float* __restrict__ dqw,
+                    float* __restrict__ dkw) {
+  __shared__ float s[32][33];
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5, col = blockIdx.x * 32 + x;
+  float sum = 0.f;
+  if (col < 2 * dh)
+    for (int i = y; i < n; i += 32) sum += partial[static_cast<int64_t>(i) * 2 * dh + col];
+  s[y][x] = sum;
+  __syncthreads();
+  sum = warp_sum(s[x][y]);  // column y of this block, summed over the rows
+  const int out = blockIdx.x * 32 + y;
+  if (x == 0 && out < 2 * dh) (out < dh ? dqw[out] : dkw[out - dh]) = sum;
+}
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 1;
+  return n < 1 ? 1 : n;
+}
+
+unsigned blocks_for(int64_t units, int per_block, int most) {
+  int64_t b = (units + per_block - 1) / per_block;
+  return static_cast<unsigned>(b < 1 ? 1 : b > most ? most : b);
+}
+
+int check_rope(const ra_rope* rope, int head_dim) {
+  if (rope == nullptr) return RA_OK;
+  if (rope->rotary_dim < 2 || rope->rotary_dim > RA_MAX_ROTARY_DIM || rope->rotary_dim % 2)
+    return record_error(RA_ERR_INVALID_ARG, "rope: rotary_dim must be even, 2..%d (use ra_rope_init)",
+                        RA_MAX_ROTARY_DIM);
+  if (rope->rotary_dim > head_dim)
+    return record_error(RA_ERR_SHAPE, "rotary_dim %d > head_dim %d", rope->rotary_dim, head_dim);
+  return RA_OK;
+}
+
+int check_norm(const void* qw, const void* kw, float eps) {
+  if ((qw == nullptr) != (kw == nullptr))
+    return record_error(RA_ERR_INVALID_ARG, "pass both weights or neither");
+  if (qw != nullptr && !(eps >= 0.f && std::isfinite(eps)))
+    return record_error(RA_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  return RA_OK;
+}
+
+// The rows of a (validated) problem.
+int rows_of(const ra_problem* p) { return p->batch > 0 ? p->batch * p->seqlen : p->cu_seqlens[p->n_seqs]; }
+
+void fill_rows(const ra_problem* p, RingRows* R) {
+  R->layout = p->layout;
+  R->D = p->D;
+  R->cu_local[0] = 0;
+  if (p->batch > 0) {
+    R->seqlen = p->seqlen;
+    R->shard_rows = 0;
+    R->n_seqs = p->batch;
+  } else {
+    R->seqlen = 0;
+    R->n_seqs = p->n_seqs;
+    for (int i = 0; i <= p->n_seqs; ++i) R->cu_local[i] = p->cu_seqlens[i] / p->D;
+    R->shard_rows = rows_of(p) / p->D;
+  }
+}
+
+void fill_args(HeadArgs* A, const ra_rope* rope, float eps, int hq, int hkv, int dh, int n_rows) {
+  if (rope != nullptr) A->rope = *rope; else A->rope.rotary_dim = 0;
+  A->eps = eps;
+  A->hq = hq;
+  A->hkv = hkv;
+  A->dh = dh;
+  A->n_rows = n_rows;
+  A->kv_head = dh;
+  A->q_stride = A->k_stride = A->v_stride = 0;
+}
+
+template <typename T, typename Rows, bool CACHE>
+cudaError_t launch_fwd(const HeadArgs& A, const Rows& R, const void* qw, const void* kw,
+                       const void* q, const void* k, const void* v, void* q_out, void* k_out,
+                       void* v_out, cudaStream_t st) {
+  const int64_t units = static_cast<int64_t>(A.n_rows) * (A.hq + A.hkv * (CACHE ? 2 : 1));
+  heads_fwd_any<T, Rows, CACHE><<<blocks_for(units, kWarps, 8 * sm_count()), kThreads, 0, st>>>(
+      A, R, static_cast<const T*>(qw), static_cast<const T*>(kw), static_cast<const T*>(q),
+      static_cast<const T*>(k), static_cast<const T*>(v), static_cast<T*>(q_out),
+      static_cast<T*>(k_out), static_cast<T*>(v_out));
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_bwd(const HeadArgs& A, const RingRows& R, const void* qw, const void* kw,
+                       const void* q, const void* k, const void* dq_out, const void* dk_out,
+                       void* dq, void* dk, float* partial, float* dqw, float* dkw, cudaStream_t st) {
+  const unsigned blocks = blocks_for(A.n_rows, kWarps, kHeadBwdBlocks);
+  heads_bwd_any<T><<<blocks, kThreads, 0, st>>>(
+      A, R, static_cast<const T*>(qw), static_cast<const T*>(kw), static_cast<const T*>(q),
+      static_cast<const T*>(k), static_cast<const T*>(dq_out), static_cast<const T*>(dk_out),
+      static_cast<T*>(dq), static_cast<T*>(dk), partial);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || qw == nullptr) return e;
+  weight_grad_sum<<<(2 * A.dh + 31) / 32, 1024, 0, st>>>(partial, blocks, A.dh, dqw, dkw);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t append_status(unsigned int* value, bool reset) {
+  cudaError_t e = cudaMemcpyFromSymbol(value, g_status_append, sizeof(unsigned int));
+  if (e == cudaSuccess && reset) {
+    const unsigned int zero = 0;
+    e = cudaMemcpyToSymbol(g_status_append, &zero, sizeof(unsigned int));
+  }
+  return e;
+}
+
+// Shared with the decode attention. Leaves dtype-specific demands (alignment) to the caller.
+int check_cache(const ra_paged_cache* c) {
+  if (c == nullptr) return record_error(RA_ERR_INVALID_ARG, "cache is NULL");
+  if (c->dtype != RA_F32 && c->dtype != RA_BF16)
+    return record_error(RA_ERR_INVALID_ARG, "bad dtype %d", c->dtype);
+  if (c->hkv < 1 || c->head_dim < 1 || c->page_size < 1 || c->n_pages < 1 || c->n_seqs < 0 ||
+      c->max_pages < 0)
+    return record_error(RA_ERR_INVALID_ARG, "cache: heads, head_dim, page_size and n_pages must be >= 1, "
+                                            "n_seqs and max_pages >= 0");
+  if (c->dtype == RA_BF16 && c->head_dim != 64 && c->head_dim != 128)
+    return record_error(RA_ERR_UNSUPPORTED, "bf16 supports head_dim 64 or 128 (got %d)", c->head_dim);
+  if (c->head_dim > 128)
+    return record_error(RA_ERR_UNSUPPORTED, "f32 supports head_dim <= 128 (got %d)", c->head_dim);
+  if (c->n_seqs > RA_MAX_CACHE_SEQS)
+    return record_error(RA_ERR_UNSUPPORTED, "n_seqs > %d", RA_MAX_CACHE_SEQS);
+  if (static_cast<int64_t>(c->max_pages) * c->page_size >= (int64_t(1) << 31))
+    return record_error(RA_ERR_UNSUPPORTED, "max_pages * page_size must stay below 2^31");
+  if (c->page_stride < 1 || c->slot_stride < 1 || c->head_stride < 1 || c->table_stride < c->max_pages)
+    return record_error(RA_ERR_INVALID_ARG, "cache: strides must be positive, table_stride >= max_pages");
+  if (c->k_pages == nullptr || c->v_pages == nullptr ||
+      (c->block_table == nullptr && c->n_seqs > 0 && c->max_pages > 0))
+    return record_error(RA_ERR_INVALID_ARG, "null cache pointer");
+  return RA_OK;
+}
+
+size_t heads_bwd_workspace(int head_dim) {
+  return static_cast<size_t>(kHeadBwdBlocks) * 2 * head_dim * sizeof(float);
+}
+
+}  // namespace ra
+
+using namespace ra;
+
+extern "C" int ra_rope_init(ra_rope* rope, int rotary_dim, int interleaved, const double* inv_freq) {
+  if (rope == nullptr || inv_freq == nullptr) return record_error(RA_ERR_INVALID_ARG, "null pointer");
+  if (rotary_dim < 2 || rotary_dim > RA_MAX_ROTARY_DIM || rotary_dim % 2)
+    return record_error(RA_ERR_INVALID_ARG, "rotary_dim must be even, 2..%d (got %d)", RA_MAX_ROTARY_DIM,
+                        rotary_dim);
+  rope->rotary_dim = rotary_dim;
+  rope->interleaved = interleaved ? 1 : 0;
+  for (int i = 0; i < RA_MAX_ROTARY_DIM / 2; ++i) rope->turns[i] = 0;
+  for (int i = 0; i < rotary_dim / 2; ++i) {
+    if (!std::isfinite(inv_freq[i])) return record_error(RA_ERR_INVALID_ARG, "inv_freq[%d] is not finite", i);
+    const double t = inv_freq[i] * 0.15915494309189533577;  // 1 / 2pi
+    double f = t - std::floor(t);                           // [0, 1], 1 only by rounding
+    if (f >= 1.0) f = 0.0;
+    rope->turns[i] = static_cast<uint64_t>(f * 18446744073709551616.0);
+  }
+  record_error(RA_OK, "%s", "");
+  return RA_OK;
+}
+
+extern "C" int ra_qk_norm_rope_fwd(const ra_problem* p, const ra_rope* rope, float eps, const void* q,
+                                   int64_t q_row_stride, const void* k, int64_t k_row_stride,
+                                   const void* q_weight, const void* k_weight, void* q_out, void* k_out,
+                                   void* stream) {
+  if (int e = ra_validate(p)) return e;
+  const bool some = rows_of(p) > 0;  // empty tensors may have null pointers
+  if (some && (!q || !k || !q_out || !k_out)) return record_error(RA_ERR_INVALID_ARG, "null tensor pointer");
+  if (int e = check_rope(rope, p->head_dim)) return e;
+  if (int e = check_norm(q_weight, k_weight, eps)) return e;
+  if (rope == nullptr && q_weight == nullptr)
+    return record_error(RA_ERR_INVALID_ARG, "neither weights nor a rotation: nothing to do");
+  const int64_t nq = static_cast<int64_t>(p->hq) * p->head_dim, nk = static_cast<int64_t>(p->hkv) * p->head_dim;
+  if (q_row_stride < nq || k_row_stride < nk)
+    return record_error(RA_ERR_SHAPE, "row strides must be >= heads * head_dim");
+  if (some && ((q == q_out && q_row_stride != nq) || (k == k_out && k_row_stride != nk)))
+    return record_error(RA_ERR_INVALID_ARG, "in place wants contiguous rows");
+  if (!some) return record_error(RA_OK, "%s", "");
+  const int n_rows = rows_of(p);
+  RingRows R;
+  HeadArgs A;
+  fill_rows(p, &R);
+  fill_args(&A, rope, eps, p->hq, p->hkv, p->head_dim, n_rows);
+  A.q_stride = q_row_stride;
+  A.k_stride = k_row_stride;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e =
+      p->dtype == RA_F32
+          ? launch_fwd<float, RingRows, false>(A, R, q_weight, k_weight, q, k, nullptr, q_out, k_out, nullptr, st)
+          : launch_fwd<__nv_bfloat16, RingRows, false>(A, R, q_weight, k_weight, q, k, nullptr, q_out, k_out,
+                                                       nullptr, st);
+  if (e != cudaSuccess) return record_error(RA_ERR_CUDA, "norm and rotation launch: %s", cudaGetErrorString(e));
+  return record_error(RA_OK, "%s", "");
+}
+
+extern "C" int ra_qk_norm_rope_bwd(const ra_problem* p, const ra_rope* rope, float eps, const void* dq_out,
+                                   const void* dk_out, const void* q, int64_t q_row_stride, const void* k,
+                                   int64_t k_row_stride, const void* q_weight, const void* k_weight, void* dq,
+                                   void* dk, float* dq_weight, float* dk_weight, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+  if (int e = ra_validate(p)) return e;
+  const bool some = rows_of(p) > 0;  // empty tensors may have null pointers
+  if (some && (!dq_out || !dk_out || !dq || !dk)) return record_error(RA_ERR_INVALID_ARG, "null tensor pointer");
+  if (int e = check_rope(rope, p->head_dim)) return e;
+  if (int e = check_norm(q_weight, k_weight, eps)) return e;
+  if (rope == nullptr && q_weight == nullptr)
+    return record_error(RA_ERR_INVALID_ARG, "neither weights nor a rotation: nothing to do");
+  if (q_weight != nullptr) {
+    if ((some && (!q || !k)) || !dq_weight || !dk_weight) return record_error(RA_ERR_INVALID_ARG, "null tensor pointer");
+    if (q_row_stride < static_cast<int64_t>(p->hq) * p->head_dim ||
+        k_row_stride < static_cast<int64_t>(p->hkv) * p->head_dim)
+      return record_error(RA_ERR_SHAPE, "row strides must be >= heads * head_dim");
+    if (workspace_bytes < heads_bwd_workspace(p->head_dim))
+      return record_error(RA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes,
+                          heads_bwd_workspace(p->head_dim));
+    if (workspace == nullptr || reinterpret_cast<uintptr_t>(workspace) % 256)
+      return record_error(RA_ERR_INVALID_ARG, "workspace must be a 256-byte aligned device pointer");
+  }
+  const int n_rows = rows_of(p);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  if (!some) {
+    if (q_weight != nullptr) {
+      e = cudaMemsetAsync(dq_weight, 0, p->head_dim * sizeof(float), st);
+      if (e == cudaSuccess) e = cudaMemsetAsync(dk_weight, 0, p->head_dim * sizeof(float), st);
+    }
+  } else {
+    RingRows R;
+    HeadArgs A;
+    fill_rows(p, &R);
+    fill_args(&A, rope, eps, p->hq, p->hkv, p->head_dim, n_rows);
+    A.q_stride = q_row_stride;
+    A.k_stride = k_row_stride;
+    float* partial = static_cast<float*>(workspace);
+    e = p->dtype == RA_F32 ? launch_bwd<float>(A, R, q_weight, k_weight, q, k, dq_out, dk_out, dq, dk, partial,
+                                               dq_weight, dk_weight, st)
+                           : launch_bwd<__nv_bfloat16>(A, R, q_weight, k_weight, q, k, dq_out, dk_out, dq, dk,
+                                                       partial, dq_weight, dk_weight, st);
+  }
+  if (e != cudaSuccess)
+    return record_error(RA_ERR_CUDA, "norm and rotation backward launch: %s", cudaGetErrorString(e));
+  return record_error(RA_OK, "%s", "");
+}
+
+extern "C" int ra_kv_cache_append(const ra_paged_cache* c, const ra_rope* rope, float eps, int n_tokens, int hq,
+                                  const void* q, int64_t q_row_stride, const void* k, int64_t k_row_stride,
+                                  const void* v, int64_t v_row_stride, const void* q_weight,
+                                  const void* k_weight, const int32_t* seq_lens, const int32_t* cu_new,
+                                  void* q_out, void* stream) {
+  if (int e = check_cache(c)) return e;
+  if ((q == nullptr) != (q_out == nullptr)) return record_error(RA_ERR_INVALID_ARG, "pass both q and q_out or neither");
+  const bool some = n_tokens > 0 && c->n_seqs > 0;  // empty tensors may have null pointers
+  if (some && (!k || !v || !seq_lens)) return record_error(RA_ERR_INVALID_ARG, "null tensor pointer");
+  if (n_tokens < 0) return record_error(RA_ERR_INVALID_ARG, "n_tokens must be >= 0");
+  if (q != nullptr && (hq < 1 || hq % c->hkv))
+    return record_error(RA_ERR_UNSUPPORTED, "hq (%d) must be a multiple of hkv (%d)", hq, c->hkv);
+  if (cu_new == nullptr && n_tokens != c->n_seqs)
+    return record_error(RA_ERR_SHAPE, "without cu_new there is one token for each of the %d sequences (got %d)",
+                        c->n_seqs, n_tokens);
+  if (int e = check_rope(rope, c->head_dim)) return e;
+  if (int e = check_norm(q_weight, k_weight, eps)) return e;
+  const int heads_q = q != nullptr ? hq : 0;
+  const int64_t nq = static_cast<int64_t>(heads_q) * c->head_dim, nk = static_cast<int64_t>(c->hkv) * c->head_dim;
+  if ((q != nullptr && q_row_stride < nq) || k_row_stride < nk || v_row_stride < nk)
+    return record_error(RA_ERR_SHAPE, "row strides must be >= heads * head_dim");
+  if (q != nullptr && q == q_out && q_row_stride != nq)
+    return record_error(RA_ERR_INVALID_ARG, "in place wants contiguous rows");
+  if (!some) return record_error(RA_OK, "%s", "");
+  CacheRows R;
+  R.seq_lens = seq_lens;
+  R.cu_new = cu_new;
+  R.block_table = c->block_table;
+  R.table_stride = c->table_stride;
+  R.page_stride = c->page_stride;
+  R.slot_stride = c->slot_stride;
+  R.head_stride = c->head_stride;
+  R.n_seqs = c->n_seqs;
+  R.max_pages = c->max_pages;
+  R.page_size = c->page_size;
+  R.n_pages = c->n_pages;
+  HeadArgs A;
+  fill_args(&A, rope, eps, heads_q, c->hkv, c->head_dim, n_tokens);
+  A.q_stride = q_row_stride;
+  A.k_stride = k_row_stride;
+  A.v_stride = v_row_stride;
+  A.kv_head = c->head_stride;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e =
+      c->dtype == RA_F32
+          ? launch_fwd<float, CacheRows, true>(A, R, q_weight, k_weight, q, k, v, q_out, c->k_pages, c->v_pages, st)
+          : launch_fwd<__nv_bfloat16, CacheRows, true>(A, R, q_weight, k_weight, q, k, v, q_out, c->k_pages,
+                                                       c->v_pages, st);
+  if (e != cudaSuccess) return record_error(RA_ERR_CUDA, "append launch: %s", cudaGetErrorString(e));
+  return record_error(RA_OK, "%s", "");
+}

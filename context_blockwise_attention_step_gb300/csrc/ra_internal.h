@@ -55,6 +55,13 @@ cudaError_t launch_shard_tokens(const Plan& P, int direction, const void* src, v
 cudaError_t launch_shard_lse(const Plan& P, int direction, const float* src, float* dst,
                              cudaStream_t st);
 
+// Head norms and the paged cache (ra_heads.cu, ra_decode.cu).
+constexpr int kHeadBwdBlocks = 608;  // most blocks of the head-norm backward (4 on each of 152 SMs)
+size_t heads_bwd_workspace(int head_dim);
+int check_cache(const ra_paged_cache* c);
+cudaError_t append_status(unsigned int* value, bool reset);
+cudaError_t decode_status(unsigned int* value, bool reset);
+
 // Sets the thread's ra_last_error() message (printf format) and returns `code`.
 int record_error(int code, const char* fmt, ...);
 

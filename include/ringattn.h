@@ -60,7 +60,9 @@ typedef enum ra_status {
   RA_ERR_SHAPE = -3,         /* a length not divisible by D (2D for zigzag), bad cu_seqlens */
   RA_ERR_WORKSPACE = -4,     /* workspace smaller than ra_workspace_bytes()               */
   RA_ERR_CUDA = -5,          /* a CUDA call or kernel launch failed                       */
-  RA_ERR_DEVICE_TIMEOUT = -6 /* a kernel gave up a bounded wait (see ra_check_device_status) */
+  RA_ERR_DEVICE_TIMEOUT = -6, /* a kernel gave up a bounded wait (see ra_check_device_status) */
+  RA_ERR_CACHE_INDEX = -7    /* a kernel met a page index, a length or a position outside the
+                                paged cache it was given (see ra_check_device_status)      */
 } ra_status;
 
 typedef enum ra_dtype { RA_F32 = 0, RA_BF16 = 1 } ra_dtype;
@@ -127,7 +129,7 @@ int ra_update_out_and_lse(const ra_problem* p, int rank, float* out, float* lse,
                           void* stream);
 
 /* Bytes of device workspace: which = 0 for ra_ring_attn_fwd (optional there), which = 1
- * for ra_ring_attn_bwd, which = 2 for ra_block_attn_bwd; 0 for which = 0 on the f32 path. Returns 0 for an invalid problem as well;
+ * for ra_ring_attn_bwd, which = 2 for ra_block_attn_bwd, which = 3 for ra_qk_norm_rope_bwd; 0 for which = 0 on the f32 path. Returns 0 for an invalid problem as well;
  * call ra_validate to tell the two apart. */
 size_t ra_workspace_bytes(const ra_problem* p, int which);
 
@@ -187,6 +189,113 @@ int ra_ring_attn_bwd_noalloc(const ra_problem* p, const void* q, const void* k, 
                              const void* out, const float* lse, const void* dout, void* dq,
                              void* dk, void* dv, void* stream);
 
+/* ---- head norms and position rotation ------------------------------------------------ */
+
+#define RA_MAX_ROTARY_DIM 128
+#define RA_MAX_CACHE_SEQS 8192 /* sequences of a paged cache in one call */
+
+/* A rotation by position of the first `rotary_dim` elements of a head: pair i turns by
+ * position * inv_freq[i] radians. The pairs are (i, i + rotary_dim/2), or (2i, 2i + 1) when
+ * interleaved. Filled in by ra_rope_init, passed by value to the kernels. */
+typedef struct ra_rope {
+  int32_t rotary_dim;
+  int32_t interleaved;
+  uint64_t turns[RA_MAX_ROTARY_DIM / 2]; /* turns per position, in units of 2^-64 of a turn: the
+                                            product with a position wraps at whole turns, so an
+                                            angle is exact to 2^-32 of a turn at any position */
+} ra_rope;
+
+/* Fills in `rope` from rotary_dim/2 HOST doubles (radians per position, finite). rotary_dim is
+ * even, 2..RA_MAX_ROTARY_DIM. */
+int ra_rope_init(ra_rope* rope, int rotary_dim, int interleaved, const double* inv_freq);
+
+/* Per-head norm of queries and keys with the rotation in the same pass, before
+ * ra_ring_attn_fwd: for every head x of every token of the problem
+ *   y = R(position) (x * rsqrt(mean(x^2) + eps) * weight)
+ * where the position is the token's global position in its sequence under the problem's
+ * layout (the rows are shard-major). q_weight and k_weight hold head_dim elements of the
+ * problem dtype; both NULL leaves the norm out (eps is then not looked at), rope NULL leaves
+ * the rotation out, one of the two must be there. rope->rotary_dim <= head_dim; the rest of a
+ * head is not rotated. q and k may be views into a wider tensor: q_row_stride and
+ * k_row_stride are the elements from one token to the next (>= heads * head_dim); the heads
+ * of a token are contiguous. q_out and k_out are contiguous; q_out may be q, and k_out k, when
+ * that is contiguous too. */
+int ra_qk_norm_rope_fwd(const ra_problem* p, const ra_rope* rope, float eps, const void* q,
+                        int64_t q_row_stride, const void* k, int64_t k_row_stride,
+                        const void* q_weight, const void* k_weight, void* q_out, void* k_out,
+                        void* stream);
+
+/* Its backward: from the gradients dq_out and dk_out (contiguous) of the outputs and the
+ * INPUTS q and k of the forward, the gradients dq and dk of the inputs (contiguous, problem
+ * dtype; dq may be dq_out, dk may be dk_out) and, in float32, dq_weight and dk_weight
+ * (head_dim elements each, summed over every token and head in a fixed order: run-to-run
+ * bit-identical). Without weights q, k, dq_weight and dk_weight are not used and may be NULL.
+ * The workspace (device, >= ra_workspace_bytes(p, 3), 256-byte aligned) is overwritten. */
+int ra_qk_norm_rope_bwd(const ra_problem* p, const ra_rope* rope, float eps, const void* dq_out,
+                        const void* dk_out, const void* q, int64_t q_row_stride, const void* k,
+                        int64_t k_row_stride, const void* q_weight, const void* k_weight,
+                        void* dq, void* dk, float* dq_weight, float* dk_weight,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- serving: a paged key-value cache and the attention of one new token -------------- */
+
+/* A cache of n_pages pages of page_size tokens; page p, place s, K/V head h starts at element
+ * p*page_stride + s*slot_stride + h*head_stride of k_pages and of v_pages, head_dim elements
+ * contiguous (so [n_pages, page_size, hkv, head_dim], [n_pages, hkv, page_size, head_dim] and
+ * views of them are all fine). Token t of sequence b is in page
+ * block_table[b*table_stride + t / page_size] at place t % page_size. All pointers are DEVICE
+ * pointers; entries of the table beyond a sequence's length are not looked at. An entry
+ * outside [0, n_pages), or a length beyond max_pages * page_size, is never followed: the
+ * kernels record RA_ERR_CACHE_INDEX in the device status and leave out that token (append) or
+ * read page 0 / the cache's part of the sequence in its place (decode, whose result for that
+ * sequence then means nothing). */
+typedef struct ra_paged_cache {
+  int32_t dtype;      /* ra_dtype of the pages, and of the tokens that go with them */
+  int32_t hkv;
+  int32_t head_dim;   /* bf16: 64 or 128; f32: 1..128 */
+  int32_t page_size;  /* >= 1 */
+  int32_t n_pages;    /* >= 1 */
+  int32_t n_seqs;     /* rows of the block table: the sequences of a batch */
+  int32_t max_pages;  /* entries of a row */
+  int64_t table_stride;
+  int64_t page_stride, slot_stride, head_stride; /* elements */
+  void* k_pages;
+  void* v_pages;
+  const int32_t* block_table;
+} ra_paged_cache;
+
+/* Puts new tokens into the cache: k (after norm and rotation, as in ra_qk_norm_rope_fwd) and v
+ * (as it is) go to their places, q (after the same) to q_out. seq_lens [n_seqs] (device) are
+ * the lengths WITH the new tokens, as ra_paged_attn_decode wants them. cu_new NULL: one new
+ * token for each sequence, row b of q, k, v belongs to sequence b (n_tokens = n_seqs); a
+ * sequence of length 0 is idle: nothing is stored for it and its row of q_out is 0. Else
+ * cu_new [n_seqs + 1] (device): rows cu_new[b] .. cu_new[b+1]-1 are the last tokens of
+ * sequence b; rows from cu_new[n_seqs] on are left as they are. No two rows may go to the
+ * same place. q and q_out both NULL: k and v only (hq is then not looked at). Row strides as
+ * above; q_out is contiguous. weights both NULL: no norm; rope NULL: no rotation. */
+int ra_kv_cache_append(const ra_paged_cache* c, const ra_rope* rope, float eps, int n_tokens,
+                       int hq, const void* q, int64_t q_row_stride, const void* k,
+                       int64_t k_row_stride, const void* v, int64_t v_row_stride,
+                       const void* q_weight, const void* k_weight, const int32_t* seq_lens,
+                       const int32_t* cu_new, void* q_out, void* stream);
+
+/* Attention of the last token of every sequence: q and out [n_seqs, hq, head_dim] (contiguous,
+ * cache dtype; hq % hkv == 0), lse [n_seqs, hq] (float32, natural log). The query sees the keys
+ * 0 .. seq_lens[b]-1, and with window > 0 of these only the last `window` and the first
+ * `sinks`. A sequence of length 0 gets out = 0, lse = -inf. scale <= 0 selects
+ * 1/sqrt(head_dim). The keys of the batch are dealt out evenly over the SMs whatever the
+ * lengths, and parts of a sequence are joined by the log-sum-exp merge, in a fixed order
+ * (run-to-run bit-identical). bf16 wants the pages 16-byte aligned with strides that are
+ * multiples of 8 elements. The workspace (device, >= ra_paged_workspace_bytes(c, hq), 256-byte
+ * aligned) is overwritten; nothing in it is kept from call to call, so calls and captured
+ * graphs may share it as long as they do not run at the same time. */
+int ra_paged_attn_decode(const ra_paged_cache* c, int hq, float scale, int window, int sinks,
+                         const void* q, const int32_t* seq_lens, void* out, float* lse,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace of ra_paged_attn_decode; 0 for an invalid cache or hq. */
+size_t ra_paged_workspace_bytes(const ra_paged_cache* c, int hq);
+
 /* Natural order <-> shard-major order of a token tensor (row = one token, `row_bytes`
  * bytes: H*Dh*element size), bit-exact copy. direction 0: natural -> shard-major (shard);
  * 1: shard-major -> natural (unshard). src and dst must not overlap. */
@@ -223,8 +332,9 @@ int ra_work_items(const ra_problem* p, int which, int32_t* items_out, int max_it
 /* ---- status ---- */
 
 /* Synchronises the current device, then reports whether any kernel of this library gave
- * up a bounded wait since the last reset: RA_OK or RA_ERR_DEVICE_TIMEOUT (RA_ERR_CUDA if the
- * synchronisation itself failed). reset != 0 clears the flag. */
+ * up a bounded wait since the last reset, or met an index outside a paged cache: RA_OK,
+ * RA_ERR_DEVICE_TIMEOUT, else RA_ERR_CACHE_INDEX (RA_ERR_CUDA if the synchronisation itself
+ * failed). reset != 0 clears the flags. */
 int ra_check_device_status(int reset);
 
 /* Test hook for the bounded-wait path: launches one CTA that waits, with a limit of
