@@ -15,6 +15,7 @@ from .ops import (  # noqa: F401
 )
 from .heads import (  # noqa: F401
     PagedCache, Rope, kv_cache_append, make_cache, make_rope, paged_attn_decode,
-    paged_workspace_bytes, qk_norm_rope_bwd, qk_norm_rope_fwd,
+    paged_workspace_bytes, qk_norm_rope_bwd, qk_norm_rope_fwd, window_attn_bwd, window_attn_fwd,
+    window_workspace_bytes,
 )
 from .autograd import RingSelfAttention, ring_attention, shard, unshard  # noqa: F401,E402

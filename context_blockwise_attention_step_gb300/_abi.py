@@ -24,6 +24,7 @@ RA_MAX_SEQS = 1024
 RA_NOALLOC_SCRATCH_BYTES = 64 << 20
 RA_MAX_ROTARY_DIM = 128
 RA_MAX_CACHE_SEQS = 8192
+RA_MAX_SINKS = 128
 
 # every symbol include/ringattn.h declares
 EXPORTS = (
@@ -35,6 +36,7 @@ EXPORTS = (
     "ra_version",
     "ra_rope_init", "ra_qk_norm_rope_fwd", "ra_qk_norm_rope_bwd", "ra_kv_cache_append",
     "ra_paged_attn_decode", "ra_paged_workspace_bytes",
+    "ra_window_attn_fwd", "ra_window_attn_bwd", "ra_window_workspace_bytes",
 )
 
 
@@ -134,6 +136,9 @@ def lib() -> ctypes.CDLL:
                                      vp, vp]),
         "ra_paged_attn_decode": (i32, [C, i32, f32, i32, i32, vp, vp, vp, vp, vp, size, vp]),
         "ra_paged_workspace_bytes": (size, [C, i32]),
+        "ra_window_attn_fwd": (i32, [P, i32, i32, vp, vp, vp, vp, vp, vp, size, vp]),
+        "ra_window_attn_bwd": (i32, [P, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, size, vp]),
+        "ra_window_workspace_bytes": (size, [P, i32, i32, i32]),
         "ra_last_error": (ctypes.c_char_p, []),
         "ra_version": (i32, []),
     }

@@ -129,6 +129,7 @@ Plan* make_plan(const ra_problem* p, int which, int step_begin, int step_end, in
   P->kv_shard_only = kv_shard_only;
   P->out_f32 = out_f32;
   P->bwd_accum = 0;
+  P->sink_chunk = 1;
   P->scale = p->scale > 0.f ? p->scale : 1.0f / std::sqrt(static_cast<float>(p->head_dim));
   P->scale_log2 = P->scale * 1.4426950408889634f;
   P->dq_mul = P->scale;
@@ -217,6 +218,31 @@ size_t delta_bytes(const ra_problem* p) {
 // The shared item counters of the K/V-tile pass and of the dq pass (dynamic scheduling),
 // one 256-byte block.
 size_t sched_bytes(const ra_problem* p) { return use_tc(p) ? 256 : 0; }
+
+// The window as the plans carry it: one that reaches over the longest sequence hides nothing,
+// and the ring kernels run as without one.
+int effective_window(const ra_problem* p, int window) {
+  for (int64_t x : lengths_of(p))
+    if (x > window) return window;
+  return 0;
+}
+
+int validate_window(const ra_problem* p, int window, int sinks) {
+  if (int e = validate(p)) return e;
+  if (!p->causal) return fail(RA_ERR_UNSUPPORTED, "a sliding window wants a causal problem");
+  if (window < 1) return fail(RA_ERR_INVALID_ARG, "window must be >= 1 (got %d)", window);
+  if (sinks < 0 || sinks > RA_MAX_SINKS)
+    return fail(RA_ERR_INVALID_ARG, "sinks must be 0..%d (got %d)", RA_MAX_SINKS, sinks);
+  return RA_OK;
+}
+
+// A plan (which as in make_plan) with a window.
+Plan* make_window_plan(const ra_problem* p, int which, int window, int sinks) {
+  Plan* P = make_plan(p, which, 0, p->D, -1, which == 0 && p->dtype == RA_F32);
+  P->window = effective_window(p, window);
+  P->sinks = P->window ? sinks : 0;
+  return P;
+}
 
 size_t dq_acc_bytes(const ra_problem* p) {
   if (!fused_bwd(p)) return 0;
@@ -413,6 +439,50 @@ int ra_block_attn_bwd(const ra_problem* p, int rank, int step, const void* q, co
     e = ra::launch_bwd_simt(*P.p, p->dtype, q, k, v, dout, lse, delta, dq_acc, dk_acc, dv_acc, st);
   }
   return e == cudaSuccess ? ok() : cuda_fail(e, "block backward launch");
+}
+
+size_t ra_window_workspace_bytes(const ra_problem* p, int window, int sinks, int which) {
+  if (validate_window(p, window, sinks) != RA_OK) return 0;
+  if (which == 0) return sched_bytes(p);
+  if (which == 1) return delta_bytes(p) + sched_bytes(p);
+  return 0;
+}
+
+int ra_window_attn_fwd(const ra_problem* p, int window, int sinks, const void* q, const void* k,
+                       const void* v, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                       void* stream) {
+  if (int e = validate_window(p, window, sinks)) return e;
+  if (effective_window(p, window) == 0)
+    return ra_ring_attn_fwd(p, q, k, v, out, lse, workspace, workspace_bytes, stream);
+  if (!q || !k || !v || !out || !lse) return fail(RA_ERR_INVALID_ARG, "null tensor pointer");
+  if (workspace != nullptr && reinterpret_cast<uintptr_t>(workspace) % 256)
+    return fail(RA_ERR_INVALID_ARG, "workspace must be a 256-byte aligned device pointer");
+  PlanHolder P(make_window_plan(p, 0, window, sinks));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = profiled(st, [&] { return ra::launch_fwd_simt(*P.p, p->dtype, q, k, v, out, lse, st); });
+  return e == cudaSuccess ? ok() : cuda_fail(e, "window forward launch");
+}
+
+int ra_window_attn_bwd(const ra_problem* p, int window, int sinks, const void* q, const void* k,
+                       const void* v, const void* out, const float* lse, const void* dout, void* dq,
+                       void* dk, void* dv, void* workspace, size_t workspace_bytes, void* stream) {
+  if (int e = validate_window(p, window, sinks)) return e;
+  if (effective_window(p, window) == 0)
+    return ra_ring_attn_bwd(p, q, k, v, out, lse, dout, dq, dk, dv, workspace, workspace_bytes, stream);
+  if (!q || !k || !v || !out || !lse || !dout || !dq || !dk || !dv)
+    return fail(RA_ERR_INVALID_ARG, "null tensor pointer");
+  const size_t need = ra_window_workspace_bytes(p, window, sinks, 1);
+  if (workspace_bytes < need)
+    return fail(RA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
+  if (workspace == nullptr || reinterpret_cast<uintptr_t>(workspace) % 256)
+    return fail(RA_ERR_INVALID_ARG, "workspace must be a 256-byte aligned device pointer");
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  float* delta = static_cast<float*>(workspace);
+  PlanHolder E(make_window_plan(p, 2, window, sinks));
+  cudaError_t e = ra::launch_bwd_delta(*E.p, p->dtype, out, dout, delta, st);
+  if (e != cudaSuccess) return cuda_fail(e, "backward preprocess launch");
+  e = profiled(st, [&] { return ra::launch_bwd_simt(*E.p, p->dtype, q, k, v, dout, lse, delta, dq, dk, dv, st); });
+  return e == cudaSuccess ? ok() : cuda_fail(e, "window backward launch");
 }
 
 int ra_shard_tokens(const ra_problem* p, int direction, const void* src, void* dst,

@@ -25,6 +25,7 @@ struct SeqDesc {
   int32_t lse_off;      // shard-major lse index of (rank 0, local 0), head 0
   int32_t lse_nat_off;  // natural lse index of the sequence's first token, head 0
   int32_t item_start;   // first work item of this sequence in the launched kernel
+  int32_t sink_start;   // windowed backward: first slot of this sequence in the sink sums
 };
 
 struct Plan {
@@ -40,10 +41,13 @@ struct Plan {
   int32_t out_f32;               // forward output stored as float32 (else problem dtype)
   int32_t bwd_accum;             // backward: add float32 gradients into the outputs
   int32_t bwd_kt_inner;          // backward items: K/V tiles innermost (see decode_bwd)
+  int32_t window, sinks;         // sliding window (0: none); first tokens that stay visible
+  int32_t sink_chunk;            // windowed K/V pass: query tiles of a sink item
   float scale, scale_log2;
   float dq_mul;                  // factor on dS K before it is added to the dq sums
   uint64_t timeout_ns;
   int32_t* work_counter;         // backward K/V pass: shared item counter (null: static stride)
+  float* sink_sums;              // windowed K/V pass: float32 partial dk, dv of the sink rows
   SeqDesc seq[RA_MAX_SEQS];
 };
 
@@ -149,6 +153,142 @@ RA_HD int row_key_count(const Plan& P, int L, int r, int a, int j, int b) {
                            : L - 1;
   int c = lim + 1 - b * kKvTileRows;
   return c < 0 ? 0 : (c > kKvTileRows ? kKvTileRows : c);
+}
+
+// ---- sliding window --------------------------------------------------------------------
+// A query at position p sees the keys at positions <= p that are > p - window or < sinks. In
+// every layout both conditions cut a run of local indices out of a shard: the sinks are a
+// prefix of it, the window a run [first, limit]. At most kMaxSinks sinks, so that the sinks of
+// a shard lie in its first tile.
+constexpr int kMaxSinks = 128;
+
+// Local rows of shard j that are sinks (a prefix), and the shards 0 .. sink_shards - 1 that
+// have any.
+RA_HD int sink_rows(const Plan& P, int L, int j) {
+  return P.sinks > 0 ? key_limit(P.layout, P.D, L, j, P.sinks - 1) + 1 : 0;
+}
+RA_HD int sink_shards(const Plan& P, int L) {
+  if (P.layout == kStripe) return P.sinks < P.D ? P.sinks : P.D;
+  const int c = P.layout == kZigzag ? L >> 1 : L;
+  const int n = ceil_div(P.sinks, c);
+  return n < P.D ? n : P.D;
+}
+
+// Tiles of one shard: tile 0 if `sink`, then the runs s0 .. s0+n0-1 and s1 .. s1+n1-1,
+// ascending and disjoint.
+struct TileSet {
+  int sink, s0, n0, s1, n1;
+};
+RA_HD int tile_count(const TileSet& t) { return t.sink + t.n0 + t.n1; }
+RA_HD int tile_at(const TileSet& t, int i) {
+  if (i < t.sink) return 0;
+  i -= t.sink;
+  return i < t.n0 ? t.s0 + i : t.s1 + i - t.n0;
+}
+// Adds the tiles of local rows lo .. hi (which follow those added before).
+RA_HD void add_tiles(TileSet& t, int lo, int hi, int tile_rows) {
+  if (hi < lo) return;
+  int s = lo / tile_rows;
+  const int e = hi / tile_rows;
+  if (t.n0 == 0) {
+    t.s0 = s;
+    t.n0 = e - s + 1;
+    return;
+  }
+  if (s < t.s0 + t.n0) s = t.s0 + t.n0;
+  if (s > e) return;
+  if (s == t.s0 + t.n0) {
+    t.n0 += e - s + 1;
+  } else {
+    t.s1 = s;
+    t.n1 = e - s + 1;
+  }
+}
+// Rows x0 .. x1 of a zigzag shard that lie on both sides of its two chunks have positions far
+// apart: they are looked at as two runs, split at the second chunk.
+RA_HD bool straddles(const Plan& P, int L, int x0, int x1) {
+  return P.layout == kZigzag && x0 < (L >> 1) && x1 >= (L >> 1);
+}
+
+// K/V tiles of shard j that some of the query rows a0 .. a1 of rank r sees.
+RA_HD TileSet window_kv_tiles(const Plan& P, int L, int r, int j, int a0, int a1) {
+  TileSet t = {0, 0, 0, 0, 0};
+  const int limit = key_limit(P.layout, P.D, L, j, layout_pos(P.layout, P.D, L, r, a1));
+  if (limit < 0) return t;
+  int from = a0;
+  if (straddles(P, L, a0, a1)) {
+    from = L >> 1;
+    add_tiles(t, first_query(P.layout, P.D, L, j, layout_pos(P.layout, P.D, L, r, a0) - P.window + 1),
+              key_limit(P.layout, P.D, L, j, layout_pos(P.layout, P.D, L, r, from - 1)), kKvTileRows);
+  }
+  add_tiles(t, first_query(P.layout, P.D, L, j, layout_pos(P.layout, P.D, L, r, from) - P.window + 1),
+            limit, kKvTileRows);
+  t.sink = sink_rows(P, L, j) > 0 && (t.n0 == 0 || t.s0 > 0) ? 1 : 0;
+  return t;
+}
+
+// Query tiles of rank r that see some of the rows b0 .. b1 of K/V shard j through the window.
+RA_HD TileSet window_q_tiles(const Plan& P, int L, int j, int r, int b0, int b1) {
+  TileSet t = {0, 0, 0, 0, 0};
+  int from = b0;
+  if (straddles(P, L, b0, b1)) {
+    from = L >> 1;
+    add_tiles(t, first_query(P.layout, P.D, L, r, layout_pos(P.layout, P.D, L, j, b0)),
+              key_limit(P.layout, P.D, L, r, layout_pos(P.layout, P.D, L, j, from - 1) + P.window - 1),
+              kQTileRows);
+  }
+  add_tiles(t, first_query(P.layout, P.D, L, r, layout_pos(P.layout, P.D, L, j, from)),
+            key_limit(P.layout, P.D, L, r, layout_pos(P.layout, P.D, L, j, b1) + P.window - 1), kQTileRows);
+  return t;
+}
+
+// The windowed K/V pass leaves the queries that see a sink from beyond the window to items of
+// their own, of at most sink_chunk query tiles of one rank: a sink is seen by the whole
+// sequence, and one item for it would outlast all the others. Every such item, and the
+// window's item of the same tile, adds its float32 sums of the sink rows to a slot of its own,
+// and the slots are summed in order afterwards. Slots of one (sink shard, K/V head): the
+// window's item, then rank by rank the chunks.
+RA_HD int sink_chunks(const Plan& P, int L) { return ceil_div(ceil_div(L, kQTileRows), P.sink_chunk); }
+RA_HD int sink_slots(const Plan& P, int L) { return 1 + P.D * sink_chunks(P, L); }
+RA_HD int sink_items_of(const Plan& P, int L) {
+  return sink_shards(P, L) * P.D * sink_chunks(P, L) * P.hkv;
+}
+// Slot of shard j and K/V head hk: `item` 0 for the window's item, else 1 + r * chunks + chunk.
+RA_HD int sink_slot(const Plan& P, const SeqDesc& s, int j, int hk, int item) {
+  return s.sink_start + (j * P.hkv + hk) * sink_slots(P, s.L) + item;
+}
+
+struct SinkItem { int r, chunk; };  // r < 0: a window item
+
+// Item w of the windowed K/V pass: a sequence's sink items first, then its K/V tiles.
+RA_HD BwdItem decode_window_bwd(const Plan& P, int w, SinkItem* sink) {
+  const int i = find_seq(P, w);
+  const SeqDesc& s = P.seq[i];
+  const int nsink = sink_items_of(P, s.L);
+  int x = w - s.item_start;
+  sink->r = sink->chunk = -1;
+  if (x >= nsink) {
+    BwdItem it;
+    const int nkt = ceil_div(s.L, kKvTileRows), per_head = nkt * P.D;
+    x -= nsink;
+    it.seq = i;
+    it.hk = x / per_head;
+    x %= per_head;
+    it.j = x / nkt;
+    it.kt = x % nkt;
+    return it;
+  }
+  BwdItem it;
+  it.seq = i;
+  it.kt = 0;
+  it.hk = x % P.hkv;
+  x /= P.hkv;
+  const int n = sink_chunks(P, s.L);
+  sink->chunk = x % n;
+  x /= n;
+  sink->r = x % P.D;
+  it.j = x / P.D;
+  return it;
 }
 
 // Rank that holds K/V shard j at ring step s, and the shard rank r holds at step s.

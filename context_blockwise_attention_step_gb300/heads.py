@@ -1,5 +1,6 @@
-"""Head norms, the rotation by position, and the serving path: a paged key-value cache and the
-attention of one new token over it (include/ringattn.h has the definitions).
+"""Head norms, the rotation by position, the sliding window, and the serving path: a paged
+key-value cache and the attention of one new token over it (include/ringattn.h has the
+definitions).
 
 Like ``ops``, this is a binding: every step runs in the library's kernels on the current (or a
 given) stream, outputs are allocated unless they are passed in.
@@ -69,6 +70,12 @@ def _plain(t: torch.Tensor, name: str, dtype, shape, device) -> torch.Tensor:
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
     return t
+
+
+def _token(t: torch.Tensor, numel: int, name: str, prob: Problem, device):
+    ops._check_tensor(t, prob.token_dtype, numel, name)
+    if t.device != device:
+        raise ValueError(f"{name} must be on the same CUDA device as the other tensors")
 
 
 def _weights(q_weight, k_weight, dtype, dh, device):
@@ -160,6 +167,61 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, prob: Problem, q_weight=None, k_weigh
         prob.ptr, _rope_ptr(rope), eps, _p(dq_out), _p(dk_out), _p(q), qs, _p(k), ks, _p(q_weight),
         _p(k_weight), _p(dq), _p(dk), _p(dqw), _p(dkw), _p(workspace), size, s))
     return dq, dk, dqw, dkw
+
+
+# ---- sliding window ------------------------------------------------------------------------
+
+def window_workspace_bytes(prob: Problem, window: int, sinks: int, which: int = 1) -> int:
+    return int(lib().ra_window_workspace_bytes(prob.ptr, window, sinks, which))
+
+
+def window_attn_fwd(q, k, v, prob: Problem, window: int, sinks: int = 0, out=None, lse=None,
+                    workspace=None, stream=None):
+    """Ring attention in which a query at position p sees the keys at k <= p with k > p -
+    ``window`` or k < ``sinks`` -> (out, lse), shard-major. The workspace
+    (``window_workspace_bytes(..., 0)``) is allocated when not given."""
+    r, dev = prob.raw, q.device
+    made = []
+    if out is None:
+        made.append(out := torch.empty(q.shape, device=dev, dtype=q.dtype))
+    if lse is None:
+        made.append(lse := torch.empty(ops._lse_shape(prob), device=dev, dtype=torch.float32))
+    nq, nk = prob.rows * r.hq * r.head_dim, prob.rows * r.hkv * r.head_dim
+    for t, n, name in ((q, nq, "q"), (k, nk, "k"), (v, nk, "v"), (out, nq, "out")):
+        _token(t, n, name, prob, dev)
+    _plain(lse, "lse", torch.float32, ops._lse_shape(prob), dev)
+    if workspace is None:
+        made.append(workspace := _workspace(None, max(1, window_workspace_bytes(prob, window, sinks, 0)), dev))
+    workspace = _workspace(workspace, 0, dev)
+    _launch(dev, stream, made, lambda s: lib().ra_window_attn_fwd(
+        prob.ptr, window, sinks, _p(q), _p(k), _p(v), _p(out), _p(lse), _p(workspace),
+        workspace.numel() * workspace.element_size(), s))
+    return out, lse
+
+
+def window_attn_bwd(dout, q, k, v, out, lse, prob: Problem, window: int, sinks: int = 0, dq=None,
+                    dk=None, dv=None, workspace=None, stream=None):
+    """Backward of ``window_attn_fwd`` -> (dq, dk, dv), shard-major, in the problem dtype."""
+    r, dev = prob.raw, q.device
+    made = []
+    if dq is None:
+        made.append(dq := torch.empty(q.shape, device=dev, dtype=q.dtype))
+    if dk is None:
+        made.append(dk := torch.empty(k.shape, device=dev, dtype=k.dtype))
+    if dv is None:
+        made.append(dv := torch.empty(v.shape, device=dev, dtype=v.dtype))
+    nq, nk = prob.rows * r.hq * r.head_dim, prob.rows * r.hkv * r.head_dim
+    for t, n, name in ((dout, nq, "dout"), (q, nq, "q"), (k, nk, "k"), (v, nk, "v"), (out, nq, "out"),
+                       (dq, nq, "dq"), (dk, nk, "dk"), (dv, nk, "dv")):
+        _token(t, n, name, prob, dev)
+    _plain(lse, "lse", torch.float32, ops._lse_shape(prob), dev)
+    if workspace is None:
+        made.append(workspace := _workspace(None, max(1, window_workspace_bytes(prob, window, sinks, 1)), dev))
+    workspace = _workspace(workspace, 0, dev)
+    _launch(dev, stream, made, lambda s: lib().ra_window_attn_bwd(
+        prob.ptr, window, sinks, _p(q), _p(k), _p(v), _p(out), _p(lse), _p(dout), _p(dq), _p(dk), _p(dv),
+        _p(workspace), workspace.numel() * workspace.element_size(), s))
+    return dq, dk, dv
 
 
 # ---- the paged cache -----------------------------------------------------------------------

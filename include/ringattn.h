@@ -189,6 +189,33 @@ int ra_ring_attn_bwd_noalloc(const ra_problem* p, const void* q, const void* k, 
                              const void* out, const float* lse, const void* dout, void* dq,
                              void* dk, void* dv, void* stream);
 
+/* ---- sliding window --------------------------------------------------------------------- */
+
+#define RA_MAX_SINKS 128
+
+/* Ring attention with a sliding window: the query at position p of a sequence sees the keys at
+ * positions k <= p with k > p - window or k < sinks (the first `sinks` tokens of every
+ * sequence stay visible). The problem must be causal; window >= 1, 0 <= sinks <=
+ * RA_MAX_SINKS. Tensors, layouts, lse and the optional workspace (now
+ * ra_window_workspace_bytes(p, window, sinks, 0)) are as for ra_ring_attn_fwd; K/V tiles that
+ * no query of a block sees are never loaded. With a window that no sequence is longer than,
+ * this is ra_ring_attn_fwd. As there, k and v must be finite: hidden keys of a loaded tile
+ * count with weight 0. */
+int ra_window_attn_fwd(const ra_problem* p, int window, int sinks, const void* q, const void* k,
+                       const void* v, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
+/* Its backward, arguments as for ra_ring_attn_bwd. Run-to-run bit-identical. The workspace
+ * (device, >= ra_window_workspace_bytes(p, window, sinks, 1), 256-byte aligned) is
+ * overwritten. */
+int ra_window_attn_bwd(const ra_problem* p, int window, int sinks, const void* q, const void* k,
+                       const void* v, const void* out, const float* lse, const void* dout, void* dq,
+                       void* dk, void* dv, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace of the two calls above: which = 0 forward (optional there), which = 1
+ * backward; 0 for invalid arguments. */
+size_t ra_window_workspace_bytes(const ra_problem* p, int window, int sinks, int which);
+
 /* ---- head norms and position rotation ------------------------------------------------ */
 
 #define RA_MAX_ROTARY_DIM 128

@@ -162,3 +162,30 @@ def test_python_checks_need_cuda_tensors():
     q = torch.zeros(2, 64, 8, 128, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
         ra.qk_norm_rope_fwd(q, q[:, :, :2], _prob(), rope=ra.make_rope(128))
+
+
+def test_window_refusals():
+    L, p = _abi.lib(), _prob()
+
+    def fwd(p=p, window=8, sinks=0, q=FAKE, ws=None, size=0):
+        return L.ra_window_attn_fwd(p.ptr, window, sinks, q, FAKE, FAKE, FAKE, FAKE, ws, size, None)
+    assert fwd(window=0) == _abi.RA_ERR_INVALID_ARG
+    assert fwd(window=-5) == _abi.RA_ERR_INVALID_ARG
+    assert fwd(sinks=-1) == _abi.RA_ERR_INVALID_ARG
+    assert fwd(sinks=_abi.RA_MAX_SINKS + 1) == _abi.RA_ERR_INVALID_ARG
+    assert fwd(p=_prob(causal=False)) == _abi.RA_ERR_UNSUPPORTED
+    assert fwd(p=_prob(seqlen=60)) == _abi.RA_ERR_SHAPE
+    assert fwd(q=None) == _abi.RA_ERR_INVALID_ARG
+    assert fwd(ws=64, size=1024) == _abi.RA_ERR_INVALID_ARG
+    assert fwd(window=1 << 30, q=None) == _abi.RA_ERR_INVALID_ARG  # the ring call's refusals
+    need = ra.window_workspace_bytes(p, 8, 4, 1)
+    assert need >= ra.workspace_bytes(p, 2)
+    assert ra.window_workspace_bytes(p, 0, 0, 1) == 0
+
+    def bwd(window=8, sinks=4, ws=FAKE, size=need, dq=FAKE):
+        return L.ra_window_attn_bwd(p.ptr, window, sinks, *([FAKE] * 6), dq, FAKE, FAKE, ws, size, None)
+    assert bwd(size=need - 1) == _abi.RA_ERR_WORKSPACE
+    assert bwd(ws=None) == _abi.RA_ERR_INVALID_ARG
+    assert bwd(ws=128) == _abi.RA_ERR_INVALID_ARG
+    assert bwd(dq=None) == _abi.RA_ERR_INVALID_ARG
+    assert bwd(window=0) == _abi.RA_ERR_INVALID_ARG
