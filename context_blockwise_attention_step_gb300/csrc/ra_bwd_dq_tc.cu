@@ -26,11 +26,15 @@
 // ring in shared memory. Warp roles (384 threads): warp 0 TMA producer, warp 1 TMEM
 // allocator + MMA issuer, warps 4-7 and 8-11 the P / dS warpgroups (thread = query row;
 // key columns 0-63 and 64-127; they also write dq).
+//
+// WIN (sliding window with always visible first tokens): the walk visits the K/V tiles that
+// some row of the tile sees, as in the windowed forward.
 #include <cuda_runtime.h>
 
 #include "ra_internal.h"
 #include "ra_plan.h"
 #include "ra_ptx.cuh"
+#include "ra_window.cuh"
 
 namespace ra {
 
@@ -71,6 +75,7 @@ struct DqBars {
   uint64_t drain;
   uint64_t item_full[2], item_empty[2];  // the CTA's item queue
   int item[2];
+  int item_tiles[2];  // windowed: K/V tiles of the item
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -100,6 +105,12 @@ __device__ __forceinline__ DqItem decode_dq(const Plan& P, int w) {
   return it;
 }
 
+// Windowed: the K/V tiles of the shard that the item's rank holds at step s.
+__device__ __forceinline__ TileSet dq_set(const Plan& P, const DqItem& it, int L, int s) {
+  const int a0 = it.qt * kQTileRows;
+  return window_kv_tiles(P, L, it.r, shard_at_step(P.D, it.r, s), a0, min(L, a0 + kQTileRows) - 1);
+}
+
 __device__ __forceinline__ int dq_walk_tiles(const Plan& P, const DqItem& it, int L) {
   const int a_last = min(L, (it.qt + 1) * kQTileRows) - 1;
   int n = 0;
@@ -123,15 +134,42 @@ __device__ __forceinline__ int dq_item_publish(DqBars& sh, const Plan& P, int k,
   return w;
 }
 __device__ __forceinline__ int dq_item_take(DqBars& sh, int k, volatile int* abort_flag,
-                                            uint64_t tmo, unsigned int* status) {
+                                            uint64_t tmo, unsigned int* status, int* tiles) {
   const int slot = k & 1;
   if (!mbar_wait(&sh.item_full[slot], (k >> 1) & 1, abort_flag, tmo, status)) return -1;
   const int w = *reinterpret_cast<volatile int*>(&sh.item[slot]);
+  if (tiles != nullptr) *tiles = *reinterpret_cast<volatile int*>(&sh.item_tiles[slot]);
   mbar_arrive(&sh.item_empty[slot]);
   return w;
 }
 
-template <int DH>
+// The windowed kernel's producer warp: takes the next item, counts its tiles, publishes both.
+__device__ __forceinline__ int dq_window_publish(DqBars& sh, const Plan& P, int k, int lane,
+                                                 volatile int* abort_flag, uint64_t tmo,
+                                                 unsigned int* status) {
+  const int slot = k & 1;
+  const bool ok = mbar_wait(&sh.item_empty[slot], ((k >> 1) & 1) ^ 1, abort_flag, tmo, status);
+  if (!__all_sync(0xffffffffu, ok)) return -1;
+  int w = 0;
+  if (lane == 0)
+    w = P.work_counter ? atomicAdd(P.work_counter, 1)
+                       : static_cast<int>(blockIdx.x + static_cast<unsigned>(k) * gridDim.x);
+  w = __shfl_sync(0xffffffffu, w, 0);
+  int n = 0;
+  if (w < P.n_items) {
+    const DqItem it = decode_dq(P, w);
+    const int L = P.seq[it.seq].L;
+    n = count_tiles(P.D, [&](int s) { return dq_set(P, it, L, s); });
+  }
+  if (lane == 0) {
+    sh.item[slot] = w;
+    sh.item_tiles[slot] = n;
+    mbar_arrive(&sh.item_full[slot]);
+  }
+  return w;
+}
+
+template <int DH, bool WIN>
 __global__ void __launch_bounds__(kDqThreads, 1)
     ring_bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
                           const __grid_constant__ CUtensorMap tmK,
@@ -192,7 +230,56 @@ __global__ void __launch_bounds__(kDqThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA producer
-    if (lane == 0) {
+    if constexpr (WIN) {  // the whole warp walks, lane 0 issues
+      uint32_t q_phase = 0;
+      int kc = 0;
+      auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, tmo, status));
+      };
+      for (int kq = 0;; ++kq) {
+        const int w = dq_window_publish(sh, P, kq, lane, abort_flag, tmo, status);
+        if (w < 0 || w >= P.n_items) break;
+        const DqItem it = decode_dq(P, w);
+        const SeqDesc& sd = P.seq[it.seq];
+        if (!wait(&sh.q_empty, q_phase ^ 1)) break;
+        q_phase ^= 1;
+        if (lane == 0) {
+          mbar_expect_tx(&sh.q_full, 2 * C::kTileBytes);
+          const int qrow = sd.row_off + it.r * P.shard_stride + it.qt * kQTileRows;
+          for (int d = 0; d < C::kSub; ++d) {
+            tma_load_3d(smem + C::kOffQ + d * kSubBytes, &tmQ, &sh.q_full, d * 64, it.h, qrow);
+            tma_load_3d(smem + C::kOffDO + d * kSubBytes, &tmDO, &sh.q_full, d * 64, it.h, qrow);
+          }
+        }
+        const int hk = it.h / P.group;
+        const bool ok = for_each_set(
+            P.D, [&](int s) { return dq_set(P, it, sd.L, s); },
+            [&](int s, const TileSet& set) -> bool {
+              const int krow = sd.row_off + shard_at_step(P.D, it.r, s) * P.shard_stride;
+              const int nb = tile_count(set);
+              for (int i = 0; i < nb; ++i, ++kc) {
+                const int row = krow + tile_at(set, i) * kKvTileRows;
+                const int st = kc & 1, kst = kc % C::kKStages;
+                if (!wait(&sh.k_empty[kst], ((kc / C::kKStages) & 1) ^ 1)) return false;
+                if (lane == 0) {
+                  mbar_expect_tx(&sh.k_full[kst], C::kTileBytes);
+                  for (int d = 0; d < C::kSub; ++d)
+                    tma_load_3d(smem + C::kOffK + kst * C::kTileBytes + d * kSubBytes, &tmK,
+                                &sh.k_full[kst], d * 64, hk, row);
+                }
+                if (!wait(&sh.v_empty[st], ((kc >> 1) & 1) ^ 1)) return false;
+                if (lane == 0) {
+                  mbar_expect_tx(&sh.v_full[st], C::kTileBytes);
+                  for (int d = 0; d < C::kSub; ++d)
+                    tma_load_3d(smem + C::kOffV + st * C::kTileBytes + d * kSubBytes, &tmV,
+                                &sh.v_full[st], d * 64, hk, row);
+                }
+              }
+              return true;
+            });
+        if (!ok) break;
+      }
+    } else if (lane == 0) {
       uint32_t q_phase = 0;
       int kc = 0;
       for (int kq = 0;; ++kq) {
@@ -250,11 +337,12 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       const uint32_t sK = smem_u32(smem + C::kOffK), sV = smem_u32(smem + C::kOffV);
       bool ok = true;
       for (int kq = 0; ok; ++kq) {
-        const int w = dq_item_take(sh, kq, abort_flag, tmo, status);
+        int tiles = 0;
+        const int w = dq_item_take(sh, kq, abort_flag, tmo, status, WIN ? &tiles : nullptr);
         if (w < 0) ok = false;
         if (w < 0 || w >= P.n_items) break;
         const DqItem it = decode_dq(P, w);
-        const int N = dq_walk_tiles(P, it, P.seq[it.seq].L);
+        const int N = WIN ? tiles : dq_walk_tiles(P, it, P.seq[it.seq].L);
         if (N == 0) continue;
         if (!(ok = mbar_wait(&sh.q_full, q_phase, abort_flag, tmo, status))) break;
         q_phase ^= 1;
@@ -331,7 +419,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     const uint64_t sl2x2 = f2(sl2, sl2);
     uint32_t s_phase[2] = {0, 0}, dp_phase = 0, dd_phase = 0;
     for (int kq = 0;; ++kq) {
-      const int w = dq_item_take(sh, kq, abort_flag, tmo, status);
+      const int w = dq_item_take(sh, kq, abort_flag, tmo, status, nullptr);
       if (w < 0 || w >= P.n_items) break;
       const DqItem it = decode_dq(P, w);
       const SeqDesc& sd = P.seq[it.seq];
@@ -339,7 +427,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       const int a = it.qt * kQTileRows + row;
       const bool valid = a < L;
       const size_t qrow = static_cast<size_t>(sd.row_off + it.r * P.shard_stride + a);
-      const int N = dq_walk_tiles(P, it, L);
+      const int N = WIN ? 1 : dq_walk_tiles(P, it, L);  // a windowed row sees itself
       if (N == 0) {  // no key visible: dq = 0 (nothing to add for bwd_accum)
         if (valid && !P.bwd_accum) {
           __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(dq) + (qrow * P.hq + it.h) * DH;
@@ -366,16 +454,32 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       const int a_last = min(L, (it.qt + 1) * kQTileRows) - 1;
       int n = 0;
       bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        const bool got = mbar_wait(bar, parity, abort_flag, tmo, status);
+        return WIN ? __all_sync(0xffffffffu, got) : got;  // the windowed walk is the warp's
+      };
+      unsigned shards = 0;  // windowed: the next 32 steps' shards that have tiles
       for (int s = P.step_begin; s < P.step_end && ok; ++s) {
+        if constexpr (WIN) {
+          if ((s & 31) == 0) shards = nonempty(P.D, s, [&](int i) { return dq_set(P, it, L, i); });
+          if (!((shards >> (s & 31)) & 1u)) continue;
+        }
         const int j = shard_at_step(P.D, it.r, s);
-        const int nb = kv_tiles_for(P, L, it.r, j, a_last);
+        TileSet set;
+        if constexpr (WIN) set = dq_set(P, it, L, s);
+        const int nb = WIN ? tile_count(set) : kv_tiles_for(P, L, it.r, j, a_last);
         const int lim = !valid ? -1 : (P.causal ? key_limit(P.layout, P.D, L, j, pq) : L - 1);
-        for (int b = 0; b < nb; ++b, ++n) {
+        // windowed: of the shard's keys up to lim this row sees those before sk, and from lo on
+        const int lo = WIN ? first_query(P.layout, P.D, L, j, pq - P.window + 1) : 0;
+        const int sk = WIN ? sink_rows(P, L, j) : 0;
+        for (int i = 0; i < nb; ++i, ++n) {
+          const int b = WIN ? tile_at(set, i) : i;
           const int buf = n & 1;
           const uint32_t tS = tmem + lane_off + (buf ? C::kColS1 : C::kColS0);
           int cnt = lim + 1 - b * kKvTileRows;  // visible keys of this tile (a prefix)
           cnt = cnt < 0 ? 0 : (cnt > kKvTileRows ? kKvTileRows : cnt);
-          if (!(ok = mbar_wait(&sh.s_full[buf], s_phase[buf], abort_flag, tmo, status))) break;
+          const int lo_t = WIN ? lo - b * kKvTileRows : 0, sk_t = WIN && b == 0 ? sk : 0;
+          if (!(ok = wait(&sh.s_full[buf], s_phase[buf]))) break;
           s_phase[buf] ^= 1;
           tc_fence_after();
           uint32_t pp[32], sv2[2][32];
@@ -386,7 +490,8 @@ __global__ void __launch_bounds__(kDqThreads, 1)
           for (int ch = 0; ch < 2; ++ch) {
             const int cs = c0 + 32 * ch;
             const uint32_t (&sv)[32] = sv2[ch];
-            const bool full = __all_sync(0xffffffffu, cnt >= cs + 32);
+            const uint32_t vis = WIN ? visible_bits(cs, cnt, lo_t, sk_t) : 0u;
+            const bool full = __all_sync(0xffffffffu, WIN ? vis == 0xffffffffu : cnt >= cs + 32);
             // staged: every FMA, then every exponential, then masking and packing
             uint64_t xv[16];
 #pragma unroll
@@ -402,12 +507,12 @@ __global__ void __launch_bounds__(kDqThreads, 1)
             if (!full) {
 #pragma unroll
               for (int i = 0; i < 32; ++i)
-                if (cs + i >= cnt) ev[i] = 0.f;
+                if (WIN ? !((vis >> i) & 1u) : cs + i >= cnt) ev[i] = 0.f;
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i) pp[16 * ch + i] = pack_bf16x2(ev[2 * i], ev[2 * i + 1]);
           }
-          if (!(ok = mbar_wait(&sh.dp_full, dp_phase, abort_flag, tmo, status))) break;
+          if (!(ok = wait(&sh.dp_full, dp_phase))) break;
           dp_phase ^= 1;
           tc_fence_after();
           uint32_t dp2[2][32];
@@ -486,12 +591,12 @@ __global__ void __launch_bounds__(kDqThreads, 1)
   }
 }
 
-template <int DH>
+template <int DH, bool WIN>
 cudaError_t launch_one(const Plan& P, const CUtensorMap& mq, const CUtensorMap& mk,
                        const CUtensorMap& mv, const CUtensorMap& mdo, const float* lse,
                        const float* delta, void* dq, int n_items, int n_sm, cudaStream_t st) {
   using C = DqCfg<DH>;
-  auto kern = ring_bwd_dq_tc_kernel<DH>;
+  auto kern = ring_bwd_dq_tc_kernel<DH, WIN>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        C::kSmemBytes);
   if (e != cudaSuccess) return e;
@@ -523,8 +628,11 @@ cudaError_t launch_bwd_dq_tc(const Plan& P0, const void* q, const void* k, const
   int dev = 0, n_sm = 0;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
-  if (P.head_dim == 128) return launch_one<128>(P, mq, mk, mv, mdo, lse, delta, dq, items, n_sm, st);
-  return launch_one<64>(P, mq, mk, mv, mdo, lse, delta, dq, items, n_sm, st);
+  if (P.window > 0)
+    return P.head_dim == 128 ? launch_one<128, true>(P, mq, mk, mv, mdo, lse, delta, dq, items, n_sm, st)
+                             : launch_one<64, true>(P, mq, mk, mv, mdo, lse, delta, dq, items, n_sm, st);
+  return P.head_dim == 128 ? launch_one<128, false>(P, mq, mk, mv, mdo, lse, delta, dq, items, n_sm, st)
+                           : launch_one<64, false>(P, mq, mk, mv, mdo, lse, delta, dq, items, n_sm, st);
 }
 
 cudaError_t bwd_dq_status(unsigned int* value, bool reset) {

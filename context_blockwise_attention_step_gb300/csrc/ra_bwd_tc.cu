@@ -33,6 +33,15 @@
 // backward); kAccum = true adds float32 dk / dv into the outputs instead of storing them
 // in the problem dtype (the per-step block backward of the unfused path).
 //
+// WIN (only without dQ and without kAccum): sliding window with always visible first tokens.
+// The item of a K/V tile walks the query tiles that see some of its rows through the window.
+// The queries that see a sink from beyond the window belong to items of their own (one sink
+// tile, a few query tiles of one rank): a sink is seen by every later query, and one item for
+// it would outlast all the others (4096 query tiles against 36 at 131072 tokens, window 1024,
+// 4 heads a group). Sink rows get their sum from several items, so each of these writes float32
+// sums of the sink rows to a slot of its own (ra_plan.h), and sink_sum_kernel adds the slots in
+// order, so that the result does not depend on the order of the items.
+//
 // Warp roles (512 threads; 384 without dQ): warp 0 TMA producer (K, V once per item; Q and
 // dO per query tile, two stages), warp 1 TMEM allocator + MMA issuer, warp 2 lse / delta
 // loader, warps 4-7 and 8-11 the P / dS warpgroups (thread = K/V row; query columns 0-63
@@ -43,6 +52,7 @@
 #include "ra_internal.h"
 #include "ra_plan.h"
 #include "ra_ptx.cuh"
+#include "ra_window.cuh"
 
 namespace ra {
 
@@ -83,6 +93,7 @@ struct BwdBars {
   uint64_t acc_done, drain;
   uint64_t item_full[2], item_empty[2];  // the CTA's item queue
   int item[2];
+  int item_tiles[2];  // windowed: query tiles of the item, over the heads of the group
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -131,6 +142,71 @@ __device__ __forceinline__ bool for_each_qtile(const Plan& P, const BwdItem& it,
     }
   }
   return true;
+}
+
+// ---- windowed walks
+// Item w of the windowed pass; sink.r < 0: a K/V tile's window item.
+struct WinItem {
+  BwdItem it;
+  SinkItem sink;
+  int L, b0, ranks;  // ranks: query ranks that the walk goes over
+};
+
+__device__ __forceinline__ WinItem win_item(const Plan& P, int w) {
+  WinItem x;
+  x.it = decode_window_bwd(P, w, &x.sink);
+  x.L = P.seq[x.it.seq].L;
+  x.b0 = x.it.kt * kKvTileRows;
+  x.ranks = x.sink.r >= 0 ? 1 : P.D;
+  return x;
+}
+__device__ __forceinline__ int win_rank(const WinItem& x, int i) { return x.sink.r >= 0 ? x.sink.r : i; }
+
+// The query tiles of the i-th rank of the walk.
+__device__ __forceinline__ TileSet win_set(const Plan& P, const WinItem& x, int i) {
+  if (x.sink.r < 0)
+    return window_q_tiles(P, x.L, x.it.j, i, x.b0, min(x.L, x.b0 + kKvTileRows) - 1);
+  // beyond the window of the shard's first sink
+  const int64_t p0 = layout_pos(P.layout, P.D, x.L, x.it.j, 0) + P.window;
+  const int a = first_query(P.layout, P.D, x.L, x.sink.r, p0);
+  const int first = max(a / kQTileRows, x.sink.chunk * P.sink_chunk);
+  const int end = min(ceil_div(x.L, kQTileRows), (x.sink.chunk + 1) * P.sink_chunk);
+  TileSet t = {0, 0, 0, 0, 0};
+  if (a < x.L && first < end) {
+    t.s0 = first;
+    t.n0 = end - first;
+  }
+  return t;
+}
+
+// Calls f(r, h, q0) for every query tile the item visits, in walk order, with the whole warp.
+template <typename F>
+__device__ __forceinline__ bool win_for_each_qtile(const Plan& P, const WinItem& x, F&& f) {
+  return for_each_set(
+      x.ranks, [&](int i) { return win_set(P, x, i); },
+      [&](int i, const TileSet& set) -> bool {
+        const int nq = tile_count(set);
+        for (int g = 0; g < P.group; ++g)
+          for (int k = 0; k < nq; ++k)
+            if (!f(win_rank(x, i), x.it.hk * P.group + g, tile_at(set, k) * kQTileRows)) return false;
+        return true;
+      });
+}
+
+// First element of slot row `row` (dk; dv follows after all rows) of a sink tile's item.
+__device__ __forceinline__ float* sink_row(const Plan& P, const WinItem& x, int row, int which) {
+  const SeqDesc& s = P.seq[x.it.seq];
+  const int item = x.sink.r < 0 ? 0 : 1 + x.sink.r * sink_chunks(P, x.L) + x.sink.chunk;
+  const int64_t slot = sink_slot(P, s, x.it.j, x.it.hk, item);
+  return P.sink_sums + ((slot * 2 + which) * P.sinks + row) * P.head_dim;
+}
+
+__device__ __forceinline__ void store_row32_f32(float* dst, const uint32_t (&r)[32], float mul) {
+  float4* d = reinterpret_cast<float4*>(dst);
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    d[q] = make_float4(__uint_as_float(r[4 * q]) * mul, __uint_as_float(r[4 * q + 1]) * mul,
+                       __uint_as_float(r[4 * q + 2]) * mul, __uint_as_float(r[4 * q + 3]) * mul);
 }
 
 __device__ __forceinline__ void store_row32_bf16(__nv_bfloat16* dst, const uint32_t (&r)[32],
@@ -226,16 +302,18 @@ __device__ __forceinline__ void ds_chunk(uint32_t tY, int c0, const float* dl,
 }
 
 // P^T = 2^(S^T * scale*log2e - lse*log2e) for the query columns [c0 + 32*CH, +32), from
-// their S^T registers: columns before `lo` (queries that may not see this key) are zero;
+// their S^T registers: columns before `lo` (queries that may not see this key; windowed: and
+// those from `hi` on) are zero;
 // columns past the sequence piece have -lse*log2e = -inf from the loader and give 0. The
 // bf16 result goes to X columns [32 + c0/2 + 16*CH, +16): inside the S^T columns this
 // warpgroup reads itself (the other warpgroup may still be reading its own).
-template <int CH>
+template <int CH, bool WIN>
 __device__ __forceinline__ void p_from(const uint32_t (&sv)[32], uint32_t tX, int c0, const float* nl,
-                                       uint64_t sl2x2, int lo, uint32_t (&pp)[32]) {
+                                       uint64_t sl2x2, int lo, int hi, uint32_t (&pp)[32]) {
   const int cs = c0 + 32 * CH;
   uint32_t pk[16];
-  const bool full = __all_sync(0xffffffffu, lo <= cs);
+  const uint32_t vis = WIN ? low_bits(hi - cs) & ~low_bits(lo - cs) : 0u;
+  const bool full = __all_sync(0xffffffffu, WIN ? vis == 0xffffffffu : lo <= cs);
   // staged: every FMA, then every exponential, then masking and packing
   uint64_t xv[16];
 #pragma unroll
@@ -254,7 +332,7 @@ __device__ __forceinline__ void p_from(const uint32_t (&sv)[32], uint32_t tX, in
   if (!full) {
 #pragma unroll
     for (int i = 0; i < 32; ++i)
-      if (cs + i < lo) ev[i] = 0.f;
+      if (WIN ? !((vis >> i) & 1u) : cs + i < lo) ev[i] = 0.f;
   }
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
@@ -271,7 +349,7 @@ __device__ __forceinline__ void p_chunk(uint32_t tX, int c0, const float* nl, ui
                                         int lo, uint32_t (&pp)[32]) {
   uint32_t sv[32];
   tmem_ld32(tX + c0 + 32 * CH, sv);
-  p_from<CH>(sv, tX, c0, nl, sl2x2, lo, pp);
+  p_from<CH, false>(sv, tX, c0, nl, sl2x2, lo, 0, pp);
 }
 
 // Threads per block: the dQ warpgroup only exists when dq is computed; without it the
@@ -296,15 +374,42 @@ __device__ __forceinline__ int item_publish(BwdBars& sh, const Plan& P, int k,
   return w;
 }
 __device__ __forceinline__ int item_take(BwdBars& sh, int k, volatile int* abort_flag,
-                                         uint64_t tmo, unsigned int* status) {
+                                         uint64_t tmo, unsigned int* status, int* tiles = nullptr) {
   const int slot = k & 1;
   if (!mbar_wait(&sh.item_full[slot], (k >> 1) & 1, abort_flag, tmo, status)) return -1;
   const int w = *reinterpret_cast<volatile int*>(&sh.item[slot]);
+  if (tiles != nullptr) *tiles = *reinterpret_cast<volatile int*>(&sh.item_tiles[slot]);
   mbar_arrive(&sh.item_empty[slot]);
   return w;
 }
 
-template <int DH, bool kWithDQ, bool kAccum>
+// The windowed kernel's producer warp: takes the next item, counts its tiles, publishes both.
+__device__ __forceinline__ int win_item_publish(BwdBars& sh, const Plan& P, int k, int lane,
+                                                volatile int* abort_flag, uint64_t tmo,
+                                                unsigned int* status, int* tiles) {
+  const int slot = k & 1;
+  const bool ok = mbar_wait(&sh.item_empty[slot], ((k >> 1) & 1) ^ 1, abort_flag, tmo, status);
+  if (!__all_sync(0xffffffffu, ok)) return -1;
+  int w = 0;
+  if (lane == 0)
+    w = P.work_counter ? atomicAdd(P.work_counter, 1)
+                       : static_cast<int>(blockIdx.x + static_cast<unsigned>(k) * gridDim.x);
+  w = __shfl_sync(0xffffffffu, w, 0);
+  int n = 0;
+  if (w < P.n_items) {
+    const WinItem x = win_item(P, w);
+    n = count_tiles(x.ranks, [&](int i) { return win_set(P, x, i); }) * P.group;
+  }
+  if (lane == 0) {
+    sh.item[slot] = w;
+    sh.item_tiles[slot] = n;
+    mbar_arrive(&sh.item_full[slot]);
+  }
+  *tiles = n;
+  return w;
+}
+
+template <int DH, bool kWithDQ, bool kAccum, bool WIN>
 __global__ void __launch_bounds__(bwd_threads<kWithDQ>(), 1)
     ring_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
                        const __grid_constant__ CUtensorMap tmK,
@@ -367,7 +472,48 @@ __global__ void __launch_bounds__(bwd_threads<kWithDQ>(), 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA producer
-    if (lane == 0) {
+    if constexpr (WIN) {  // the whole warp walks, lane 0 issues
+      uint32_t kv_phase = 0;
+      int qcount = 0;
+      auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, tmo, status));
+      };
+      for (int kq = 0;; ++kq) {
+        int tiles = 0;
+        const int w = win_item_publish(sh, P, kq, lane, abort_flag, tmo, status, &tiles);
+        if (w < 0 || w >= P.n_items) break;
+        if (tiles == 0) continue;
+        const WinItem x = win_item(P, w);
+        const SeqDesc& sd = P.seq[x.it.seq];
+        if (!wait(&sh.kv_empty, kv_phase ^ 1)) break;
+        kv_phase ^= 1;
+        if (lane == 0) {
+          mbar_expect_tx(&sh.kv_full, 2 * C::kTileBytes);
+          const int krow = sd.row_off + x.it.j * P.shard_stride + x.b0;
+          for (int d = 0; d < C::kSub; ++d) {
+            tma_load_3d(smem + C::kOffK + d * kSubBytes, &tmK, &sh.kv_full, d * 64, x.it.hk, krow);
+            tma_load_3d(smem + C::kOffV + d * kSubBytes, &tmV, &sh.kv_full, d * 64, x.it.hk, krow);
+          }
+        }
+        const bool ok = win_for_each_qtile(P, x, [&](int r, int h, int q0) -> bool {
+          const int st = qcount & 1;
+          if (!wait(&sh.q_empty[st], ((qcount >> 1) & 1) ^ 1)) return false;
+          if (lane == 0) {  // Q first, on its own barrier, as below
+            const int qrow = sd.row_off + r * P.shard_stride + q0;
+            uint8_t* base = smem + C::kOffQ + st * C::kStageBytes;
+            mbar_expect_tx(&sh.q_full[st], C::kTileBytes);
+            for (int d = 0; d < C::kSub; ++d)
+              tma_load_3d(base + d * kSubBytes, &tmQ, &sh.q_full[st], d * 64, h, qrow);
+            mbar_expect_tx(&sh.do_full[st], C::kTileBytes);
+            for (int d = 0; d < C::kSub; ++d)
+              tma_load_3d(base + C::kTileBytes + d * kSubBytes, &tmDO, &sh.do_full[st], d * 64, h, qrow);
+          }
+          ++qcount;
+          return true;
+        });
+        if (!ok) break;
+      }
+    } else if (lane == 0) {
       uint32_t kv_phase = 0;
       int qcount = 0;
       for (int kq = 0;; ++kq) {
@@ -427,11 +573,18 @@ __global__ void __launch_bounds__(bwd_threads<kWithDQ>(), 1)
       };
       bool ok = true;
       for (int kq = 0; ok; ++kq) {
-        const int w = item_take(sh, kq, abort_flag, tmo, status);
+        int tiles = 0;
+        const int w = item_take(sh, kq, abort_flag, tmo, status, WIN ? &tiles : nullptr);
         if (w < 0) ok = false;
         if (w < 0 || w >= P.n_items) break;
-        const BwdItem it = decode_bwd(P, w);
-        const BwdWalk wk = bwd_walk(P, it);
+        BwdItem it;
+        BwdWalk wk;
+        if constexpr (WIN) {
+          wk.N = tiles;
+        } else {
+          it = decode_bwd(P, w);
+          wk = bwd_walk(P, it);
+        }
         if (wk.N == 0) continue;
         if (!(ok = mbar_wait(&sh.kv_full, kv_phase, abort_flag, tmo, status))) break;
         kv_phase ^= 1;
@@ -446,7 +599,7 @@ __global__ void __launch_bounds__(bwd_threads<kWithDQ>(), 1)
           // Without dQ the order per tile is [dS(i-1)] dK(i-1), dP(i), [P(i)] dV(i), S(i+1):
           // dP(i) needs no P, so it runs while P(i) is computed, and S(i+1) runs while
           // dS(i) is computed.
-          ok = for_each_qtile(P, it, wk, [&](int, int, int) -> bool {
+          auto qtile = [&](int, int, int) -> bool {
             const int qi = qc + i;
             const int st = qi & 1;
             const uint32_t sQ = sQ0 + st * C::kStageBytes, sDO = sQ + C::kTileBytes;
@@ -486,7 +639,12 @@ __global__ void __launch_bounds__(bwd_threads<kWithDQ>(), 1)
             }
             ++i;
             return true;
-          });
+          };
+          if constexpr (WIN) {
+            while (ok && i < wk.N) ok = qtile(0, 0, 0);
+          } else {
+            ok = for_each_qtile(P, it, wk, qtile);
+          }
           if (ok) {  // the last tile's dK
             const int ql = qc + wk.N - 1;
             ok = mbar_wait(&sh.ds_full, ds_phase, abort_flag, tmo, status);
@@ -579,13 +737,23 @@ __global__ void __launch_bounds__(bwd_threads<kWithDQ>(), 1)
     for (int kq = 0;; ++kq) {
       const int w = item_take(sh, kq, abort_flag, tmo, status);
       if (w < 0 || w >= P.n_items) break;
-      const BwdItem it = decode_bwd(P, w);
-      const BwdWalk wk = bwd_walk(P, it);
-      if (wk.N == 0) continue;
+      WinItem x = {};
+      BwdItem it;
+      BwdWalk wk;
+      if constexpr (WIN) {
+        x = win_item(P, w);
+        it = x.it;
+        wk.L = x.L;
+      } else {
+        it = decode_bwd(P, w);
+        wk = bwd_walk(P, it);
+        if (wk.N == 0) continue;
+      }
       const SeqDesc& sd = P.seq[it.seq];
-      const bool ok = for_each_qtile(P, it, wk, [&](int r, int h, int q0) -> bool {
+      auto qtile = [&](int r, int h, int q0) -> bool {
         const int slot = t & 1;
-        if (!mbar_wait(&sh.ls_empty[slot], ((t >> 1) & 1) ^ 1, abort_flag, tmo, status)) return false;
+        const bool got = mbar_wait(&sh.ls_empty[slot], ((t >> 1) & 1) ^ 1, abort_flag, tmo, status);
+        if (!(WIN ? __all_sync(0xffffffffu, got) : got)) return false;
         float* nl = ls_base + slot * 256;
         const size_t li0 = sd.lse_off + static_cast<size_t>(h) * P.lse_hstride +
                            static_cast<size_t>(r) * P.shard_stride + q0;
@@ -604,7 +772,10 @@ __global__ void __launch_bounds__(bwd_threads<kWithDQ>(), 1)
         mbar_arrive(&sh.ls_full[slot]);
         ++t;
         return true;
-      });
+      };
+      bool ok;
+      if constexpr (WIN) ok = win_for_each_qtile(P, x, qtile);
+      else ok = for_each_qtile(P, it, wk, qtile);
       if (!ok) break;
     }
   } else if (warp >= 4 && warp < 12) {
@@ -621,18 +792,42 @@ __global__ void __launch_bounds__(bwd_threads<kWithDQ>(), 1)
     uint32_t s_phase = 0, dp_phase = 0, ad_phase = 0;
     int t = 0;
     for (int kq = 0;; ++kq) {
-      const int w = item_take(sh, kq, abort_flag, tmo, status);
+      int tiles = 0;
+      const int w = item_take(sh, kq, abort_flag, tmo, status, WIN ? &tiles : nullptr);
       if (w < 0 || w >= P.n_items) break;
-      const BwdItem it = decode_bwd(P, w);
-      const BwdWalk wk = bwd_walk(P, it);
+      WinItem x = {};
+      BwdItem it;
+      BwdWalk wk;
+      if constexpr (WIN) {
+        x = win_item(P, w);
+        it = x.it;
+        wk.L = x.L;
+        wk.b0 = x.b0;
+        wk.N = tiles;
+      } else {
+        it = decode_bwd(P, w);
+        wk = bwd_walk(P, it);
+      }
       const SeqDesc& sd = P.seq[it.seq];
       const int b = wk.b0 + row;
       const bool validk = b < wk.L;
       const size_t krow = static_cast<size_t>(sd.row_off + it.j * P.shard_stride + b);
       const size_t out_off = (krow * P.hkv + it.hk) * DH;
+      // windowed: sink rows go to the item's slot, and a sink item has no other rows
+      const bool is_sink = WIN && validk && b < sink_rows(P, wk.L, it.j);
+      const bool store = validk && !(WIN && (is_sink || x.sink.r >= 0));
       if (wk.N == 0) {
+        if constexpr (WIN) {
+          if (is_sink) {
+            uint32_t z[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) z[i] = 0u;
+#pragma unroll
+            for (int c = 0; c < DH / 32; ++c) store_row32_f32(sink_row(P, x, b, wg) + c * 32, z, 0.f);
+          }
+        }
         if constexpr (!kAccum) {
-          if (validk) {
+          if (store) {
             uint32_t z[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) z[i] = 0u;
@@ -644,14 +839,27 @@ __global__ void __launch_bounds__(bwd_threads<kWithDQ>(), 1)
         continue;
       }
       const int64_t pk = validk ? layout_pos(P.layout, P.D, wk.L, it.j, b) : 0;
-      const bool ok = for_each_qtile(P, it, wk, [&](int r, int, int q0) -> bool {
+      auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        const bool got = mbar_wait(bar, parity, abort_flag, tmo, status);
+        return WIN ? __all_sync(0xffffffffu, got) : got;  // the windowed walk is the warp's
+      };
+      auto qtile = [&](int r, int, int q0) -> bool {
         const int slot = t & 1;
-        const int lo = validk ? (P.causal ? first_query(P.layout, P.D, wk.L, r, pk) - q0 : 0) : 128;
-        if (!mbar_wait(&sh.ls_full[slot], (t >> 1) & 1, abort_flag, tmo, status)) return false;
+        int lo, hi = 128;
+        if constexpr (WIN) {  // queries at pk .. pk + window - 1, or from pk + window on
+          const bool far = x.sink.r >= 0;
+          lo = validk && (!far || is_sink)
+                   ? first_query(P.layout, P.D, wk.L, r, far ? pk + P.window : pk) - q0
+                   : 128;
+          if (!far) hi = key_limit(P.layout, P.D, wk.L, r, pk + P.window - 1) + 1 - q0;
+        } else {
+          lo = validk ? (P.causal ? first_query(P.layout, P.D, wk.L, r, pk) - q0 : 0) : 128;
+        }
+        if (!wait(&sh.ls_full[slot], (t >> 1) & 1)) return false;
         const float* nl = ls_base + slot * 256;
         const float* dl = nl + 128;
         // P^T into X (bf16), kept in registers for dS^T
-        if (!mbar_wait(&sh.s_full, s_phase, abort_flag, tmo, status)) return false;
+        if (!wait(&sh.s_full, s_phase)) return false;
         s_phase ^= 1;
         tc_fence_after();
         uint32_t pp[32];
@@ -660,8 +868,8 @@ __global__ void __launch_bounds__(bwd_threads<kWithDQ>(), 1)
           tmem_ld32_nowait(tX + c0, s0);
           tmem_ld32_nowait(tX + c0 + 32, s1);
           tmem_wait_ld();
-          p_from<0>(s0, tX, c0, nl, sl2x2, lo, pp);
-          p_from<1>(s1, tX, c0, nl, sl2x2, lo, pp);
+          p_from<0, WIN>(s0, tX, c0, nl, sl2x2, lo, hi, pp);
+          p_from<1, WIN>(s1, tX, c0, nl, sl2x2, lo, hi, pp);
         } else if (wg == 0) {
           p_chunk<1>(tX, c0, nl, sl2x2, lo, pp);
           p_chunk<0>(tX, c0, nl, sl2x2, lo, pp);
@@ -674,7 +882,7 @@ __global__ void __launch_bounds__(bwd_threads<kWithDQ>(), 1)
         mbar_arrive(&sh.p_full);
         // dS^T = P^T * (dP^T - delta). Each chunk's output lands on dP^T columns this thread
         // has already read, so the chunk order differs between the two warpgroups.
-        if (!mbar_wait(&sh.dp_full, dp_phase, abort_flag, tmo, status)) return false;
+        if (!wait(&sh.dp_full, dp_phase)) return false;
         dp_phase ^= 1;
         tc_fence_after();
         if constexpr (!kWithDQ) {
@@ -697,7 +905,10 @@ __global__ void __launch_bounds__(bwd_threads<kWithDQ>(), 1)
         tc_fence_before();
         mbar_arrive(&sh.ds_full);
         return true;
-      });
+      };
+      bool ok;
+      if constexpr (WIN) ok = win_for_each_qtile(P, x, qtile);
+      else ok = for_each_qtile(P, it, wk, qtile);
       if (!ok) break;
       // dK (times scale; warpgroup 0) and dV (warpgroup 1) of this tile
       if (!mbar_wait(&sh.acc_done, ad_phase, abort_flag, tmo, status)) break;
@@ -709,7 +920,8 @@ __global__ void __launch_bounds__(bwd_threads<kWithDQ>(), 1)
       for (int c = 0; c < DH / 32; ++c) {
         uint32_t rr[32];
         tmem_ld32(tacc + c * 32, rr);
-        if (validk) {
+        if (is_sink) store_row32_f32(sink_row(P, x, b, wg) + c * 32, rr, mul);
+        if (store) {
           if constexpr (kAccum)
             add_row32_f32(static_cast<float*>(wg == 0 ? dk_out : dv_out) + out_off + c * 32, rr, mul);
           else
@@ -776,13 +988,31 @@ __global__ void __launch_bounds__(bwd_threads<kWithDQ>(), 1)
   }
 }
 
-template <int DH, bool kWithDQ, bool kAccum>
+// dk and dv of the sink rows: the sum of their slots. Block x: a sink row; y: sink shard and K/V
+// head; z: sequence. Threads: dk's head_dim elements, then dv's.
+template <int DH>
+__global__ void __launch_bounds__(2 * DH)
+    sink_sum_kernel(const __grid_constant__ Plan P, __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv) {
+  const SeqDesc& s = P.seq[blockIdx.z];
+  const int j = blockIdx.y / P.hkv, hk = blockIdx.y % P.hkv, row = blockIdx.x;
+  if (j >= sink_shards(P, s.L) || row >= sink_rows(P, s.L, j)) return;
+  const int which = threadIdx.x / DH, d = threadIdx.x % DH, n = sink_slots(P, s.L);
+  const int64_t slot = sink_slot(P, s, j, hk, 0);
+  const float* src = P.sink_sums + ((slot * 2 + which) * P.sinks + row) * DH + d;
+  float sum = 0.f;
+#pragma unroll 8
+  for (int i = 0; i < n; ++i) sum += src[static_cast<int64_t>(i) * 2 * P.sinks * DH];
+  const size_t at = (static_cast<size_t>(s.row_off + j * P.shard_stride + row) * P.hkv + hk) * DH + d;
+  (which ? dv : dk)[at] = __float2bfloat16_rn(sum);
+}
+
+template <int DH, bool kWithDQ, bool kAccum, bool WIN = false>
 cudaError_t launch_one(const Plan& P, const CUtensorMap& mq, const CUtensorMap& mk,
                        const CUtensorMap& mv, const CUtensorMap& mdo, const float* lse,
                        const float* delta, float* dq_acc, void* dk, void* dv, int n_sm,
                        cudaStream_t st) {
   using C = BwdCfg<DH>;
-  auto kern = ring_bwd_tc_kernel<DH, kWithDQ, kAccum>;
+  auto kern = ring_bwd_tc_kernel<DH, kWithDQ, kAccum, WIN>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        C::kSmemBytes);
   if (e != cudaSuccess) return e;
@@ -803,6 +1033,44 @@ cudaError_t launch_dh(const Plan& P, const CUtensorMap& mq, const CUtensorMap& m
 }
 
 }  // namespace
+
+int window_bwd_items(Plan& P) {
+  int items = 0, slots = 0;
+  for (int i = 0; i < P.n_seqs; ++i) {
+    SeqDesc& s = P.seq[i];
+    s.item_start = items;
+    s.sink_start = slots;
+    items += sink_items_of(P, s.L) + bwd_items_of(P, s.L);
+    slots += sink_shards(P, s.L) * P.hkv * sink_slots(P, s.L);
+  }
+  P.n_items = items;
+  return slots;
+}
+
+cudaError_t launch_window_bwd_tc(const Plan& P, const void* q, const void* k, const void* v, const void* dout,
+                                 const float* lse, const float* delta, void* dk, void* dv, cudaStream_t st) {
+  if (P.n_items == 0) return cudaSuccess;
+  CUtensorMap mq, mk, mv, mdo;
+  cudaError_t e = make_token_tmap(&mq, q, P.n_rows, P.hq, P.head_dim);
+  if (e == cudaSuccess) e = make_token_tmap(&mk, k, P.n_rows, P.hkv, P.head_dim);
+  if (e == cudaSuccess) e = make_token_tmap(&mv, v, P.n_rows, P.hkv, P.head_dim);
+  if (e == cudaSuccess) e = make_token_tmap(&mdo, dout, P.n_rows, P.hq, P.head_dim);
+  if (e != cudaSuccess) return e;
+  int dev = 0, n_sm = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
+  e = P.head_dim == 128
+          ? launch_one<128, false, false, true>(P, mq, mk, mv, mdo, lse, delta, nullptr, dk, dv, n_sm, st)
+          : launch_one<64, false, false, true>(P, mq, mk, mv, mdo, lse, delta, nullptr, dk, dv, n_sm, st);
+  if (e != cudaSuccess || P.sinks == 0) return e;
+  int shards = 0;
+  for (int i = 0; i < P.n_seqs; ++i) shards = max(shards, sink_shards(P, P.seq[i].L));
+  const dim3 grid(P.sinks, shards * P.hkv, P.n_seqs);
+  __nv_bfloat16 *ok = static_cast<__nv_bfloat16*>(dk), *ov = static_cast<__nv_bfloat16*>(dv);
+  if (P.head_dim == 128) sink_sum_kernel<128><<<grid, 256, 0, st>>>(P, ok, ov);
+  else sink_sum_kernel<64><<<grid, 128, 0, st>>>(P, ok, ov);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_bwd_tc(const Plan& P, BwdKind kind, const void* q, const void* k, const void* v,
                           const void* dout, const float* lse, const float* delta, float* dq_acc,

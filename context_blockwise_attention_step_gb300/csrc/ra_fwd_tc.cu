@@ -30,11 +30,16 @@
 // goes to S columns [32, 96), each half on its own S columns. The two tiles ping-pong: the
 // MMA order S0(n) S1(n) | O0(n) S0(n+1) O1(n) S1(n+1) | ... lets one tile's softmax run
 // while the tensor core works on the other tile.
+//
+// WIN (sliding window with always visible first tokens): a block walks the K/V tiles that some
+// of its rows sees through the window, and the first tile of the shards that hold sinks; the
+// producer warp counts them and hands the count to the MMA thread with the item.
 #include <cuda_runtime.h>
 
 #include "ra_internal.h"
 #include "ra_plan.h"
 #include "ra_ptx.cuh"
+#include "ra_window.cuh"
 
 namespace ra {
 
@@ -69,6 +74,7 @@ struct FwdShared {
   uint64_t xmax_bar[2][2], xl_bar[2];  // half-row exchanges: [tile][slot], [tile]
   uint64_t item_full[2], item_empty[2];  // the CTA's item queue
   int item[2];
+  int item_tiles[2];  // windowed: K/V tiles of the item
   uint32_t tmem_base;
   int abort_flag;
   float xmax[2][2][2][128];  // [tile][slot][half][row]: partial row maxima
@@ -81,6 +87,7 @@ struct FwdWalk {
   bool two;
 };
 
+template <bool WIN>
 __device__ __forceinline__ FwdWalk fwd_walk(const Plan& P, const FwdItem& it) {
   FwdWalk w;
   w.L = P.seq[it.seq].L;
@@ -89,9 +96,15 @@ __device__ __forceinline__ FwdWalk fwd_walk(const Plan& P, const FwdItem& it) {
   w.a_last = a_end - 1;
   w.two = (a_end - w.a0) > kQTileRows;
   w.N = 0;
-  for (int s = P.step_begin; s < P.step_end; ++s)
-    w.N += kv_tiles_for(P, w.L, it.r, shard_at_step(P.D, it.r, s), w.a_last);
+  if constexpr (!WIN)
+    for (int s = P.step_begin; s < P.step_end; ++s)
+      w.N += kv_tiles_for(P, w.L, it.r, shard_at_step(P.D, it.r, s), w.a_last);
   return w;
+}
+
+// Windowed: the K/V tiles of the shard that the item's rank holds at step s.
+__device__ __forceinline__ TileSet fwd_set(const Plan& P, const FwdItem& it, const FwdWalk& w, int s) {
+  return window_kv_tiles(P, w.L, it.r, shard_at_step(P.D, it.r, s), w.a0, w.a_last);
 }
 
 template <typename OutT>
@@ -133,15 +146,42 @@ __device__ __forceinline__ int fwd_item_publish(FwdShared& sh, const Plan& P, in
   return w;
 }
 __device__ __forceinline__ int fwd_item_take(FwdShared& sh, int k, volatile int* abort_flag,
-                                             uint64_t tmo, unsigned int* status) {
+                                             uint64_t tmo, unsigned int* status, int* tiles) {
   const int slot = k & 1;
   if (!mbar_wait(&sh.item_full[slot], (k >> 1) & 1, abort_flag, tmo, status)) return -1;
   const int w = *reinterpret_cast<volatile int*>(&sh.item[slot]);
+  if (tiles != nullptr) *tiles = *reinterpret_cast<volatile int*>(&sh.item_tiles[slot]);
   mbar_arrive(&sh.item_empty[slot]);
   return w;
 }
 
-template <int DH, typename OutT>
+// The windowed kernel's producer warp: takes the next item, counts its tiles, publishes both.
+__device__ __forceinline__ int fwd_window_publish(FwdShared& sh, const Plan& P, int k, int lane,
+                                                  volatile int* abort_flag, uint64_t tmo,
+                                                  unsigned int* status) {
+  const int slot = k & 1;
+  const bool ok = mbar_wait(&sh.item_empty[slot], ((k >> 1) & 1) ^ 1, abort_flag, tmo, status);
+  if (!__all_sync(0xffffffffu, ok)) return -1;
+  int w = 0;
+  if (lane == 0)
+    w = P.work_counter ? atomicAdd(P.work_counter, 1)
+                       : static_cast<int>(blockIdx.x + static_cast<unsigned>(k) * gridDim.x);
+  w = __shfl_sync(0xffffffffu, w, 0);
+  int n = 0;
+  if (w < P.n_items) {
+    const FwdItem it = decode_fwd(P, w);
+    const FwdWalk wk = fwd_walk<true>(P, it);
+    n = count_tiles(P.D, [&](int s) { return fwd_set(P, it, wk, s); });
+  }
+  if (lane == 0) {
+    sh.item[slot] = w;
+    sh.item_tiles[slot] = n;
+    mbar_arrive(&sh.item_full[slot]);
+  }
+  return w;
+}
+
+template <int DH, typename OutT, bool WIN>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     ring_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
                        const __grid_constant__ CUtensorMap tmK,
@@ -199,14 +239,65 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA producer
-    if (lane == 0) {
+    if constexpr (WIN) {  // the whole warp walks, lane 0 issues
+      int kv_count = 0;
+      uint32_t q_phase = 0;
+      auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, tmo, status));
+      };
+      for (int kq = 0;; ++kq) {
+        const int w = fwd_window_publish(sh, P, kq, lane, abort_flag, tmo, status);
+        if (w < 0 || w >= P.n_items) break;
+        const FwdItem it = decode_fwd(P, w);
+        const FwdWalk wk = fwd_walk<WIN>(P, it);
+        const SeqDesc& sd = P.seq[it.seq];
+        if (!wait(&sh.q_empty, q_phase ^ 1)) break;
+        q_phase ^= 1;
+        if (lane == 0) {
+          mbar_expect_tx(&sh.q_full, (wk.two ? 2 : 1) * C::kTileBytes);
+          const int qrow = sd.row_off + it.r * P.shard_stride + wk.a0;
+          for (int t = 0; t < (wk.two ? 2 : 1); ++t)
+            for (int d = 0; d < C::kSub; ++d)
+              tma_load_3d(smem + C::kOffQ + t * C::kTileBytes + d * kSubBytes, &tmQ, &sh.q_full,
+                          d * 64, it.h, qrow + t * kQTileRows);
+        }
+        const int hk = it.h / P.group;
+        const bool ok = for_each_set(
+            P.D, [&](int s) { return fwd_set(P, it, wk, s); },
+            [&](int s, const TileSet& set) -> bool {
+              const int krow = sd.row_off + shard_at_step(P.D, it.r, s) * P.shard_stride;
+              const int nb = tile_count(set);
+              for (int i = 0; i < nb; ++i, ++kv_count) {
+                const int row = krow + tile_at(set, i) * kKvTileRows;
+                const int st = kv_count % C::kStages;
+                const uint32_t ph = (kv_count / C::kStages) & 1;
+                if (!wait(&sh.k_empty[st], ph ^ 1)) return false;
+                if (lane == 0) {
+                  mbar_expect_tx(&sh.k_full[st], C::kTileBytes);
+                  for (int d = 0; d < C::kSub; ++d)
+                    tma_load_3d(smem + C::kOffK + st * C::kTileBytes + d * kSubBytes, &tmK,
+                                &sh.k_full[st], d * 64, hk, row);
+                }
+                if (!wait(&sh.v_empty[st], ph ^ 1)) return false;
+                if (lane == 0) {
+                  mbar_expect_tx(&sh.v_full[st], C::kTileBytes);
+                  for (int d = 0; d < C::kSub; ++d)
+                    tma_load_3d(smem + C::kOffV + st * C::kTileBytes + d * kSubBytes, &tmV,
+                                &sh.v_full[st], d * 64, hk, row);
+                }
+              }
+              return true;
+            });
+        if (!ok) break;
+      }
+    } else if (lane == 0) {
       int kv_count = 0;
       uint32_t q_phase = 0;
       for (int kq = 0;; ++kq) {
         const int w = fwd_item_publish(sh, P, kq, abort_flag, tmo, status);
         if (w < 0 || w >= P.n_items) break;
         const FwdItem it = decode_fwd(P, w);
-        const FwdWalk wk = fwd_walk(P, it);
+        const FwdWalk wk = fwd_walk<WIN>(P, it);
         if (wk.N == 0) continue;
         const SeqDesc& sd = P.seq[it.seq];
         if (!mbar_wait(&sh.q_empty, q_phase ^ 1, abort_flag, tmo, status)) goto producer_done;
@@ -254,12 +345,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const uint32_t sV = smem_u32(smem + C::kOffV);
       bool ok = true;
       for (int kq = 0; ok; ++kq) {
-        const int w = fwd_item_take(sh, kq, abort_flag, tmo, status);
+        int tiles = 0;
+        const int w = fwd_item_take(sh, kq, abort_flag, tmo, status, WIN ? &tiles : nullptr);
         if (w < 0) ok = false;
         if (w < 0 || w >= P.n_items) break;
         const FwdItem it = decode_fwd(P, w);
-        const FwdWalk wk = fwd_walk(P, it);
-        const int N = wk.N;
+        const FwdWalk wk = fwd_walk<WIN>(P, it);
+        const int N = WIN ? tiles : wk.N;
         if (N == 0) continue;
         const int nt = wk.two ? 2 : 1;
         if (!(ok = mbar_wait(&sh.q_full, q_phase, abort_flag, tmo, status))) break;
@@ -338,10 +430,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     uint32_t xm_phase[2] = {0, 0};
     int xn = 0;  // max exchanges done (slot = xn & 1)
     for (int kq = 0;; ++kq) {
-      const int w = fwd_item_take(sh, kq, abort_flag, tmo, status);
+      const int w = fwd_item_take(sh, kq, abort_flag, tmo, status, nullptr);
       if (w < 0 || w >= P.n_items) break;
       const FwdItem it = decode_fwd(P, w);
-      const FwdWalk wk = fwd_walk(P, it);
+      const FwdWalk wk = fwd_walk<WIN>(P, it);
       if (t == 1 && !wk.two) continue;
       const SeqDesc& sd = P.seq[it.seq];
       const int a = wk.a0 + t * kQTileRows + row;
@@ -350,7 +442,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       OutT* orow_ptr = out + (static_cast<size_t>(orow) * P.hq + it.h) * DH;
       float* lse_ptr = lse + sd.lse_off + static_cast<size_t>(it.h) * P.lse_hstride +
                        static_cast<size_t>(it.r) * P.shard_stride + a;
-      if (wk.N == 0) {  // a block with no visible key at these steps
+      if (!WIN && wk.N == 0) {  // a block with no visible key at these steps
         if (valid) {
           float z[32];
 #pragma unroll
@@ -365,17 +457,39 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       float m = -INFINITY, l = 0.f;
       int n = 0;
       bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        const bool got = mbar_wait(bar, parity, abort_flag, tmo, status);
+        return WIN ? __all_sync(0xffffffffu, got) : got;  // the windowed walk is the warp's
+      };
+      unsigned shards = 0;  // windowed: the next 32 steps' shards that have tiles
       for (int s = P.step_begin; s < P.step_end && ok; ++s) {
+        if constexpr (WIN) {
+          if ((s & 31) == 0) shards = nonempty(P.D, s, [&](int i) { return fwd_set(P, it, wk, i); });
+          if (!((shards >> (s & 31)) & 1u)) continue;
+        }
         const int j = shard_at_step(P.D, it.r, s);
-        const int nb = kv_tiles_for(P, wk.L, it.r, j, wk.a_last);
+        TileSet set;
+        if constexpr (WIN) set = fwd_set(P, it, wk, s);
+        const int nb = WIN ? tile_count(set) : kv_tiles_for(P, wk.L, it.r, j, wk.a_last);
         const int lim = !valid ? -1 : (P.causal ? key_limit(P.layout, P.D, wk.L, j, pq) : wk.L - 1);
-        for (int b = 0; b < nb; ++b, ++n) {
-          if (!(ok = mbar_wait(&sh.s_full[t], s_phase, abort_flag, tmo, status))) break;
+        // windowed: of the shard's keys up to lim this row sees those before sk, and from lo on
+        const int lo = WIN ? first_query(P.layout, P.D, wk.L, j, pq - P.window + 1) : 0;
+        const int sk = WIN ? sink_rows(P, wk.L, j) : 0;
+        for (int i = 0; i < nb; ++i, ++n) {
+          const int b = WIN ? tile_at(set, i) : i;
+          if (!(ok = wait(&sh.s_full[t], s_phase))) break;
           s_phase ^= 1;
           tc_fence_after();
           int cnt = lim + 1 - b * kKvTileRows;
           cnt = cnt < 0 ? 0 : (cnt > kKvTileRows ? kKvTileRows : cnt);
-          const bool full = __all_sync(0xffffffffu, cnt == kKvTileRows);  // no mask needed
+          const int lo_t = WIN ? lo - b * kKvTileRows : 0, sk_t = WIN && b == 0 ? sk : 0;
+          const bool full =  // no mask needed
+              __all_sync(0xffffffffu, cnt == kKvTileRows && (!WIN || lo_t <= sk_t));
+          uint32_t vis[2];
+          if constexpr (WIN) {
+            vis[0] = visible_bits(c0, cnt, lo_t, sk_t);
+            vis[1] = visible_bits(c0 + 32, cnt, lo_t, sk_t);
+          }
           // pass 1: partial row max over this half's visible columns, then both halves'
           uint32_t r2[2][32];
           tmem_ld32_nowait(tS + c0, r2[0]);
@@ -398,7 +512,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
               for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
-                  const float v = (c0 + 32 * h + i < cnt) ? __uint_as_float(r2[h][i]) : -INFINITY;
+                  const bool see = WIN ? (vis[h] >> i) & 1u : c0 + 32 * h + i < cnt;
+                  const float v = see ? __uint_as_float(r2[h][i]) : -INFINITY;
                   mq[2 * h + (i & 1)] = fmaxf(mq[2 * h + (i & 1)], v);
                 }
             }
@@ -408,7 +523,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             const int slot = xn & 1;
             sh.xmax[t][slot][hf][row] = mx;
             mbar_arrive(&sh.xmax_bar[t][slot]);
-            if (!(ok = mbar_wait(&sh.xmax_bar[t][slot], xm_phase[slot], abort_flag, tmo, status))) break;
+            if (!(ok = wait(&sh.xmax_bar[t][slot], xm_phase[slot]))) break;
             xm_phase[slot] ^= 1;
             mx = fmaxf(mx, sh.xmax[t][slot][hf ^ 1][row]);
             ++xn;
@@ -461,7 +576,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             if (!full) {
 #pragma unroll
               for (int i = 0; i < 32; ++i)
-                if (cs + i >= cnt) ev[i] = 0.f;
+                if (WIN ? !((vis[ch] >> i) & 1u) : cs + i >= cnt) ev[i] = 0.f;
             }
             uint64_t la = f2(0.f, 0.f);
 #pragma unroll
@@ -540,11 +655,11 @@ __global__ void exp2_poly_kernel(const float* __restrict__ x, float* __restrict_
   if (i + 1 < n) y[i + 1] = r.y;
 }
 
-template <int DH, typename OutT>
+template <int DH, typename OutT, bool WIN>
 cudaError_t launch_one(const Plan& P, const CUtensorMap& mq, const CUtensorMap& mk,
                        const CUtensorMap& mv, OutT* out, float* lse, int n_sm, cudaStream_t st) {
   using C = FwdCfg<DH>;
-  auto kern = ring_fwd_tc_kernel<DH, OutT>;
+  auto kern = ring_fwd_tc_kernel<DH, OutT, WIN>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        C::kSmemBytes);
   if (e != cudaSuccess) return e;
@@ -566,12 +681,20 @@ cudaError_t launch_fwd_tc(const Plan& P, const void* q, const void* k, const voi
   int dev = 0, n_sm = 0;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
-  if (P.head_dim == 128) {
-    return P.out_f32 ? launch_one<128, float>(P, mq, mk, mv, static_cast<float*>(out), lse, n_sm, st)
-                     : launch_one<128, __nv_bfloat16>(P, mq, mk, mv, static_cast<__nv_bfloat16*>(out), lse, n_sm, st);
+  using B = __nv_bfloat16;
+  if (P.window > 0) {  // (block outputs, the float32 ones, have no window)
+    B* o = static_cast<B*>(out);
+    return P.head_dim == 128 ? launch_one<128, B, true>(P, mq, mk, mv, o, lse, n_sm, st)
+                             : launch_one<64, B, true>(P, mq, mk, mv, o, lse, n_sm, st);
   }
-  return P.out_f32 ? launch_one<64, float>(P, mq, mk, mv, static_cast<float*>(out), lse, n_sm, st)
-                   : launch_one<64, __nv_bfloat16>(P, mq, mk, mv, static_cast<__nv_bfloat16*>(out), lse, n_sm, st);
+  if (P.out_f32) {
+    float* o = static_cast<float*>(out);
+    return P.head_dim == 128 ? launch_one<128, float, false>(P, mq, mk, mv, o, lse, n_sm, st)
+                             : launch_one<64, float, false>(P, mq, mk, mv, o, lse, n_sm, st);
+  }
+  B* o = static_cast<B*>(out);
+  return P.head_dim == 128 ? launch_one<128, B, false>(P, mq, mk, mv, o, lse, n_sm, st)
+                           : launch_one<64, B, false>(P, mq, mk, mv, o, lse, n_sm, st);
 }
 
 cudaError_t launch_exp2_poly(const float* x, float* y, int n, cudaStream_t st) {

@@ -31,6 +31,12 @@ cudaError_t launch_bwd_tc(const Plan& P, BwdKind kind, const void* q, const void
 cudaError_t launch_bwd_dq_tc(const Plan& P, const void* q, const void* k, const void* v,
                              const void* dout, const float* lse, const float* delta, void* dq,
                              cudaStream_t st);
+// Windowed K/V pass: numbers the plan's items and sink slots (returns the slots, each of 2 *
+// sinks * head_dim floats of P.sink_sums); dk and dv, the sinks' rows summed from the slots.
+int window_bwd_items(Plan& P);
+cudaError_t launch_window_bwd_tc(const Plan& P, const void* q, const void* k, const void* v,
+                                 const void* dout, const float* lse, const float* delta, void* dk,
+                                 void* dv, cudaStream_t st);
 cudaError_t bwd_dq_status(unsigned int* value, bool reset);
 cudaError_t launch_wait_timeout(uint64_t timeout_ns, cudaStream_t st);
 cudaError_t launch_exp2_poly(const float* x, float* y, int n, cudaStream_t st);

@@ -2,7 +2,9 @@
 
 Tolerances: bf16 out: the weights are rounded once (2^-8) and the result once, so |err| <= 2^-8
 |out| + 1.1 * 2^-8 * sum p |v| elementwise; lse 2^-12 (float32 scores of size < 8 over 128
-products). Gradients: four roundings of at most 2^-8 each (weights, dS, the stored out inside
+products). Gradients: dP and delta are float32 sums of dh <= 128 products, each off by at most dh
+* 2^-24 * sum |dO v| < 7e-4 here, which times scale and a few keys of size 1 is below 1e-4 an
+element (it shows where dP - delta is 0 in exact arithmetic: a query of one key); and four roundings of at most 2^-8 each (weights, dS, the stored out inside
 delta, the result), independent: 2^-7 in relative L2. Float32: 1e-5 (out, lse absolute;
 gradients relative L2), as for the ring calls.
 """
@@ -12,8 +14,6 @@ import torch
 
 import context_blockwise_attention_step_gb300 as ra
 from oracle import heads as H
-
-from _gpu_path import rel_l2
 
 pytestmark = pytest.mark.gpu
 
@@ -29,6 +29,12 @@ def _build():
 
 def f64(t):
     return t.detach().double().cpu().numpy()
+
+
+def check_l2(got, ref, dt, what):
+    off, size = np.linalg.norm(got - ref), np.linalg.norm(ref)
+    tol = (2.0 ** -7 * size + 1e-4 * ref.size ** 0.5) if dt == BF16 else 1e-5 * size
+    assert off <= tol, f"{what}: off by {off:.3e} of {size:.3e}, allowed {tol:.3e}"
 
 
 def randn(seed, *shape, dtype=BF16):
@@ -108,13 +114,11 @@ def test_window_forward_and_backward(case):
     for name, got, ref in zip(("dq", "dk", "dv"), nat[1:], refs[1:]):
         ref = np.concatenate(ref)
         assert np.isfinite(got).all(), name
-        e = rel_l2(got, ref)
-        assert e <= (2.0 ** -7 if dt == BF16 else 1e-5), f"{name}: rel-L2 {e:.3e}"
+        check_l2(got, ref, dt, name)
         # and where it is easiest to go wrong: the sinks' own rows of every sequence
         first = np.concatenate([np.arange(min(n, max(sinks, 1))) + s for s, n in
                                 zip(np.concatenate([[0], np.cumsum(lens)[:-1]]), lens) if n])
-        e = rel_l2(got[first], ref[first])
-        assert e <= (2.0 ** -7 if dt == BF16 else 1e-5), f"{name} of the first rows: rel-L2 {e:.3e}"
+        check_l2(got[first], ref[first], dt, name + " of the first rows")
 
 
 @pytest.mark.parametrize("case", [CASES[1], CASES[9], CASES[15]], ids=["basic", "varlen", "f32"])
