@@ -16,6 +16,7 @@
 
 #include "ra_internal.h"
 #include "ra_layout.h"
+#include "ra_ptx.cuh"
 
 namespace ra {
 
@@ -305,6 +306,308 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
+// ---------------------------------------------------------------- head size 64 or 128, 16-byte loads
+// A head is held by LANES lanes, each with two 16-byte pieces: c-th of the first half and c-th
+// of the second half of the head, so that both members of a rotated pair (half-split or
+// interleaved) are in one thread, and the HEADS heads of a warp are loaded 128 bytes at a time.
+template <typename T, int DH>
+struct Vec {
+  static constexpr int N = 16 / sizeof(T);          // elements of a piece
+  static constexpr int LANES = DH / 2 / N;          // lanes of a head
+  static constexpr int HEADS = 32 / LANES;          // heads of a warp at a time
+  static constexpr int PER = N / HEADS > 0 ? N / HEADS : 1;  // angles a lane works out
+};
+
+template <typename T, int DH>
+struct Piece {  // a lane's two pieces, as loaded
+  uint4 a, b;
+};
+template <typename T, int DH>
+__device__ __forceinline__ Piece<T, DH> load_piece(const T* head, int c) {
+  Piece<T, DH> p;
+  p.a = *reinterpret_cast<const uint4*>(head + c * Vec<T, DH>::N);
+  p.b = *reinterpret_cast<const uint4*>(head + DH / 2 + c * Vec<T, DH>::N);
+  return p;
+}
+template <typename T, int DH>
+__device__ __forceinline__ void store_piece(T* head, int c, const Piece<T, DH>& p) {
+  *reinterpret_cast<uint4*>(head + c * Vec<T, DH>::N) = p.a;
+  *reinterpret_cast<uint4*>(head + DH / 2 + c * Vec<T, DH>::N) = p.b;
+}
+
+__device__ __forceinline__ void widen(const uint4& v, float (&x)[4]) {
+  x[0] = __uint_as_float(v.x);
+  x[1] = __uint_as_float(v.y);
+  x[2] = __uint_as_float(v.z);
+  x[3] = __uint_as_float(v.w);
+}
+__device__ __forceinline__ void widen(const uint4& v, float (&x)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ uint4 narrow(const float (&x)[4]) {
+  return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+}
+__device__ __forceinline__ uint4 narrow(const float (&x)[8]) {
+  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                    pack_bf16x2(x[6], x[7]));
+}
+
+// Cosines and sines of the pairs of this lane's pieces. The HEADS lanes that hold the same
+// pieces of different heads need the same angles: each works out its share, and they exchange.
+template <typename T, int DH, bool INTER>
+__device__ __forceinline__ void piece_angles(const HeadArgs& A, int64_t pos, int lane,
+                                             float (&cs)[Vec<T, DH>::N], float (&sn)[Vec<T, DH>::N]) {
+  using V = Vec<T, DH>;
+  const int c = lane % V::LANES, sub = lane / V::LANES;
+  float2 mine[V::PER];
+#pragma unroll
+  for (int k = 0; k < V::PER; ++k) {
+    const int j = (sub * V::PER + k) % V::N;
+    const int pair = !INTER ? c * V::N + j : j < V::N / 2 ? c * V::N / 2 + j : DH / 4 + c * V::N / 2 + j - V::N / 2;
+    mine[k] = cos_sin(A.rope.turns[pair], pos);
+  }
+#pragma unroll
+  for (int j = 0; j < V::N; ++j) {
+    const int from = j / V::PER * V::LANES + c;
+    cs[j] = __shfl_sync(0xffffffffu, mine[j % V::PER].x, from);
+    sn[j] = __shfl_sync(0xffffffffu, mine[j % V::PER].y, from);
+  }
+}
+
+// Turns a lane's pieces by +angle (sign 1) or -angle (sign -1).
+template <int N, bool INTER>
+__device__ __forceinline__ void turn(float (&a)[N], float (&b)[N], const float (&cs)[N], const float (&sn)[N],
+                                     float sign) {
+  if constexpr (INTER) {
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) {
+      const float x = a[2 * j], y = a[2 * j + 1], s = sign * sn[j];
+      a[2 * j] = x * cs[j] - y * s;
+      a[2 * j + 1] = y * cs[j] + x * s;
+      const float u = b[2 * j], v = b[2 * j + 1], t = sign * sn[N / 2 + j];
+      b[2 * j] = u * cs[N / 2 + j] - v * t;
+      b[2 * j + 1] = v * cs[N / 2 + j] + u * t;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const float x = a[j], y = b[j], s = sign * sn[j];
+      a[j] = x * cs[j] - y * s;
+      b[j] = y * cs[j] + x * s;
+    }
+  }
+}
+
+template <int LANES>
+__device__ __forceinline__ float group_sum(float x) {
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// The heads `first`, `first + step`, ... (in warps' loads of HEADS heads) of one token's q, k or
+// v: U loads in flight, then norm, rotation and store of each. The token's cosines and sines
+// are in registers.
+template <typename T, int DH, bool INTER, int U>
+__device__ __forceinline__ void head_run(const HeadArgs& A, const T* __restrict__ w, bool turned, const T* src,
+                                         T* dst, int64_t dst_head, int heads, int first, int step, int lane,
+                                         const float (&cs)[Vec<T, DH>::N], const float (&sn)[Vec<T, DH>::N]) {
+  using V = Vec<T, DH>;
+  const int c = lane % V::LANES, sub = lane / V::LANES;
+  const int runs = (heads + V::HEADS - 1) / V::HEADS;
+  Piece<T, DH> wp;
+  if (w != nullptr) wp = load_piece<T, DH>(w, c);
+  for (int i0 = first; i0 < runs; i0 += step * U) {
+    Piece<T, DH> p[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int h = (i0 + u * step) * V::HEADS + sub;
+      if (h < heads) p[u] = load_piece<T, DH>(src + h * DH, c);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int h = (i0 + u * step) * V::HEADS + sub;
+      if (i0 + u * step >= runs) break;  // (the same for the whole warp)
+      if (w != nullptr || turned) {
+        float a[V::N], b[V::N];
+        widen(p[u].a, a);
+        widen(p[u].b, b);
+        if (w != nullptr) {
+          float ss = 0.f, wa[V::N], wb[V::N];
+#pragma unroll
+          for (int j = 0; j < V::N; ++j) ss += a[j] * a[j] + b[j] * b[j];
+          const float r = rsqrtf(group_sum<V::LANES>(ss) * (1.f / DH) + A.eps);
+          widen(wp.a, wa);
+          widen(wp.b, wb);
+#pragma unroll
+          for (int j = 0; j < V::N; ++j) {
+            a[j] *= r * wa[j];
+            b[j] *= r * wb[j];
+          }
+        }
+        if (turned) turn<V::N, INTER>(a, b, cs, sn, 1.f);
+        p[u].a = narrow(a);
+        p[u].b = narrow(b);
+      }
+      if (h < heads) store_piece<T, DH>(dst + h * dst_head, c, p[u]);
+    }
+  }
+}
+
+// A warp takes a token, or one of `parts` shares of its heads.
+template <typename T, int DH, bool INTER, typename Rows, bool CACHE>
+__global__ void __launch_bounds__(kThreads)
+    heads_fwd_vec(const __grid_constant__ HeadArgs A, const __grid_constant__ Rows R, int parts,
+                  const T* __restrict__ qw, const T* __restrict__ kw, const T* q, const T* k, const T* v,
+                  T* q_out, T* k_out, T* v_out) {
+  using V = Vec<T, DH>;
+  const int lane = threadIdx.x & 31;
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int64_t t = unit / parts;
+  const int part = static_cast<int>(unit - t * parts);
+  if (t >= A.n_rows) return;
+  const Token tok = locate(R, static_cast<int>(t), A.hkv * static_cast<int64_t>(DH));
+  if (tok.absent) return;
+  T* qo = q_out + t * A.hq * DH;
+  if (tok.idle) {
+    for (int h = part * V::HEADS + lane / V::LANES; h < A.hq; h += parts * V::HEADS) {
+      Piece<T, DH> zero = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+      store_piece<T, DH>(qo + h * DH, lane % V::LANES, zero);
+    }
+    return;
+  }
+  float cs[V::N], sn[V::N];
+  const bool turned = A.rope.rotary_dim > 0;
+  if (turned) piece_angles<T, DH, INTER>(A, tok.pos, lane, cs, sn);
+  constexpr int U = 4;
+  head_run<T, DH, INTER, U>(A, qw, turned, q + t * A.q_stride, qo, DH, A.hq, part, parts, lane, cs, sn);
+  // the next run of heads goes on with the part after the last one's
+  const int runs_q = (A.hq + V::HEADS - 1) / V::HEADS, runs_k = (A.hkv + V::HEADS - 1) / V::HEADS;
+  const int pk = ((part - runs_q) % parts + parts) % parts;
+  head_run<T, DH, INTER, 2>(A, kw, turned, k + t * A.k_stride, k_out + tok.kv, A.kv_head, A.hkv, pk, parts, lane,
+                            cs, sn);
+  if constexpr (CACHE) {
+    const int pv = ((pk - runs_k) % parts + parts) % parts;
+    head_run<T, DH, INTER, 2>(A, nullptr, false, v + t * A.v_stride, v_out + tok.kv, A.kv_head, A.hkv, pv, parts,
+                              lane, cs, sn);
+  }
+}
+
+constexpr int kBwdThreads = 128;
+
+// Backward of one token's q or k heads; `acc` gathers g * n of the lane's elements.
+template <typename T, int DH, bool INTER, int U>
+__device__ __forceinline__ void head_run_bwd(const HeadArgs& A, const T* __restrict__ w, bool turned, const T* x,
+                                             const T* dy, T* dx, int heads, int lane,
+                                             const float (&cs)[Vec<T, DH>::N], const float (&sn)[Vec<T, DH>::N],
+                                             float (&acc_a)[Vec<T, DH>::N], float (&acc_b)[Vec<T, DH>::N]) {
+  using V = Vec<T, DH>;
+  const int c = lane % V::LANES, sub = lane / V::LANES;
+  Piece<T, DH> wp;
+  if (w != nullptr) wp = load_piece<T, DH>(w, c);
+  for (int h0 = sub; h0 - sub < heads; h0 += V::HEADS * U) {
+    Piece<T, DH> g[U], p[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int h = h0 + u * V::HEADS;
+      g[u].a = g[u].b = p[u].a = p[u].b = make_uint4(0u, 0u, 0u, 0u);
+      if (h < heads) {
+        g[u] = load_piece<T, DH>(dy + h * DH, c);
+        if (w != nullptr) p[u] = load_piece<T, DH>(x + h * DH, c);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int h = h0 + u * V::HEADS;
+      if (h - sub >= heads) break;  // (the same for the whole warp)
+      float a[V::N], b[V::N];
+      widen(g[u].a, a);
+      widen(g[u].b, b);
+      if (turned) turn<V::N, INTER>(a, b, cs, sn, -1.f);
+      if (w != nullptr) {
+        float xa[V::N], xb[V::N], wv[V::N], ss = 0.f, hn = 0.f;
+        widen(p[u].a, xa);
+        widen(p[u].b, xb);
+#pragma unroll
+        for (int j = 0; j < V::N; ++j) ss += xa[j] * xa[j] + xb[j] * xb[j];
+        const float r = rsqrtf(group_sum<V::LANES>(ss) * (1.f / DH) + A.eps);
+        widen(wp.a, wv);
+#pragma unroll
+        for (int j = 0; j < V::N; ++j) {
+          xa[j] *= r;
+          acc_a[j] += a[j] * xa[j];
+          a[j] *= wv[j];
+          hn += a[j] * xa[j];
+        }
+        widen(wp.b, wv);
+#pragma unroll
+        for (int j = 0; j < V::N; ++j) {
+          xb[j] *= r;
+          acc_b[j] += b[j] * xb[j];
+          b[j] *= wv[j];
+          hn += b[j] * xb[j];
+        }
+        const float mean = group_sum<V::LANES>(hn) * (1.f / DH);
+#pragma unroll
+        for (int j = 0; j < V::N; ++j) {
+          a[j] = r * (a[j] - xa[j] * mean);
+          b[j] = r * (b[j] - xb[j] * mean);
+        }
+      }
+      g[u].a = narrow(a);
+      g[u].b = narrow(b);
+      if (h < heads) store_piece<T, DH>(dx + h * DH, c, g[u]);
+    }
+  }
+}
+
+template <typename T, int DH, bool INTER>
+__global__ void __launch_bounds__(kBwdThreads, 4)
+    heads_bwd_vec(const __grid_constant__ HeadArgs A, const __grid_constant__ RingRows R,
+                  const T* __restrict__ qw, const T* __restrict__ kw, const T* __restrict__ q,
+                  const T* __restrict__ k, const T* dq_out, const T* dk_out, T* dq, T* dk,
+                  float* __restrict__ partial) {
+  using V = Vec<T, DH>;
+  constexpr int WARPS = kBwdThreads / 32;
+  __shared__ float sums[WARPS][2][DH];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool turned = A.rope.rotary_dim > 0;
+  float acc[2][2][V::N] = {};
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * WARPS + warp; t < A.n_rows;
+       t += static_cast<int64_t>(gridDim.x) * WARPS) {
+    float cs[V::N], sn[V::N];
+    if (turned) piece_angles<T, DH, INTER>(A, locate(R, static_cast<int>(t), 0).pos, lane, cs, sn);
+    const int64_t oq = t * A.hq * DH, ok = t * A.hkv * DH;
+    head_run_bwd<T, DH, INTER, 2>(A, qw, turned, q + t * A.q_stride, dq_out + oq, dq + oq, A.hq, lane, cs, sn,
+                                  acc[0][0], acc[0][1]);
+    head_run_bwd<T, DH, INTER, 2>(A, kw, turned, k + t * A.k_stride, dk_out + ok, dk + ok, A.hkv, lane, cs, sn,
+                                  acc[1][0], acc[1][1]);
+  }
+  if (qw == nullptr) return;
+#pragma unroll
+  for (int which = 0; which < 2; ++which)
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+      for (int j = 0; j < V::N; ++j) {
+        float x = acc[which][half][j];  // over the heads of the warp: lanes with the same pieces
+#pragma unroll
+        for (int o = V::LANES; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        if (lane < V::LANES) sums[warp][which][half * (DH / 2) + lane * V::N + j] = x;
+      }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * DH; i += kBwdThreads) {
+    float s = 0.f;
+    for (int w = 0; w < WARPS; ++w) s += sums[w][i / DH][i % DH];
+    partial[static_cast<int64_t>(blockIdx.x) * 2 * DH + i] = s;
+  }
+}
+
 // Sums the blocks' weight gradients: a block for 32 of the 2*dh columns, a warp-row for every
 // 32nd partial.
 __global__ void __launch_bounds__(1024)
@@ -382,10 +685,45 @@ void fill_args(HeadArgs* A, const ra_rope* rope, float eps, int hq, int hkv, int
   A->q_stride = A->k_stride = A->v_stride = 0;
 }
 
+// Whether the 16-byte kernels can take a call: a whole-head rotation or none, and rows that all
+// start on 16 bytes. (Measured at 131072 tokens, 32/8 heads of 128, bf16, forward and backward:
+// 16-byte kernels 1.2 ms, one warp a head 10.6 ms.)
+bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+bool can_vec(const HeadArgs& A, int elem) {
+  auto rows16 = [&](int64_t stride) { return stride * elem % 16 == 0; };
+  return (A.dh == 64 || A.dh == 128) && (A.rope.rotary_dim == 0 || A.rope.rotary_dim == A.dh) &&
+         rows16(A.q_stride) && rows16(A.k_stride) && rows16(A.v_stride) && rows16(A.kv_head);
+}
+
+template <typename T, int DH, bool INTER, typename Rows, bool CACHE>
+cudaError_t fwd_vec(const HeadArgs& A, const Rows& R, const void* qw, const void* kw, const void* q,
+                    const void* k, const void* v, void* q_out, void* k_out, void* v_out, cudaStream_t st) {
+  using V = Vec<T, DH>;
+  // Few tokens: their heads are shared between warps until there are 16 warps for every SM.
+  const int runs = (A.hq + V::HEADS - 1) / V::HEADS + (A.hkv + V::HEADS - 1) / V::HEADS * (CACHE ? 2 : 1);
+  const int want = (16 * sm_count() + A.n_rows - 1) / A.n_rows;
+  const int parts = want < 1 ? 1 : want > runs ? runs : want;
+  const int64_t units = static_cast<int64_t>(A.n_rows) * parts;
+  heads_fwd_vec<T, DH, INTER, Rows, CACHE><<<static_cast<unsigned>((units + kWarps - 1) / kWarps), kThreads, 0, st>>>(
+      A, R, parts, static_cast<const T*>(qw), static_cast<const T*>(kw), static_cast<const T*>(q),
+      static_cast<const T*>(k), static_cast<const T*>(v), static_cast<T*>(q_out), static_cast<T*>(k_out),
+      static_cast<T*>(v_out));
+  return cudaGetLastError();
+}
+
 template <typename T, typename Rows, bool CACHE>
 cudaError_t launch_fwd(const HeadArgs& A, const Rows& R, const void* qw, const void* kw,
                        const void* q, const void* k, const void* v, void* q_out, void* k_out,
-                       void* v_out, cudaStream_t st) {
+                       void* v_out, bool aligned, cudaStream_t st) {
+  if (aligned && can_vec(A, sizeof(T)) && aligned16(qw) && aligned16(kw) && aligned16(q) && aligned16(k) &&
+      aligned16(v) && aligned16(q_out) && aligned16(k_out) && aligned16(v_out)) {
+    const bool inter = A.rope.rotary_dim > 0 && A.rope.interleaved;
+    if (A.dh == 128)
+      return inter ? fwd_vec<T, 128, true, Rows, CACHE>(A, R, qw, kw, q, k, v, q_out, k_out, v_out, st)
+                   : fwd_vec<T, 128, false, Rows, CACHE>(A, R, qw, kw, q, k, v, q_out, k_out, v_out, st);
+    return inter ? fwd_vec<T, 64, true, Rows, CACHE>(A, R, qw, kw, q, k, v, q_out, k_out, v_out, st)
+                 : fwd_vec<T, 64, false, Rows, CACHE>(A, R, qw, kw, q, k, v, q_out, k_out, v_out, st);
+  }
   const int64_t units = static_cast<int64_t>(A.n_rows) * (A.hq + A.hkv * (CACHE ? 2 : 1));
   heads_fwd_any<T, Rows, CACHE><<<blocks_for(units, kWarps, 8 * sm_count()), kThreads, 0, st>>>(
       A, R, static_cast<const T*>(qw), static_cast<const T*>(kw), static_cast<const T*>(q),
@@ -394,15 +732,39 @@ cudaError_t launch_fwd(const HeadArgs& A, const Rows& R, const void* qw, const v
   return cudaGetLastError();
 }
 
+template <typename T, int DH, bool INTER>
+void bwd_vec(unsigned blocks, const HeadArgs& A, const RingRows& R, const void* qw, const void* kw, const void* q,
+             const void* k, const void* dq_out, const void* dk_out, void* dq, void* dk, float* partial,
+             cudaStream_t st) {
+  heads_bwd_vec<T, DH, INTER><<<blocks, kBwdThreads, 0, st>>>(
+      A, R, static_cast<const T*>(qw), static_cast<const T*>(kw), static_cast<const T*>(q),
+      static_cast<const T*>(k), static_cast<const T*>(dq_out), static_cast<const T*>(dk_out),
+      static_cast<T*>(dq), static_cast<T*>(dk), partial);
+}
+
 template <typename T>
 cudaError_t launch_bwd(const HeadArgs& A, const RingRows& R, const void* qw, const void* kw,
                        const void* q, const void* k, const void* dq_out, const void* dk_out,
                        void* dq, void* dk, float* partial, float* dqw, float* dkw, cudaStream_t st) {
-  const unsigned blocks = blocks_for(A.n_rows, kWarps, kHeadBwdBlocks);
-  heads_bwd_any<T><<<blocks, kThreads, 0, st>>>(
-      A, R, static_cast<const T*>(qw), static_cast<const T*>(kw), static_cast<const T*>(q),
-      static_cast<const T*>(k), static_cast<const T*>(dq_out), static_cast<const T*>(dk_out),
-      static_cast<T*>(dq), static_cast<T*>(dk), partial);
+  unsigned blocks;
+  if (can_vec(A, sizeof(T)) && aligned16(qw) && aligned16(kw) && aligned16(q) && aligned16(k) &&
+      aligned16(dq_out) && aligned16(dk_out) && aligned16(dq) && aligned16(dk)) {
+    blocks = blocks_for(A.n_rows, kBwdThreads / 32, kHeadBwdBlocks);
+    const bool inter = A.rope.rotary_dim > 0 && A.rope.interleaved;
+    if (A.dh == 128) {
+      if (inter) bwd_vec<T, 128, true>(blocks, A, R, qw, kw, q, k, dq_out, dk_out, dq, dk, partial, st);
+      else bwd_vec<T, 128, false>(blocks, A, R, qw, kw, q, k, dq_out, dk_out, dq, dk, partial, st);
+    } else {
+      if (inter) bwd_vec<T, 64, true>(blocks, A, R, qw, kw, q, k, dq_out, dk_out, dq, dk, partial, st);
+      else bwd_vec<T, 64, false>(blocks, A, R, qw, kw, q, k, dq_out, dk_out, dq, dk, partial, st);
+    }
+  } else {
+    blocks = blocks_for(A.n_rows, kWarps, kHeadBwdBlocks);
+    heads_bwd_any<T><<<blocks, kThreads, 0, st>>>(
+        A, R, static_cast<const T*>(qw), static_cast<const T*>(kw), static_cast<const T*>(q),
+        static_cast<const T*>(k), static_cast<const T*>(dq_out), static_cast<const T*>(dk_out),
+        static_cast<T*>(dq), static_cast<T*>(dk), partial);
+  }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || qw == nullptr) return e;
   weight_grad_sum<<<(2 * A.dh + 31) / 32, 1024, 0, st>>>(partial, blocks, A.dh, dqw, dkw);
@@ -499,9 +861,9 @@ extern "C" int ra_qk_norm_rope_fwd(const ra_problem* p, const ra_rope* rope, flo
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e =
       p->dtype == RA_F32
-          ? launch_fwd<float, RingRows, false>(A, R, q_weight, k_weight, q, k, nullptr, q_out, k_out, nullptr, st)
+          ? launch_fwd<float, RingRows, false>(A, R, q_weight, k_weight, q, k, nullptr, q_out, k_out, nullptr, true, st)
           : launch_fwd<__nv_bfloat16, RingRows, false>(A, R, q_weight, k_weight, q, k, nullptr, q_out, k_out,
-                                                       nullptr, st);
+                                                       nullptr, true, st);
   if (e != cudaSuccess) return record_error(RA_ERR_CUDA, "norm and rotation launch: %s", cudaGetErrorString(e));
   return record_error(RA_OK, "%s", "");
 }
@@ -597,12 +959,14 @@ extern "C" int ra_kv_cache_append(const ra_paged_cache* c, const ra_rope* rope, 
   A.k_stride = k_row_stride;
   A.v_stride = v_row_stride;
   A.kv_head = c->head_stride;
+  const int elem = c->dtype == RA_F32 ? 4 : 2;  // of the pages, kv_head is looked at with the rows
+  const bool pages16 = c->page_stride * elem % 16 == 0 && c->slot_stride * elem % 16 == 0;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e =
       c->dtype == RA_F32
-          ? launch_fwd<float, CacheRows, true>(A, R, q_weight, k_weight, q, k, v, q_out, c->k_pages, c->v_pages, st)
+          ? launch_fwd<float, CacheRows, true>(A, R, q_weight, k_weight, q, k, v, q_out, c->k_pages, c->v_pages, pages16, st)
           : launch_fwd<__nv_bfloat16, CacheRows, true>(A, R, q_weight, k_weight, q, k, v, q_out, c->k_pages,
-                                                       c->v_pages, st);
+                                                       c->v_pages, pages16, st);
   if (e != cudaSuccess) return record_error(RA_ERR_CUDA, "append launch: %s", cudaGetErrorString(e));
   return record_error(RA_OK, "%s", "");
 }
