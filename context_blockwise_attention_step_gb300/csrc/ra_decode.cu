@@ -78,6 +78,11 @@ __device__ __forceinline__ Visible visible(const DecodeArgs& A, int b, bool flag
   return v;
 }
 
+// The join kernel is launched while the main one runs (programmatic dependent launch), works out
+// what it has to join, and waits here for the main kernel's end.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_main() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 __device__ __forceinline__ int units_of(const DecodeArgs& A, int b) {
   return (visible(A, b, false).vis + kUnit - 1) / kUnit;
 }
@@ -232,11 +237,6 @@ __device__ __forceinline__ float lane_sums(float (&x)[N], int lane) {
   return x[0];
 }
 
-template <typename T> __device__ __forceinline__ float ldv(const T* p);
-template <> __device__ __forceinline__ float ldv<float>(const float* p) { return *p; }
-template <> __device__ __forceinline__ float ldv<__nv_bfloat16>(const __nv_bfloat16* p) {
-  return __bfloat162float(*p);
-}
 template <typename T> __device__ __forceinline__ void stv(T* p, float v);
 template <> __device__ __forceinline__ void stv<float>(float* p, float v) { *p = v; }
 template <> __device__ __forceinline__ void stv<__nv_bfloat16>(__nv_bfloat16* p, float v) {
@@ -250,21 +250,22 @@ __device__ __forceinline__ void store_lse(const DecodeArgs& A, int b, int h, flo
   A.lse[static_cast<int64_t>(b) * A.hq + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
-// Four warps, each 16 keys of a unit, four keys at a time; lane l holds elements l, l + 32, ...
+// Float32. Four warps, each 16 keys of a unit, four keys at a time; lane l holds elements l, l + 32, ...
 // of q, of the keys and of the sums, for HB query heads.
-template <typename T, int HB>
+template <int HB>
 __global__ void __launch_bounds__(kThreads) decode_simt(const __grid_constant__ DecodeArgs A) {
   constexpr int NI = 4;  // elements per lane: head_dim <= 128
   __shared__ int64_t scan[kThreads / 32 < 4 ? 4 : kThreads / 32];
   __shared__ float sm_m[4][HB], sm_l[4][HB], sm_o[4][HB][128];
+  launch_dependents();
   Share S;
   int64_t total;
   int ctas;
   if (!share_begin(A, S, scan, &total, &ctas)) return;
   const int64_t share0 = S.u;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, dh = A.dh;
-  const T* kp = static_cast<const T*>(A.k_pages);
-  const T* vp = static_cast<const T*>(A.v_pages);
+  const float* kp = static_cast<const float*>(A.k_pages);
+  const float* vp = static_cast<const float*>(A.v_pages);
   for (;;) {
     const int hk = S.pair / A.blocks_per_kv, blk = S.pair % A.blocks_per_kv;
     const int g0 = blk * HB, heads = min(HB, A.group - g0), h0 = hk * A.group + g0;
@@ -281,7 +282,7 @@ __global__ void __launch_bounds__(kThreads) decode_simt(const __grid_constant__ 
         const int d = lane + 32 * i;
         o[h][i] = 0.f;
         qr[h][i] = h < heads && d < dh
-                       ? ldv<T>(static_cast<const T*>(A.q) + (static_cast<int64_t>(S.b) * A.hq + h0 + h) * dh + d)
+                       ? *(static_cast<const float*>(A.q) + (static_cast<int64_t>(S.b) * A.hq + h0 + h) * dh + d)
                        : 0.f;
       }
     }
@@ -298,8 +299,8 @@ __global__ void __launch_bounds__(kThreads) decode_simt(const __grid_constant__ 
 #pragma unroll
           for (int i = 0; i < NI; ++i) {
             const int d = lane + 32 * i;
-            kr[j][i] = d < dh ? ldv<T>(kp + at + d) : 0.f;
-            vr[j][i] = d < dh ? ldv<T>(vp + at + d) : 0.f;
+            kr[j][i] = d < dh ? *(kp + at + d) : 0.f;
+            vr[j][i] = d < dh ? *(vp + at + d) : 0.f;
           }
         }
         float s[4 * HB];
@@ -368,7 +369,7 @@ __global__ void __launch_bounds__(kThreads) decode_simt(const __grid_constant__ 
 #pragma unroll
         for (int w = 0; w < 4; ++w) x += f[w] * sm_o[w][h][d];
         if (whole)
-          stv<T>(static_cast<T*>(A.out) + (static_cast<int64_t>(S.b) * A.hq + h0 + h) * dh + d, x * inv);
+          static_cast<float*>(A.out)[(static_cast<int64_t>(S.b) * A.hq + h0 + h) * dh + d] = x * inv;
         else
           part[h * (dh + 2) + d] = x;
       }
@@ -384,6 +385,311 @@ __global__ void __launch_bounds__(kThreads) decode_simt(const __grid_constant__ 
     __syncthreads();
     if (S.base + S.units >= S.end) break;
     share_next(A, S);
+  }
+}
+
+// ---------------------------------------------------------------- bf16: matrix instructions
+// Memory-bound: 4 * dh bytes of K and V per key and K/V head, whose 2 * heads * dh products go
+// through mma.sync m16n8k16 with the query heads of the K/V head as its 16 rows (the rows
+// beyond them are zero; tcgen05's 64 or 128 rows would be emptier still, and its operands would
+// have to go through shared memory in whole 128-row tiles). A warp takes 16 keys of each unit
+// and is on its own until its share of a pair is done: it copies its keys' rows by cp.async
+// into its own ring of stages (rows 16 bytes longer than the data, so that ldmatrix meets every
+// bank once), the page of the next tile's keys looked up while the copies of this one fly, and
+// keeps running max, sum and O = P V in registers. The ring runs on over the end of a pair.
+// S = Q K^T as [heads x keys], so that P is the A operand of P V without any exchange. O is
+// rescaled only when a row's max grows by more than 2^8 (the same values in exact arithmetic).
+// P is rounded to bf16 for the product (relative 2^-9 on average over hundreds of keys); its
+// sum is taken before, in float32.
+//
+// WIDE: more than 8 query heads per K/V head (rows 8..15 of the products are used).
+template <int DH, bool WIDE>
+struct MmaCfg {
+  static constexpr int PITCH = DH * 2 + 16;                  // bytes of a key's row in a stage
+  static constexpr int STAGE = 2 * 16 * PITCH;               // a warp's K and V of 16 keys
+  static constexpr int STAGES = DH == 128 ? 3 : 5;
+  static constexpr int RING = 4 * STAGES * STAGE;
+  static constexpr int CHUNK = 8192 / (4 * DH * 4);          // rows joined at a time
+  static constexpr int SMEM = RING + 8192;                   // two CTAs on an SM
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// A walk over the tiles of a CTA's share: the pieces (pairs) of the share, and their units.
+struct Cursor {
+  Share S;
+  Visible vis;
+  int hk, blk;  // K/V head, block of its query heads
+  int u, u1;    // next unit and last + 1 of this piece
+  bool more;
+
+  __device__ __forceinline__ void piece(const DecodeArgs& A, bool flag) {
+    hk = S.pair / A.blocks_per_kv;
+    blk = S.pair - hk * A.blocks_per_kv;
+    vis = visible(A, S.b, flag);
+    u = static_cast<int>(S.u - S.base);
+    u1 = static_cast<int>(min(static_cast<int64_t>(S.units), S.end - S.base));
+  }
+  __device__ __forceinline__ void begin(const DecodeArgs& A, const Share& share, bool flag) {
+    S = share;
+    more = true;
+    piece(A, flag);
+  }
+  __device__ __forceinline__ void next_piece(const DecodeArgs& A, bool flag) {
+    if (S.base + S.units >= S.end) {
+      more = false;
+      return;
+    }
+    share_next(A, S);
+    piece(A, flag);
+  }
+};
+
+template <int DH, bool WIDE>
+__global__ void __launch_bounds__(kThreads) decode_mma(const __grid_constant__ DecodeArgs A) {
+  using C = MmaCfg<DH, WIDE>;
+  constexpr int KS = DH / 16;                  // steps of 16 elements
+  constexpr int LANES = DH * 2 / 16;           // lanes that copy one row
+  constexpr int ROWS = 32 / LANES;             // rows of one copy instruction
+  constexpr int NS = C::STAGES;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int64_t scan[4];
+  __shared__ float sm_m[4][16], sm_l[4][16];
+  launch_dependents();
+  Share share;
+  int64_t total;
+  int ctas;
+  if (!share_begin(A, share, scan, &total, &ctas)) return;
+  const int64_t share0 = share.u;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+  const uint32_t ring = smem_u32(smem) + warp * NS * C::STAGE;
+  float* joined = reinterpret_cast<float*>(smem + C::RING);  // [4][CHUNK][DH]
+  const char* kp = static_cast<const char*>(A.k_pages);
+  const char* vp = static_cast<const char*>(A.v_pages);
+
+  // the load side: rows of the next tile's keys (lane i: key i; -1: no tile), then its copies
+  Cursor load;
+  load.begin(A, share, true);
+  int64_t row = -1;
+  auto look_up = [&]() {
+    row = -1;
+    if (!load.more) return;
+    const int key0 = load.u * kUnit + warp * 16;
+    if (key0 < load.vis.vis)
+      row = (key_row(A, load.S.b, load.vis, min(key0 + (lane & 15), load.vis.vis - 1)) + load.hk * A.head_stride) * 2;
+    if (++load.u == load.u1) load.next_piece(A, true);
+  };
+  auto copy = [&](int stage) {
+    if (__shfl_sync(0xffffffffu, row, 0) >= 0) {
+      const uint32_t dst = ring + stage * C::STAGE + (lane / LANES) * C::PITCH + (lane % LANES) * 16;
+#pragma unroll
+      for (int i = 0; i < 16 / ROWS; ++i) {
+        const int64_t at = __shfl_sync(0xffffffffu, row, i * ROWS + lane / LANES) + (lane % LANES) * 16;
+        cp_async16(dst + i * ROWS * C::PITCH, kp + at);
+        cp_async16(dst + i * ROWS * C::PITCH + 16 * C::PITCH, vp + at);
+      }
+    }
+    cp_async_commit();
+  };
+  look_up();
+#pragma unroll
+  for (int i = 0; i < NS - 1; ++i) {
+    copy(i);
+    look_up();
+  }
+
+  int stage = 0;
+  Cursor at;
+  at.begin(A, share, false);
+  while (at.more) {
+    const int heads = min(A.block_heads, A.group - at.blk * A.block_heads);
+    const int h0 = at.hk * A.group + at.blk * A.block_heads;
+    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(A.q) + (static_cast<int64_t>(at.S.b) * A.hq + h0) * DH;
+    uint32_t qa[KS][WIDE ? 4 : 2];
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+#pragma unroll
+      for (int i = 0; i < (WIDE ? 4 : 2); ++i) {  // i: element half, then row half
+        const int r = g + (i >> 1) * 8, d = 16 * k + (i & 1) * 8 + 2 * c;
+        qa[k][i] = r < heads ? *reinterpret_cast<const uint32_t*>(q + r * DH + d) : 0u;
+      }
+    float o[DH / 8][WIDE ? 4 : 2];
+#pragma unroll
+    for (int n = 0; n < DH / 8; ++n)
+#pragma unroll
+      for (int i = 0; i < (WIDE ? 4 : 2); ++i) o[n][i] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+
+    const int u0 = at.u;
+    for (; at.u < at.u1; ++at.u) {
+      copy(stage == 0 ? NS - 1 : stage - 1);
+      look_up();
+      cp_async_wait<NS - 1>();
+      __syncwarp();
+      const int key0 = at.u * kUnit + warp * 16;
+      if (key0 < at.vis.vis) {
+        const uint32_t ks = ring + stage * C::STAGE, vs = ks + 16 * C::PITCH;
+        float s[2][4] = {};
+        const uint32_t ka = ks + ((lane & 7) + (lane >> 4) * 8) * C::PITCH + ((lane >> 3) & 1) * 16;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          uint32_t b[4];
+          ldmatrix4(b, ka + k * 32);
+          if constexpr (WIDE) {
+            mma_bf16(s[0], qa[k][0], qa[k][2], qa[k][1], qa[k][3], b[0], b[1]);
+            mma_bf16(s[1], qa[k][0], qa[k][2], qa[k][1], qa[k][3], b[2], b[3]);
+          } else {
+            mma_bf16(s[0], qa[k][0], 0u, qa[k][1], 0u, b[0], b[1]);
+            mma_bf16(s[1], qa[k][0], 0u, qa[k][1], 0u, b[2], b[3]);
+          }
+        }
+        uint32_t p[2][2];  // [row half][key half]
+        const bool part = key0 + 16 > at.vis.vis;
+#pragma unroll
+        for (int r = 0; r < (WIDE ? 2 : 1); ++r) {
+          float x[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            x[i] = s[i >> 1][2 * r + (i & 1)] * A.scale_log2;
+            if (part && key0 + (i >> 1) * 8 + 2 * c + (i & 1) >= at.vis.vis) x[i] = -INFINITY;
+          }
+          float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const bool grow = mx > m[r] + 8.f;  // also of the first finite score
+          if (__any_sync(0xffffffffu, grow)) {
+            const float alpha = grow ? (m[r] == -INFINITY ? 0.f : ex2(m[r] - mx)) : 1.f;
+            if (grow) m[r] = mx;
+            l[r] *= alpha;
+#pragma unroll
+            for (int n = 0; n < DH / 8; ++n) {
+              o[n][2 * r] *= alpha;
+              o[n][2 * r + 1] *= alpha;
+            }
+          }
+          const float ref = m[r] == -INFINITY ? 0.f : m[r];
+          float e[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) e[i] = ex2(x[i] - ref);
+          l[r] += (e[0] + e[1]) + (e[2] + e[3]);
+          p[r][0] = pack_bf16x2(e[0], e[1]);
+          p[r][1] = pack_bf16x2(e[2], e[3]);
+        }
+        const uint32_t va = vs + ((lane & 7) + ((lane >> 3) & 1) * 8) * C::PITCH + (lane >> 4) * 16;
+#pragma unroll
+        for (int d = 0; d < KS; ++d) {
+          uint32_t b[4];
+          ldmatrix4_trans(b, va + d * 32);
+          if constexpr (WIDE) {
+            mma_bf16(o[2 * d], p[0][0], p[1][0], p[0][1], p[1][1], b[0], b[1]);
+            mma_bf16(o[2 * d + 1], p[0][0], p[1][0], p[0][1], p[1][1], b[2], b[3]);
+          } else {
+            float t[4] = {o[2 * d][0], o[2 * d][1], 0.f, 0.f};
+            mma_bf16(t, p[0][0], 0u, p[0][1], 0u, b[0], b[1]);
+            o[2 * d][0] = t[0];
+            o[2 * d][1] = t[1];
+            float w[4] = {o[2 * d + 1][0], o[2 * d + 1][1], 0.f, 0.f};
+            mma_bf16(w, p[0][0], 0u, p[0][1], 0u, b[2], b[3]);
+            o[2 * d + 1][0] = w[0];
+            o[2 * d + 1][1] = w[1];
+          }
+        }
+      }
+      __syncwarp();  // every lane has read the stage: the next copy may go there
+      stage = stage + 1 == NS ? 0 : stage + 1;
+    }
+
+    // the four warps' states into one, CHUNK heads at a time
+#pragma unroll
+    for (int r = 0; r < (WIDE ? 2 : 1); ++r) {
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+      if (c == 0) {
+        sm_m[warp][g + 8 * r] = m[r];
+        sm_l[warp][g + 8 * r] = l[r];
+      }
+    }
+    const bool whole = u0 == 0 && at.u1 == at.S.units;
+    float* part = part_of(A, blockIdx.x, at.S.u == share0 ? 0 : 1);
+    for (int r0 = 0; r0 < heads; r0 += C::CHUNK) {
+#pragma unroll
+      for (int r = 0; r < (WIDE ? 2 : 1); ++r) {
+        const int h = g + 8 * r - r0;
+        if (h >= 0 && h < C::CHUNK) {
+#pragma unroll
+          for (int n = 0; n < DH / 8; ++n)
+            *reinterpret_cast<float2*>(joined + (warp * C::CHUNK + h) * DH + 8 * n + 2 * c) =
+                make_float2(o[n][2 * r], o[n][2 * r + 1]);
+        }
+      }
+      __syncthreads();
+      for (int i = threadIdx.x; i < C::CHUNK * (DH / 4); i += kThreads) {
+        const int h = i / (DH / 4), d = i % (DH / 4) * 4, hh = r0 + h;
+        if (hh >= heads) break;
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) M = fmaxf(M, sm_m[w][hh]);
+        const float ref = M == -INFINITY ? 0.f : M;
+        float L = 0.f;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float f = ex2(sm_m[w][hh] - ref);
+          const float4 y = *reinterpret_cast<const float4*>(joined + (w * C::CHUNK + h) * DH + d);
+          L += f * sm_l[w][hh];
+          x.x += f * y.x;
+          x.y += f * y.y;
+          x.z += f * y.z;
+          x.w += f * y.w;
+        }
+        if (whole) {
+          const float inv = inverse(L);
+          uint2 u;
+          u.x = pack_bf16x2(x.x * inv, x.y * inv);
+          u.y = pack_bf16x2(x.z * inv, x.w * inv);
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(A.out) +
+                                    (static_cast<int64_t>(at.S.b) * A.hq + h0 + hh) * DH + d) = u;
+          if (d == 0) store_lse(A, at.S.b, h0 + hh, M, L);
+        } else {
+          float* to = part + hh * (DH + 2);
+          *reinterpret_cast<float2*>(to + d) = make_float2(x.x, x.y);
+          *reinterpret_cast<float2*>(to + d + 2) = make_float2(x.z, x.w);
+          if (d == 0) {
+            to[DH] = M;
+            to[DH + 1] = L;
+          }
+        }
+      }
+      __syncthreads();
+    }
+    at.next_piece(A, false);
   }
 }
 
@@ -405,6 +711,7 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join(const __grid_constan
   const int n = (visible(A, b, tid == 0).vis + kUnit - 1) / kUnit, per = A.hkv * A.blocks_per_kv;
   const int64_t total = sum * per;
   T* out = static_cast<T*>(A.out) + (static_cast<int64_t>(b) * A.hq + h) * dh;
+  wait_for_main();  // in every block: what follows in the stream waits for this kernel alone
   if (n == 0) {
     for (int d = tid; d < dh; d += kJoinThreads) stv<T>(out + d, 0.f);
     if (tid == 0) A.lse[static_cast<int64_t>(b) * A.hq + h] = -INFINITY;
@@ -457,30 +764,60 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join(const __grid_constan
   if (tid == 0) store_lse(A, b, h, mx, l);
 }
 
-// Query heads that share one read of a K/V head.
-int heads_of_block(int group) { return group >= 8 ? 8 : group >= 4 ? 4 : group >= 2 ? 2 : 1; }
+// Query heads that share one read of a K/V head: on the CUDA cores a power of two up to 8 (the
+// states of 8 heads fill a thread's registers), for the matrix instructions up to their 16 rows,
+// evenly.
+int heads_of_block(int dtype, int group) {
+  if (dtype == RA_F32) return group >= 8 ? 8 : group >= 4 ? 4 : group >= 2 ? 2 : 1;
+  const int blocks = (group + 15) / 16;
+  return (group + blocks - 1) / blocks;
+}
 
-template <typename T>
-cudaError_t launch(DecodeArgs& A, cudaStream_t st) {
+template <int DH, bool WIDE>
+cudaError_t launch_mma(const DecodeArgs& A, int grid, cudaStream_t st) {
+  using C = MmaCfg<DH, WIDE>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(decode_mma<DH, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  decode_mma<DH, WIDE><<<grid, kThreads, C::SMEM, st>>>(A);
+  return cudaGetLastError();
+}
+
+cudaError_t launch(DecodeArgs& A, int dtype, cudaStream_t st) {
   int dev = 0, n_sm = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   const int grid = 2 * n_sm < kMaxCtas ? 2 * n_sm : kMaxCtas;
-  switch (A.block_heads) {
-    case 1: decode_simt<T, 1><<<grid, kThreads, 0, st>>>(A); break;
-    case 2: decode_simt<T, 2><<<grid, kThreads, 0, st>>>(A); break;
-    case 4: decode_simt<T, 4><<<grid, kThreads, 0, st>>>(A); break;
-    default: decode_simt<T, 8><<<grid, kThreads, 0, st>>>(A); break;
+  if (dtype == RA_F32) {
+    switch (A.block_heads) {
+      case 1: decode_simt<1><<<grid, kThreads, 0, st>>>(A); break;
+      case 2: decode_simt<2><<<grid, kThreads, 0, st>>>(A); break;
+      case 4: decode_simt<4><<<grid, kThreads, 0, st>>>(A); break;
+      default: decode_simt<8><<<grid, kThreads, 0, st>>>(A); break;
+    }
+    e = cudaGetLastError();
+  } else if (A.dh == 128) {
+    e = A.block_heads > 8 ? launch_mma<128, true>(A, grid, st) : launch_mma<128, false>(A, grid, st);
+  } else {
+    e = A.block_heads > 8 ? launch_mma<64, true>(A, grid, st) : launch_mma<64, false>(A, grid, st);
   }
-  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  decode_join<T><<<A.n_seqs * A.hq, kJoinThreads, 0, st>>>(A, grid);
-  return cudaGetLastError();
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(A.n_seqs * A.hq);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = st;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return dtype == RA_F32 ? cudaLaunchKernelEx(&cfg, decode_join<float>, A, grid)
+                         : cudaLaunchKernelEx(&cfg, decode_join<__nv_bfloat16>, A, grid);
 }
 
 size_t workspace_of(const ra_paged_cache* c, int hq) {
-  const size_t part = heads_of_block(hq / c->hkv) * (c->head_dim + 2) * sizeof(float);
+  const size_t part = heads_of_block(c->dtype, hq / c->hkv) * (c->head_dim + 2) * sizeof(float);
   return (2 * kMaxCtas * part + 255) & ~size_t(255);
 }
 
@@ -526,6 +863,13 @@ extern "C" int ra_paged_attn_decode(const ra_paged_cache* c, int hq, float scale
   if (workspace == nullptr || reinterpret_cast<uintptr_t>(workspace) % 256)
     return record_error(RA_ERR_INVALID_ARG, "workspace must be a 256-byte aligned device pointer");
   if (c->n_seqs == 0) return record_error(RA_OK, "%s", "");
+  if (c->dtype == RA_BF16) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(c->k_pages) | reinterpret_cast<uintptr_t>(c->v_pages) |
+                        reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out);
+    if (p % 16 || c->page_stride % 8 || c->slot_stride % 8 || c->head_stride % 8)
+      return record_error(RA_ERR_INVALID_ARG,
+                          "bf16 decode: q, out and pages must be 16-byte aligned, strides multiples of 8 elements");
+  }
   DecodeArgs A;
   A.q = q;
   A.k_pages = c->k_pages;
@@ -544,7 +888,7 @@ extern "C" int ra_paged_attn_decode(const ra_paged_cache* c, int hq, float scale
   A.hkv = c->hkv;
   A.group = hq / c->hkv;
   A.dh = c->head_dim;
-  A.block_heads = heads_of_block(A.group);
+  A.block_heads = heads_of_block(c->dtype, A.group);
   A.blocks_per_kv = (A.group + A.block_heads - 1) / A.block_heads;
   A.window = window;
   A.sinks = sinks;
@@ -553,7 +897,7 @@ extern "C" int ra_paged_attn_decode(const ra_paged_cache* c, int hq, float scale
   A.out = out;
   A.lse = lse;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = c->dtype == RA_F32 ? launch<float>(A, st) : launch<__nv_bfloat16>(A, st);
+  const cudaError_t e = launch(A, c->dtype, st);
   if (e != cudaSuccess) return record_error(RA_ERR_CUDA, "decode attention launch: %s", cudaGetErrorString(e));
   return record_error(RA_OK, "%s", "");
 }

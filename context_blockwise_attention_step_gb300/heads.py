@@ -14,7 +14,7 @@ import torch
 
 from . import ops
 from ._abi import RA_BF16, RA_F32, RA_MAX_ROTARY_DIM, RaPagedCache, RaRope, check, lib
-from .ops import Problem, _p, _stream
+from .ops import Problem
 
 
 @dataclass
@@ -47,63 +47,81 @@ def make_rope(rotary_dim: int, base: float = 10000.0, inv_freq=None, interleaved
     return Rope(raw)
 
 
-def _rows(t: torch.Tensor, name: str, dtype, rows: int, heads: int, dh: int, device) -> int:
+def _rows(t: torch.Tensor, name: str, dtype, rows: int, heads: int, dh: int, dev: int) -> int:
     """Checks a token tensor [rows, heads, dh] or [B, S, heads, dh], possibly a view into a
     wider one, and returns the elements from one token to the next."""
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device or not t.is_cuda:
+    if t.get_device() != dev or dev < 0:
         raise ValueError(f"{name} must be on the same CUDA device as the other tensors")
-    if t.dim() not in (3, 4) or t.shape[-1] != dh or t.shape[-2] != heads or t.numel() != rows * heads * dh:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {rows} tokens of {heads} x {dh}")
-    size, stride = t.shape, t.stride()
+    size = t.shape
+    n = len(size)
+    if n not in (3, 4) or size[-1] != dh or size[-2] != heads or t.numel() != rows * heads * dh:
+        raise ValueError(f"{name} has shape {tuple(size)}, expected {rows} tokens of {heads} x {dh}")
+    if t.is_contiguous():
+        return heads * dh
+    stride = t.stride()
     if (dh > 1 and stride[-1] != 1) or (heads > 1 and stride[-2] != dh):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    tokens = [(size[i], stride[i]) for i in range(t.dim() - 2) if size[i] > 1]
+    tokens = [(size[i], stride[i]) for i in range(n - 2) if size[i] > 1]
     if len(tokens) == 2 and tokens[0][1] != tokens[1][0] * tokens[1][1]:
         raise ValueError(f"{name}: batch elements must follow one another")
-    return tokens[-1][1] if tokens and rows > 1 else heads * dh
+    return tokens[-1][1] if tokens and rows > 0 else heads * dh
 
 
-def _plain(t: torch.Tensor, name: str, dtype, shape, device) -> torch.Tensor:
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
-                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+def _plain(t: torch.Tensor, name: str, dtype, shape, dev: int) -> torch.Tensor:
+    if t.dtype != dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on CUDA device "
+                         f"{dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t
 
 
-def _token(t: torch.Tensor, numel: int, name: str, prob: Problem, device):
-    ops._check_tensor(t, prob.token_dtype, numel, name)
-    if t.device != device:
-        raise ValueError(f"{name} must be on the same CUDA device as the other tensors")
+def _token(t: torch.Tensor, numel: int, name: str, prob: Problem, dev: int):
+    if t.dtype != prob.token_dtype or t.numel() != numel or t.get_device() != dev or dev < 0 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {prob.token_dtype} tensor of {numel} elements on CUDA "
+                         f"device {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-def _weights(q_weight, k_weight, dtype, dh, device):
+def _weights(q_weight, k_weight, dtype, dh, dev):
     if (q_weight is None) != (k_weight is None):
         raise ValueError("pass both q_weight and k_weight, or neither")
     if q_weight is not None:
-        _plain(q_weight, "q_weight", dtype, (dh,), device)
-        _plain(k_weight, "k_weight", dtype, (dh,), device)
+        _plain(q_weight, "q_weight", dtype, (dh,), dev)
+        _plain(k_weight, "k_weight", dtype, (dh,), dev)
 
 
-def _workspace(workspace, need: int, device):
+def _like(t: torch.Tensor) -> torch.Tensor:
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
+def _workspace(workspace, need: int, like: torch.Tensor, made: list):
+    """The given workspace, or a new one on ``like``'s device; and its bytes."""
     if workspace is None:
-        return torch.empty(need, device=device, dtype=torch.uint8)
-    if not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {device}")
-    return workspace
+        made.append(workspace := torch.empty(max(1, need), device=like.device, dtype=torch.uint8))
+        return workspace, need
+    if workspace.get_device() != like.get_device() or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {like.device}")
+    return workspace, workspace.numel() * workspace.element_size()
 
 
-def _launch(device, stream, made, call):
-    """Runs ``call(stream)`` with ``device`` current. Tensors made for the call come from the
-    current stream's pool: another ``stream`` waits for that stream first, and keeps them from
-    reuse until it has done with them."""
-    with torch.cuda.device(device):
-        if stream is not None and made and stream != torch.cuda.current_stream():
+def _ptr(t: torch.Tensor | None):
+    return None if t is None else t.data_ptr()
+
+
+def _launch(dev: int, stream, made, call):
+    """Runs ``call(stream handle)`` with device ``dev`` current. Tensors made for the call come
+    from the current stream's pool: another ``stream`` waits for that stream first, and keeps
+    them from reuse until it has done with them."""
+    if stream is None and dev == torch.cuda.current_device():
+        return check(call(torch._C._cuda_getCurrentRawStream(dev)))
+    with torch.cuda.device(dev):
+        if stream is None:
+            return check(call(torch.cuda.current_stream().cuda_stream))
+        if made and stream != torch.cuda.current_stream():
             stream.wait_stream(torch.cuda.current_stream())
             for t in made:
                 t.record_stream(stream)
-        return check(call(_stream(stream)))
+        return check(call(stream.cuda_stream))
 
 
 def _rope_ptr(rope: Rope | None):
@@ -117,20 +135,20 @@ def qk_norm_rope_fwd(q, k, prob: Problem, q_weight=None, k_weight=None, rope: Ro
     (q_out, k_out). q and k may be views into a wider tensor (a fused projection); q_out may be
     a contiguous q, k_out a contiguous k."""
     r = prob.raw
-    dh, dev = r.head_dim, q.device
+    dh, dev = r.head_dim, q.get_device()
     qs = _rows(q, "q", prob.token_dtype, prob.rows, r.hq, dh, dev)
     ks = _rows(k, "k", prob.token_dtype, prob.rows, r.hkv, dh, dev)
     _weights(q_weight, k_weight, prob.token_dtype, dh, dev)
     made = []
     if q_out is None:
-        made.append(q_out := torch.empty(q.shape, device=dev, dtype=q.dtype))
+        made.append(q_out := _like(q))
     if k_out is None:
-        made.append(k_out := torch.empty(k.shape, device=dev, dtype=k.dtype))
+        made.append(k_out := _like(k))
     _plain(q_out, "q_out", prob.token_dtype, q.shape, dev)
     _plain(k_out, "k_out", prob.token_dtype, k.shape, dev)
     _launch(dev, stream, made, lambda s: lib().ra_qk_norm_rope_fwd(
-        prob.ptr, _rope_ptr(rope), eps, _p(q), qs, _p(k), ks, _p(q_weight), _p(k_weight), _p(q_out),
-        _p(k_out), s))
+        prob.ptr, _rope_ptr(rope), eps, _ptr(q), qs, _ptr(k), ks, _ptr(q_weight), _ptr(k_weight), _ptr(q_out),
+        _ptr(k_out), s))
     return q_out, k_out
 
 
@@ -141,7 +159,7 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, prob: Problem, q_weight=None, k_weigh
     from those of its outputs. The weight gradients are float32 (None without weights), summed
     in a fixed order. dq may be dq_out, dk may be dk_out."""
     r = prob.raw
-    dh, dev = r.head_dim, dq_out.device
+    dh, dev = r.head_dim, dq_out.get_device()
     _plain(dq_out, "dq_out", prob.token_dtype, q.shape, dev)
     _plain(dk_out, "dk_out", prob.token_dtype, k.shape, dev)
     qs = _rows(q, "q", prob.token_dtype, prob.rows, r.hq, dh, dev)
@@ -149,23 +167,20 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, prob: Problem, q_weight=None, k_weigh
     _weights(q_weight, k_weight, prob.token_dtype, dh, dev)
     made = []
     if dq is None:
-        made.append(dq := torch.empty(q.shape, device=dev, dtype=q.dtype))
+        made.append(dq := _like(q))
     if dk is None:
-        made.append(dk := torch.empty(k.shape, device=dev, dtype=k.dtype))
+        made.append(dk := _like(k))
     _plain(dq, "dq", prob.token_dtype, q.shape, dev)
     _plain(dk, "dk", prob.token_dtype, k.shape, dev)
     dqw = dkw = None
     size = 0
     if q_weight is not None:
-        made.append(dqw := torch.empty(dh, device=dev, dtype=torch.float32))
-        made.append(dkw := torch.empty(dh, device=dev, dtype=torch.float32))
-        if workspace is None:
-            made.append(workspace := _workspace(None, ops.workspace_bytes(prob, 3), dev))
-        workspace = _workspace(workspace, 0, dev)
-        size = workspace.numel() * workspace.element_size()
+        made.append(dqw := torch.empty(dh, device=dq_out.device, dtype=torch.float32))
+        made.append(dkw := torch.empty(dh, device=dq_out.device, dtype=torch.float32))
+        workspace, size = _workspace(workspace, workspace is None and ops.workspace_bytes(prob, 3), q, made)
     _launch(dev, stream, made, lambda s: lib().ra_qk_norm_rope_bwd(
-        prob.ptr, _rope_ptr(rope), eps, _p(dq_out), _p(dk_out), _p(q), qs, _p(k), ks, _p(q_weight),
-        _p(k_weight), _p(dq), _p(dk), _p(dqw), _p(dkw), _p(workspace), size, s))
+        prob.ptr, _rope_ptr(rope), eps, _ptr(dq_out), _ptr(dk_out), _ptr(q), qs, _ptr(k), ks, _ptr(q_weight),
+        _ptr(k_weight), _ptr(dq), _ptr(dk), _ptr(dqw), _ptr(dkw), _ptr(workspace), size, s))
     return dq, dk, dqw, dkw
 
 
@@ -180,47 +195,45 @@ def window_attn_fwd(q, k, v, prob: Problem, window: int, sinks: int = 0, out=Non
     """Ring attention in which a query at position p sees the keys at k <= p with k > p -
     ``window`` or k < ``sinks`` -> (out, lse), shard-major. The workspace
     (``window_workspace_bytes(..., 0)``) is allocated when not given."""
-    r, dev = prob.raw, q.device
+    r, dev = prob.raw, q.get_device()
     made = []
     if out is None:
-        made.append(out := torch.empty(q.shape, device=dev, dtype=q.dtype))
+        made.append(out := _like(q))
     if lse is None:
-        made.append(lse := torch.empty(ops._lse_shape(prob), device=dev, dtype=torch.float32))
+        made.append(lse := torch.empty(ops._lse_shape(prob), device=q.device, dtype=torch.float32))
     nq, nk = prob.rows * r.hq * r.head_dim, prob.rows * r.hkv * r.head_dim
     for t, n, name in ((q, nq, "q"), (k, nk, "k"), (v, nk, "v"), (out, nq, "out")):
         _token(t, n, name, prob, dev)
     _plain(lse, "lse", torch.float32, ops._lse_shape(prob), dev)
-    if workspace is None:
-        made.append(workspace := _workspace(None, max(1, window_workspace_bytes(prob, window, sinks, 0)), dev))
-    workspace = _workspace(workspace, 0, dev)
+    workspace, size = _workspace(
+        workspace, workspace is None and window_workspace_bytes(prob, window, sinks, 0), q, made)
     _launch(dev, stream, made, lambda s: lib().ra_window_attn_fwd(
-        prob.ptr, window, sinks, _p(q), _p(k), _p(v), _p(out), _p(lse), _p(workspace),
-        workspace.numel() * workspace.element_size(), s))
+        prob.ptr, window, sinks, _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(workspace),
+        size, s))
     return out, lse
 
 
 def window_attn_bwd(dout, q, k, v, out, lse, prob: Problem, window: int, sinks: int = 0, dq=None,
                     dk=None, dv=None, workspace=None, stream=None):
     """Backward of ``window_attn_fwd`` -> (dq, dk, dv), shard-major, in the problem dtype."""
-    r, dev = prob.raw, q.device
+    r, dev = prob.raw, q.get_device()
     made = []
     if dq is None:
-        made.append(dq := torch.empty(q.shape, device=dev, dtype=q.dtype))
+        made.append(dq := _like(q))
     if dk is None:
-        made.append(dk := torch.empty(k.shape, device=dev, dtype=k.dtype))
+        made.append(dk := _like(k))
     if dv is None:
-        made.append(dv := torch.empty(v.shape, device=dev, dtype=v.dtype))
+        made.append(dv := _like(v))
     nq, nk = prob.rows * r.hq * r.head_dim, prob.rows * r.hkv * r.head_dim
     for t, n, name in ((dout, nq, "dout"), (q, nq, "q"), (k, nk, "k"), (v, nk, "v"), (out, nq, "out"),
                        (dq, nq, "dq"), (dk, nk, "dk"), (dv, nk, "dv")):
         _token(t, n, name, prob, dev)
     _plain(lse, "lse", torch.float32, ops._lse_shape(prob), dev)
-    if workspace is None:
-        made.append(workspace := _workspace(None, max(1, window_workspace_bytes(prob, window, sinks, 1)), dev))
-    workspace = _workspace(workspace, 0, dev)
+    workspace, size = _workspace(
+        workspace, workspace is None and window_workspace_bytes(prob, window, sinks, 1), q, made)
     _launch(dev, stream, made, lambda s: lib().ra_window_attn_bwd(
-        prob.ptr, window, sinks, _p(q), _p(k), _p(v), _p(out), _p(lse), _p(dout), _p(dq), _p(dk), _p(dv),
-        _p(workspace), workspace.numel() * workspace.element_size(), s))
+        prob.ptr, window, sinks, _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv),
+        _ptr(workspace), size, s))
     return dq, dk, dv
 
 
@@ -282,7 +295,7 @@ def kv_cache_append(q, k, v, cache: PagedCache, seq_lens, cu_new=None, q_weight=
     q_out is 0); with it (int32 [n_seqs + 1], on the device) rows cu_new[b]:cu_new[b+1] are the
     last tokens of sequence b, and rows behind the last are left as they are."""
     r = cache.raw
-    dt, dh, dev = cache.k_pages.dtype, r.head_dim, cache.k_pages.device
+    dt, dh, dev = cache.k_pages.dtype, r.head_dim, cache.k_pages.get_device()
     n = k.shape[0] if k.dim() == 3 else k.shape[0] * k.shape[1]
     ks = _rows(k, "k", dt, n, r.hkv, dh, dev)
     vs = _rows(v, "v", dt, n, r.hkv, dh, dev)
@@ -295,13 +308,13 @@ def kv_cache_append(q, k, v, cache: PagedCache, seq_lens, cu_new=None, q_weight=
         hq = q.shape[-2]
         qs = _rows(q, "q", dt, n, hq, dh, dev)
         if q_out is None:
-            made.append(q_out := torch.empty(q.shape, device=dev, dtype=dt))
+            made.append(q_out := _like(q))
         _plain(q_out, "q_out", dt, q.shape, dev)
     elif q_out is not None:
         raise ValueError("q_out without q")
     _launch(dev, stream, made, lambda s: lib().ra_kv_cache_append(
-        cache.ptr, _rope_ptr(rope), eps, n, hq, _p(q), qs, _p(k), ks, _p(v), vs, _p(q_weight),
-        _p(k_weight), _p(seq_lens), _p(cu_new), _p(q_out), s))
+        cache.ptr, _rope_ptr(rope), eps, n, hq, _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(q_weight),
+        _ptr(k_weight), _ptr(seq_lens), _ptr(cu_new), _ptr(q_out), s))
     return q_out
 
 
@@ -317,7 +330,7 @@ def paged_attn_decode(q, cache: PagedCache, seq_lens, window: int = 0, sinks: in
     length 0 gets out = 0, lse = -inf. The workspace (``paged_workspace_bytes``) is allocated
     when not given."""
     r = cache.raw
-    dt, dev = cache.k_pages.dtype, cache.k_pages.device
+    dt, dev = cache.k_pages.dtype, cache.k_pages.get_device()
     if q.dim() != 3:
         raise ValueError("q must be [n_seqs, hq, head_dim]")
     hq = q.shape[1]
@@ -325,15 +338,13 @@ def paged_attn_decode(q, cache: PagedCache, seq_lens, window: int = 0, sinks: in
     _lens(seq_lens, "seq_lens", r.n_seqs, dev)
     made = []
     if out is None:
-        made.append(out := torch.empty(q.shape, device=dev, dtype=dt))
+        made.append(out := _like(q))
     if lse is None:
-        made.append(lse := torch.empty((r.n_seqs, hq), device=dev, dtype=torch.float32))
+        made.append(lse := torch.empty((r.n_seqs, hq), device=q.device, dtype=torch.float32))
     _plain(out, "out", dt, q.shape, dev)
     _plain(lse, "lse", torch.float32, (r.n_seqs, hq), dev)
-    if workspace is None:
-        made.append(workspace := _workspace(None, max(1, paged_workspace_bytes(cache, hq)), dev))
-    workspace = _workspace(workspace, 0, dev)
+    workspace, size = _workspace(workspace, workspace is None and paged_workspace_bytes(cache, hq), q, made)
     _launch(dev, stream, made, lambda s: lib().ra_paged_attn_decode(
-        cache.ptr, hq, 0.0 if scale is None else scale, window, sinks, _p(q), _p(seq_lens), _p(out),
-        _p(lse), _p(workspace), workspace.numel() * workspace.element_size(), s))
+        cache.ptr, hq, 0.0 if scale is None else scale, window, sinks, _ptr(q), _ptr(seq_lens), _ptr(out),
+        _ptr(lse), _ptr(workspace), size, s))
     return out, lse

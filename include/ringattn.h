@@ -312,8 +312,8 @@ int ra_kv_cache_append(const ra_paged_cache* c, const ra_rope* rope, float eps, 
  * `sinks`. A sequence of length 0 gets out = 0, lse = -inf. scale <= 0 selects
  * 1/sqrt(head_dim). The keys of the batch are dealt out evenly over the SMs whatever the
  * lengths, and parts of a sequence are joined by the log-sum-exp merge, in a fixed order
- * (run-to-run bit-identical). bf16 wants the pages 16-byte aligned with strides that are
- * multiples of 8 elements. The workspace (device, >= ra_paged_workspace_bytes(c, hq), 256-byte
+ * (run-to-run bit-identical). bf16 wants q, out and the pages 16-byte aligned, and strides that
+ * are multiples of 8 elements. The workspace (device, >= ra_paged_workspace_bytes(c, hq), 256-byte
  * aligned) is overwritten; nothing in it is kept from call to call, so calls and captured
  * graphs may share it as long as they do not run at the same time. */
 int ra_paged_attn_decode(const ra_paged_cache* c, int hq, float scale, int window, int sinks,
