@@ -230,6 +230,8 @@ int effective_window(const ra_problem* p, int window) {
 int validate_window(const ra_problem* p, int window, int sinks) {
   if (int e = validate(p)) return e;
   if (!p->causal) return fail(RA_ERR_UNSUPPORTED, "a sliding window wants a causal problem");
+  if (use_tc(p) && p->D > ra::kMaxWindowShards)
+    return fail(RA_ERR_UNSUPPORTED, "bf16 windows support D <= %d (got %d)", ra::kMaxWindowShards, p->D);
   if (window < 1) return fail(RA_ERR_INVALID_ARG, "window must be >= 1 (got %d)", window);
   if (sinks < 0 || sinks > RA_MAX_SINKS)
     return fail(RA_ERR_INVALID_ARG, "sinks must be 0..%d (got %d)", RA_MAX_SINKS, sinks);

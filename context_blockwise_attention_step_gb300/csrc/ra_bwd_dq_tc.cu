@@ -62,6 +62,8 @@ struct DqCfg {
   static constexpr int kOffV = kOffK + kKStages * kTileBytes; // 2 stages
   static constexpr int kOffBar = kOffV + 2 * kTileBytes;
   static constexpr int kSmemBytes = kOffBar + 256;
+  static constexpr int kOffWin = kOffBar + 256;  // windowed: the item queue's slots
+  static constexpr int kSmemWindow = kOffWin + 2 * sizeof(WinSlot);
   static constexpr int kKSteps = DH / 16;
   static constexpr uint32_t kTmemCols = 512;
   // TMEM columns: S0 | S1 | dP | dQ
@@ -75,12 +77,11 @@ struct DqBars {
   uint64_t drain;
   uint64_t item_full[2], item_empty[2];  // the CTA's item queue
   int item[2];
-  int item_tiles[2];  // windowed: K/V tiles of the item
   uint32_t tmem_base;
   int abort_flag;
 };
 static_assert(sizeof(DqBars) <= 256, "barrier block");
-static_assert(DqCfg<128>::kSmemBytes <= 232448, "shared memory budget");
+static_assert(DqCfg<128>::kSmemWindow <= 232448, "shared memory budget");
 
 // Query-tile items: K/V heads outermost (CTAs that run together share K/V in L2), then
 // the last query tile first (causal: it sees the most keys), then ranks, then the query
@@ -103,12 +104,6 @@ __device__ __forceinline__ DqItem decode_dq(const Plan& P, int w) {
   const int hk = x / nqt;
   it.h = hk * P.group + g;
   return it;
-}
-
-// Windowed: the K/V tiles of the shard that the item's rank holds at step s.
-__device__ __forceinline__ TileSet dq_set(const Plan& P, const DqItem& it, int L, int s) {
-  const int a0 = it.qt * kQTileRows;
-  return window_kv_tiles(P, L, it.r, shard_at_step(P.D, it.r, s), a0, min(L, a0 + kQTileRows) - 1);
 }
 
 __device__ __forceinline__ int dq_walk_tiles(const Plan& P, const DqItem& it, int L) {
@@ -134,17 +129,16 @@ __device__ __forceinline__ int dq_item_publish(DqBars& sh, const Plan& P, int k,
   return w;
 }
 __device__ __forceinline__ int dq_item_take(DqBars& sh, int k, volatile int* abort_flag,
-                                            uint64_t tmo, unsigned int* status, int* tiles) {
+                                            uint64_t tmo, unsigned int* status) {
   const int slot = k & 1;
   if (!mbar_wait(&sh.item_full[slot], (k >> 1) & 1, abort_flag, tmo, status)) return -1;
   const int w = *reinterpret_cast<volatile int*>(&sh.item[slot]);
-  if (tiles != nullptr) *tiles = *reinterpret_cast<volatile int*>(&sh.item_tiles[slot]);
   mbar_arrive(&sh.item_empty[slot]);
   return w;
 }
 
-// The windowed kernel's producer warp: takes the next item, counts its tiles, publishes both.
-__device__ __forceinline__ int dq_window_publish(DqBars& sh, const Plan& P, int k, int lane,
+// The windowed kernel's item queue, as in the windowed forward.
+__device__ __forceinline__ int dq_window_publish(DqBars& sh, WinSlot* slots, const Plan& P, int k, int lane,
                                                  volatile int* abort_flag, uint64_t tmo,
                                                  unsigned int* status) {
   const int slot = k & 1;
@@ -155,15 +149,13 @@ __device__ __forceinline__ int dq_window_publish(DqBars& sh, const Plan& P, int 
     w = P.work_counter ? atomicAdd(P.work_counter, 1)
                        : static_cast<int>(blockIdx.x + static_cast<unsigned>(k) * gridDim.x);
   w = __shfl_sync(0xffffffffu, w, 0);
-  int n = 0;
   if (w < P.n_items) {
     const DqItem it = decode_dq(P, w);
-    const int L = P.seq[it.seq].L;
-    n = count_tiles(P.D, [&](int s) { return dq_set(P, it, L, s); });
+    const int a0 = it.qt * kQTileRows;
+    fill_slot(slots[slot], P, it.seq, it.h, it.r, a0, min(P.seq[it.seq].L, a0 + kQTileRows) - 1);
   }
   if (lane == 0) {
-    sh.item[slot] = w;
-    sh.item_tiles[slot] = n;
+    slots[slot].item = w;
     mbar_arrive(&sh.item_full[slot]);
   }
   return w;
@@ -180,6 +172,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
   using C = DqCfg<DH>;
   extern __shared__ __align__(1024) uint8_t smem[];
   DqBars& sh = *reinterpret_cast<DqBars*>(smem + C::kOffBar);
+  WinSlot* slots = reinterpret_cast<WinSlot*>(smem + C::kOffWin);  // windowed only
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (smem_u32(smem) & 1023u) {
     if (threadIdx.x == 0) atomicOr(&g_status_dq, 2u);
@@ -206,7 +199,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     mbar_init(&sh.dq_done, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.item_full[i], 1);
-      mbar_init(&sh.item_empty[i], 1 + 256);
+      mbar_init(&sh.item_empty[i], 1 + 256 + (WIN ? 1 : 0));  // windowed: the producer reads the slot too
     }
     mbar_init(&sh.dq_free, 256);
     mbar_init(&sh.drain, 1);
@@ -237,46 +230,45 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, tmo, status));
       };
       for (int kq = 0;; ++kq) {
-        const int w = dq_window_publish(sh, P, kq, lane, abort_flag, tmo, status);
+        const int w = dq_window_publish(sh, slots, P, kq, lane, abort_flag, tmo, status);
         if (w < 0 || w >= P.n_items) break;
-        const DqItem it = decode_dq(P, w);
-        const SeqDesc& sd = P.seq[it.seq];
+        const WinSlot& item = slots[kq & 1];
         if (!wait(&sh.q_empty, q_phase ^ 1)) break;
         q_phase ^= 1;
         if (lane == 0) {
           mbar_expect_tx(&sh.q_full, 2 * C::kTileBytes);
-          const int qrow = sd.row_off + it.r * P.shard_stride + it.qt * kQTileRows;
           for (int d = 0; d < C::kSub; ++d) {
-            tma_load_3d(smem + C::kOffQ + d * kSubBytes, &tmQ, &sh.q_full, d * 64, it.h, qrow);
-            tma_load_3d(smem + C::kOffDO + d * kSubBytes, &tmDO, &sh.q_full, d * 64, it.h, qrow);
+            tma_load_3d(smem + C::kOffQ + d * kSubBytes, &tmQ, &sh.q_full, d * 64, item.h, item.row);
+            tma_load_3d(smem + C::kOffDO + d * kSubBytes, &tmDO, &sh.q_full, d * 64, item.h, item.row);
           }
         }
-        const int hk = it.h / P.group;
-        const bool ok = for_each_set(
-            P.D, [&](int s) { return dq_set(P, it, sd.L, s); },
-            [&](int s, const TileSet& set) -> bool {
-              const int krow = sd.row_off + shard_at_step(P.D, it.r, s) * P.shard_stride;
-              const int nb = tile_count(set);
-              for (int i = 0; i < nb; ++i, ++kc) {
-                const int row = krow + tile_at(set, i) * kKvTileRows;
-                const int st = kc & 1, kst = kc % C::kKStages;
-                if (!wait(&sh.k_empty[kst], ((kc / C::kKStages) & 1) ^ 1)) return false;
-                if (lane == 0) {
-                  mbar_expect_tx(&sh.k_full[kst], C::kTileBytes);
-                  for (int d = 0; d < C::kSub; ++d)
-                    tma_load_3d(smem + C::kOffK + kst * C::kTileBytes + d * kSubBytes, &tmK,
-                                &sh.k_full[kst], d * 64, hk, row);
-                }
-                if (!wait(&sh.v_empty[st], ((kc >> 1) & 1) ^ 1)) return false;
-                if (lane == 0) {
-                  mbar_expect_tx(&sh.v_full[st], C::kTileBytes);
-                  for (int d = 0; d < C::kSub; ++d)
-                    tma_load_3d(smem + C::kOffV + st * C::kTileBytes + d * kSubBytes, &tmV,
-                                &sh.v_full[st], d * 64, hk, row);
-                }
-              }
-              return true;
-            });
+        const int hk = item.h / P.group, nseg = item.nseg;
+        const int row0 = item.row - item.a0 - item.r * P.shard_stride;  // of shard 0
+        bool ok = true;
+        for (int g = 0; g < nseg && ok; ++g) {
+          const TileSet set = tiles_of(item.seg[g]);
+          const int krow = row0 + item.seg[g].j * P.shard_stride, nb = tile_count(set);
+          for (int i = 0; i < nb; ++i, ++kc) {
+            const int row = krow + tile_at(set, i) * kKvTileRows;
+            const int st = kc & 1, kst = kc % C::kKStages;
+            if (!(ok = wait(&sh.k_empty[kst], ((kc / C::kKStages) & 1) ^ 1))) break;
+            if (lane == 0) {
+              mbar_expect_tx(&sh.k_full[kst], C::kTileBytes);
+              for (int d = 0; d < C::kSub; ++d)
+                tma_load_3d(smem + C::kOffK + kst * C::kTileBytes + d * kSubBytes, &tmK,
+                            &sh.k_full[kst], d * 64, hk, row);
+            }
+            if (!(ok = wait(&sh.v_empty[st], ((kc >> 1) & 1) ^ 1))) break;
+            if (lane == 0) {
+              mbar_expect_tx(&sh.v_full[st], C::kTileBytes);
+              for (int d = 0; d < C::kSub; ++d)
+                tma_load_3d(smem + C::kOffV + st * C::kTileBytes + d * kSubBytes, &tmV,
+                            &sh.v_full[st], d * 64, hk, row);
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.item_empty[kq & 1]);
         if (!ok) break;
       }
     } else if (lane == 0) {
@@ -337,12 +329,20 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       const uint32_t sK = smem_u32(smem + C::kOffK), sV = smem_u32(smem + C::kOffV);
       bool ok = true;
       for (int kq = 0; ok; ++kq) {
-        int tiles = 0;
-        const int w = dq_item_take(sh, kq, abort_flag, tmo, status, WIN ? &tiles : nullptr);
-        if (w < 0) ok = false;
-        if (w < 0 || w >= P.n_items) break;
-        const DqItem it = decode_dq(P, w);
-        const int N = WIN ? tiles : dq_walk_tiles(P, it, P.seq[it.seq].L);
+        int w, N;
+        if constexpr (WIN) {
+          if (!(ok = mbar_wait(&sh.item_full[kq & 1], (kq >> 1) & 1, abort_flag, tmo, status))) break;
+          w = slots[kq & 1].item;
+          N = slots[kq & 1].tiles;
+          mbar_arrive(&sh.item_empty[kq & 1]);
+          if (w >= P.n_items) break;
+        } else {
+          w = dq_item_take(sh, kq, abort_flag, tmo, status);
+          if (w < 0) ok = false;
+          if (w < 0 || w >= P.n_items) break;
+          const DqItem it = decode_dq(P, w);
+          N = dq_walk_tiles(P, it, P.seq[it.seq].L);
+        }
         if (N == 0) continue;
         if (!(ok = mbar_wait(&sh.q_full, q_phase, abort_flag, tmo, status))) break;
         q_phase ^= 1;
@@ -419,59 +419,83 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     const uint64_t sl2x2 = f2(sl2, sl2);
     uint32_t s_phase[2] = {0, 0}, dp_phase = 0, dd_phase = 0;
     for (int kq = 0;; ++kq) {
-      const int w = dq_item_take(sh, kq, abort_flag, tmo, status, nullptr);
-      if (w < 0 || w >= P.n_items) break;
-      const DqItem it = decode_dq(P, w);
-      const SeqDesc& sd = P.seq[it.seq];
-      const int L = sd.L;
-      const int a = it.qt * kQTileRows + row;
-      const bool valid = a < L;
-      const size_t qrow = static_cast<size_t>(sd.row_off + it.r * P.shard_stride + a);
-      const int N = WIN ? 1 : dq_walk_tiles(P, it, L);  // a windowed row sees itself
-      if (N == 0) {  // no key visible: dq = 0 (nothing to add for bwd_accum)
-        if (valid && !P.bwd_accum) {
-          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(dq) + (qrow * P.hq + it.h) * DH;
+      const WinSlot* item = nullptr;  // windowed: in its slot until the item is done with
+      DqItem it;
+      int L, a;
+      size_t qrow, li = 0;
+      bool valid;
+      if constexpr (WIN) {
+        if (!mbar_wait(&sh.item_full[kq & 1], (kq >> 1) & 1, abort_flag, tmo, status)) break;
+        item = &slots[kq & 1];
+        if (item->item >= P.n_items) break;
+        it.h = item->h;
+        it.r = item->r;
+        L = item->L;
+        a = item->a0 + row;
+        valid = a < L;
+        qrow = static_cast<size_t>(item->row + row);
+        li = static_cast<size_t>(item->lse + row);
+      } else {
+        const int w = dq_item_take(sh, kq, abort_flag, tmo, status);
+        if (w < 0 || w >= P.n_items) break;
+        it = decode_dq(P, w);
+        const SeqDesc& sd = P.seq[it.seq];
+        L = sd.L;
+        a = it.qt * kQTileRows + row;
+        valid = a < L;
+        qrow = static_cast<size_t>(sd.row_off + it.r * P.shard_stride + a);
+        const int N = dq_walk_tiles(P, it, L);
+        if (N == 0) {  // no key visible: dq = 0 (nothing to add for bwd_accum)
+          if (valid && !P.bwd_accum) {
+            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(dq) + (qrow * P.hq + it.h) * DH;
 #pragma unroll
-          for (int c = wg * DH / 64; c < (wg + 1) * DH / 64; ++c) {
-            uint4* d = reinterpret_cast<uint4*>(dst + c * 32);
+            for (int c = wg * DH / 64; c < (wg + 1) * DH / 64; ++c) {
+              uint4* d = reinterpret_cast<uint4*>(dst + c * 32);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) d[q] = make_uint4(0u, 0u, 0u, 0u);
+              for (int q = 0; q < 4; ++q) d[q] = make_uint4(0u, 0u, 0u, 0u);
+            }
           }
+          continue;
         }
-        continue;
+        if (valid)
+          li = sd.lse_off + static_cast<size_t>(it.h) * P.lse_hstride +
+               static_cast<size_t>(it.r) * P.shard_stride + a;
       }
       float nl = -INFINITY, dl = 0.f;
       int64_t pq = 0;
       if (valid) {
-        const size_t li = sd.lse_off + static_cast<size_t>(it.h) * P.lse_hstride +
-                          static_cast<size_t>(it.r) * P.shard_stride + a;
         const float l = lse[li];
         nl = l == -INFINITY ? -INFINITY : -l * kLog2e;
         dl = delta[li];
         pq = layout_pos(P.layout, P.D, L, it.r, a);
       }
+      KeyLimit upto, before;  // windowed: the last key seen, the last one before the window
+      if constexpr (WIN) {
+        upto = key_limit_of(P, static_cast<int>(pq));
+        before = key_limit_of(P, static_cast<int>(pq - P.window));
+      }
       const uint64_t nl2 = f2(nl, nl), dl2 = f2(dl, dl);
-      const int a_last = min(L, (it.qt + 1) * kQTileRows) - 1;
+      const int a_last = WIN ? 0 : min(L, (it.qt + 1) * kQTileRows) - 1;
       int n = 0;
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
         const bool got = mbar_wait(bar, parity, abort_flag, tmo, status);
         return WIN ? __all_sync(0xffffffffu, got) : got;  // the windowed walk is the warp's
       };
-      unsigned shards = 0;  // windowed: the next 32 steps' shards that have tiles
-      for (int s = P.step_begin; s < P.step_end && ok; ++s) {
-        if constexpr (WIN) {
-          if ((s & 31) == 0) shards = nonempty(P.D, s, [&](int i) { return dq_set(P, it, L, i); });
-          if (!((shards >> (s & 31)) & 1u)) continue;
-        }
-        const int j = shard_at_step(P.D, it.r, s);
+      const int s_end = WIN ? item->nseg : P.step_end;
+      for (int s = WIN ? 0 : P.step_begin; s < s_end && ok; ++s) {
+        const int j = WIN ? item->seg[s].j : shard_at_step(P.D, it.r, s);
         TileSet set;
-        if constexpr (WIN) set = dq_set(P, it, L, s);
+        if constexpr (WIN) set = tiles_of(item->seg[s]);
         const int nb = WIN ? tile_count(set) : kv_tiles_for(P, L, it.r, j, a_last);
-        const int lim = !valid ? -1 : (P.causal ? key_limit(P.layout, P.D, L, j, pq) : L - 1);
-        // windowed: of the shard's keys up to lim this row sees those before sk, and from lo on
-        const int lo = WIN ? first_query(P.layout, P.D, L, j, pq - P.window + 1) : 0;
-        const int sk = WIN ? sink_rows(P, L, j) : 0;
+        int lim, lo = 0, sk = 0;
+        if constexpr (WIN) {  // of the shard's keys up to lim this row sees those before sk, and from lo on
+          lim = valid ? limit_in(P, L, j, upto) : -1;
+          lo = limit_in(P, L, j, before) + 1;
+          sk = item->seg[s].sk;
+        } else {
+          lim = !valid ? -1 : (P.causal ? key_limit(P.layout, P.D, L, j, pq) : L - 1);
+        }
         for (int i = 0; i < nb; ++i, ++n) {
           const int b = WIN ? tile_at(set, i) : i;
           const int buf = n & 1;
@@ -580,6 +604,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       }
       tc_fence_before();
       mbar_arrive(&sh.dq_free);
+      if constexpr (WIN) mbar_arrive(&sh.item_empty[kq & 1]);
     }
   }
 
@@ -597,11 +622,11 @@ cudaError_t launch_one(const Plan& P, const CUtensorMap& mq, const CUtensorMap& 
                        const float* delta, void* dq, int n_items, int n_sm, cudaStream_t st) {
   using C = DqCfg<DH>;
   auto kern = ring_bwd_dq_tc_kernel<DH, WIN>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       C::kSmemBytes);
+  constexpr int smem = WIN ? C::kSmemWindow : C::kSmemBytes;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int grid = n_items < n_sm ? n_items : n_sm;
-  kern<<<grid, kDqThreads, C::kSmemBytes, st>>>(mq, mk, mv, mdo, P, lse, delta, dq);
+  kern<<<grid, kDqThreads, smem, st>>>(mq, mk, mv, mdo, P, lse, delta, dq);
   return cudaGetLastError();
 }
 

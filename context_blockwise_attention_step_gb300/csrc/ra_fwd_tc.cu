@@ -32,8 +32,9 @@
 // while the tensor core works on the other tile.
 //
 // WIN (sliding window with always visible first tokens): a block walks the K/V tiles that some
-// of its rows sees through the window, and the first tile of the shards that hold sinks; the
-// producer warp counts them and hands the count to the MMA thread with the item.
+// of its rows sees through the window, and the first tile of the shards that hold sinks. The
+// producer warp works these out ahead of time, one shard a lane, and leaves them with the item's
+// other data in the item queue's slot, where the other roles read them until they are done.
 #include <cuda_runtime.h>
 
 #include "ra_internal.h"
@@ -74,12 +75,18 @@ struct FwdShared {
   uint64_t xmax_bar[2][2], xl_bar[2];  // half-row exchanges: [tile][slot], [tile]
   uint64_t item_full[2], item_empty[2];  // the CTA's item queue
   int item[2];
-  int item_tiles[2];  // windowed: K/V tiles of the item
   uint32_t tmem_base;
   int abort_flag;
   float xmax[2][2][2][128];  // [tile][slot][half][row]: partial row maxima
   float xl[2][2][128];       // [tile][half][row]: partial row sums
 };
+// Windowed: the item queue's slots.
+template <bool WIN>
+struct FwdSlots {
+  WinSlot slot[2];
+};
+template <>
+struct FwdSlots<false> {};
 
 // Total K/V tiles a forward item walks, and its first/last valid query rows.
 struct FwdWalk {
@@ -87,7 +94,6 @@ struct FwdWalk {
   bool two;
 };
 
-template <bool WIN>
 __device__ __forceinline__ FwdWalk fwd_walk(const Plan& P, const FwdItem& it) {
   FwdWalk w;
   w.L = P.seq[it.seq].L;
@@ -96,15 +102,9 @@ __device__ __forceinline__ FwdWalk fwd_walk(const Plan& P, const FwdItem& it) {
   w.a_last = a_end - 1;
   w.two = (a_end - w.a0) > kQTileRows;
   w.N = 0;
-  if constexpr (!WIN)
-    for (int s = P.step_begin; s < P.step_end; ++s)
-      w.N += kv_tiles_for(P, w.L, it.r, shard_at_step(P.D, it.r, s), w.a_last);
+  for (int s = P.step_begin; s < P.step_end; ++s)
+    w.N += kv_tiles_for(P, w.L, it.r, shard_at_step(P.D, it.r, s), w.a_last);
   return w;
-}
-
-// Windowed: the K/V tiles of the shard that the item's rank holds at step s.
-__device__ __forceinline__ TileSet fwd_set(const Plan& P, const FwdItem& it, const FwdWalk& w, int s) {
-  return window_kv_tiles(P, w.L, it.r, shard_at_step(P.D, it.r, s), w.a0, w.a_last);
 }
 
 template <typename OutT>
@@ -146,17 +146,17 @@ __device__ __forceinline__ int fwd_item_publish(FwdShared& sh, const Plan& P, in
   return w;
 }
 __device__ __forceinline__ int fwd_item_take(FwdShared& sh, int k, volatile int* abort_flag,
-                                             uint64_t tmo, unsigned int* status, int* tiles) {
+                                             uint64_t tmo, unsigned int* status) {
   const int slot = k & 1;
   if (!mbar_wait(&sh.item_full[slot], (k >> 1) & 1, abort_flag, tmo, status)) return -1;
   const int w = *reinterpret_cast<volatile int*>(&sh.item[slot]);
-  if (tiles != nullptr) *tiles = *reinterpret_cast<volatile int*>(&sh.item_tiles[slot]);
   mbar_arrive(&sh.item_empty[slot]);
   return w;
 }
 
-// The windowed kernel's producer warp: takes the next item, counts its tiles, publishes both.
-__device__ __forceinline__ int fwd_window_publish(FwdShared& sh, const Plan& P, int k, int lane,
+// The windowed kernel's item queue: the producer warp takes the next item and fills in its slot;
+// the other roles read it in place and release it when they have done with the item.
+__device__ __forceinline__ int fwd_window_publish(FwdShared& sh, WinSlot* slots, const Plan& P, int k, int lane,
                                                   volatile int* abort_flag, uint64_t tmo,
                                                   unsigned int* status) {
   const int slot = k & 1;
@@ -167,15 +167,13 @@ __device__ __forceinline__ int fwd_window_publish(FwdShared& sh, const Plan& P, 
     w = P.work_counter ? atomicAdd(P.work_counter, 1)
                        : static_cast<int>(blockIdx.x + static_cast<unsigned>(k) * gridDim.x);
   w = __shfl_sync(0xffffffffu, w, 0);
-  int n = 0;
   if (w < P.n_items) {
     const FwdItem it = decode_fwd(P, w);
-    const FwdWalk wk = fwd_walk<true>(P, it);
-    n = count_tiles(P.D, [&](int s) { return fwd_set(P, it, wk, s); });
+    const int a0 = it.blk * kFwdBlockRows;
+    fill_slot(slots[slot], P, it.seq, it.h, it.r, a0, min(P.seq[it.seq].L, a0 + kFwdBlockRows) - 1);
   }
   if (lane == 0) {
-    sh.item[slot] = w;
-    sh.item_tiles[slot] = n;
+    slots[slot].item = w;
     mbar_arrive(&sh.item_full[slot]);
   }
   return w;
@@ -190,6 +188,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   using C = FwdCfg<DH>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ FwdShared sh;
+  __shared__ FwdSlots<WIN> win;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -218,7 +217,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     mbar_init(&sh.drain, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.item_full[i], 1);
-      mbar_init(&sh.item_empty[i], 1 + (kFwdThreads - 128));  // MMA thread + softmax warps
+      // MMA thread and softmax warps; windowed also the producer, which reads the slot itself
+      mbar_init(&sh.item_empty[i], (WIN ? 2 : 1) + (kFwdThreads - 128));
     }
     sh.abort_flag = 0;
     fence_mbar_init();
@@ -246,48 +246,47 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, tmo, status));
       };
       for (int kq = 0;; ++kq) {
-        const int w = fwd_window_publish(sh, P, kq, lane, abort_flag, tmo, status);
+        const int w = fwd_window_publish(sh, win.slot, P, kq, lane, abort_flag, tmo, status);
         if (w < 0 || w >= P.n_items) break;
-        const FwdItem it = decode_fwd(P, w);
-        const FwdWalk wk = fwd_walk<WIN>(P, it);
-        const SeqDesc& sd = P.seq[it.seq];
+        const WinSlot& item = win.slot[kq & 1];
+        const bool two = item.a1 - item.a0 >= kQTileRows;
         if (!wait(&sh.q_empty, q_phase ^ 1)) break;
         q_phase ^= 1;
         if (lane == 0) {
-          mbar_expect_tx(&sh.q_full, (wk.two ? 2 : 1) * C::kTileBytes);
-          const int qrow = sd.row_off + it.r * P.shard_stride + wk.a0;
-          for (int t = 0; t < (wk.two ? 2 : 1); ++t)
+          mbar_expect_tx(&sh.q_full, (two ? 2 : 1) * C::kTileBytes);
+          for (int t = 0; t < (two ? 2 : 1); ++t)
             for (int d = 0; d < C::kSub; ++d)
               tma_load_3d(smem + C::kOffQ + t * C::kTileBytes + d * kSubBytes, &tmQ, &sh.q_full,
-                          d * 64, it.h, qrow + t * kQTileRows);
+                          d * 64, item.h, item.row + t * kQTileRows);
         }
-        const int hk = it.h / P.group;
-        const bool ok = for_each_set(
-            P.D, [&](int s) { return fwd_set(P, it, wk, s); },
-            [&](int s, const TileSet& set) -> bool {
-              const int krow = sd.row_off + shard_at_step(P.D, it.r, s) * P.shard_stride;
-              const int nb = tile_count(set);
-              for (int i = 0; i < nb; ++i, ++kv_count) {
-                const int row = krow + tile_at(set, i) * kKvTileRows;
-                const int st = kv_count % C::kStages;
-                const uint32_t ph = (kv_count / C::kStages) & 1;
-                if (!wait(&sh.k_empty[st], ph ^ 1)) return false;
-                if (lane == 0) {
-                  mbar_expect_tx(&sh.k_full[st], C::kTileBytes);
-                  for (int d = 0; d < C::kSub; ++d)
-                    tma_load_3d(smem + C::kOffK + st * C::kTileBytes + d * kSubBytes, &tmK,
-                                &sh.k_full[st], d * 64, hk, row);
-                }
-                if (!wait(&sh.v_empty[st], ph ^ 1)) return false;
-                if (lane == 0) {
-                  mbar_expect_tx(&sh.v_full[st], C::kTileBytes);
-                  for (int d = 0; d < C::kSub; ++d)
-                    tma_load_3d(smem + C::kOffV + st * C::kTileBytes + d * kSubBytes, &tmV,
-                                &sh.v_full[st], d * 64, hk, row);
-                }
-              }
-              return true;
-            });
+        const int hk = item.h / P.group, nseg = item.nseg;
+        const int row0 = item.row - item.a0 - item.r * P.shard_stride;  // of shard 0
+        bool ok = true;
+        for (int g = 0; g < nseg && ok; ++g) {
+          const TileSet set = tiles_of(item.seg[g]);
+          const int krow = row0 + item.seg[g].j * P.shard_stride, nb = tile_count(set);
+          for (int i = 0; i < nb; ++i, ++kv_count) {
+            const int row = krow + tile_at(set, i) * kKvTileRows;
+            const int st = kv_count % C::kStages;
+            const uint32_t ph = (kv_count / C::kStages) & 1;
+            if (!(ok = wait(&sh.k_empty[st], ph ^ 1))) break;
+            if (lane == 0) {
+              mbar_expect_tx(&sh.k_full[st], C::kTileBytes);
+              for (int d = 0; d < C::kSub; ++d)
+                tma_load_3d(smem + C::kOffK + st * C::kTileBytes + d * kSubBytes, &tmK,
+                            &sh.k_full[st], d * 64, hk, row);
+            }
+            if (!(ok = wait(&sh.v_empty[st], ph ^ 1))) break;
+            if (lane == 0) {
+              mbar_expect_tx(&sh.v_full[st], C::kTileBytes);
+              for (int d = 0; d < C::kSub; ++d)
+                tma_load_3d(smem + C::kOffV + st * C::kTileBytes + d * kSubBytes, &tmV,
+                            &sh.v_full[st], d * 64, hk, row);
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.item_empty[kq & 1]);
         if (!ok) break;
       }
     } else if (lane == 0) {
@@ -297,7 +296,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const int w = fwd_item_publish(sh, P, kq, abort_flag, tmo, status);
         if (w < 0 || w >= P.n_items) break;
         const FwdItem it = decode_fwd(P, w);
-        const FwdWalk wk = fwd_walk<WIN>(P, it);
+        const FwdWalk wk = fwd_walk(P, it);
         if (wk.N == 0) continue;
         const SeqDesc& sd = P.seq[it.seq];
         if (!mbar_wait(&sh.q_empty, q_phase ^ 1, abort_flag, tmo, status)) goto producer_done;
@@ -345,15 +344,27 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const uint32_t sV = smem_u32(smem + C::kOffV);
       bool ok = true;
       for (int kq = 0; ok; ++kq) {
-        int tiles = 0;
-        const int w = fwd_item_take(sh, kq, abort_flag, tmo, status, WIN ? &tiles : nullptr);
-        if (w < 0) ok = false;
-        if (w < 0 || w >= P.n_items) break;
-        const FwdItem it = decode_fwd(P, w);
-        const FwdWalk wk = fwd_walk<WIN>(P, it);
-        const int N = WIN ? tiles : wk.N;
+        int w, N;
+        bool two;
+        if constexpr (WIN) {
+          if (!(ok = mbar_wait(&sh.item_full[kq & 1], (kq >> 1) & 1, abort_flag, tmo, status))) break;
+          const WinSlot& item = win.slot[kq & 1];
+          w = item.item;
+          N = item.tiles;
+          two = item.a1 - item.a0 >= kQTileRows;
+          mbar_arrive(&sh.item_empty[kq & 1]);
+          if (w >= P.n_items) break;
+        } else {
+          w = fwd_item_take(sh, kq, abort_flag, tmo, status);
+          if (w < 0) ok = false;
+          if (w < 0 || w >= P.n_items) break;
+          const FwdItem it = decode_fwd(P, w);
+          const FwdWalk wk = fwd_walk(P, it);
+          N = wk.N;
+          two = wk.two;
+        }
         if (N == 0) continue;
-        const int nt = wk.two ? 2 : 1;
+        const int nt = two ? 2 : 1;
         if (!(ok = mbar_wait(&sh.q_full, q_phase, abort_flag, tmo, status))) break;
         q_phase ^= 1;
         tc_fence_after();
@@ -430,30 +441,56 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     uint32_t xm_phase[2] = {0, 0};
     int xn = 0;  // max exchanges done (slot = xn & 1)
     for (int kq = 0;; ++kq) {
-      const int w = fwd_item_take(sh, kq, abort_flag, tmo, status, nullptr);
-      if (w < 0 || w >= P.n_items) break;
-      const FwdItem it = decode_fwd(P, w);
-      const FwdWalk wk = fwd_walk<WIN>(P, it);
-      if (t == 1 && !wk.two) continue;
-      const SeqDesc& sd = P.seq[it.seq];
+      const WinSlot* item = nullptr;  // windowed: in its slot until the item is done with
+      FwdItem it;
+      FwdWalk wk;
+      if constexpr (WIN) {
+        if (!mbar_wait(&sh.item_full[kq & 1], (kq >> 1) & 1, abort_flag, tmo, status)) break;
+        item = &win.slot[kq & 1];
+        if (item->item >= P.n_items) break;
+        wk.L = item->L;
+        wk.a0 = item->a0;
+        wk.two = item->a1 - item->a0 >= kQTileRows;
+        it.r = item->r;
+        if (t == 1 && !wk.two) {
+          mbar_arrive(&sh.item_empty[kq & 1]);
+          continue;
+        }
+      } else {
+        const int w = fwd_item_take(sh, kq, abort_flag, tmo, status);
+        if (w < 0 || w >= P.n_items) break;
+        it = decode_fwd(P, w);
+        wk = fwd_walk(P, it);
+        if (t == 1 && !wk.two) continue;
+      }
       const int a = wk.a0 + t * kQTileRows + row;
       const bool valid = a < wk.L;
-      const int orow = sd.row_off + it.r * P.shard_stride + a;
-      OutT* orow_ptr = out + (static_cast<size_t>(orow) * P.hq + it.h) * DH;
-      float* lse_ptr = lse + sd.lse_off + static_cast<size_t>(it.h) * P.lse_hstride +
-                       static_cast<size_t>(it.r) * P.shard_stride + a;
-      if (!WIN && wk.N == 0) {  // a block with no visible key at these steps
-        if (valid) {
-          float z[32];
+      OutT* orow_ptr = nullptr;
+      float* lse_ptr = nullptr;
+      if constexpr (!WIN) {
+        const SeqDesc& sd = P.seq[it.seq];
+        const int orow = sd.row_off + it.r * P.shard_stride + a;
+        orow_ptr = out + (static_cast<size_t>(orow) * P.hq + it.h) * DH;
+        lse_ptr = lse + sd.lse_off + static_cast<size_t>(it.h) * P.lse_hstride +
+                  static_cast<size_t>(it.r) * P.shard_stride + a;
+        if (wk.N == 0) {  // a block with no visible key at these steps
+          if (valid) {
+            float z[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) z[i] = 0.f;
+            for (int i = 0; i < 32; ++i) z[i] = 0.f;
 #pragma unroll
-          for (int c = 0; c < DH / 64; ++c) store_row32<OutT>(orow_ptr + hf * (DH / 2) + c * 32, z);
-          if (hf == 0) *lse_ptr = -INFINITY;
+            for (int c = 0; c < DH / 64; ++c) store_row32<OutT>(orow_ptr + hf * (DH / 2) + c * 32, z);
+            if (hf == 0) *lse_ptr = -INFINITY;
+          }
+          continue;
         }
-        continue;
       }
       const int64_t pq = valid ? layout_pos(P.layout, P.D, wk.L, it.r, a) : 0;
+      KeyLimit upto, before;  // windowed: the last key seen, the last one before the window
+      if constexpr (WIN) {
+        upto = key_limit_of(P, static_cast<int>(pq));
+        before = key_limit_of(P, static_cast<int>(pq - P.window));
+      }
       float m = -INFINITY, l = 0.f;
       int n = 0;
       bool ok = true;
@@ -461,20 +498,20 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const bool got = mbar_wait(bar, parity, abort_flag, tmo, status);
         return WIN ? __all_sync(0xffffffffu, got) : got;  // the windowed walk is the warp's
       };
-      unsigned shards = 0;  // windowed: the next 32 steps' shards that have tiles
-      for (int s = P.step_begin; s < P.step_end && ok; ++s) {
-        if constexpr (WIN) {
-          if ((s & 31) == 0) shards = nonempty(P.D, s, [&](int i) { return fwd_set(P, it, wk, i); });
-          if (!((shards >> (s & 31)) & 1u)) continue;
-        }
-        const int j = shard_at_step(P.D, it.r, s);
+      const int s_end = WIN ? item->nseg : P.step_end;
+      for (int s = WIN ? 0 : P.step_begin; s < s_end && ok; ++s) {
+        const int j = WIN ? item->seg[s].j : shard_at_step(P.D, it.r, s);
         TileSet set;
-        if constexpr (WIN) set = fwd_set(P, it, wk, s);
+        if constexpr (WIN) set = tiles_of(item->seg[s]);
         const int nb = WIN ? tile_count(set) : kv_tiles_for(P, wk.L, it.r, j, wk.a_last);
-        const int lim = !valid ? -1 : (P.causal ? key_limit(P.layout, P.D, wk.L, j, pq) : wk.L - 1);
-        // windowed: of the shard's keys up to lim this row sees those before sk, and from lo on
-        const int lo = WIN ? first_query(P.layout, P.D, wk.L, j, pq - P.window + 1) : 0;
-        const int sk = WIN ? sink_rows(P, wk.L, j) : 0;
+        int lim, lo = 0, sk = 0;
+        if constexpr (WIN) {  // of the shard's keys up to lim this row sees those before sk, and from lo on
+          lim = valid ? limit_in(P, wk.L, j, upto) : -1;
+          lo = limit_in(P, wk.L, j, before) + 1;
+          sk = item->seg[s].sk;
+        } else {
+          lim = !valid ? -1 : (P.causal ? key_limit(P.layout, P.D, wk.L, j, pq) : wk.L - 1);
+        }
         for (int i = 0; i < nb; ++i, ++n) {
           const int b = WIN ? tile_at(set, i) : i;
           if (!(ok = wait(&sh.s_full[t], s_phase))) break;
@@ -608,6 +645,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       od_phase ^= 1;
       tc_fence_after();
       const float inv_l = l > 0.f ? 1.f / l : 0.f;
+      if constexpr (WIN) {
+        orow_ptr = out + (static_cast<size_t>(item->row + t * kQTileRows + row) * P.hq + item->h) * DH;
+        lse_ptr = lse + item->lse + t * kQTileRows + row;
+      }
 #pragma unroll
       for (int c = 0; c < DH / 64; ++c) {
         uint32_t r[32];
@@ -620,6 +661,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       if (valid && hf == 0) *lse_ptr = l > 0.f ? (m + lg2(l)) * 0.69314718055994531f : -INFINITY;
       tc_fence_before();
       mbar_arrive(&sh.o_free[t]);
+      if constexpr (WIN) mbar_arrive(&sh.item_empty[kq & 1]);
     }
   }
 

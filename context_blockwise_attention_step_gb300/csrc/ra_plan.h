@@ -161,6 +161,7 @@ RA_HD int row_key_count(const Plan& P, int L, int r, int a, int j, int b) {
 // prefix of it, the window a run [first, limit]. At most kMaxSinks sinks, so that the sinks of
 // a shard lie in its first tile.
 constexpr int kMaxSinks = 128;
+constexpr int kMaxWindowShards = 64;  // D of the tensor-core kernels' windows
 
 // Local rows of shard j that are sinks (a prefix), and the shards 0 .. sink_shards - 1 that
 // have any.

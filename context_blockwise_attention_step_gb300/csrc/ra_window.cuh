@@ -1,4 +1,4 @@
-// ra_window.cuh — warp-collective walks of the windowed kernels over a block's tiles.
+// ra_window.cuh — the windowed kernels' walks over a block's tiles.
 //
 // A windowed block sees tiles of few shards, and finding a shard's tiles takes a chain of
 // layout arithmetic (~200 cycles): a warp works out 32 shards at once, one per lane, and walks
@@ -33,13 +33,6 @@ __device__ __forceinline__ bool for_each_set(int n, SetF&& set, BodyF&& body) {
   return true;
 }
 
-// Bit i: set(base + i) is not empty, for the 32 sets from base on.
-template <typename SetF>
-__device__ __forceinline__ unsigned nonempty(int n, int base, SetF&& set) {
-  const int i = base + (threadIdx.x & 31);
-  return __ballot_sync(0xffffffffu, i < n && tile_count(set(i)) > 0);
-}
-
 // The tiles of all n sets.
 template <typename SetF>
 __device__ __forceinline__ int count_tiles(int n, SetF&& set) {
@@ -58,6 +51,82 @@ __device__ __forceinline__ uint32_t low_bits(int n) {
 // The visible columns c of a tile among [cs, cs + 32): c < cnt and (c >= lo or c < sk).
 __device__ __forceinline__ uint32_t visible_bits(int cs, int cnt, int lo, int sk) {
   return low_bits(cnt - cs) & (~low_bits(lo - cs) | low_bits(sk - cs));
+}
+
+// ---- query blocks: what the producer warp works out of an item ahead of the other warps, which
+// would have to wait for the arithmetic (12000 cycles of a 60000-cycle item, measured) ----------
+struct WinSeg {
+  uint8_t j, sk;           // K/V shard, its sink rows (<= 128)
+  uint16_t sink;           // its tiles (TileSet)
+  int s0, n0, s1, n1;
+};
+struct WinSlot {
+  int item;       // >= n_items: the end
+  int tiles, nseg;
+  int h, r, L, a0, a1;  // query head, rank, local length, first and last row of the block
+  int row, lse;   // shard-major row of a0; element of lse of a0
+  WinSeg seg[kMaxWindowShards];
+};
+
+// Fills in a slot for query rows a0 .. a1 of rank r (the whole warp).
+__device__ __forceinline__ void fill_slot(WinSlot& w, const Plan& P, int seq, int h, int r, int a0, int a1) {
+  const SeqDesc& sd = P.seq[seq];
+  const int lane = threadIdx.x & 31, L = sd.L;
+  int nseg = 0, tiles = 0;
+  for (int base = 0; base < P.D; base += 32) {
+    TileSet t = {0, 0, 0, 0, 0};
+    const int j = base + lane < P.D ? shard_at_step(P.D, r, base + lane) : 0;
+    if (base + lane < P.D) t = window_kv_tiles(P, L, r, j, a0, a1);
+    const int n = tile_count(t);
+    const unsigned some = __ballot_sync(0xffffffffu, n > 0);
+    if (n > 0) w.seg[nseg + __popc(some & ((1u << lane) - 1u))] =
+          {static_cast<uint8_t>(j), static_cast<uint8_t>(sink_rows(P, L, j)), static_cast<uint16_t>(t.sink),
+           t.s0, t.n0, t.s1, t.n1};
+    nseg += __popc(some);
+    tiles += n;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
+  if (lane == 0) {
+    w.tiles = tiles;
+    w.nseg = nseg;
+    w.h = h;
+    w.r = r;
+    w.L = L;
+    w.a0 = a0;
+    w.a1 = a1;
+    w.row = sd.row_off + r * P.shard_stride + a0;
+    w.lse = sd.lse_off + h * P.lse_hstride + r * P.shard_stride + a0;
+  }
+  __syncwarp();
+}
+__device__ __forceinline__ TileSet tiles_of(const WinSeg& g) { return {g.sink, g.s0, g.n0, g.s1, g.n1}; }
+
+// key_limit() for one position and many shards, in 32 bits (positions stay below 2^31): the
+// stripe layout's division is done once.
+struct KeyLimit {
+  int p, d, m;  // position; p / D and p % D (stripe)
+};
+__device__ __forceinline__ KeyLimit key_limit_of(const Plan& P, int p) {
+  KeyLimit k = {p, 0, 0};
+  if (P.layout == kStripe && p >= 0) {
+    k.d = p / P.D;
+    k.m = p - k.d * P.D;
+  }
+  return k;
+}
+__device__ __forceinline__ int limit_in(const Plan& P, int L, int j, const KeyLimit& k) {
+  if (k.p < 0) return -1;
+  int b;
+  if (P.layout == kStripe) {
+    b = k.d - (j > k.m ? 1 : 0);
+  } else if (P.layout == kBasic) {
+    b = k.p - j * L;
+  } else {
+    const int c = L >> 1, second = (2 * P.D - 1 - j) * c;
+    b = k.p >= second ? c + k.p - second : min(k.p - j * c, c - 1);
+  }
+  return max(-1, min(b, L - 1));
 }
 
 }  // namespace ra

@@ -195,8 +195,8 @@ int ra_ring_attn_bwd_noalloc(const ra_problem* p, const void* q, const void* k, 
 
 /* Ring attention with a sliding window: the query at position p of a sequence sees the keys at
  * positions k <= p with k > p - window or k < sinks (the first `sinks` tokens of every
- * sequence stay visible). The problem must be causal; window >= 1, 0 <= sinks <=
- * RA_MAX_SINKS. Tensors, layouts, lse and the optional workspace (now
+ * sequence stay visible). The problem must be causal, with D <= 64 in bf16; window >= 1, 0 <=
+ * sinks <= RA_MAX_SINKS. Tensors, layouts, lse and the optional workspace (now
  * ra_window_workspace_bytes(p, window, sinks, 0)) are as for ra_ring_attn_fwd; K/V tiles that
  * no query of a block sees are never loaded. With a window that no sequence is longer than,
  * this is ra_ring_attn_fwd. As there, k and v must be finite: hidden keys of a loaded tile

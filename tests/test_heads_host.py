@@ -175,6 +175,7 @@ def test_window_refusals():
     assert fwd(sinks=_abi.RA_MAX_SINKS + 1) == _abi.RA_ERR_INVALID_ARG
     assert fwd(p=_prob(causal=False)) == _abi.RA_ERR_UNSUPPORTED
     assert fwd(p=_prob(seqlen=60)) == _abi.RA_ERR_SHAPE
+    assert fwd(p=_prob(D=65, layout="basic", seqlen=650)) == _abi.RA_ERR_UNSUPPORTED
     assert fwd(q=None) == _abi.RA_ERR_INVALID_ARG
     assert fwd(ws=64, size=1024) == _abi.RA_ERR_INVALID_ARG
     assert fwd(window=1 << 30, q=None) == _abi.RA_ERR_INVALID_ARG  # the ring call's refusals
