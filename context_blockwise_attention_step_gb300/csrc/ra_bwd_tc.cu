@@ -80,6 +80,8 @@ struct BwdCfg {
   static constexpr int kOffLs = kOffDS + 2 * kSubBytes;      // [2 slots][-lse*log2e | delta][128]
   static constexpr int kOffBar = kOffLs + 2 * 2 * 128 * 4;
   static constexpr int kSmemBytes = kOffBar + 256;
+  static constexpr int kOffWin = kOffBar + 256;  // windowed: the item queue's slots
+  static constexpr int kSmemWindow = kOffWin + 256;
   static constexpr int kKSteps = DH / 16;
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kColDK = 0, kColDV = DH, kColX = 2 * DH, kColY = 2 * DH + 128;
@@ -93,12 +95,11 @@ struct BwdBars {
   uint64_t acc_done, drain;
   uint64_t item_full[2], item_empty[2];  // the CTA's item queue
   int item[2];
-  int item_tiles[2];  // windowed: query tiles of the item, over the heads of the group
   uint32_t tmem_base;
   int abort_flag;
 };
 static_assert(sizeof(BwdBars) <= 256, "barrier block");
-static_assert(BwdCfg<128>::kSmemBytes <= 232448, "shared memory budget");
+static_assert(BwdCfg<128>::kSmemWindow <= 232448, "shared memory budget");
 
 struct BwdWalk {
   int L, b0, N, nqt;
@@ -145,60 +146,84 @@ __device__ __forceinline__ bool for_each_qtile(const Plan& P, const BwdItem& it,
 }
 
 // ---- windowed walks
-// Item w of the windowed pass; sink.r < 0: a K/V tile's window item.
+// An item of the windowed pass, worked out by the producer warp and left in the item queue's slot.
 struct WinItem {
-  BwdItem it;
-  SinkItem sink;
-  int L, b0, ranks;  // ranks: query ranks that the walk goes over
+  int item;             // >= n_items: the end
+  int tiles;            // query tiles, over the heads of the group
+  int L, j, hk, b0;     // local length; K/V shard, head, first row of the tile
+  int row_off, lse_off; // of the sequence
+  int sink_r, sink_chunk;  // a sink item's query rank (< 0: a K/V tile's window item) and chunk
+  int sinks, slot;      // sink rows of the tile, and the slot for their sums
 };
+static_assert(2 * sizeof(WinItem) <= 256, "windowed slots");
 
-__device__ __forceinline__ WinItem win_item(const Plan& P, int w) {
-  WinItem x;
-  x.it = decode_window_bwd(P, w, &x.sink);
-  x.L = P.seq[x.it.seq].L;
-  x.b0 = x.it.kt * kKvTileRows;
-  x.ranks = x.sink.r >= 0 ? 1 : P.D;
-  return x;
-}
-__device__ __forceinline__ int win_rank(const WinItem& x, int i) { return x.sink.r >= 0 ? x.sink.r : i; }
-
-// The query tiles of the i-th rank of the walk.
-__device__ __forceinline__ TileSet win_set(const Plan& P, const WinItem& x, int i) {
-  if (x.sink.r < 0)
-    return window_q_tiles(P, x.L, x.it.j, i, x.b0, min(x.L, x.b0 + kKvTileRows) - 1);
-  // beyond the window of the shard's first sink
-  const int64_t p0 = layout_pos(P.layout, P.D, x.L, x.it.j, 0) + P.window;
-  const int a = first_query(P.layout, P.D, x.L, x.sink.r, p0);
-  const int first = max(a / kQTileRows, x.sink.chunk * P.sink_chunk);
-  const int end = min(ceil_div(x.L, kQTileRows), (x.sink.chunk + 1) * P.sink_chunk);
-  TileSet t = {0, 0, 0, 0, 0};
-  if (a < x.L && first < end) {
-    t.s0 = first;
-    t.n0 = end - first;
+// The query positions that an item's tile is seen from: one run, or two where the tile lies on
+// both sides of a zigzag shard's chunks.
+struct WinSpan {
+  KeyLimit before0, last0, before1, last1;
+  bool two;
+};
+__device__ __forceinline__ WinSpan win_span(const Plan& P, const WinItem& x) {
+  WinSpan s;
+  const int b1 = min(x.L, x.b0 + kKvTileRows) - 1;
+  auto pos = [&](int b) { return static_cast<int>(layout_pos(P.layout, P.D, x.L, x.j, b)); };
+  auto from = [&](int p) { return key_limit_of(P, p - 1); };
+  auto upto = [&](int p) {
+    return key_limit_of(P, static_cast<int>(min(static_cast<int64_t>(p) + P.window - 1, int64_t(0x7fffffff))));
+  };
+  s.two = straddles(P, x.L, x.b0, b1);
+  const int mid = s.two ? x.L >> 1 : x.b0;
+  if (x.sink_r >= 0) {  // beyond the window of the shard's first sink
+    s.before0 = upto(pos(0));
+    return s;
   }
+  if (s.two) {
+    s.before0 = from(pos(x.b0));
+    s.last0 = upto(pos(mid - 1));
+  }
+  s.before1 = from(pos(mid));
+  s.last1 = upto(pos(b1));
+  return s;
+}
+
+// The query tiles of rank r.
+__device__ __forceinline__ TileSet win_set(const Plan& P, const WinItem& x, const WinSpan& s, int r) {
+  TileSet t = {0, 0, 0, 0, 0};
+  if (x.sink_r >= 0) {
+    const int a = limit_in(P, x.L, r, s.before0) + 1;
+    const int first = max(a / kQTileRows, x.sink_chunk * P.sink_chunk);
+    const int end = min(ceil_div(x.L, kQTileRows), (x.sink_chunk + 1) * P.sink_chunk);
+    if (a < x.L && first < end) {
+      t.s0 = first;
+      t.n0 = end - first;
+    }
+    return t;
+  }
+  if (s.two) add_tiles(t, limit_in(P, x.L, r, s.before0) + 1, limit_in(P, x.L, r, s.last0), kQTileRows);
+  add_tiles(t, limit_in(P, x.L, r, s.before1) + 1, limit_in(P, x.L, r, s.last1), kQTileRows);
   return t;
 }
 
-// Calls f(r, h, q0) for every query tile the item visits, in walk order, with the whole warp.
-template <typename F>
-__device__ __forceinline__ bool win_for_each_qtile(const Plan& P, const WinItem& x, F&& f) {
+// For every rank with tiles, rank(r), then f(r, h, q0) for its query tiles, in walk order, with
+// the whole warp.
+template <typename RankF, typename F>
+__device__ __forceinline__ bool win_for_each_qtile(const Plan& P, const WinItem& x, RankF&& rank, F&& f) {
+  const WinSpan span = win_span(P, x);
   return for_each_set(
-      x.ranks, [&](int i) { return win_set(P, x, i); },
+      x.sink_r >= 0 ? 1 : P.D, [&](int i) { return win_set(P, x, span, x.sink_r >= 0 ? x.sink_r : i); },
       [&](int i, const TileSet& set) -> bool {
-        const int nq = tile_count(set);
+        const int r = x.sink_r >= 0 ? x.sink_r : i, nq = tile_count(set);
+        rank(r);
         for (int g = 0; g < P.group; ++g)
           for (int k = 0; k < nq; ++k)
-            if (!f(win_rank(x, i), x.it.hk * P.group + g, tile_at(set, k) * kQTileRows)) return false;
+            if (!f(r, x.hk * P.group + g, tile_at(set, k) * kQTileRows)) return false;
         return true;
       });
 }
 
-// First element of slot row `row` (dk; dv follows after all rows) of a sink tile's item.
+// Slot row `row` of the item's sink sums, dk (which 0) or dv (1).
 __device__ __forceinline__ float* sink_row(const Plan& P, const WinItem& x, int row, int which) {
-  const SeqDesc& s = P.seq[x.it.seq];
-  const int item = x.sink.r < 0 ? 0 : 1 + x.sink.r * sink_chunks(P, x.L) + x.sink.chunk;
-  const int64_t slot = sink_slot(P, s, x.it.j, x.it.hk, item);
-  return P.sink_sums + ((slot * 2 + which) * P.sinks + row) * P.head_dim;
+  return P.sink_sums + ((static_cast<int64_t>(x.slot) * 2 + which) * P.sinks + row) * P.head_dim;
 }
 
 __device__ __forceinline__ void store_row32_f32(float* dst, const uint32_t (&r)[32], float mul) {
@@ -374,19 +399,19 @@ __device__ __forceinline__ int item_publish(BwdBars& sh, const Plan& P, int k,
   return w;
 }
 __device__ __forceinline__ int item_take(BwdBars& sh, int k, volatile int* abort_flag,
-                                         uint64_t tmo, unsigned int* status, int* tiles = nullptr) {
+                                         uint64_t tmo, unsigned int* status) {
   const int slot = k & 1;
   if (!mbar_wait(&sh.item_full[slot], (k >> 1) & 1, abort_flag, tmo, status)) return -1;
   const int w = *reinterpret_cast<volatile int*>(&sh.item[slot]);
-  if (tiles != nullptr) *tiles = *reinterpret_cast<volatile int*>(&sh.item_tiles[slot]);
   mbar_arrive(&sh.item_empty[slot]);
   return w;
 }
 
-// The windowed kernel's producer warp: takes the next item, counts its tiles, publishes both.
-__device__ __forceinline__ int win_item_publish(BwdBars& sh, const Plan& P, int k, int lane,
+// The windowed kernel's producer warp: takes the next item and fills in its slot, which the other
+// roles read in place and release when they have done with the item.
+__device__ __forceinline__ int win_item_publish(BwdBars& sh, WinItem* slots, const Plan& P, int k, int lane,
                                                 volatile int* abort_flag, uint64_t tmo,
-                                                unsigned int* status, int* tiles) {
+                                                unsigned int* status) {
   const int slot = k & 1;
   const bool ok = mbar_wait(&sh.item_empty[slot], ((k >> 1) & 1) ^ 1, abort_flag, tmo, status);
   if (!__all_sync(0xffffffffu, ok)) return -1;
@@ -395,17 +420,32 @@ __device__ __forceinline__ int win_item_publish(BwdBars& sh, const Plan& P, int 
     w = P.work_counter ? atomicAdd(P.work_counter, 1)
                        : static_cast<int>(blockIdx.x + static_cast<unsigned>(k) * gridDim.x);
   w = __shfl_sync(0xffffffffu, w, 0);
-  int n = 0;
+  WinItem x = {};
+  x.item = w;
   if (w < P.n_items) {
-    const WinItem x = win_item(P, w);
-    n = count_tiles(x.ranks, [&](int i) { return win_set(P, x, i); }) * P.group;
+    SinkItem sink;
+    const BwdItem it = decode_window_bwd(P, w, &sink);
+    const SeqDesc& sd = P.seq[it.seq];
+    x.L = sd.L;
+    x.j = it.j;
+    x.hk = it.hk;
+    x.b0 = it.kt * kKvTileRows;
+    x.row_off = sd.row_off;
+    x.lse_off = sd.lse_off;
+    x.sink_r = sink.r;
+    x.sink_chunk = sink.chunk;
+    x.sinks = it.kt == 0 ? sink_rows(P, sd.L, it.j) : 0;
+    if (x.sinks > 0)
+      x.slot = sink_slot(P, sd, it.j, it.hk, sink.r < 0 ? 0 : 1 + sink.r * sink_chunks(P, sd.L) + sink.chunk);
+    const WinSpan span = win_span(P, x);
+    x.tiles = P.group * count_tiles(sink.r >= 0 ? 1 : P.D,
+                                    [&](int i) { return win_set(P, x, span, sink.r >= 0 ? sink.r : i); });
   }
   if (lane == 0) {
-    sh.item[slot] = w;
-    sh.item_tiles[slot] = n;
+    slots[slot] = x;
     mbar_arrive(&sh.item_full[slot]);
   }
-  *tiles = n;
+  __syncwarp();
   return w;
 }
 
@@ -421,6 +461,7 @@ __global__ void __launch_bounds__(bwd_threads<kWithDQ>(), 1)
   using C = BwdCfg<DH>;
   extern __shared__ __align__(1024) uint8_t smem[];
   BwdBars& sh = *reinterpret_cast<BwdBars*>(smem + C::kOffBar);
+  WinItem* slots = reinterpret_cast<WinItem*>(smem + C::kOffWin);  // windowed only
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (smem_u32(smem) & 1023u) {  // the swizzled tiles need a 1024-byte aligned base
     if (threadIdx.x == 0) atomicOr(&g_status_bwd, 2u);
@@ -449,7 +490,8 @@ __global__ void __launch_bounds__(bwd_threads<kWithDQ>(), 1)
     mbar_init(&sh.acc_done, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.item_full[i], 1);
-      mbar_init(&sh.item_empty[i], 1 + 32 + 256 + (kWithDQ ? 128 : 0));
+      // windowed: the producer reads the slot too
+      mbar_init(&sh.item_empty[i], 1 + 32 + 256 + (kWithDQ ? 128 : 0) + (WIN ? 1 : 0));
     }
     mbar_init(&sh.drain, 1);
     sh.abort_flag = 0;
@@ -479,27 +521,27 @@ __global__ void __launch_bounds__(bwd_threads<kWithDQ>(), 1)
         return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, tmo, status));
       };
       for (int kq = 0;; ++kq) {
-        int tiles = 0;
-        const int w = win_item_publish(sh, P, kq, lane, abort_flag, tmo, status, &tiles);
+        const int w = win_item_publish(sh, slots, P, kq, lane, abort_flag, tmo, status);
         if (w < 0 || w >= P.n_items) break;
-        if (tiles == 0) continue;
-        const WinItem x = win_item(P, w);
-        const SeqDesc& sd = P.seq[x.it.seq];
+        const WinItem x = slots[kq & 1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.item_empty[kq & 1]);
+        if (x.tiles == 0) continue;
         if (!wait(&sh.kv_empty, kv_phase ^ 1)) break;
         kv_phase ^= 1;
         if (lane == 0) {
           mbar_expect_tx(&sh.kv_full, 2 * C::kTileBytes);
-          const int krow = sd.row_off + x.it.j * P.shard_stride + x.b0;
+          const int krow = x.row_off + x.j * P.shard_stride + x.b0;
           for (int d = 0; d < C::kSub; ++d) {
-            tma_load_3d(smem + C::kOffK + d * kSubBytes, &tmK, &sh.kv_full, d * 64, x.it.hk, krow);
-            tma_load_3d(smem + C::kOffV + d * kSubBytes, &tmV, &sh.kv_full, d * 64, x.it.hk, krow);
+            tma_load_3d(smem + C::kOffK + d * kSubBytes, &tmK, &sh.kv_full, d * 64, x.hk, krow);
+            tma_load_3d(smem + C::kOffV + d * kSubBytes, &tmV, &sh.kv_full, d * 64, x.hk, krow);
           }
         }
-        const bool ok = win_for_each_qtile(P, x, [&](int r, int h, int q0) -> bool {
+        const bool ok = win_for_each_qtile(P, x, [](int) {}, [&](int r, int h, int q0) -> bool {
           const int st = qcount & 1;
           if (!wait(&sh.q_empty[st], ((qcount >> 1) & 1) ^ 1)) return false;
           if (lane == 0) {  // Q first, on its own barrier, as below
-            const int qrow = sd.row_off + r * P.shard_stride + q0;
+            const int qrow = x.row_off + r * P.shard_stride + q0;
             uint8_t* base = smem + C::kOffQ + st * C::kStageBytes;
             mbar_expect_tx(&sh.q_full[st], C::kTileBytes);
             for (int d = 0; d < C::kSub; ++d)
@@ -573,15 +615,18 @@ __global__ void __launch_bounds__(bwd_threads<kWithDQ>(), 1)
       };
       bool ok = true;
       for (int kq = 0; ok; ++kq) {
-        int tiles = 0;
-        const int w = item_take(sh, kq, abort_flag, tmo, status, WIN ? &tiles : nullptr);
-        if (w < 0) ok = false;
-        if (w < 0 || w >= P.n_items) break;
         BwdItem it;
         BwdWalk wk;
         if constexpr (WIN) {
-          wk.N = tiles;
+          if (!(ok = mbar_wait(&sh.item_full[kq & 1], (kq >> 1) & 1, abort_flag, tmo, status))) break;
+          const int w = slots[kq & 1].item;
+          wk.N = slots[kq & 1].tiles;
+          mbar_arrive(&sh.item_empty[kq & 1]);
+          if (w >= P.n_items) break;
         } else {
+          const int w = item_take(sh, kq, abort_flag, tmo, status);
+          if (w < 0) ok = false;
+          if (w < 0 || w >= P.n_items) break;
           it = decode_bwd(P, w);
           wk = bwd_walk(P, it);
         }
@@ -735,27 +780,32 @@ __global__ void __launch_bounds__(bwd_threads<kWithDQ>(), 1)
     float* ls_base = reinterpret_cast<float*>(smem + C::kOffLs);
     int t = 0;
     for (int kq = 0;; ++kq) {
-      const int w = item_take(sh, kq, abort_flag, tmo, status);
-      if (w < 0 || w >= P.n_items) break;
       WinItem x = {};
       BwdItem it;
       BwdWalk wk;
+      int lse_off;
       if constexpr (WIN) {
-        x = win_item(P, w);
-        it = x.it;
+        const bool got = mbar_wait(&sh.item_full[kq & 1], (kq >> 1) & 1, abort_flag, tmo, status);
+        if (!__all_sync(0xffffffffu, got)) break;
+        x = slots[kq & 1];
+        mbar_arrive(&sh.item_empty[kq & 1]);
+        if (x.item >= P.n_items) break;
         wk.L = x.L;
+        lse_off = x.lse_off;
       } else {
+        const int w = item_take(sh, kq, abort_flag, tmo, status);
+        if (w < 0 || w >= P.n_items) break;
         it = decode_bwd(P, w);
         wk = bwd_walk(P, it);
         if (wk.N == 0) continue;
+        lse_off = P.seq[it.seq].lse_off;
       }
-      const SeqDesc& sd = P.seq[it.seq];
       auto qtile = [&](int r, int h, int q0) -> bool {
         const int slot = t & 1;
         const bool got = mbar_wait(&sh.ls_empty[slot], ((t >> 1) & 1) ^ 1, abort_flag, tmo, status);
         if (!(WIN ? __all_sync(0xffffffffu, got) : got)) return false;
         float* nl = ls_base + slot * 256;
-        const size_t li0 = sd.lse_off + static_cast<size_t>(h) * P.lse_hstride +
+        const size_t li0 = lse_off + static_cast<size_t>(h) * P.lse_hstride +
                            static_cast<size_t>(r) * P.shard_stride + q0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -774,7 +824,7 @@ __global__ void __launch_bounds__(bwd_threads<kWithDQ>(), 1)
         return true;
       };
       bool ok;
-      if constexpr (WIN) ok = win_for_each_qtile(P, x, qtile);
+      if constexpr (WIN) ok = win_for_each_qtile(P, x, [](int) {}, qtile);
       else ok = for_each_qtile(P, it, wk, qtile);
       if (!ok) break;
     }
@@ -792,30 +842,36 @@ __global__ void __launch_bounds__(bwd_threads<kWithDQ>(), 1)
     uint32_t s_phase = 0, dp_phase = 0, ad_phase = 0;
     int t = 0;
     for (int kq = 0;; ++kq) {
-      int tiles = 0;
-      const int w = item_take(sh, kq, abort_flag, tmo, status, WIN ? &tiles : nullptr);
-      if (w < 0 || w >= P.n_items) break;
       WinItem x = {};
       BwdItem it;
       BwdWalk wk;
+      int row_off;
       if constexpr (WIN) {
-        x = win_item(P, w);
-        it = x.it;
+        const bool got = mbar_wait(&sh.item_full[kq & 1], (kq >> 1) & 1, abort_flag, tmo, status);
+        if (!__all_sync(0xffffffffu, got)) break;
+        x = slots[kq & 1];
+        mbar_arrive(&sh.item_empty[kq & 1]);
+        if (x.item >= P.n_items) break;
+        it.j = x.j;
+        it.hk = x.hk;
         wk.L = x.L;
         wk.b0 = x.b0;
-        wk.N = tiles;
+        wk.N = x.tiles;
+        row_off = x.row_off;
       } else {
+        const int w = item_take(sh, kq, abort_flag, tmo, status);
+        if (w < 0 || w >= P.n_items) break;
         it = decode_bwd(P, w);
         wk = bwd_walk(P, it);
+        row_off = P.seq[it.seq].row_off;
       }
-      const SeqDesc& sd = P.seq[it.seq];
       const int b = wk.b0 + row;
       const bool validk = b < wk.L;
-      const size_t krow = static_cast<size_t>(sd.row_off + it.j * P.shard_stride + b);
+      const size_t krow = static_cast<size_t>(row_off + it.j * P.shard_stride + b);
       const size_t out_off = (krow * P.hkv + it.hk) * DH;
       // windowed: sink rows go to the item's slot, and a sink item has no other rows
-      const bool is_sink = WIN && validk && b < sink_rows(P, wk.L, it.j);
-      const bool store = validk && !(WIN && (is_sink || x.sink.r >= 0));
+      const bool is_sink = WIN && validk && b < x.sinks;
+      const bool store = validk && !(WIN && (is_sink || x.sink_r >= 0));
       if (wk.N == 0) {
         if constexpr (WIN) {
           if (is_sink) {
@@ -843,15 +899,25 @@ __global__ void __launch_bounds__(bwd_threads<kWithDQ>(), 1)
         const bool got = mbar_wait(bar, parity, abort_flag, tmo, status);
         return WIN ? __all_sync(0xffffffffu, got) : got;  // the windowed walk is the warp's
       };
+      // windowed: the row's queries in the current rank are a_lo .. a_hi - 1: positions pk .. pk +
+      // window - 1, or, of a sink item, from pk + window on
+      KeyLimit before, last;
+      int a_lo = 0, a_hi = 0;
+      if constexpr (WIN) {
+        last = key_limit_of(P, static_cast<int>(min(pk + P.window - 1, int64_t(0x7fffffff))));
+        before = x.sink_r >= 0 ? last : key_limit_of(P, static_cast<int>(pk) - 1);
+      }
+      auto rank = [&](int r) {
+        const bool far = x.sink_r >= 0;
+        a_lo = validk && (!far || is_sink) ? limit_in(P, wk.L, r, before) + 1 : wk.L + kQTileRows;
+        a_hi = far ? wk.L + kQTileRows : limit_in(P, wk.L, r, last) + 1;
+      };
       auto qtile = [&](int r, int, int q0) -> bool {
         const int slot = t & 1;
         int lo, hi = 128;
-        if constexpr (WIN) {  // queries at pk .. pk + window - 1, or from pk + window on
-          const bool far = x.sink.r >= 0;
-          lo = validk && (!far || is_sink)
-                   ? first_query(P.layout, P.D, wk.L, r, far ? pk + P.window : pk) - q0
-                   : 128;
-          if (!far) hi = key_limit(P.layout, P.D, wk.L, r, pk + P.window - 1) + 1 - q0;
+        if constexpr (WIN) {
+          lo = a_lo - q0;
+          hi = a_hi - q0;
         } else {
           lo = validk ? (P.causal ? first_query(P.layout, P.D, wk.L, r, pk) - q0 : 0) : 128;
         }
@@ -907,7 +973,7 @@ __global__ void __launch_bounds__(bwd_threads<kWithDQ>(), 1)
         return true;
       };
       bool ok;
-      if constexpr (WIN) ok = win_for_each_qtile(P, x, qtile);
+      if constexpr (WIN) ok = win_for_each_qtile(P, x, rank, qtile);
       else ok = for_each_qtile(P, it, wk, qtile);
       if (!ok) break;
       // dK (times scale; warpgroup 0) and dV (warpgroup 1) of this tile
@@ -1013,11 +1079,11 @@ cudaError_t launch_one(const Plan& P, const CUtensorMap& mq, const CUtensorMap& 
                        cudaStream_t st) {
   using C = BwdCfg<DH>;
   auto kern = ring_bwd_tc_kernel<DH, kWithDQ, kAccum, WIN>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       C::kSmemBytes);
+  constexpr int smem = WIN ? C::kSmemWindow : C::kSmemBytes;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int grid = P.n_items < n_sm ? P.n_items : n_sm;
-  kern<<<grid, bwd_threads<kWithDQ>(), C::kSmemBytes, st>>>(mq, mk, mv, mdo, P, lse, delta, dq_acc,
+  kern<<<grid, bwd_threads<kWithDQ>(), smem, st>>>(mq, mk, mv, mdo, P, lse, delta, dq_acc,
                                                             dk, dv);
   return cudaGetLastError();
 }

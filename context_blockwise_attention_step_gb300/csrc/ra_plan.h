@@ -228,21 +228,6 @@ RA_HD TileSet window_kv_tiles(const Plan& P, int L, int r, int j, int a0, int a1
   return t;
 }
 
-// Query tiles of rank r that see some of the rows b0 .. b1 of K/V shard j through the window.
-RA_HD TileSet window_q_tiles(const Plan& P, int L, int j, int r, int b0, int b1) {
-  TileSet t = {0, 0, 0, 0, 0};
-  int from = b0;
-  if (straddles(P, L, b0, b1)) {
-    from = L >> 1;
-    add_tiles(t, first_query(P.layout, P.D, L, r, layout_pos(P.layout, P.D, L, j, b0)),
-              key_limit(P.layout, P.D, L, r, layout_pos(P.layout, P.D, L, j, from - 1) + P.window - 1),
-              kQTileRows);
-  }
-  add_tiles(t, first_query(P.layout, P.D, L, r, layout_pos(P.layout, P.D, L, j, from)),
-            key_limit(P.layout, P.D, L, r, layout_pos(P.layout, P.D, L, j, b1) + P.window - 1), kQTileRows);
-  return t;
-}
-
 // The windowed K/V pass leaves the queries that see a sink from beyond the window to items of
 // their own, of at most sink_chunk query tiles of one rank: a sink is seen by the whole
 // sequence, and one item for it would outlast all the others. Every such item, and the

@@ -53,6 +53,33 @@ __device__ __forceinline__ uint32_t visible_bits(int cs, int cnt, int lo, int sk
   return low_bits(cnt - cs) & (~low_bits(lo - cs) | low_bits(sk - cs));
 }
 
+// key_limit() for one position and many shards, in 32 bits (positions stay below 2^31): the
+// stripe layout's division is done once.
+struct KeyLimit {
+  int p, d, m;  // position; p / D and p % D (stripe)
+};
+__device__ __forceinline__ KeyLimit key_limit_of(const Plan& P, int p) {
+  KeyLimit k = {p, 0, 0};
+  if (P.layout == kStripe && p >= 0) {
+    k.d = p / P.D;
+    k.m = p - k.d * P.D;
+  }
+  return k;
+}
+__device__ __forceinline__ int limit_in(const Plan& P, int L, int j, const KeyLimit& k) {
+  if (k.p < 0) return -1;
+  int b;
+  if (P.layout == kStripe) {
+    b = k.d - (j > k.m ? 1 : 0);
+  } else if (P.layout == kBasic) {
+    b = k.p - j * L;
+  } else {
+    const int c = L >> 1, second = (2 * P.D - 1 - j) * c;
+    b = k.p >= second ? k.p - second + c : min(k.p - j * c, c - 1);
+  }
+  return max(-1, min(b, L - 1));
+}
+
 // ---- query blocks: what the producer warp works out of an item ahead of the other warps, which
 // would have to wait for the arithmetic (12000 cycles of a 60000-cycle item, measured) ----------
 struct WinSeg {
@@ -101,32 +128,5 @@ __device__ __forceinline__ void fill_slot(WinSlot& w, const Plan& P, int seq, in
   __syncwarp();
 }
 __device__ __forceinline__ TileSet tiles_of(const WinSeg& g) { return {g.sink, g.s0, g.n0, g.s1, g.n1}; }
-
-// key_limit() for one position and many shards, in 32 bits (positions stay below 2^31): the
-// stripe layout's division is done once.
-struct KeyLimit {
-  int p, d, m;  // position; p / D and p % D (stripe)
-};
-__device__ __forceinline__ KeyLimit key_limit_of(const Plan& P, int p) {
-  KeyLimit k = {p, 0, 0};
-  if (P.layout == kStripe && p >= 0) {
-    k.d = p / P.D;
-    k.m = p - k.d * P.D;
-  }
-  return k;
-}
-__device__ __forceinline__ int limit_in(const Plan& P, int L, int j, const KeyLimit& k) {
-  if (k.p < 0) return -1;
-  int b;
-  if (P.layout == kStripe) {
-    b = k.d - (j > k.m ? 1 : 0);
-  } else if (P.layout == kBasic) {
-    b = k.p - j * L;
-  } else {
-    const int c = L >> 1, second = (2 * P.D - 1 - j) * c;
-    b = k.p >= second ? c + k.p - second : min(k.p - j * c, c - 1);
-  }
-  return max(-1, min(b, L - 1));
-}
 
 }  // namespace ra
