@@ -152,7 +152,7 @@ __device__ __forceinline__ int dq_window_publish(DqBars& sh, WinSlot* slots, con
   if (w < P.n_items) {
     const DqItem it = decode_dq(P, w);
     const int a0 = it.qt * kQTileRows;
-    fill_slot(slots[slot], P, it.seq, it.h, it.r, a0, min(P.seq[it.seq].L, a0 + kQTileRows) - 1);
+    fill_slot<false>(slots[slot], nullptr, P, it.seq, it.h, it.r, a0, min(P.seq[it.seq].L, a0 + kQTileRows) - 1);
   }
   if (lane == 0) {
     slots[slot].item = w;

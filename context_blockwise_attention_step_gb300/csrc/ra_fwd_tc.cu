@@ -84,6 +84,8 @@ struct FwdShared {
 template <bool WIN>
 struct FwdSlots {
   WinSlot slot[2];
+  WinSeg half[2][2][kMaxWindowShards];  // [slot][query tile]: the tiles each query tile sees
+  uint8_t flags[8];  // of the K/V tiles in flight: bit t: query tile t sees it; bit 2 + t: as its last
 };
 template <>
 struct FwdSlots<false> {};
@@ -156,7 +158,7 @@ __device__ __forceinline__ int fwd_item_take(FwdShared& sh, int k, volatile int*
 
 // The windowed kernel's item queue: the producer warp takes the next item and fills in its slot;
 // the other roles read it in place and release it when they have done with the item.
-__device__ __forceinline__ int fwd_window_publish(FwdShared& sh, WinSlot* slots, const Plan& P, int k, int lane,
+__device__ __forceinline__ int fwd_window_publish(FwdShared& sh, FwdSlots<true>& win, const Plan& P, int k, int lane,
                                                   volatile int* abort_flag, uint64_t tmo,
                                                   unsigned int* status) {
   const int slot = k & 1;
@@ -170,10 +172,10 @@ __device__ __forceinline__ int fwd_window_publish(FwdShared& sh, WinSlot* slots,
   if (w < P.n_items) {
     const FwdItem it = decode_fwd(P, w);
     const int a0 = it.blk * kFwdBlockRows;
-    fill_slot(slots[slot], P, it.seq, it.h, it.r, a0, min(P.seq[it.seq].L, a0 + kFwdBlockRows) - 1);
+    fill_slot<true>(win.slot[slot], win.half[slot][0], P, it.seq, it.h, it.r, a0, min(P.seq[it.seq].L, a0 + kFwdBlockRows) - 1);
   }
   if (lane == 0) {
-    slots[slot].item = w;
+    win.slot[slot].item = w;
     mbar_arrive(&sh.item_full[slot]);
   }
   return w;
@@ -246,7 +248,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, tmo, status));
       };
       for (int kq = 0;; ++kq) {
-        const int w = fwd_window_publish(sh, win.slot, P, kq, lane, abort_flag, tmo, status);
+        const int w = fwd_window_publish(sh, win, P, kq, lane, abort_flag, tmo, status);
         if (w < 0 || w >= P.n_items) break;
         const WinSlot& item = win.slot[kq & 1];
         const bool two = item.a1 - item.a0 >= kQTileRows;
@@ -261,16 +263,24 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         }
         const int hk = item.h / P.group, nseg = item.nseg;
         const int row0 = item.row - item.a0 - item.r * P.shard_stride;  // of shard 0
+        int left[2] = {0, 0};  // K/V tiles that the query tiles have yet to see
+        for (int g = 0; g < nseg; ++g)
+          for (int t = 0; t < 2; ++t) left[t] += tile_count(tiles_of(win.half[kq & 1][t][g]));
         bool ok = true;
         for (int g = 0; g < nseg && ok; ++g) {
           const TileSet set = tiles_of(item.seg[g]);
+          const TileSet half[2] = {tiles_of(win.half[kq & 1][0][g]), tiles_of(win.half[kq & 1][1][g])};
           const int krow = row0 + item.seg[g].j * P.shard_stride, nb = tile_count(set);
           for (int i = 0; i < nb; ++i, ++kv_count) {
-            const int row = krow + tile_at(set, i) * kKvTileRows;
+            const int b = tile_at(set, i), row = krow + b * kKvTileRows;
+            unsigned flags = 0;
+            for (int t = 0; t < 2; ++t)
+              if (has_tile(half[t], b)) flags |= (--left[t] == 0 ? 5u : 1u) << t;
             const int st = kv_count % C::kStages;
             const uint32_t ph = (kv_count / C::kStages) & 1;
             if (!(ok = wait(&sh.k_empty[st], ph ^ 1))) break;
             if (lane == 0) {
+              win.flags[kv_count & 7] = static_cast<uint8_t>(flags);  // read after k_full
               mbar_expect_tx(&sh.k_full[st], C::kTileBytes);
               for (int d = 0; d < C::kSub; ++d)
                 tma_load_3d(smem + C::kOffK + st * C::kTileBytes + d * kSubBytes, &tmK,
@@ -368,6 +378,57 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         if (!(ok = mbar_wait(&sh.q_full, q_phase, abort_flag, tmo, status))) break;
         q_phase ^= 1;
         tc_fence_after();
+        if constexpr (WIN) {
+          // Tile n of the walk goes to the query tiles that see it: O_t(n-1), S_t(n) for t = 0, 1.
+          unsigned prev = 0;
+          bool first[2] = {true, true};
+          for (int n = 0; n <= N && ok; ++n) {
+            unsigned cur = 0;
+            const int c = kv_count + n, st = c % C::kStages, pst = (c + C::kStages - 1) % C::kStages;
+            for (int t = 0; t < 2 && ok; ++t) {
+              if ((prev >> t) & 1u) {
+                if (t == 0 || !(prev & 1u))
+                  if (!(ok = mbar_wait(&sh.v_full[pst], ((c - 1) / C::kStages) & 1, abort_flag, tmo, status))) break;
+                if (!(ok = mbar_wait(&sh.p_full[t], p_phase[t], abort_flag, tmo, status))) break;
+                p_phase[t] ^= 1;
+                if (first[t]) {
+                  if (!(ok = mbar_wait(&sh.o_free[t], of_phase[t] ^ 1, abort_flag, tmo, status))) break;
+                  of_phase[t] ^= 1;
+                }
+                tc_fence_after();
+                const uint32_t va = sV + pst * C::kTileBytes;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                  mma_ts(tmem + C::col_o(t), tmem + C::col_s(t) + 32 + 8 * k,
+                         sdesc_sw128(va + k * 2048, kSubBytes, 1024), idO, (!first[t] || k > 0) ? 1u : 0u);
+                first[t] = false;
+                if ((prev >> (2 + t)) & 1u) tc_commit(&sh.o_done[t]);
+                if (t == 1 || !(prev & 2u)) tc_commit(&sh.v_empty[pst]);
+              }
+              if (n == N) continue;
+              if (t == 0) {
+                if (!(ok = mbar_wait(&sh.k_full[st], (c / C::kStages) & 1, abort_flag, tmo, status))) break;
+                tc_fence_after();
+                cur = *reinterpret_cast<volatile uint8_t*>(&win.flags[c & 7]);
+              }
+              if ((cur >> t) & 1u) {
+                const uint32_t qa = sQ + t * C::kTileBytes, ka = sK + st * C::kTileBytes;
+#pragma unroll
+                for (int k = 0; k < C::kKSteps; ++k) {
+                  const uint32_t off = (k >> 2) * kSubBytes + (k & 3) * 32;
+                  mma_ss(tmem + C::col_s(t), sdesc_sw128(qa + off, 16, 1024),
+                         sdesc_sw128(ka + off, 16, 1024), idS, k > 0);
+                }
+                tc_commit(&sh.s_full[t]);
+                if (t == 1 || !(cur & 2u)) tc_commit(&sh.k_empty[st]);
+              }
+            }
+            prev = cur;
+          }
+          tc_commit(&sh.q_empty);
+          kv_count += N;
+          continue;
+        }
         auto issue_S = [&](int t, int n) -> bool {
           const int c = kv_count + n;
           const int st = c % C::kStages;
@@ -502,7 +563,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       for (int s = WIN ? 0 : P.step_begin; s < s_end && ok; ++s) {
         const int j = WIN ? item->seg[s].j : shard_at_step(P.D, it.r, s);
         TileSet set;
-        if constexpr (WIN) set = tiles_of(item->seg[s]);
+        if constexpr (WIN) set = tiles_of(win.half[kq & 1][t][s]);
         const int nb = WIN ? tile_count(set) : kv_tiles_for(P, wk.L, it.r, j, wk.a_last);
         int lim, lo = 0, sk = 0;
         if constexpr (WIN) {  // of the shard's keys up to lim this row sees those before sk, and from lo on

@@ -87,6 +87,13 @@ struct WinSeg {
   uint16_t sink;           // its tiles (TileSet)
   int s0, n0, s1, n1;
 };
+__device__ __forceinline__ TileSet tiles_of(const WinSeg& g) { return {g.sink, g.s0, g.n0, g.s1, g.n1}; }
+__device__ __forceinline__ WinSeg seg_of(int j, int sk, const TileSet& t) {
+  return {static_cast<uint8_t>(j), static_cast<uint8_t>(sk), static_cast<uint16_t>(t.sink), t.s0, t.n0, t.s1, t.n1};
+}
+__device__ __forceinline__ bool has_tile(const TileSet& t, int b) {
+  return (t.sink && b == 0) || (b >= t.s0 && b < t.s0 + t.n0) || (b >= t.s1 && b < t.s1 + t.n1);
+}
 struct WinSlot {
   int item;       // >= n_items: the end
   int tiles, nseg;
@@ -95,8 +102,11 @@ struct WinSlot {
   WinSeg seg[kMaxWindowShards];
 };
 
-// Fills in a slot for query rows a0 .. a1 of rank r (the whole warp).
-__device__ __forceinline__ void fill_slot(WinSlot& w, const Plan& P, int seq, int h, int r, int a0, int a1) {
+// Fills in a slot for query rows a0 .. a1 of rank r (the whole warp); with HALVES also the tiles
+// of the block's two query tiles, one after the other in half[2 * kMaxWindowShards].
+template <bool HALVES>
+__device__ __forceinline__ void fill_slot(WinSlot& w, WinSeg* half, const Plan& P, int seq, int h, int r, int a0,
+                                          int a1) {
   const SeqDesc& sd = P.seq[seq];
   const int lane = threadIdx.x & 31, L = sd.L;
   int nseg = 0, tiles = 0;
@@ -106,9 +116,16 @@ __device__ __forceinline__ void fill_slot(WinSlot& w, const Plan& P, int seq, in
     if (base + lane < P.D) t = window_kv_tiles(P, L, r, j, a0, a1);
     const int n = tile_count(t);
     const unsigned some = __ballot_sync(0xffffffffu, n > 0);
-    if (n > 0) w.seg[nseg + __popc(some & ((1u << lane) - 1u))] =
-          {static_cast<uint8_t>(j), static_cast<uint8_t>(sink_rows(P, L, j)), static_cast<uint16_t>(t.sink),
-           t.s0, t.n0, t.s1, t.n1};
+    if (n > 0) {
+      const int at = nseg + __popc(some & ((1u << lane) - 1u)), sk = sink_rows(P, L, j);
+      w.seg[at] = seg_of(j, sk, t);
+      if constexpr (HALVES) {  // and of the block's two query tiles
+        const int mid = min(a1 + 1, a0 + kQTileRows);
+        half[at] = seg_of(j, sk, window_kv_tiles(P, L, r, j, a0, mid - 1));
+        half[kMaxWindowShards + at] =
+            seg_of(j, sk, mid <= a1 ? window_kv_tiles(P, L, r, j, mid, a1) : TileSet{0, 0, 0, 0, 0});
+      }
+    }
     nseg += __popc(some);
     tiles += n;
   }
@@ -127,6 +144,5 @@ __device__ __forceinline__ void fill_slot(WinSlot& w, const Plan& P, int seq, in
   }
   __syncwarp();
 }
-__device__ __forceinline__ TileSet tiles_of(const WinSeg& g) { return {g.sink, g.s0, g.n0, g.s1, g.n1}; }
 
 }  // namespace ra
