@@ -243,15 +243,16 @@ Plan* make_window_plan(const ra_problem* p, int which, int window, int sinks) {
   Plan* P = make_plan(p, which, 0, p->D, -1, which == 0 && p->dtype == RA_F32);
   P->window = effective_window(p, window);
   P->sinks = P->window ? sinks : 0;
-  // A sink item as long as a K/V tile's window item: the tiles of the window, 8 at least, since
-  // an item's loads and stores cost about one query tile.
-  P->sink_chunk = std::max(8, P->window / ra::kQTileRows + 1);
+  // Tensor cores: a sink item as long as a K/V tile's window item, the tiles of the window, 8 at
+  // least, since an item's loads and stores cost about one query tile. CUDA cores: a warp for
+  // every 128 queries.
+  P->sink_chunk = use_tc(p) ? std::max(8, P->window / ra::kQTileRows + 1) : 1;
   return P;
 }
 
 // Backward workspace: delta, item counters, and the slots of the sink rows.
 size_t sink_bytes(const ra_problem* p, int window, int sinks) {
-  if (!use_tc(p) || sinks == 0) return 0;
+  if (sinks == 0) return 0;
   PlanHolder P(make_window_plan(p, 2, window, sinks));
   if (P.p->window == 0) return 0;
   return align256(static_cast<size_t>(ra::window_bwd_items(*P.p)) * 2 * sinks * p->head_dim * sizeof(float));
@@ -479,7 +480,7 @@ int ra_window_attn_fwd(const ra_problem* p, int window, int sinks, const void* q
   }
   const cudaError_t e = profiled(st, [&] {
     return use_tc(p) ? ra::launch_fwd_tc(*P.p, q, k, v, out, lse, st)
-                     : ra::launch_fwd_simt(*P.p, p->dtype, q, k, v, out, lse, st);
+                     : ra::launch_window_fwd_simt(*P.p, p->dtype, q, k, v, out, lse, st);
   });
   return e == cudaSuccess ? ok() : cuda_fail(e, "window forward launch");
 }
@@ -502,15 +503,14 @@ int ra_window_attn_bwd(const ra_problem* p, int window, int sinks, const void* q
   PlanHolder E(make_window_plan(p, 2, window, sinks));
   cudaError_t e = ra::launch_bwd_delta(*E.p, p->dtype, out, dout, delta, st);
   if (e != cudaSuccess) return cuda_fail(e, "backward preprocess launch");
+  char* at = static_cast<char*>(workspace) + delta_bytes(p);
+  PlanHolder P(make_window_plan(p, 1, window, sinks));
+  P.p->sink_sums = reinterpret_cast<float*>(at + sched_bytes(p));
+  ra::window_bwd_items(*P.p);
   if (use_tc(p)) {
-    char* at = static_cast<char*>(workspace) + delta_bytes(p);
-    int32_t* counter = reinterpret_cast<int32_t*>(at);  // of the K/V pass, then of the dq pass
-    e = cudaMemsetAsync(counter, 0, 2 * sizeof(int32_t), st);
+    P.p->work_counter = reinterpret_cast<int32_t*>(at);  // of the K/V pass, then of the dq pass
+    e = cudaMemsetAsync(at, 0, 2 * sizeof(int32_t), st);
     if (e != cudaSuccess) return cuda_fail(e, "item counter clear");
-    PlanHolder P(make_window_plan(p, 1, window, sinks));
-    P.p->work_counter = counter;
-    P.p->sink_sums = reinterpret_cast<float*>(at + sched_bytes(p));
-    ra::window_bwd_items(*P.p);
     e = profiled(st, [&] {
       cudaError_t r = ra::launch_window_bwd_tc(*P.p, q, k, v, dout, lse, delta, dk, dv, st);
       if (r != cudaSuccess) return r;
@@ -518,7 +518,7 @@ int ra_window_attn_bwd(const ra_problem* p, int window, int sinks, const void* q
       return ra::launch_bwd_dq_tc(*P.p, q, k, v, dout, lse, delta, dq, st);
     });
   } else {
-    e = profiled(st, [&] { return ra::launch_bwd_simt(*E.p, p->dtype, q, k, v, dout, lse, delta, dq, dk, dv, st); });
+    e = profiled(st, [&] { return ra::launch_window_bwd_simt(*P.p, p->dtype, q, k, v, dout, lse, delta, dq, dk, dv, st); });
   }
   return e == cudaSuccess ? ok() : cuda_fail(e, "window backward launch");
 }

@@ -39,7 +39,7 @@
 // tile, a few query tiles of one rank): a sink is seen by every later query, and one item for
 // it would outlast all the others (4096 query tiles against 36 at 131072 tokens, window 1024,
 // 4 heads a group). Sink rows get their sum from several items, so each of these writes float32
-// sums of the sink rows to a slot of its own (ra_plan.h), and sink_sum_kernel adds the slots in
+// sums of the sink rows to a slot of its own (ra_plan.h), and launch_sink_sum adds the slots in
 // order, so that the result does not depend on the order of the items.
 //
 // Warp roles (512 threads; 384 without dQ): warp 0 TMA producer (K, V once per item; Q and
@@ -1054,24 +1054,6 @@ __global__ void __launch_bounds__(bwd_threads<kWithDQ>(), 1)
   }
 }
 
-// dk and dv of the sink rows: the sum of their slots. Block x: a sink row; y: sink shard and K/V
-// head; z: sequence. Threads: dk's head_dim elements, then dv's.
-template <int DH>
-__global__ void __launch_bounds__(2 * DH)
-    sink_sum_kernel(const __grid_constant__ Plan P, __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv) {
-  const SeqDesc& s = P.seq[blockIdx.z];
-  const int j = blockIdx.y / P.hkv, hk = blockIdx.y % P.hkv, row = blockIdx.x;
-  if (j >= sink_shards(P, s.L) || row >= sink_rows(P, s.L, j)) return;
-  const int which = threadIdx.x / DH, d = threadIdx.x % DH, n = sink_slots(P, s.L);
-  const int64_t slot = sink_slot(P, s, j, hk, 0);
-  const float* src = P.sink_sums + ((slot * 2 + which) * P.sinks + row) * DH + d;
-  float sum = 0.f;
-#pragma unroll 8
-  for (int i = 0; i < n; ++i) sum += src[static_cast<int64_t>(i) * 2 * P.sinks * DH];
-  const size_t at = (static_cast<size_t>(s.row_off + j * P.shard_stride + row) * P.hkv + hk) * DH + d;
-  (which ? dv : dk)[at] = __float2bfloat16_rn(sum);
-}
-
 template <int DH, bool kWithDQ, bool kAccum, bool WIN = false>
 cudaError_t launch_one(const Plan& P, const CUtensorMap& mq, const CUtensorMap& mk,
                        const CUtensorMap& mv, const CUtensorMap& mdo, const float* lse,
@@ -1128,14 +1110,7 @@ cudaError_t launch_window_bwd_tc(const Plan& P, const void* q, const void* k, co
   e = P.head_dim == 128
           ? launch_one<128, false, false, true>(P, mq, mk, mv, mdo, lse, delta, nullptr, dk, dv, n_sm, st)
           : launch_one<64, false, false, true>(P, mq, mk, mv, mdo, lse, delta, nullptr, dk, dv, n_sm, st);
-  if (e != cudaSuccess || P.sinks == 0) return e;
-  int shards = 0;
-  for (int i = 0; i < P.n_seqs; ++i) shards = max(shards, sink_shards(P, P.seq[i].L));
-  const dim3 grid(P.sinks, shards * P.hkv, P.n_seqs);
-  __nv_bfloat16 *ok = static_cast<__nv_bfloat16*>(dk), *ov = static_cast<__nv_bfloat16*>(dv);
-  if (P.head_dim == 128) sink_sum_kernel<128><<<grid, 256, 0, st>>>(P, ok, ov);
-  else sink_sum_kernel<64><<<grid, 128, 0, st>>>(P, ok, ov);
-  return cudaGetLastError();
+  return e == cudaSuccess ? launch_sink_sum(P, RA_BF16, dk, dv, st) : e;
 }
 
 cudaError_t launch_bwd_tc(const Plan& P, BwdKind kind, const void* q, const void* k, const void* v,

@@ -37,6 +37,13 @@ int window_bwd_items(Plan& P);
 cudaError_t launch_window_bwd_tc(const Plan& P, const void* q, const void* k, const void* v,
                                  const void* dout, const float* lse, const float* delta, void* dk,
                                  void* dv, cudaStream_t st);
+// The same on the CUDA cores (float32; bf16 for cross-checks), dq too; and the sum of the slots.
+cudaError_t launch_window_fwd_simt(const Plan& P, int dtype, const void* q, const void* k, const void* v,
+                                   void* out, float* lse, cudaStream_t st);
+cudaError_t launch_window_bwd_simt(const Plan& P, int dtype, const void* q, const void* k, const void* v,
+                                   const void* dout, const float* lse, const float* delta, void* dq,
+                                   void* dk, void* dv, cudaStream_t st);
+cudaError_t launch_sink_sum(const Plan& P, int dtype, void* dk, void* dv, cudaStream_t st);
 cudaError_t bwd_dq_status(unsigned int* value, bool reset);
 cudaError_t launch_wait_timeout(uint64_t timeout_ns, cudaStream_t st);
 cudaError_t launch_exp2_poly(const float* x, float* y, int n, cudaStream_t st);

@@ -62,8 +62,7 @@ __device__ __forceinline__ float dot_row(const float (&x)[kMaxPerLane], const T*
 }
 
 // -------------------------------------------------------------------------------- forward
-// WIN: sliding window with sinks; keys between the sinks and the window are stepped over.
-template <typename T, typename OutT, bool WIN>
+template <typename T, typename OutT>
 __global__ void __launch_bounds__(32 * kWarpsPerBlock)
     fwd_simt_kernel(const __grid_constant__ Plan P, const T* __restrict__ q,
                     const T* __restrict__ k, const T* __restrict__ v, OutT* __restrict__ out,
@@ -88,13 +87,7 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock)
     for (int s = P.step_begin; s < P.step_end; ++s) {
       const int j = shard_at_step(P.D, r, s);
       const int lim = P.causal ? key_limit(P.layout, P.D, L, j, pq) : L - 1;
-      const int sk = WIN ? sink_rows(P, L, j) : 0;
-      const int lo = WIN ? first_query(P.layout, P.D, L, j, pq - P.window + 1) : 0;
       for (int b = 0; b <= lim; ++b) {
-        if (WIN && b >= sk && b < lo) {
-          b = lo;
-          if (b > lim) break;
-        }
         const size_t krow = static_cast<size_t>(sd.row_off + j * P.shard_stride + b);
         const float x = dot_row(qr, k + (krow * P.hkv + hk) * dh, dh, lane) * P.scale;
         const float m_new = fmaxf(m, x);
@@ -126,7 +119,7 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock)
 // -------------------------------------------------------------------------------- backward
 // Block mode (the unfused path's per-step backward): only the steps [step_begin, step_end)
 // and, if set, the rank rank_only; OutT = float with kAccum adds into the outputs.
-template <typename T, typename OutT, bool kAccum, bool WIN>
+template <typename T, typename OutT, bool kAccum>
 __global__ void __launch_bounds__(32 * kWarpsPerBlock)
     bwd_dq_simt_kernel(const __grid_constant__ Plan P, const T* __restrict__ q,
                        const T* __restrict__ k, const T* __restrict__ v,
@@ -153,13 +146,7 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock)
     for (int s = P.step_begin; s < P.step_end; ++s) {
       const int j = shard_at_step(P.D, r, s);
       const int lim = P.causal ? key_limit(P.layout, P.D, L, j, pq) : L - 1;
-      const int sk = WIN ? sink_rows(P, L, j) : 0;
-      const int lo = WIN ? first_query(P.layout, P.D, L, j, pq - P.window + 1) : 0;
       for (int b = 0; b <= lim; ++b) {
-        if (WIN && b >= sk && b < lo) {
-          b = lo;
-          if (b > lim) break;
-        }
         const size_t krow = static_cast<size_t>(sd.row_off + j * P.shard_stride + b);
         const T* kr = k + (krow * P.hkv + hk) * dh;
         const float p = expf(dot_row(qr, kr, dh, lane) * P.scale - lse_a);
@@ -184,7 +171,7 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock)
   }
 }
 
-template <typename T, typename OutT, bool kAccum, bool WIN>
+template <typename T, typename OutT, bool kAccum>
 __global__ void __launch_bounds__(32 * kWarpsPerBlock)
     bwd_dkv_simt_kernel(const __grid_constant__ Plan P, const T* __restrict__ q,
                         const T* __restrict__ k, const T* __restrict__ v,
@@ -211,8 +198,7 @@ __global__ void __launch_bounds__(32 * kWarpsPerBlock)
         const int r = rank_at_step(P.D, j, s);
         if (P.rank_only >= 0 && r != P.rank_only) continue;
         const int a_begin = P.causal ? first_query(P.layout, P.D, L, r, pk) : 0;
-        const int a_end = WIN && pk >= P.sinks ? key_limit(P.layout, P.D, L, r, pk + P.window - 1) + 1 : L;
-        for (int a = a_begin; a < a_end; ++a) {
+        for (int a = a_begin; a < L; ++a) {
           const size_t qrow = static_cast<size_t>(sd.row_off + r * P.shard_stride + a);
           const size_t li = sd.lse_off + static_cast<size_t>(h) * P.lse_hstride + static_cast<size_t>(r) * P.shard_stride + a;
           const T* qa = q + (qrow * P.hq + h) * dh;
@@ -262,66 +248,58 @@ long max_len(const Plan& P) {
 
 }  // namespace
 
-namespace {
-
-template <bool WIN>
-cudaError_t fwd_simt(const Plan& P, int dtype, const void* q, const void* k, const void* v, void* out,
-                     float* lse, cudaStream_t st) {
+cudaError_t launch_fwd_simt(const Plan& P, int dtype, const void* q, const void* k, const void* v,
+                            void* out, float* lse, cudaStream_t st) {
   const dim3 grid = seq_grid(P, plan_ranks(P) * max_len(P) * P.hq);
   const dim3 block(32 * kWarpsPerBlock);
   if (dtype == RA_F32) {
-    fwd_simt_kernel<float, float, WIN><<<grid, block, 0, st>>>(
+    fwd_simt_kernel<float, float><<<grid, block, 0, st>>>(
         P, static_cast<const float*>(q), static_cast<const float*>(k), static_cast<const float*>(v),
         static_cast<float*>(out), lse);
   } else if (P.out_f32) {
-    if constexpr (!WIN)  // block outputs: no window there
-      fwd_simt_kernel<__nv_bfloat16, float, false><<<grid, block, 0, st>>>(
-          P, static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
-          static_cast<const __nv_bfloat16*>(v), static_cast<float*>(out), lse);
+    fwd_simt_kernel<__nv_bfloat16, float><<<grid, block, 0, st>>>(
+        P, static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
+        static_cast<const __nv_bfloat16*>(v), static_cast<float*>(out), lse);
   } else {
-    fwd_simt_kernel<__nv_bfloat16, __nv_bfloat16, WIN><<<grid, block, 0, st>>>(
+    fwd_simt_kernel<__nv_bfloat16, __nv_bfloat16><<<grid, block, 0, st>>>(
         P, static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
         static_cast<const __nv_bfloat16*>(v), static_cast<__nv_bfloat16*>(out), lse);
   }
   return cudaGetLastError();
 }
 
-template <typename T, typename OutT, bool kAccum, bool WIN>
-void bwd_simt(const Plan& P, const void* q, const void* k, const void* v, const void* dout, const float* lse,
-              const float* delta, void* dq, void* dk, void* dv, cudaStream_t st) {
-  const dim3 gq = seq_grid(P, plan_ranks(P) * max_len(P) * P.hq);
-  const dim3 gk = seq_grid(P, plan_kv_shards(P) * max_len(P) * P.hkv);
-  const dim3 block(32 * kWarpsPerBlock);
-  bwd_dq_simt_kernel<T, OutT, kAccum, WIN><<<gq, block, 0, st>>>(
-      P, static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v),
-      static_cast<const T*>(dout), lse, delta, static_cast<OutT*>(dq));
-  bwd_dkv_simt_kernel<T, OutT, kAccum, WIN><<<gk, block, 0, st>>>(
-      P, static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v),
-      static_cast<const T*>(dout), lse, delta, static_cast<OutT*>(dk), static_cast<OutT*>(dv));
-}
-
-}  // namespace
-
-cudaError_t launch_fwd_simt(const Plan& P, int dtype, const void* q, const void* k, const void* v,
-                            void* out, float* lse, cudaStream_t st) {
-  return P.window > 0 ? fwd_simt<true>(P, dtype, q, k, v, out, lse, st)
-                      : fwd_simt<false>(P, dtype, q, k, v, out, lse, st);
-}
-
 cudaError_t launch_bwd_simt(const Plan& P, int dtype, const void* q, const void* k,
                             const void* v, const void* dout, const float* lse,
                             const float* delta, void* dq, void* dk, void* dv, cudaStream_t st) {
-  using B = __nv_bfloat16;
-  if (P.window > 0) {
-    if (dtype == RA_F32) bwd_simt<float, float, false, true>(P, q, k, v, dout, lse, delta, dq, dk, dv, st);
-    else bwd_simt<B, B, false, true>(P, q, k, v, dout, lse, delta, dq, dk, dv, st);
-  } else if (P.bwd_accum) {
-    if (dtype == RA_F32) bwd_simt<float, float, true, false>(P, q, k, v, dout, lse, delta, dq, dk, dv, st);
-    else bwd_simt<B, float, true, false>(P, q, k, v, dout, lse, delta, dq, dk, dv, st);
+  const dim3 gq = seq_grid(P, plan_ranks(P) * max_len(P) * P.hq);
+  const dim3 gk = seq_grid(P, plan_kv_shards(P) * max_len(P) * P.hkv);
+  const dim3 block(32 * kWarpsPerBlock);
+  if (P.bwd_accum) {
+    if (dtype == RA_F32) {
+      using T = float;
+      bwd_dq_simt_kernel<T, float, true><<<gq, block, 0, st>>>(
+          P, (const T*)q, (const T*)k, (const T*)v, (const T*)dout, lse, delta, (float*)dq);
+      bwd_dkv_simt_kernel<T, float, true><<<gk, block, 0, st>>>(
+          P, (const T*)q, (const T*)k, (const T*)v, (const T*)dout, lse, delta, (float*)dk, (float*)dv);
+    } else {
+      using T = __nv_bfloat16;
+      bwd_dq_simt_kernel<T, float, true><<<gq, block, 0, st>>>(
+          P, (const T*)q, (const T*)k, (const T*)v, (const T*)dout, lse, delta, (float*)dq);
+      bwd_dkv_simt_kernel<T, float, true><<<gk, block, 0, st>>>(
+          P, (const T*)q, (const T*)k, (const T*)v, (const T*)dout, lse, delta, (float*)dk, (float*)dv);
+    }
   } else if (dtype == RA_F32) {
-    bwd_simt<float, float, false, false>(P, q, k, v, dout, lse, delta, dq, dk, dv, st);
+    using T = float;
+    bwd_dq_simt_kernel<T, T, false><<<gq, block, 0, st>>>(P, (const T*)q, (const T*)k, (const T*)v,
+                                                           (const T*)dout, lse, delta, (T*)dq);
+    bwd_dkv_simt_kernel<T, T, false><<<gk, block, 0, st>>>(P, (const T*)q, (const T*)k, (const T*)v,
+                                                            (const T*)dout, lse, delta, (T*)dk, (T*)dv);
   } else {
-    bwd_simt<B, B, false, false>(P, q, k, v, dout, lse, delta, dq, dk, dv, st);
+    using T = __nv_bfloat16;
+    bwd_dq_simt_kernel<T, T, false><<<gq, block, 0, st>>>(P, (const T*)q, (const T*)k, (const T*)v,
+                                                           (const T*)dout, lse, delta, (T*)dq);
+    bwd_dkv_simt_kernel<T, T, false><<<gk, block, 0, st>>>(P, (const T*)q, (const T*)k, (const T*)v,
+                                                            (const T*)dout, lse, delta, (T*)dk, (T*)dv);
   }
   return cudaGetLastError();
 }

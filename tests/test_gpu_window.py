@@ -157,6 +157,20 @@ def test_window_repeats_bit_for_bit_and_in_graphs(case):
     assert torch.equal(o5, out) and torch.equal(l5, lse) and all(torch.equal(a, b) for a, b in zip(grads, g5))
 
 
+@pytest.mark.parametrize("case", [CASES[4], CASES[11]], ids=["zigzag", "varlen_stripe"])
+def test_window_on_the_cuda_cores_in_bf16(case, monkeypatch):
+    """The cross-check path (RA_IMPL=simt): no rounding of the weights or of dS there, so it agrees
+    with the tensor cores to theirs."""
+    window, sinks = case[-2:]
+    x, prob = make(case, seed=70)
+    out, lse, grads = run(x, prob, window, sinks)
+    monkeypatch.setenv("RA_IMPL", "simt")
+    o, l, g = run(x, prob, window, sinks)
+    assert (lse - l).abs().max() <= 2.0 ** -11
+    for a, b, name in zip((out, *grads), (o, *g), ("out", "dq", "dk", "dv")):
+        check_l2(f64(a), f64(b), BF16, name)
+
+
 def test_a_window_over_everything_is_the_ring():
     x, prob = make(CASES[9], seed=60)
     q, k, v, do = (ra.shard_tokens(t, prob) for t in x)
