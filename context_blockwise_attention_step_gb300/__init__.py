@@ -18,4 +18,4 @@ from .heads import (  # noqa: F401
     paged_workspace_bytes, qk_norm_rope_bwd, qk_norm_rope_fwd, window_attn_bwd, window_attn_fwd,
     window_workspace_bytes,
 )
-from .autograd import RingSelfAttention, ring_attention, shard, unshard  # noqa: F401,E402
+from .autograd import RingSelfAttention, qk_norm_rope, ring_attention, shard, unshard  # noqa: F401,E402

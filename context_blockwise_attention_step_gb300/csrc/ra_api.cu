@@ -12,6 +12,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <new>
 #include <numeric>
 #include <string>
 #include <vector>
@@ -116,6 +117,7 @@ int validate(const ra_problem* p) {
 Plan* make_plan(const ra_problem* p, int which, int step_begin, int step_end, int rank_only,
                 int out_f32, std::vector<int>* natural_index = nullptr, int kv_shard_only = -1) {
   Plan* P = static_cast<Plan*>(calloc(1, sizeof(Plan)));
+  if (P == nullptr) throw std::bad_alloc();
   P->layout = p->layout;
   P->causal = p->causal ? 1 : 0;
   P->D = p->D;
@@ -455,16 +457,18 @@ int ra_block_attn_bwd(const ra_problem* p, int rank, int step, const void* q, co
   return e == cudaSuccess ? ok() : cuda_fail(e, "block backward launch");
 }
 
-size_t ra_window_workspace_bytes(const ra_problem* p, int window, int sinks, int which) {
+size_t ra_window_workspace_bytes(const ra_problem* p, int window, int sinks, int which) try {
   if (validate_window(p, window, sinks) != RA_OK) return 0;
   if (which == 0) return sched_bytes(p);
   if (which == 1) return delta_bytes(p) + sched_bytes(p) + sink_bytes(p, window, sinks);
+  return 0;
+} catch (const std::bad_alloc&) {
   return 0;
 }
 
 int ra_window_attn_fwd(const ra_problem* p, int window, int sinks, const void* q, const void* k,
                        const void* v, void* out, float* lse, void* workspace, size_t workspace_bytes,
-                       void* stream) {
+                       void* stream) try {
   if (int e = validate_window(p, window, sinks)) return e;
   if (effective_window(p, window) == 0)
     return ra_ring_attn_fwd(p, q, k, v, out, lse, workspace, workspace_bytes, stream);
@@ -483,11 +487,13 @@ int ra_window_attn_fwd(const ra_problem* p, int window, int sinks, const void* q
                      : ra::launch_window_fwd_simt(*P.p, p->dtype, q, k, v, out, lse, st);
   });
   return e == cudaSuccess ? ok() : cuda_fail(e, "window forward launch");
+} catch (const std::bad_alloc&) {
+  return fail(RA_ERR_CUDA, "out of host memory");
 }
 
 int ra_window_attn_bwd(const ra_problem* p, int window, int sinks, const void* q, const void* k,
                        const void* v, const void* out, const float* lse, const void* dout, void* dq,
-                       void* dk, void* dv, void* workspace, size_t workspace_bytes, void* stream) {
+                       void* dk, void* dv, void* workspace, size_t workspace_bytes, void* stream) try {
   if (int e = validate_window(p, window, sinks)) return e;
   if (effective_window(p, window) == 0)
     return ra_ring_attn_bwd(p, q, k, v, out, lse, dout, dq, dk, dv, workspace, workspace_bytes, stream);
@@ -521,6 +527,8 @@ int ra_window_attn_bwd(const ra_problem* p, int window, int sinks, const void* q
     e = profiled(st, [&] { return ra::launch_window_bwd_simt(*P.p, p->dtype, q, k, v, dout, lse, delta, dq, dk, dv, st); });
   }
   return e == cudaSuccess ? ok() : cuda_fail(e, "window backward launch");
+} catch (const std::bad_alloc&) {
+  return fail(RA_ERR_CUDA, "out of host memory");
 }
 
 int ra_shard_tokens(const ra_problem* p, int direction, const void* src, void* dst,

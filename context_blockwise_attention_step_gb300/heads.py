@@ -23,9 +23,8 @@ class Rope:
 
     raw: RaRope
 
-    @property
-    def ptr(self):
-        return ctypes.byref(self.raw)
+    def __post_init__(self):
+        self.ptr = ctypes.byref(self.raw)
 
 
 def make_rope(rotary_dim: int, base: float = 10000.0, inv_freq=None, interleaved: bool = False) -> Rope:
@@ -90,8 +89,9 @@ def _weights(q_weight, k_weight, dtype, dh, dev):
         _plain(k_weight, "k_weight", dtype, (dh,), dev)
 
 
-def _like(t: torch.Tensor) -> torch.Tensor:
-    return torch.empty_like(t, memory_format=torch.contiguous_format)
+def _made_like(t: torch.Tensor, made: list) -> torch.Tensor:
+    made.append(new := torch.empty_like(t, memory_format=torch.contiguous_format))
+    return new
 
 
 def _workspace(workspace, need: int, like: torch.Tensor, made: list):
@@ -140,12 +140,8 @@ def qk_norm_rope_fwd(q, k, prob: Problem, q_weight=None, k_weight=None, rope: Ro
     ks = _rows(k, "k", prob.token_dtype, prob.rows, r.hkv, dh, dev)
     _weights(q_weight, k_weight, prob.token_dtype, dh, dev)
     made = []
-    if q_out is None:
-        made.append(q_out := _like(q))
-    if k_out is None:
-        made.append(k_out := _like(k))
-    _plain(q_out, "q_out", prob.token_dtype, q.shape, dev)
-    _plain(k_out, "k_out", prob.token_dtype, k.shape, dev)
+    q_out = _made_like(q, made) if q_out is None else _plain(q_out, "q_out", prob.token_dtype, q.shape, dev)
+    k_out = _made_like(k, made) if k_out is None else _plain(k_out, "k_out", prob.token_dtype, k.shape, dev)
     _launch(dev, stream, made, lambda s: lib().ra_qk_norm_rope_fwd(
         prob.ptr, _rope_ptr(rope), eps, _ptr(q), qs, _ptr(k), ks, _ptr(q_weight), _ptr(k_weight), _ptr(q_out),
         _ptr(k_out), s))
@@ -166,12 +162,8 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, prob: Problem, q_weight=None, k_weigh
     ks = _rows(k, "k", prob.token_dtype, prob.rows, r.hkv, dh, dev)
     _weights(q_weight, k_weight, prob.token_dtype, dh, dev)
     made = []
-    if dq is None:
-        made.append(dq := _like(q))
-    if dk is None:
-        made.append(dk := _like(k))
-    _plain(dq, "dq", prob.token_dtype, q.shape, dev)
-    _plain(dk, "dk", prob.token_dtype, k.shape, dev)
+    dq = _made_like(q, made) if dq is None else _plain(dq, "dq", prob.token_dtype, q.shape, dev)
+    dk = _made_like(k, made) if dk is None else _plain(dk, "dk", prob.token_dtype, k.shape, dev)
     dqw = dkw = None
     size = 0
     if q_weight is not None:
@@ -197,8 +189,7 @@ def window_attn_fwd(q, k, v, prob: Problem, window: int, sinks: int = 0, out=Non
     (``window_workspace_bytes(..., 0)``) is allocated when not given."""
     r, dev = prob.raw, q.get_device()
     made = []
-    if out is None:
-        made.append(out := _like(q))
+    out = _made_like(q, made) if out is None else out
     if lse is None:
         made.append(lse := torch.empty(ops._lse_shape(prob), device=q.device, dtype=torch.float32))
     nq, nk = prob.rows * r.hq * r.head_dim, prob.rows * r.hkv * r.head_dim
@@ -218,12 +209,9 @@ def window_attn_bwd(dout, q, k, v, out, lse, prob: Problem, window: int, sinks: 
     """Backward of ``window_attn_fwd`` -> (dq, dk, dv), shard-major, in the problem dtype."""
     r, dev = prob.raw, q.get_device()
     made = []
-    if dq is None:
-        made.append(dq := _like(q))
-    if dk is None:
-        made.append(dk := _like(k))
-    if dv is None:
-        made.append(dv := _like(v))
+    dq = _made_like(q, made) if dq is None else dq
+    dk = _made_like(k, made) if dk is None else dk
+    dv = _made_like(v, made) if dv is None else dv
     nq, nk = prob.rows * r.hq * r.head_dim, prob.rows * r.hkv * r.head_dim
     for t, n, name in ((dout, nq, "dout"), (q, nq, "q"), (k, nk, "k"), (v, nk, "v"), (out, nq, "out"),
                        (dq, nq, "dq"), (dk, nk, "dk"), (dv, nk, "dv")):
@@ -249,9 +237,11 @@ class PagedCache:
     v_pages: torch.Tensor
     block_table: torch.Tensor
 
-    @property
-    def ptr(self):
-        return ctypes.byref(self.raw)
+    def __post_init__(self):
+        r = self.raw
+        self.ptr = ctypes.byref(r)
+        self.dtype, self.device_index = self.k_pages.dtype, self.k_pages.get_device()
+        self.n_seqs, self.hkv, self.head_dim = r.n_seqs, r.hkv, r.head_dim
 
 
 def make_cache(k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor) -> PagedCache:
@@ -282,10 +272,6 @@ def make_cache(k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.
     return PagedCache(raw, k_pages, v_pages, block_table)
 
 
-def _lens(t: torch.Tensor, name: str, n: int, device):
-    return _plain(t, name, torch.int32, (n,), device)
-
-
 def kv_cache_append(q, k, v, cache: PagedCache, seq_lens, cu_new=None, q_weight=None, k_weight=None,
                     rope: Rope | None = None, eps: float = 1e-6, q_out=None, stream=None):
     """Put new tokens into the cache: norm and rotation of q and k as in ``qk_norm_rope_fwd``
@@ -294,22 +280,19 @@ def kv_cache_append(q, k, v, cache: PagedCache, seq_lens, cu_new=None, q_weight=
     [n_seqs, hq, head_dim], k, v is the new token of sequence b (of length 0: idle, its row of
     q_out is 0); with it (int32 [n_seqs + 1], on the device) rows cu_new[b]:cu_new[b+1] are the
     last tokens of sequence b, and rows behind the last are left as they are."""
-    r = cache.raw
-    dt, dh, dev = cache.k_pages.dtype, r.head_dim, cache.k_pages.get_device()
+    dt, dh, dev, hkv = cache.dtype, cache.head_dim, cache.device_index, cache.hkv
     n = k.shape[0] if k.dim() == 3 else k.shape[0] * k.shape[1]
-    ks = _rows(k, "k", dt, n, r.hkv, dh, dev)
-    vs = _rows(v, "v", dt, n, r.hkv, dh, dev)
+    ks = _rows(k, "k", dt, n, hkv, dh, dev)
+    vs = _rows(v, "v", dt, n, hkv, dh, dev)
     _weights(q_weight, k_weight, dt, dh, dev)
-    _lens(seq_lens, "seq_lens", r.n_seqs, dev)
+    _plain(seq_lens, "seq_lens", torch.int32, (cache.n_seqs,), dev)
     if cu_new is not None:
-        _lens(cu_new, "cu_new", r.n_seqs + 1, dev)
+        _plain(cu_new, "cu_new", torch.int32, (cache.n_seqs + 1,), dev)
     hq, qs, made = 0, 0, []
     if q is not None:
         hq = q.shape[-2]
         qs = _rows(q, "q", dt, n, hq, dh, dev)
-        if q_out is None:
-            made.append(q_out := _like(q))
-        _plain(q_out, "q_out", dt, q.shape, dev)
+        q_out = _made_like(q, made) if q_out is None else _plain(q_out, "q_out", dt, q.shape, dev)
     elif q_out is not None:
         raise ValueError("q_out without q")
     _launch(dev, stream, made, lambda s: lib().ra_kv_cache_append(
@@ -329,20 +312,19 @@ def paged_attn_decode(q, cache: PagedCache, seq_lens, window: int = 0, sinks: in
     last ``window`` and the first ``sinks`` of the seq_lens[b] keys are seen. A sequence of
     length 0 gets out = 0, lse = -inf. The workspace (``paged_workspace_bytes``) is allocated
     when not given."""
-    r = cache.raw
-    dt, dev = cache.k_pages.dtype, cache.k_pages.get_device()
+    dt, dev, n = cache.dtype, cache.device_index, cache.n_seqs
     if q.dim() != 3:
         raise ValueError("q must be [n_seqs, hq, head_dim]")
-    hq = q.shape[1]
-    _plain(q, "q", dt, (r.n_seqs, hq, r.head_dim), dev)
-    _lens(seq_lens, "seq_lens", r.n_seqs, dev)
+    shape = q.shape
+    hq = shape[1]
+    _plain(q, "q", dt, (n, hq, cache.head_dim), dev)
+    _plain(seq_lens, "seq_lens", torch.int32, (n,), dev)
     made = []
-    if out is None:
-        made.append(out := _like(q))
+    out = _made_like(q, made) if out is None else _plain(out, "out", dt, shape, dev)
     if lse is None:
-        made.append(lse := torch.empty((r.n_seqs, hq), device=q.device, dtype=torch.float32))
-    _plain(out, "out", dt, q.shape, dev)
-    _plain(lse, "lse", torch.float32, (r.n_seqs, hq), dev)
+        made.append(lse := torch.empty((n, hq), device=q.device, dtype=torch.float32))
+    else:
+        _plain(lse, "lse", torch.float32, (n, hq), dev)
     workspace, size = _workspace(workspace, workspace is None and paged_workspace_bytes(cache, hq), q, made)
     _launch(dev, stream, made, lambda s: lib().ra_paged_attn_decode(
         cache.ptr, hq, 0.0 if scale is None else scale, window, sinks, _ptr(q), _ptr(seq_lens), _ptr(out),
