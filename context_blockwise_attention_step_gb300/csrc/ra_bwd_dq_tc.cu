@@ -534,7 +534,8 @@ __global__ void __launch_bounds__(kDqThreads, 1)
                 if (WIN ? !((vis >> i) & 1u) : cs + i >= cnt) ev[i] = 0.f;
             }
 #pragma unroll
-            for (int i = 0; i < 16; ++i) pp[16 * ch + i] = pack_bf16x2(ev[2 * i], ev[2 * i + 1]);
+            for (int i = 0; i < 16; ++i)
+              pp[16 * ch + i] = WIN ? pack_f16x2(ev[2 * i], ev[2 * i + 1]) : pack_bf16x2(ev[2 * i], ev[2 * i + 1]);
           }
           if (!(ok = wait(&sh.dp_full, dp_phase))) break;
           dp_phase ^= 1;
@@ -552,7 +553,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
             for (int i = 0; i < 16; ++i)
               xv[i] = sub2(f2(__uint_as_float(dp[2 * i]), __uint_as_float(dp[2 * i + 1])), dl2);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) xv[i] = mul2(xv[i], f2_of_bf16x2(pp[16 * ch + i]));
+            for (int i = 0; i < 16; ++i) xv[i] = mul2(xv[i], WIN ? f2_of_f16x2(pp[16 * ch + i]) : f2_of_bf16x2(pp[16 * ch + i]));
 #pragma unroll
             for (int i = 0; i < 16; ++i) o[i] = bf16x2_of(xv[i]);
             // dS (bf16) into columns [32, 96) of this tile's S buffer (read into registers

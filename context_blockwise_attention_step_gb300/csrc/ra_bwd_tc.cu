@@ -290,7 +290,7 @@ __device__ __forceinline__ void transpose8_f4(uint32_t (&r)[32], int t) {
 // [K/V row][query], the A operand of the dK MMA (K-major) and of the dQ MMA (MN-major).
 // (Kept out of TMEM: MMAs that read an operand from TMEM slow down while the softmax
 // warps load and store TMEM.)
-template <int CH, bool kWithDQ>
+template <int CH, bool kWithDQ, bool WIN = false>
 __device__ __forceinline__ void ds_from(const uint32_t (&dp)[32], uint32_t tY, int c0, const float* dl,
                                         const uint32_t (&pp)[32], uint8_t* ds_row, int row) {
   const int cs = c0 + 32 * CH;
@@ -302,7 +302,8 @@ __device__ __forceinline__ void ds_from(const uint32_t (&dp)[32], uint32_t tY, i
     xv[i] = sub2(f2(__uint_as_float(dp[2 * i]), __uint_as_float(dp[2 * i + 1])), f2(d2.x, d2.y));
   }
 #pragma unroll
-  for (int i = 0; i < 16; ++i) xv[i] = mul2(xv[i], f2_of_bf16x2(pp[16 * CH + i]));
+  for (int i = 0; i < 16; ++i)
+    xv[i] = mul2(xv[i], WIN ? f2_of_f16x2(pp[16 * CH + i]) : f2_of_bf16x2(pp[16 * CH + i]));
 #pragma unroll
   for (int i = 0; i < 16; ++i) o[i] = bf16x2_of(xv[i]);
 #pragma unroll
@@ -362,7 +363,7 @@ __device__ __forceinline__ void p_from(const uint32_t (&sv)[32], uint32_t tX, in
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     pk[i] = pack_bf16x2(ev[2 * i], ev[2 * i + 1]);
-    pp[16 * CH + i] = pk[i];
+    pp[16 * CH + i] = WIN ? pack_f16x2(ev[2 * i], ev[2 * i + 1]) : pk[i];
   }
   tmem_st16(tX + 32 + c0 / 2 + 16 * CH, pk);
 }
@@ -956,8 +957,8 @@ __global__ void __launch_bounds__(bwd_threads<kWithDQ>(), 1)
           tmem_ld32_nowait(tY + c0, d0);
           tmem_ld32_nowait(tY + c0 + 32, d1);
           tmem_wait_ld();
-          ds_from<0, kWithDQ>(d0, tY, c0, dl, pp, ds_row, row);
-          ds_from<1, kWithDQ>(d1, tY, c0, dl, pp, ds_row, row);
+          ds_from<0, kWithDQ, WIN>(d0, tY, c0, dl, pp, ds_row, row);
+          ds_from<1, kWithDQ, WIN>(d1, tY, c0, dl, pp, ds_row, row);
         } else if (wg == 0) {
           ds_chunk<1, kWithDQ>(tY, c0, dl, pp, ds_row, row);
           ds_chunk<0, kWithDQ>(tY, c0, dl, pp, ds_row, row);

@@ -317,6 +317,21 @@ __device__ __forceinline__ uint64_t f2_of_bf16x2(uint32_t v) {
   return f2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
 }
 
+// The same for a pair of halves: numbers up to 1 to a relative 2^-11 (below 2^-14 to an absolute
+// 2^-25), where bf16 has 2^-9.
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_of_f16x2(uint32_t v) {
+  float lo, hi;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
+      : "=f"(lo), "=f"(hi)
+      : "r"(v));
+  return f2(lo, hi);
+}
+
 // Fire-and-forget vector reduction into global memory (four f32 adds, 16-byte aligned).
 __device__ __forceinline__ void red_add_v4(float* dst, float a, float b, float c, float d) {
   asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(dst), "f"(a), "f"(b), "f"(c),
