@@ -26,8 +26,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxPerLane = 4;  // head_dim <= 128
-
 // Rows of a ring problem, in natural order of the sequences (unlike the launch plans' table,
 // which is sorted by length).
 struct RingRows {
@@ -140,100 +138,172 @@ struct HeadArgs {
   int64_t kv_head;                       // elements between the heads of k_out and v_out
 };
 
-// The rotated (sign = 1) or back-rotated (sign = -1) element d of a head whose elements lie in
-// `row` (shared memory).
-__device__ __forceinline__ float rotated(const HeadArgs& A, const float* row, int d, int64_t pos,
-                                         float sign) {
+// ---------------------------------------------------------------- any head size and alignment
+// Lane l holds elements l, l + 32, ... of a head; a head's row goes through shared memory to reach
+// the lanes' rotation partners: y[d] = cs[d] x[d] + sn[d] x[other[d]]. A warp takes a token (or a
+// share of its heads), so that a token's position and angles are worked out once.
+constexpr int kPerLane = 4;  // head_dim <= 128
+struct LaneTurn {
+  float cs[kPerLane], sn[kPerLane];
+  int other[kPerLane];
+};
+__device__ __forceinline__ LaneTurn lane_turn(const HeadArgs& A, int64_t pos, int lane, float sign) {
+  LaneTurn t;
   const int rd = A.rope.rotary_dim;
-  if (d >= rd) return row[d];
-  int i, other;
-  bool second;
-  if (A.rope.interleaved) {
-    i = d >> 1;
-    second = d & 1;
-    other = d ^ 1;
-  } else {
-    second = d >= rd / 2;
-    i = second ? d - rd / 2 : d;
-    other = second ? d - rd / 2 : d + rd / 2;
+#pragma unroll
+  for (int i = 0; i < kPerLane; ++i) {
+    const int d = lane + 32 * i;
+    t.cs[i] = 1.f;
+    t.sn[i] = 0.f;
+    t.other[i] = d;
+    if (d < rd) {
+      const bool second = A.rope.interleaved ? d & 1 : d >= rd / 2;
+      const int pair = A.rope.interleaved ? d >> 1 : second ? d - rd / 2 : d;
+      t.other[i] = A.rope.interleaved ? d ^ 1 : second ? d - rd / 2 : d + rd / 2;
+      const float2 c = cos_sin(A.rope.turns[pair], pos);
+      t.cs[i] = c.x;
+      t.sn[i] = second ? sign * c.y : -sign * c.y;
+    }
   }
-  const float2 cs = cos_sin(A.rope.turns[i], pos);
-  return row[d] * cs.x + (second ? sign : -sign) * row[other] * cs.y;
+  return t;
+}
+__device__ __forceinline__ void apply(const LaneTurn& t, float* row, int dh, int lane, float (&x)[kPerLane]) {
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < kPerLane; ++i)
+    if (lane + 32 * i < dh) row[lane + 32 * i] = x[i];
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < kPerLane; ++i)
+    if (lane + 32 * i < dh) x[i] = t.cs[i] * x[i] + t.sn[i] * row[t.other[i]];
+}
+template <typename T>
+__device__ __forceinline__ void load_lane(const T* p, int dh, int lane, float (&x)[kPerLane]) {
+#pragma unroll
+  for (int i = 0; i < kPerLane; ++i) x[i] = lane + 32 * i < dh ? ldf(p + lane + 32 * i) : 0.f;
+}
+template <typename T>
+__device__ __forceinline__ void store_lane(T* p, int dh, int lane, const float (&x)[kPerLane]) {
+#pragma unroll
+  for (int i = 0; i < kPerLane; ++i)
+    if (lane + 32 * i < dh) stf(p + lane + 32 * i, x[i]);
 }
 
-// ---------------------------------------------------------------- any head size, one warp a head
-// Lane l holds elements l, l + 32, ... of its head; the row goes through shared memory to reach
-// its rotation partners.
+// Heads first, first + step, ... of a token's q, k or v, U of them loaded ahead.
+template <typename T>
+__device__ __forceinline__ void any_run(const HeadArgs& A, const T* w, bool turned, const LaneTurn& turn,
+                                        const T* src, T* dst, int64_t dst_head, int heads, int first, int step,
+                                        float* row, int lane) {
+  constexpr int U = 2;
+  const int dh = A.dh;
+  float wl[kPerLane];
+  if (w != nullptr) load_lane(w, dh, lane, wl);
+  for (int h0 = first; h0 < heads; h0 += U * step) {
+    float x[U][kPerLane];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (h0 + u * step < heads) load_lane(src + static_cast<int64_t>(h0 + u * step) * dh, dh, lane, x[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int h = h0 + u * step;
+      if (h >= heads) break;
+      if (w != nullptr) {
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i) ss += x[u][i] * x[u][i];
+        const float r = rsqrtf(warp_sum(ss) / dh + A.eps);
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i) x[u][i] = lane + 32 * i < dh ? x[u][i] * r * wl[i] : 0.f;
+      }
+      if (turned) apply(turn, row, dh, lane, x[u]);
+      store_lane(dst + h * dst_head, dh, lane, x[u]);
+    }
+  }
+}
+
 template <typename T, typename Rows, bool CACHE>
 __global__ void __launch_bounds__(kThreads)
-    heads_fwd_any(const __grid_constant__ HeadArgs A, const __grid_constant__ Rows R,
-                  const T* __restrict__ qw, const T* __restrict__ kw, const T* q, const T* k,
-                  const T* v, T* q_out, T* k_out, T* v_out) {
+    heads_fwd_any(const __grid_constant__ HeadArgs A, const __grid_constant__ Rows R, int parts,
+                  const T* __restrict__ qw, const T* __restrict__ kw, const T* q, const T* k, const T* v,
+                  T* q_out, T* k_out, T* v_out) {
   __shared__ float rows[kWarps][128];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, dh = A.dh;
-  float* row = rows[warp];
-  const int per = A.hq + A.hkv * (CACHE ? 2 : 1);
-  const int64_t units = static_cast<int64_t>(A.n_rows) * per;
-  for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + warp; u < units;
-       u += static_cast<int64_t>(gridDim.x) * kWarps) {
-    const int t = static_cast<int>(u / per), h = static_cast<int>(u % per);
-    const Token tok = locate(R, t, A.hkv * static_cast<int64_t>(dh));
-    if (tok.absent) continue;
-    const T* src;
-    T* dst;
-    const T* w = nullptr;
-    bool turn = A.rope.rotary_dim > 0;
-    if (h < A.hq) {
-      src = q + t * A.q_stride + h * dh;
-      dst = q_out + (static_cast<int64_t>(t) * A.hq + h) * dh;
-      w = qw;
-    } else if (h < A.hq + A.hkv) {
-      src = k + t * A.k_stride + (h - A.hq) * dh;
-      dst = k_out + tok.kv + (h - A.hq) * A.kv_head;
-      w = kw;
-    } else {
-      src = v + t * A.v_stride + (h - A.hq - A.hkv) * dh;
-      dst = v_out + tok.kv + (h - A.hq - A.hkv) * A.kv_head;
-      turn = false;
-    }
-    if (tok.idle) {
-      if (h < A.hq)
-        for (int d = lane; d < dh; d += 32) stf(dst + d, 0.f);
-      continue;
-    }
-    float x[kMaxPerLane], ss = 0.f;
+  const int lane = threadIdx.x & 31, dh = A.dh;
+  float* row = rows[threadIdx.x >> 5];
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int64_t t = unit / parts;
+  const int part = static_cast<int>(unit - t * parts);
+  if (t >= A.n_rows) return;
+  const Token tok = locate(R, static_cast<int>(t), A.hkv * static_cast<int64_t>(dh));
+  if (tok.absent) return;
+  T* qo = q_out + t * A.hq * dh;
+  if (tok.idle) {
+    const float zero[kPerLane] = {};
+    for (int h = part; h < A.hq; h += parts) store_lane(qo + static_cast<int64_t>(h) * dh, dh, lane, zero);
+    return;
+  }
+  const bool turned = A.rope.rotary_dim > 0;
+  const LaneTurn turn = lane_turn(A, tok.pos, lane, 1.f);
+  any_run(A, qw, turned, turn, q + t * A.q_stride, qo, dh, A.hq, part, parts, row, lane);
+  // the next run of heads goes on with the part after the last one's
+  const int pk = ((part - A.hq) % parts + parts) % parts;
+  any_run(A, kw, turned, turn, k + t * A.k_stride, k_out + tok.kv, A.kv_head, A.hkv, pk, parts, row, lane);
+  if constexpr (CACHE) {
+    const int pv = ((pk - A.hkv) % parts + parts) % parts;
+    any_run<T>(A, nullptr, false, turn, v + t * A.v_stride, v_out + tok.kv, A.kv_head, A.hkv, pv, parts, row, lane);
+  }
+}
+
+// The weight gradients of the lanes' elements are summed in registers over a warp's tokens, over
+// the block's warps in shared memory, and written per block. `parts` as above (a part's heads stay
+// the same, so that the sums do not depend on the order).
+template <typename T>
+__device__ __forceinline__ void any_run_bwd(const HeadArgs& A, const T* w, bool turned, const LaneTurn& turn,
+                                            const T* x, const T* dy, T* dx, int heads, int first, int step,
+                                            float* row, int lane, float (&acc)[kPerLane]) {
+  const int dh = A.dh;
+  float wl[kPerLane];
+  if (w != nullptr) load_lane(w, dh, lane, wl);
+  constexpr int U = 2;
+  for (int h0 = first; h0 < heads; h0 += U * step) {
+    float gu[U][kPerLane], nu[U][kPerLane];
 #pragma unroll
-    for (int i = 0; i < kMaxPerLane; ++i) {
-      const int d = lane + 32 * i;
-      x[i] = d < dh ? ldf(src + d) : 0.f;
-      ss += x[i] * x[i];
-    }
-    if (w != nullptr) {
-      const float r = rsqrtf(warp_sum(ss) / dh + A.eps);
-#pragma unroll
-      for (int i = 0; i < kMaxPerLane; ++i) {
-        const int d = lane + 32 * i;
-        if (d < dh) x[i] = x[i] * r * ldf(w + d);
+    for (int u = 0; u < U; ++u) {
+      const int64_t h = h0 + u * step;
+      if (h < heads) {
+        load_lane(dy + h * dh, dh, lane, gu[u]);
+        if (w != nullptr) load_lane(x + h * dh, dh, lane, nu[u]);
       }
     }
-    __syncwarp();
 #pragma unroll
-    for (int i = 0; i < kMaxPerLane; ++i)
-      if (lane + 32 * i < dh) row[lane + 32 * i] = x[i];
-    __syncwarp();
+    for (int u = 0; u < U; ++u) {
+      const int h = h0 + u * step;
+      if (h >= heads) break;
+      float (&g)[kPerLane] = gu[u], (&n)[kPerLane] = nu[u];
+      if (turned) apply(turn, row, dh, lane, g);
+      if (w != nullptr) {
+        float ss = 0.f, hn = 0.f;
 #pragma unroll
-    for (int i = 0; i < kMaxPerLane; ++i) {
-      const int d = lane + 32 * i;
-      if (d < dh) stf(dst + d, turn ? rotated(A, row, d, tok.pos, 1.f) : x[i]);
+        for (int i = 0; i < kPerLane; ++i) ss += n[i] * n[i];
+        const float r = rsqrtf(warp_sum(ss) / dh + A.eps);
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i) {
+          n[i] *= r;
+          acc[i] += g[i] * n[i];
+          g[i] = lane + 32 * i < dh ? g[i] * wl[i] : 0.f;
+          hn += g[i] * n[i];
+        }
+        const float mean = warp_sum(hn) / dh;
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i) g[i] = r * (g[i] - n[i] * mean);
+      }
+      store_lane(dx + static_cast<int64_t>(h) * dh, dh, lane, g);
     }
   }
 }
 
-// A warp takes all heads of its tokens; the weight gradients of its lanes' elements are summed
-// in registers, over the block's warps in shared memory, and written per block.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-    heads_bwd_any(const __grid_constant__ HeadArgs A, const __grid_constant__ RingRows R,
+    heads_bwd_any(const __grid_constant__ HeadArgs A, const __grid_constant__ RingRows R, int parts,
                   const T* __restrict__ qw, const T* __restrict__ kw, const T* __restrict__ q,
                   const T* __restrict__ k, const T* dq_out, const T* dk_out, T* dq, T* dk,
                   float* __restrict__ partial) {
@@ -241,59 +311,22 @@ __global__ void __launch_bounds__(kThreads)
   __shared__ float sums[kWarps][2][128];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, dh = A.dh;
   float* row = rows[warp];
-  float acc[2][kMaxPerLane] = {};
-  for (int t = blockIdx.x * kWarps + warp; t < A.n_rows; t += gridDim.x * kWarps) {
-    const Token tok = locate(R, t, 0);
-    for (int which = 0; which < 2; ++which) {
-      const int heads = which ? A.hkv : A.hq;
-      const T* w = which ? kw : qw;
-      for (int h = 0; h < heads; ++h) {
-        const int64_t o = (static_cast<int64_t>(t) * heads + h) * dh;
-        const T* dy = (which ? dk_out : dq_out) + o;
-        T* dx = (which ? dk : dq) + o;
-        __syncwarp();
-        for (int d = lane; d < dh; d += 32) row[d] = ldf(dy + d);
-        __syncwarp();
-        float g[kMaxPerLane];
-#pragma unroll
-        for (int i = 0; i < kMaxPerLane; ++i) {
-          const int d = lane + 32 * i;
-          g[i] = d < dh ? (A.rope.rotary_dim > 0 ? rotated(A, row, d, tok.pos, -1.f) : row[d]) : 0.f;
-        }
-        if (w != nullptr) {
-          const T* src = which ? k + t * A.k_stride + h * dh : q + t * A.q_stride + h * dh;
-          float x[kMaxPerLane], ss = 0.f;
-#pragma unroll
-          for (int i = 0; i < kMaxPerLane; ++i) {
-            const int d = lane + 32 * i;
-            x[i] = d < dh ? ldf(src + d) : 0.f;
-            ss += x[i] * x[i];
-          }
-          const float r = rsqrtf(warp_sum(ss) / dh + A.eps);
-          float hn = 0.f;
-#pragma unroll
-          for (int i = 0; i < kMaxPerLane; ++i) {
-            const int d = lane + 32 * i;
-            x[i] *= r;
-            if (which) acc[1][i] += g[i] * x[i]; else acc[0][i] += g[i] * x[i];
-            g[i] *= d < dh ? ldf(w + d) : 0.f;
-            hn += g[i] * x[i];
-          }
-          const float mean = warp_sum(hn) / dh;
-#pragma unroll
-          for (int i = 0; i < kMaxPerLane; ++i) g[i] = r * (g[i] - x[i] * mean);
-        }
-#pragma unroll
-        for (int i = 0; i < kMaxPerLane; ++i) {
-          const int d = lane + 32 * i;
-          if (d < dh) stf(dx + d, g[i]);
-        }
-      }
-    }
+  float acc[2][kPerLane] = {};
+  const bool turned = A.rope.rotary_dim > 0;
+  const int64_t units = static_cast<int64_t>(A.n_rows) * parts;
+  for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + warp; u < units;
+       u += static_cast<int64_t>(gridDim.x) * kWarps) {
+    const int64_t t = u / parts;
+    const int part = static_cast<int>(u - t * parts);
+    const LaneTurn turn = lane_turn(A, locate(R, static_cast<int>(t), 0).pos, lane, -1.f);
+    const int64_t oq = t * A.hq * dh, ok = t * A.hkv * dh;
+    any_run_bwd(A, qw, turned, turn, q + t * A.q_stride, dq_out + oq, dq + oq, A.hq, part, parts, row, lane, acc[0]);
+    const int pk = ((part - A.hq) % parts + parts) % parts;
+    any_run_bwd(A, kw, turned, turn, k + t * A.k_stride, dk_out + ok, dk + ok, A.hkv, pk, parts, row, lane, acc[1]);
   }
   if (qw == nullptr) return;
 #pragma unroll
-  for (int i = 0; i < kMaxPerLane; ++i) {
+  for (int i = 0; i < kPerLane; ++i) {
     sums[warp][0][lane + 32 * i] = acc[0][i];
     sums[warp][1][lane + 32 * i] = acc[1][i];
   }
@@ -411,12 +444,13 @@ __device__ __forceinline__ float group_sum(float x) {
 }
 
 // The heads `first`, `first + step`, ... (in warps' loads of HEADS heads) of one token's q, k or
-// v: U loads in flight, then norm, rotation and store of each. The token's cosines and sines
-// are in registers.
-template <typename T, int DH, bool INTER, int U>
+// v: U loads in flight, then norm, rotation and store of each. The token's cosines and sines are in
+// registers; prepare() is called once, with the first loads under way.
+template <typename T, int DH, bool INTER, int U, typename F>
 __device__ __forceinline__ void head_run(const HeadArgs& A, const T* __restrict__ w, bool turned, const T* src,
                                          T* dst, int64_t dst_head, int heads, int first, int step, int lane,
-                                         const float (&cs)[Vec<T, DH>::N], const float (&sn)[Vec<T, DH>::N]) {
+                                         const float (&cs)[Vec<T, DH>::N], const float (&sn)[Vec<T, DH>::N],
+                                         F&& prepare) {
   using V = Vec<T, DH>;
   const int c = lane % V::LANES, sub = lane / V::LANES;
   const int runs = (heads + V::HEADS - 1) / V::HEADS;
@@ -429,6 +463,7 @@ __device__ __forceinline__ void head_run(const HeadArgs& A, const T* __restrict_
       const int h = (i0 + u * step) * V::HEADS + sub;
       if (h < heads) p[u] = load_piece<T, DH>(src + h * DH, c);
     }
+    if (i0 == first) prepare();
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int h = (i0 + u * step) * V::HEADS + sub;
@@ -483,29 +518,33 @@ __global__ void __launch_bounds__(kThreads)
   }
   float cs[V::N], sn[V::N];
   const bool turned = A.rope.rotary_dim > 0;
-  if (turned) piece_angles<T, DH, INTER>(A, tok.pos, lane, cs, sn);
-  constexpr int U = 4;
-  head_run<T, DH, INTER, U>(A, qw, turned, q + t * A.q_stride, qo, DH, A.hq, part, parts, lane, cs, sn);
-  // the next run of heads goes on with the part after the last one's
+  auto angles = [&]() {
+    if (turned) piece_angles<T, DH, INTER>(A, tok.pos, lane, cs, sn);
+  };
+  auto none = []() {};
   const int runs_q = (A.hq + V::HEADS - 1) / V::HEADS, runs_k = (A.hkv + V::HEADS - 1) / V::HEADS;
+  if (part >= runs_q) angles();
+  head_run<T, DH, INTER, 4>(A, qw, turned, q + t * A.q_stride, qo, DH, A.hq, part, parts, lane, cs, sn, angles);
+  // the next run of heads goes on with the part after the last one's
   const int pk = ((part - runs_q) % parts + parts) % parts;
   head_run<T, DH, INTER, 2>(A, kw, turned, k + t * A.k_stride, k_out + tok.kv, A.kv_head, A.hkv, pk, parts, lane,
-                            cs, sn);
+                            cs, sn, none);
   if constexpr (CACHE) {
     const int pv = ((pk - runs_k) % parts + parts) % parts;
     head_run<T, DH, INTER, 2>(A, nullptr, false, v + t * A.v_stride, v_out + tok.kv, A.kv_head, A.hkv, pv, parts,
-                              lane, cs, sn);
+                              lane, cs, sn, none);
   }
 }
 
 constexpr int kBwdThreads = 128;
 
 // Backward of one token's q or k heads; `acc` gathers g * n of the lane's elements.
-template <typename T, int DH, bool INTER, int U>
+template <typename T, int DH, bool INTER, int U, typename F>
 __device__ __forceinline__ void head_run_bwd(const HeadArgs& A, const T* __restrict__ w, bool turned, const T* x,
                                              const T* dy, T* dx, int heads, int lane,
                                              const float (&cs)[Vec<T, DH>::N], const float (&sn)[Vec<T, DH>::N],
-                                             float (&acc_a)[Vec<T, DH>::N], float (&acc_b)[Vec<T, DH>::N]) {
+                                             float (&acc_a)[Vec<T, DH>::N], float (&acc_b)[Vec<T, DH>::N],
+                                             F&& prepare) {
   using V = Vec<T, DH>;
   const int c = lane % V::LANES, sub = lane / V::LANES;
   Piece<T, DH> wp;
@@ -521,6 +560,7 @@ __device__ __forceinline__ void head_run_bwd(const HeadArgs& A, const T* __restr
         if (w != nullptr) p[u] = load_piece<T, DH>(x + h * DH, c);
       }
     }
+    if (h0 == sub) prepare();
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int h = h0 + u * V::HEADS;
@@ -581,12 +621,13 @@ __global__ void __launch_bounds__(kBwdThreads, 4)
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * WARPS + warp; t < A.n_rows;
        t += static_cast<int64_t>(gridDim.x) * WARPS) {
     float cs[V::N], sn[V::N];
-    if (turned) piece_angles<T, DH, INTER>(A, locate(R, static_cast<int>(t), 0).pos, lane, cs, sn);
     const int64_t oq = t * A.hq * DH, ok = t * A.hkv * DH;
-    head_run_bwd<T, DH, INTER, 2>(A, qw, turned, q + t * A.q_stride, dq_out + oq, dq + oq, A.hq, lane, cs, sn,
-                                  acc[0][0], acc[0][1]);
+    head_run_bwd<T, DH, INTER, 2>(
+        A, qw, turned, q + t * A.q_stride, dq_out + oq, dq + oq, A.hq, lane, cs, sn, acc[0][0], acc[0][1], [&]() {
+          if (turned) piece_angles<T, DH, INTER>(A, locate(R, static_cast<int>(t), 0).pos, lane, cs, sn);
+        });
     head_run_bwd<T, DH, INTER, 2>(A, kw, turned, k + t * A.k_stride, dk_out + ok, dk + ok, A.hkv, lane, cs, sn,
-                                  acc[1][0], acc[1][1]);
+                                  acc[1][0], acc[1][1], []() {});
   }
   if (qw == nullptr) return;
 #pragma unroll
@@ -685,6 +726,13 @@ void fill_args(HeadArgs* A, const ra_rope* rope, float eps, int hq, int hkv, int
   A->q_stride = A->k_stride = A->v_stride = 0;
 }
 
+// Few tokens: the `runs` of their heads are shared between warps until there are 16 warps for every
+// SM.
+int parts_of(int n_rows, int runs) {
+  const int want = (16 * sm_count() + n_rows - 1) / n_rows;
+  return want < 1 ? 1 : want > runs ? runs : want;
+}
+
 // Whether the 16-byte kernels can take a call: a whole-head rotation or none, and rows that all
 // start on 16 bytes. (Measured at 131072 tokens, 32/8 heads of 128, bf16, forward and backward:
 // 16-byte kernels 1.2 ms, one warp a head 10.6 ms.)
@@ -699,10 +747,8 @@ template <typename T, int DH, bool INTER, typename Rows, bool CACHE>
 cudaError_t fwd_vec(const HeadArgs& A, const Rows& R, const void* qw, const void* kw, const void* q,
                     const void* k, const void* v, void* q_out, void* k_out, void* v_out, cudaStream_t st) {
   using V = Vec<T, DH>;
-  // Few tokens: their heads are shared between warps until there are 16 warps for every SM.
   const int runs = (A.hq + V::HEADS - 1) / V::HEADS + (A.hkv + V::HEADS - 1) / V::HEADS * (CACHE ? 2 : 1);
-  const int want = (16 * sm_count() + A.n_rows - 1) / A.n_rows;
-  const int parts = want < 1 ? 1 : want > runs ? runs : want;
+  const int parts = parts_of(A.n_rows, runs);
   const int64_t units = static_cast<int64_t>(A.n_rows) * parts;
   heads_fwd_vec<T, DH, INTER, Rows, CACHE><<<static_cast<unsigned>((units + kWarps - 1) / kWarps), kThreads, 0, st>>>(
       A, R, parts, static_cast<const T*>(qw), static_cast<const T*>(kw), static_cast<const T*>(q),
@@ -724,9 +770,10 @@ cudaError_t launch_fwd(const HeadArgs& A, const Rows& R, const void* qw, const v
     return inter ? fwd_vec<T, 64, true, Rows, CACHE>(A, R, qw, kw, q, k, v, q_out, k_out, v_out, st)
                  : fwd_vec<T, 64, false, Rows, CACHE>(A, R, qw, kw, q, k, v, q_out, k_out, v_out, st);
   }
-  const int64_t units = static_cast<int64_t>(A.n_rows) * (A.hq + A.hkv * (CACHE ? 2 : 1));
-  heads_fwd_any<T, Rows, CACHE><<<blocks_for(units, kWarps, 8 * sm_count()), kThreads, 0, st>>>(
-      A, R, static_cast<const T*>(qw), static_cast<const T*>(kw), static_cast<const T*>(q),
+  const int parts = parts_of(A.n_rows, A.hq + A.hkv * (CACHE ? 2 : 1));
+  const int64_t units = static_cast<int64_t>(A.n_rows) * parts;
+  heads_fwd_any<T, Rows, CACHE><<<static_cast<unsigned>((units + kWarps - 1) / kWarps), kThreads, 0, st>>>(
+      A, R, parts, static_cast<const T*>(qw), static_cast<const T*>(kw), static_cast<const T*>(q),
       static_cast<const T*>(k), static_cast<const T*>(v), static_cast<T*>(q_out),
       static_cast<T*>(k_out), static_cast<T*>(v_out));
   return cudaGetLastError();
@@ -759,9 +806,10 @@ cudaError_t launch_bwd(const HeadArgs& A, const RingRows& R, const void* qw, con
       else bwd_vec<T, 64, false>(blocks, A, R, qw, kw, q, k, dq_out, dk_out, dq, dk, partial, st);
     }
   } else {
-    blocks = blocks_for(A.n_rows, kWarps, kHeadBwdBlocks);
+    const int parts = parts_of(A.n_rows, A.hq + A.hkv);
+    blocks = blocks_for(static_cast<int64_t>(A.n_rows) * parts, kWarps, kHeadBwdBlocks);
     heads_bwd_any<T><<<blocks, kThreads, 0, st>>>(
-        A, R, static_cast<const T*>(qw), static_cast<const T*>(kw), static_cast<const T*>(q),
+        A, R, parts, static_cast<const T*>(qw), static_cast<const T*>(kw), static_cast<const T*>(q),
         static_cast<const T*>(k), static_cast<const T*>(dq_out), static_cast<const T*>(dk_out),
         static_cast<T*>(dq), static_cast<T*>(dk), partial);
   }
