@@ -33,7 +33,9 @@ static __device__ unsigned int g_status_decode;
 namespace {
 
 constexpr int kUnit = 64;       // keys of a unit
-constexpr int kMaxCtas = 304;   // two on each of 152 SMs
+constexpr int kSms = 152;
+constexpr int kMaxPerSm = 3;
+constexpr int kMaxCtas = kMaxPerSm * kSms;
 constexpr int kThreads = 128;
 constexpr int kJoinThreads = 256;
 
@@ -407,10 +409,14 @@ template <int DH, bool WIDE>
 struct MmaCfg {
   static constexpr int PITCH = DH * 2 + 16;                  // bytes of a key's row in a stage
   static constexpr int STAGE = 2 * 16 * PITCH;               // a warp's K and V of 16 keys
-  static constexpr int STAGES = DH == 128 ? 3 : 5;
+  // Measured on GB300 (ragged batch of 64, heads of 128; windowed batch of 33, heads of 64): two
+  // stages and two CTAs an SM 343 us, three stages 349, five and one CTA 419; heads of 64 three
+  // stages and three CTAs 17 us, two CTAs 20.
+  static constexpr int STAGES = DH == 128 ? 2 : 3;
+  static constexpr int CTAS = DH == 128 ? 2 : 3;             // on an SM
   static constexpr int RING = 4 * STAGES * STAGE;
   static constexpr int CHUNK = 8192 / (4 * DH * 4);          // rows joined at a time
-  static constexpr int SMEM = RING + 8192;                   // two CTAs on an SM
+  static constexpr int SMEM = RING + 8192;
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
@@ -473,7 +479,7 @@ struct Cursor {
 };
 
 template <int DH, bool WIDE>
-__global__ void __launch_bounds__(kThreads) decode_mma(const __grid_constant__ DecodeArgs A) {
+__global__ void __launch_bounds__(kThreads, (MmaCfg<DH, WIDE>::CTAS)) decode_mma(const __grid_constant__ DecodeArgs A) {
   using C = MmaCfg<DH, WIDE>;
   constexpr int KS = DH / 16;                  // steps of 16 elements
   constexpr int LANES = DH * 2 / 16;           // lanes that copy one row
@@ -773,6 +779,8 @@ int heads_of_block(int dtype, int group) {
   return (group + blocks - 1) / blocks;
 }
 
+int ctas_per_sm(int dtype, int dh) { return dtype == RA_F32 ? 2 : dh == 64 ? MmaCfg<64, false>::CTAS : MmaCfg<128, false>::CTAS; }
+
 template <int DH, bool WIDE>
 cudaError_t launch_mma(const DecodeArgs& A, int grid, cudaStream_t st) {
   using C = MmaCfg<DH, WIDE>;
@@ -788,7 +796,7 @@ cudaError_t launch(DecodeArgs& A, int dtype, cudaStream_t st) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  const int grid = 2 * n_sm < kMaxCtas ? 2 * n_sm : kMaxCtas;
+  const int grid = ctas_per_sm(dtype, A.dh) * (n_sm < kSms ? n_sm : kSms);
   if (dtype == RA_F32) {
     switch (A.block_heads) {
       case 1: decode_simt<1><<<grid, kThreads, 0, st>>>(A); break;
@@ -818,7 +826,7 @@ cudaError_t launch(DecodeArgs& A, int dtype, cudaStream_t st) {
 
 size_t workspace_of(const ra_paged_cache* c, int hq) {
   const size_t part = heads_of_block(c->dtype, hq / c->hkv) * (c->head_dim + 2) * sizeof(float);
-  return (2 * kMaxCtas * part + 255) & ~size_t(255);
+  return (2 * ctas_per_sm(c->dtype, c->head_dim) * kSms * part + 255) & ~size_t(255);
 }
 
 int check_heads(const ra_paged_cache* c, int hq) {
