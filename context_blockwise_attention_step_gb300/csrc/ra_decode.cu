@@ -6,7 +6,8 @@
 // as a ragged batch, and the host need not know the lengths. A CTA whose share covers a pair
 // whole writes its result; else it writes its part of the pair (running max m, denominator l,
 // unnormalised sum) to the workspace, at most two parts (the first and the last pair of its
-// share), and a second kernel joins the parts of each pair in the order of the CTAs:
+// share). A pair is cut only where one CTA's share ends and the next one's begins, so a second
+// kernel looks at these places and joins the parts of each cut pair in the order of the CTAs:
 //
 //   M = max m_i,  l = sum 2^(m_i - M) l_i,  out = sum 2^(m_i - M) o_i / l,
 //   lse = (M + log2 l) ln 2
@@ -57,6 +58,12 @@ struct DecodeArgs {
   float* lse;
 };
 
+template <typename T> __device__ __forceinline__ void stv(T* p, float v);
+template <> __device__ __forceinline__ void stv<float>(float* p, float v) { *p = v; }
+template <> __device__ __forceinline__ void stv<__nv_bfloat16>(__nv_bfloat16* p, float v) {
+  *p = __float2bfloat16_rn(v);
+}
+
 struct Visible {
   int vis, head, skip;  // keys seen; of these the first `head` are keys 0.. , the rest skip + i
 };
@@ -101,30 +108,6 @@ __device__ __forceinline__ int64_t key_row(const DecodeArgs& A, int b, const Vis
   return at * A.page_stride + static_cast<int64_t>(key - page * A.page_size) * A.slot_stride;
 }
 
-__device__ __forceinline__ int64_t block_sum(int64_t x, int64_t* smem) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  if ((threadIdx.x & 31) == 0) smem[threadIdx.x >> 5] = x;
-  __syncthreads();
-  int64_t s = 0;
-  for (int w = 0; w < static_cast<int>(blockDim.x) / 32; ++w) s += smem[w];
-  __syncthreads();
-  return s;
-}
-
-// Units before sequence b and in all, in units per block of query heads and K/V head.
-__device__ __forceinline__ void count_units(const DecodeArgs& A, int b, int64_t* before, int64_t* total,
-                                            int64_t* smem) {
-  int64_t lo = 0, all = 0;
-  for (int i = threadIdx.x; i < A.n_seqs; i += blockDim.x) {
-    const int u = units_of(A, i);
-    all += u;
-    if (i < b) lo += u;
-  }
-  *before = block_sum(lo, smem);
-  *total = block_sum(all, smem);
-}
-
 // CTAs that get work, and the first unit of CTA i.
 __device__ __forceinline__ int active_ctas(int64_t units, int ctas) {
   return units < ctas ? static_cast<int>(units) : ctas;
@@ -132,8 +115,7 @@ __device__ __forceinline__ int active_ctas(int64_t units, int ctas) {
 __device__ __forceinline__ int64_t first_unit(int64_t units, int ctas, int i) { return units * i / ctas; }
 // The CTA that has unit u: the largest i with first_unit(i) <= u.
 __device__ __forceinline__ int cta_of(int64_t units, int ctas, int64_t u) {
-  int i = static_cast<int>(((u + 1) * ctas - 1) / units);
-  return i;
+  return static_cast<int>(((u + 1) * ctas - 1) / units);
 }
 
 // A walk over the pieces of a CTA's share: (sequence, block of query heads) and a range of its
@@ -144,12 +126,14 @@ struct Share {
   int b, pair, units;   // sequence, pair within it (hk * blocks_per_kv + block), its units
 };
 
-// Sets up the share of CTA blockIdx.x of gridDim.x; false if it is empty. `scan`: kThreads + 1.
-__device__ __forceinline__ bool share_begin(const DecodeArgs& A, Share& S, int64_t* scan, int64_t* total,
-                                            int* ctas) {
+// The share of CTA `cta` of `grid`, worked out by the block's THREADS threads; false if it is empty.
+// `scan`: 8 values in shared memory.
+template <int THREADS>
+__device__ __forceinline__ bool share_of(const DecodeArgs& A, int cta, int grid, Share& S, int64_t* scan,
+                                         int64_t* total, int* ctas) {
   const int tid = threadIdx.x;
   const int per = A.hkv * A.blocks_per_kv;
-  const int chunk = (A.n_seqs + kThreads - 1) / kThreads;
+  const int chunk = (A.n_seqs + THREADS - 1) / THREADS;
   const int b0 = min(A.n_seqs, tid * chunk), b1 = min(A.n_seqs, b0 + chunk);
   int64_t mine = 0;
   for (int b = b0; b < b1; ++b) mine += units_of(A, b);
@@ -163,18 +147,18 @@ __device__ __forceinline__ bool share_begin(const DecodeArgs& A, Share& S, int64
   if ((tid & 31) == 31) scan[tid >> 5] = x;
   __syncthreads();
   int64_t before = 0, sum = 0;
-  for (int w = 0; w < kThreads / 32; ++w) {
+  for (int w = 0; w < THREADS / 32; ++w) {
     if (w < tid >> 5) before += scan[w];
     sum += scan[w];
   }
   before += x - mine;  // units (per pair) before this thread's sequences
   const int64_t units = sum * per;
   *total = units;
-  *ctas = active_ctas(units, gridDim.x);
+  *ctas = active_ctas(units, grid);
   __syncthreads();
-  if (static_cast<int>(blockIdx.x) >= *ctas) return false;
-  S.u = first_unit(units, *ctas, blockIdx.x);
-  S.end = first_unit(units, *ctas, blockIdx.x + 1);
+  if (cta >= *ctas) return false;
+  S.u = first_unit(units, *ctas, cta);
+  S.end = first_unit(units, *ctas, cta + 1);
   // the thread whose sequences hold unit S.u finds the pair
   if (S.u >= before * per && S.u < (before + mine) * per) {
     int64_t base = before * per;
@@ -209,6 +193,30 @@ __device__ __forceinline__ void share_next(const DecodeArgs& A, Share& S) {
   }
 }
 
+// A main CTA's start: lets the join kernel launch, finds its share of the units.
+__device__ __forceinline__ bool share_begin(const DecodeArgs& A, Share& S, int64_t* scan) {
+  launch_dependents();
+  int64_t total;
+  int ctas;
+  return share_of<kThreads>(A, blockIdx.x, gridDim.x, S, scan, &total, &ctas);
+}
+
+// A main CTA's end: the results of its part of the idle sequences (lengths outside the cache are
+// reported here too). 32 sequences a warp at once.
+template <typename T>
+__device__ __forceinline__ void finish_idle(const DecodeArgs& A) {
+  const int lane = threadIdx.x & 31, step = gridDim.x * (kThreads / 32);
+  for (int b0 = blockIdx.x + gridDim.x * (threadIdx.x >> 5); b0 < A.n_seqs; b0 += 32 * step) {
+    const int b = b0 + lane * step;
+    unsigned idle = __ballot_sync(0xffffffffu, b < A.n_seqs && visible(A, b, true).vis == 0);
+    for (; idle != 0; idle &= idle - 1) {
+      const int64_t row = static_cast<int64_t>(b0 + (__ffs(idle) - 1) * step) * A.hq;
+      for (int i = lane; i < A.hq * A.dh; i += 32) stv<T>(static_cast<T*>(A.out) + row * A.dh + i, 0.f);
+      for (int h = lane; h < A.hq; h += 32) A.lse[row + h] = -INFINITY;
+    }
+  }
+}
+
 __device__ __forceinline__ float* part_of(const DecodeArgs& A, int cta, int which) {
   return A.parts + (static_cast<int64_t>(cta) * 2 + which) * A.block_heads * (A.dh + 2);
 }
@@ -239,11 +247,6 @@ __device__ __forceinline__ float lane_sums(float (&x)[N], int lane) {
   return x[0];
 }
 
-template <typename T> __device__ __forceinline__ void stv(T* p, float v);
-template <> __device__ __forceinline__ void stv<float>(float* p, float v) { *p = v; }
-template <> __device__ __forceinline__ void stv<__nv_bfloat16>(__nv_bfloat16* p, float v) {
-  *p = __float2bfloat16_rn(v);
-}
 
 // 1 / l; a query whose every score is -inf has l = 0 and gets out = 0, lse = -inf.
 __device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
@@ -255,20 +258,17 @@ __device__ __forceinline__ void store_lse(const DecodeArgs& A, int b, int h, flo
 // Float32. Four warps, each 16 keys of a unit, four keys at a time; lane l holds elements l, l + 32, ...
 // of q, of the keys and of the sums, for HB query heads.
 template <int HB>
-__global__ void __launch_bounds__(kThreads) decode_simt(const __grid_constant__ DecodeArgs A) {
+__global__ void __launch_bounds__(kThreads, HB == 8 ? 2 : 3) decode_simt(const __grid_constant__ DecodeArgs A) {
   constexpr int NI = 4;  // elements per lane: head_dim <= 128
-  __shared__ int64_t scan[kThreads / 32 < 4 ? 4 : kThreads / 32];
+  __shared__ int64_t scan[8];
   __shared__ float sm_m[4][HB], sm_l[4][HB], sm_o[4][HB][128];
-  launch_dependents();
   Share S;
-  int64_t total;
-  int ctas;
-  if (!share_begin(A, S, scan, &total, &ctas)) return;
+  const bool some = share_begin(A, S, scan);
   const int64_t share0 = S.u;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, dh = A.dh;
   const float* kp = static_cast<const float*>(A.k_pages);
   const float* vp = static_cast<const float*>(A.v_pages);
-  for (;;) {
+  while (some) {
     const int hk = S.pair / A.blocks_per_kv, blk = S.pair % A.blocks_per_kv;
     const int g0 = blk * HB, heads = min(HB, A.group - g0), h0 = hk * A.group + g0;
     const Visible vis = visible(A, S.b, true);
@@ -288,56 +288,66 @@ __global__ void __launch_bounds__(kThreads) decode_simt(const __grid_constant__ 
                        : 0.f;
       }
     }
-    for (int u = u0; u < u1; ++u) {
-      for (int t = 0; t < 4; ++t) {
-        const int key0 = u * kUnit + warp * 16 + t * 4;
-        if (key0 >= vis.vis) break;
-        int64_t row = 0;
-        if (lane < 4) row = key_row(A, S.b, vis, min(key0 + lane, vis.vis - 1)) + hk * A.head_stride;
-        float kr[4][NI], vr[4][NI];
+    // four keys at a time, the next four loaded meanwhile (step i: keys 4i .. 4i+3 of this warp's 16
+    // of unit u0 + i/4)
+    float kr[4][NI], vr[4][NI];
+    auto first_key = [&](int i) { return (u0 + (i >> 2)) * kUnit + warp * 16 + (i & 3) * 4; };
+    auto fetch = [&](int i) {
+      const int key0 = first_key(i);
+      if (i >= 4 * (u1 - u0) || key0 >= vis.vis) return;
+      int64_t row = 0;
+      if (lane < 4) row = key_row(A, S.b, vis, min(key0 + lane, vis.vis - 1)) + hk * A.head_stride;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int64_t at = __shfl_sync(0xffffffffu, row, j);
+      for (int j = 0; j < 4; ++j) {
+        const int64_t at = __shfl_sync(0xffffffffu, row, j);
 #pragma unroll
-          for (int i = 0; i < NI; ++i) {
-            const int d = lane + 32 * i;
-            kr[j][i] = d < dh ? *(kp + at + d) : 0.f;
-            vr[j][i] = d < dh ? *(vp + at + d) : 0.f;
-          }
+        for (int e = 0; e < NI; ++e) {
+          const int d = lane + 32 * e;
+          kr[j][e] = d < dh ? kp[at + d] : 0.f;
+          vr[j][e] = d < dh ? vp[at + d] : 0.f;
         }
-        float s[4 * HB];
+      }
+    };
+    fetch(0);
+    for (int i = 0; i < 4 * (u1 - u0); ++i) {
+      const int key0 = first_key(i);
+      float s[4 * HB], vc[4][NI];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int h = 0; h < HB; ++h) {
-            float x = 0.f;
-#pragma unroll
-            for (int i = 0; i < NI; ++i) x += qr[h][i] * kr[j][i];
-            s[j * HB + h] = x;
-          }
-        const float mine = lane_sums<4 * HB>(s, lane) * A.scale_log2;
+      for (int j = 0; j < 4; ++j) {
 #pragma unroll
         for (int h = 0; h < HB; ++h) {
-          float x[4], mx = m[h];
+          float x = 0.f;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            x[j] = __shfl_sync(0xffffffffu, mine, (j * HB + h) * (32 / (4 * HB)));
-            if (key0 + j >= vis.vis) x[j] = -INFINITY;
-            mx = fmaxf(mx, x[j]);
-          }
-          const float ref = mx == -INFINITY ? 0.f : mx;
-          const float alpha = exp2f(m[h] - ref);
-          m[h] = mx;
-          l[h] *= alpha;
+          for (int e = 0; e < NI; ++e) x += qr[h][e] * kr[j][e];
+          s[j * HB + h] = x;
+        }
 #pragma unroll
-          for (int i = 0; i < NI; ++i) o[h][i] *= alpha;
+        for (int e = 0; e < NI; ++e) vc[j][e] = vr[j][e];
+      }
+      fetch(i + 1);
+      if (key0 >= vis.vis) continue;
+      const float mine = lane_sums<4 * HB>(s, lane) * A.scale_log2;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float p = exp2f(x[j] - ref);
-            l[h] += p;
+      for (int h = 0; h < HB; ++h) {
+        float x[4], mx = m[h];
 #pragma unroll
-            for (int i = 0; i < NI; ++i) o[h][i] += key0 + j < vis.vis ? p * vr[j][i] : 0.f;
-          }
+        for (int j = 0; j < 4; ++j) {
+          x[j] = __shfl_sync(0xffffffffu, mine, (j * HB + h) * (32 / (4 * HB)));
+          if (key0 + j >= vis.vis) x[j] = -INFINITY;
+          mx = fmaxf(mx, x[j]);
+        }
+        const float ref = mx == -INFINITY ? 0.f : mx;
+        const float alpha = exp2f(m[h] - ref);
+        m[h] = mx;
+        l[h] *= alpha;
+#pragma unroll
+        for (int e = 0; e < NI; ++e) o[h][e] *= alpha;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float p = exp2f(x[j] - ref);
+          l[h] += p;
+#pragma unroll
+          for (int e = 0; e < NI; ++e) o[h][e] += key0 + j < vis.vis ? p * vc[j][e] : 0.f;
         }
       }
     }
@@ -388,6 +398,7 @@ __global__ void __launch_bounds__(kThreads) decode_simt(const __grid_constant__ 
     if (S.base + S.units >= S.end) break;
     share_next(A, S);
   }
+  finish_idle<float>(A);
 }
 
 // ---------------------------------------------------------------- bf16: matrix instructions
@@ -486,13 +497,13 @@ __global__ void __launch_bounds__(kThreads, (MmaCfg<DH, WIDE>::CTAS)) decode_mma
   constexpr int ROWS = 32 / LANES;             // rows of one copy instruction
   constexpr int NS = C::STAGES;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t scan[4];
+  __shared__ int64_t scan[8];
   __shared__ float sm_m[4][16], sm_l[4][16];
-  launch_dependents();
   Share share;
-  int64_t total;
-  int ctas;
-  if (!share_begin(A, share, scan, &total, &ctas)) return;
+  if (!share_begin(A, share, scan)) {
+    finish_idle<__nv_bfloat16>(A);
+    return;
+  }
   const int64_t share0 = share.u;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
   const uint32_t ring = smem_u32(smem) + warp * NS * C::STAGE;
@@ -697,77 +708,116 @@ __global__ void __launch_bounds__(kThreads, (MmaCfg<DH, WIDE>::CTAS)) decode_mma
     }
     at.next_piece(A, false);
   }
+  finish_idle<__nv_bfloat16>(A);
 }
 
 // ---------------------------------------------------------------- the join
-// One block per (sequence, query head). Its warps take every eighth part, the lanes four
-// elements each; sums over the warps in a fixed order.
-template <typename T>
+// Units (of one pair each) before sequence b, and of all sequences, by the block's threads.
+__device__ __forceinline__ void count_units(const DecodeArgs& A, int b, int64_t* before, int64_t* all,
+                                            int64_t* scan) {
+  int64_t lo = 0, sum = 0;
+  for (int i = threadIdx.x; i < A.n_seqs; i += kJoinThreads) {
+    const int u = units_of(A, i);
+    sum += u;
+    if (i < b) lo += u;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    lo += __shfl_xor_sync(0xffffffffu, lo, o);
+    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  }
+  if ((threadIdx.x & 31) == 0) {
+    scan[threadIdx.x >> 5] = lo;
+    scan[8 + (threadIdx.x >> 5)] = sum;
+  }
+  __syncthreads();
+  *before = *all = 0;
+  for (int w = 0; w < kJoinThreads / 32; ++w) {
+    *before += scan[w];
+    *all += scan[8 + w];
+  }
+}
+
+// The blocks that go by pairs (few pairs, of many parts): x the pair, y the query head of its block
+// of heads, the eight warps every eighth part each. The blocks that go by cuts: x the pair that CTA
+// x's share ends in, if it goes on in CTA x + 1 and begins in CTA x; two warps a head, four heads
+// at a time. The lanes take four elements each; every sum is taken in a fixed order. (Most blocks
+// start when the main kernel's end leaves room for them, so few blocks matter more than short
+// ones. In all, by pairs and by cuts: one sequence of 700 keys, 8 pairs, 7.7 and 9.1 us; 16
+// sequences of 8000, 32/1 heads, 27 and 43 us; 1000 sequences of 100, 32/8 heads, 230 and 112 us.)
+template <typename T, bool PAIRS>
 __global__ void __launch_bounds__(kJoinThreads) decode_join(const __grid_constant__ DecodeArgs A, int grid) {
-  __shared__ int64_t scan[kJoinThreads / 32];
-  __shared__ float wt[kMaxCtas + 1];
-  __shared__ float red[kJoinThreads / 32];
-  __shared__ float sums[kJoinThreads / 32][128];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, dh = A.dh;
-  const int b = blockIdx.x / A.hq, h = blockIdx.x % A.hq;
-  const int hk = h / A.group, g = h % A.group, blk = g / A.block_heads, row = g % A.block_heads;
-  int64_t before, sum;
-  count_units(A, b, &before, &sum, scan);
-  // (the main kernel does not come by a sequence whose length is negative: reported here)
-  const int n = (visible(A, b, tid == 0).vis + kUnit - 1) / kUnit, per = A.hkv * A.blocks_per_kv;
-  const int64_t total = sum * per;
-  T* out = static_cast<T*>(A.out) + (static_cast<int64_t>(b) * A.hq + h) * dh;
+  constexpr int ROWS = PAIRS ? 1 : 4, WARPS = kJoinThreads / 32 / ROWS;
+  __shared__ int64_t scan[16];
+  __shared__ float sums[kJoinThreads / 32][128], sm_l[kJoinThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, dh = A.dh;
+  Share S;
+  int64_t total;
+  int ctas;
+  bool some;
+  if constexpr (PAIRS) {
+    const int per = A.hkv * A.blocks_per_kv;
+    S.b = blockIdx.x / per;
+    S.pair = blockIdx.x - S.b * per;
+    S.units = units_of(A, S.b);
+    int64_t before;
+    count_units(A, S.b, &before, &total, scan);
+    total *= per;
+    ctas = active_ctas(total, grid);
+    S.base = before * per + static_cast<int64_t>(S.pair) * S.units;
+    some = S.units > 0;
+  } else {  // the pair of the next CTA's first unit
+    some = share_of<kJoinThreads>(A, blockIdx.x + 1, grid, S, scan, &total, &ctas) && S.base < S.u;
+  }
+  int c0 = 0, c1 = 0;
+  if (some) {
+    c0 = cta_of(total, ctas, S.base);
+    c1 = cta_of(total, ctas, S.base + S.units - 1);
+  }
   wait_for_main();  // in every block: what follows in the stream waits for this kernel alone
-  if (n == 0) {
-    for (int d = tid; d < dh; d += kJoinThreads) stv<T>(out + d, 0.f);
-    if (tid == 0) A.lse[static_cast<int64_t>(b) * A.hq + h] = -INFINITY;
-    return;
-  }
-  const int ctas = active_ctas(total, grid);
-  const int64_t u0 = before * per + static_cast<int64_t>(hk * A.blocks_per_kv + blk) * n;
-  const int c0 = cta_of(total, ctas, u0), c1 = cta_of(total, ctas, u0 + n - 1);
-  if (c0 == c1) return;  // one CTA had the whole pair
-  const int parts = c1 - c0 + 1;
-  auto part = [&](int i) {  // the pair is the first of a CTA's share, or its last
-    return part_of(A, c0 + i, u0 <= first_unit(total, ctas, c0 + i) ? 0 : 1) + row * (dh + 2);
-  };
-  float mx = -INFINITY;
-  for (int i = tid; i < parts; i += kJoinThreads) mx = fmaxf(mx, wt[i] = part(i)[dh]);
+  if (c0 == c1 || (!PAIRS && c0 != static_cast<int>(blockIdx.x))) return;  // not cut, or cut earlier
+  const int hk = S.pair / A.blocks_per_kv, blk = S.pair - hk * A.blocks_per_kv;
+  const int heads = min(A.block_heads, A.group - blk * A.block_heads), parts = c1 - c0 + 1;
+  for (int row0 = PAIRS ? blockIdx.y : 0; row0 < heads; row0 += PAIRS ? heads : ROWS) {
+    const int row = row0 + warp / WARPS, w = warp % WARPS;
+    const bool mine = row < heads;
+    auto part = [&](int i) {  // the pair is the first of a CTA's share, or its last
+      return part_of(A, c0 + i, S.base <= first_unit(total, ctas, c0 + i) ? 0 : 1) + row * (dh + 2);
+    };
+    float mx = -INFINITY, l = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+    if (mine) {  // every warp of a head takes the maximum of all parts
+      for (int i = lane; i < parts; i += 32) mx = fmaxf(mx, part(i)[dh]);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  if (lane == 0) red[warp] = mx;
-  __syncthreads();
-  for (int w = 0; w < kJoinThreads / 32; ++w) mx = fmaxf(mx, red[w]);
-  __syncthreads();
-  const float ref = mx == -INFINITY ? 0.f : mx;
-  float l = 0.f;
-  for (int i = tid; i < parts; i += kJoinThreads) {
-    wt[i] = exp2f(wt[i] - ref);
-    l += wt[i] * part(i)[dh + 1];
-  }
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const float ref = mx == -INFINITY ? 0.f : mx;
+#pragma unroll 4
+      for (int i = w; i < parts; i += WARPS) {
+        const float* p = part(i);
+        const float f = exp2f(p[dh] - ref);
+        l += f * p[dh + 1];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  if (lane == 0) red[warp] = l;
-  __syncthreads();
-  l = 0.f;
-  for (int w = 0; w < kJoinThreads / 32; ++w) l += red[w];
-  float x[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int i = warp; i < parts; i += kJoinThreads / 32) {
-    const float* p = part(i);
-    const float f = wt[i];
+        for (int e = 0; e < 4; ++e)
+          if (lane + 32 * e < dh) x[e] += f * p[lane + 32 * e];
+      }
+    }
+    if (lane == 0) sm_l[warp] = l;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (lane + 32 * e < dh) x[e] += f * p[lane + 32 * e];
+    for (int e = 0; e < 4; ++e) sums[warp][lane + 32 * e] = x[e];
+    __syncthreads();
+    if (mine && w == 0) {
+      const int h = hk * A.group + blk * A.block_heads + row;
+      l = 0.f;
+      for (int k = 0; k < WARPS; ++k) l += sm_l[warp + k];
+      T* out = static_cast<T*>(A.out) + (static_cast<int64_t>(S.b) * A.hq + h) * dh;
+      for (int d = lane; d < dh; d += 32) {
+        float s = 0.f;
+        for (int k = 0; k < WARPS; ++k) s += sums[warp + k][d];
+        stv<T>(out + d, s * inverse(l));
+      }
+      if (lane == 0) store_lse(A, S.b, h, mx, l);
+    }
+    __syncthreads();
   }
-#pragma unroll
-  for (int e = 0; e < 4; ++e) sums[warp][lane + 32 * e] = x[e];
-  __syncthreads();
-  for (int d = tid; d < dh; d += kJoinThreads) {
-    float s = 0.f;
-    for (int w = 0; w < kJoinThreads / 32; ++w) s += sums[w][d];
-    stv<T>(out + d, s * inverse(l));
-  }
-  if (tid == 0) store_lse(A, b, h, mx, l);
 }
 
 // Query heads that share one read of a K/V head: on the CUDA cores a power of two up to 8 (the
@@ -779,7 +829,7 @@ int heads_of_block(int dtype, int group) {
   return (group + blocks - 1) / blocks;
 }
 
-int ctas_per_sm(int dtype, int dh) { return dtype == RA_F32 ? 2 : dh == 64 ? MmaCfg<64, false>::CTAS : MmaCfg<128, false>::CTAS; }
+int ctas_per_sm(int dtype, int dh) { return dtype == RA_F32 ? 3 : dh == 64 ? MmaCfg<64, false>::CTAS : MmaCfg<128, false>::CTAS; }
 
 template <int DH, bool WIDE>
 cudaError_t launch_mma(const DecodeArgs& A, int grid, cudaStream_t st) {
@@ -789,6 +839,17 @@ cudaError_t launch_mma(const DecodeArgs& A, int grid, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   decode_mma<DH, WIDE><<<grid, kThreads, C::SMEM, st>>>(A);
   return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_join(cudaLaunchConfig_t& cfg, const DecodeArgs& A, int grid) {
+  const int64_t pairs = static_cast<int64_t>(A.n_seqs) * A.hkv * A.blocks_per_kv;
+  if (pairs * A.block_heads <= 4 * grid) {
+    cfg.gridDim = dim3(static_cast<unsigned>(pairs), A.block_heads);
+    return cudaLaunchKernelEx(&cfg, decode_join<T, true>, A, grid);
+  }
+  cfg.gridDim = dim3(grid - 1);
+  return cudaLaunchKernelEx(&cfg, decode_join<T, false>, A, grid);
 }
 
 cudaError_t launch(DecodeArgs& A, int dtype, cudaStream_t st) {
@@ -815,13 +876,11 @@ cudaError_t launch(DecodeArgs& A, int dtype, cudaStream_t st) {
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(A.n_seqs * A.hq);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = st;
   cfg.attrs = &early;
   cfg.numAttrs = 1;
-  return dtype == RA_F32 ? cudaLaunchKernelEx(&cfg, decode_join<float>, A, grid)
-                         : cudaLaunchKernelEx(&cfg, decode_join<__nv_bfloat16>, A, grid);
+  return dtype == RA_F32 ? launch_join<float>(cfg, A, grid) : launch_join<__nv_bfloat16>(cfg, A, grid);
 }
 
 size_t workspace_of(const ra_paged_cache* c, int hq) {
