@@ -340,9 +340,10 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // ---------------------------------------------------------------- head size 64 or 128, 16-byte loads
-// A head is held by LANES lanes, each with two 16-byte pieces: c-th of the first half and c-th
-// of the second half of the head, so that both members of a rotated pair (half-split or
-// interleaved) are in one thread, and the HEADS heads of a warp are loaded 128 bytes at a time.
+// A head is held by LANES lanes, each with two 16-byte pieces: the c-th of the first half and the
+// c-th of the second half of the rotated elements, so that both members of a rotated pair are in
+// one thread (interleaved pairs are anyway), or two neighbouring pieces of what is not rotated.
+// The HEADS heads of a warp are loaded together.
 template <typename T, int DH>
 struct Vec {
   static constexpr int N = 16 / sizeof(T);          // elements of a piece
@@ -355,17 +356,28 @@ template <typename T, int DH>
 struct Piece {  // a lane's two pieces, as loaded
   uint4 a, b;
 };
+struct Place {
+  int a, b;  // first elements of a lane's two pieces
+};
+template <typename T, int DH, bool INTER>
+__device__ __forceinline__ Place place_of(const HeadArgs& A, int c) {
+  constexpr int N = Vec<T, DH>::N;
+  const int rd = A.rope.rotary_dim, turned = rd / 2 / N;  // lanes with pairs (not interleaved)
+  if (INTER || rd == 0) return {c * N, DH / 2 + c * N};
+  if (c < turned) return {c * N, rd / 2 + c * N};
+  return {rd + (c - turned) * 2 * N, rd + (c - turned) * 2 * N + N};
+}
 template <typename T, int DH>
-__device__ __forceinline__ Piece<T, DH> load_piece(const T* head, int c) {
+__device__ __forceinline__ Piece<T, DH> load_piece(const T* head, Place at) {
   Piece<T, DH> p;
-  p.a = *reinterpret_cast<const uint4*>(head + c * Vec<T, DH>::N);
-  p.b = *reinterpret_cast<const uint4*>(head + DH / 2 + c * Vec<T, DH>::N);
+  p.a = *reinterpret_cast<const uint4*>(head + at.a);
+  p.b = *reinterpret_cast<const uint4*>(head + at.b);
   return p;
 }
 template <typename T, int DH>
-__device__ __forceinline__ void store_piece(T* head, int c, const Piece<T, DH>& p) {
-  *reinterpret_cast<uint4*>(head + c * Vec<T, DH>::N) = p.a;
-  *reinterpret_cast<uint4*>(head + DH / 2 + c * Vec<T, DH>::N) = p.b;
+__device__ __forceinline__ void store_piece(T* head, Place at, const Piece<T, DH>& p) {
+  *reinterpret_cast<uint4*>(head + at.a) = p.a;
+  *reinterpret_cast<uint4*>(head + at.b) = p.b;
 }
 
 __device__ __forceinline__ void widen(const uint4& v, float (&x)[4]) {
@@ -402,7 +414,7 @@ __device__ __forceinline__ void piece_angles(const HeadArgs& A, int64_t pos, int
   for (int k = 0; k < V::PER; ++k) {
     const int j = (sub * V::PER + k) % V::N;
     const int pair = !INTER ? c * V::N + j : j < V::N / 2 ? c * V::N / 2 + j : DH / 4 + c * V::N / 2 + j - V::N / 2;
-    mine[k] = cos_sin(A.rope.turns[pair], pos);
+    mine[k] = pair < A.rope.rotary_dim / 2 ? cos_sin(A.rope.turns[pair], pos) : make_float2(1.f, 0.f);
   }
 #pragma unroll
   for (int j = 0; j < V::N; ++j) {
@@ -452,16 +464,16 @@ __device__ __forceinline__ void head_run(const HeadArgs& A, const T* __restrict_
                                          const float (&cs)[Vec<T, DH>::N], const float (&sn)[Vec<T, DH>::N],
                                          F&& prepare) {
   using V = Vec<T, DH>;
-  const int c = lane % V::LANES, sub = lane / V::LANES;
-  const int runs = (heads + V::HEADS - 1) / V::HEADS;
+  const Place at = place_of<T, DH, INTER>(A, lane % V::LANES);
+  const int sub = lane / V::LANES, runs = (heads + V::HEADS - 1) / V::HEADS;
   Piece<T, DH> wp;
-  if (w != nullptr) wp = load_piece<T, DH>(w, c);
+  if (w != nullptr) wp = load_piece<T, DH>(w, at);
   for (int i0 = first; i0 < runs; i0 += step * U) {
     Piece<T, DH> p[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int h = (i0 + u * step) * V::HEADS + sub;
-      if (h < heads) p[u] = load_piece<T, DH>(src + h * DH, c);
+      if (h < heads) p[u] = load_piece<T, DH>(src + h * DH, at);
     }
     if (i0 == first) prepare();
 #pragma unroll
@@ -489,7 +501,7 @@ __device__ __forceinline__ void head_run(const HeadArgs& A, const T* __restrict_
         p[u].a = narrow(a);
         p[u].b = narrow(b);
       }
-      if (h < heads) store_piece<T, DH>(dst + h * dst_head, c, p[u]);
+      if (h < heads) store_piece<T, DH>(dst + h * dst_head, at, p[u]);
     }
   }
 }
@@ -512,7 +524,7 @@ __global__ void __launch_bounds__(kThreads)
   if (tok.idle) {
     for (int h = part * V::HEADS + lane / V::LANES; h < A.hq; h += parts * V::HEADS) {
       Piece<T, DH> zero = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-      store_piece<T, DH>(qo + h * DH, lane % V::LANES, zero);
+      store_piece<T, DH>(qo + h * DH, place_of<T, DH, INTER>(A, lane % V::LANES), zero);
     }
     return;
   }
@@ -546,9 +558,10 @@ __device__ __forceinline__ void head_run_bwd(const HeadArgs& A, const T* __restr
                                              float (&acc_a)[Vec<T, DH>::N], float (&acc_b)[Vec<T, DH>::N],
                                              F&& prepare) {
   using V = Vec<T, DH>;
-  const int c = lane % V::LANES, sub = lane / V::LANES;
+  const Place at = place_of<T, DH, INTER>(A, lane % V::LANES);
+  const int sub = lane / V::LANES;
   Piece<T, DH> wp;
-  if (w != nullptr) wp = load_piece<T, DH>(w, c);
+  if (w != nullptr) wp = load_piece<T, DH>(w, at);
   for (int h0 = sub; h0 - sub < heads; h0 += V::HEADS * U) {
     Piece<T, DH> g[U], p[U];
 #pragma unroll
@@ -556,8 +569,8 @@ __device__ __forceinline__ void head_run_bwd(const HeadArgs& A, const T* __restr
       const int h = h0 + u * V::HEADS;
       g[u].a = g[u].b = p[u].a = p[u].b = make_uint4(0u, 0u, 0u, 0u);
       if (h < heads) {
-        g[u] = load_piece<T, DH>(dy + h * DH, c);
-        if (w != nullptr) p[u] = load_piece<T, DH>(x + h * DH, c);
+        g[u] = load_piece<T, DH>(dy + h * DH, at);
+        if (w != nullptr) p[u] = load_piece<T, DH>(x + h * DH, at);
       }
     }
     if (h0 == sub) prepare();
@@ -601,7 +614,7 @@ __device__ __forceinline__ void head_run_bwd(const HeadArgs& A, const T* __restr
       }
       g[u].a = narrow(a);
       g[u].b = narrow(b);
-      if (h < heads) store_piece<T, DH>(dx + h * DH, c, g[u]);
+      if (h < heads) store_piece<T, DH>(dx + h * DH, at, g[u]);
     }
   }
 }
@@ -630,6 +643,7 @@ __global__ void __launch_bounds__(kBwdThreads, 4)
                                   acc[1][0], acc[1][1], []() {});
   }
   if (qw == nullptr) return;
+  const Place at = place_of<T, DH, INTER>(A, lane % V::LANES);
 #pragma unroll
   for (int which = 0; which < 2; ++which)
 #pragma unroll
@@ -639,7 +653,7 @@ __global__ void __launch_bounds__(kBwdThreads, 4)
         float x = acc[which][half][j];  // over the heads of the warp: lanes with the same pieces
 #pragma unroll
         for (int o = V::LANES; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-        if (lane < V::LANES) sums[warp][which][half * (DH / 2) + lane * V::N + j] = x;
+        if (lane < V::LANES) sums[warp][which][(half ? at.b : at.a) + j] = x;
       }
   __syncthreads();
   for (int i = threadIdx.x; i < 2 * DH; i += kBwdThreads) {
@@ -716,7 +730,7 @@ void fill_rows(const ra_problem* p, RingRows* R) {
 }
 
 void fill_args(HeadArgs* A, const ra_rope* rope, float eps, int hq, int hkv, int dh, int n_rows) {
-  if (rope != nullptr) A->rope = *rope; else A->rope.rotary_dim = 0;
+  if (rope != nullptr) A->rope = *rope; else A->rope.rotary_dim = A->rope.interleaved = 0;
   A->eps = eps;
   A->hq = hq;
   A->hkv = hkv;
@@ -733,13 +747,13 @@ int parts_of(int n_rows, int runs) {
   return want < 1 ? 1 : want > runs ? runs : want;
 }
 
-// Whether the 16-byte kernels can take a call: a whole-head rotation or none, and rows that all
-// start on 16 bytes. (Measured at 131072 tokens, 32/8 heads of 128, bf16, forward and backward:
-// 16-byte kernels 1.2 ms, one warp a head 10.6 ms.)
+// Whether the 16-byte kernels can take a call: heads of 64 or 128, a rotation that falls into whole
+// pieces, and rows that all start on 16 bytes. (Measured at 131072 tokens, 32/8 heads of 128,
+// bf16, forward and backward: 16-byte kernels 1.15 ms, the others 3.9 ms.)
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 bool can_vec(const HeadArgs& A, int elem) {
   auto rows16 = [&](int64_t stride) { return stride * elem % 16 == 0; };
-  return (A.dh == 64 || A.dh == 128) && (A.rope.rotary_dim == 0 || A.rope.rotary_dim == A.dh) &&
+  return (A.dh == 64 || A.dh == 128) && (A.rope.interleaved || A.rope.rotary_dim % (32 / elem) == 0) &&
          rows16(A.q_stride) && rows16(A.k_stride) && rows16(A.v_stride) && rows16(A.kv_head);
 }
 
@@ -763,7 +777,7 @@ cudaError_t launch_fwd(const HeadArgs& A, const Rows& R, const void* qw, const v
                        void* v_out, bool aligned, cudaStream_t st) {
   if (aligned && can_vec(A, sizeof(T)) && aligned16(qw) && aligned16(kw) && aligned16(q) && aligned16(k) &&
       aligned16(v) && aligned16(q_out) && aligned16(k_out) && aligned16(v_out)) {
-    const bool inter = A.rope.rotary_dim > 0 && A.rope.interleaved;
+    const bool inter = A.rope.interleaved;
     if (A.dh == 128)
       return inter ? fwd_vec<T, 128, true, Rows, CACHE>(A, R, qw, kw, q, k, v, q_out, k_out, v_out, st)
                    : fwd_vec<T, 128, false, Rows, CACHE>(A, R, qw, kw, q, k, v, q_out, k_out, v_out, st);
@@ -797,7 +811,7 @@ cudaError_t launch_bwd(const HeadArgs& A, const RingRows& R, const void* qw, con
   if (can_vec(A, sizeof(T)) && aligned16(qw) && aligned16(kw) && aligned16(q) && aligned16(k) &&
       aligned16(dq_out) && aligned16(dk_out) && aligned16(dq) && aligned16(dk)) {
     blocks = blocks_for(A.n_rows, kBwdThreads / 32, kHeadBwdBlocks);
-    const bool inter = A.rope.rotary_dim > 0 && A.rope.interleaved;
+    const bool inter = A.rope.interleaved;
     if (A.dh == 128) {
       if (inter) bwd_vec<T, 128, true>(blocks, A, R, qw, kw, q, k, dq_out, dk_out, dq, dk, partial, st);
       else bwd_vec<T, 128, false>(blocks, A, R, qw, kw, q, k, dq_out, dk_out, dq, dk, partial, st);

@@ -74,6 +74,12 @@ NORM_CASES = [
     (F32, "basic", 1, [17], False, 3, 3, 33, 2, False),
     (F32, "basic", 5, [25, 5], True, 5, 1, 1, None, False),
     (F32, "zigzag", 1, [10], False, 2, 1, 64, 64, True),
+    (BF16, "zigzag", 1, [70], False, 5, 5, 128, 16, False),  # rotations of part of the head, in whole
+    (BF16, "basic", 2, [12], False, 3, 1, 128, 112, False),  # 16-byte pieces
+    (BF16, "basic", 2, [12], False, 3, 1, 64, 22, True),
+    (BF16, "basic", 2, [12], False, 3, 1, 64, 22, False),    # and not
+    (F32, "stripe", 2, [12], False, 9, 3, 128, 24, False),
+    (F32, "stripe", 2, [12], False, 9, 3, 64, 6, True),
 ]
 
 
