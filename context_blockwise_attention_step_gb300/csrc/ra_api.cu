@@ -221,6 +221,12 @@ size_t delta_bytes(const ra_problem* p) {
 // one 256-byte block.
 size_t sched_bytes(const ra_problem* p) { return use_tc(p) ? 256 : 0; }
 
+int64_t total_rows(const ra_problem* p) {
+  int64_t rows = 0;
+  for (int64_t x : lengths_of(p)) rows += x;
+  return rows;
+}
+
 // The window as the plans carry it: one that reaches over the longest sequence hides nothing,
 // and the ring kernels run as without one.
 int effective_window(const ra_problem* p, int window) {
@@ -245,10 +251,15 @@ Plan* make_window_plan(const ra_problem* p, int which, int window, int sinks) {
   Plan* P = make_plan(p, which, 0, p->D, -1, which == 0 && p->dtype == RA_F32);
   P->window = effective_window(p, window);
   P->sinks = P->window ? sinks : 0;
+  int longest = 0;
+  for (int i = 0; i < P->n_seqs; ++i) longest = std::max(longest, P->seq[i].L);
+  // A sink's rows in one shard: every D-th token, or all of them if the shard is as long.
+  P->sink_stride = P->layout == RA_LAYOUT_STRIPE ? ra::ceil_div(P->sinks, P->D) : std::min(P->sinks, longest);
   // Tensor cores: a sink item as long as a K/V tile's window item, the tiles of the window, 8 at
   // least, since an item's loads and stores cost about one query tile. CUDA cores: a warp for
-  // every 128 queries.
-  P->sink_chunk = use_tc(p) ? std::max(8, P->window / ra::kQTileRows + 1) : 1;
+  // every 128 queries, or a 64th of the longest sequence's.
+  P->sink_chunk = use_tc(p) ? std::max(8, P->window / ra::kQTileRows + 1)
+                            : std::max(1, ra::ceil_div(ra::ceil_div(longest, ra::kQTileRows) * P->D, 64));
   return P;
 }
 
@@ -257,7 +268,8 @@ size_t sink_bytes(const ra_problem* p, int window, int sinks) {
   if (sinks == 0) return 0;
   PlanHolder P(make_window_plan(p, 2, window, sinks));
   if (P.p->window == 0) return 0;
-  return align256(static_cast<size_t>(ra::window_bwd_items(*P.p)) * 2 * sinks * p->head_dim * sizeof(float));
+  return align256(static_cast<size_t>(ra::window_bwd_items(*P.p)) * 2 * P.p->sink_stride * p->head_dim *
+                  sizeof(float));
 }
 
 size_t dq_acc_bytes(const ra_problem* p) {
@@ -459,6 +471,7 @@ int ra_block_attn_bwd(const ra_problem* p, int rank, int step, const void* q, co
 
 size_t ra_window_workspace_bytes(const ra_problem* p, int window, int sinks, int which) try {
   if (validate_window(p, window, sinks) != RA_OK) return 0;
+  if (effective_window(p, window) == 0) return which == 0 || which == 1 ? ra_workspace_bytes(p, which) : 0;
   if (which == 0) return sched_bytes(p);
   if (which == 1) return delta_bytes(p) + sched_bytes(p) + sink_bytes(p, window, sinks);
   return 0;
@@ -470,6 +483,7 @@ int ra_window_attn_fwd(const ra_problem* p, int window, int sinks, const void* q
                        const void* v, void* out, float* lse, void* workspace, size_t workspace_bytes,
                        void* stream) try {
   if (int e = validate_window(p, window, sinks)) return e;
+  if (total_rows(p) == 0) return ok();
   if (effective_window(p, window) == 0)
     return ra_ring_attn_fwd(p, q, k, v, out, lse, workspace, workspace_bytes, stream);
   if (!q || !k || !v || !out || !lse) return fail(RA_ERR_INVALID_ARG, "null tensor pointer");
@@ -495,6 +509,7 @@ int ra_window_attn_bwd(const ra_problem* p, int window, int sinks, const void* q
                        const void* v, const void* out, const float* lse, const void* dout, void* dq,
                        void* dk, void* dv, void* workspace, size_t workspace_bytes, void* stream) try {
   if (int e = validate_window(p, window, sinks)) return e;
+  if (total_rows(p) == 0) return ok();
   if (effective_window(p, window) == 0)
     return ra_ring_attn_bwd(p, q, k, v, out, lse, dout, dq, dk, dv, workspace, workspace_bytes, stream);
   if (!q || !k || !v || !out || !lse || !dout || !dq || !dk || !dv)

@@ -223,7 +223,7 @@ __device__ __forceinline__ bool win_for_each_qtile(const Plan& P, const WinItem&
 
 // Slot row `row` of the item's sink sums, dk (which 0) or dv (1).
 __device__ __forceinline__ float* sink_row(const Plan& P, const WinItem& x, int row, int which) {
-  return P.sink_sums + ((static_cast<int64_t>(x.slot) * 2 + which) * P.sinks + row) * P.head_dim;
+  return P.sink_sums + ((static_cast<int64_t>(x.slot) * 2 + which) * P.sink_stride + row) * P.head_dim;
 }
 
 __device__ __forceinline__ void store_row32_f32(float* dst, const uint32_t (&r)[32], float mul) {

@@ -32,7 +32,7 @@ cudaError_t launch_bwd_dq_tc(const Plan& P, const void* q, const void* k, const 
                              const void* dout, const float* lse, const float* delta, void* dq,
                              cudaStream_t st);
 // Windowed K/V pass: numbers the plan's items and sink slots (returns the slots, each of 2 *
-// sinks * head_dim floats of P.sink_sums); dk and dv, the sinks' rows summed from the slots.
+// sink_stride * head_dim floats of P.sink_sums); dk and dv, the sinks' rows summed from the slots.
 int window_bwd_items(Plan& P);
 cudaError_t launch_window_bwd_tc(const Plan& P, const void* q, const void* k, const void* v,
                                  const void* dout, const float* lse, const float* delta, void* dk,

@@ -43,6 +43,7 @@ struct Plan {
   int32_t bwd_kt_inner;          // backward items: K/V tiles innermost (see decode_bwd)
   int32_t window, sinks;         // sliding window (0: none); first tokens that stay visible
   int32_t sink_chunk;            // windowed K/V pass: query tiles of a sink item
+  int32_t sink_stride;           // most sink rows of a shard: rows of a slot
   float scale, scale_log2;
   float dq_mul;                  // factor on dS K before it is added to the dq sums
   uint64_t timeout_ns;

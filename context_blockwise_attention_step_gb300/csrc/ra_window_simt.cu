@@ -9,8 +9,8 @@
 // (2048 tokens, 4/2 heads of 64, window 300): one key at a time 310 us forward and 2.66 ms
 // backward, eight at a time 123 us and 253 us.
 //
-// A sink is seen by the whole sequence: its far queries go, 128 of a rank at a time, to warps of
-// their own, which leave float32 sums in the slots that ra_plan.h describes.
+// A sink is seen by the whole sequence: its far queries go, a chunk of a rank at a time, to warps
+// of their own, which leave float32 sums in the slots that ra_plan.h describes.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kThreads)
   const SeqDesc& sd = P.seq[blockIdx.y];
   const int L = sd.L, dh = P.head_dim, lane = threadIdx.x & 31;
   const int chunks = sink_chunks(P, L);
-  const uint32_t far_units = static_cast<uint32_t>(sink_items_of(P, L)) * P.sinks;
+  const uint32_t far_units = static_cast<uint32_t>(sink_items_of(P, L)) * P.sink_stride;
   const uint32_t units = far_units + static_cast<uint32_t>(P.D) * L * P.hkv;
   for (uint32_t u = blockIdx.x * kWarps + (threadIdx.x >> 5); u < units; u += gridDim.x * kWarps) {
     int j, b, hk, far_r = -1, chunk = 0;
@@ -217,8 +217,8 @@ __global__ void __launch_bounds__(kThreads)
       x /= chunks;
       far_r = x % P.D;
       x /= P.D;
-      b = x % P.sinks;
-      j = x / P.sinks;
+      b = x % P.sink_stride;
+      j = x / P.sink_stride;
       if (b >= sink_rows(P, L, j)) continue;
     } else {
       uint32_t x = u - far_units;
@@ -277,8 +277,8 @@ __global__ void __launch_bounds__(kThreads)
       const int d = lane + 32 * i;
       if (d < dh) {
         if (sink) {
-          P.sink_sums[((slot * 2 + 0) * P.sinks + b) * dh + d] = dka[i] * P.scale;
-          P.sink_sums[((slot * 2 + 1) * P.sinks + b) * dh + d] = dva[i];
+          P.sink_sums[((slot * 2 + 0) * P.sink_stride + b) * dh + d] = dka[i] * P.scale;
+          P.sink_sums[((slot * 2 + 1) * P.sink_stride + b) * dh + d] = dva[i];
         } else {
           stf(dk + at + d, dka[i] * P.scale);
           stf(dv + at + d, dva[i]);
@@ -298,10 +298,10 @@ __global__ void __launch_bounds__(kThreads)
   if (j >= sink_shards(P, s.L) || row >= sink_rows(P, s.L, j) || threadIdx.x >= 2 * dh) return;
   const int which = threadIdx.x / dh, d = threadIdx.x % dh, n = sink_slots(P, s.L);
   const int64_t slot = sink_slot(P, s, j, hk, 0);
-  const float* src = P.sink_sums + ((slot * 2 + which) * P.sinks + row) * dh + d;
+  const float* src = P.sink_sums + ((slot * 2 + which) * P.sink_stride + row) * dh + d;
   float sum = 0.f;
 #pragma unroll 8
-  for (int i = 0; i < n; ++i) sum += src[static_cast<int64_t>(i) * 2 * P.sinks * dh];
+  for (int i = 0; i < n; ++i) sum += src[static_cast<int64_t>(i) * 2 * P.sink_stride * dh];
   const int64_t krow = s.row_off + static_cast<int64_t>(j) * P.shard_stride + row;
   stf((which ? dv : dk) + (krow * P.hkv + hk) * dh + d, sum);
 }
@@ -332,7 +332,7 @@ cudaError_t bwd(const Plan& P, const void* q, const void* k, const void* v, cons
           *do_ = static_cast<const T*>(dout);
   int64_t far = 0;
   for (int i = 0; i < P.n_seqs; ++i) {
-    const int64_t f = static_cast<int64_t>(sink_items_of(P, P.seq[i].L)) * P.sinks;
+    const int64_t f = static_cast<int64_t>(sink_items_of(P, P.seq[i].L)) * P.sink_stride;
     far = f > far ? f : far;
   }
   window_dkv_simt<T, NI><<<grid_of(P, far + static_cast<int64_t>(P.D) * max_len(P) * P.hkv), kThreads, 0, st>>>(
@@ -377,7 +377,7 @@ cudaError_t launch_sink_sum(const Plan& P, int dtype, void* dk, void* dv, cudaSt
     const int n = sink_shards(P, P.seq[i].L);
     shards = n > shards ? n : shards;
   }
-  const dim3 grid(P.sinks, shards * P.hkv, P.n_seqs);
+  const dim3 grid(P.sink_stride, shards * P.hkv, P.n_seqs);
   if (dtype == RA_F32)
     sink_sum_kernel<float><<<grid, kThreads, 0, st>>>(P, static_cast<float*>(dk), static_cast<float*>(dv));
   else

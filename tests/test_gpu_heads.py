@@ -450,3 +450,47 @@ def test_empty_batches():
     assert ra.qk_norm_rope_fwd(q, q[:, :2], prob, **how)[0].shape == (0, 4, 64)
     grads = ra.qk_norm_rope_bwd(q, q[:, :2].contiguous(), q, q[:, :2], prob, **how)
     assert (grads[2] == 0).all() and (grads[3] == 0).all()
+
+
+def test_rows_past_32_bit_offsets():
+    """Rows 2^30 elements apart: the last of four starts past 2^31."""
+    wide = torch.empty(4, 1 << 30, device="cuda", dtype=BF16)
+    q, k = wide[:, :512].view(4, 4, 128), wide[:, 512:768].view(4, 2, 128)
+    q.copy_(randn(121, 4, 4, 128))
+    k.copy_(randn(122, 4, 2, 128))
+    prob = ra.make_problem(dtype=BF16, layout="basic", causal=True, D=1, hq=4, hkv=2, head_dim=128, cu_seqlens=[0, 4])
+    w = randn(123, 128)
+    how = dict(q_weight=w, k_weight=w, rope=ra.make_rope(128))
+    for a, b in zip(ra.qk_norm_rope_fwd(q, k, prob, **how), ra.qk_norm_rope_fwd(q.clone(), k.clone(), prob, **how)):
+        assert torch.equal(a, b)
+    g1, g2 = randn(124, 4, 4, 128), randn(125, 4, 2, 128)
+    for a, b in zip(ra.qk_norm_rope_bwd(g1, g2, q, k, prob, **how), ra.qk_norm_rope_bwd(g1, g2, q.clone(), k.clone(), prob, **how)):
+        assert torch.equal(a, b)
+    kp, vp, table = make_pages(126, [4], 16, 2, 128, BF16)
+    cache = ra.make_cache(kp, vp, torch.from_numpy(table).cuda())
+    cu = torch.tensor([0, 4], dtype=torch.int32).cuda()
+    ra.kv_cache_append(q, k, k, cache, cu[1:], cu_new=cu)
+    assert torch.equal(vp[int(table[0, 0]), :4], k)
+
+
+def test_calls_at_once_on_two_streams():
+    """Decodes and windowed attention side by side, each with its own outputs and workspace."""
+    lens = [3000, 5, 700]
+    kp, vp, table = make_pages(131, lens, 16, 2, 128, BF16)
+    cache = ra.make_cache(kp, vp, torch.from_numpy(table).cuda())
+    q = randn(132, 3, 8, 128)
+    lt = torch.tensor(lens, dtype=torch.int32).cuda()
+    x = [randn(133 + i, 1, 1024, h, 128) for i, h in enumerate((8, 2, 2))]
+    prob = ra.make_problem(dtype=BF16, layout="zigzag", causal=True, D=2, hq=8, hkv=2, head_dim=128, batch=1, seqlen=1024)
+    want = ra.paged_attn_decode(q, cache, lt), ra.window_attn_fwd(*x, prob, 100, 3)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = []
+    for _ in range(20):
+        got.append((ra.paged_attn_decode(q, cache, lt, stream=streams[0]), ra.paged_attn_decode(q, cache, lt, stream=streams[1]),
+                    ra.window_attn_fwd(*x, prob, 100, 3, stream=streams[2])))
+    torch.cuda.synchronize()
+    for a, b, c in got:
+        for u, v in zip((*a, *b, *c), (*want[0], *want[0], *want[1])):
+            assert torch.equal(u, v)
+    assert ra.check_device_status() == 0

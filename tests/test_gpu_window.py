@@ -62,6 +62,7 @@ CASES = [
     (F32, "stripe", 2, [200], False, 4, 2, 64, 30, 2),
     (F32, "zigzag", 4, [40, 96, 0, 8], True, 2, 1, 33, 9, 3),
     (F32, "basic", 3, [60, 60], False, 3, 3, 1, 20, 128),
+    (F32, "stripe", 3, [900], False, 2, 1, 32, 50, 100),
 ]
 IDS = [f"{str(c[0])[6:]}_{c[1]}_D{c[2]}_{max(c[3])}_{c[5]}x{c[6]}_dh{c[7]}_w{c[8]}_s{c[9]}" for c in CASES]
 

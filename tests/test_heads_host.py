@@ -190,3 +190,26 @@ def test_window_refusals():
     assert bwd(ws=128) == _abi.RA_ERR_INVALID_ARG
     assert bwd(dq=None) == _abi.RA_ERR_INVALID_ARG
     assert bwd(window=0) == _abi.RA_ERR_INVALID_ARG
+
+
+def test_window_workspace(monkeypatch):
+    """The slots of the sinks' sums stay small beside the tensors: a slot holds the sink rows of one
+    shard, and a sequence has about as many slots as windows, or 64."""
+    rows, hkv, dh = 131072, 8, 128
+    for dt, layout, D in ((torch.bfloat16, "zigzag", 16), (torch.bfloat16, "stripe", 64), (torch.float32, "stripe", 64),
+                          (torch.float32, "basic", 1)):
+        p = _prob(dtype=dt, layout=layout, D=D, hq=32, hkv=hkv, batch=1, seqlen=rows)
+        plain = ra.window_workspace_bytes(p, 1024, 0)
+        kv = 2 * rows * hkv * dh * (2 if dt == torch.bfloat16 else 4)
+        assert 0 < ra.window_workspace_bytes(p, 1024, 128) - plain < kv
+        assert ra.window_workspace_bytes(p, 1024, 4) - plain < kv // 8
+        assert ra.window_workspace_bytes(p, 1024, 4, 0) == ra.workspace_bytes(p, 0)
+    p = _prob()
+    monkeypatch.setenv("RA_BWD", "fused")  # a window over everything is the ring call, with its workspace
+    assert ra.window_workspace_bytes(p, 64, 4, 1) == ra.workspace_bytes(p, 1)
+
+
+def test_window_of_no_tokens():
+    L, p = _abi.lib(), _prob(batch=0, cu_seqlens=[0, 0, 0])
+    assert L.ra_window_attn_fwd(p.ptr, 8, 2, *([None] * 6), 0, None) == _abi.RA_OK
+    assert L.ra_window_attn_bwd(p.ptr, 8, 2, *([None] * 10), 0, None) == _abi.RA_OK
