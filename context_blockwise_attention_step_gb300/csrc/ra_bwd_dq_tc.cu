@@ -507,6 +507,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
           s_phase[buf] ^= 1;
           tc_fence_after();
           uint32_t pp[32], sv2[2][32];
+          bool some[2];  // windowed: the warp's rows see some key of the chunk
           tmem_ld32_nowait(tS + c0, sv2[0]);  // both chunks in flight, one wait
           tmem_ld32_nowait(tS + c0 + 32, sv2[1]);
           tmem_wait_ld();
@@ -515,6 +516,10 @@ __global__ void __launch_bounds__(kDqThreads, 1)
             const int cs = c0 + 32 * ch;
             const uint32_t (&sv)[32] = sv2[ch];
             const uint32_t vis = WIN ? visible_bits(cs, cnt, lo_t, sk_t) : 0u;
+            if constexpr (WIN) {
+              some[ch] = __any_sync(0xffffffffu, vis != 0);
+              if (!some[ch]) continue;
+            }
             const bool full = __all_sync(0xffffffffu, WIN ? vis == 0xffffffffu : cnt >= cs + 32);
             // staged: every FMA, then every exponential, then masking and packing
             uint64_t xv[16];
@@ -548,6 +553,12 @@ __global__ void __launch_bounds__(kDqThreads, 1)
           for (int ch = 0; ch < 2; ++ch) {
             const uint32_t (&dp)[32] = dp2[ch];
             uint32_t o[16];
+            if (WIN && !some[ch]) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = 0;
+              tmem_st16(tS + 32 + c0 / 2 + 16 * ch, o);
+              continue;
+            }
             uint64_t xv[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i)

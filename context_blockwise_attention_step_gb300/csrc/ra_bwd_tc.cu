@@ -292,8 +292,14 @@ __device__ __forceinline__ void transpose8_f4(uint32_t (&r)[32], int t) {
 // warps load and store TMEM.)
 template <int CH, bool kWithDQ, bool WIN = false>
 __device__ __forceinline__ void ds_from(const uint32_t (&dp)[32], uint32_t tY, int c0, const float* dl,
-                                        const uint32_t (&pp)[32], uint8_t* ds_row, int row) {
+                                        const uint32_t (&pp)[32], uint8_t* ds_row, int row, bool some = true) {
   const int cs = c0 + 32 * CH;
+  if (WIN && !some) {  // p_from's
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      *reinterpret_cast<uint4*>(ds_row + (((4 * CH + q) ^ (row & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+    return;
+  }
   uint32_t o[16];
   uint64_t xv[16];
 #pragma unroll
@@ -332,13 +338,20 @@ __device__ __forceinline__ void ds_chunk(uint32_t tY, int c0, const float* dl,
 // those from `hi` on) are zero;
 // columns past the sequence piece have -lse*log2e = -inf from the loader and give 0. The
 // bf16 result goes to X columns [32 + c0/2 + 16*CH, +16): inside the S^T columns this
-// warpgroup reads itself (the other warpgroup may still be reading its own).
+// warpgroup reads itself (the other warpgroup may still be reading its own). Returns whether
+// some column is visible to some row of the warp (windowed; else true).
 template <int CH, bool WIN>
-__device__ __forceinline__ void p_from(const uint32_t (&sv)[32], uint32_t tX, int c0, const float* nl,
+__device__ __forceinline__ bool p_from(const uint32_t (&sv)[32], uint32_t tX, int c0, const float* nl,
                                        uint64_t sl2x2, int lo, int hi, uint32_t (&pp)[32]) {
   const int cs = c0 + 32 * CH;
   uint32_t pk[16];
   const uint32_t vis = WIN ? low_bits(hi - cs) & ~low_bits(lo - cs) : 0u;
+  if (WIN && !__any_sync(0xffffffffu, vis != 0)) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) pk[i] = 0;
+    tmem_st16(tX + 32 + c0 / 2 + 16 * CH, pk);
+    return false;
+  }
   const bool full = __all_sync(0xffffffffu, WIN ? vis == 0xffffffffu : lo <= cs);
   // staged: every FMA, then every exponential, then masking and packing
   uint64_t xv[16];
@@ -366,6 +379,7 @@ __device__ __forceinline__ void p_from(const uint32_t (&sv)[32], uint32_t tX, in
     pp[16 * CH + i] = WIN ? pack_f16x2(ev[2 * i], ev[2 * i + 1]) : pk[i];
   }
   tmem_st16(tX + 32 + c0 / 2 + 16 * CH, pk);
+  return true;
 }
 
 // One chunk at a time, on columns of a chunk this thread has already read (hence the
@@ -930,13 +944,14 @@ __global__ void __launch_bounds__(bwd_threads<kWithDQ>(), 1)
         s_phase ^= 1;
         tc_fence_after();
         uint32_t pp[32];
+        bool some0 = true, some1 = true;
         if constexpr (!kWithDQ) {  // both chunks in registers before any write
           uint32_t s0[32], s1[32];
           tmem_ld32_nowait(tX + c0, s0);
           tmem_ld32_nowait(tX + c0 + 32, s1);
           tmem_wait_ld();
-          p_from<0, WIN>(s0, tX, c0, nl, sl2x2, lo, hi, pp);
-          p_from<1, WIN>(s1, tX, c0, nl, sl2x2, lo, hi, pp);
+          some0 = p_from<0, WIN>(s0, tX, c0, nl, sl2x2, lo, hi, pp);
+          some1 = p_from<1, WIN>(s1, tX, c0, nl, sl2x2, lo, hi, pp);
         } else if (wg == 0) {
           p_chunk<1>(tX, c0, nl, sl2x2, lo, pp);
           p_chunk<0>(tX, c0, nl, sl2x2, lo, pp);
@@ -957,8 +972,8 @@ __global__ void __launch_bounds__(bwd_threads<kWithDQ>(), 1)
           tmem_ld32_nowait(tY + c0, d0);
           tmem_ld32_nowait(tY + c0 + 32, d1);
           tmem_wait_ld();
-          ds_from<0, kWithDQ, WIN>(d0, tY, c0, dl, pp, ds_row, row);
-          ds_from<1, kWithDQ, WIN>(d1, tY, c0, dl, pp, ds_row, row);
+          ds_from<0, kWithDQ, WIN>(d0, tY, c0, dl, pp, ds_row, row, some0);
+          ds_from<1, kWithDQ, WIN>(d1, tY, c0, dl, pp, ds_row, row, some1);
         } else if (wg == 0) {
           ds_chunk<1, kWithDQ>(tY, c0, dl, pp, ds_row, row);
           ds_chunk<0, kWithDQ>(tY, c0, dl, pp, ds_row, row);

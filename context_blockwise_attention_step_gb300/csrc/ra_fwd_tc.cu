@@ -584,9 +584,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           const bool full =  // no mask needed
               __all_sync(0xffffffffu, cnt == kKvTileRows && (!WIN || lo_t <= sk_t));
           uint32_t vis[2];
+          bool some[2], all[2];  // of a chunk: the warp's rows see some column, every column
           if constexpr (WIN) {
-            vis[0] = visible_bits(c0, cnt, lo_t, sk_t);
-            vis[1] = visible_bits(c0 + 32, cnt, lo_t, sk_t);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              vis[h] = visible_bits(c0 + 32 * h, cnt, lo_t, sk_t);
+              some[h] = __any_sync(0xffffffffu, vis[h] != 0);
+              all[h] = __all_sync(0xffffffffu, vis[h] == 0xffffffffu);
+            }
           }
           // pass 1: partial row max over this half's visible columns, then both halves'
           uint32_t r2[2][32];
@@ -607,13 +612,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 }
             } else {
 #pragma unroll
-              for (int h = 0; h < 2; ++h)
+              for (int h = 0; h < 2; ++h) {
+                if (WIN && !some[h]) continue;
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
                   const bool see = WIN ? (vis[h] >> i) & 1u : c0 + 32 * h + i < cnt;
                   const float v = see ? __uint_as_float(r2[h][i]) : -INFINITY;
                   mq[2 * h + (i & 1)] = fmaxf(mq[2 * h + (i & 1)], v);
                 }
+              }
             }
             mx = fmaxf(max3(mq[0], mq[1], mq[2]), mq[3]);
           }
@@ -658,6 +665,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             const int cs = c0 + 32 * ch;
             uint32_t (&r)[32] = rr[ch];
             uint32_t pk[16];
+            if (WIN && !some[ch]) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) pk[i] = 0;
+              tmem_st16(tS + 32 + c0 / 2 + 16 * ch, pk);
+              continue;
+            }
             // staged: every FMA, then every exponential (independent, so they issue back to
             // back), then packing and two partial sums
             uint64_t xv[16];
@@ -671,7 +684,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
               ev[2 * i] = ex2(e.x);
               ev[2 * i + 1] = ex2(e.y);
             }
-            if (!full) {
+            if (WIN ? !all[ch] : !full) {
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if (WIN ? !((vis[ch] >> i) & 1u) : cs + i >= cnt) ev[i] = 0.f;
