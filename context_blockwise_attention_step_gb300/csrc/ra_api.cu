@@ -536,7 +536,8 @@ int ra_window_attn_bwd(const ra_problem* p, int window, int sinks, const void* q
       cudaError_t r = ra::launch_window_bwd_tc(*P.p, q, k, v, dout, lse, delta, dk, dv, st);
       if (r != cudaSuccess) return r;
       if (g_prof_mid) cudaEventRecord(g_prof_mid, st);
-      return ra::launch_bwd_dq_tc(*P.p, q, k, v, dout, lse, delta, dq, st);
+      r = ra::launch_bwd_dq_tc(*P.p, q, k, v, dout, lse, delta, dq, st);
+      return r == cudaSuccess ? ra::launch_sink_sum(*P.p, RA_BF16, dk, dv, st) : r;
     });
   } else {
     e = profiled(st, [&] { return ra::launch_window_bwd_simt(*P.p, p->dtype, q, k, v, dout, lse, delta, dq, dk, dv, st); });

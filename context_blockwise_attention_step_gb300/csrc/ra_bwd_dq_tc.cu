@@ -626,6 +626,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
   }
+  if constexpr (WIN) wait_for_previous();  // what follows this kernel reads the K/V pass' sums too
 }
 
 template <int DH, bool WIN>
@@ -638,6 +639,19 @@ cudaError_t launch_one(const Plan& P, const CUtensorMap& mq, const CUtensorMap& 
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int grid = n_items < n_sm ? n_items : n_sm;
+  if constexpr (WIN) {  // starts where the K/V pass leaves an SM free
+    cudaLaunchAttribute early = {};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kDqThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, mdo, P, lse, delta, dq);
+  }
   kern<<<grid, kDqThreads, smem, st>>>(mq, mk, mv, mdo, P, lse, delta, dq);
   return cudaGetLastError();
 }

@@ -474,6 +474,7 @@ __global__ void __launch_bounds__(bwd_threads<kWithDQ>(), 1)
                        float* __restrict__ dq_acc, void* __restrict__ dk_out,
                        void* __restrict__ dv_out) {
   using C = BwdCfg<DH>;
+  if constexpr (WIN) launch_dependents();  // the dq pass reads nothing of this one
   extern __shared__ __align__(1024) uint8_t smem[];
   BwdBars& sh = *reinterpret_cast<BwdBars*>(smem + C::kOffBar);
   WinItem* slots = reinterpret_cast<WinItem*>(smem + C::kOffWin);  // windowed only
@@ -1123,10 +1124,9 @@ cudaError_t launch_window_bwd_tc(const Plan& P, const void* q, const void* k, co
   int dev = 0, n_sm = 0;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
-  e = P.head_dim == 128
-          ? launch_one<128, false, false, true>(P, mq, mk, mv, mdo, lse, delta, nullptr, dk, dv, n_sm, st)
-          : launch_one<64, false, false, true>(P, mq, mk, mv, mdo, lse, delta, nullptr, dk, dv, n_sm, st);
-  return e == cudaSuccess ? launch_sink_sum(P, RA_BF16, dk, dv, st) : e;
+  return P.head_dim == 128
+             ? launch_one<128, false, false, true>(P, mq, mk, mv, mdo, lse, delta, nullptr, dk, dv, n_sm, st)
+             : launch_one<64, false, false, true>(P, mq, mk, mv, mdo, lse, delta, nullptr, dk, dv, n_sm, st);
 }
 
 cudaError_t launch_bwd_tc(const Plan& P, BwdKind kind, const void* q, const void* k, const void* v,

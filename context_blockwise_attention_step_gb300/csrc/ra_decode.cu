@@ -88,9 +88,7 @@ __device__ __forceinline__ Visible visible(const DecodeArgs& A, int b, bool flag
 }
 
 // The join kernel is launched while the main one runs (programmatic dependent launch), works out
-// what it has to join, and waits here for the main kernel's end.
-__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_main() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// what it has to join, and then waits for the main kernel's end.
 
 __device__ __forceinline__ int units_of(const DecodeArgs& A, int b) {
   return (visible(A, b, false).vis + kUnit - 1) / kUnit;
@@ -774,7 +772,7 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join(const __grid_constan
     c0 = cta_of(total, ctas, S.base);
     c1 = cta_of(total, ctas, S.base + S.units - 1);
   }
-  wait_for_main();  // in every block: what follows in the stream waits for this kernel alone
+  wait_for_previous();  // in every block: what follows in the stream waits for this kernel alone
   if (c0 == c1 || (!PAIRS && c0 != static_cast<int>(blockIdx.x))) return;  // not cut, or cut earlier
   const int hk = S.pair / A.blocks_per_kv, blk = S.pair - hk * A.blocks_per_kv;
   const int heads = min(A.block_heads, A.group - blk * A.block_heads), parts = c1 - c0 + 1;

@@ -22,6 +22,7 @@
 
 #include "ra_internal.h"
 #include "ra_plan.h"
+#include "ra_ptx.cuh"
 #include "ra_window.cuh"
 
 namespace ra {
@@ -331,7 +332,7 @@ __global__ void __launch_bounds__(kThreads)
     __syncwarp();
     accumulate<DHP>(sp, sk_, ty, tx, acc);
   });
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // so that the end of this kernel is that of window_dkv_simt too
+  wait_for_previous();  // so that the end of this kernel is that of window_dkv_simt too
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     if (4 * ty + i < b.n)
@@ -349,7 +350,7 @@ __global__ void __launch_bounds__(kThreads)
   float* sk_ = reinterpret_cast<float*>(smem4);
   float *sv = sk_ + tile_floats<DHP, kRows>(), *sq = sv + tile_floats<DHP, kRows>(),
         *sdo = sq + tile_floats<DHP, kCols>(), *sp = sdo + tile_floats<DHP, kCols>();
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  launch_dependents();
   __shared__ float s_lse[kCols], s_delta[kCols];
   __shared__ int s_lo[kRows], s_hi[kRows];
   const SeqDesc& sd = P.seq[blockIdx.y];
