@@ -13,6 +13,7 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "ra_internal.h"
 #include "ra_layout.h"
@@ -339,18 +340,31 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// ---------------------------------------------------------------- head size 64 or 128, 16-byte loads
+// ---------------------------------------------------------------- 16-byte loads
 // A head is held by LANES lanes, each with two 16-byte pieces: the c-th of the first half and the
 // c-th of the second half of the rotated elements, so that both members of a rotated pair are in
 // one thread (interleaved pairs are anyway), or two neighbouring pieces of what is not rotated.
 // The HEADS heads of a warp are loaded together.
+// DH is the head size (64 or 128), or -32, -64, -128 for a multiple of 8 up to that: the last lanes
+// of a head then have nothing, and HeadArgs has the size.
 template <typename T, int DH>
 struct Vec {
+  static constexpr int SPAN = DH < 0 ? -DH : DH;
   static constexpr int N = 16 / sizeof(T);          // elements of a piece
-  static constexpr int LANES = DH / 2 / N;          // lanes of a head
+  static constexpr int LANES = SPAN / 2 / N;        // lanes of a head
   static constexpr int HEADS = 32 / LANES;          // heads of a warp at a time
   static constexpr int PER = N / HEADS > 0 ? N / HEADS : 1;  // angles a lane works out
 };
+
+template <int DH>
+__device__ __forceinline__ int size_of(const HeadArgs& A) {
+  return DH < 0 ? A.dh : DH;
+}
+// Whether lane c of a head has pieces.
+template <typename T, int DH>
+__device__ __forceinline__ bool has_piece(const HeadArgs& A, int c) {
+  return DH > 0 || c * 2 * Vec<T, DH>::N < A.dh;
+}
 
 template <typename T, int DH>
 struct Piece {  // a lane's two pieces, as loaded
@@ -363,7 +377,7 @@ template <typename T, int DH, bool INTER>
 __device__ __forceinline__ Place place_of(const HeadArgs& A, int c) {
   constexpr int N = Vec<T, DH>::N;
   const int rd = A.rope.rotary_dim, turned = rd / 2 / N;  // lanes with pairs (not interleaved)
-  if (INTER || rd == 0) return {c * N, DH / 2 + c * N};
+  if (INTER || rd == 0) return {c * N, size_of<DH>(A) / 2 + c * N};
   if (c < turned) return {c * N, rd / 2 + c * N};
   return {rd + (c - turned) * 2 * N, rd + (c - turned) * 2 * N + N};
 }
@@ -413,7 +427,7 @@ __device__ __forceinline__ void piece_angles(const HeadArgs& A, int64_t pos, int
 #pragma unroll
   for (int k = 0; k < V::PER; ++k) {
     const int j = (sub * V::PER + k) % V::N;
-    const int pair = !INTER ? c * V::N + j : j < V::N / 2 ? c * V::N / 2 + j : DH / 4 + c * V::N / 2 + j - V::N / 2;
+    const int pair = !INTER ? c * V::N + j : j < V::N / 2 ? c * V::N / 2 + j : size_of<DH>(A) / 4 + c * V::N / 2 + j - V::N / 2;
     mine[k] = pair < A.rope.rotary_dim / 2 ? cos_sin(A.rope.turns[pair], pos) : make_float2(1.f, 0.f);
   }
 #pragma unroll
@@ -465,15 +479,18 @@ __device__ __forceinline__ void head_run(const HeadArgs& A, const T* __restrict_
                                          F&& prepare) {
   using V = Vec<T, DH>;
   const Place at = place_of<T, DH, INTER>(A, lane % V::LANES);
-  const int sub = lane / V::LANES, runs = (heads + V::HEADS - 1) / V::HEADS;
-  Piece<T, DH> wp;
-  if (w != nullptr) wp = load_piece<T, DH>(w, at);
+  const int sub = lane / V::LANES, runs = (heads + V::HEADS - 1) / V::HEADS, dh = size_of<DH>(A);
+  const bool on = has_piece<T, DH>(A, lane % V::LANES);
+  const float per_dh = 1.f / dh;
+  Piece<T, DH> wp = {};
+  if (w != nullptr && on) wp = load_piece<T, DH>(w, at);
   for (int i0 = first; i0 < runs; i0 += step * U) {
     Piece<T, DH> p[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int h = (i0 + u * step) * V::HEADS + sub;
-      if (h < heads) p[u] = load_piece<T, DH>(src + h * DH, at);
+      if (DH < 0 && !on) p[u] = {};
+      if (h < heads && on) p[u] = load_piece<T, DH>(src + h * dh, at);
     }
     if (i0 == first) prepare();
 #pragma unroll
@@ -488,7 +505,7 @@ __device__ __forceinline__ void head_run(const HeadArgs& A, const T* __restrict_
           float ss = 0.f, wa[V::N], wb[V::N];
 #pragma unroll
           for (int j = 0; j < V::N; ++j) ss += a[j] * a[j] + b[j] * b[j];
-          const float r = rsqrtf(group_sum<V::LANES>(ss) * (1.f / DH) + A.eps);
+          const float r = rsqrtf(group_sum<V::LANES>(ss) * per_dh + A.eps);
           widen(wp.a, wa);
           widen(wp.b, wb);
 #pragma unroll
@@ -501,7 +518,7 @@ __device__ __forceinline__ void head_run(const HeadArgs& A, const T* __restrict_
         p[u].a = narrow(a);
         p[u].b = narrow(b);
       }
-      if (h < heads) store_piece<T, DH>(dst + h * dst_head, at, p[u]);
+      if (h < heads && on) store_piece<T, DH>(dst + h * dst_head, at, p[u]);
     }
   }
 }
@@ -516,15 +533,15 @@ __global__ void __launch_bounds__(kThreads)
   const int lane = threadIdx.x & 31;
   const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   const int64_t t = unit / parts;
-  const int part = static_cast<int>(unit - t * parts);
+  const int part = static_cast<int>(unit - t * parts), dh = size_of<DH>(A);
   if (t >= A.n_rows) return;
-  const Token tok = locate(R, static_cast<int>(t), A.hkv * static_cast<int64_t>(DH));
+  const Token tok = locate(R, static_cast<int>(t), A.hkv * static_cast<int64_t>(dh));
   if (tok.absent) return;
-  T* qo = q_out + t * A.hq * DH;
+  T* qo = q_out + t * A.hq * dh;
   if (tok.idle) {
     for (int h = part * V::HEADS + lane / V::LANES; h < A.hq; h += parts * V::HEADS) {
       Piece<T, DH> zero = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-      store_piece<T, DH>(qo + h * DH, place_of<T, DH, INTER>(A, lane % V::LANES), zero);
+      if (has_piece<T, DH>(A, lane % V::LANES)) store_piece<T, DH>(qo + h * dh, place_of<T, DH, INTER>(A, lane % V::LANES), zero);
     }
     return;
   }
@@ -536,7 +553,7 @@ __global__ void __launch_bounds__(kThreads)
   auto none = []() {};
   const int runs_q = (A.hq + V::HEADS - 1) / V::HEADS, runs_k = (A.hkv + V::HEADS - 1) / V::HEADS;
   if (part >= runs_q) angles();
-  head_run<T, DH, INTER, 4>(A, qw, turned, q + t * A.q_stride, qo, DH, A.hq, part, parts, lane, cs, sn, angles);
+  head_run<T, DH, INTER, 4>(A, qw, turned, q + t * A.q_stride, qo, dh, A.hq, part, parts, lane, cs, sn, angles);
   // the next run of heads goes on with the part after the last one's
   const int pk = ((part - runs_q) % parts + parts) % parts;
   head_run<T, DH, INTER, 2>(A, kw, turned, k + t * A.k_stride, k_out + tok.kv, A.kv_head, A.hkv, pk, parts, lane,
@@ -559,18 +576,20 @@ __device__ __forceinline__ void head_run_bwd(const HeadArgs& A, const T* __restr
                                              F&& prepare) {
   using V = Vec<T, DH>;
   const Place at = place_of<T, DH, INTER>(A, lane % V::LANES);
-  const int sub = lane / V::LANES;
-  Piece<T, DH> wp;
-  if (w != nullptr) wp = load_piece<T, DH>(w, at);
+  const int sub = lane / V::LANES, dh = size_of<DH>(A);
+  const bool on = has_piece<T, DH>(A, lane % V::LANES);
+  const float per_dh = 1.f / dh;
+  Piece<T, DH> wp = {};
+  if (w != nullptr && on) wp = load_piece<T, DH>(w, at);
   for (int h0 = sub; h0 - sub < heads; h0 += V::HEADS * U) {
     Piece<T, DH> g[U], p[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int h = h0 + u * V::HEADS;
       g[u].a = g[u].b = p[u].a = p[u].b = make_uint4(0u, 0u, 0u, 0u);
-      if (h < heads) {
-        g[u] = load_piece<T, DH>(dy + h * DH, at);
-        if (w != nullptr) p[u] = load_piece<T, DH>(x + h * DH, at);
+      if (h < heads && on) {
+        g[u] = load_piece<T, DH>(dy + h * dh, at);
+        if (w != nullptr) p[u] = load_piece<T, DH>(x + h * dh, at);
       }
     }
     if (h0 == sub) prepare();
@@ -588,7 +607,7 @@ __device__ __forceinline__ void head_run_bwd(const HeadArgs& A, const T* __restr
         widen(p[u].b, xb);
 #pragma unroll
         for (int j = 0; j < V::N; ++j) ss += xa[j] * xa[j] + xb[j] * xb[j];
-        const float r = rsqrtf(group_sum<V::LANES>(ss) * (1.f / DH) + A.eps);
+        const float r = rsqrtf(group_sum<V::LANES>(ss) * per_dh + A.eps);
         widen(wp.a, wv);
 #pragma unroll
         for (int j = 0; j < V::N; ++j) {
@@ -605,7 +624,7 @@ __device__ __forceinline__ void head_run_bwd(const HeadArgs& A, const T* __restr
           b[j] *= wv[j];
           hn += b[j] * xb[j];
         }
-        const float mean = group_sum<V::LANES>(hn) * (1.f / DH);
+        const float mean = group_sum<V::LANES>(hn) * per_dh;
 #pragma unroll
         for (int j = 0; j < V::N; ++j) {
           a[j] = r * (a[j] - xa[j] * mean);
@@ -614,7 +633,7 @@ __device__ __forceinline__ void head_run_bwd(const HeadArgs& A, const T* __restr
       }
       g[u].a = narrow(a);
       g[u].b = narrow(b);
-      if (h < heads) store_piece<T, DH>(dx + h * DH, at, g[u]);
+      if (h < heads && on) store_piece<T, DH>(dx + h * dh, at, g[u]);
     }
   }
 }
@@ -627,14 +646,14 @@ __global__ void __launch_bounds__(kBwdThreads, 4)
                   float* __restrict__ partial) {
   using V = Vec<T, DH>;
   constexpr int WARPS = kBwdThreads / 32;
-  __shared__ float sums[WARPS][2][DH];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __shared__ float sums[WARPS][2][V::SPAN];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, dh = size_of<DH>(A);
   const bool turned = A.rope.rotary_dim > 0;
   float acc[2][2][V::N] = {};
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * WARPS + warp; t < A.n_rows;
        t += static_cast<int64_t>(gridDim.x) * WARPS) {
     float cs[V::N], sn[V::N];
-    const int64_t oq = t * A.hq * DH, ok = t * A.hkv * DH;
+    const int64_t oq = t * A.hq * dh, ok = t * A.hkv * dh;
     head_run_bwd<T, DH, INTER, 2>(
         A, qw, turned, q + t * A.q_stride, dq_out + oq, dq + oq, A.hq, lane, cs, sn, acc[0][0], acc[0][1], [&]() {
           if (turned) piece_angles<T, DH, INTER>(A, locate(R, static_cast<int>(t), 0).pos, lane, cs, sn);
@@ -653,13 +672,13 @@ __global__ void __launch_bounds__(kBwdThreads, 4)
         float x = acc[which][half][j];  // over the heads of the warp: lanes with the same pieces
 #pragma unroll
         for (int o = V::LANES; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-        if (lane < V::LANES) sums[warp][which][(half ? at.b : at.a) + j] = x;
+        if (lane < V::LANES && has_piece<T, DH>(A, lane)) sums[warp][which][(half ? at.b : at.a) + j] = x;
       }
   __syncthreads();
-  for (int i = threadIdx.x; i < 2 * DH; i += kBwdThreads) {
+  for (int i = threadIdx.x; i < 2 * dh; i += kBwdThreads) {
     float s = 0.f;
-    for (int w = 0; w < WARPS; ++w) s += sums[w][i / DH][i % DH];
-    partial[static_cast<int64_t>(blockIdx.x) * 2 * DH + i] = s;
+    for (int w = 0; w < WARPS; ++w) s += sums[w][i / dh][i % dh];
+    partial[static_cast<int64_t>(blockIdx.x) * 2 * dh + i] = s;
   }
 }
 
@@ -747,14 +766,27 @@ int parts_of(int n_rows, int runs) {
   return want < 1 ? 1 : want > runs ? runs : want;
 }
 
-// Whether the 16-byte kernels can take a call: heads of 64 or 128, a rotation that falls into whole
-// pieces, and rows that all start on 16 bytes. (Measured at 131072 tokens, 32/8 heads of 128,
-// bf16, forward and backward: 16-byte kernels 1.15 ms, the others 3.9 ms.)
+// Whether the 16-byte kernels can take a call: heads of 64 or 128, in float32 any multiple of 8, a
+// rotation that falls into whole pieces, and rows that all start on 16 bytes. (Measured, forward
+// and backward: 131072 tokens, 32/8 heads of 128, bf16, 1.15 ms against the others' 3.9 ms; 32768
+// tokens, float32 heads of 80, 0.40 against 0.69 ms.)
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 bool can_vec(const HeadArgs& A, int elem) {
   auto rows16 = [&](int64_t stride) { return stride * elem % 16 == 0; };
-  return (A.dh == 64 || A.dh == 128) && (A.rope.interleaved || A.rope.rotary_dim % (32 / elem) == 0) &&
+  return (A.dh == 64 || A.dh == 128 || (elem == 4 && A.dh % 8 == 0)) && (A.rope.interleaved || A.rope.rotary_dim % (32 / elem) == 0) &&
          rows16(A.q_stride) && rows16(A.k_stride) && rows16(A.v_stride) && rows16(A.kv_head);
+}
+
+// Calls f with the 16-byte kernels' DH for the call's head size.
+template <typename T, typename F>
+auto with_span(const HeadArgs& A, F&& f) {
+  if (A.dh == 128) return f(std::integral_constant<int, 128>());
+  if constexpr (sizeof(T) == 4) {
+    if (A.dh <= 32) return f(std::integral_constant<int, -32>());
+    if (A.dh < 64) return f(std::integral_constant<int, -64>());
+    if (A.dh > 64) return f(std::integral_constant<int, -128>());
+  }
+  return f(std::integral_constant<int, 64>());
 }
 
 template <typename T, int DH, bool INTER, typename Rows, bool CACHE>
@@ -777,12 +809,12 @@ cudaError_t launch_fwd(const HeadArgs& A, const Rows& R, const void* qw, const v
                        void* v_out, bool aligned, cudaStream_t st) {
   if (aligned && can_vec(A, sizeof(T)) && aligned16(qw) && aligned16(kw) && aligned16(q) && aligned16(k) &&
       aligned16(v) && aligned16(q_out) && aligned16(k_out) && aligned16(v_out)) {
-    const bool inter = A.rope.interleaved;
-    if (A.dh == 128)
-      return inter ? fwd_vec<T, 128, true, Rows, CACHE>(A, R, qw, kw, q, k, v, q_out, k_out, v_out, st)
-                   : fwd_vec<T, 128, false, Rows, CACHE>(A, R, qw, kw, q, k, v, q_out, k_out, v_out, st);
-    return inter ? fwd_vec<T, 64, true, Rows, CACHE>(A, R, qw, kw, q, k, v, q_out, k_out, v_out, st)
-                 : fwd_vec<T, 64, false, Rows, CACHE>(A, R, qw, kw, q, k, v, q_out, k_out, v_out, st);
+    return with_span<T>(A, [&](auto span) {
+      constexpr int DH = decltype(span)::value;
+      return A.rope.interleaved
+                 ? fwd_vec<T, DH, true, Rows, CACHE>(A, R, qw, kw, q, k, v, q_out, k_out, v_out, st)
+                 : fwd_vec<T, DH, false, Rows, CACHE>(A, R, qw, kw, q, k, v, q_out, k_out, v_out, st);
+    });
   }
   const int parts = parts_of(A.n_rows, A.hq + A.hkv * (CACHE ? 2 : 1));
   const int64_t units = static_cast<int64_t>(A.n_rows) * parts;
@@ -811,14 +843,11 @@ cudaError_t launch_bwd(const HeadArgs& A, const RingRows& R, const void* qw, con
   if (can_vec(A, sizeof(T)) && aligned16(qw) && aligned16(kw) && aligned16(q) && aligned16(k) &&
       aligned16(dq_out) && aligned16(dk_out) && aligned16(dq) && aligned16(dk)) {
     blocks = blocks_for(A.n_rows, kBwdThreads / 32, kHeadBwdBlocks);
-    const bool inter = A.rope.interleaved;
-    if (A.dh == 128) {
-      if (inter) bwd_vec<T, 128, true>(blocks, A, R, qw, kw, q, k, dq_out, dk_out, dq, dk, partial, st);
-      else bwd_vec<T, 128, false>(blocks, A, R, qw, kw, q, k, dq_out, dk_out, dq, dk, partial, st);
-    } else {
-      if (inter) bwd_vec<T, 64, true>(blocks, A, R, qw, kw, q, k, dq_out, dk_out, dq, dk, partial, st);
-      else bwd_vec<T, 64, false>(blocks, A, R, qw, kw, q, k, dq_out, dk_out, dq, dk, partial, st);
-    }
+    with_span<T>(A, [&](auto span) {
+      constexpr int DH = decltype(span)::value;
+      if (A.rope.interleaved) bwd_vec<T, DH, true>(blocks, A, R, qw, kw, q, k, dq_out, dk_out, dq, dk, partial, st);
+      else bwd_vec<T, DH, false>(blocks, A, R, qw, kw, q, k, dq_out, dk_out, dq, dk, partial, st);
+    });
   } else {
     const int parts = parts_of(A.n_rows, A.hq + A.hkv);
     blocks = blocks_for(static_cast<int64_t>(A.n_rows) * parts, kWarps, kHeadBwdBlocks);

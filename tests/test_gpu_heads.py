@@ -80,6 +80,17 @@ NORM_CASES = [
     (BF16, "basic", 2, [12], False, 3, 1, 64, 22, False),    # and not
     (F32, "stripe", 2, [12], False, 9, 3, 128, 24, False),
     (F32, "stripe", 2, [12], False, 9, 3, 64, 6, True),
+    (F32, "zigzag", 2, [40], False, 10, 2, 8, 8, False),      # float32 heads of any multiple of 8
+    (F32, "basic", 1, [33], False, 18, 3, 32, 16, False),
+    (F32, "basic", 2, [34], False, 6, 3, 24, 10, True),
+    (F32, "zigzag", 2, [40], False, 6, 2, 48, 48, False),
+    (F32, "stripe", 2, [40], False, 6, 2, 40, 8, False),
+    (F32, "zigzag", 2, [40], False, 4, 2, 96, 48, False),
+    (F32, "zigzag", 2, [40], False, 4, 2, 80, 80, True),
+    (F32, "basic", 2, [40], False, 4, 2, 120, 24, False),
+    (F32, "basic", 2, [40], False, 4, 2, 112, None, False),
+    (F32, "basic", 2, [40], False, 4, 2, 100, 48, False),
+    (F32, "basic", 2, [40], False, 4, 2, 96, 20, False),
 ]
 
 
@@ -199,6 +210,9 @@ APPEND_CASES = [  # dtype, hq, hkv, dh, page, rotary, lens with the new tokens, 
     (BF16, 4, 4, 64, 7, 32, [100, 33, 64], [60, 0, 64]),
     (F32, 3, 1, 50, 1, 50, [4, 9], [4, 1]),
     (F32, 2, 2, 128, 64, None, [70, 64, 3], None),
+    (F32, 6, 2, 96, 16, 48, [40, 0, 16], None),
+    (F32, 9, 3, 48, 16, 48, [40, 7], [33, 7]),
+    (F32, 9, 3, 32, 16, 16, [40, 7], [33, 7]),
     (BF16, 32, 8, 128, 64, 128, [1], None),
 ]
 
