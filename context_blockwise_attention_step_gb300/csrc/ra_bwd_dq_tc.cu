@@ -28,7 +28,8 @@
 // key columns 0-63 and 64-127; they also write dq).
 //
 // WIN (sliding window with always visible first tokens): the walk visits the K/V tiles that
-// some row of the tile sees, as in the windowed forward.
+// some row of the tile sees, as in the windowed forward. It is launched with the K/V pass and
+// needs nothing of it, so it only waits for it at its own end.
 #include <cuda_runtime.h>
 
 #include "ra_internal.h"

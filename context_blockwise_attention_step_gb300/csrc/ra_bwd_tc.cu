@@ -40,7 +40,10 @@
 // it would outlast all the others (4096 query tiles against 36 at 131072 tokens, window 1024,
 // 4 heads a group). Sink rows get their sum from several items, so each of these writes float32
 // sums of the sink rows to a slot of its own (ra_plan.h), and launch_sink_sum adds the slots in
-// order, so that the result does not depend on the order of the items.
+// order, so that the result does not depend on the order of the items. The dq pass is launched
+// while this one runs and takes the SMs that it leaves. Measured at 65536 tokens in 16 sequences
+// over 8 shards, 32/8 heads of 128, window 1024: K/V pass 2.79 ms, dq pass 2.38, the whole
+// backward 5.53; 2 x 4096 tokens, 8 heads of 64, window 500: 105 us (115 with one after the other).
 //
 // Warp roles (512 threads; 384 without dQ): warp 0 TMA producer (K, V once per item; Q and
 // dO per query tile, two stages), warp 1 TMEM allocator + MMA issuer, warp 2 lse / delta

