@@ -40,13 +40,13 @@ FALLBACK_PEAKS = {"hbm_gbs": 6800.0, "bf16_tflops": 1900.0, "bf16_tflops_sustain
 # null until re-measured.
 TRAFFIC = {
     ("ring_bwd_tc (K/V-tile pass)", "long_s131072_gqa32x8_dh128_D16_zigzag"):
-        {"bytes": 55050429696 + 541969408, "source_sha": "f32b290a402a8697"},
+        {"bytes": 55109247744 + 542303488, "source_sha": "38b434ff2fe9b617"},
     ("ring_fwd_tc", "long_s131072_gqa32x8_dh128_D16_zigzag"):
-        {"bytes": 118658146816 + 1258202880, "source_sha": "2b895ee9cb12a15d"},
+        {"bytes": 119308476672 + 1258622464, "source_sha": "55762b8b8add01f5"},
     ("ring_bwd_dq_tc (dq pass)", "long_s131072_gqa32x8_dh128_D16_zigzag"):
-        {"bytes": 16206185984 + 1060122624, "source_sha": "8733957a884564f0"},
+        {"bytes": 16026640640 + 1060443392, "source_sha": "71a383ba753f0e0c"},
     ("merge_kernel", "long_s131072_gqa32x8_dh128_D16_zigzag"):
-        {"bytes": 3255621888 + 2109105664, "source_sha": "59a72745c75670f4"},
+        {"bytes": 3255936256 + 2109106688, "source_sha": "8d166f36bdc3345f"},
 }
 
 

@@ -205,7 +205,8 @@ int ra_window_attn_fwd(const ra_problem* p, int window, int sinks, const void* q
                        const void* v, void* out, float* lse, void* workspace, size_t workspace_bytes,
                        void* stream);
 
-/* Its backward, arguments as for ra_ring_attn_bwd. Run-to-run bit-identical. The workspace
+/* Its backward, arguments as for ra_ring_attn_bwd (as there, the row sums dO . out are formed from
+ * `out` in its dtype). Run-to-run bit-identical. The workspace
  * (device, >= ra_window_workspace_bytes(p, window, sinks, 1), 256-byte aligned) is
  * overwritten. */
 int ra_window_attn_bwd(const ra_problem* p, int window, int sinks, const void* q, const void* k,
