@@ -7,13 +7,15 @@
 // where the window does, on any row, so the last tile of a run alone is not full. A thread has 4
 // rows x 4 columns of the products, and 4 rows x head_dim / 16 elements of the sums: what bounds
 // such kernels is the 128 bytes a cycle that shared memory gives an SM, and 4 x 4 takes two
-// multiplications from every word (1 x 4 took less than one, and 10.5 against 5.5 ms at 4096
-// tokens, 16/4 heads of 128, window 1024). Rows of a tile are 16 bytes longer than the data, so that
-// eight threads on eight rows meet every bank once. Weights are exchanged between the sixteen
-// threads of a row through shared memory. dq's kernel starts while that of dk and dv, which has
-// fewer CTAs, is running (4.9 against 5.5 ms, 0.26 against 0.31 at the sizes below). Measured on
-// GB300 (2048 tokens, 4/2 heads of 64, window 300): 67 us forward, 152 us backward; one warp a row,
-// eight keys at a time, took 119 and 251. The larger size runs at 21 TFLOP/s.
+// multiplications from every word (1 x 4 took less than one, and 10.5 against 5.5 ms for a forward
+// and backward of 4096 tokens, 16/4 heads of 128, window 1024). Rows of a tile are 16 bytes longer
+// than the data, so that eight threads on eight rows meet every bank once. Weights are exchanged
+// between the sixteen threads of a row through shared memory. dq's kernel starts while that of dk and dv, which has
+// fewer CTAs, is running, and float32 tiles are loaded by asynchronous copies. CTAs of 16 rows are
+// slower, backward and forward, at eight of nine sizes (2048 tokens, 4/2 heads of 64, window 300: forward 63 against 56 us, before
+// the copies), for a tile's loads then feed half the products.
+// Measured on GB300: that size 45 us forward, 137 us backward (one warp a row, eight keys at a
+// time, took 119 and 251); 4096 tokens, 16/4 heads of 128, window 1024: 4.5 ms in all, 23 TFLOP/s.
 //
 // A sink is seen by the whole sequence: its far queries go, a chunk of a rank at a time, to CTAs
 // of their own, which leave float32 sums in the slots that ra_plan.h describes.
@@ -44,6 +46,21 @@ __device__ __forceinline__ float4 ld4(const __nv_bfloat16* p) {
 __device__ __forceinline__ void stf(float* p, float v) { *p = v; }
 __device__ __forceinline__ void stf(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
+// Four elements into shared memory, zeros if not `in`: float32 by an asynchronous copy, so that all
+// the loads of a tile are under way together, without registers.
+__device__ __forceinline__ void copy4(float* to, const float* from, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(in ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy4(float* to, const __nv_bfloat16* from, bool in) {
+  *reinterpret_cast<float4*>(to) = in ? ld4(from) : make_float4(0.f, 0.f, 0.f, 0.f);
+}
+// All tiles that the threads have loaded are there.
+__device__ __forceinline__ void wait_tiles() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
+}
+
 // Rows row0 .. row0 + n - 1 of head h of a [rows, heads, dh] tensor into a tile of ROWS rows, zeros
 // behind them and behind dh. vec: dh and the tensor allow loads of four elements.
 template <typename T, int DHP, int ROWS>
@@ -53,8 +70,9 @@ __device__ __forceinline__ void load_tile(float* to, const T* from, int64_t row0
 #pragma unroll 4
     for (int i = threadIdx.x; i < ROWS * (DHP / 4); i += kThreads) {
       const int r = i / (DHP / 4), d = i % (DHP / 4) * 4;
-      const float4 x = r < n && d < dh ? ld4(from + ((row0 + r) * heads + h) * dh + d) : make_float4(0.f, 0.f, 0.f, 0.f);
-      *reinterpret_cast<float4*>(to + r * (DHP + 4) + d) = x;
+      const bool in = r < n && d < dh;
+      const T* at = from + (in ? ((row0 + r) * heads + h) * dh + d : 0);
+      copy4(to + r * (DHP + 4) + d, at, in);
     }
   } else {
 #pragma unroll 4
@@ -65,9 +83,9 @@ __device__ __forceinline__ void load_tile(float* to, const T* from, int64_t row0
   }
 }
 
-// x[i][j] = row 4 ty + i of A times row tx + 16 j of B.
-template <int DHP>
-__device__ __forceinline__ void products(const float* A, const float* B, int ty, int tx, float (&x)[4][4]) {
+// x[i][j] = row 4 ty + i of A times row tx + 16 j of B, j < J.
+template <int DHP, int J>
+__device__ __forceinline__ void products_of(const float* A, const float* B, int ty, int tx, float (&x)[4][4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -78,7 +96,7 @@ __device__ __forceinline__ void products(const float* A, const float* B, int ty,
 #pragma unroll
     for (int i = 0; i < 4; ++i) u[i] = *reinterpret_cast<const float4*>(A + (4 * ty + i) * (DHP + 4) + d);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < J; ++j) {
       const float4 v = *reinterpret_cast<const float4*>(B + (tx + 16 * j) * (DHP + 4) + d);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -91,17 +109,25 @@ __device__ __forceinline__ void products(const float* A, const float* B, int ty,
   }
 }
 
-// acc[i][4 j + e] (row 4 ty + i, element 4 tx + 64 j + e) += sum over the columns c of W[row][c] B[c].
+// The first n of the 64 columns: a tile of a few first tokens takes a quarter of the products.
+template <int DHP>
+__device__ __forceinline__ void products(const float* A, const float* B, int ty, int tx, int n, float (&x)[4][4]) {
+  if (n <= 16) products_of<DHP, 1>(A, B, ty, tx, x);
+  else products_of<DHP, 4>(A, B, ty, tx, x);
+}
+
+// acc[i][4 j + e] (row 4 ty + i, element 4 tx + 64 j + e) += sum over the first n columns c of W[row][c] B[c]
+// (W is 0 from n on).
 template <int DHP>
 struct Acc {
   static constexpr int J = DHP >= 64 ? DHP / 64 : 1;  // DHP 32: the upper eight threads of a row idle
   float v[4][4 * J];
 };
 template <int DHP>
-__device__ __forceinline__ void accumulate(const float* W, const float* B, int ty, int tx, Acc<DHP>& acc) {
+__device__ __forceinline__ void accumulate(const float* W, const float* B, int ty, int tx, int n, Acc<DHP>& acc) {
   if (4 * tx >= DHP) return;
 #pragma unroll 2
-  for (int c0 = 0; c0 < kCols; c0 += 4) {
+  for (int c0 = 0; c0 < n; c0 += 4) {
     float w[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -246,9 +272,9 @@ __global__ void __launch_bounds__(kThreads)
     __syncthreads();
     load_tile<T, DHP, kCols>(sk_, k, krow, n, P.hkv, hk, dh, vec);
     load_tile<T, DHP, kCols>(sv, v, krow, n, P.hkv, hk, dh, vec);
-    __syncthreads();
+    wait_tiles();
     float x[4][4];
-    products<DHP>(sq, sk_, ty, tx, x);
+    products<DHP>(sq, sk_, ty, tx, n, x);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int lim = keys.lim[4 * ty + i], lo = keys.lo[4 * ty + i];
@@ -275,7 +301,7 @@ __global__ void __launch_bounds__(kThreads)
       for (int d = 0; d < 4 * Acc<DHP>::J; ++d) acc.v[i][d] *= alpha;
     }
     __syncwarp();  // a row's sixteen threads are in one warp
-    accumulate<DHP>(sp, sv, ty, tx, acc);
+    accumulate<DHP>(sp, sv, ty, tx, n, acc);
   });
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -315,10 +341,10 @@ __global__ void __launch_bounds__(kThreads)
     __syncthreads();
     load_tile<T, DHP, kCols>(sk_, k, krow, n, P.hkv, hk, dh, vec);
     load_tile<T, DHP, kCols>(sv, v, krow, n, P.hkv, hk, dh, vec);
-    __syncthreads();
+    wait_tiles();
     float x[4][4], y[4][4];
-    products<DHP>(sq, sk_, ty, tx, x);
-    products<DHP>(sdo, sv, ty, tx, y);
+    products<DHP>(sq, sk_, ty, tx, n, x);
+    products<DHP>(sdo, sv, ty, tx, n, y);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int lim = keys.lim[4 * ty + i], lo = keys.lo[4 * ty + i];
@@ -330,7 +356,7 @@ __global__ void __launch_bounds__(kThreads)
       }
     }
     __syncwarp();
-    accumulate<DHP>(sp, sk_, ty, tx, acc);
+    accumulate<DHP>(sp, sk_, ty, tx, n, acc);
   });
   wait_for_previous();  // so that the end of this kernel is that of window_dkv_simt too
 #pragma unroll
@@ -432,10 +458,10 @@ __global__ void __launch_bounds__(kThreads)
             s_lse[threadIdx.x] = lse[li0 + a + threadIdx.x];
             s_delta[threadIdx.x] = delta[li0 + a + threadIdx.x];
           }
-          __syncthreads();
+          wait_tiles();
           float x[4][4], y[4][4];
-          products<DHP>(sk_, sq, ty, tx, x);
-          products<DHP>(sv, sdo, ty, tx, y);
+          products<DHP>(sk_, sq, ty, tx, n, x);
+          products<DHP>(sv, sdo, ty, tx, n, y);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int lo = s_lo[4 * ty + i], hi = s_hi[4 * ty + i];
@@ -449,18 +475,19 @@ __global__ void __launch_bounds__(kThreads)
             }
           }
           __syncwarp();
-          accumulate<DHP>(sp, sdo, ty, tx, dva);
+          accumulate<DHP>(sp, sdo, ty, tx, n, dva);
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int c = 0; c < 4; ++c) sp[(4 * ty + i) * kPStride + tx + 16 * c] = y[i][c];
           __syncwarp();
-          accumulate<DHP>(sp, sq, ty, tx, dka);
+          accumulate<DHP>(sp, sq, ty, tx, n, dka);
         }
       }
     }
   }
+  wait_tiles();  // (a block without queries)
   const int sinks = sink_rows(P, L, j);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
