@@ -30,6 +30,8 @@
 // WIN (sliding window with always visible first tokens): the walk visits the K/V tiles that
 // some row of the tile sees, as in the windowed forward. It is launched with the K/V pass and
 // needs nothing of it, so it only waits for it at its own end.
+// DELTA (windows of few keys): the walk without dQ; a row's two threads add their halves of
+// sum_j P_j dP_j to the row's delta, which is 0 before.
 #include <cuda_runtime.h>
 
 #include "ra_internal.h"
@@ -162,7 +164,7 @@ __device__ __forceinline__ int dq_window_publish(DqBars& sh, WinSlot* slots, con
   return w;
 }
 
-template <int DH, bool WIN>
+template <int DH, bool WIN, bool DELTA = false>
 __global__ void __launch_bounds__(kDqThreads, 1)
     ring_bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
                           const __grid_constant__ CUtensorMap tmK,
@@ -392,12 +394,14 @@ __global__ void __launch_bounds__(kDqThreads, 1)
           // dP(n+1) first: dP(n) has been read (ds_full), and dS(n+1) goes to the other S
           // buffer, so the softmax threads can compute it while dQ(n) runs
           if (n + 1 < N && !(ok = issue_dP(n + 1))) break;
-          const uint32_t ka = sK + st * C::kTileBytes;
-          const uint32_t tds = tmem + (n & 1 ? C::kColS1 : C::kColS0) + 32;
+          if constexpr (!DELTA) {
+            const uint32_t ka = sK + st * C::kTileBytes;
+            const uint32_t tds = tmem + (n & 1 ? C::kColS1 : C::kColS0) + 32;
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mma_ts(tmem + C::kColDQ, tds + 8 * k, sdesc_sw128(ka + k * 2048, kSubBytes, 1024), idQ,
-                   (n > 0 || k > 0) ? 1u : 0u);
+            for (int k = 0; k < 8; ++k)
+              mma_ts(tmem + C::kColDQ, tds + 8 * k, sdesc_sw128(ka + k * 2048, kSubBytes, 1024), idQ,
+                     (n > 0 || k > 0) ? 1u : 0u);
+          }
           tc_commit(&sh.k_empty[st]);
           if (n + 2 < N) ok = issue_S(n + 2);
         }
@@ -467,7 +471,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       if (valid) {
         const float l = lse[li];
         nl = l == -INFINITY ? -INFINITY : -l * kLog2e;
-        dl = delta[li];
+        if constexpr (!DELTA) dl = delta[li];
         pq = layout_pos(P.layout, P.D, L, it.r, a);
       }
       KeyLimit upto, before;  // windowed: the last key seen, the last one before the window
@@ -476,6 +480,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         before = key_limit_of(P, static_cast<int>(pq - P.window));
       }
       const uint64_t nl2 = f2(nl, nl), dl2 = f2(dl, dl);
+      uint64_t row_sum = f2(0.f, 0.f);  // DELTA: of P dP
       const int a_last = WIN ? 0 : min(L, (it.qt + 1) * kQTileRows) - 1;
       int n = 0;
       bool ok = true;
@@ -553,6 +558,15 @@ __global__ void __launch_bounds__(kDqThreads, 1)
 #pragma unroll
           for (int ch = 0; ch < 2; ++ch) {
             const uint32_t (&dp)[32] = dp2[ch];
+            if constexpr (DELTA) {
+              if (some[ch]) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  row_sum = fma2(f2(__uint_as_float(dp[2 * i]), __uint_as_float(dp[2 * i + 1])),
+                                 f2_of_f16x2(pp[16 * ch + i]), row_sum);
+              }
+              continue;
+            }
             uint32_t o[16];
             if (WIN && !some[ch]) {
 #pragma unroll
@@ -583,6 +597,14 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       if (!mbar_wait(&sh.dq_done, dd_phase, abort_flag, tmo, status)) break;
       dd_phase ^= 1;
       tc_fence_after();
+      if constexpr (DELTA) {  // two addends on 0: the same sum in either order
+        const float2 half = f2_split(row_sum);
+        if (valid) atomicAdd(static_cast<float*>(dq) + li, half.x + half.y);
+        tc_fence_before();
+        mbar_arrive(&sh.dq_free);
+        mbar_arrive(&sh.item_empty[kq & 1]);
+        continue;
+      }
       const size_t qoff = (qrow * P.hq + it.h) * DH;
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(dq) + qoff;
       float* dst_acc = static_cast<float*>(dq) + qoff;
@@ -627,20 +649,20 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
   }
-  if constexpr (WIN) wait_for_previous();  // what follows this kernel reads the K/V pass' sums too
+  if constexpr (WIN && !DELTA) wait_for_previous();  // what follows this kernel reads the K/V pass' sums too
 }
 
-template <int DH, bool WIN>
+template <int DH, bool WIN, bool DELTA = false>
 cudaError_t launch_one(const Plan& P, const CUtensorMap& mq, const CUtensorMap& mk,
                        const CUtensorMap& mv, const CUtensorMap& mdo, const float* lse,
                        const float* delta, void* dq, int n_items, int n_sm, cudaStream_t st) {
   using C = DqCfg<DH>;
-  auto kern = ring_bwd_dq_tc_kernel<DH, WIN>;
+  auto kern = ring_bwd_dq_tc_kernel<DH, WIN, DELTA>;
   constexpr int smem = WIN ? C::kSmemWindow : C::kSmemBytes;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int grid = n_items < n_sm ? n_items : n_sm;
-  if constexpr (WIN) {  // starts where the K/V pass leaves an SM free
+  if constexpr (WIN && !DELTA) {  // starts where the K/V pass leaves an SM free
     cudaLaunchAttribute early = {};
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     early.val.programmaticStreamSerializationAllowed = 1;
@@ -659,11 +681,15 @@ cudaError_t launch_one(const Plan& P, const CUtensorMap& mq, const CUtensorMap& 
 
 }  // namespace
 
-cudaError_t launch_bwd_dq_tc(const Plan& P0, const void* q, const void* k, const void* v,
-                             const void* dout, const float* lse, const float* delta, void* dq,
-                             cudaStream_t st) {
-  Plan P = P0;  // re-number the items for query tiles; the next counter of the block
-  P.work_counter = P0.work_counter ? P0.work_counter + 1 : nullptr;
+namespace {
+
+// The tensor maps and the plan of a pass over query tiles (its items renumbered), and its launch:
+// launch(plan, maps of q, k, v, dout, SMs).
+template <typename F>
+cudaError_t over_query_tiles(const Plan& P0, int counter, const void* q, const void* k, const void* v,
+                             const void* dout, F&& launch) {
+  Plan P = P0;
+  P.work_counter = P0.work_counter ? P0.work_counter + counter : nullptr;
   int items = 0;
   for (int i = 0; i < P.n_seqs; ++i) {
     P.seq[i].item_start = items;
@@ -680,11 +706,31 @@ cudaError_t launch_bwd_dq_tc(const Plan& P0, const void* q, const void* k, const
   int dev = 0, n_sm = 0;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
-  if (P.window > 0)
-    return P.head_dim == 128 ? launch_one<128, true>(P, mq, mk, mv, mdo, lse, delta, dq, items, n_sm, st)
-                             : launch_one<64, true>(P, mq, mk, mv, mdo, lse, delta, dq, items, n_sm, st);
-  return P.head_dim == 128 ? launch_one<128, false>(P, mq, mk, mv, mdo, lse, delta, dq, items, n_sm, st)
-                           : launch_one<64, false>(P, mq, mk, mv, mdo, lse, delta, dq, items, n_sm, st);
+  return launch(P, mq, mk, mv, mdo, n_sm);
+}
+
+}  // namespace
+
+cudaError_t launch_bwd_dq_tc(const Plan& P0, const void* q, const void* k, const void* v,
+                             const void* dout, const float* lse, const float* delta, void* dq,
+                             cudaStream_t st) {
+  // the second counter of the block
+  return over_query_tiles(P0, 1, q, k, v, dout, [&](const Plan& P, auto& mq, auto& mk, auto& mv, auto& mdo, int n_sm) {
+    if (P.window > 0)
+      return P.head_dim == 128 ? launch_one<128, true>(P, mq, mk, mv, mdo, lse, delta, dq, P.n_items, n_sm, st)
+                               : launch_one<64, true>(P, mq, mk, mv, mdo, lse, delta, dq, P.n_items, n_sm, st);
+    return P.head_dim == 128 ? launch_one<128, false>(P, mq, mk, mv, mdo, lse, delta, dq, P.n_items, n_sm, st)
+                             : launch_one<64, false>(P, mq, mk, mv, mdo, lse, delta, dq, P.n_items, n_sm, st);
+  });
+}
+
+cudaError_t launch_window_delta_tc(const Plan& P0, const void* q, const void* k, const void* v, const void* dout,
+                                   const float* lse, float* delta, cudaStream_t st) {
+  return over_query_tiles(P0, 2, q, k, v, dout, [&](const Plan& P, auto& mq, auto& mk, auto& mv, auto& mdo, int n_sm) {
+    return P.head_dim == 128
+               ? launch_one<128, true, true>(P, mq, mk, mv, mdo, lse, nullptr, delta, P.n_items, n_sm, st)
+               : launch_one<64, true, true>(P, mq, mk, mv, mdo, lse, nullptr, delta, P.n_items, n_sm, st);
+  });
 }
 
 cudaError_t bwd_dq_status(unsigned int* value, bool reset) {

@@ -37,6 +37,9 @@ int window_bwd_items(Plan& P);
 cudaError_t launch_window_bwd_tc(const Plan& P, const void* q, const void* k, const void* v,
                                  const void* dout, const float* lse, const float* delta, void* dk,
                                  void* dv, cudaStream_t st);
+// delta (cleared before) += sum_j P dP over the visible keys, with the block's third counter.
+cudaError_t launch_window_delta_tc(const Plan& P, const void* q, const void* k, const void* v,
+                                   const void* dout, const float* lse, float* delta, cudaStream_t st);
 // The same on the CUDA cores (float32; bf16 for cross-checks), dq too; and the sum of the slots.
 cudaError_t launch_window_fwd_simt(const Plan& P, int dtype, const void* q, const void* k, const void* v,
                                    void* out, float* lse, cudaStream_t st);

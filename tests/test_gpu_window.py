@@ -199,3 +199,30 @@ def test_sinks_alone_carry_the_far_past():
     without, lse = ra.window_attn_fwd(q, k, v, prob, 100, 0)
     assert (without[0, :100] == 1).all() and (without[0, 100:] == 0).all()
     assert (lse[0, 0, 100:] - np.log(100)).abs().max() < 1e-5
+
+
+@pytest.mark.parametrize("layout,D", [("basic", 1), ("zigzag", 4), ("stripe", 2)])
+@pytest.mark.parametrize("window,sinks,dh", [(2, 0, 64), (3, 1, 128)])
+def test_few_visible_keys_keep_their_gradients(layout, D, window, sinks, dh):
+    """dq and dk of a window of two or three keys have two roundings to bf16, of dS and of the
+    result: each is off by at most half a step of 2^-7 of a number's leading bit, uniformly, so
+    2^-7 / sqrt(12) of the number in the mean square, and both together 2^-7 / sqrt(6) = 0.0032.
+    (Row sums dO . O from the bf16 output would put a third and larger one into dS: 0.0038 with two
+    keys.)"""
+    n, hq, hkv = 768, 4, 2
+    q, k, v, do = (randn(91 + i, 1, n, h, dh) for i, h in enumerate((hq, hkv, hkv, hq)))
+    prob = ra.make_problem(dtype=BF16, layout=layout, causal=True, D=D, hq=hq, hkv=hkv, head_dim=dh, batch=1, seqlen=n)
+    _, _, (dq, dk, _) = run((q, k, v, do), prob, window, sinks)
+    dq, dk = (ra.unshard_tokens(t, prob)[0].double() for t in (dq, dk))
+    i = torch.arange(n, device="cuda")
+    hide = ~((i[None] <= i[:, None]) & ((i[None] > i[:, None] - window) | (i[None] < sinks)))
+    want_q, want_k = torch.zeros_like(dq), torch.zeros_like(dk)
+    for h in range(hq):
+        x, y, z, w = q[0, :, h].double(), k[0, :, h // 2].double(), v[0, :, h // 2].double(), do[0, :, h].double()
+        p = torch.softmax((x @ y.T * dh ** -0.5).masked_fill(hide, -1e300), -1)
+        dp = w @ z.T
+        ds = p * (dp - (p * dp).sum(-1, keepdim=True)) * dh ** -0.5
+        want_q[:, h] = ds @ y
+        want_k[:, h // 2] += ds.T @ x
+    for got, want in ((dq, want_q), (dk, want_k)):
+        assert (got - want).norm() <= 2.0 ** -7 / 6 ** 0.5 * want.norm()
