@@ -40,13 +40,13 @@ FALLBACK_PEAKS = {"hbm_gbs": 6800.0, "bf16_tflops": 1900.0, "bf16_tflops_sustain
 # null until re-measured.
 TRAFFIC = {
     ("ring_bwd_tc (K/V-tile pass)", "long_s131072_gqa32x8_dh128_D16_zigzag"):
-        {"bytes": 55109247744 + 542303488, "source_sha": "38b434ff2fe9b617"},
+        {"bytes": 54650642944 + 541963776, "source_sha": "1148028bd2fe2206"},
     ("ring_fwd_tc", "long_s131072_gqa32x8_dh128_D16_zigzag"):
-        {"bytes": 119308476672 + 1258622464, "source_sha": "55762b8b8add01f5"},
+        {"bytes": 120181535232 + 1258478336, "source_sha": "537770ba4364fabe"},
     ("ring_bwd_dq_tc (dq pass)", "long_s131072_gqa32x8_dh128_D16_zigzag"):
-        {"bytes": 16026640640 + 1060443392, "source_sha": "71a383ba753f0e0c"},
+        {"bytes": 16007171072 + 1060596480, "source_sha": "74dcea1a729ae302"},
     ("merge_kernel", "long_s131072_gqa32x8_dh128_D16_zigzag"):
-        {"bytes": 3255936256 + 2109106688, "source_sha": "8d166f36bdc3345f"},
+        {"bytes": 3255466752 + 2109336064, "source_sha": "533bf0eed829723f"},
 }
 
 
