@@ -256,7 +256,7 @@ Plan* make_window_plan(const ra_problem* p, int which, int window, int sinks) {
   // A sink's rows in one shard: every D-th token, or all of them if the shard is as long.
   P->sink_stride = P->layout == RA_LAYOUT_STRIPE ? ra::ceil_div(P->sinks, P->D) : std::min(P->sinks, longest);
   // Tensor cores: a sink item as long as a K/V tile's window item, the tiles of the window, 8 at
-  // least, since an item's loads and stores cost about one query tile. CUDA cores: a warp for
+  // least, since an item's loads and stores cost about one query tile. CUDA cores: a CTA for
   // every 128 queries, or a 64th of the longest sequence's.
   P->sink_chunk = use_tc(p) ? std::max(8, P->window / ra::kQTileRows + 1)
                             : std::max(1, ra::ceil_div(ra::ceil_div(longest, ra::kQTileRows) * P->D, 64));

@@ -258,7 +258,48 @@ __device__ __forceinline__ void store_lse(const DecodeArgs& A, int b, int h, flo
   A.lse[static_cast<int64_t>(b) * A.hq + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
-// Float32. Four warps, each 16 keys of a unit, four keys at a time; lane l holds elements l, l + 32, ...
+// The four warps' states of a block of query heads into the result of the pair, or into a part of it
+// (units u0 .. u1 - 1).
+template <int HB, int W>
+__device__ __forceinline__ void store_pair(const DecodeArgs& A, const Share& S, int64_t share0, int u0, int u1, int h0,
+                                           int heads, const float (&sm_m)[4][HB], const float (&sm_l)[4][HB],
+                                           const float (&sm_o)[4][HB][W]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, dh = A.dh;
+  const bool whole = u0 == 0 && u1 == S.units;
+  float* part = part_of(A, blockIdx.x, S.u == share0 ? 0 : 1);
+  for (int h = warp; h < heads; h += 4) {
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) M = fmaxf(M, sm_m[w][h]);
+    const float ref = M == -INFINITY ? 0.f : M;
+    float f[4], L = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      f[w] = exp2f(sm_m[w][h] - ref);
+      L += f[w] * sm_l[w][h];
+    }
+    const float inv = whole ? inverse(L) : 1.f;
+    for (int d = lane; d < dh; d += 32) {
+      float x = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) x += f[w] * sm_o[w][h][d];
+      if (whole)
+        static_cast<float*>(A.out)[(static_cast<int64_t>(S.b) * A.hq + h0 + h) * dh + d] = x * inv;
+      else
+        part[h * (dh + 2) + d] = x;
+    }
+    if (lane == 0) {
+      if (whole) {
+        store_lse(A, S.b, h0 + h, M, L);
+      } else {
+        part[h * (dh + 2) + dh] = M;
+        part[h * (dh + 2) + dh + 1] = L;
+      }
+    }
+  }
+}
+
+// Float32, any size and alignment (decode_f32 takes what it can). Four warps, each 16 keys of a unit, four keys at a time; lane l holds elements l, l + 32, ...
 // of q, of the keys and of the sums, for HB query heads.
 template <int HB>
 __global__ void __launch_bounds__(kThreads, HB == 8 ? 2 : 3) decode_simt(const __grid_constant__ DecodeArgs A) {
@@ -365,38 +406,141 @@ __global__ void __launch_bounds__(kThreads, HB == 8 ? 2 : 3) decode_simt(const _
       for (int i = 0; i < NI; ++i) sm_o[warp][h][lane + 32 * i] = o[h][i];
     }
     __syncthreads();
-    const bool whole = u0 == 0 && u1 == S.units;
-    float* part = part_of(A, blockIdx.x, S.u == share0 ? 0 : 1);
-    for (int h = warp; h < heads; h += 4) {
-      float M = -INFINITY;
+    store_pair<HB, 128>(A, S, share0, u0, u1, h0, heads, sm_m, sm_l, sm_o);
+    __syncthreads();
+    if (S.base + S.units >= S.end) break;
+    share_next(A, S);
+  }
+  finish_idle<float>(A);
+}
+
+// Float32 in 16-byte loads: LANES lanes take a key, lane c of a key the pieces c, c + LANES, ... of
+// four elements (E of them; head_dim <= 4 LANES E). The lanes of a key keep a state of their own, so
+// that a weight is worked out once a key and not once a lane, and the states are joined when the
+// pair ends. Keys are loaded a step ahead, their places in the table two. What bounds it is the products'
+// instructions: 16 sequences of 8192 keys of 128, 32/8 heads 203 us (5.3 TB/s), 8/8 heads 166 us
+// (6.5 TB/s), where decode_simt takes 300 and 260.
+template <int HB, int E, int LANES>
+__global__ void __launch_bounds__(kThreads, HB * E > 8 ? 2 : 3) decode_f32(const __grid_constant__ DecodeArgs A) {
+  __shared__ int64_t scan[8];
+  __shared__ float sm_m[4][HB], sm_l[4][HB];
+  __shared__ __align__(16) float sm_o[4][HB][4 * LANES * E];
+  constexpr int KEYS = 32 / LANES, SPLIT = 16 / KEYS;  // a warp's keys at a time, steps of its 16 of a unit
+  Share S;
+  const bool some = share_begin(A, S, scan);
+  const int64_t share0 = S.u;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane % LANES, dh = A.dh;
+  const float* kp = static_cast<const float*>(A.k_pages);
+  const float* vp = static_cast<const float*>(A.v_pages);
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto has = [&](int e) { return 4 * (c + LANES * e) < dh; };
+  while (some) {
+    const int hk = S.pair / A.blocks_per_kv, blk = S.pair % A.blocks_per_kv;
+    const int g0 = blk * HB, heads = min(HB, A.group - g0), h0 = hk * A.group + g0;
+    const Visible vis = visible(A, S.b, true);
+    const int u0 = static_cast<int>(S.u - S.base);
+    const int u1 = static_cast<int>(min(static_cast<int64_t>(S.units), S.end - S.base));
+    float4 q[HB][E], o[HB][E];
+    float m[HB], l[HB];
 #pragma unroll
-      for (int w = 0; w < 4; ++w) M = fmaxf(M, sm_m[w][h]);
-      const float ref = M == -INFINITY ? 0.f : M;
-      float f[4], L = 0.f;
+    for (int h = 0; h < HB; ++h) {
+      const float* row = static_cast<const float*>(A.q) + (static_cast<int64_t>(S.b) * A.hq + h0 + h) * dh;
+      m[h] = -INFINITY;
+      l[h] = 0.f;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        f[w] = exp2f(sm_m[w][h] - ref);
-        L += f[w] * sm_l[w][h];
+      for (int e = 0; e < E; ++e) {
+        o[h][e] = zero;
+        q[h][e] = h < heads && has(e) ? *reinterpret_cast<const float4*>(row + 4 * (c + LANES * e)) : zero;
       }
-      const float inv = whole ? inverse(L) : 1.f;
-      for (int d = lane; d < dh; d += 32) {
-        float x = 0.f;
+    }
+    const int steps = SPLIT * (u1 - u0);
+    auto key_of = [&](int i) { return (u0 + i / SPLIT) * kUnit + warp * 16 + i % SPLIT * KEYS + lane / LANES; };
+    auto seen = [&](int i) { return i < steps && key_of(i) < vis.vis; };
+    auto place = [&](int i) { return seen(i) ? key_row(A, S.b, vis, key_of(i)) + hk * A.head_stride : int64_t(-1); };
+    float4 kn[E], vn[E];
+    auto load = [&](int64_t at) {
 #pragma unroll
-        for (int w = 0; w < 4; ++w) x += f[w] * sm_o[w][h][d];
-        if (whole)
-          static_cast<float*>(A.out)[(static_cast<int64_t>(S.b) * A.hq + h0 + h) * dh + d] = x * inv;
-        else
-          part[h * (dh + 2) + d] = x;
+      for (int e = 0; e < E; ++e) {
+        const bool in = at >= 0 && has(e);
+        kn[e] = in ? *reinterpret_cast<const float4*>(kp + at + 4 * (c + LANES * e)) : zero;
+        vn[e] = in ? *reinterpret_cast<const float4*>(vp + at + 4 * (c + LANES * e)) : zero;
       }
-      if (lane == 0) {
-        if (whole) {
-          store_lse(A, S.b, h0 + h, M, L);
-        } else {
-          part[h * (dh + 2) + dh] = M;
-          part[h * (dh + 2) + dh + 1] = L;
+    };
+    load(place(0));
+    int64_t next = place(1);
+    for (int i = 0; i < steps; ++i) {
+      float4 v[E];
+      float x[HB];
+#pragma unroll
+      for (int h = 0; h < HB; ++h) {
+        x[h] = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          x[h] += q[h][e].x * kn[e].x;
+          x[h] += q[h][e].y * kn[e].y;
+          x[h] += q[h][e].z * kn[e].z;
+          x[h] += q[h][e].w * kn[e].w;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = vn[e];
+      load(next);
+      next = place(i + 2);
+      const bool hidden = !seen(i);
+#pragma unroll
+      for (int h = 0; h < HB; ++h) {
+#pragma unroll
+        for (int w = LANES / 2; w > 0; w >>= 1) x[h] += __shfl_xor_sync(0xffffffffu, x[h], w);
+        x[h] = hidden ? -INFINITY : x[h] * A.scale_log2;
+        const float mx = fmaxf(m[h], x[h]), ref = mx == -INFINITY ? 0.f : mx;
+        if (__any_sync(0xffffffffu, mx > m[h])) {
+          const float alpha = exp2f(m[h] - ref);
+          m[h] = mx;
+          l[h] *= alpha;
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            o[h][e].x *= alpha;
+            o[h][e].y *= alpha;
+            o[h][e].z *= alpha;
+            o[h][e].w *= alpha;
+          }
+        }
+        const float p = exp2f(x[h] - ref);  // 0 for a hidden key, whose v is 0 too
+        l[h] += p;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          o[h][e].x += p * v[e].x;
+          o[h][e].y += p * v[e].y;
+          o[h][e].z += p * v[e].z;
+          o[h][e].w += p * v[e].w;
         }
       }
     }
+#pragma unroll
+    for (int h = 0; h < HB; ++h) {
+      float M = m[h];
+#pragma unroll
+      for (int w = LANES; w < 32; w <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
+      const float f = exp2f(m[h] - (M == -INFINITY ? 0.f : M));
+      l[h] *= f;
+#pragma unroll
+      for (int w = LANES; w < 32; w <<= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], w);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        float y[4] = {o[h][e].x * f, o[h][e].y * f, o[h][e].z * f, o[h][e].w * f};
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+          for (int w = LANES; w < 32; w <<= 1) y[n] += __shfl_xor_sync(0xffffffffu, y[n], w);
+        if (lane < LANES) *reinterpret_cast<float4*>(&sm_o[warp][h][4 * (c + LANES * e)]) = make_float4(y[0], y[1], y[2], y[3]);
+      }
+      if (lane == 0) {
+        sm_m[warp][h] = M;
+        sm_l[warp][h] = l[h];
+      }
+    }
+    __syncthreads();
+    store_pair<HB, 4 * LANES * E>(A, S, share0, u0, u1, h0, heads, sm_m, sm_l, sm_o);
     __syncthreads();
     if (S.base + S.units >= S.end) break;
     share_next(A, S);
@@ -844,6 +988,35 @@ cudaError_t launch_mma(const DecodeArgs& A, int grid, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+// Whether every row of a float32 call starts on 16 bytes.
+bool wide_f32(const DecodeArgs& A) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(A.q) | reinterpret_cast<uintptr_t>(A.k_pages) |
+                      reinterpret_cast<uintptr_t>(A.v_pages);
+  return p % 16 == 0 && A.dh % 4 == 0 && A.page_stride % 4 == 0 && A.slot_stride % 4 == 0 && A.head_stride % 4 == 0;
+}
+
+// Lanes of a key, and pieces of a lane. Four lanes where their pieces fit the registers: half the
+// steps of eight, and with them half the sums over lanes and half the weights (16 sequences of 16384
+// keys of 64, 32/8 heads: 205 against 246 us).
+int f32_lanes(int dh) { return dh <= 64 ? 4 : 8; }
+int f32_pieces(int dh) { return (dh + 4 * f32_lanes(dh) - 1) / (4 * f32_lanes(dh)); }
+
+template <int HB>
+void launch_f32(const DecodeArgs& A, int grid, cudaStream_t st) {
+  const int e = f32_pieces(A.dh);
+  if (f32_lanes(A.dh) == 8) {
+    if (e == 3) decode_f32<HB, 3, 8><<<grid, kThreads, 0, st>>>(A);
+    else decode_f32<HB, 4, 8><<<grid, kThreads, 0, st>>>(A);
+  } else {
+    switch (e) {
+      case 1: decode_f32<HB, 1, 4><<<grid, kThreads, 0, st>>>(A); break;
+      case 2: decode_f32<HB, 2, 4><<<grid, kThreads, 0, st>>>(A); break;
+      case 3: decode_f32<HB, 3, 4><<<grid, kThreads, 0, st>>>(A); break;
+      default: decode_f32<HB, 4, 4><<<grid, kThreads, 0, st>>>(A); break;
+    }
+  }
+}
+
 template <typename T>
 cudaError_t launch_join(cudaLaunchConfig_t& cfg, const DecodeArgs& A, int grid) {
   const int64_t pairs = static_cast<int64_t>(A.n_seqs) * A.hkv * A.blocks_per_kv;
@@ -860,8 +1033,18 @@ cudaError_t launch(DecodeArgs& A, int dtype, cudaStream_t st) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  const int grid = ctas_per_sm(dtype, A.dh) * (n_sm < kSms ? n_sm : kSms);
-  if (dtype == RA_F32) {
+  int per_sm = ctas_per_sm(dtype, A.dh);
+  if (dtype == RA_F32 && (wide_f32(A) ? A.block_heads * f32_pieces(A.dh) > 8 : A.block_heads == 8))
+    per_sm = 2;  // their registers
+  const int grid = per_sm * (n_sm < kSms ? n_sm : kSms);
+  if (dtype == RA_F32 && wide_f32(A)) {
+    switch (A.block_heads) {
+      case 1: launch_f32<1>(A, grid, st); break;
+      case 2: launch_f32<2>(A, grid, st); break;
+      default: launch_f32<4>(A, grid, st); break;
+    }
+    e = cudaGetLastError();
+  } else if (dtype == RA_F32) {
     switch (A.block_heads) {
       case 1: decode_simt<1><<<grid, kThreads, 0, st>>>(A); break;
       case 2: decode_simt<2><<<grid, kThreads, 0, st>>>(A); break;
@@ -959,6 +1142,8 @@ extern "C" int ra_paged_attn_decode(const ra_paged_cache* c, int hq, float scale
   A.group = hq / c->hkv;
   A.dh = c->head_dim;
   A.block_heads = heads_of_block(c->dtype, A.group);
+  // the 16-byte kernel's states of four heads of 128 fill a thread's registers
+  if (c->dtype == RA_F32 && A.block_heads > 4 && wide_f32(A)) A.block_heads = 4;
   A.blocks_per_kv = (A.group + A.block_heads - 1) / A.block_heads;
   A.window = window;
   A.sinks = sinks;

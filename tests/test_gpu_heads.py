@@ -297,6 +297,13 @@ DECODE_CASES = [  # dtype, hq, hkv, dh, page, lens, window, sinks, order
     (F32, 8, 1, 128, 64, [1500, 64], 700, 4, "nhpd"),
     (F32, 17, 1, 33, 1, [70], 0, 0, "nphd"),
     (F32, 2, 2, 1, 16, [40], 7, 1, "nphd"),
+    (F32, 8, 8, 128, 16, [1, 15, 16, 17, 0, 300, 64, 65], 0, 0, "nphd"),
+    (F32, 32, 8, 64, 64, [700, 3], 0, 0, "nphd"),
+    (F32, 12, 4, 96, 48, [5, 63, 64, 65, 2000], 64, 5, "nhpd"),
+    (F32, 4, 2, 48, 7, [33, 1000, 2], 0, 0, "nhpd"),
+    (F32, 16, 2, 32, 16, [40, 1, 90, 0, 500], 30, 2, "nphd"),
+    (F32, 5, 1, 100, 16, [129, 0, 4096], 100, 3, "nphd"),
+    (F32, 2, 1, 4, 3, [40], 0, 0, "nphd"),
 ]
 
 
