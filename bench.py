@@ -40,13 +40,13 @@ FALLBACK_PEAKS = {"hbm_gbs": 6800.0, "bf16_tflops": 1900.0, "bf16_tflops_sustain
 # null until re-measured.
 TRAFFIC = {
     ("ring_bwd_tc (K/V-tile pass)", "long_s131072_gqa32x8_dh128_D16_zigzag"):
-        {"bytes": 54650642944 + 541963776, "source_sha": "1148028bd2fe2206"},
+        {"bytes": 54524749568 + 541799936, "source_sha": "7613bd53cc15c73d"},
     ("ring_fwd_tc", "long_s131072_gqa32x8_dh128_D16_zigzag"):
-        {"bytes": 120181535232 + 1258478336, "source_sha": "537770ba4364fabe"},
+        {"bytes": 119736225536 + 1257460480, "source_sha": "3c623c5defece725"},
     ("ring_bwd_dq_tc (dq pass)", "long_s131072_gqa32x8_dh128_D16_zigzag"):
-        {"bytes": 16007171072 + 1060596480, "source_sha": "74dcea1a729ae302"},
+        {"bytes": 16148093952 + 1059086848, "source_sha": "62205b05bd9ec6c6"},
     ("merge_kernel", "long_s131072_gqa32x8_dh128_D16_zigzag"):
-        {"bytes": 3255466752 + 2109336064, "source_sha": "533bf0eed829723f"},
+        {"bytes": 3255625472 + 2109254656, "source_sha": "022f255206ff4139"},
 }
 
 
