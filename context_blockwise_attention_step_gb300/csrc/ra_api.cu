@@ -469,10 +469,22 @@ int ra_block_attn_bwd(const ra_problem* p, int rank, int step, const void* q, co
   return e == cudaSuccess ? ok() : cuda_fail(e, "block backward launch");
 }
 
+// Whether the items of a persistent kernel should come from a counter: with one at most for every
+// SM the static stride gives out the same ones, and clearing the counter is a call of its own (a
+// forward of 256 tokens from the host: 13 against 17 us).
+static bool wants_counter(int64_t items) {
+  int dev = 0, n_sm = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return true;
+  return cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || items > n_sm;
+}
+
 size_t ra_window_workspace_bytes(const ra_problem* p, int window, int sinks, int which) try {
   if (validate_window(p, window, sinks) != RA_OK) return 0;
   if (effective_window(p, window) == 0) return which == 0 || which == 1 ? ra_workspace_bytes(p, which) : 0;
-  if (which == 0) return sched_bytes(p);
+  if (which == 0) {
+    PlanHolder P(make_window_plan(p, 0, window, sinks));
+    return wants_counter(P.p->n_items) ? sched_bytes(p) : 0;
+  }
   if (which == 1) return delta_bytes(p) + sched_bytes(p) + sink_bytes(p, window, sinks);
   return 0;
 } catch (const std::bad_alloc&) {
@@ -498,7 +510,7 @@ int ra_window_attn_fwd(const ra_problem* p, int window, int sinks, const void* q
     return fail(RA_ERR_INVALID_ARG, "workspace must be a 256-byte aligned device pointer");
   PlanHolder P(make_window_plan(p, 0, window, sinks));
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (workspace != nullptr && use_tc(p) && workspace_bytes >= sched_bytes(p)) {
+  if (workspace != nullptr && use_tc(p) && workspace_bytes >= sched_bytes(p) && wants_counter(P.p->n_items)) {
     P.p->work_counter = static_cast<int32_t*>(workspace);
     const cudaError_t c = cudaMemsetAsync(workspace, 0, sizeof(int32_t), st);
     if (c != cudaSuccess) return cuda_fail(c, "item counter clear");
@@ -532,8 +544,11 @@ int ra_window_attn_bwd(const ra_problem* p, int window, int sinks, const void* q
   PlanHolder P(make_window_plan(p, 1, window, sinks));
   P.p->sink_sums = reinterpret_cast<float*>(at + sched_bytes(p));
   ra::window_bwd_items(*P.p);
+  int64_t query_items = 0;
+  for (int i = 0; i < P.p->n_seqs; ++i)
+    query_items += static_cast<int64_t>(ra::ceil_div(P.p->seq[i].L, ra::kQTileRows)) * p->D * p->hq;
   cudaError_t e = cudaSuccess;
-  if (use_tc(p)) {
+  if (use_tc(p) && wants_counter(std::max<int64_t>(query_items, P.p->n_items))) {
     // of the K/V pass, of the dq pass, and of the row sums' pass
     P.p->work_counter = reinterpret_cast<int32_t*>(at);
     e = cudaMemsetAsync(at, 0, 3 * sizeof(int32_t), st);

@@ -95,9 +95,10 @@ def _made_like(t: torch.Tensor, made: list) -> torch.Tensor:
 
 
 def _workspace(workspace, need: int, like: torch.Tensor, made: list):
-    """The given workspace, or a new one on ``like``'s device; and its bytes."""
+    """The given workspace, or a new one on ``like``'s device (None if none is needed); and its bytes."""
     if workspace is None:
-        made.append(workspace := torch.empty(max(1, need), device=like.device, dtype=torch.uint8))
+        if need > 0:
+            made.append(workspace := torch.empty(need, device=like.device, dtype=torch.uint8))
         return workspace, need
     if workspace.get_device() != like.get_device() or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {like.device}")
