@@ -40,13 +40,13 @@ FALLBACK_PEAKS = {"hbm_gbs": 6800.0, "bf16_tflops": 1900.0, "bf16_tflops_sustain
 # null until re-measured.
 TRAFFIC = {
     ("ring_bwd_tc (K/V-tile pass)", "long_s131072_gqa32x8_dh128_D16_zigzag"):
-        {"bytes": 54524749568 + 541799936, "source_sha": "7613bd53cc15c73d"},
+        {"bytes": 54709244672 + 541931520, "source_sha": "39289a7e91f00299"},
     ("ring_fwd_tc", "long_s131072_gqa32x8_dh128_D16_zigzag"):
-        {"bytes": 119736225536 + 1257460480, "source_sha": "3c623c5defece725"},
+        {"bytes": 117793662208 + 1258559744, "source_sha": "13e1b9113b74863a"},
     ("ring_bwd_dq_tc (dq pass)", "long_s131072_gqa32x8_dh128_D16_zigzag"):
-        {"bytes": 16148093952 + 1059086848, "source_sha": "62205b05bd9ec6c6"},
+        {"bytes": 16063049216 + 1060016384, "source_sha": "c808724a08ad9770"},
     ("merge_kernel", "long_s131072_gqa32x8_dh128_D16_zigzag"):
-        {"bytes": 3255625472 + 2109254656, "source_sha": "022f255206ff4139"},
+        {"bytes": 3255436544 + 2109264896, "source_sha": "5314b5707f03b07b"},
 }
 
 
