@@ -559,8 +559,12 @@ __global__ void __launch_bounds__(kThreads, HB * E > 8 ? 2 : 3) decode_f32(const
 // keeps running max, sum and O = P V in registers. The ring runs on over the end of a pair.
 // S = Q K^T as [heads x keys], so that P is the A operand of P V without any exchange. O is
 // rescaled only when a row's max grows by more than 2^8 (the same values in exact arithmetic).
-// P is rounded to bf16 for the product (relative 2^-9 on average over hundreds of keys); its
-// sum is taken before, in float32.
+// P is given to the product as two bf16 numbers, its rounding and the rounding of what that leaves
+// out: 2^-16 of P, so that the result's own rounding is the only one that shows (one bf16 number
+// alone put 0.0012 of `out` beside that rounding's 0.0017, relative L2). Up to 8 query heads the
+// second number takes the product's empty rows and costs no instruction. The sums of the second
+// numbers are kept apart until a pair ends, for an infinite v takes its sign from P alone: there
+// they count for nothing. P's own sum is taken before, in float32.
 //
 // WIDE: more than 8 query heads per K/V head (rows 8..15 of the products are used).
 template <int DH, bool WIDE>
@@ -704,11 +708,11 @@ __global__ void __launch_bounds__(kThreads, (MmaCfg<DH, WIDE>::CTAS)) decode_mma
         const int r = g + (i >> 1) * 8, d = 16 * k + (i & 1) * 8 + 2 * c;
         qa[k][i] = r < heads ? *reinterpret_cast<const uint32_t*>(q + r * DH + d) : 0u;
       }
-    float o[DH / 8][WIDE ? 4 : 2];
+    float o[DH / 8][4], small[DH / 8][4];  // P V, and that of P's second numbers (not WIDE: o's rows 8..15)
 #pragma unroll
     for (int n = 0; n < DH / 8; ++n)
 #pragma unroll
-      for (int i = 0; i < (WIDE ? 4 : 2); ++i) o[n][i] = 0.f;
+      for (int i = 0; i < 4; ++i) o[n][i] = small[n][i] = 0.f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
     const int u0 = at.u;
@@ -734,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, (MmaCfg<DH, WIDE>::CTAS)) decode_mma
             mma_bf16(s[1], qa[k][0], 0u, qa[k][1], 0u, b[2], b[3]);
           }
         }
-        uint32_t p[2][2];  // [row half][key half]
+        uint32_t p[2][2], rest[2][2];  // [row half][key half]
         const bool part = key0 + 16 > at.vis.vis;
 #pragma unroll
         for (int r = 0; r < (WIDE ? 2 : 1); ++r) {
@@ -756,6 +760,8 @@ __global__ void __launch_bounds__(kThreads, (MmaCfg<DH, WIDE>::CTAS)) decode_mma
             for (int n = 0; n < DH / 8; ++n) {
               o[n][2 * r] *= alpha;
               o[n][2 * r + 1] *= alpha;
+              (WIDE ? small[n][2 * r] : o[n][2]) *= alpha;
+              (WIDE ? small[n][2 * r + 1] : o[n][3]) *= alpha;
             }
           }
           const float ref = m[r] == -INFINITY ? 0.f : m[r];
@@ -765,6 +771,10 @@ __global__ void __launch_bounds__(kThreads, (MmaCfg<DH, WIDE>::CTAS)) decode_mma
           l[r] += (e[0] + e[1]) + (e[2] + e[3]);
           p[r][0] = pack_bf16x2(e[0], e[1]);
           p[r][1] = pack_bf16x2(e[2], e[3]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            rest[r][i] = pack_bf16x2(e[2 * i] - __uint_as_float(p[r][i] << 16),
+                                     e[2 * i + 1] - __uint_as_float(p[r][i] & 0xffff0000u));
         }
         const uint32_t va = vs + ((lane & 7) + ((lane >> 3) & 1) * 8) * C::PITCH + (lane >> 4) * 16;
 #pragma unroll
@@ -774,15 +784,11 @@ __global__ void __launch_bounds__(kThreads, (MmaCfg<DH, WIDE>::CTAS)) decode_mma
           if constexpr (WIDE) {
             mma_bf16(o[2 * d], p[0][0], p[1][0], p[0][1], p[1][1], b[0], b[1]);
             mma_bf16(o[2 * d + 1], p[0][0], p[1][0], p[0][1], p[1][1], b[2], b[3]);
+            mma_bf16(small[2 * d], rest[0][0], rest[1][0], rest[0][1], rest[1][1], b[0], b[1]);
+            mma_bf16(small[2 * d + 1], rest[0][0], rest[1][0], rest[0][1], rest[1][1], b[2], b[3]);
           } else {
-            float t[4] = {o[2 * d][0], o[2 * d][1], 0.f, 0.f};
-            mma_bf16(t, p[0][0], 0u, p[0][1], 0u, b[0], b[1]);
-            o[2 * d][0] = t[0];
-            o[2 * d][1] = t[1];
-            float w[4] = {o[2 * d + 1][0], o[2 * d + 1][1], 0.f, 0.f};
-            mma_bf16(w, p[0][0], 0u, p[0][1], 0u, b[2], b[3]);
-            o[2 * d + 1][0] = w[0];
-            o[2 * d + 1][1] = w[1];
+            mma_bf16(o[2 * d], p[0][0], rest[0][0], p[0][1], rest[0][1], b[0], b[1]);
+            mma_bf16(o[2 * d + 1], p[0][0], rest[0][0], p[0][1], rest[0][1], b[2], b[3]);
           }
         }
       }
@@ -790,6 +796,10 @@ __global__ void __launch_bounds__(kThreads, (MmaCfg<DH, WIDE>::CTAS)) decode_mma
       stage = stage + 1 == NS ? 0 : stage + 1;
     }
 
+    auto sum_of = [&](int n, int r, int i) {  // of row half r, with what is finite of the second numbers'
+      const float x = WIDE ? small[n][2 * r + i] : o[n][2 + i];
+      return o[n][2 * r + i] + (fabsf(x) <= 3.402823466e38f ? x : 0.f);
+    };
     // the four warps' states into one, CHUNK heads at a time
 #pragma unroll
     for (int r = 0; r < (WIDE ? 2 : 1); ++r) {
@@ -810,7 +820,7 @@ __global__ void __launch_bounds__(kThreads, (MmaCfg<DH, WIDE>::CTAS)) decode_mma
 #pragma unroll
           for (int n = 0; n < DH / 8; ++n)
             *reinterpret_cast<float2*>(joined + (warp * C::CHUNK + h) * DH + 8 * n + 2 * c) =
-                make_float2(o[n][2 * r], o[n][2 * r + 1]);
+                make_float2(sum_of(n, r, 0), sum_of(n, r, 1));
         }
       }
       __syncthreads();
