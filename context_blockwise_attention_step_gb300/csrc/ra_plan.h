@@ -187,24 +187,24 @@ RA_HD int tile_at(const TileSet& t, int i) {
   i -= t.sink;
   return i < t.n0 ? t.s0 + i : t.s1 + i - t.n0;
 }
-// Adds the tiles of local rows lo .. hi (which follow those added before).
-RA_HD void add_tiles(TileSet& t, int lo, int hi, int tile_rows) {
-  if (hi < lo) return;
-  int s = lo / tile_rows;
-  const int e = hi / tile_rows;
-  if (t.n0 == 0) {
+// Adds the tiles s .. e, which begin in or behind the last run added before; a third run does not
+// come up (both_tiles).
+RA_HD void add_run(TileSet& t, int s, int e) {
+  int& s_last = t.n1 > 0 ? t.s1 : t.s0;
+  int& n_last = t.n1 > 0 ? t.n1 : t.n0;
+  if (n_last == 0) {
     t.s0 = s;
     t.n0 = e - s + 1;
-    return;
-  }
-  if (s < t.s0 + t.n0) s = t.s0 + t.n0;
-  if (s > e) return;
-  if (s == t.s0 + t.n0) {
-    t.n0 += e - s + 1;
+  } else if (s <= s_last + n_last || t.n1 > 0) {
+    if (e >= s_last + n_last) n_last = e - s_last + 1;
   } else {
     t.s1 = s;
     t.n1 = e - s + 1;
   }
+}
+// Adds the tiles of local rows lo .. hi (which follow those added before).
+RA_HD void add_tiles(TileSet& t, int lo, int hi, int tile_rows) {
+  if (lo <= hi) add_run(t, lo / tile_rows, hi / tile_rows);
 }
 // Rows x0 .. x1 of a zigzag shard that lie on both sides of its two chunks have positions far
 // apart: they are looked at as two runs, split at the second chunk.
@@ -226,6 +226,19 @@ RA_HD TileSet window_kv_tiles(const Plan& P, int L, int r, int j, int a0, int a1
   add_tiles(t, first_query(P.layout, P.D, L, j, layout_pos(P.layout, P.D, L, r, from) - P.window + 1),
             limit, kKvTileRows);
   t.sink = sink_rows(P, L, j) > 0 && (t.n0 == 0 || t.s0 > 0) ? 1 : 0;
+  return t;
+}
+
+// The tiles that one or both of a block's two query tiles see: a, whose rows come first, and b. It
+// is not the set of the block's first and last row: in the stripe layout neighbouring rows are D
+// positions apart, and with a window below D a key can lie between the windows of both query tiles,
+// alone in its tile. The union has two runs at most: zigzag rows of one chunk see one run together,
+// the rows of basic and stripe shards one in each query tile.
+RA_HD TileSet both_tiles(const TileSet& a, const TileSet& b) {
+  TileSet t = a;
+  if (b.n0 > 0) add_run(t, b.s0, b.s0 + b.n0 - 1);
+  if (b.n1 > 0) add_run(t, b.s1, b.s1 + b.n1 - 1);
+  t.sink = (a.sink || b.sink) && (t.n0 == 0 || t.s0 > 0) ? 1 : 0;
   return t;
 }
 

@@ -102,28 +102,29 @@ struct WinSlot {
   WinSeg seg[kMaxWindowShards];
 };
 
-// Fills in a slot for query rows a0 .. a1 of rank r (the whole warp); with HALVES also the tiles
-// of the block's two query tiles, one after the other in half[2 * kMaxWindowShards].
+// Fills in a slot for query rows a0 .. a1 of rank r (the whole warp): of one query tile, or with HALVES
+// of two, whose own tiles go to half[2 * kMaxWindowShards], one after the other.
 template <bool HALVES>
 __device__ __forceinline__ void fill_slot(WinSlot& w, WinSeg* half, const Plan& P, int seq, int h, int r, int a0,
                                           int a1) {
   const SeqDesc& sd = P.seq[seq];
-  const int lane = threadIdx.x & 31, L = sd.L;
+  const int lane = threadIdx.x & 31, L = sd.L, mid = HALVES ? min(a1 + 1, a0 + kQTileRows) : a1 + 1;
   int nseg = 0, tiles = 0;
   for (int base = 0; base < P.D; base += 32) {
-    TileSet t = {0, 0, 0, 0, 0};
+    TileSet t = {0, 0, 0, 0, 0}, t0 = t, t1 = t;
     const int j = base + lane < P.D ? shard_at_step(P.D, r, base + lane) : 0;
-    if (base + lane < P.D) t = window_kv_tiles(P, L, r, j, a0, a1);
+    if (base + lane < P.D) {
+      t = t0 = window_kv_tiles(P, L, r, j, a0, mid - 1);
+      if (HALVES && mid <= a1) t = both_tiles(t0, t1 = window_kv_tiles(P, L, r, j, mid, a1));
+    }
     const int n = tile_count(t);
     const unsigned some = __ballot_sync(0xffffffffu, n > 0);
     if (n > 0) {
       const int at = nseg + __popc(some & ((1u << lane) - 1u)), sk = sink_rows(P, L, j);
       w.seg[at] = seg_of(j, sk, t);
-      if constexpr (HALVES) {  // and of the block's two query tiles
-        const int mid = min(a1 + 1, a0 + kQTileRows);
-        half[at] = seg_of(j, sk, window_kv_tiles(P, L, r, j, a0, mid - 1));
-        half[kMaxWindowShards + at] =
-            seg_of(j, sk, mid <= a1 ? window_kv_tiles(P, L, r, j, mid, a1) : TileSet{0, 0, 0, 0, 0});
+      if constexpr (HALVES) {
+        half[at] = seg_of(j, sk, t0);
+        half[kMaxWindowShards + at] = seg_of(j, sk, t1);
       }
     }
     nseg += __popc(some);
