@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       int64_t pq = 0;
       if (valid) {
         const float l = lse[li];
-        nl = l == -INFINITY ? -INFINITY : -l * kLog2e;
+        nl = l == -INFINITY ? -INFINITY : -l * kLog2e + (WIN ? kWeightShift : 0.f);
         if constexpr (!DELTA) dl = delta[li];
         pq = layout_pos(P.layout, P.D, L, it.r, a);
       }
@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       tc_fence_after();
       if constexpr (DELTA) {  // two addends on 0: the same sum in either order
         const float2 half = f2_split(row_sum);
-        if (valid) atomicAdd(static_cast<float*>(dq) + li, half.x + half.y);
+        if (valid) atomicAdd(static_cast<float*>(dq) + li, (half.x + half.y) * kWeightUnit);
         tc_fence_before();
         mbar_arrive(&sh.dq_free);
         mbar_arrive(&sh.item_empty[kq & 1]);
@@ -608,6 +608,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       const size_t qoff = (qrow * P.hq + it.h) * DH;
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(dq) + qoff;
       float* dst_acc = static_cast<float*>(dq) + qoff;
+      const float mul = P.scale * (WIN ? kWeightUnit : 1.f);
 #pragma unroll
       for (int c = 0; c < DH / 64; ++c) {
         const int col = wg * (DH / 2) + 32 * c;
@@ -629,10 +630,10 @@ __global__ void __launch_bounds__(kDqThreads, 1)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             uint4 u;
-            u.x = pack_bf16x2(__uint_as_float(rr[8 * q + 0]) * P.scale, __uint_as_float(rr[8 * q + 1]) * P.scale);
-            u.y = pack_bf16x2(__uint_as_float(rr[8 * q + 2]) * P.scale, __uint_as_float(rr[8 * q + 3]) * P.scale);
-            u.z = pack_bf16x2(__uint_as_float(rr[8 * q + 4]) * P.scale, __uint_as_float(rr[8 * q + 5]) * P.scale);
-            u.w = pack_bf16x2(__uint_as_float(rr[8 * q + 6]) * P.scale, __uint_as_float(rr[8 * q + 7]) * P.scale);
+            u.x = pack_bf16x2(__uint_as_float(rr[8 * q + 0]) * mul, __uint_as_float(rr[8 * q + 1]) * mul);
+            u.y = pack_bf16x2(__uint_as_float(rr[8 * q + 2]) * mul, __uint_as_float(rr[8 * q + 3]) * mul);
+            u.z = pack_bf16x2(__uint_as_float(rr[8 * q + 4]) * mul, __uint_as_float(rr[8 * q + 5]) * mul);
+            u.w = pack_bf16x2(__uint_as_float(rr[8 * q + 6]) * mul, __uint_as_float(rr[8 * q + 7]) * mul);
             d[q] = u;
           }
         }

@@ -336,7 +336,7 @@ __device__ __forceinline__ void ds_chunk(uint32_t tY, int c0, const float* dl,
   ds_from<CH, kWithDQ>(dp, tY, c0, dl, pp, ds_row, row);
 }
 
-// P^T = 2^(S^T * scale*log2e - lse*log2e) for the query columns [c0 + 32*CH, +32), from
+// P^T = 2^(S^T * scale*log2e - lse*log2e) (windowed: times 2^kWeightShift) for the query columns [c0 + 32*CH, +32), from
 // their S^T registers: columns before `lo` (queries that may not see this key; windowed: and
 // those from `hi` on) are zero;
 // columns past the sequence piece have -lse*log2e = -inf from the loader and give 0. The
@@ -832,7 +832,7 @@ __global__ void __launch_bounds__(bwd_threads<kWithDQ>(), 1)
           float n = -INFINITY, d = 0.f;
           if (q0 + c < wk.L) {
             const float l = lse[li0 + c];
-            n = l == -INFINITY ? -INFINITY : -l * kLog2e;
+            n = l == -INFINITY ? -INFINITY : -l * kLog2e + (WIN ? kWeightShift : 0.f);
             d = delta[li0 + c];
           }
           nl[c] = n;
@@ -1001,7 +1001,7 @@ __global__ void __launch_bounds__(bwd_threads<kWithDQ>(), 1)
       ad_phase ^= 1;
       tc_fence_after();
       const uint32_t tacc = tmem + lane_off + (wg == 0 ? C::kColDK : C::kColDV);
-      const float mul = wg == 0 ? P.scale : 1.f;
+      const float mul = (wg == 0 ? P.scale : 1.f) * (WIN ? kWeightUnit : 1.f);
 #pragma unroll
       for (int c = 0; c < DH / 32; ++c) {
         uint32_t rr[32];

@@ -317,8 +317,8 @@ __device__ __forceinline__ uint64_t f2_of_bf16x2(uint32_t v) {
   return f2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
 }
 
-// The same for a pair of halves: numbers up to 1 to a relative 2^-11 (below 2^-14 to an absolute
-// 2^-25), where bf16 has 2^-9.
+// The same for a pair of halves: numbers up to 65504 to a relative 2^-11 (below 2^-14 to an absolute
+// 2^-25), where bf16 has 2^-8.
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));

@@ -80,6 +80,13 @@ __device__ __forceinline__ int limit_in(const Plan& P, int L, int j, const KeyLi
   return max(-1, min(b, L - 1));
 }
 
+// The weights P of the backward kernels, up to the products with dS, are kept as halves (2^-11) times
+// 2^kWeightShift, and the results multiplied by kWeightUnit: half numbers lose bits below 2^-14, so
+// that without it a weight of 2^-18, one of 2^18 equal keys or of a key whose score lies 12 below the
+// others', was off by 2^-8, and one of 2^-26 was 0. Now weights keep their 11 bits down to 2^-28 and
+// are 0 below 2^-39. There is room for P up to 4, where rounding of an lse of millions would take it.
+constexpr float kWeightShift = 14.f, kWeightUnit = 1.f / 16384.f;
+
 // ---- query blocks: what the producer warp works out of an item ahead of the other warps, which
 // would have to wait for the arithmetic (12000 cycles of a 60000-cycle item, measured) ----------
 struct WinSeg {
