@@ -179,8 +179,8 @@ __device__ __forceinline__ void apply(const LaneTurn& t, float* row, int dh, int
     if (lane + 32 * i < dh) row[lane + 32 * i] = x[i];
   __syncwarp();
 #pragma unroll
-  for (int i = 0; i < kPerLane; ++i)
-    if (lane + 32 * i < dh) x[i] = t.cs[i] * x[i] + t.sn[i] * row[t.other[i]];
+  for (int i = 0; i < kPerLane; ++i)  // (what is not rotated stays as it is, infinities too)
+    if (lane + 32 * i < dh && t.other[i] != lane + 32 * i) x[i] = t.cs[i] * x[i] + t.sn[i] * row[t.other[i]];
 }
 template <typename T>
 __device__ __forceinline__ void load_lane(const T* p, int dh, int lane, float (&x)[kPerLane]) {
@@ -442,21 +442,38 @@ __device__ __forceinline__ void piece_angles(const HeadArgs& A, int64_t pos, int
   }
 }
 
+// The rotated pairs of a lane's pieces: if interleaved, the first `a` of the first piece's and the
+// first `b` of the second's; else all pairs that the two pieces make if a > 0, or none. What is not
+// rotated stays as it is: turned by nothing, an infinity would make its neighbour and itself NaN.
+struct Turned {
+  int a, b;
+};
+template <typename T, int DH, bool INTER>
+__device__ __forceinline__ Turned turned_of(const HeadArgs& A, int c) {
+  constexpr int N = Vec<T, DH>::N;
+  const int pairs = A.rope.rotary_dim / 2;
+  if (INTER) return {pairs - c * N / 2, pairs - size_of<DH>(A) / 4 - c * N / 2};
+  return {pairs - c * N, 0};
+}
 // Turns a lane's pieces by +angle (sign 1) or -angle (sign -1).
 template <int N, bool INTER>
 __device__ __forceinline__ void turn(float (&a)[N], float (&b)[N], const float (&cs)[N], const float (&sn)[N],
-                                     float sign) {
+                                     float sign, Turned n) {
   if constexpr (INTER) {
 #pragma unroll
     for (int j = 0; j < N / 2; ++j) {
       const float x = a[2 * j], y = a[2 * j + 1], s = sign * sn[j];
-      a[2 * j] = x * cs[j] - y * s;
-      a[2 * j + 1] = y * cs[j] + x * s;
+      if (j < n.a) {
+        a[2 * j] = x * cs[j] - y * s;
+        a[2 * j + 1] = y * cs[j] + x * s;
+      }
       const float u = b[2 * j], v = b[2 * j + 1], t = sign * sn[N / 2 + j];
-      b[2 * j] = u * cs[N / 2 + j] - v * t;
-      b[2 * j + 1] = v * cs[N / 2 + j] + u * t;
+      if (j < n.b) {
+        b[2 * j] = u * cs[N / 2 + j] - v * t;
+        b[2 * j + 1] = v * cs[N / 2 + j] + u * t;
+      }
     }
-  } else {
+  } else if (n.a > 0) {
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       const float x = a[j], y = b[j], s = sign * sn[j];
@@ -486,6 +503,7 @@ __device__ __forceinline__ void head_run(const HeadArgs& A, const T* __restrict_
   const int sub = lane / V::LANES, runs = (heads + V::HEADS - 1) / V::HEADS, dh = size_of<DH>(A);
   const bool on = has_piece<T, DH>(A, lane % V::LANES);
   const float per_dh = 1.f / dh;
+  const Turned rotated = turned_of<T, DH, INTER>(A, lane % V::LANES);
   Piece<T, DH> wp = {};
   if (w != nullptr && on) wp = load_piece<T, DH>(w, at);
   for (int i0 = first; i0 < runs; i0 += step * U) {
@@ -518,7 +536,7 @@ __device__ __forceinline__ void head_run(const HeadArgs& A, const T* __restrict_
             b[j] *= r * wb[j];
           }
         }
-        if (turned) turn<V::N, INTER>(a, b, cs, sn, 1.f);
+        if (turned) turn<V::N, INTER>(a, b, cs, sn, 1.f, rotated);
         p[u].a = narrow(a);
         p[u].b = narrow(b);
       }
@@ -585,6 +603,7 @@ __device__ __forceinline__ void head_run_bwd(const HeadArgs& A, const T* __restr
   const int sub = lane / V::LANES, dh = size_of<DH>(A);
   const bool on = has_piece<T, DH>(A, lane % V::LANES);
   const float per_dh = 1.f / dh;
+  const Turned rotated = turned_of<T, DH, INTER>(A, lane % V::LANES);
   Piece<T, DH> wp = {};
   if (w != nullptr && on) wp = load_piece<T, DH>(w, at);
   for (int h0 = sub; h0 - sub < heads; h0 += V::HEADS * U) {
@@ -606,7 +625,7 @@ __device__ __forceinline__ void head_run_bwd(const HeadArgs& A, const T* __restr
       float a[V::N], b[V::N];
       widen(g[u].a, a);
       widen(g[u].b, b);
-      if (turned) turn<V::N, INTER>(a, b, cs, sn, -1.f);
+      if (turned) turn<V::N, INTER>(a, b, cs, sn, -1.f, rotated);
       if (w != nullptr) {
         float xa[V::N], xb[V::N], wv[V::N], ss = 0.f, hn = 0.f;
         widen(p[u].a, xa);
