@@ -8,7 +8,8 @@
 // Angles: pair i turns by pos * inv_freq[i]. A float product would lose the angle at far
 // positions (at 2^17 the spacing of floats near pos * 1 rad is 2^-7 rad), so inv_freq / 2pi is
 // kept as a 64-bit fraction of a turn: its product with the position, modulo 2^64, is the
-// angle within the turn, and the top 32 bits go to sincospif.
+// angle within the turn, and the top 32 bits, rounded to a float, go to sincospif: 2^-26 of a turn at
+// any position.
 //
 // What bounds these kernels is the bytes: every element is read once and written once, statistics
 // and angles stay in registers. 131072 tokens, 32/8 heads of 128, bf16, on GB300: forward 436 us
@@ -925,6 +926,24 @@ int check_cache(const ra_paged_cache* c) {
   return RA_OK;
 }
 
+// |x| / 2pi modulo 1 in units of 2^-64, to a unit, and its negative for x < 0. 1 / 2pi is two doubles
+// (hi + lo, from the decimal expansion of pi), and what the product with hi is rounded by comes back
+// from an fma: one double product would be off by up to 2^10 units for x = 1, which a position of 2^30
+// makes 2^-24 of a turn. (volatile: the product has to be the rounded one everywhere.)
+uint64_t turns_of(double x) {
+  constexpr double hi = 0.15915494309189535, lo = -9.839338337591243e-18;
+  const double f = std::fabs(x);
+  volatile double product = f * hi;
+  const double p = product;
+  double rest = std::fma(f, hi, -p) + f * lo;  // f / 2pi = p + rest
+  rest -= std::rint(rest);
+  const double a = (p - std::floor(p)) * 18446744073709551616.0, whole = std::floor(a);  // exact
+  double b = std::rint(rest * 18446744073709551616.0 + (a - whole));
+  if (b >= 9223372036854775808.0) b = -9223372036854775808.0;  // half a turn either way
+  const uint64_t t = static_cast<uint64_t>(whole) + static_cast<uint64_t>(static_cast<int64_t>(b));
+  return x < 0 ? uint64_t(0) - t : t;
+}
+
 size_t heads_bwd_workspace(int head_dim) {
   return static_cast<size_t>(kHeadBwdBlocks) * 2 * head_dim * sizeof(float);
 }
@@ -943,10 +962,7 @@ extern "C" int ra_rope_init(ra_rope* rope, int rotary_dim, int interleaved, cons
   for (int i = 0; i < RA_MAX_ROTARY_DIM / 2; ++i) rope->turns[i] = 0;
   for (int i = 0; i < rotary_dim / 2; ++i) {
     if (!std::isfinite(inv_freq[i])) return record_error(RA_ERR_INVALID_ARG, "inv_freq[%d] is not finite", i);
-    const double t = inv_freq[i] * 0.15915494309189533577;  // 1 / 2pi
-    double f = t - std::floor(t);                           // [0, 1], 1 only by rounding
-    if (f >= 1.0) f = 0.0;
-    rope->turns[i] = static_cast<uint64_t>(f * 18446744073709551616.0);
+    rope->turns[i] = turns_of(inv_freq[i]);
   }
   record_error(RA_OK, "%s", "");
   return RA_OK;

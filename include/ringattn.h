@@ -230,7 +230,8 @@ typedef struct ra_rope {
   int32_t interleaved;
   uint64_t turns[RA_MAX_ROTARY_DIM / 2]; /* turns per position, in units of 2^-64 of a turn: the
                                             product with a position wraps at whole turns, so an
-                                            angle is exact to 2^-32 of a turn at any position */
+                                            angle is good to 2^-26 of a turn (the float that its
+                                            sine and cosine are taken of) at any position */
 } ra_rope;
 
 /* Fills in `rope` from rotary_dim/2 HOST doubles (radians per position, finite). rotary_dim is
