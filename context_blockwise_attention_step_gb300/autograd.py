@@ -10,6 +10,9 @@ shard-major order with their inverse permutation as gradient, ``qk_norm_rope`` i
 and rotation before it, and ``RingSelfAttention`` is a multi-head (GQA) self-attention layer with
 random weights that uses them, with a serving form over a paged key-value cache.
 
+Gradients are of first order: a second derivative through the attention or the head norm raises (the
+permutations have theirs).
+
 A backward captured into a CUDA graph wants the gradients by ``torch.autograd.grad``, or no other
 graph of the same parameters alive: accumulating into ``.grad`` would run on the stream of the
 first graph, outside the capture.
@@ -19,6 +22,7 @@ from __future__ import annotations
 import math
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import heads, ops
 
@@ -36,6 +40,7 @@ class _RingAttention(torch.autograd.Function):
         return out, lse
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout, _dlse):
         q, k, v, out, lse = ctx.saved_tensors
         if ctx.window:
@@ -54,6 +59,7 @@ class _QkNormRope(torch.autograd.Function):
         return heads.qk_norm_rope_fwd(q, k, prob, q_weight=q_weight, k_weight=k_weight, rope=rope, eps=eps)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dq_out, dk_out):
         dq_out, dk_out = dq_out.contiguous(), dk_out.contiguous()
         q, k, q_weight, k_weight = ctx.saved_tensors or (dq_out, dk_out, None, None)
@@ -74,9 +80,7 @@ class _Shard(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, g):
-        g = g.contiguous()
-        back = ops.unshard_tokens(g, ctx.prob) if ctx.direction == 0 else ops.shard_tokens(g, ctx.prob)
-        return back, None, None
+        return _Shard.apply(g, ctx.prob, 1 - ctx.direction), None, None
 
 
 def ring_attention(q, k, v, prob: ops.Problem, window: int = 0, sinks: int = 0):
