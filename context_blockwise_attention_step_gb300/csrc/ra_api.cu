@@ -12,6 +12,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <initializer_list>
 #include <new>
 #include <numeric>
 #include <string>
@@ -200,6 +201,14 @@ bool force_simt() {
 
 bool use_tc(const ra_problem* p) { return p->dtype == RA_BF16 && !force_simt(); }
 
+// The tensor-core kernels copy and store their token tensors 16 bytes at a time.
+int check_aligned(const ra_problem* p, std::initializer_list<const void*> tensors) {
+  uintptr_t bits = 0;
+  for (const void* t : tensors) bits |= reinterpret_cast<uintptr_t>(t);
+  if (use_tc(p) && bits % 16) return fail(RA_ERR_INVALID_ARG, "bf16 tensors must be 16-byte aligned");
+  return RA_OK;
+}
+
 // The tensor-core backward runs as two atomic-free passes (K/V tiles for dk / dv, query
 // tiles for dq), which is both faster and run-to-run deterministic. RA_BWD=fused selects
 // the single K/V-tile pass that adds dq with float reductions instead (for comparison;
@@ -306,6 +315,7 @@ int ra_ring_attn_fwd(const ra_problem* p, const void* q, const void* k, const vo
                      float* lse, void* workspace, size_t workspace_bytes, void* stream) {
   if (int e = validate(p)) return e;
   if (!q || !k || !v || !out || !lse) return fail(RA_ERR_INVALID_ARG, "null tensor pointer");
+  if (int e = check_aligned(p, {q, k, v, out})) return e;
   if (workspace != nullptr && reinterpret_cast<uintptr_t>(workspace) % 256)
     return fail(RA_ERR_INVALID_ARG, "workspace must be a 256-byte aligned device pointer");
   PlanHolder P(make_plan(p, 0, 0, p->D, -1, p->dtype == RA_F32));
@@ -328,6 +338,7 @@ int ra_block_attn_fwd(const ra_problem* p, int rank, int step, const void* q, co
                       void* stream) {
   if (int e = validate(p)) return e;
   if (!q || !k || !v || !block_out || !block_lse) return fail(RA_ERR_INVALID_ARG, "null tensor pointer");
+  if (int e = check_aligned(p, {q, k, v, block_out})) return e;
   if (rank >= p->D || rank < -1) return fail(RA_ERR_INVALID_ARG, "rank %d out of range", rank);
   if (step < 0 || step >= p->D) return fail(RA_ERR_INVALID_ARG, "step %d out of range", step);
   if (block_out_dtype != RA_F32 && block_out_dtype != RA_BF16)
@@ -371,6 +382,7 @@ int ra_ring_attn_bwd(const ra_problem* p, const void* q, const void* k, const vo
   if (int e = validate(p)) return e;
   if (!q || !k || !v || !out || !lse || !dout || !dq || !dk || !dv)
     return fail(RA_ERR_INVALID_ARG, "null tensor pointer");
+  if (int e = check_aligned(p, {q, k, v, dout, dq, dk, dv})) return e;
   const size_t need = delta_bytes(p) + dq_acc_bytes(p) + sched_bytes(p);
   if (workspace_bytes < need)
     return fail(RA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
@@ -426,6 +438,7 @@ int ra_block_attn_bwd(const ra_problem* p, int rank, int step, const void* q, co
   if (int e = validate(p)) return e;
   if (!q || !k || !v || !out || !lse || !dout || !dq_acc || !dk_acc || !dv_acc)
     return fail(RA_ERR_INVALID_ARG, "null tensor pointer");
+  if (int e = check_aligned(p, {q, k, v, dout, dq_acc, dk_acc, dv_acc})) return e;
   if (rank >= p->D || rank < -1) return fail(RA_ERR_INVALID_ARG, "rank %d out of range", rank);
   if (step < 0 || step >= p->D) return fail(RA_ERR_INVALID_ARG, "step %d out of range", step);
   const size_t need = delta_bytes(p) + sched_bytes(p);
@@ -506,6 +519,7 @@ int ra_window_attn_fwd(const ra_problem* p, int window, int sinks, const void* q
   if (effective_window(p, window) == 0)
     return ra_ring_attn_fwd(p, q, k, v, out, lse, workspace, workspace_bytes, stream);
   if (!q || !k || !v || !out || !lse) return fail(RA_ERR_INVALID_ARG, "null tensor pointer");
+  if (int e = check_aligned(p, {q, k, v, out})) return e;
   if (workspace != nullptr && reinterpret_cast<uintptr_t>(workspace) % 256)
     return fail(RA_ERR_INVALID_ARG, "workspace must be a 256-byte aligned device pointer");
   PlanHolder P(make_window_plan(p, 0, window, sinks));
@@ -533,6 +547,7 @@ int ra_window_attn_bwd(const ra_problem* p, int window, int sinks, const void* q
     return ra_ring_attn_bwd(p, q, k, v, out, lse, dout, dq, dk, dv, workspace, workspace_bytes, stream);
   if (!q || !k || !v || !out || !lse || !dout || !dq || !dk || !dv)
     return fail(RA_ERR_INVALID_ARG, "null tensor pointer");
+  if (int e = check_aligned(p, {q, k, v, dout, dq, dk, dv})) return e;
   const size_t need = ra_window_workspace_bytes(p, window, sinks, 1);
   if (workspace_bytes < need)
     return fail(RA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);

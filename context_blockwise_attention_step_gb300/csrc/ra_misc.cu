@@ -224,7 +224,8 @@ __global__ void __launch_bounds__(kThreads)
 
 cudaError_t launch_merge(const Plan& P, float* out, float* lse, const void* block_out,
                          int block_f32, const float* block_lse, cudaStream_t st) {
-  const int vec = P.head_dim % 4 == 0 ? 4 : 1;
+  const bool aligned = (reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(block_out)) % 16 == 0;
+  const int vec = P.head_dim % 4 == 0 && aligned ? 4 : 1;
   const long work = plan_ranks(P) * max_len(P) * P.hq;  // one warp per (row, head)
   const dim3 grid(grid_for(work, kThreads / 32), P.n_seqs);
   if (block_f32) {

@@ -36,8 +36,8 @@
  * - Return value: RA_OK (0) or a negative ra_status. On error nothing was launched (except
  *   RA_ERR_CUDA, which reports a failed launch) and ra_last_error() returns a message.
  *
- * Supported: bf16 with head_dim 64 or 128 (tensor-core path); f32 with head_dim 1..128
- * (CUDA-core path). D >= 1 and every sequence length divisible by D (2D for zigzag).
+ * Supported: bf16 with head_dim 64 or 128 (tensor-core path; every token tensor but a backward's
+ * `out` begins on 16 bytes); f32 with head_dim 1..128 (CUDA-core path). D >= 1 and every sequence length divisible by D (2D for zigzag).
  * Up to RA_MAX_SEQS sequences (batch elements or varlen sequences) per call.
  */
 #ifndef RINGATTN_H
