@@ -505,13 +505,15 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// dk and dv of the sink rows: the sum of their slots. Block x: a sink row; y: sink shard and K/V
-// head; z: sequence. Threads: dk's head_dim elements, then dv's.
+// dk and dv of the sink rows: the sum of their slots. Block x: a sink row of a sink shard and K/V head
+// (all in x: y ends at 65535, which 128 sink shards of 512 heads reach); y: sequence. Threads: dk's
+// head_dim elements, then dv's.
 template <typename T>
 __global__ void __launch_bounds__(256)
     sink_sum_kernel(const __grid_constant__ Plan P, T* __restrict__ dk, T* __restrict__ dv) {
-  const SeqDesc& s = P.seq[blockIdx.z];
-  const int dh = P.head_dim, j = blockIdx.y / P.hkv, hk = blockIdx.y % P.hkv, row = blockIdx.x;
+  const SeqDesc& s = P.seq[blockIdx.y];
+  const int dh = P.head_dim, row = blockIdx.x % P.sink_stride, head = blockIdx.x / P.sink_stride;
+  const int j = head / P.hkv, hk = head % P.hkv;
   if (j >= sink_shards(P, s.L) || row >= sink_rows(P, s.L, j) || threadIdx.x >= 2 * dh) return;
   const int which = threadIdx.x / dh, d = threadIdx.x % dh, n = sink_slots(P, s.L);
   const int64_t slot = sink_slot(P, s, j, hk, 0);
@@ -622,7 +624,9 @@ cudaError_t launch_sink_sum(const Plan& P, int dtype, void* dk, void* dv, cudaSt
     const int n = sink_shards(P, P.seq[i].L);
     shards = n > shards ? n : shards;
   }
-  const dim3 grid(P.sink_stride, shards * P.hkv, P.n_seqs);
+  const int64_t blocks = static_cast<int64_t>(P.sink_stride) * shards * P.hkv;
+  if (blocks >= (int64_t(1) << 31)) return cudaErrorInvalidConfiguration;
+  const dim3 grid(static_cast<unsigned>(blocks), P.n_seqs);
   if (dtype == RA_F32)
     sink_sum_kernel<float><<<grid, 256, 0, st>>>(P, static_cast<float*>(dk), static_cast<float*>(dv));
   else
