@@ -508,10 +508,12 @@ size_t ra_window_workspace_bytes(const ra_problem* p, int window, int sinks, int
 
 // Up to so many visible keys the backward forms delta as sum_j P_j dP_j, in a pass over the query
 // tiles, instead of dO . O: the rounding of the bf16 `out` would come into dS, which for few keys is
-// as large as dS' own. Relative L2 error of dq (4096 tokens, heads of 128): 8 keys 0.00235 against
-// 0.00268, 64 keys 0.00237 against 0.00243, 256 keys 0.00237 against 0.00242. Time of the backward
-// (65536 tokens, 32/8 heads of 128): window 64 1.78 against 1.65 ms, window 256 2.22 against 1.96.
-constexpr int kFewKeys = 64;
+// as large as dS' own. The pass is there where it takes more off the error than it adds to the time.
+// Relative L2 error of dq (4096 tokens, 4/2 heads of 128) with it 0.00236 at any window, without it
+// 0.00378 at 2 keys, 0.00300 at 4, 0.00269 at 8, 0.00255 at 16 (8 % more), 0.00249 at 24 (6 %), 0.00242
+// at 64. Time of the backward (65536 tokens, 32/8 heads of 128) 1.76 against 1.64 ms (7 %) at all of
+// them.
+constexpr int kFewKeys = 16;
 
 int ra_window_attn_fwd(const ra_problem* p, int window, int sinks, const void* q, const void* k,
                        const void* v, void* out, float* lse, void* workspace, size_t workspace_bytes,

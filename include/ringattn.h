@@ -206,7 +206,7 @@ int ra_window_attn_fwd(const ra_problem* p, int window, int sinks, const void* q
                        void* stream);
 
 /* Its backward, arguments as for ra_ring_attn_bwd (as there, the row sums dO . O are formed from
- * `out` in its dtype, but for bf16 windows of up to 64 visible keys, where its rounding would tell).
+ * `out` in its dtype, but for bf16 windows of up to 16 visible keys, where its rounding would tell).
  * Run-to-run bit-identical. The workspace (device, >= ra_window_workspace_bytes(p, window, sinks,
  * 1), 256-byte aligned) is overwritten. */
 int ra_window_attn_bwd(const ra_problem* p, int window, int sinks, const void* q, const void* k,

@@ -69,3 +69,24 @@ def test_keys_of_small_weight_keep_their_gradients(layout, D, dh, gap):
         rows = slice(1, None)  # without the first token
         off = ((got[rows] - ref[rows]).norm() / ref[rows].norm()).item()
         assert off <= TOL, f"{name}: relative L2 {off:.5f}, allowed {TOL:.5f}"
+
+
+@pytest.mark.parametrize("window,sinks", [(16, 0), (12, 4), (17, 0), (13, 4), (5, 0), (64, 1)])
+@pytest.mark.parametrize("layout,D", [("zigzag", 2), ("stripe", 4)])
+def test_gradients_on_both_sides_of_the_row_sums_rule(window, sinks, layout, D):
+    """Up to 16 visible keys the row sums come from P and dP, from 17 on from the rounded `out`."""
+    n, hq, hkv, dh = 1024, 4, 2, 64
+    g = torch.Generator().manual_seed(5)
+    q, k, v, do = (torch.randn(1, n, h, dh, generator=g).to(torch.bfloat16).cuda() for h in (hq, hkv, hkv, hq))
+    prob = ra.problem_for(q, k, D=D, layout=layout)
+    qs, ks, vs, ds = (ra.shard_tokens(t, prob) for t in (q, k, v, do))
+    out, lse = ra.window_attn_fwd(qs, ks, vs, prob, window, sinks)
+    grads = ra.window_attn_bwd(ds, qs, ks, vs, out, lse, prob, window, sinks)
+    again = ra.window_attn_bwd(ds, qs, ks, vs, torch.zeros_like(out), lse, prob, window, sinks)
+    assert all(torch.equal(a, b) for a, b in zip(grads, again)) == (window + sinks <= 16)  # `out` is not looked at
+    i = torch.arange(n, device="cuda")
+    hide = ~((i[None] <= i[:, None]) & ((i[None] > i[:, None] - window) | (i[None] < sinks)))
+    want = formulas(*(t[0].double() for t in (q, k, v, do)), hide, dh ** -0.5)
+    for got, ref, name in zip(grads, want, ("dq", "dk", "dv")):
+        off = ((ra.unshard_tokens(got, prob)[0].double() - ref).norm() / ref.norm()).item()
+        assert off <= TOL, f"{name}: relative L2 {off:.5f}, allowed {TOL:.5f}"
