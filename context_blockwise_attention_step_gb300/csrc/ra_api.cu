@@ -272,13 +272,11 @@ Plan* make_window_plan(const ra_problem* p, int which, int window, int sinks) {
   return P;
 }
 
-// Backward workspace: delta, item counters, and the slots of the sink rows.
-size_t sink_bytes(const ra_problem* p, int window, int sinks) {
-  if (sinks == 0) return 0;
-  PlanHolder P(make_window_plan(p, 2, window, sinks));
-  if (P.p->window == 0) return 0;
-  return align256(static_cast<size_t>(ra::window_bwd_items(*P.p)) * 2 * P.p->sink_stride * p->head_dim *
-                  sizeof(float));
+// Backward workspace: delta, item counters, and the slots of the sink rows (P: a windowed plan with
+// its `slots`).
+size_t sink_bytes(const Plan& P, int64_t slots) {
+  if (P.sinks == 0) return 0;
+  return align256(static_cast<size_t>(slots) * 2 * P.sink_stride * P.head_dim * sizeof(float));
 }
 
 size_t dq_acc_bytes(const ra_problem* p) {
@@ -500,7 +498,11 @@ size_t ra_window_workspace_bytes(const ra_problem* p, int window, int sinks, int
     PlanHolder P(make_window_plan(p, 0, window, sinks));
     return wants_counter(P.p->n_items) ? sched_bytes(p) : 0;
   }
-  if (which == 1) return delta_bytes(p) + sched_bytes(p) + sink_bytes(p, window, sinks);
+  if (which == 1) {
+    PlanHolder P(make_window_plan(p, 2, window, sinks));
+    int64_t slots = 0;
+    return ra::window_bwd_items(*P.p, &slots) ? delta_bytes(p) + sched_bytes(p) + sink_bytes(*P.p, slots) : 0;
+  }
   return 0;
 } catch (const std::bad_alloc&) {
   return 0;
@@ -552,7 +554,11 @@ int ra_window_attn_bwd(const ra_problem* p, int window, int sinks, const void* q
   if (!q || !k || !v || !out || !lse || !dout || !dq || !dk || !dv)
     return fail(RA_ERR_INVALID_ARG, "null tensor pointer");
   if (int e = check_aligned(p, {q, k, v, dout, dq, dk, dv})) return e;
-  const size_t need = ra_window_workspace_bytes(p, window, sinks, 1);
+  PlanHolder P(make_window_plan(p, 1, window, sinks));
+  int64_t slots = 0;
+  if (!ra::window_bwd_items(*P.p, &slots))
+    return fail(RA_ERR_UNSUPPORTED, "more shards, heads and sinks than 2^31 sums of the sinks' gradients hold");
+  const size_t need = delta_bytes(p) + sched_bytes(p) + sink_bytes(*P.p, slots);
   if (workspace_bytes < need)
     return fail(RA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
   if (workspace == nullptr || reinterpret_cast<uintptr_t>(workspace) % 256)
@@ -560,9 +566,7 @@ int ra_window_attn_bwd(const ra_problem* p, int window, int sinks, const void* q
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   float* delta = static_cast<float*>(workspace);
   char* at = static_cast<char*>(workspace) + delta_bytes(p);
-  PlanHolder P(make_window_plan(p, 1, window, sinks));
   P.p->sink_sums = reinterpret_cast<float*>(at + sched_bytes(p));
-  ra::window_bwd_items(*P.p);
   int64_t query_items = 0;
   for (int i = 0; i < P.p->n_seqs; ++i)
     query_items += static_cast<int64_t>(ra::ceil_div(P.p->seq[i].L, ra::kQTileRows)) * p->D * p->hq;

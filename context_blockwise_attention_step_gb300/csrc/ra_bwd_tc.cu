@@ -1102,17 +1102,21 @@ cudaError_t launch_dh(const Plan& P, const CUtensorMap& mq, const CUtensorMap& m
 
 }  // namespace
 
-int window_bwd_items(Plan& P) {
-  int items = 0, slots = 0;
+bool window_bwd_items(Plan& P, int64_t* slots) {
+  int64_t items = 0, n = 0;
   for (int i = 0; i < P.n_seqs; ++i) {
     SeqDesc& s = P.seq[i];
-    s.item_start = items;
-    s.sink_start = slots;
-    items += sink_items_of(P, s.L) + bwd_items_of(P, s.L);
-    slots += sink_shards(P, s.L) * P.hkv * sink_slots(P, s.L);
+    s.item_start = static_cast<int32_t>(items);
+    s.sink_start = static_cast<int32_t>(n);
+    const int64_t shard_slots = 1 + static_cast<int64_t>(P.D) * sink_chunks(P, s.L);
+    n += static_cast<int64_t>(sink_shards(P, s.L)) * P.hkv * shard_slots;
+    if (n >= (int64_t(1) << 31)) return false;  // (a sequence's sink items are fewer than its slots)
+    items += static_cast<int64_t>(sink_items_of(P, s.L)) + bwd_items_of(P, s.L);
+    if (items >= (int64_t(1) << 31)) return false;
   }
-  P.n_items = items;
-  return slots;
+  P.n_items = static_cast<int32_t>(items);
+  *slots = n;
+  return true;
 }
 
 cudaError_t launch_window_bwd_tc(const Plan& P, const void* q, const void* k, const void* v, const void* dout,

@@ -31,9 +31,10 @@ cudaError_t launch_bwd_tc(const Plan& P, BwdKind kind, const void* q, const void
 cudaError_t launch_bwd_dq_tc(const Plan& P, const void* q, const void* k, const void* v,
                              const void* dout, const float* lse, const float* delta, void* dq,
                              cudaStream_t st);
-// Windowed K/V pass: numbers the plan's items and sink slots (returns the slots, each of 2 *
-// sink_stride * head_dim floats of P.sink_sums); dk and dv, the sinks' rows summed from the slots.
-int window_bwd_items(Plan& P);
+// Windowed K/V pass: numbers the plan's items and sink slots (each of 2 * sink_stride * head_dim floats
+// of P.sink_sums; false if there are more than 32 bits count); dk and dv, the sinks' rows summed from
+// the slots.
+bool window_bwd_items(Plan& P, int64_t* slots);
 cudaError_t launch_window_bwd_tc(const Plan& P, const void* q, const void* k, const void* v,
                                  const void* dout, const float* lse, const float* delta, void* dk,
                                  void* dv, cudaStream_t st);
