@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       size_t qrow, li = 0;
       bool valid;
       if constexpr (WIN) {
-        if (!mbar_wait(&sh.item_full[kq & 1], (kq >> 1) & 1, abort_flag, tmo, status)) break;
+        if (!__all_sync(0xffffffffu, mbar_wait(&sh.item_full[kq & 1], (kq >> 1) & 1, abort_flag, tmo, status))) break;
         item = &slots[kq & 1];
         if (item->item >= P.n_items) break;
         it.h = item->h;
@@ -594,7 +594,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       if (!ok) break;
       // dq = scale * dQ (or dq += scale * dQ into float32 sums for bwd_accum, the per-step
       // block backward): warpgroup 0 takes columns [0, DH/2), warpgroup 1 the rest
-      if (!mbar_wait(&sh.dq_done, dd_phase, abort_flag, tmo, status)) break;
+      if (!wait(&sh.dq_done, dd_phase)) break;
       dd_phase ^= 1;
       tc_fence_after();
       if constexpr (DELTA) {  // two addends on 0: the same sum in either order

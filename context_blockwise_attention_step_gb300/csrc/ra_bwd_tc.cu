@@ -997,7 +997,7 @@ __global__ void __launch_bounds__(bwd_threads<kWithDQ>(), 1)
       else ok = for_each_qtile(P, it, wk, qtile);
       if (!ok) break;
       // dK (times scale; warpgroup 0) and dV (warpgroup 1) of this tile
-      if (!mbar_wait(&sh.acc_done, ad_phase, abort_flag, tmo, status)) break;
+      if (!wait(&sh.acc_done, ad_phase)) break;
       ad_phase ^= 1;
       tc_fence_after();
       const uint32_t tacc = tmem + lane_off + (wg == 0 ? C::kColDK : C::kColDV);

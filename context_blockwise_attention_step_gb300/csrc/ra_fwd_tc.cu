@@ -511,7 +511,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       FwdItem it;
       FwdWalk wk;
       if constexpr (WIN) {
-        if (!mbar_wait(&sh.item_full[kq & 1], (kq >> 1) & 1, abort_flag, tmo, status)) break;
+        if (!__all_sync(0xffffffffu, mbar_wait(&sh.item_full[kq & 1], (kq >> 1) & 1, abort_flag, tmo, status))) break;
         item = &win.slot[kq & 1];
         if (item->item >= P.n_items) break;
         wk.L = item->L;
@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
         const bool got = mbar_wait(bar, parity, abort_flag, tmo, status);
-        return WIN ? __all_sync(0xffffffffu, got) : got;  // the windowed walk is the warp's
+        return WIN ? __all_sync(0xffffffffu, got) : got;  // the windowed walk is the warp's, to its end
       };
       const int s_end = WIN ? item->nseg : P.step_end;
       for (int s = WIN ? 0 : P.step_begin; s < s_end && ok; ++s) {
@@ -717,10 +717,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       // epilogue: both halves' sums, out = O / l for this half's columns, lse
       sh.xl[t][hf][row] = l;
       mbar_arrive(&sh.xl_bar[t]);
-      if (!mbar_wait(&sh.xl_bar[t], xl_phase, abort_flag, tmo, status)) break;
+      if (!wait(&sh.xl_bar[t], xl_phase)) break;
       xl_phase ^= 1;
       l += sh.xl[t][hf ^ 1][row];
-      if (!mbar_wait(&sh.o_done[t], od_phase, abort_flag, tmo, status)) break;
+      if (!wait(&sh.o_done[t], od_phase)) break;
       od_phase ^= 1;
       tc_fence_after();
       const float inv_l = l > 0.f ? 1.f / l : 0.f;
