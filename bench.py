@@ -40,13 +40,13 @@ FALLBACK_PEAKS = {"hbm_gbs": 6800.0, "bf16_tflops": 1900.0, "bf16_tflops_sustain
 # null until re-measured.
 TRAFFIC = {
     ("ring_bwd_tc (K/V-tile pass)", "long_s131072_gqa32x8_dh128_D16_zigzag"):
-        {"bytes": 54709244672 + 541931520, "source_sha": "39289a7e91f00299"},
+        {"bytes": 54702025472 + 542446080, "source_sha": "1566ad716793696f"},
     ("ring_fwd_tc", "long_s131072_gqa32x8_dh128_D16_zigzag"):
-        {"bytes": 117793662208 + 1258559744, "source_sha": "13e1b9113b74863a"},
+        {"bytes": 119668151552 + 1258698496, "source_sha": "7ab6baf4dd53997c"},
     ("ring_bwd_dq_tc (dq pass)", "long_s131072_gqa32x8_dh128_D16_zigzag"):
-        {"bytes": 16063049216 + 1060016384, "source_sha": "c808724a08ad9770"},
+        {"bytes": 16150972416 + 1060189440, "source_sha": "3de0e3344efe6290"},
     ("merge_kernel", "long_s131072_gqa32x8_dh128_D16_zigzag"):
-        {"bytes": 3255436544 + 2109264896, "source_sha": "5314b5707f03b07b"},
+        {"bytes": 3256050432 + 2109006336, "source_sha": "407e400454aef449"},
 }
 
 

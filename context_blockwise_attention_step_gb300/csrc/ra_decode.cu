@@ -24,9 +24,9 @@
 // m16n8k16 product, so that the tensor cores are 18 % busy with mma.sync and a wider instruction
 // would only have more empty rows. The join kernel is launched while the main one runs
 // (programmatic dependent launch), works out what it has to join, and then waits for the main
-// kernel's end. Measured on GB300 with 32/8 heads of 128, bf16: one sequence of 131072 keys 92 us
-// (5.9 TB/s), 64 ragged ones of up to 16384 keys 325 us (6.6 TB/s), one of 700 keys 7.5 us, which
-// is two launches and one trip to memory each.
+// kernel's end. Measured on GB300 with 32/8 heads of 128, bf16: one sequence of 131072 keys 91 us
+// (5.9 TB/s), 64 ragged ones of up to 16384 keys 335 to 345 us (6.2 to 6.4 TB/s), one of 700 keys 7.5
+// us, which is two launches and one trip to memory each.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -12,9 +12,9 @@
 // any position.
 //
 // What bounds these kernels is the bytes: every element is read once and written once, statistics
-// and angles stay in registers. 131072 tokens, 32/8 heads of 128, bf16, on GB300: forward 436 us
-// (6.16 TB/s), backward 659 us (6.11 TB/s); 16 prompts of up to 8192 tokens into a cache 256 us
-// (6.2 TB/s); 2 x 4096 tokens, 8 heads of 64: 12 and 16 us, four new tokens 4 us, which is latency.
+// and angles stay in registers. 131072 tokens, 32/8 heads of 128, bf16, on GB300: forward 440 us
+// (6.10 TB/s), backward 669 us (6.02 TB/s); 16 prompts of up to 8192 tokens into a cache 260 us
+// (6.2 TB/s); 2 x 4096 tokens, 8 heads of 64: 11 and 16 us, four new tokens 4 us, which is latency.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -445,7 +445,8 @@ __device__ __forceinline__ void piece_angles(const HeadArgs& A, int64_t pos, int
 
 // The rotated pairs of a lane's pieces: if interleaved, the first `a` of the first piece's and the
 // first `b` of the second's; else all pairs that the two pieces make if a > 0, or none. What is not
-// rotated stays as it is: turned by nothing, an infinity would make its neighbour and itself NaN.
+// rotated stays as it is: turned by nothing, an infinity would make its neighbour and itself NaN. (1 %
+// of the time where the whole head is rotated; a branch of its own for that case costs 1 % more.)
 struct Turned {
   int a, b;
 };
@@ -547,7 +548,7 @@ __device__ __forceinline__ void head_run(const HeadArgs& A, const T* __restrict_
 }
 
 // A warp takes a token, or one of `parts` shares of its heads. Three blocks an SM with two loads of a
-// lane in flight, measured at 131072 tokens, 32/8 heads of 128, bf16: 436 us (6.16 TB/s); two blocks
+// lane in flight, measured at 131072 tokens, 32/8 heads of 128, bf16 (when it took 436 us): two blocks
 // with four loads 450, three with four 485, four with two 475, three with one 487.
 template <typename T, int DH, bool INTER, typename Rows, bool CACHE>
 __global__ void __launch_bounds__(kThreads, 3)
@@ -664,7 +665,7 @@ __device__ __forceinline__ void head_run_bwd(const HeadArgs& A, const T* __restr
   }
 }
 
-// Four blocks an SM with two heads' loads of a lane in flight, at the same size: 659 us (6.11 TB/s);
+// Four blocks an SM with two heads' loads of a lane in flight, at the same size (659 us then):
 // four with one 777, five with one 933, three with two 946.
 template <typename T, int DH, bool INTER>
 __global__ void __launch_bounds__(kBwdThreads, 4)

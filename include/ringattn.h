@@ -206,15 +206,17 @@ int ra_window_attn_fwd(const ra_problem* p, int window, int sinks, const void* q
                        void* stream);
 
 /* Its backward, arguments as for ra_ring_attn_bwd (as there, the row sums dO . O are formed from
- * `out` in its dtype, but for bf16 windows of up to 16 visible keys, where its rounding would tell).
+ * `out` in its dtype, but for bf16 windows of up to 16 visible keys, where its rounding would tell;
+ * dout must be finite as well). In bf16 dq and dk take a weight of less than 2^-39 for 0.
  * Run-to-run bit-identical. The workspace (device, >= ra_window_workspace_bytes(p, window, sinks,
- * 1), 256-byte aligned) is overwritten. */
+ * 1), 256-byte aligned) is overwritten. With D shards and hkv K/V heads the sinks' sums have up to
+ * min(D, sinks) * hkv * (D + 1) slots a sequence; 2^31 of them are refused. */
 int ra_window_attn_bwd(const ra_problem* p, int window, int sinks, const void* q, const void* k,
                        const void* v, const void* out, const float* lse, const void* dout, void* dq,
                        void* dk, void* dv, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Bytes of workspace of the two calls above: which = 0 forward (optional there), which = 1
- * backward; 0 for invalid arguments. */
+ * backward; 0 for arguments that the calls refuse. */
 size_t ra_window_workspace_bytes(const ra_problem* p, int window, int sinks, int which);
 
 /* ---- head norms and position rotation ------------------------------------------------ */
