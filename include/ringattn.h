@@ -37,7 +37,8 @@
  *   RA_ERR_CUDA, which reports a failed launch) and ra_last_error() returns a message.
  *
  * Supported: bf16 with head_dim 64 or 128 (tensor-core path; every token tensor but a backward's
- * `out` begins on 16 bytes); f32 with head_dim 1..128 (CUDA-core path). D >= 1 and every sequence length divisible by D (2D for zigzag).
+ * `out` begins on 16 bytes); f32 with head_dim 1..128 (CUDA-core path). D >= 1 and every
+ * sequence length divisible by D (2D for zigzag).
  * Up to RA_MAX_SEQS sequences (batch elements or varlen sequences) per call.
  */
 #ifndef RINGATTN_H
@@ -209,8 +210,9 @@ int ra_window_attn_fwd(const ra_problem* p, int window, int sinks, const void* q
  * `out` in its dtype, but for bf16 windows of up to 16 visible keys, where its rounding would tell;
  * dout must be finite as well). In bf16 dq and dk take a weight of less than 2^-39 for 0.
  * Run-to-run bit-identical. The workspace (device, >= ra_window_workspace_bytes(p, window, sinks,
- * 1), 256-byte aligned) is overwritten. With D shards and hkv K/V heads the sinks' sums have up to
- * min(D, sinks) * hkv * (D + 1) slots a sequence; 2^31 of them are refused. */
+ * 1), 256-byte aligned) is overwritten. It holds a sum of the sinks' gradients for every K/V head,
+ * shard with sinks and piece of a shard's queries; a problem with 2^31 of them is refused
+ * (RA_ERR_UNSUPPORTED). */
 int ra_window_attn_bwd(const ra_problem* p, int window, int sinks, const void* q, const void* k,
                        const void* v, const void* out, const float* lse, const void* dout, void* dq,
                        void* dk, void* dv, void* workspace, size_t workspace_bytes, void* stream);
