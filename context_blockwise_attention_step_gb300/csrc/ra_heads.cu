@@ -917,8 +917,9 @@ int check_cache(const ra_paged_cache* c) {
     return record_error(RA_ERR_UNSUPPORTED, "f32 supports head_dim <= 128 (got %d)", c->head_dim);
   if (c->n_seqs > RA_MAX_CACHE_SEQS)
     return record_error(RA_ERR_UNSUPPORTED, "n_seqs > %d", RA_MAX_CACHE_SEQS);
-  if (static_cast<int64_t>(c->max_pages) * c->page_size >= (int64_t(1) << 31))
-    return record_error(RA_ERR_UNSUPPORTED, "max_pages * page_size must stay below 2^31");
+  // (the decode kernels round a length up to units of 64 keys in 32 bits)
+  if (static_cast<int64_t>(c->max_pages) * c->page_size > (int64_t(1) << 31) - 64)
+    return record_error(RA_ERR_UNSUPPORTED, "max_pages * page_size must be 2^31 - 64 at most");
   if (c->page_stride < 1 || c->slot_stride < 1 || c->head_stride < 1 || c->table_stride < c->max_pages)
     return record_error(RA_ERR_INVALID_ARG, "cache: strides must be positive, table_stride >= max_pages");
   if (c->k_pages == nullptr || c->v_pages == nullptr ||

@@ -289,7 +289,7 @@ typedef struct ra_paged_cache {
   int32_t page_size;  /* >= 1 */
   int32_t n_pages;    /* >= 1 */
   int32_t n_seqs;     /* rows of the block table: the sequences of a batch */
-  int32_t max_pages;  /* entries of a row */
+  int32_t max_pages;  /* entries of a row; max_pages * page_size <= 2^31 - 64 */
   int64_t table_stride;
   int64_t page_stride, slot_stride, head_stride; /* elements */
   void* k_pages;
