@@ -35,7 +35,8 @@ EXPORTS = (
     "ra_last_error",
     "ra_version",
     "ra_rope_init", "ra_qk_norm_rope_fwd", "ra_qk_norm_rope_bwd", "ra_kv_cache_append",
-    "ra_paged_attn_decode", "ra_paged_workspace_bytes",
+    "ra_paged_attn_decode", "ra_paged_workspace_bytes", "ra_paged_attn_extend",
+    "ra_paged_extend_workspace_bytes",
     "ra_window_attn_fwd", "ra_window_attn_bwd", "ra_window_workspace_bytes",
 )
 
@@ -82,6 +83,14 @@ class RaPagedCache(ctypes.Structure):
         ("k_pages", ctypes.c_void_p),
         ("v_pages", ctypes.c_void_p),
         ("block_table", ctypes.c_void_p),
+    ]
+
+
+class RaSharedPrefix(ctypes.Structure):
+    _fields_ = [
+        ("n_groups", ctypes.c_int32),
+        ("cu_groups", ctypes.c_void_p),
+        ("prefix_lens", ctypes.c_void_p),
     ]
 
 
@@ -136,6 +145,9 @@ def lib() -> ctypes.CDLL:
                                      vp, vp]),
         "ra_paged_attn_decode": (i32, [C, i32, f32, i32, i32, vp, vp, vp, vp, vp, size, vp]),
         "ra_paged_workspace_bytes": (size, [C, i32]),
+        "ra_paged_attn_extend": (i32, [C, ctypes.POINTER(RaSharedPrefix), i32, i32, f32, i32, i32, vp, vp, vp, vp,
+                                       vp, vp, size, vp]),
+        "ra_paged_extend_workspace_bytes": (size, [C, i32, i32, i32]),
         "ra_window_attn_fwd": (i32, [P, i32, i32, vp, vp, vp, vp, vp, vp, size, vp]),
         "ra_window_attn_bwd": (i32, [P, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, size, vp]),
         "ra_window_workspace_bytes": (size, [P, i32, i32, i32]),

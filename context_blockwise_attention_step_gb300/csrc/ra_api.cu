@@ -681,18 +681,21 @@ int ra_work_items(const ra_problem* p, int which, int32_t* items_out, int max_it
 int ra_check_device_status(int reset) {
   cudaError_t e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return cuda_fail(e, "device synchronize");
-  unsigned int f = 0, b = 0, d = 0, ap = 0, dc = 0;
+  unsigned int f = 0, b = 0, d = 0, ap = 0, dc = 0, ex[2] = {0, 0};
   e = ra::fwd_status(&f, reset != 0);
   if (e == cudaSuccess) e = ra::bwd_status(&b, reset != 0);
   if (e == cudaSuccess) e = ra::bwd_dq_status(&d, reset != 0);
   if (e == cudaSuccess) e = ra::append_status(&ap, reset != 0);
   if (e == cudaSuccess) e = ra::decode_status(&dc, reset != 0);
+  if (e == cudaSuccess) e = ra::extend_status(ex, reset != 0);
   if (e != cudaSuccess) return cuda_fail(e, "status read");
-  if (f | b | d)
-    return fail(RA_ERR_DEVICE_TIMEOUT, "device status: forward 0x%x backward 0x%x dq 0x%x", f, b, d);
-  if (ap | dc)
-    return fail(RA_ERR_CACHE_INDEX, "device status: an index outside the paged cache (append 0x%x decode 0x%x)",
-                ap, dc);
+  if (f | b | d | ex[0])
+    return fail(RA_ERR_DEVICE_TIMEOUT, "device status: forward 0x%x backward 0x%x dq 0x%x extend 0x%x", f, b, d,
+                ex[0]);
+  if (ap | dc | ex[1])
+    return fail(RA_ERR_CACHE_INDEX,
+                "device status: an index outside the paged cache (append 0x%x decode 0x%x extend 0x%x)", ap, dc,
+                ex[1]);
   return ok();
 }
 

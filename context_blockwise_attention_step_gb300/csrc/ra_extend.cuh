@@ -1,0 +1,163 @@
+// ra_extend.cuh — what the kernels of ra_extend.cu and ra_extend_tc.cu share: the call's arguments,
+// a CTA's walk over its share of the work, and where the parts of a cut block go.
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "ra_extend.h"
+#include "ra_internal.h"
+#include "ra_ptx.cuh"
+
+namespace ra {
+
+constexpr int kExtSms = 152;
+constexpr int kExtMaxCtas = 2 * kExtSms;
+
+// What the planning kernel finds out, at the beginning of the workspace; the segments follow.
+struct ExtHead {
+  int64_t units;
+  int32_t ctas, segs, own_blocks, pad;
+};
+
+struct ExtArgs {
+  const void* q;
+  const void* k_pages;
+  const void* v_pages;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* cu_new;       // null: one new token of every sequence
+  const int32_t* cu_groups;
+  const int32_t* prefix_lens;
+  int64_t table_stride, page_stride, slot_stride, head_stride;
+  int32_t n_seqs, n_groups, n_tokens, max_pages, page_size, n_pages;
+  int32_t hq, hkv, group, dh;
+  int32_t hb, blocks_per_kv;   // query heads of a block (the last one may have fewer), blocks of a K/V head
+  int32_t slot_rows;           // rows of a part: those of the largest block
+  int32_t most_ctas;
+  int32_t box_rows, ord[3];    // tensor-core kernel: keys of a copy; places of head, slot, page in the map
+  ExtShape sh;
+  float scale_log2;
+  uint64_t timeout_ns;
+  ExtHead* head;
+  ExtSeg* segs;
+  float* part_o;               // [CTA][2][slot_rows][dh]: sums of a cut block, not divided by l
+  float2* part_ml;             // [CTA][2][slot_rows]: running max (log2), denominator
+  float* row_o;                // the same of whole blocks that are joined: [2][n_tokens][hq][dh]
+  float2* row_ml;
+  void* out;
+  float* lse;
+};
+
+// Where a block's result goes.
+enum : int { kExtFinal = 0, kExtPart = 1, kExtRows = 2 };
+
+// A piece of a block: walk indexes j0 .. j0 + tiles - 1.
+struct ExtItem {
+  ExtWalk walk;
+  int32_t tiles, j0;
+  int32_t tok0, ntok, two;     // token row of the block's first row, tokens; more than `half`
+  int32_t hk, g0, heads;       // K/V head, first query head of its group, heads
+  int32_t base, shared;        // position of tok0; prefix: every row sees keys 0 .. end - 1
+  int32_t low, end;            // keys of the block: low .. end - 1, and with a window sinks
+  int32_t seq, dest, slot;     // kExtPart: which part; kExtRows: 0 prefix, 1 own
+};
+
+// The walk of one warp over the pieces of a CTA's share (every lane holds the same state).
+struct ExtCursor {
+  int64_t u0, u1, base;
+  ExtSeg g;
+  int cta, segs, seg, pair, blk, blocks;
+
+  __device__ __forceinline__ bool begin(const ExtArgs& A, int which) {
+    const int64_t units = A.head->units;
+    const int ctas = A.head->ctas;
+    segs = A.head->segs;
+    cta = which;
+    if (which >= ctas) return false;
+    u0 = ext_first(units, ctas, which);
+    u1 = ext_first(units, ctas, which + 1);
+    // the last segment that begins at u0 or before: 32 places at a time
+    const int lane = threadIdx.x & 31;
+    int lo = 0, n = segs;
+    while (n > 1) {
+      const int step = (n + 31) / 32, at = lo + lane * step;
+      const bool before = at < lo + n && A.segs[at].unit0 <= u0;
+      const int k = __popc(__ballot_sync(0xffffffffu, before)) - 1;
+      const int next = lo + k * step;
+      n = min(step, lo + n - next);
+      lo = next;
+    }
+    seg = lo;
+    g = A.segs[seg];
+    int64_t r = u0 - g.unit0;
+    pair = static_cast<int>(r / g.units);
+    r -= pair * g.units;
+    blocks = ext_blocks(A.sh, g.n);
+    blk = ext_block_of(A.sh, g, r);
+    base = g.unit0 + pair * g.units + ext_units_before(A.sh, g, blk);
+    return true;
+  }
+
+  __device__ __forceinline__ bool next(const ExtArgs& A, ExtItem& it) {
+    while (base < u1) {
+      const ExtWalk w = ext_walk(A.sh, g, blk);
+      const int weight = ext_weight(A.sh, g, blk);
+      const int j0 = ext_tile_from(base, weight, w.count, u0), j1 = ext_tile_from(base, weight, w.count, u1);
+      if (j0 < j1) {
+        const int a = blk * A.sh.bt, hblk = pair % A.blocks_per_kv;
+        it.walk = w;
+        it.j0 = j0;
+        it.tiles = j1 - j0;
+        it.tok0 = g.t0 + a;
+        it.ntok = min(A.sh.bt, g.n - a);
+        it.two = it.ntok > A.sh.half;
+        it.hk = pair / A.blocks_per_kv;
+        it.g0 = hblk * A.hb;
+        it.heads = min(A.hb, A.group - it.g0);
+        it.shared = g.shared;
+        it.base = g.base + a;
+        it.low = g.shared ? 0 : static_cast<int>(ext_low(A.sh, g, blk));
+        it.end = g.shared ? g.k1 : it.base + it.ntok;
+        it.seq = g.seq;
+        const bool whole = j0 == 0 && j1 == w.count, joined = g.shared || g.prefix >= 0;
+        it.dest = !whole ? kExtPart : joined ? kExtRows : kExtFinal;
+        it.slot = !whole ? cta * 2 + (j0 > 0 ? 0 : 1) : g.shared ? 0 : 1;
+      }
+      base += static_cast<int64_t>(w.count) * weight;
+      if (++blk == blocks) {
+        blk = 0;
+        if (++pair == A.hkv * A.blocks_per_kv) {
+          pair = 0;
+          do {
+            if (++seg >= segs) {
+              base = u1;
+              break;
+            }
+            g = A.segs[seg];
+          } while (g.units == 0);
+          blocks = ext_blocks(A.sh, g.n);
+        }
+      }
+      if (j0 < j1) return true;
+    }
+    return false;
+  }
+};
+
+// Where page `page` of a sequence is (page 0 in place of one outside the cache, which is recorded).
+__device__ __forceinline__ int ext_page(const ExtArgs& A, int seq, int page, unsigned int* status) {
+  const int at = A.block_table[seq * A.table_stride + page];
+  if (at >= 0 && at < A.n_pages) return at;
+  atomicOr(status, 1u);
+  return 0;
+}
+
+// The tensor-core kernel: its tensor maps (they also fill in box_rows and ord), and its launch.
+struct ExtMaps {
+  CUtensorMap q, k, v;
+};
+cudaError_t make_extend_maps(ExtMaps* maps, const ra_paged_cache* c, ExtArgs* A);
+cudaError_t launch_extend_tc(const ExtArgs& A, const ExtMaps& maps, cudaStream_t st);
+cudaError_t extend_tc_status(unsigned int value[2], bool reset);  // as extend_status, of that kernel alone
+
+}  // namespace ra

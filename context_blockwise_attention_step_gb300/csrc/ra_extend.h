@@ -1,0 +1,168 @@
+// ra_extend.h — integer part of the attention of several new tokens over a paged cache: which keys
+// a block of query rows walks, and how the walks are dealt out. Host and device.
+//
+// The work is a list of segments, each a run of query tokens against a run of keys:
+//   prefix segment  the tokens of all sequences of a group against the keys [0, k1) that they
+//                   share; every row sees every key
+//   own segment     the tokens of one sequence, at positions base .. base + n - 1, against the
+//                   keys [k0, base + n); row j sees the keys up to base + j, with a window only
+//                   the last `window` of these and the first `sinks`
+// k0 and k1 are whole key tiles. A segment's tokens are cut into blocks of `bt`; a block walks the
+// key tiles that one of its rows sees. A tile of a block costs a unit if the block has at most
+// `half` tokens, else `wide` units, and every CTA gets the same share of all units, in the
+// order segment, pair (K/V head and block of its query heads), block, tile. A tile belongs to the
+// CTA that its first unit falls to; with shares of `wide` units at least, each CTA between the first
+// and the last of a block has a tile of it.
+#pragma once
+#include <stdint.h>
+
+#include "ra_layout.h"
+
+namespace ra {
+
+struct ExtShape {
+  int32_t bt, half;  // tokens of a block, and of one that costs one unit a tile
+  int32_t wide;      // units of a tile of a larger block
+  int32_t shift;     // log2 of a tile's keys
+  int32_t window, sinks;
+};
+
+struct ExtSeg {
+  int64_t unit0;   // units before this segment
+  int64_t units;   // units of one pair; 0: nothing to walk
+  int32_t t0, n;   // first token row, tokens
+  int32_t base;    // own: position of token t0
+  int32_t k0, k1;  // own: first key, keys; prefix: 0, keys
+  int32_t seq;     // row of the block table
+  int32_t blocks0; // own blocks before this segment
+  int32_t prefix;  // own: the prefix segment that has the keys before k0, or -1
+  int32_t shared;  // 1: a prefix segment
+  int32_t pad;
+};
+
+// Tiles of a block: walk index j is tile j for j < ns (first tokens before the window), else
+// first + j - ns.
+struct ExtWalk {
+  int32_t first, ns, count;
+};
+RA_HD int ext_tile(const ExtWalk& w, int j) { return j < w.ns ? j : w.first + j - w.ns; }
+
+RA_HD int ext_blocks(const ExtShape& s, int n) { return n > 0 ? (n - 1) / s.bt + 1 : 0; }
+
+// The lowest key of the window of block i's first row.
+RA_HD int64_t ext_low(const ExtShape& s, const ExtSeg& g, int64_t i) {
+  const int64_t at = g.base + i * s.bt - s.window + 1;
+  return s.window > 0 && at > g.k0 ? at : g.k0;
+}
+
+RA_HD ExtWalk ext_walk(const ExtShape& s, const ExtSeg& g, int i) {
+  const int kt = 1 << s.shift;
+  if (g.shared) return {0, 0, (g.k1 + kt - 1) >> s.shift};
+  const int64_t end = static_cast<int64_t>(i + 1) * s.bt;
+  const int hi = g.base + static_cast<int>(end < g.n ? end : g.n);
+  ExtWalk w;
+  w.first = static_cast<int>(ext_low(s, g, i) >> s.shift);
+  w.ns = 0;
+  if (s.window > 0 && s.sinks > 0) {
+    w.ns = (s.sinks + kt - 1) >> s.shift;
+    if (w.ns > w.first) w.ns = w.first;
+  }
+  w.count = ((hi - 1) >> s.shift) - w.first + 1 + w.ns;
+  return w;
+}
+
+// sum over i < n of floor((a i + b) / 2^shift); a >= 1, b >= 0 (the Euclid-like reduction of a
+// floor sum: take out the whole parts, then count lattice points by the other axis)
+RA_HD int64_t ext_floor_sum(int64_t n, int shift, int64_t a, int64_t b) {
+  int64_t m = int64_t(1) << shift, sum = 0;
+  while (n > 0) {
+    if (a >= m) {
+      sum += (n - 1) * n / 2 * (a / m);
+      a %= m;
+    }
+    if (b >= m) {
+      sum += n * (b / m);
+      b %= m;
+    }
+    const int64_t y = a * n + b;
+    if (y < m) break;
+    n = y / m;
+    b = y % m;
+    const int64_t t = m;
+    m = a;
+    a = t;
+  }
+  return sum;
+}
+
+// Tiles of the blocks before block i <= blocks, all of them whole (i == blocks: the last one counted
+// as whole, which it need not be).
+RA_HD int64_t ext_tiles_before(const ExtShape& s, const ExtSeg& g, int64_t i) {
+  const int64_t kt = int64_t(1) << s.shift;
+  if (g.shared) return i * ((g.k1 + kt - 1) >> s.shift);
+  int64_t sum = ext_floor_sum(i, s.shift, s.bt, g.base + kt + s.bt - 1);  // ends: (hi - 1) / kt + 1
+  if (s.window <= 0) return sum - i * (g.k0 >> s.shift);
+  const int64_t low = static_cast<int64_t>(g.base) - s.window + 1;  // of block 0; k0 is 0
+  const int64_t skip = low >= 0 ? 0 : (-low + s.bt - 1) / s.bt;  // blocks whose window begins at key 0
+  if (i > skip) sum -= ext_floor_sum(i - skip, s.shift, s.bt, low + skip * s.bt);
+  if (s.sinks > 0) {
+    const int64_t most = (s.sinks + kt - 1) >> s.shift;
+    for (int64_t k = 1; k <= most; ++k) {  // blocks whose window begins at tile k or later
+      const int64_t need = k * kt - low, from = need <= 0 ? 0 : (need + s.bt - 1) / s.bt;
+      if (i > from) sum += i - from;
+    }
+  }
+  return sum;
+}
+
+// Units of a tile of block i, and of the blocks before block i <= blocks (of one pair).
+RA_HD int ext_weight(const ExtShape& s, const ExtSeg& g, int i) {
+  return g.n - static_cast<int64_t>(i) * s.bt > s.half ? s.wide : 1;
+}
+RA_HD int64_t ext_units_before(const ExtShape& s, const ExtSeg& g, int i) {
+  const int nb = ext_blocks(s, g.n);
+  if (i <= 0 || nb == 0) return 0;
+  if (i < nb) return ext_tiles_before(s, g, i) * s.wide;
+  return ext_tiles_before(s, g, nb - 1) * s.wide +
+         static_cast<int64_t>(ext_walk(s, g, nb - 1).count) * ext_weight(s, g, nb - 1);
+}
+// The block that unit u of a pair falls to.
+RA_HD int ext_block_of(const ExtShape& s, const ExtSeg& g, int64_t u) {
+  int lo = 0, hi = ext_blocks(s, g.n) - 1;
+  while (lo < hi) {
+    const int mid = lo + (hi - lo + 1) / 2;
+    if (ext_units_before(s, g, mid) <= u) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Shares: of `units` units CTA i of `ctas` has [ext_first(i), ext_first(i + 1)).
+RA_HD int ext_ctas(int64_t units, int most, int wide) {
+  const int64_t c = units / wide;
+  return static_cast<int>(c < 1 ? (units > 0 ? 1 : 0) : c < most ? c : most);
+}
+RA_HD int64_t ext_first(int64_t units, int ctas, int i) { return units * i / ctas; }
+RA_HD int ext_cta_of(int64_t units, int ctas, int64_t u) {
+  return static_cast<int>(((u + 1) * ctas - 1) / units);
+}
+// The first tile of a block (its first unit `base`, `count` tiles of `weight` units) whose first unit
+// is not before unit u.
+RA_HD int ext_tile_from(int64_t base, int weight, int count, int64_t u) {
+  if (u <= base) return 0;
+  const int64_t j = (u - base + weight - 1) / weight;
+  return j < count ? static_cast<int>(j) : count;
+}
+
+// Units a prefix of `tiles` key tiles costs a group's sequences, each by itself (w: the units of a tile
+// of their blocks) or together; whether to share it. Sharing leaves two float parts of every row in
+// memory, written and read once, about what six tiles of the row's block take.
+RA_HD int64_t ext_block_units(const ExtShape& s, int64_t n) {
+  if (n <= 0) return 0;
+  const int64_t nb = (n - 1) / s.bt + 1;
+  return (nb - 1) * s.wide + (n - (nb - 1) * s.bt > s.half ? s.wide : 1);
+}
+RA_HD bool ext_worth_sharing(int64_t tiles, int64_t apart, int64_t together) {
+  return tiles > 0 && tiles * (apart - together) > 6 * together;
+}
+
+}  // namespace ra

@@ -15,6 +15,9 @@ constexpr uint64_t kDefaultTimeoutNs = 2000000000ull;
 
 // 3-D TMA map over a bf16 token tensor [rows, heads, head_dim]: box 64 x 1 x 128, 128B swizzle.
 cudaError_t make_token_tmap(CUtensorMap* map, const void* base, int rows, int heads, int head_dim);
+// Any bf16 map of up to 5 dimensions, innermost first, strides in bytes; 128B swizzle, 0 outside.
+cudaError_t make_tmap_bf16(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
+                           const uint64_t* strides, const uint32_t* box);
 
 // Tensor-core (bf16, head_dim 64/128) kernels.
 cudaError_t launch_fwd_tc(const Plan& P, const void* q, const void* k, const void* v, void* out,
@@ -72,12 +75,13 @@ cudaError_t launch_shard_tokens(const Plan& P, int direction, const void* src, v
 cudaError_t launch_shard_lse(const Plan& P, int direction, const float* src, float* dst,
                              cudaStream_t st);
 
-// Head norms and the paged cache (ra_heads.cu, ra_decode.cu).
+// Head norms and the paged cache (ra_heads.cu, ra_decode.cu, ra_extend.cu).
 constexpr int kHeadBwdBlocks = 608;  // most blocks of the head-norm backward (4 on each of 152 SMs)
 size_t heads_bwd_workspace(int head_dim);
 int check_cache(const ra_paged_cache* c);
 cudaError_t append_status(unsigned int* value, bool reset);
 cudaError_t decode_status(unsigned int* value, bool reset);
+cudaError_t extend_status(unsigned int value[2], bool reset);  // waits that ran out; indexes
 
 // Sets the thread's ra_last_error() message (printf format) and returns `code`.
 int record_error(int code, const char* fmt, ...);

@@ -1,6 +1,6 @@
 """Head norms, the rotation by position, the sliding window, and the serving path: a paged
-key-value cache and the attention of one new token over it (include/ringattn.h has the
-definitions).
+key-value cache and the attention of one or several new tokens over it, with prefixes that sequences
+share (include/ringattn.h has the definitions).
 
 Like ``ops``, this is a binding: every step runs in the library's kernels on the current (or a
 given) stream, outputs are allocated unless they are passed in.
@@ -13,7 +13,7 @@ from dataclasses import dataclass
 import torch
 
 from . import ops
-from ._abi import RA_BF16, RA_F32, RA_MAX_ROTARY_DIM, RaPagedCache, RaRope, check, lib
+from ._abi import RA_BF16, RA_F32, RA_MAX_ROTARY_DIM, RaPagedCache, RaRope, RaSharedPrefix, check, lib
 from .ops import Problem
 
 
@@ -307,12 +307,16 @@ def paged_workspace_bytes(cache: PagedCache, hq: int) -> int:
 
 
 def paged_attn_decode(q, cache: PagedCache, seq_lens, window: int = 0, sinks: int = 0,
-                      scale: float | None = None, out=None, lse=None, workspace=None, stream=None):
+                      scale: float | None = None, out=None, lse=None, workspace=None, stream=None,
+                      shared: SharedPrefix | None = None):
     """Attention of the last token of every sequence over the cache -> (out, lse): q, out
     [n_seqs, hq, head_dim], lse [n_seqs, hq] float32 (natural log). With ``window`` > 0 only the
     last ``window`` and the first ``sinks`` of the seq_lens[b] keys are seen. A sequence of
-    length 0 gets out = 0, lse = -inf. The workspace (``paged_workspace_bytes``) is allocated
-    when not given."""
+    length 0 gets out = 0, lse = -inf. With ``shared`` the keys that groups of sequences have in
+    common are read once for the group. The workspace (``paged_workspace_bytes``, with ``shared``
+    ``paged_extend_workspace_bytes``) is allocated when not given."""
+    if shared is not None:
+        return paged_attn_extend(q, cache, seq_lens, None, shared, window, sinks, scale, out, lse, workspace, stream)
     dt, dev, n = cache.dtype, cache.device_index, cache.n_seqs
     if q.dim() != 3:
         raise ValueError("q must be [n_seqs, hq, head_dim]")
@@ -330,4 +334,71 @@ def paged_attn_decode(q, cache: PagedCache, seq_lens, window: int = 0, sinks: in
     _launch(dev, stream, made, lambda s: lib().ra_paged_attn_decode(
         cache.ptr, hq, 0.0 if scale is None else scale, window, sinks, _ptr(q), _ptr(seq_lens), _ptr(out),
         _ptr(lse), _ptr(workspace), size, s))
+    return out, lse
+
+
+# ---- several new tokens, shared prefixes ---------------------------------------------------
+
+@dataclass
+class SharedPrefix:
+    """Prefixes that groups of a cache's sequences have in common: the sequences cu_groups[g] ..
+    cu_groups[g+1]-1 begin with the same prefix_lens[g] tokens, as a rule in the same pages. int32
+    on the device, cu_groups [n_groups + 1], prefix_lens [n_groups]; their values are read when a
+    call runs."""
+
+    cu_groups: torch.Tensor
+    prefix_lens: torch.Tensor
+
+    def __post_init__(self):
+        n = self.prefix_lens.numel()
+        for t, name, size in ((self.cu_groups, "cu_groups", n + 1), (self.prefix_lens, "prefix_lens", n)):
+            if t.dtype != torch.int32 or t.shape != (size,) or not t.is_contiguous() or not t.is_cuda:
+                raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of {size} elements, got {t.dtype} "
+                                 f"{tuple(t.shape)} on {t.device}")
+        if self.cu_groups.device != self.prefix_lens.device:
+            raise ValueError("cu_groups and prefix_lens must be on the same device")
+        self.n_groups = n
+        self.raw = RaSharedPrefix(n, self.cu_groups.data_ptr(), self.prefix_lens.data_ptr())
+        self.ptr = ctypes.byref(self.raw)
+
+
+def paged_extend_workspace_bytes(cache: PagedCache, n_tokens: int, hq: int, shared: SharedPrefix | None = None) -> int:
+    n = 0 if shared is None else shared.n_groups
+    return int(lib().ra_paged_extend_workspace_bytes(cache.ptr, n, n_tokens, hq))
+
+
+def paged_attn_extend(q, cache: PagedCache, seq_lens, cu_new=None, shared: SharedPrefix | None = None,
+                      window: int = 0, sinks: int = 0, scale: float | None = None, out=None, lse=None,
+                      workspace=None, stream=None):
+    """Causal attention of the last tokens of every sequence, which are in the cache already ->
+    (out, lse): q, out [n_tokens, hq, head_dim], lse [n_tokens, hq] float32 (natural log). seq_lens
+    [n_seqs] int32 are the lengths with the new tokens; rows cu_new[b]:cu_new[b+1] (int32
+    [n_seqs + 1], on the device) are the last tokens of sequence b, other rows are left as they
+    are. Without ``cu_new`` every sequence has one new token, or is idle (length 0: out = 0, lse =
+    -inf). The row at position p sees the keys k <= p, with ``window`` > 0 those with k > p -
+    window or k < sinks. With ``shared`` (not with a window) the keys that groups of sequences have
+    in common are read once for the group where that saves work. The workspace
+    (``paged_extend_workspace_bytes``) is allocated when not given."""
+    dt, dev = cache.dtype, cache.device_index
+    if q.dim() != 3:
+        raise ValueError("q must be [n_tokens, hq, head_dim]")
+    shape = q.shape
+    n, hq = shape[0], shape[1]
+    _plain(q, "q", dt, (n, hq, cache.head_dim), dev)
+    _plain(seq_lens, "seq_lens", torch.int32, (cache.n_seqs,), dev)
+    if cu_new is not None:
+        _plain(cu_new, "cu_new", torch.int32, (cache.n_seqs + 1,), dev)
+    if shared is not None and shared.cu_groups.get_device() != dev:
+        raise ValueError(f"shared must be on CUDA device {dev}")
+    made = []
+    out = _made_like(q, made) if out is None else _plain(out, "out", dt, shape, dev)
+    if lse is None:
+        made.append(lse := torch.empty((n, hq), device=q.device, dtype=torch.float32))
+    else:
+        _plain(lse, "lse", torch.float32, (n, hq), dev)
+    workspace, size = _workspace(
+        workspace, workspace is None and paged_extend_workspace_bytes(cache, n, hq, shared), q, made)
+    _launch(dev, stream, made, lambda s: lib().ra_paged_attn_extend(
+        cache.ptr, None if shared is None else shared.ptr, n, hq, 0.0 if scale is None else scale, window, sinks,
+        _ptr(q), _ptr(seq_lens), _ptr(cu_new), _ptr(out), _ptr(lse), _ptr(workspace), size, s))
     return out, lse

@@ -329,6 +329,48 @@ int ra_paged_attn_decode(const ra_paged_cache* c, int hq, float scale, int windo
 /* Bytes of workspace of ra_paged_attn_decode; 0 for an invalid cache or hq. */
 size_t ra_paged_workspace_bytes(const ra_paged_cache* c, int hq);
 
+/* Prefixes that groups of sequences of a batch have in common: the sequences cu_groups[g] ..
+ * cu_groups[g+1]-1 begin with the same prefix_lens[g] tokens (a document, instructions), so that
+ * their keys and values there are equal; as a rule their rows of the block table name the same
+ * pages. Sequences of no group, or with a prefix_lens of 0, share nothing. Both arrays are DEVICE
+ * arrays, cu_groups [n_groups + 1] non-decreasing within 0 .. n_seqs, prefix_lens [n_groups].
+ * Sharing changes how the keys are read, not the result: the whole key tiles (128 keys, in float32
+ * 64) of a prefix are read once for the group, by the block table row of its first sequence that has
+ * tokens, where that saves work, and where every sequence of the group has the prefix before its
+ * new tokens; else each sequence reads its own. */
+typedef struct ra_shared_prefix {
+  int32_t n_groups; /* <= n_seqs; 0: none */
+  const int32_t* cu_groups;
+  const int32_t* prefix_lens;
+} ra_shared_prefix;
+
+/* Causal attention of the last tokens of every sequence, which are in the cache already (see
+ * ra_kv_cache_append): a question after a document, a prompt that comes in chunks, drafted tokens
+ * to be checked. q and out [n_tokens, hq, head_dim] (contiguous, cache dtype; hq % hkv == 0), lse
+ * [n_tokens, hq] (float32, natural log). seq_lens [n_seqs] (device) are the lengths WITH the new
+ * tokens. cu_new [n_seqs + 1] (device): rows cu_new[b] .. cu_new[b+1]-1 are the last tokens of
+ * sequence b; rows before cu_new[0] and from cu_new[n_seqs] on are left as they are. cu_new NULL: one
+ * new token of every sequence (n_tokens = n_seqs), and a sequence of length 0 is idle: its row gets
+ * out = 0, lse = -inf. The row at position p of its sequence sees the keys k <= p, with window > 0
+ * only those with k > p - window or k < sinks (0 <= sinks <= RA_MAX_SINKS). shared may be NULL; with
+ * a window it must be. Keys that no row of a sequence sees are not read; those that some row sees
+ * must be finite (a key that a row does not see may count with weight 0). scale <= 0 selects
+ * 1/sqrt(head_dim). A sequence with more new tokens than its length, offsets that decrease or pass
+ * n_tokens, or a page index outside the cache is recorded in the device status
+ * (RA_ERR_CACHE_INDEX), and never followed. bf16 wants q, out and the pages 16-byte aligned, and
+ * strides that are multiples of 8 elements. Run-to-run bit-identical. The workspace (device, >=
+ * ra_paged_extend_workspace_bytes, 256-byte aligned) is overwritten; nothing in it is kept from
+ * call to call, so calls and captured graphs may share it as long as they do not run at the same
+ * time. */
+int ra_paged_attn_extend(const ra_paged_cache* c, const ra_shared_prefix* shared, int n_tokens, int hq,
+                         float scale, int window, int sinks, const void* q, const int32_t* seq_lens,
+                         const int32_t* cu_new, void* out, float* lse, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace of ra_paged_attn_extend (n_groups 0: nothing shared; with groups every row
+ * has two float32 results in it); 0 for arguments that the call refuses. */
+size_t ra_paged_extend_workspace_bytes(const ra_paged_cache* c, int n_groups, int n_tokens, int hq);
+
 /* Natural order <-> shard-major order of a token tensor (row = one token, `row_bytes`
  * bytes: H*Dh*element size), bit-exact copy. direction 0: natural -> shard-major (shard);
  * 1: shard-major -> natural (unshard). src and dst must not overlap. */
