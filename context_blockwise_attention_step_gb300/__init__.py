@@ -14,8 +14,8 @@ from .ops import (  # noqa: F401
     test_wait_timeout, profile_events, profile_split_event, last_error, version,
 )
 from .heads import (  # noqa: F401
-    PagedCache, Rope, SharedPrefix, kv_cache_append, make_cache, make_rope, paged_attn_decode,
-    paged_attn_extend, paged_extend_workspace_bytes, paged_workspace_bytes, qk_norm_rope_bwd,
+    AxisRope, PagedCache, Rope, SharedPrefix, axis_sections, kv_cache_append, make_axis_rope, make_cache,
+    make_rope, paged_attn_decode, paged_attn_extend, paged_extend_workspace_bytes, paged_workspace_bytes, qk_norm_rope_bwd,
     qk_norm_rope_fwd, window_attn_bwd, window_attn_fwd, window_workspace_bytes,
 )
 from .autograd import RingSelfAttention, qk_norm_rope, ring_attention, shard, unshard  # noqa: F401,E402

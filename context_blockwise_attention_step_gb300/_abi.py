@@ -25,6 +25,7 @@ RA_NOALLOC_SCRATCH_BYTES = 64 << 20
 RA_MAX_ROTARY_DIM = 128
 RA_MAX_CACHE_SEQS = 8192
 RA_MAX_SINKS = 128
+RA_MAX_AXES = 8
 
 # every symbol include/ringattn.h declares
 EXPORTS = (
@@ -36,7 +37,8 @@ EXPORTS = (
     "ra_version",
     "ra_rope_init", "ra_qk_norm_rope_fwd", "ra_qk_norm_rope_bwd", "ra_kv_cache_append",
     "ra_paged_attn_decode", "ra_paged_workspace_bytes", "ra_paged_attn_extend",
-    "ra_paged_extend_workspace_bytes",
+    "ra_paged_extend_workspace_bytes", "ra_axis_rope_init", "ra_qk_norm_axis_rope_fwd",
+    "ra_qk_norm_axis_rope_bwd", "ra_kv_cache_append_axes",
     "ra_window_attn_fwd", "ra_window_attn_bwd", "ra_window_workspace_bytes",
 )
 
@@ -64,6 +66,14 @@ class RaRope(ctypes.Structure):
         ("rotary_dim", ctypes.c_int32),
         ("interleaved", ctypes.c_int32),
         ("turns", ctypes.c_uint64 * (RA_MAX_ROTARY_DIM // 2)),
+    ]
+
+
+class RaAxisRope(ctypes.Structure):
+    _fields_ = [
+        ("rope", RaRope),
+        ("n_axes", ctypes.c_int32),
+        ("axis", ctypes.c_uint8 * (RA_MAX_ROTARY_DIM // 2)),
     ]
 
 
@@ -115,6 +125,7 @@ def lib() -> ctypes.CDLL:
     L = ctypes.CDLL(LIB_PATH)
     P = ctypes.POINTER(RaProblem)
     R, C = ctypes.POINTER(RaRope), ctypes.POINTER(RaPagedCache)
+    X = ctypes.POINTER(RaAxisRope)
     vp, i32, i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64
     f32, size = ctypes.c_float, ctypes.c_size_t
     sig = {
@@ -143,6 +154,12 @@ def lib() -> ctypes.CDLL:
                                       vp, size, vp]),
         "ra_kv_cache_append": (i32, [C, R, f32, i32, i32, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp,
                                      vp, vp]),
+        "ra_axis_rope_init": (i32, [X, i32, i32, ctypes.POINTER(ctypes.c_double), i32, ctypes.POINTER(ctypes.c_int32)]),
+        "ra_qk_norm_axis_rope_fwd": (i32, [P, X, vp, i64, f32, vp, i64, vp, i64, vp, vp, vp, vp, vp]),
+        "ra_qk_norm_axis_rope_bwd": (i32, [P, X, vp, i64, f32, vp, vp, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp,
+                                           vp, size, vp]),
+        "ra_kv_cache_append_axes": (i32, [C, X, vp, i64, f32, i32, i32, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp,
+                                          vp, vp]),
         "ra_paged_attn_decode": (i32, [C, i32, f32, i32, i32, vp, vp, vp, vp, vp, size, vp]),
         "ra_paged_workspace_bytes": (size, [C, i32]),
         "ra_paged_attn_extend": (i32, [C, ctypes.POINTER(RaSharedPrefix), i32, i32, f32, i32, i32, vp, vp, vp, vp,

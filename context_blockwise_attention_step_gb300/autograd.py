@@ -52,22 +52,24 @@ class _RingAttention(torch.autograd.Function):
 
 class _QkNormRope(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, q_weight, k_weight, prob, rope, eps):
+    def forward(ctx, q, k, q_weight, k_weight, prob, rope, eps, positions):
         # without a norm the backward does not look at q and k
-        ctx.save_for_backward(*((q, k, q_weight, k_weight) if q_weight is not None else ()))
+        ctx.save_for_backward(positions, *((q, k, q_weight, k_weight) if q_weight is not None else ()))
         ctx.prob, ctx.rope, ctx.eps = prob, rope, eps
-        return heads.qk_norm_rope_fwd(q, k, prob, q_weight=q_weight, k_weight=k_weight, rope=rope, eps=eps)
+        return heads.qk_norm_rope_fwd(q, k, prob, q_weight=q_weight, k_weight=k_weight, rope=rope, eps=eps,
+                                      positions=positions)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dq_out, dk_out):
         dq_out, dk_out = dq_out.contiguous(), dk_out.contiguous()
-        q, k, q_weight, k_weight = ctx.saved_tensors or (dq_out, dk_out, None, None)
+        positions, *saved = ctx.saved_tensors
+        q, k, q_weight, k_weight = saved or (dq_out, dk_out, None, None)
         dq, dk, dqw, dkw = heads.qk_norm_rope_bwd(dq_out, dk_out, q, k, ctx.prob, q_weight=q_weight,
-                                                  k_weight=k_weight, rope=ctx.rope, eps=ctx.eps)
+                                                  k_weight=k_weight, rope=ctx.rope, eps=ctx.eps, positions=positions)
         if dqw is not None:  # float32 sums, rounded once to the parameter's type
             dqw, dkw = dqw.to(q_weight.dtype), dkw.to(k_weight.dtype)
-        return dq, dk, dqw, dkw, None, None, None
+        return dq, dk, dqw, dkw, None, None, None, None
 
 
 class _Shard(torch.autograd.Function):
@@ -91,10 +93,11 @@ def ring_attention(q, k, v, prob: ops.Problem, window: int = 0, sinks: int = 0):
     return _RingAttention.apply(q, k, v, prob, window, sinks)
 
 
-def qk_norm_rope(q, k, prob: ops.Problem, q_weight=None, k_weight=None, rope: heads.Rope | None = None,
-                 eps: float = 1e-6):
-    """Differentiable per-head norm and rotation by position of shard-major q and k."""
-    return _QkNormRope.apply(q, k, q_weight, k_weight, prob, rope, eps)
+def qk_norm_rope(q, k, prob: ops.Problem, q_weight=None, k_weight=None,
+                 rope: heads.Rope | heads.AxisRope | None = None, eps: float = 1e-6, positions=None):
+    """Differentiable per-head norm and rotation by position of shard-major q and k (with an
+    ``AxisRope`` by ``positions``, shard-major too)."""
+    return _QkNormRope.apply(q, k, q_weight, k_weight, prob, rope, eps, positions)
 
 
 def shard(x, prob: ops.Problem):
@@ -117,14 +120,16 @@ class RingSelfAttention(torch.nn.Module):
     tokens once at the input keeps them so through every token-wise layer).
 
     ``qk_norm`` adds a norm of every query and key head (weights of head_dim), ``rope`` a rotation
-    by position, ``window`` and ``sinks`` a sliding window with always visible first tokens.
-    ``prefill`` and ``decode`` are the layer's serving form over a paged key-value cache.
+    by position, ``window`` and ``sinks`` a sliding window with always visible first tokens. With an
+    ``AxisRope`` every call takes the tokens' ``positions`` (int32, x's leading shape and n_axes).
+    ``prefill``, ``extend`` and ``decode`` are the layer's serving form over a paged key-value cache.
     """
 
     def __init__(self, hidden: int, hq: int, hkv: int, head_dim: int, *, D: int,
                  layout: str = "zigzag", causal: bool = True, shard_major: bool = False,
                  device=None, dtype=torch.bfloat16, seed: int = 0, qk_norm: bool = False,
-                 rope: heads.Rope | None = None, window: int = 0, sinks: int = 0, eps: float = 1e-6):
+                 rope: heads.Rope | heads.AxisRope | None = None, window: int = 0, sinks: int = 0,
+                 eps: float = 1e-6):
         super().__init__()
         if hq % hkv:
             raise ValueError("hq must be a multiple of hkv")
@@ -159,26 +164,28 @@ class RingSelfAttention(torch.nn.Module):
                 (x @ self.wk.t()).view(*lead, self.hkv, self.head_dim),
                 (x @ self.wv.t()).view(*lead, self.hkv, self.head_dim))
 
-    def _attend(self, q, k, v, prob):
+    def _attend(self, q, k, v, prob, positions):
         """Norm, rotation and attention of shard-major q, k, v -> (out, the k that was attended to)."""
         if self.q_norm is not None or self.rope is not None:
-            q, k = qk_norm_rope(q, k, prob, self.q_norm, self.k_norm, self.rope, self.eps)
+            q, k = qk_norm_rope(q, k, prob, self.q_norm, self.k_norm, self.rope, self.eps, positions)
         out, _ = ring_attention(q.contiguous(), k.contiguous(), v.contiguous(), prob, self.window, self.sinks)
         return out, k
 
-    def forward(self, x):
+    def forward(self, x, positions=None):
         b, s, _ = x.shape
         prob = self.problem(b, s)
         q, k, v = self._qkv(x)
         if not self.shard_major:
             q, k, v = shard(q, prob), shard(k, prob), shard(v, prob)
-        out, _ = self._attend(q, k, v, prob)
+            if positions is not None:
+                positions = ops.shard_tokens(positions.contiguous(), prob)
+        out, _ = self._attend(q, k, v, prob, positions)
         if not self.shard_major:
             out = unshard(out, prob)
         return out.reshape(b, s, self.hq * self.head_dim) @ self.wo.t()
 
     @torch.no_grad()
-    def prefill(self, x, cache: heads.PagedCache, cu_seqlens):
+    def prefill(self, x, cache: heads.PagedCache, cu_seqlens, positions=None):
         """The prompts of the cache's sequences, packed [T, hidden] in natural order with host
         offsets ``cu_seqlens`` [n_seqs + 1]: y [T, hidden], and their keys and values in the cache
         from its first place on."""
@@ -187,21 +194,39 @@ class RingSelfAttention(torch.nn.Module):
         prob = ops.make_problem(dtype=self.wq.dtype, layout="basic", causal=True, D=1, hq=self.hq,
                                 hkv=self.hkv, head_dim=self.head_dim, cu_seqlens=cu_seqlens)
         q, k, v = self._qkv(x)
-        out, k = self._attend(q, k, v, prob)
+        out, k = self._attend(q, k, v, prob, positions)
         cu = torch.from_numpy(prob.cu_host).to(x.device)
         heads.kv_cache_append(None, k, v, cache, cu[1:] - cu[:-1], cu_new=cu)
         return out.reshape(x.shape[0], self.hq * self.head_dim) @ self.wo.t()
 
-    @torch.no_grad()
-    def decode(self, x, cache: heads.PagedCache, seq_lens, workspace=None):
-        """One new token of every sequence, x [n_seqs, hidden] -> y [n_seqs, hidden]. seq_lens
-        [n_seqs] (int32, on the device) are the lengths with the new tokens; a sequence of length
-        0 is idle, and its row of y is 0."""
+    def _append(self, x, cache, seq_lens, cu_new, positions):
+        """New tokens x into the cache -> their queries."""
         if not self.causal:
             raise ValueError("a cache wants causal attention")
         q, k, v = self._qkv(x)
-        q = heads.kv_cache_append(q, k, v, cache, seq_lens, q_weight=self.q_norm, k_weight=self.k_norm,
-                                  rope=self.rope, eps=self.eps)
+        return heads.kv_cache_append(q, k, v, cache, seq_lens, cu_new=cu_new, q_weight=self.q_norm,
+                                     k_weight=self.k_norm, rope=self.rope, eps=self.eps, positions=positions)
+
+    @torch.no_grad()
+    def extend(self, x, cache: heads.PagedCache, seq_lens, cu_new, positions=None,
+               shared: heads.SharedPrefix | None = None, workspace=None):
+        """Several new tokens of every sequence after those in the cache, packed x [T, hidden] -> y
+        [T, hidden]: rows cu_new[b]:cu_new[b+1] (int32 [n_seqs + 1], on the device; from 0 to T) are the
+        last of the seq_lens[b] tokens that sequence b has with them. ``shared`` tells of prefixes
+        that sequences have in common (their keys are in the cache already); a layer with a window
+        reads every sequence's own."""
+        q = self._append(x, cache, seq_lens, cu_new, positions)
+        out, _ = heads.paged_attn_extend(q, cache, seq_lens, cu_new, shared=None if self.window else shared,
+                                         window=self.window, sinks=self.sinks, workspace=workspace)
+        return out.view(x.shape[0], self.hq * self.head_dim) @ self.wo.t()
+
+    @torch.no_grad()
+    def decode(self, x, cache: heads.PagedCache, seq_lens, workspace=None, positions=None,
+               shared: heads.SharedPrefix | None = None):
+        """One new token of every sequence, x [n_seqs, hidden] -> y [n_seqs, hidden]. seq_lens
+        [n_seqs] (int32, on the device) are the lengths with the new tokens; a sequence of length
+        0 is idle, and its row of y is 0. ``shared`` as for ``extend``."""
+        q = self._append(x, cache, seq_lens, None, positions)
         out, _ = heads.paged_attn_decode(q, cache, seq_lens, window=self.window, sinks=self.sinks,
-                                         workspace=workspace)
+                                         workspace=workspace, shared=None if self.window else shared)
         return out.view(x.shape[0], self.hq * self.head_dim) @ self.wo.t()

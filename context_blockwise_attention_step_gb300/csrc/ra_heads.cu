@@ -5,6 +5,9 @@
 //   n = x * r,  r = rsqrt(mean(x^2) + eps);   y = R(pos) (n * w)
 //   backward: g = R(pos)^T dy;  dw = sum g * n;  h = g * w;  dx = r * (h - n * mean(h * n))
 //
+// A token's position is its place in its sequence, or it has positions on several axes (time, height,
+// width), given with the tokens, and every pair of the rotation turns by one of them.
+//
 // Angles: pair i turns by pos * inv_freq[i]. A float product would lose the angle at far
 // positions (at 2^17 the spacing of floats near pos * 1 rad is 2^-7 rad), so inv_freq / 2pi is
 // kept as a 64-bit fraction of a turn: its product with the position, modulo 2^64, is the
@@ -49,6 +52,21 @@ struct CacheRows {
   const int32_t* block_table;
   int64_t table_stride, page_stride, slot_stride, head_stride;
   int32_t n_seqs, max_pages, page_size, n_pages;
+};
+
+// Positions on several axes: `stride` elements from one row's to the next.
+struct AxisPos {
+  const int32_t* pos;
+  int64_t stride;
+  uint8_t axis[RA_MAX_ROTARY_DIM / 2];  // of every pair
+};
+// The rows of a ring problem, whose order does not matter then, and of a cache.
+struct RingAxisRows {
+  AxisPos at;
+};
+struct CacheAxisRows {
+  CacheRows rows;
+  AxisPos at;
 };
 
 // One token: its position, and where its k and v go.
@@ -117,6 +135,32 @@ __device__ __forceinline__ Token locate(const CacheRows& R, int row, int64_t) {
   return t;
 }
 
+__device__ __forceinline__ Token locate(const RingAxisRows&, int row, int64_t kv_row) {
+  Token t;
+  t.absent = t.idle = false;
+  t.kv = static_cast<int64_t>(row) * kv_row;
+  t.pos = 0;
+  return t;
+}
+__device__ __forceinline__ Token locate(const CacheAxisRows& R, int row, int64_t kv_row) {
+  return locate(R.rows, row, kv_row);
+}
+
+// The position that pair `pair` of row `row` turns by; `place` is the row's place in its sequence.
+template <typename Rows>
+__device__ __forceinline__ int64_t turn_by(const Rows&, int64_t, int64_t place, int) {
+  return place;
+}
+__device__ __forceinline__ int64_t turn_by(const AxisPos& P, int64_t row, int pair) {
+  return P.pos[row * P.stride + P.axis[pair]];
+}
+__device__ __forceinline__ int64_t turn_by(const RingAxisRows& R, int64_t row, int64_t, int pair) {
+  return turn_by(R.at, row, pair);
+}
+__device__ __forceinline__ int64_t turn_by(const CacheAxisRows& R, int64_t row, int64_t, int pair) {
+  return turn_by(R.at, row, pair);
+}
+
 __device__ __forceinline__ float ldf(const float* p) { return *p; }
 __device__ __forceinline__ float ldf(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 __device__ __forceinline__ void stf(float* p, float v) { *p = v; }
@@ -153,7 +197,9 @@ struct LaneTurn {
   float cs[kPerLane], sn[kPerLane];
   int other[kPerLane];
 };
-__device__ __forceinline__ LaneTurn lane_turn(const HeadArgs& A, int64_t pos, int lane, float sign) {
+template <typename Rows>
+__device__ __forceinline__ LaneTurn lane_turn(const HeadArgs& A, const Rows& R, int64_t token, int64_t place, int lane,
+                                              float sign) {
   LaneTurn t;
   const int rd = A.rope.rotary_dim;
 #pragma unroll
@@ -166,7 +212,7 @@ __device__ __forceinline__ LaneTurn lane_turn(const HeadArgs& A, int64_t pos, in
       const bool second = A.rope.interleaved ? d & 1 : d >= rd / 2;
       const int pair = A.rope.interleaved ? d >> 1 : second ? d - rd / 2 : d;
       t.other[i] = A.rope.interleaved ? d ^ 1 : second ? d - rd / 2 : d + rd / 2;
-      const float2 c = cos_sin(A.rope.turns[pair], pos);
+      const float2 c = cos_sin(A.rope.turns[pair], turn_by(R, token, place, pair));
       t.cs[i] = c.x;
       t.sn[i] = second ? sign * c.y : -sign * c.y;
     }
@@ -248,7 +294,7 @@ __global__ void __launch_bounds__(kThreads)
     return;
   }
   const bool turned = A.rope.rotary_dim > 0;
-  const LaneTurn turn = lane_turn(A, tok.pos, lane, 1.f);
+  const LaneTurn turn = lane_turn(A, R, t, tok.pos, lane, 1.f);
   any_run(A, qw, turned, turn, q + t * A.q_stride, qo, dh, A.hq, part, parts, row, lane);
   // the next run of heads goes on with the part after the last one's
   const int pk = ((part - A.hq) % parts + parts) % parts;
@@ -307,9 +353,9 @@ __device__ __forceinline__ void any_run_bwd(const HeadArgs& A, const T* w, bool 
   }
 }
 
-template <typename T>
+template <typename T, typename Rows>
 __global__ void __launch_bounds__(kThreads)
-    heads_bwd_any(const __grid_constant__ HeadArgs A, const __grid_constant__ RingRows R, int parts,
+    heads_bwd_any(const __grid_constant__ HeadArgs A, const __grid_constant__ Rows R, int parts,
                   const T* __restrict__ qw, const T* __restrict__ kw, const T* __restrict__ q,
                   const T* __restrict__ k, const T* dq_out, const T* dk_out, T* dq, T* dk,
                   float* __restrict__ partial) {
@@ -324,7 +370,7 @@ __global__ void __launch_bounds__(kThreads)
        u += static_cast<int64_t>(gridDim.x) * kWarps) {
     const int64_t t = u / parts;
     const int part = static_cast<int>(u - t * parts);
-    const LaneTurn turn = lane_turn(A, locate(R, static_cast<int>(t), 0).pos, lane, -1.f);
+    const LaneTurn turn = lane_turn(A, R, t, locate(R, static_cast<int>(t), 0).pos, lane, -1.f);
     const int64_t oq = t * A.hq * dh, ok = t * A.hkv * dh;
     any_run_bwd(A, qw, turned, turn, q + t * A.q_stride, dq_out + oq, dq + oq, A.hq, part, parts, row, lane, acc[0]);
     const int pk = ((part - A.hq) % parts + parts) % parts;
@@ -423,8 +469,8 @@ __device__ __forceinline__ uint4 narrow(const float (&x)[8]) {
 
 // Cosines and sines of the pairs of this lane's pieces. The HEADS lanes that hold the same
 // pieces of different heads need the same angles: each works out its share, and they exchange.
-template <typename T, int DH, bool INTER>
-__device__ __forceinline__ void piece_angles(const HeadArgs& A, int64_t pos, int lane,
+template <typename T, int DH, bool INTER, typename Rows>
+__device__ __forceinline__ void piece_angles(const HeadArgs& A, const Rows& R, int64_t token, int64_t place, int lane,
                                              float (&cs)[Vec<T, DH>::N], float (&sn)[Vec<T, DH>::N]) {
   using V = Vec<T, DH>;
   const int c = lane % V::LANES, sub = lane / V::LANES;
@@ -433,7 +479,7 @@ __device__ __forceinline__ void piece_angles(const HeadArgs& A, int64_t pos, int
   for (int k = 0; k < V::PER; ++k) {
     const int j = (sub * V::PER + k) % V::N;
     const int pair = !INTER ? c * V::N + j : j < V::N / 2 ? c * V::N / 2 + j : size_of<DH>(A) / 4 + c * V::N / 2 + j - V::N / 2;
-    mine[k] = pair < A.rope.rotary_dim / 2 ? cos_sin(A.rope.turns[pair], pos) : make_float2(1.f, 0.f);
+    mine[k] = pair < A.rope.rotary_dim / 2 ? cos_sin(A.rope.turns[pair], turn_by(R, token, place, pair)) : make_float2(1.f, 0.f);
   }
 #pragma unroll
   for (int j = 0; j < V::N; ++j) {
@@ -574,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 3)
   float cs[V::N], sn[V::N];
   const bool turned = A.rope.rotary_dim > 0;
   auto angles = [&]() {
-    if (turned) piece_angles<T, DH, INTER>(A, tok.pos, lane, cs, sn);
+    if (turned) piece_angles<T, DH, INTER>(A, R, t, tok.pos, lane, cs, sn);
   };
   auto none = []() {};
   const int runs_q = (A.hq + V::HEADS - 1) / V::HEADS, runs_k = (A.hkv + V::HEADS - 1) / V::HEADS;
@@ -667,9 +713,9 @@ __device__ __forceinline__ void head_run_bwd(const HeadArgs& A, const T* __restr
 
 // Four blocks an SM with two heads' loads of a lane in flight, at the same size (659 us then):
 // four with one 777, five with one 933, three with two 946.
-template <typename T, int DH, bool INTER>
+template <typename T, int DH, bool INTER, typename Rows>
 __global__ void __launch_bounds__(kBwdThreads, 4)
-    heads_bwd_vec(const __grid_constant__ HeadArgs A, const __grid_constant__ RingRows R,
+    heads_bwd_vec(const __grid_constant__ HeadArgs A, const __grid_constant__ Rows R,
                   const T* __restrict__ qw, const T* __restrict__ kw, const T* __restrict__ q,
                   const T* __restrict__ k, const T* dq_out, const T* dk_out, T* dq, T* dk,
                   float* __restrict__ partial) {
@@ -685,7 +731,7 @@ __global__ void __launch_bounds__(kBwdThreads, 4)
     const int64_t oq = t * A.hq * dh, ok = t * A.hkv * dh;
     head_run_bwd<T, DH, INTER, 2>(
         A, qw, turned, q + t * A.q_stride, dq_out + oq, dq + oq, A.hq, lane, cs, sn, acc[0][0], acc[0][1], [&]() {
-          if (turned) piece_angles<T, DH, INTER>(A, locate(R, static_cast<int>(t), 0).pos, lane, cs, sn);
+          if (turned) piece_angles<T, DH, INTER>(A, R, t, locate(R, static_cast<int>(t), 0).pos, lane, cs, sn);
         });
     head_run_bwd<T, DH, INTER, 2>(A, kw, turned, k + t * A.k_stride, dk_out + ok, dk + ok, A.hkv, lane, cs, sn,
                                   acc[1][0], acc[1][1], []() {});
@@ -854,18 +900,18 @@ cudaError_t launch_fwd(const HeadArgs& A, const Rows& R, const void* qw, const v
   return cudaGetLastError();
 }
 
-template <typename T, int DH, bool INTER>
-void bwd_vec(unsigned blocks, const HeadArgs& A, const RingRows& R, const void* qw, const void* kw, const void* q,
+template <typename T, int DH, bool INTER, typename Rows>
+void bwd_vec(unsigned blocks, const HeadArgs& A, const Rows& R, const void* qw, const void* kw, const void* q,
              const void* k, const void* dq_out, const void* dk_out, void* dq, void* dk, float* partial,
              cudaStream_t st) {
-  heads_bwd_vec<T, DH, INTER><<<blocks, kBwdThreads, 0, st>>>(
+  heads_bwd_vec<T, DH, INTER, Rows><<<blocks, kBwdThreads, 0, st>>>(
       A, R, static_cast<const T*>(qw), static_cast<const T*>(kw), static_cast<const T*>(q),
       static_cast<const T*>(k), static_cast<const T*>(dq_out), static_cast<const T*>(dk_out),
       static_cast<T*>(dq), static_cast<T*>(dk), partial);
 }
 
-template <typename T>
-cudaError_t launch_bwd(const HeadArgs& A, const RingRows& R, const void* qw, const void* kw,
+template <typename T, typename Rows>
+cudaError_t launch_bwd(const HeadArgs& A, const Rows& R, const void* qw, const void* kw,
                        const void* q, const void* k, const void* dq_out, const void* dk_out,
                        void* dq, void* dk, float* partial, float* dqw, float* dkw, cudaStream_t st) {
   unsigned blocks;
@@ -880,7 +926,7 @@ cudaError_t launch_bwd(const HeadArgs& A, const RingRows& R, const void* qw, con
   } else {
     const int parts = parts_of(A.n_rows, A.hq + A.hkv);
     blocks = blocks_for(static_cast<int64_t>(A.n_rows) * parts, kWarps, kHeadBwdBlocks);
-    heads_bwd_any<T><<<blocks, kThreads, 0, st>>>(
+    heads_bwd_any<T, Rows><<<blocks, kThreads, 0, st>>>(
         A, R, parts, static_cast<const T*>(qw), static_cast<const T*>(kw), static_cast<const T*>(q),
         static_cast<const T*>(k), static_cast<const T*>(dq_out), static_cast<const T*>(dk_out),
         static_cast<T*>(dq), static_cast<T*>(dk), partial);
@@ -970,11 +1016,49 @@ extern "C" int ra_rope_init(ra_rope* rope, int rotary_dim, int interleaved, cons
   return RA_OK;
 }
 
-extern "C" int ra_qk_norm_rope_fwd(const ra_problem* p, const ra_rope* rope, float eps, const void* q,
-                                   int64_t q_row_stride, const void* k, int64_t k_row_stride,
-                                   const void* q_weight, const void* k_weight, void* q_out, void* k_out,
-                                   void* stream) {
-  if (int e = ra_validate(p)) return e;
+namespace {
+
+// Positions on several axes of a call: none for a rotation by place.
+struct Axes {
+  const ra_axis_rope* rope;
+  const int32_t* pos;
+  int64_t stride;
+};
+constexpr Axes kNoAxes = {nullptr, nullptr, 0};
+
+int check_axes(const ra_axis_rope* rope, const int32_t* pos, int64_t stride, bool some) {
+  if (rope == nullptr) return record_error(RA_ERR_INVALID_ARG, "rope is NULL");
+  if (rope->n_axes < 1 || rope->n_axes > RA_MAX_AXES)
+    return record_error(RA_ERR_INVALID_ARG, "rope: n_axes must be 1..%d (use ra_axis_rope_init)", RA_MAX_AXES);
+  for (int i = 0; i < rope->rope.rotary_dim / 2 && i < RA_MAX_ROTARY_DIM / 2; ++i)
+    if (rope->axis[i] >= rope->n_axes)
+      return record_error(RA_ERR_INVALID_ARG, "rope: axis[%d] is %d of %d axes", i, rope->axis[i], rope->n_axes);
+  if (some && pos == nullptr) return record_error(RA_ERR_INVALID_ARG, "positions is NULL");
+  if (stride < rope->n_axes)
+    return record_error(RA_ERR_SHAPE, "pos_row_stride must be >= n_axes (%d)", rope->n_axes);
+  return RA_OK;
+}
+
+AxisPos axis_pos(const Axes& x) {
+  AxisPos a;
+  a.pos = x.pos;
+  a.stride = x.stride;
+  for (int i = 0; i < RA_MAX_ROTARY_DIM / 2; ++i) a.axis[i] = x.rope->axis[i];
+  return a;
+}
+
+// Calls f with the rows of a ring problem.
+template <typename F>
+cudaError_t with_rows(const ra_problem* p, const Axes& x, F&& f) {
+  if (x.rope != nullptr) return f(RingAxisRows{axis_pos(x)});
+  RingRows R;
+  fill_rows(p, &R);
+  return f(R);
+}
+
+int norm_rope_fwd(const ra_problem* p, const ra_rope* rope, const Axes& axes, float eps, const void* q,
+                  int64_t q_row_stride, const void* k, int64_t k_row_stride, const void* q_weight,
+                  const void* k_weight, void* q_out, void* k_out, void* stream) {
   const bool some = rows_of(p) > 0;  // empty tensors may have null pointers
   if (some && (!q || !k || !q_out || !k_out)) return record_error(RA_ERR_INVALID_ARG, "null tensor pointer");
   if (int e = check_rope(rope, p->head_dim)) return e;
@@ -987,29 +1071,26 @@ extern "C" int ra_qk_norm_rope_fwd(const ra_problem* p, const ra_rope* rope, flo
   if (some && ((q == q_out && q_row_stride != nq) || (k == k_out && k_row_stride != nk)))
     return record_error(RA_ERR_INVALID_ARG, "in place wants contiguous rows");
   if (!some) return record_error(RA_OK, "%s", "");
-  const int n_rows = rows_of(p);
-  RingRows R;
   HeadArgs A;
-  fill_rows(p, &R);
-  fill_args(&A, rope, eps, p->hq, p->hkv, p->head_dim, n_rows);
+  fill_args(&A, rope, eps, p->hq, p->hkv, p->head_dim, rows_of(p));
   A.q_stride = q_row_stride;
   A.k_stride = k_row_stride;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e =
-      p->dtype == RA_F32
-          ? launch_fwd<float, RingRows, false>(A, R, q_weight, k_weight, q, k, nullptr, q_out, k_out, nullptr, true, st)
-          : launch_fwd<__nv_bfloat16, RingRows, false>(A, R, q_weight, k_weight, q, k, nullptr, q_out, k_out,
-                                                       nullptr, true, st);
+  const cudaError_t e = with_rows(p, axes, [&](const auto& R) {
+    using Rows = std::decay_t<decltype(R)>;
+    return p->dtype == RA_F32
+               ? launch_fwd<float, Rows, false>(A, R, q_weight, k_weight, q, k, nullptr, q_out, k_out, nullptr, true, st)
+               : launch_fwd<__nv_bfloat16, Rows, false>(A, R, q_weight, k_weight, q, k, nullptr, q_out, k_out,
+                                                        nullptr, true, st);
+  });
   if (e != cudaSuccess) return record_error(RA_ERR_CUDA, "norm and rotation launch: %s", cudaGetErrorString(e));
   return record_error(RA_OK, "%s", "");
 }
 
-extern "C" int ra_qk_norm_rope_bwd(const ra_problem* p, const ra_rope* rope, float eps, const void* dq_out,
-                                   const void* dk_out, const void* q, int64_t q_row_stride, const void* k,
-                                   int64_t k_row_stride, const void* q_weight, const void* k_weight, void* dq,
-                                   void* dk, float* dq_weight, float* dk_weight, void* workspace,
-                                   size_t workspace_bytes, void* stream) {
-  if (int e = ra_validate(p)) return e;
+int norm_rope_bwd(const ra_problem* p, const ra_rope* rope, const Axes& axes, float eps, const void* dq_out,
+                  const void* dk_out, const void* q, int64_t q_row_stride, const void* k, int64_t k_row_stride,
+                  const void* q_weight, const void* k_weight, void* dq, void* dk, float* dq_weight,
+                  float* dk_weight, void* workspace, size_t workspace_bytes, void* stream) {
   const bool some = rows_of(p) > 0;  // empty tensors may have null pointers
   if (some && (!dq_out || !dk_out || !dq || !dk)) return record_error(RA_ERR_INVALID_ARG, "null tensor pointer");
   if (int e = check_rope(rope, p->head_dim)) return e;
@@ -1036,29 +1117,27 @@ extern "C" int ra_qk_norm_rope_bwd(const ra_problem* p, const ra_rope* rope, flo
       if (e == cudaSuccess) e = cudaMemsetAsync(dk_weight, 0, p->head_dim * sizeof(float), st);
     }
   } else {
-    RingRows R;
     HeadArgs A;
-    fill_rows(p, &R);
     fill_args(&A, rope, eps, p->hq, p->hkv, p->head_dim, n_rows);
     A.q_stride = q_row_stride;
     A.k_stride = k_row_stride;
     float* partial = static_cast<float*>(workspace);
-    e = p->dtype == RA_F32 ? launch_bwd<float>(A, R, q_weight, k_weight, q, k, dq_out, dk_out, dq, dk, partial,
-                                               dq_weight, dk_weight, st)
-                           : launch_bwd<__nv_bfloat16>(A, R, q_weight, k_weight, q, k, dq_out, dk_out, dq, dk,
-                                                       partial, dq_weight, dk_weight, st);
+    e = with_rows(p, axes, [&](const auto& R) {
+      return p->dtype == RA_F32 ? launch_bwd<float>(A, R, q_weight, k_weight, q, k, dq_out, dk_out, dq, dk, partial,
+                                                    dq_weight, dk_weight, st)
+                                : launch_bwd<__nv_bfloat16>(A, R, q_weight, k_weight, q, k, dq_out, dk_out, dq, dk,
+                                                            partial, dq_weight, dk_weight, st);
+    });
   }
   if (e != cudaSuccess)
     return record_error(RA_ERR_CUDA, "norm and rotation backward launch: %s", cudaGetErrorString(e));
   return record_error(RA_OK, "%s", "");
 }
 
-extern "C" int ra_kv_cache_append(const ra_paged_cache* c, const ra_rope* rope, float eps, int n_tokens, int hq,
-                                  const void* q, int64_t q_row_stride, const void* k, int64_t k_row_stride,
-                                  const void* v, int64_t v_row_stride, const void* q_weight,
-                                  const void* k_weight, const int32_t* seq_lens, const int32_t* cu_new,
-                                  void* q_out, void* stream) {
-  if (int e = check_cache(c)) return e;
+int cache_append(const ra_paged_cache* c, const ra_rope* rope, const Axes& axes, float eps, int n_tokens, int hq,
+                 const void* q, int64_t q_row_stride, const void* k, int64_t k_row_stride, const void* v,
+                 int64_t v_row_stride, const void* q_weight, const void* k_weight, const int32_t* seq_lens,
+                 const int32_t* cu_new, void* q_out, void* stream) {
   if ((q == nullptr) != (q_out == nullptr)) return record_error(RA_ERR_INVALID_ARG, "pass both q and q_out or neither");
   const bool some = n_tokens > 0 && c->n_seqs > 0;  // empty tensors may have null pointers
   if (some && (!k || !v || !seq_lens)) return record_error(RA_ERR_INVALID_ARG, "null tensor pointer");
@@ -1098,11 +1177,94 @@ extern "C" int ra_kv_cache_append(const ra_paged_cache* c, const ra_rope* rope, 
   const int elem = c->dtype == RA_F32 ? 4 : 2;  // of the pages, kv_head is looked at with the rows
   const bool pages16 = c->page_stride * elem % 16 == 0 && c->slot_stride * elem % 16 == 0;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e =
-      c->dtype == RA_F32
-          ? launch_fwd<float, CacheRows, true>(A, R, q_weight, k_weight, q, k, v, q_out, c->k_pages, c->v_pages, pages16, st)
-          : launch_fwd<__nv_bfloat16, CacheRows, true>(A, R, q_weight, k_weight, q, k, v, q_out, c->k_pages,
+  auto put = [&](const auto& rows) {
+    using Rows = std::decay_t<decltype(rows)>;
+    return c->dtype == RA_F32
+               ? launch_fwd<float, Rows, true>(A, rows, q_weight, k_weight, q, k, v, q_out, c->k_pages, c->v_pages, pages16, st)
+               : launch_fwd<__nv_bfloat16, Rows, true>(A, rows, q_weight, k_weight, q, k, v, q_out, c->k_pages,
                                                        c->v_pages, pages16, st);
+  };
+  const cudaError_t e = axes.rope != nullptr ? put(CacheAxisRows{R, axis_pos(axes)}) : put(R);
   if (e != cudaSuccess) return record_error(RA_ERR_CUDA, "append launch: %s", cudaGetErrorString(e));
   return record_error(RA_OK, "%s", "");
+}
+
+}  // namespace
+
+extern "C" int ra_qk_norm_rope_fwd(const ra_problem* p, const ra_rope* rope, float eps, const void* q,
+                                   int64_t q_row_stride, const void* k, int64_t k_row_stride,
+                                   const void* q_weight, const void* k_weight, void* q_out, void* k_out,
+                                   void* stream) {
+  if (int e = ra_validate(p)) return e;
+  return norm_rope_fwd(p, rope, kNoAxes, eps, q, q_row_stride, k, k_row_stride, q_weight, k_weight, q_out, k_out,
+                       stream);
+}
+
+extern "C" int ra_qk_norm_rope_bwd(const ra_problem* p, const ra_rope* rope, float eps, const void* dq_out,
+                                   const void* dk_out, const void* q, int64_t q_row_stride, const void* k,
+                                   int64_t k_row_stride, const void* q_weight, const void* k_weight, void* dq,
+                                   void* dk, float* dq_weight, float* dk_weight, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+  if (int e = ra_validate(p)) return e;
+  return norm_rope_bwd(p, rope, kNoAxes, eps, dq_out, dk_out, q, q_row_stride, k, k_row_stride, q_weight, k_weight, dq,
+                       dk, dq_weight, dk_weight, workspace, workspace_bytes, stream);
+}
+
+extern "C" int ra_kv_cache_append(const ra_paged_cache* c, const ra_rope* rope, float eps, int n_tokens, int hq,
+                                  const void* q, int64_t q_row_stride, const void* k, int64_t k_row_stride,
+                                  const void* v, int64_t v_row_stride, const void* q_weight,
+                                  const void* k_weight, const int32_t* seq_lens, const int32_t* cu_new,
+                                  void* q_out, void* stream) {
+  if (int e = check_cache(c)) return e;
+  return cache_append(c, rope, kNoAxes, eps, n_tokens, hq, q, q_row_stride, k, k_row_stride, v, v_row_stride, q_weight,
+                      k_weight, seq_lens, cu_new, q_out, stream);
+}
+
+extern "C" int ra_axis_rope_init(ra_axis_rope* rope, int rotary_dim, int interleaved, const double* inv_freq,
+                                 int n_axes, const int32_t* axis) {
+  if (rope == nullptr || axis == nullptr) return record_error(RA_ERR_INVALID_ARG, "null pointer");
+  if (n_axes < 1 || n_axes > RA_MAX_AXES)
+    return record_error(RA_ERR_INVALID_ARG, "n_axes must be 1..%d (got %d)", RA_MAX_AXES, n_axes);
+  if (int e = ra_rope_init(&rope->rope, rotary_dim, interleaved, inv_freq)) return e;
+  rope->n_axes = n_axes;
+  for (int i = 0; i < RA_MAX_ROTARY_DIM / 2; ++i) {
+    const int a = i < rotary_dim / 2 ? axis[i] : 0;
+    if (a < 0 || a >= n_axes) return record_error(RA_ERR_INVALID_ARG, "axis[%d] is %d of %d axes", i, a, n_axes);
+    rope->axis[i] = static_cast<uint8_t>(a);
+  }
+  return record_error(RA_OK, "%s", "");
+}
+
+extern "C" int ra_qk_norm_axis_rope_fwd(const ra_problem* p, const ra_axis_rope* rope, const int32_t* positions,
+                                        int64_t pos_row_stride, float eps, const void* q, int64_t q_row_stride,
+                                        const void* k, int64_t k_row_stride, const void* q_weight,
+                                        const void* k_weight, void* q_out, void* k_out, void* stream) {
+  if (int e = ra_validate(p)) return e;
+  if (int e = check_axes(rope, positions, pos_row_stride, rows_of(p) > 0)) return e;
+  return norm_rope_fwd(p, &rope->rope, {rope, positions, pos_row_stride}, eps, q, q_row_stride, k, k_row_stride,
+                       q_weight, k_weight, q_out, k_out, stream);
+}
+
+extern "C" int ra_qk_norm_axis_rope_bwd(const ra_problem* p, const ra_axis_rope* rope, const int32_t* positions,
+                                        int64_t pos_row_stride, float eps, const void* dq_out, const void* dk_out,
+                                        const void* q, int64_t q_row_stride, const void* k, int64_t k_row_stride,
+                                        const void* q_weight, const void* k_weight, void* dq, void* dk,
+                                        float* dq_weight, float* dk_weight, void* workspace,
+                                        size_t workspace_bytes, void* stream) {
+  if (int e = ra_validate(p)) return e;
+  if (int e = check_axes(rope, positions, pos_row_stride, rows_of(p) > 0)) return e;
+  return norm_rope_bwd(p, &rope->rope, {rope, positions, pos_row_stride}, eps, dq_out, dk_out, q, q_row_stride, k,
+                       k_row_stride, q_weight, k_weight, dq, dk, dq_weight, dk_weight, workspace, workspace_bytes,
+                       stream);
+}
+
+extern "C" int ra_kv_cache_append_axes(const ra_paged_cache* c, const ra_axis_rope* rope, const int32_t* positions,
+                                       int64_t pos_row_stride, float eps, int n_tokens, int hq, const void* q,
+                                       int64_t q_row_stride, const void* k, int64_t k_row_stride, const void* v,
+                                       int64_t v_row_stride, const void* q_weight, const void* k_weight,
+                                       const int32_t* seq_lens, const int32_t* cu_new, void* q_out, void* stream) {
+  if (int e = check_cache(c)) return e;
+  if (int e = check_axes(rope, positions, pos_row_stride, n_tokens > 0 && c->n_seqs > 0)) return e;
+  return cache_append(c, &rope->rope, {rope, positions, pos_row_stride}, eps, n_tokens, hq, q, q_row_stride, k,
+                      k_row_stride, v, v_row_stride, q_weight, k_weight, seq_lens, cu_new, q_out, stream);
 }

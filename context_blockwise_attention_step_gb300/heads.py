@@ -13,7 +13,8 @@ from dataclasses import dataclass
 import torch
 
 from . import ops
-from ._abi import RA_BF16, RA_F32, RA_MAX_ROTARY_DIM, RaPagedCache, RaRope, RaSharedPrefix, check, lib
+from ._abi import (RA_BF16, RA_F32, RA_MAX_AXES, RA_MAX_ROTARY_DIM, RaAxisRope, RaPagedCache, RaRope,
+                   RaSharedPrefix, check, lib)
 from .ops import Problem
 
 
@@ -31,6 +32,13 @@ def make_rope(rotary_dim: int, base: float = 10000.0, inv_freq=None, interleaved
     """The rotation of the first ``rotary_dim`` elements of a head: pair i turns by position *
     ``inv_freq[i]`` radians (default base ** (-2i / rotary_dim)). Pairs are (i, i +
     rotary_dim/2), or (2i, 2i+1) if ``interleaved``."""
+    inv_freq = _inv_freq(rotary_dim, base, inv_freq)
+    raw = RaRope()
+    check(lib().ra_rope_init(ctypes.byref(raw), rotary_dim, 1 if interleaved else 0, inv_freq))
+    return Rope(raw)
+
+
+def _inv_freq(rotary_dim: int, base: float, inv_freq):
     if rotary_dim % 2 or not 2 <= rotary_dim <= RA_MAX_ROTARY_DIM:
         raise ValueError(f"rotary_dim must be even, 2..{RA_MAX_ROTARY_DIM}, got {rotary_dim}")
     if inv_freq is None:
@@ -40,10 +48,50 @@ def make_rope(rotary_dim: int, base: float = 10000.0, inv_freq=None, interleaved
     inv_freq = [float(x) for x in inv_freq]
     if len(inv_freq) != rotary_dim // 2:
         raise ValueError(f"inv_freq has {len(inv_freq)} entries, expected {rotary_dim // 2}")
-    raw = RaRope()
-    check(lib().ra_rope_init(ctypes.byref(raw), rotary_dim, 1 if interleaved else 0,
-                             (ctypes.c_double * len(inv_freq))(*inv_freq)))
-    return Rope(raw)
+    return (ctypes.c_double * len(inv_freq))(*inv_freq)
+
+
+@dataclass
+class AxisRope:
+    """A rotation of tokens with positions on several axes; ``raw`` is the C struct handed to the
+    library. The calls that take it take the tokens' ``positions`` too."""
+
+    raw: RaAxisRope
+
+    def __post_init__(self):
+        self.ptr = ctypes.byref(self.raw)
+        self.n_axes = self.raw.n_axes
+
+
+def make_axis_rope(rotary_dim: int, axis, base: float = 10000.0, inv_freq=None,
+                   interleaved: bool = False) -> AxisRope:
+    """``make_rope`` for tokens that have a position on each of several axes: pair i turns by the
+    position on axis ``axis[i]`` (rotary_dim/2 integers, see ``axis_sections``) * ``inv_freq[i]``
+    radians."""
+    inv_freq = _inv_freq(rotary_dim, base, inv_freq)
+    if isinstance(axis, torch.Tensor):
+        axis = axis.detach().cpu().tolist()
+    axis = [int(a) for a in axis]
+    if len(axis) != rotary_dim // 2:
+        raise ValueError(f"axis has {len(axis)} entries, expected {rotary_dim // 2}")
+    n_axes = max(axis) + 1
+    if min(axis) < 0 or n_axes > RA_MAX_AXES:
+        raise ValueError(f"axis must hold numbers from 0 to {RA_MAX_AXES - 1}, got {min(axis)}..{max(axis)}")
+    raw = RaAxisRope()
+    check(lib().ra_axis_rope_init(ctypes.byref(raw), rotary_dim, 1 if interleaved else 0, inv_freq, n_axes,
+                                  (ctypes.c_int32 * len(axis))(*axis)))
+    return AxisRope(raw)
+
+
+def axis_sections(sections, cyclic: bool = False) -> list:
+    """The axis of every pair for ``make_axis_rope``: the first sections[0] pairs on axis 0, the next
+    sections[1] on axis 1, and so on; or, ``cyclic``, the axes in turn (pair i on axis i % n as long
+    as that axis has pairs left by its section: i < n * sections[i % n], else on axis 0)."""
+    sections = [int(x) for x in sections]
+    n = len(sections)
+    if not cyclic:
+        return [a for a, s in enumerate(sections) for _ in range(s)]
+    return [i % n if i < n * sections[i % n] else 0 for i in range(sum(sections))]
 
 
 def _rows(t: torch.Tensor, name: str, dtype, rows: int, heads: int, dh: int, dev: int) -> int:
@@ -129,12 +177,26 @@ def _rope_ptr(rope: Rope | None):
     return None if rope is None else rope.ptr
 
 
-def qk_norm_rope_fwd(q, k, prob: Problem, q_weight=None, k_weight=None, rope: Rope | None = None,
-                     eps: float = 1e-6, q_out=None, k_out=None, stream=None):
+def _positions(rope, positions, rows: int, dev: int):
+    """Whether the rotation takes positions on several axes, and the elements from one row's to the next."""
+    if not isinstance(rope, AxisRope):
+        if positions is not None:
+            raise ValueError("positions go with a rotation on several axes (make_axis_rope)")
+        return False, 0
+    if positions is None:
+        raise ValueError("a rotation on several axes wants positions")
+    if positions.dim() not in (2, 3):
+        raise ValueError(f"positions must be [rows, {rope.n_axes}] or [B, S, {rope.n_axes}]")
+    return True, _rows(positions.unsqueeze(-2), "positions", torch.int32, rows, 1, rope.n_axes, dev)
+
+
+def qk_norm_rope_fwd(q, k, prob: Problem, q_weight=None, k_weight=None, rope: Rope | AxisRope | None = None,
+                     eps: float = 1e-6, q_out=None, k_out=None, stream=None, positions=None):
     """Per-head root-mean-square norm (weights [head_dim] in the token dtype, or None for no
     norm) and rotation by global position (or None for no rotation) of shard-major q and k ->
     (q_out, k_out). q and k may be views into a wider tensor (a fused projection); q_out may be
-    a contiguous q, k_out a contiguous k."""
+    a contiguous q, k_out a contiguous k. With an ``AxisRope`` the rotation goes by ``positions``
+    (int32, [rows, n_axes] or [B, S, n_axes], shard-major like q and k)."""
     r = prob.raw
     dh, dev = r.head_dim, q.get_device()
     qs = _rows(q, "q", prob.token_dtype, prob.rows, r.hq, dh, dev)
@@ -143,18 +205,22 @@ def qk_norm_rope_fwd(q, k, prob: Problem, q_weight=None, k_weight=None, rope: Ro
     made = []
     q_out = _made_like(q, made) if q_out is None else _plain(q_out, "q_out", prob.token_dtype, q.shape, dev)
     k_out = _made_like(k, made) if k_out is None else _plain(k_out, "k_out", prob.token_dtype, k.shape, dev)
-    _launch(dev, stream, made, lambda s: lib().ra_qk_norm_rope_fwd(
-        prob.ptr, _rope_ptr(rope), eps, _ptr(q), qs, _ptr(k), ks, _ptr(q_weight), _ptr(k_weight), _ptr(q_out),
-        _ptr(k_out), s))
+    axes, ps = _positions(rope, positions, prob.rows, dev)
+    rest = (eps, _ptr(q), qs, _ptr(k), ks, _ptr(q_weight), _ptr(k_weight), _ptr(q_out), _ptr(k_out))
+    if axes:
+        _launch(dev, stream, made, lambda s: lib().ra_qk_norm_axis_rope_fwd(prob.ptr, rope.ptr, _ptr(positions), ps,
+                                                                            *rest, s))
+    else:
+        _launch(dev, stream, made, lambda s: lib().ra_qk_norm_rope_fwd(prob.ptr, _rope_ptr(rope), *rest, s))
     return q_out, k_out
 
 
 def qk_norm_rope_bwd(dq_out, dk_out, q, k, prob: Problem, q_weight=None, k_weight=None,
-                     rope: Rope | None = None, eps: float = 1e-6, dq=None, dk=None, workspace=None,
-                     stream=None):
+                     rope: Rope | AxisRope | None = None, eps: float = 1e-6, dq=None, dk=None, workspace=None,
+                     stream=None, positions=None):
     """Gradients (dq, dk, dq_weight, dk_weight) of ``qk_norm_rope_fwd`` at its inputs q and k
     from those of its outputs. The weight gradients are float32 (None without weights), summed
-    in a fixed order. dq may be dq_out, dk may be dk_out."""
+    in a fixed order. dq may be dq_out, dk may be dk_out. ``positions`` as there."""
     r = prob.raw
     dh, dev = r.head_dim, dq_out.get_device()
     _plain(dq_out, "dq_out", prob.token_dtype, q.shape, dev)
@@ -171,9 +237,14 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, prob: Problem, q_weight=None, k_weigh
         made.append(dqw := torch.empty(dh, device=dq_out.device, dtype=torch.float32))
         made.append(dkw := torch.empty(dh, device=dq_out.device, dtype=torch.float32))
         workspace, size = _workspace(workspace, workspace is None and ops.workspace_bytes(prob, 3), q, made)
-    _launch(dev, stream, made, lambda s: lib().ra_qk_norm_rope_bwd(
-        prob.ptr, _rope_ptr(rope), eps, _ptr(dq_out), _ptr(dk_out), _ptr(q), qs, _ptr(k), ks, _ptr(q_weight),
-        _ptr(k_weight), _ptr(dq), _ptr(dk), _ptr(dqw), _ptr(dkw), _ptr(workspace), size, s))
+    axes, ps = _positions(rope, positions, prob.rows, dev)
+    rest = (eps, _ptr(dq_out), _ptr(dk_out), _ptr(q), qs, _ptr(k), ks, _ptr(q_weight), _ptr(k_weight), _ptr(dq),
+            _ptr(dk), _ptr(dqw), _ptr(dkw), _ptr(workspace), size)
+    if axes:
+        _launch(dev, stream, made, lambda s: lib().ra_qk_norm_axis_rope_bwd(prob.ptr, rope.ptr, _ptr(positions), ps,
+                                                                            *rest, s))
+    else:
+        _launch(dev, stream, made, lambda s: lib().ra_qk_norm_rope_bwd(prob.ptr, _rope_ptr(rope), *rest, s))
     return dq, dk, dqw, dkw
 
 
@@ -274,13 +345,15 @@ def make_cache(k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.
 
 
 def kv_cache_append(q, k, v, cache: PagedCache, seq_lens, cu_new=None, q_weight=None, k_weight=None,
-                    rope: Rope | None = None, eps: float = 1e-6, q_out=None, stream=None):
+                    rope: Rope | AxisRope | None = None, eps: float = 1e-6, q_out=None, stream=None,
+                    positions=None):
     """Put new tokens into the cache: norm and rotation of q and k as in ``qk_norm_rope_fwd``
     (None leaves them out), k and v to their pages -> q_out (None if q is None). seq_lens
     [n_seqs] int32 are the lengths with the new tokens. Without ``cu_new`` row b of q
     [n_seqs, hq, head_dim], k, v is the new token of sequence b (of length 0: idle, its row of
     q_out is 0); with it (int32 [n_seqs + 1], on the device) rows cu_new[b]:cu_new[b+1] are the
-    last tokens of sequence b, and rows behind the last are left as they are."""
+    last tokens of sequence b, and rows behind the last are left as they are. With an ``AxisRope``
+    the rotation goes by ``positions`` (int32, [rows, n_axes])."""
     dt, dh, dev, hkv = cache.dtype, cache.head_dim, cache.device_index, cache.hkv
     n = k.shape[0] if k.dim() == 3 else k.shape[0] * k.shape[1]
     ks = _rows(k, "k", dt, n, hkv, dh, dev)
@@ -296,9 +369,14 @@ def kv_cache_append(q, k, v, cache: PagedCache, seq_lens, cu_new=None, q_weight=
         q_out = _made_like(q, made) if q_out is None else _plain(q_out, "q_out", dt, q.shape, dev)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    _launch(dev, stream, made, lambda s: lib().ra_kv_cache_append(
-        cache.ptr, _rope_ptr(rope), eps, n, hq, _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(q_weight),
-        _ptr(k_weight), _ptr(seq_lens), _ptr(cu_new), _ptr(q_out), s))
+    axes, ps = _positions(rope, positions, n, dev)
+    rest = (eps, n, hq, _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(q_weight), _ptr(k_weight), _ptr(seq_lens),
+            _ptr(cu_new), _ptr(q_out))
+    if axes:
+        _launch(dev, stream, made, lambda s: lib().ra_kv_cache_append_axes(cache.ptr, rope.ptr, _ptr(positions), ps,
+                                                                           *rest, s))
+    else:
+        _launch(dev, stream, made, lambda s: lib().ra_kv_cache_append(cache.ptr, _rope_ptr(rope), *rest, s))
     return q_out
 
 

@@ -270,6 +270,40 @@ int ra_qk_norm_rope_bwd(const ra_problem* p, const ra_rope* rope, float eps, con
                         void* dq, void* dk, float* dq_weight, float* dk_weight,
                         void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- positions on several axes ---------------------------------------------------------- */
+
+#define RA_MAX_AXES 8
+
+/* A rotation of tokens that have a position on each of n_axes axes (time, height and width of a
+ * video's patches; text has the same on all): pair i turns by the token's position on axis axis[i]
+ * times inv_freq[i] radians. Filled in by ra_axis_rope_init. */
+typedef struct ra_axis_rope {
+  ra_rope rope;
+  int32_t n_axes;
+  uint8_t axis[RA_MAX_ROTARY_DIM / 2];
+} ra_axis_rope;
+
+/* Fills in `rope`: rotary_dim, interleaved and inv_freq as for ra_rope_init, axis rotary_dim/2 HOST
+ * integers in [0, n_axes), n_axes 1..RA_MAX_AXES. */
+int ra_axis_rope_init(ra_axis_rope* rope, int rotary_dim, int interleaved, const double* inv_freq,
+                      int n_axes, const int32_t* axis);
+
+/* ra_qk_norm_rope_fwd, ra_qk_norm_rope_bwd (below: ra_kv_cache_append) with such a rotation, the
+ * other arguments as there. positions (device, int32, any values) has n_axes elements for every row
+ * of q and k, pos_row_stride (>= n_axes) elements from one row to the next, in the rows' own order:
+ * shard-major like q and k (ra_shard_tokens with row_bytes 4 * n_axes brings them there). A row's
+ * place in its sequence plays no part. Angles are as good as with one axis. */
+int ra_qk_norm_axis_rope_fwd(const ra_problem* p, const ra_axis_rope* rope, const int32_t* positions,
+                             int64_t pos_row_stride, float eps, const void* q, int64_t q_row_stride,
+                             const void* k, int64_t k_row_stride, const void* q_weight,
+                             const void* k_weight, void* q_out, void* k_out, void* stream);
+int ra_qk_norm_axis_rope_bwd(const ra_problem* p, const ra_axis_rope* rope, const int32_t* positions,
+                             int64_t pos_row_stride, float eps, const void* dq_out, const void* dk_out,
+                             const void* q, int64_t q_row_stride, const void* k, int64_t k_row_stride,
+                             const void* q_weight, const void* k_weight, void* dq, void* dk,
+                             float* dq_weight, float* dk_weight, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
 /* ---- serving: a paged key-value cache and the attention of one new token -------------- */
 
 /* A cache of n_pages pages of page_size tokens; page p, place s, K/V head h starts at element
@@ -311,6 +345,15 @@ int ra_kv_cache_append(const ra_paged_cache* c, const ra_rope* rope, float eps, 
                        int64_t k_row_stride, const void* v, int64_t v_row_stride,
                        const void* q_weight, const void* k_weight, const int32_t* seq_lens,
                        const int32_t* cu_new, void* q_out, void* stream);
+
+/* The same with positions on several axes: positions and pos_row_stride as for
+ * ra_qk_norm_axis_rope_fwd, a row for each of the n_tokens rows. Where a token goes in the cache is
+ * its place in its sequence, as before. */
+int ra_kv_cache_append_axes(const ra_paged_cache* c, const ra_axis_rope* rope, const int32_t* positions,
+                            int64_t pos_row_stride, float eps, int n_tokens, int hq, const void* q,
+                            int64_t q_row_stride, const void* k, int64_t k_row_stride, const void* v,
+                            int64_t v_row_stride, const void* q_weight, const void* k_weight,
+                            const int32_t* seq_lens, const int32_t* cu_new, void* q_out, void* stream);
 
 /* Attention of the last token of every sequence: q and out [n_seqs, hq, head_dim] (contiguous,
  * cache dtype; hq % hkv == 0), lse [n_seqs, hq] (float32, natural log). The query sees the keys

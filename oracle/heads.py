@@ -13,6 +13,12 @@ def phases(pos, inv_freq):
     return np.exp(1j * np.asarray(pos, np.float64)[:, None] * np.asarray(inv_freq, np.float64)[None, :])
 
 
+def axis_phases(pos, axis, inv_freq):
+    """The same for positions on several axes, pos [tokens, axes]: pair i turns by axis[i]."""
+    angle = np.stack([np.asarray(pos, np.float64)[:, a] * f for a, f in zip(axis, inv_freq)], -1)
+    return np.exp(1j * angle)
+
+
 def turn(x, z, interleaved):
     """The first 2 * pairs elements of every head of x [tokens, heads, dh], read as complex
     numbers, multiplied by z [tokens, pairs]."""
