@@ -56,11 +56,13 @@ __device__ __forceinline__ Tokens tokens_of(const ExtArgs& A, int b) {
 }
 
 __global__ void __launch_bounds__(kPlanThreads) extend_plan(const __grid_constant__ ExtArgs A) {
-  __shared__ int64_t scan_units[32];
+  __shared__ int64_t scan_units[2][32];
   __shared__ int scan_blocks[32];
+  __shared__ int group_keys[kPlanThreads];  // of the first groups: the keys that are shared, 0: none
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const ExtShape& s = A.sh;
+  const ExtShape& s = A.sh[kExtMany];
   launch_dependents();
+  auto class_of = [&](int n) { return n * int64_t(A.group) <= A.few_rows ? kExtFew : kExtMany; };
   // groups, a warp each: whether the prefix lies before every new token, and whether sharing it pays
   for (int g = warp; g < A.n_groups; g += 32) {
     const int b0 = bounded(A.cu_groups[g], A.n_seqs), b1 = bounded(A.cu_groups[g + 1], A.n_seqs);
@@ -86,33 +88,35 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan(const __grid_constan
       ExtSeg e = {};
       e.shared = 1;
       e.prefix = -1;
-      e.k1 = tiles << s.shift;
       if (b0 < b1 && first < A.n_seqs && ok) {
         const Tokens a = tokens_of(A, b0), z = tokens_of(A, b1 - 1);
         const int n = z.t0 + z.n - a.t0;
         const int64_t together = ext_block_units(s, n);
         if (n > 0 && ext_worth_sharing(tiles, apart, together)) {
+          e.k1 = tiles << s.shift;
           e.t0 = a.t0;
           e.n = n;
           e.seq = first;
-          e.units = together * tiles;
+          e.cls = class_of(n);
+          e.units = ext_units_before(A.sh[e.cls], e, ext_blocks(A.sh[e.cls], n));
         }
       }
       A.segs[g] = e;
+      if (g < kPlanThreads) group_keys[g] = e.k1;
     }
   }
   __syncthreads();
-  // all segments in order, a run of them for each thread
+  // all segments in order, a thread each
   const int segs = A.n_groups + A.n_seqs, pairs = A.hkv * A.blocks_per_kv;
-  const int chunk = (segs + kPlanThreads - 1) / kPlanThreads;
-  const int i0 = min(segs, tid * chunk), i1 = min(segs, i0 + chunk);
-  int64_t units = 0;
-  int blocks = 0;
-  for (int i = i0; i < i1; ++i) {
+  int64_t done[2] = {0, 0};
+  int done_blocks = 0;
+  for (int i0 = 0; i0 < segs; i0 += kPlanThreads) {
+    const int i = i0 + tid;
     ExtSeg e = {};
+    int blocks = 0;
     if (i < A.n_groups) {
       e = A.segs[i];
-    } else {
+    } else if (i < segs) {
       const int b = i - A.n_groups;
       const Tokens t = tokens_of(A, b);
       if (t.bad) atomicOr(&g_status_extend, 1u);
@@ -122,62 +126,76 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan(const __grid_constan
       e.k1 = t.len;
       e.seq = b;
       e.prefix = -1;
+      e.cls = class_of(t.n);
       if (A.n_groups > 0 && t.live) {
         int lo = 0, hi = A.n_groups - 1;  // the last group that begins at b or before
         while (lo < hi) {
           const int mid = (lo + hi + 1) >> 1;
           if (A.cu_groups[mid] <= b) lo = mid; else hi = mid - 1;
         }
-        if (A.cu_groups[lo] <= b && b < A.cu_groups[lo + 1] && A.segs[lo].units > 0) {
-          e.prefix = lo;
-          e.k0 = A.segs[lo].k1;
+        if (A.cu_groups[lo] <= b && b < A.cu_groups[lo + 1]) {
+          e.k0 = lo < kPlanThreads ? group_keys[lo] : A.segs[lo].k1;
+          if (e.k0 > 0) e.prefix = lo;
         }
       }
-      if (t.live) e.units = ext_units_before(s, e, ext_blocks(s, t.n));
-      e.blocks0 = blocks;
-      blocks += ext_blocks(s, t.n);
+      blocks = ext_blocks(s, t.n);
+      if (t.live) e.units = ext_units_before(A.sh[e.cls], e, ext_blocks(A.sh[e.cls], t.n));
     }
-    e.unit0 = units;
-    units += e.units * pairs;
-    A.segs[i] = e;
-  }
-  int64_t x = units;
-  int y = blocks;
+    // units of each class and blocks before this segment
+    int64_t x[2];
+    int y = blocks;
+    x[0] = e.cls == kExtMany ? e.units * pairs : 0;
+    x[1] = e.cls == kExtFew ? e.units * pairs : 0;
+    const int64_t mine[2] = {x[0], x[1]};
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t a = __shfl_up_sync(0xffffffffu, x, o);
-    const int c = __shfl_up_sync(0xffffffffu, y, o);
-    if (lane >= o) {
-      x += a;
-      y += c;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t u = __shfl_up_sync(0xffffffffu, x[0], o), v = __shfl_up_sync(0xffffffffu, x[1], o);
+      const int z = __shfl_up_sync(0xffffffffu, y, o);
+      if (lane >= o) {
+        x[0] += u;
+        x[1] += v;
+        y += z;
+      }
     }
-  }
-  if (lane == 31) {
-    scan_units[warp] = x;
-    scan_blocks[warp] = y;
-  }
-  __syncthreads();
-  int64_t before = x - units, all = 0;
-  int blocks_before = y - blocks, all_blocks = 0;
-  for (int w = 0; w < 32; ++w) {
-    if (w < warp) {
-      before += scan_units[w];
-      blocks_before += scan_blocks[w];
+    __syncthreads();  // the round before has read the sums
+    if (lane == 31) {
+      scan_units[0][warp] = x[0];
+      scan_units[1][warp] = x[1];
+      scan_blocks[warp] = y;
     }
-    all += scan_units[w];
-    all_blocks += scan_blocks[w];
-  }
-  for (int i = i0; i < i1; ++i) {
-    A.segs[i].unit0 += before;
-    A.segs[i].blocks0 += blocks_before;
+    __syncthreads();
+    // each warp sums the warps before it, a lane a warp
+    int64_t p0 = scan_units[0][lane], p1 = scan_units[1][lane];
+    int pb = scan_blocks[lane];
+    int64_t before[2] = {lane < warp ? p0 : 0, lane < warp ? p1 : 0};
+    int before_blocks = lane < warp ? pb : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      p0 += __shfl_xor_sync(0xffffffffu, p0, o);
+      p1 += __shfl_xor_sync(0xffffffffu, p1, o);
+      pb += __shfl_xor_sync(0xffffffffu, pb, o);
+      before[0] += __shfl_xor_sync(0xffffffffu, before[0], o);
+      before[1] += __shfl_xor_sync(0xffffffffu, before[1], o);
+      before_blocks += __shfl_xor_sync(0xffffffffu, before_blocks, o);
+    }
+    if (i < segs) {
+      e.unit0[0] = done[0] + before[0] + x[0] - mine[0];
+      e.unit0[1] = done[1] + before[1] + x[1] - mine[1];
+      e.blocks0 = done_blocks + before_blocks + y - blocks;
+      A.segs[i] = e;
+    }
+    done[0] += p0;
+    done[1] += p1;
+    done_blocks += pb;
   }
   if (tid == 0) {
     ExtHead h;
-    h.units = all;
-    h.ctas = ext_ctas(all, A.most_ctas, s.wide);
+    for (int c = 0; c < 2; ++c) {
+      h.units[c] = done[c];
+      h.ctas[c] = ext_ctas(done[c], A.part[c].most_ctas, A.sh[c].wide);
+    }
     h.segs = segs;
-    h.own_blocks = all_blocks;
-    h.pad = 0;
+    h.own_blocks = done_blocks;
     *A.head = h;
   }
 }
@@ -199,6 +217,7 @@ template <int COLS>
 __global__ void __launch_bounds__(kSimtThreads, 2) extend_simt(const __grid_constant__ ExtArgs A, int vec) {
   extern __shared__ __align__(16) float sm[];
   __shared__ ExtItem sh_it;
+  __shared__ int64_t sh_at[kSimtKeys];  // of the tile's keys: where they are (-1: not read)
   const int dh = A.dh, pitch = simt_pitch(dh), d4 = (dh + 3) / 4;
   float* sq = sm;                                 // [64][pitch], times scale * log2(e)
   float* sk = sm + kSimtRows * pitch;             // [64][pitch], then the weights [64][68]
@@ -206,7 +225,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) extend_simt(const __grid_cons
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, x = tid & 15, y = tid >> 4;
   launch_dependents();
   wait_for_previous();
-  ExtCursor cur;
+  ExtCursor<kExtMany> cur;
   bool more = false;
   if (warp == 0) more = cur.begin(A, blockIdx.x);
   while (true) {
@@ -250,7 +269,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) extend_simt(const __grid_cons
       const int row = 4 * y + r, tok = row / A.hb;
       valid[r] = row < rows && row - tok * A.hb < it.heads;
       hi[r] = !valid[r] ? 0 : it.shared ? it.end : it.base + tok + 1;
-      lo[r] = A.sh.window > 0 ? max(0, hi[r] - A.sh.window) : 0;
+      lo[r] = A.sh[kExtMany].window > 0 ? max(0, hi[r] - A.sh[kExtMany].window) : 0;
       m[r] = -INFINITY;
       l[r] = 0.f;
 #pragma unroll
@@ -261,23 +280,32 @@ __global__ void __launch_bounds__(kSimtThreads, 2) extend_simt(const __grid_cons
     const bool idle = 8 * warp >= rows;  // a warp without rows helps with the copies only
     for (int j = it.j0; j < it.j0 + it.tiles; ++j) {
       const int k0 = ext_tile(it.walk, j) * kSimtKeys;
-      const int sinks = A.sh.window > 0 ? min(A.sh.sinks, it.end) : 0;
+      const int sinks = A.sh[kExtMany].window > 0 ? min(A.sh[kExtMany].sinks, it.end) : 0;
       // keys that some row sees; the rest of the tile is 0
-      __syncthreads();  // the tile before has been read
-      for (int r = warp; r < kSimtKeys; r += kSimtThreads / 32) {
-        const int key = k0 + r;
-        const bool on = key < sinks || (key >= it.low && key < it.end);
-        int64_t at = 0;
-        if (on) {
+      if (tid < kSimtKeys) {
+        const int key = k0 + tid;
+        int64_t at = -1;
+        if (key < sinks || (key >= it.low && key < it.end)) {
           const int page = key / A.page_size;
-          at = ext_page(A, it.seq, page, &g_status_extend) * A.page_stride + static_cast<int64_t>(key - page * A.page_size) * A.slot_stride +
-               it.hk * A.head_stride;
+          at = ext_page(A, it.seq, page, &g_status_extend) * A.page_stride +
+               static_cast<int64_t>(key - page * A.page_size) * A.slot_stride + it.hk * A.head_stride;
         }
-        for (int d = lane; d < d4; d += 32) {
-          copy_row4(static_cast<const float*>(A.k_pages) + at, sk + r * pitch, 4 * d, on, 1.f);
-          copy_row4(static_cast<const float*>(A.v_pages) + at, sv + r * pitch, 4 * d, on, 1.f);
+        sh_at[tid] = at;
+      }
+      __syncthreads();  // the tile before has been read
+      for (int i = tid; i < kSimtKeys * d4; i += kSimtThreads) {
+        const int r = i / d4, d = (i - r * d4) * 4;
+        const int64_t at = sh_at[r];
+        if (vec && at >= 0) {
+          cp_async16(smem_u32(sk + r * pitch + d), static_cast<const float*>(A.k_pages) + at + d);
+          cp_async16(smem_u32(sv + r * pitch + d), static_cast<const float*>(A.v_pages) + at + d);
+        } else {
+          copy_row4(static_cast<const float*>(A.k_pages) + (at < 0 ? 0 : at), sk + r * pitch, d, at >= 0, 1.f);
+          copy_row4(static_cast<const float*>(A.v_pages) + (at < 0 ? 0 : at), sv + r * pitch, d, at >= 0, 1.f);
         }
       }
+      cp_async_commit();
+      cp_async_wait<0>();
       __syncthreads();
       float s[4][4] = {};
       if (!idle) {
@@ -303,7 +331,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) extend_simt(const __grid_cons
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const int key = k0 + x + 16 * c;
-            if (!(key < hi[r] && (key >= lo[r] || key < A.sh.sinks))) s[r][c] = -INFINITY;
+            if (!(key < hi[r] && (key >= lo[r] || key < A.sh[kExtMany].sinks))) s[r][c] = -INFINITY;
             mx = fmaxf(mx, s[r][c]);
           }
 #pragma unroll
@@ -364,8 +392,8 @@ __global__ void __launch_bounds__(kSimtThreads, 2) extend_simt(const __grid_cons
       const int64_t at = static_cast<int64_t>(it.tok0 + tok) * A.hq + it.hk * A.group + it.g0 + row - tok * A.hb;
       const int64_t to = it.dest == kExtFinal ? at
                          : it.dest == kExtRows ? static_cast<int64_t>(it.slot) * A.n_tokens * A.hq + at
-                                               : static_cast<int64_t>(it.slot) * A.slot_rows + row;
-      float* out = (it.dest == kExtFinal ? static_cast<float*>(A.out) : it.dest == kExtRows ? A.row_o : A.part_o) + to * dh;
+                                               : static_cast<int64_t>(it.slot) * A.part[kExtMany].rows + row;
+      float* out = (it.dest == kExtFinal ? static_cast<float*>(A.out) : it.dest == kExtRows ? A.row_o : A.part[kExtMany].o) + to * dh;
       const float inv = it.dest != kExtFinal ? 1.f : l[r] > 0.f ? 1.f / l[r] : 0.f;
 #pragma unroll
       for (int c = 0; c < COLS; ++c)
@@ -374,7 +402,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) extend_simt(const __grid_cons
           if (64 * c + 4 * x + e < dh) out[64 * c + 4 * x + e] = o[r][c][e] * inv;
       if (x == 0) {
         if (it.dest == kExtFinal) A.lse[at] = l[r] > 0.f ? (m[r] + log2f(l[r])) * 0.69314718055994531f : -INFINITY;
-        else (it.dest == kExtRows ? A.row_ml : A.part_ml)[to] = make_float2(m[r], l[r]);
+        else (it.dest == kExtRows ? A.row_ml : A.part[kExtMany].ml)[to] = make_float2(m[r], l[r]);
       }
     }
     __syncthreads();
@@ -382,50 +410,54 @@ __global__ void __launch_bounds__(kSimtThreads, 2) extend_simt(const __grid_cons
 }
 
 // ---------------------------------------------------------------- the join
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 
-// The parts of a block: CTAs c0 .. c1 (c0 == c1: it is whole, in the row buffers).
+// The parts of a block: CTAs c0 .. c1 of its class (c0 == c1: it is whole, in the row buffers).
 struct Cut {
-  int c0, c1;
+  int c0, c1, cls;
   int tok0;  // token row of its first row
 };
 __device__ __forceinline__ Cut cut_of(const ExtArgs& A, const ExtSeg& g, int pair, int blk) {
-  const int64_t units = A.head->units;
-  const int ctas = A.head->ctas;
-  const int64_t base = g.unit0 + pair * g.units + ext_units_before(A.sh, g, blk);
+  const ExtShape& sh = A.sh[g.cls];
+  const int64_t units = A.head->units[g.cls];
+  const int ctas = A.head->ctas[g.cls];
+  const int64_t base = g.unit0[g.cls] + pair * g.units + ext_units_before(sh, g, blk);
   Cut c;
-  c.tok0 = g.t0 + blk * A.sh.bt;
+  c.cls = g.cls;
+  c.tok0 = g.t0 + blk * sh.bt;
   c.c0 = ext_cta_of(units, ctas, base);
-  c.c1 = ext_cta_of(units, ctas,
-                    base + static_cast<int64_t>(ext_walk(A.sh, g, blk).count - 1) * ext_weight(A.sh, g, blk));
+  c.c1 = ext_cta_of(units, ctas, base + static_cast<int64_t>(ext_walk(sh, g, blk).count - 1) * ext_weight(sh, g, blk));
   return c;
 }
 
-template <typename T> __device__ __forceinline__ void put(T* p, float v);
-template <> __device__ __forceinline__ void put<float>(float* p, float v) { *p = v; }
-template <> __device__ __forceinline__ void put<__nv_bfloat16>(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+template <typename T> __device__ __forceinline__ void put4(T* p, const float (&v)[4]);
+template <> __device__ __forceinline__ void put4<float>(float* p, const float (&v)[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+template <> __device__ __forceinline__ void put4<__nv_bfloat16>(__nv_bfloat16* p, const float (&v)[4]) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+}
 
 // A block for the rows of a block of one sequence's tokens (x: block and pair): nothing to do where one
-// CTA had it whole and no prefix is shared; 0 and -inf where nothing is seen. Threads take a row's
-// columns, E at a time, and where the block has few rows a share of the parts each; sums are taken in a
-// fixed order.
-template <typename T, int E>
+// CTA had it whole and no prefix is shared; 0 and -inf where nothing is seen. A warp takes a row, or
+// where there are few rows a share of its parts: a lane has a part's state, all lanes its sums, four
+// columns each (QUADS), or every 32nd. Sums are taken in a fixed order.
+template <typename T, bool QUADS>
 __global__ void __launch_bounds__(kJoinThreads) extend_join(const __grid_constant__ ExtArgs A) {
   __shared__ Cut sh_cut[3];  // own, the prefix's block of the first token, the next one
   __shared__ ExtSeg sh_seg;
-  __shared__ int sh_blk, sh_pair;
-  __shared__ float sums[kJoinThreads * E];
-  __shared__ float sh_l[kJoinThreads];
-  const int tid = threadIdx.x, dh = A.dh, bt = A.sh.bt;
+  __shared__ int sh_blk;
+  __shared__ float sums[kJoinWarps][128], sum_l[kJoinWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, dh = A.dh, bt = A.sh[kExtMany].bt;
+  const int pairs = A.hkv * A.blocks_per_kv, block = blockIdx.x / pairs, pair = blockIdx.x - block * pairs;
   wait_for_previous();
-  const int pairs = A.hkv * A.blocks_per_kv;
-  if (tid < 32) {
-    const int lane = tid, block = blockIdx.x / pairs, pair = blockIdx.x - block * pairs;
-    const bool some = block < A.head->own_blocks;
-    int blk = -1;
-    if (some) {
+  if (warp == 0) {
+    int lo = A.n_groups, n = A.n_seqs, blk = -1;
+    if (A.cu_new == nullptr) {
+      lo += block;  // a block is a sequence
+      blk = 0;
+    } else if (block < A.head->own_blocks) {
       // the last segment that begins at the block or before: 32 places at a time
-      int lo = A.n_groups, n = A.n_seqs;
       while (n > 1) {
         const int step = (n + 31) / 32, at = lo + lane * step;
         const bool before = at < lo + n && A.segs[at].blocks0 <= block;
@@ -433,107 +465,132 @@ __global__ void __launch_bounds__(kJoinThreads) extend_join(const __grid_constan
         n = min(step, lo + n - next);
         lo = next;
       }
+      blk = block - A.segs[lo].blocks0;
+    }
+    if (blk >= 0 && lane < 3) {
       const ExtSeg g = A.segs[lo];
-      blk = block - g.blocks0;
-      if (lane < 3) {
-        Cut c = {0, -1, 0};
-        if (lane == 0 && g.units > 0) c = cut_of(A, g, pair, blk);
-        if (lane > 0 && g.prefix >= 0) {
-          const ExtSeg p = A.segs[g.prefix];
-          const int i = (g.t0 + blk * bt - p.t0) / bt + lane - 1;
-          if (i < ext_blocks(A.sh, p.n)) c = cut_of(A, p, pair, i);
-        }
-        sh_cut[lane] = c;
+      Cut c = {0, -1, 0, 0};
+      if (lane == 0 && g.units > 0) c = cut_of(A, g, pair, g.cls == kExtFew ? 0 : blk);
+      if (lane > 0 && g.prefix >= 0) {
+        const ExtSeg p = A.segs[g.prefix];
+        const int i = (g.t0 + blk * bt - p.t0) / A.sh[p.cls].bt + lane - 1;
+        if (i < ext_blocks(A.sh[p.cls], p.n)) c = cut_of(A, p, pair, i);
       }
+      sh_cut[lane] = c;
       if (lane == 0) sh_seg = g;
     }
-    if (lane == 0) {
-      sh_blk = blk;
-      sh_pair = pair;
-    }
+    if (lane == 0) sh_blk = blk;
   }
   __syncthreads();
   if (sh_blk < 0) return;
   const ExtSeg& g = sh_seg;
   const bool empty = g.units == 0, joined = g.prefix >= 0;
-  if (!empty && !joined && sh_cut[0].c0 == sh_cut[0].c1) return;
-  const int hk = sh_pair / A.blocks_per_kv, g0 = sh_pair % A.blocks_per_kv * A.hb, heads = min(A.hb, A.group - g0);
-  const int tok0 = g.t0 + sh_blk * bt, ntok = min(bt, g.n - sh_blk * bt);
-  const int cols = dh / E, work = ntok * heads * cols;
-  int split = 1;  // shares of the parts
-  while (split < 8 && 2 * split * work <= kJoinThreads) split *= 2;
-  const int per = kJoinThreads / split, share = tid / per;
-  for (int w0 = 0; w0 < work; w0 += per) {
-    const int w = w0 + tid - share * per;
-    const bool on = w < work;
-    float x[E], l = 0.f, mx = -INFINITY;
-#pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = 0.f;
-    const int r = on ? w / cols : 0, d = on ? (w - r * cols) * E : 0, tok = r / heads, h = r - tok * heads;
+  const Cut own = sh_cut[0];
+  if (!empty && !joined && own.c0 == own.c1) return;
+  const int hk = pair / A.blocks_per_kv, g0 = pair % A.blocks_per_kv * A.hb, heads = min(A.hb, A.group - g0);
+  const int tok0 = g.t0 + sh_blk * bt, rows = min(bt, g.n - sh_blk * bt) * heads;
+  int split = 1;  // warps of a row
+  while (split < kJoinWarps && 2 * split * rows <= kJoinWarps) split *= 2;
+  const int share = warp % split, at_once = kJoinWarps / split;
+  for (int r = warp / split; r < (rows + at_once - 1) / at_once * at_once; r += at_once) {
+    const bool on = r < rows;
+    const int tok = on ? r / heads : 0, h = on ? r - tok * heads : 0;
     const int64_t at = static_cast<int64_t>(tok0 + tok) * A.hq + hk * A.group + g0 + h;
+    float x[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f, mx = -INFINITY;
     if (on && !empty) {
-      const Cut own = sh_cut[0];
-      Cut pre = {0, -1, 0};
-      if (joined) pre = tok0 + tok - sh_cut[1].tok0 < bt ? sh_cut[1] : sh_cut[2];
+      Cut pre = {0, -1, 0, 0};
+      if (joined) pre = tok0 + tok - sh_cut[1].tok0 < A.sh[sh_cut[1].cls].bt ? sh_cut[1] : sh_cut[2];
       const int n0 = own.c1 - own.c0 + 1, n = n0 + pre.c1 - pre.c0 + 1;
-      const int own_row = tok * A.hb + h, pre_row = (tok0 + tok - pre.tok0) * A.hb + h;
-      // part i: its state and its sums
+      // the row of part i: in the row buffers, or among its class's parts
       auto place = [&](int i, const float2** ml, const float** o) {
         const bool mine = i < n0;
         const Cut& c = mine ? own : pre;
         if (!mine) i -= n0;
         const bool whole = c.c0 == c.c1;
         const int64_t row = whole ? (mine ? static_cast<int64_t>(A.n_tokens) * A.hq : 0) + at
-                                  : (static_cast<int64_t>(c.c0 + i) * 2 + (i == 0 ? 1 : 0)) * A.slot_rows +
-                                        (mine ? own_row : pre_row);
-        *ml = (whole ? A.row_ml : A.part_ml) + row;
-        *o = (whole ? A.row_o : A.part_o) + row * dh + d;
+                                  : (static_cast<int64_t>(c.c0 + i) * 2 + (i == 0 ? 1 : 0)) * A.part[c.cls].rows +
+                                        (tok0 + tok - c.tok0) * A.hb + h;
+        *ml = (whole ? A.row_ml : A.part[c.cls].ml) + row;
+        *o = (whole ? A.row_o : A.part[c.cls].o) + row * dh;
       };
-      const float2* ml;
-      const float* o;
-#pragma unroll 4
-      for (int i = 0; i < n; ++i) {
-        place(i, &ml, &o);
-        mx = fmaxf(mx, ml->x);
-      }
-      const float ref = mx == -INFINITY ? 0.f : mx;
-#pragma unroll 4
-      for (int i = share; i < n; i += split) {
-        place(i, &ml, &o);
-        const float2 s = *ml;
-        const float f = exp2f(s.x - ref);
-        l += f * s.y;
-        if constexpr (E == 4) {
-          const float4 v = *reinterpret_cast<const float4*>(o);
-          x[0] += f * v.x;
-          x[1] += f * v.y;
-          x[2] += f * v.z;
-          x[3] += f * v.w;
-        } else {
-          x[0] += f * *o;
+      // 32 parts of this warp at a time: their states, then their sums
+      for (int i0 = share; i0 < n; i0 += 32 * split) {
+        const int i = i0 + lane * split;
+        const float2* ml = nullptr;
+        const float* o = nullptr;
+        float2 s = make_float2(-INFINITY, 0.f);
+        if (i < n) {
+          place(i, &ml, &o);
+          s = *ml;
+        }
+        float top = s.x;
+#pragma unroll
+        for (int w = 16; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+        top = fmaxf(top, mx);
+        const float ref = top == -INFINITY ? 0.f : top, alpha = exp2f(mx - ref), f = exp2f(s.x - ref);
+        mx = top;
+        float part_l = f * s.y;
+#pragma unroll
+        for (int w = 16; w > 0; w >>= 1) part_l += __shfl_xor_sync(0xffffffffu, part_l, w);
+        l = l * alpha + part_l;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] *= alpha;
+        const int count = min(32, (n - i0 + split - 1) / split);
+#pragma unroll 8
+        for (int k = 0; k < count; ++k) {
+          const float fk = __shfl_sync(0xffffffffu, f, k);
+          const float* ok = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(o), k));
+          if constexpr (QUADS) {
+            if (4 * lane < dh) {
+              const float4 v = *reinterpret_cast<const float4*>(ok + 4 * lane);
+              x[0] += fk * v.x;
+              x[1] += fk * v.y;
+              x[2] += fk * v.z;
+              x[3] += fk * v.w;
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (lane + 32 * e < dh) x[e] += fk * ok[lane + 32 * e];
+          }
         }
       }
     }
-    if (split > 1) {
-#pragma unroll
-      for (int e = 0; e < E; ++e) sums[tid * E + e] = x[e];
-      sh_l[tid] = l;
+    if (split > 1) {  // (one round of the loop: the rows' warps are all here)
+      if (lane == 0) sum_l[warp] = mx;
       __syncthreads();
-      if (share == 0) {
-        for (int k = 1; k < split; ++k) {
-          l += sh_l[tid + k * per];
+      float top = -INFINITY;
+      for (int k = 0; k < split; ++k) top = fmaxf(top, sum_l[warp - share + k]);
+      const float f = exp2f(mx - (top == -INFINITY ? 0.f : top));
+      mx = top;
+      __syncthreads();
+      if (lane == 0) sum_l[warp] = l * f;
 #pragma unroll
-          for (int e = 0; e < E; ++e) x[e] += sums[(tid + k * per) * E + e];
-        }
+      for (int e = 0; e < 4; ++e) sums[warp][QUADS ? (4 * lane + e) : (lane + 32 * e)] = x[e] * f;
+      __syncthreads();
+      if (share != 0) continue;
+      l = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = 0.f;
+      for (int k = 0; k < split; ++k) {
+        l += sum_l[warp + k];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] += sums[warp + k][QUADS ? (4 * lane + e) : (lane + 32 * e)];
       }
     }
-    if (on && share == 0) {
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+    if (!on) continue;
+    const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
-      for (int e = 0; e < E; ++e) put<T>(static_cast<T*>(A.out) + at * dh + d + e, x[e] * inv);
-      if (d == 0) A.lse[at] = l > 0.f ? (mx + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    for (int e = 0; e < 4; ++e) x[e] *= inv;
+    T* out = static_cast<T*>(A.out) + at * dh;
+    if constexpr (QUADS) {
+      if (4 * lane < dh) put4<T>(out + 4 * lane, x);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (lane + 32 * e < dh) out[lane + 32 * e] = x[e];
     }
-    if (split > 1) __syncthreads();
+    if (lane == 0) A.lse[at] = l > 0.f ? (mx + log2f(l)) * 0.69314718055994531f : -INFINITY;
   }
 }
 
@@ -561,7 +618,7 @@ cudaError_t launch_extend_simt(ExtArgs& A, cudaStream_t st) {
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   void* args[] = {&A, &vec};
-  return launch_after(kernel, A.most_ctas, kSimtThreads, smem, st, args);
+  return launch_after(kernel, A.part[kExtMany].most_ctas, kSimtThreads, smem, st, args);
 }
 
 // Blocks of query heads of one K/V head, as even as can be.
@@ -582,23 +639,40 @@ ExtShape shape_of(int dtype, int hb, int window, int sinks) {
   return s;
 }
 
+// Rows of a K/V head up to which a segment goes to the kernel for few rows, bf16: 16, or 8 where the
+// sequences have no more than that on average and the kernel for 8 rows, which is faster, will do.
+int few_rows_of(const ra_paged_cache* c, bool decode, int n_tokens, int hq) {
+  const int group = hq / c->hkv;
+  if (c->dtype != RA_BF16 || group > 16 || c->n_seqs == 0) return 0;
+  const int64_t rows = (decode ? 1 : (static_cast<int64_t>(n_tokens) + c->n_seqs - 1) / c->n_seqs) * group;
+  return rows <= 8 ? 8 : 16;
+}
+
 // The workspace's regions, one after the other.
 struct Regions {
-  size_t segs, part_o, part_ml, row_o, row_ml, total;
+  size_t segs, part_o[2], part_ml[2], row_o, row_ml, total;
+  int rows[2], ctas[2];  // of the parts of each class
 };
 Regions regions_of(const ra_paged_cache* c, int n_groups, int n_tokens, int hq) {
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   int hb, blocks;
   head_blocks(hq / c->hkv, c->dtype == RA_BF16 ? 128 : kSimtRows, &hb, &blocks);
   const ExtShape s = shape_of(c->dtype, hb, 0, 0);
-  const size_t ctas = (c->dtype == RA_BF16 ? 1 : 2) * kExtSms;
-  const size_t slot_rows = static_cast<size_t>(n_tokens < s.bt ? n_tokens : s.bt) * hb, parts = ctas * 2 * slot_rows;
-  const size_t rows = n_groups > 0 ? size_t(2) * n_tokens * hq : 0;
   Regions r;
+  r.ctas[kExtMany] = (c->dtype == RA_BF16 ? 1 : 2) * kExtSms;
+  r.rows[kExtMany] = (n_tokens < s.bt ? n_tokens : s.bt) * hb;
+  r.ctas[kExtFew] = c->dtype == RA_BF16 ? extend_few_ctas(c->head_dim) : 0;
+  r.rows[kExtFew] = r.ctas[kExtFew] > 0 ? 16 : 0;
+  const size_t rows = n_groups > 0 ? size_t(2) * n_tokens * hq : 0;
   r.segs = 256;
-  r.part_o = r.segs + up((static_cast<size_t>(n_groups) + c->n_seqs) * sizeof(ExtSeg));
-  r.part_ml = r.part_o + up(parts * c->head_dim * 4);
-  r.row_o = r.part_ml + up(parts * 8);
+  size_t at = r.segs + up((static_cast<size_t>(n_groups) + c->n_seqs) * sizeof(ExtSeg));
+  for (int k = 0; k < 2; ++k) {
+    const size_t parts = static_cast<size_t>(r.ctas[k]) * 2 * r.rows[k];
+    r.part_o[k] = at;
+    r.part_ml[k] = r.part_o[k] + up(parts * c->head_dim * 4);
+    at = r.part_ml[k] + up(parts * 8);
+  }
+  r.row_o = at;
   r.row_ml = r.row_o + up(rows * c->head_dim * 4);
   r.total = r.row_ml + up(rows * 8);
   return r;
@@ -619,13 +693,15 @@ int check_extend(const ra_paged_cache* c, int n_groups, int n_tokens, int hq) {
 
 cudaError_t extend_status(unsigned int value[2], bool reset) {
   unsigned int index = 0;
+  unsigned int few = 0;
   cudaError_t e = extend_tc_status(value, reset);
+  if (e == cudaSuccess) e = extend_few_status(&few, reset);
   if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&index, g_status_extend, sizeof index);
   if (e == cudaSuccess && reset) {
     const unsigned int zero = 0;
     e = cudaMemcpyToSymbol(g_status_extend, &zero, sizeof zero);
   }
-  value[1] |= index;
+  value[1] |= index | few;
   return e;
 }
 
@@ -698,16 +774,18 @@ extern "C" int ra_paged_attn_extend(const ra_paged_cache* c, const ra_shared_pre
   A.group = hq / c->hkv;
   A.dh = c->head_dim;
   head_blocks(A.group, c->dtype == RA_BF16 ? 128 : kSimtRows, &A.hb, &A.blocks_per_kv);
-  A.sh = shape_of(c->dtype, A.hb, window, window > 0 ? sinks : 0);
-  A.slot_rows = (n_tokens < A.sh.bt ? n_tokens : A.sh.bt) * A.hb;
-  A.most_ctas = (c->dtype == RA_BF16 ? 1 : 2) * (n_sm < kExtSms ? n_sm : kExtSms);
+  A.sh[kExtMany] = shape_of(c->dtype, A.hb, window, window > 0 ? sinks : 0);
+  A.few_rows = few_rows_of(c, cu_new == nullptr, n_tokens, hq);
+  A.sh[kExtFew] = {16, 16, 1, 6, window, window > 0 ? sinks : 0};  // one block, tiles of 64 keys
+  const int sms = n_sm < kExtSms ? n_sm : kExtSms;
   A.scale_log2 = (scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(c->head_dim))) * 1.4426950408889634f;
   A.timeout_ns = kDefaultTimeoutNs;
   char* ws = static_cast<char*>(workspace);
   A.head = reinterpret_cast<ExtHead*>(ws);
   A.segs = reinterpret_cast<ExtSeg*>(ws + at.segs);
-  A.part_o = reinterpret_cast<float*>(ws + at.part_o);
-  A.part_ml = reinterpret_cast<float2*>(ws + at.part_ml);
+  for (int k = 0; k < 2; ++k)
+    A.part[k] = {reinterpret_cast<float*>(ws + at.part_o[k]), reinterpret_cast<float2*>(ws + at.part_ml[k]),
+                 k == kExtFew ? A.few_rows : at.rows[k], at.ctas[k] / kExtSms * sms};
   A.row_o = reinterpret_cast<float*>(ws + at.row_o);
   A.row_ml = reinterpret_cast<float2*>(ws + at.row_ml);
   A.out = out;
@@ -718,15 +796,21 @@ extern "C" int ra_paged_attn_extend(const ra_paged_cache* c, const ra_shared_pre
     return record_error(RA_ERR_UNSUPPORTED, "the pages' strides do not fit a tensor map");
   extend_plan<<<1, kPlanThreads, 0, st>>>(A);
   e = cudaGetLastError();
-  if (e == cudaSuccess) e = c->dtype == RA_BF16 ? launch_extend_tc(A, maps, st) : launch_extend_simt(A, st);
+  // the kernels that can have work: one new token of every sequence and nothing shared is few rows
+  // unless a K/V head has many query heads
+  const bool many = A.few_rows == 0 || (static_cast<int64_t>(n_tokens) * A.group > A.few_rows &&
+                                        (cu_new != nullptr || n_groups > 0 || A.group > A.few_rows));
+  if (e == cudaSuccess && many) e = c->dtype == RA_BF16 ? launch_extend_tc(A, maps, st) : launch_extend_simt(A, st);
+  if (e == cudaSuccess && A.few_rows > 0) e = launch_extend_few(A, st);
   if (e == cudaSuccess) {
     // at most one block of a sequence has fewer tokens than the others
-    int64_t blocks = static_cast<int64_t>(n_tokens / A.sh.bt) + c->n_seqs;
+    int64_t blocks = static_cast<int64_t>(n_tokens / A.sh[kExtMany].bt) + c->n_seqs;
     if (blocks > n_tokens) blocks = n_tokens;
     void* args[] = {&A};
-    const void* kernel = c->dtype == RA_BF16 ? reinterpret_cast<const void*>(extend_join<__nv_bfloat16, 4>)
-                         : A.dh % 4 == 0     ? reinterpret_cast<const void*>(extend_join<float, 4>)
-                                             : reinterpret_cast<const void*>(extend_join<float, 1>);
+    const void* kernel = c->dtype == RA_BF16 ? reinterpret_cast<const void*>(extend_join<__nv_bfloat16, true>)
+                         : A.dh % 4 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0
+                             ? reinterpret_cast<const void*>(extend_join<float, true>)
+                             : reinterpret_cast<const void*>(extend_join<float, false>);
     e = launch_after(kernel, static_cast<unsigned>(blocks * A.hkv * A.blocks_per_kv), kJoinThreads, 0, st, args);
   }
   if (e != cudaSuccess) return record_error(RA_ERR_CUDA, "extend attention launch: %s", cudaGetErrorString(e));

@@ -11,12 +11,17 @@
 namespace ra {
 
 constexpr int kExtSms = 152;
-constexpr int kExtMaxCtas = 2 * kExtSms;
 
 // What the planning kernel finds out, at the beginning of the workspace; the segments follow.
 struct ExtHead {
-  int64_t units;
-  int32_t ctas, segs, own_blocks, pad;
+  int64_t units[2];
+  int32_t ctas[2], segs, own_blocks;
+};
+// The parts of the blocks of a class that are cut between CTAs: [CTA][2][rows], and [dh].
+struct ExtParts {
+  float* o;    // sums, not divided by l
+  float2* ml;  // running max (log2), denominator
+  int32_t rows, most_ctas;
 };
 
 struct ExtArgs {
@@ -32,17 +37,15 @@ struct ExtArgs {
   int32_t n_seqs, n_groups, n_tokens, max_pages, page_size, n_pages;
   int32_t hq, hkv, group, dh;
   int32_t hb, blocks_per_kv;   // query heads of a block (the last one may have fewer), blocks of a K/V head
-  int32_t slot_rows;           // rows of a part: those of the largest block
-  int32_t most_ctas;
   int32_t box_rows, ord[3];    // tensor-core kernel: keys of a copy; places of head, slot, page in the map
-  ExtShape sh;
+  ExtShape sh[2];              // of each class
+  int32_t few_rows;            // most rows a K/V head of a segment of few rows; 0: that class is not used
+  ExtParts part[2];
   float scale_log2;
   uint64_t timeout_ns;
   ExtHead* head;
   ExtSeg* segs;
-  float* part_o;               // [CTA][2][slot_rows][dh]: sums of a cut block, not divided by l
-  float2* part_ml;             // [CTA][2][slot_rows]: running max (log2), denominator
-  float* row_o;                // the same of whole blocks that are joined: [2][n_tokens][hq][dh]
+  float* row_o;                // results like a part's, of whole blocks that are joined: [2][n_tokens][hq][dh]
   float2* row_ml;
   void* out;
   float* lse;
@@ -63,14 +66,15 @@ struct ExtItem {
 };
 
 // The walk of one warp over the pieces of a CTA's share (every lane holds the same state).
+template <int CLS>
 struct ExtCursor {
   int64_t u0, u1, base;
   ExtSeg g;
   int cta, segs, seg, pair, blk, blocks;
 
   __device__ __forceinline__ bool begin(const ExtArgs& A, int which) {
-    const int64_t units = A.head->units;
-    const int ctas = A.head->ctas;
+    const int64_t units = A.head->units[CLS];
+    const int ctas = A.head->ctas[CLS];
     segs = A.head->segs;
     cta = which;
     if (which >= ctas) return false;
@@ -81,7 +85,7 @@ struct ExtCursor {
     int lo = 0, n = segs;
     while (n > 1) {
       const int step = (n + 31) / 32, at = lo + lane * step;
-      const bool before = at < lo + n && A.segs[at].unit0 <= u0;
+      const bool before = at < lo + n && A.segs[at].unit0[CLS] <= u0;
       const int k = __popc(__ballot_sync(0xffffffffu, before)) - 1;
       const int next = lo + k * step;
       n = min(step, lo + n - next);
@@ -89,34 +93,35 @@ struct ExtCursor {
     }
     seg = lo;
     g = A.segs[seg];
-    int64_t r = u0 - g.unit0;
+    int64_t r = u0 - g.unit0[CLS];
     pair = static_cast<int>(r / g.units);
     r -= pair * g.units;
-    blocks = ext_blocks(A.sh, g.n);
-    blk = ext_block_of(A.sh, g, r);
-    base = g.unit0 + pair * g.units + ext_units_before(A.sh, g, blk);
+    blocks = ext_blocks(A.sh[CLS], g.n);
+    blk = ext_block_of(A.sh[CLS], g, r);
+    base = g.unit0[CLS] + pair * g.units + ext_units_before(A.sh[CLS], g, blk);
     return true;
   }
 
   __device__ __forceinline__ bool next(const ExtArgs& A, ExtItem& it) {
+    const ExtShape& sh = A.sh[CLS];
     while (base < u1) {
-      const ExtWalk w = ext_walk(A.sh, g, blk);
-      const int weight = ext_weight(A.sh, g, blk);
+      const ExtWalk w = ext_walk(sh, g, blk);
+      const int weight = ext_weight(sh, g, blk);
       const int j0 = ext_tile_from(base, weight, w.count, u0), j1 = ext_tile_from(base, weight, w.count, u1);
       if (j0 < j1) {
-        const int a = blk * A.sh.bt, hblk = pair % A.blocks_per_kv;
+        const int a = blk * sh.bt, hblk = pair % A.blocks_per_kv;
         it.walk = w;
         it.j0 = j0;
         it.tiles = j1 - j0;
         it.tok0 = g.t0 + a;
-        it.ntok = min(A.sh.bt, g.n - a);
-        it.two = it.ntok > A.sh.half;
+        it.ntok = min(sh.bt, g.n - a);
+        it.two = it.ntok > sh.half;
         it.hk = pair / A.blocks_per_kv;
         it.g0 = hblk * A.hb;
         it.heads = min(A.hb, A.group - it.g0);
         it.shared = g.shared;
         it.base = g.base + a;
-        it.low = g.shared ? 0 : static_cast<int>(ext_low(A.sh, g, blk));
+        it.low = g.shared ? 0 : static_cast<int>(ext_low(sh, g, blk));
         it.end = g.shared ? g.k1 : it.base + it.ntok;
         it.seq = g.seq;
         const bool whole = j0 == 0 && j1 == w.count, joined = g.shared || g.prefix >= 0;
@@ -134,8 +139,8 @@ struct ExtCursor {
               break;
             }
             g = A.segs[seg];
-          } while (g.units == 0);
-          blocks = ext_blocks(A.sh, g.n);
+          } while (g.units == 0 || g.cls != CLS);
+          blocks = ext_blocks(sh, g.n);
         }
       }
       if (j0 < j1) return true;
@@ -159,5 +164,10 @@ struct ExtMaps {
 cudaError_t make_extend_maps(ExtMaps* maps, const ra_paged_cache* c, ExtArgs* A);
 cudaError_t launch_extend_tc(const ExtArgs& A, const ExtMaps& maps, cudaStream_t st);
 cudaError_t extend_tc_status(unsigned int value[2], bool reset);  // as extend_status, of that kernel alone
+
+// The kernel of the segments of few rows, bf16.
+int extend_few_ctas(int head_dim);  // most CTAs
+cudaError_t launch_extend_few(const ExtArgs& A, cudaStream_t st);
+cudaError_t extend_few_status(unsigned int* value, bool reset);
 
 }  // namespace ra

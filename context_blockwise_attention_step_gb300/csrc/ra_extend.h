@@ -13,12 +13,17 @@
 // order segment, pair (K/V head and block of its query heads), block, tile. A tile belongs to the
 // CTA that its first unit falls to; with shares of `wide` units at least, each CTA between the first
 // and the last of a block has a tile of it.
+//
+// Segments are of two classes, each with a kernel, a shape and shares of its own: those of few rows
+// (at most 16 a K/V head, all in one block), and the others.
 #pragma once
 #include <stdint.h>
 
 #include "ra_layout.h"
 
 namespace ra {
+
+enum : int { kExtMany = 0, kExtFew = 1 };
 
 struct ExtShape {
   int32_t bt, half;  // tokens of a block, and of one that costs one unit a tile
@@ -28,8 +33,8 @@ struct ExtShape {
 };
 
 struct ExtSeg {
-  int64_t unit0;   // units before this segment
-  int64_t units;   // units of one pair; 0: nothing to walk
+  int64_t unit0[2];  // units of each class before this segment
+  int64_t units;     // units of one pair, of the segment's class; 0: nothing to walk
   int32_t t0, n;   // first token row, tokens
   int32_t base;    // own: position of token t0
   int32_t k0, k1;  // own: first key, keys; prefix: 0, keys
@@ -37,7 +42,7 @@ struct ExtSeg {
   int32_t blocks0; // own blocks before this segment
   int32_t prefix;  // own: the prefix segment that has the keys before k0, or -1
   int32_t shared;  // 1: a prefix segment
-  int32_t pad;
+  int32_t cls;
 };
 
 // Tiles of a block: walk index j is tile j for j < ns (first tokens before the window), else

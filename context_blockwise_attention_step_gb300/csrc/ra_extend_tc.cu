@@ -22,8 +22,8 @@
 // Keys that no row of a block sees are not read, and their values in a tile are made 0 before the
 // product (what lies in a page behind a sequence's end may be NaN); their scores are masked.
 //
-// Warp roles (640 threads): 0 = TMA producer (a lane a box), 1 = TMEM and MMA, 2 = the walk over the
-// pieces, four ahead of the others, 4-11 and 12-19 = the softmax teams.
+// Warp roles (640 threads): 0 = TMA of Q and K (a lane a box), 3 = TMA of V, 1 = TMEM and MMA, 2 = the
+// walk over the pieces, four ahead of the others, 4-11 and 12-19 = the softmax teams.
 #include "ra_extend.cuh"
 #include "ra_window.cuh"
 
@@ -75,7 +75,7 @@ struct TileKeys {
 __device__ __forceinline__ TileKeys tile_keys(const ExtArgs& A, const ExtItem& it, int j) {
   const int tile = ext_tile(it.walk, j), k0 = tile * 128;
   TileKeys t;
-  t.sinks = A.sh.window > 0 && tile == 0 ? min(A.sh.sinks, it.end) : 0;
+  t.sinks = A.sh[kExtMany].window > 0 && tile == 0 ? min(A.sh[kExtMany].sinks, it.end) : 0;
   t.from = j < it.walk.ns ? 128 : max(0, it.low - k0);
   t.to = j < it.walk.ns ? 128 : min(128, it.end - k0);
   if (j < it.walk.ns) t.to = t.from = t.sinks;  // sinks only
@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sh.drain, 1);
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&sh.item_full[i], 1);
-      mbar_init(&sh.item_empty[i], 2 + 512);  // producer, MMA thread, softmax threads
+      mbar_init(&sh.item_empty[i], 3 + 512);  // producers, MMA thread, softmax threads
     }
     sh.abort_flag = 0;
     fence_mbar_init();
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 2) {
     // ------------------------------------------------------------------ the walk
-    ExtCursor cur;
+    ExtCursor<kExtMany> cur;
     bool more = cur.begin(A, blockIdx.x);
     for (int kq = 0;; ++kq) {
       const int slot = kq % kItems;
@@ -233,8 +233,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!more) break;
     }
-  } else if (warp == 0) {
-    // ------------------------------------------------------------------ TMA producer
+  } else if (warp == 0 || warp == 3) {
+    // ------------------------------------------------------------------ TMA producers: Q and K, V
     int kv = 0, qt = 0;  // key tiles and query tiles so far
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, tmo, status));
@@ -247,25 +247,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.item_empty[slot]);
       if (it.tiles == 0) break;
-      for (int t = 0; t < (it.two ? 2 : 1) && ok; ++t, ++qt) {
+      for (int t = 0; warp == 0 && t < (it.two ? 2 : 1) && ok; ++t, ++qt) {
         const int qs = qt & 1;
         if (!(ok = wait(&sh.q_empty[qs], ((qt >> 1) & 1) ^ 1))) break;
         if (lane == 0) {
-          mbar_expect_tx(&sh.q_full[qs], A.sh.half * A.hb * DH * 2);
+          mbar_expect_tx(&sh.q_full[qs], A.sh[kExtMany].half * A.hb * DH * 2);
           for (int d = 0; d < C::kSub; ++d)
             tma_load_4d(smem + qs * C::kTileBytes + d * kSubBytes, &tmQ, &sh.q_full[qs], d * 64, it.g0, it.hk,
-                        it.tok0 + t * A.sh.half);
+                        it.tok0 + t * A.sh[kExtMany].half);
         }
       }
       if (!ok) break;
+      uint64_t* full = warp == 0 ? sh.k_full : sh.v_full;
+      uint64_t* empty = warp == 0 ? sh.k_empty : sh.v_empty;
+      const CUtensorMap* map = warp == 0 ? &tmK : &tmV;
+      uint8_t* ring = smem + (warp == 0 ? C::kOffK : C::kOffV);
       for (int j = it.j0; j < it.j0 + it.tiles; ++j, ++kv) {
         const Boxes b = boxes_of(A, it, j, lane);
         const int st = kv % C::kStages;
-        const uint32_t ph = ((kv / C::kStages) & 1) ^ 1;
-        if (!(ok = wait(&sh.k_empty[st], ph))) break;
-        load_boxes<DH>(A, b, &tmK, &sh.k_full[st], smem + C::kOffK + st * C::kTileBytes, it.hk, lane);
-        if (!(ok = wait(&sh.v_empty[st], ph))) break;
-        load_boxes<DH>(A, b, &tmV, &sh.v_full[st], smem + C::kOffV + st * C::kTileBytes, it.hk, lane);
+        if (!(ok = wait(&empty[st], ((kv / C::kStages) & 1) ^ 1))) break;
+        load_boxes<DH>(A, b, map, &full[st], ring + st * C::kTileBytes, it.hk, lane);
       }
     }
   } else if (warp == 1) {
@@ -363,13 +364,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (N == 0) break;
       const bool two = it.two != 0;
       const int count0 = two ? N : (N + 1) / 2, count1 = two ? N : N / 2, mine = t ? count1 : count0;
-      const int tk = tok + (two && t ? A.sh.half : 0);  // token of the block
-      const bool valid = tok < A.sh.half && tk < it.ntok && head < it.heads;
+      const int tk = tok + (two && t ? A.sh[kExtMany].half : 0);  // token of the block
+      const bool valid = tok < A.sh[kExtMany].half && tk < it.ntok && head < it.heads;
       const bool idle = !__any_sync(0xffffffffu, valid);
       // keys lo .. hi - 1, and the first `sinks`. What a row that is none is given does not matter (no
       // row of a product depends on another): it sees everything, so that it asks for no mask.
       const int hi = !valid ? 0x7fffffff : it.shared ? it.end : it.base + tk + 1;
-      const int lo = valid && A.sh.window > 0 ? max(0, hi - A.sh.window) : 0;
+      const int lo = valid && A.sh[kExtMany].window > 0 ? max(0, hi - A.sh[kExtMany].window) : 0;
       float m = -INFINITY, l = 0.f;
       bool ok = true;
       for (int k = 0; k < mine; ++k) {
@@ -384,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++xn;
         } else {
           const int cnt = min(max(hi - k0, 0), 128);
-          const int lo_t = lo - k0, sk_t = A.sh.window > 0 && k0 == 0 ? A.sh.sinks : 0;
+          const int lo_t = lo - k0, sk_t = A.sh[kExtMany].window > 0 && k0 == 0 ? A.sh[kExtMany].sinks : 0;
           const bool full = __all_sync(0xffffffffu, cnt == 128 && lo_t <= sk_t);  // no mask needed
           uint32_t vis[2] = {0xffffffffu, 0xffffffffu};
           if (!full) {
@@ -541,13 +542,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float inv = dest != kExtFinal ? 1.f : L > 0.f ? 1.f / L : 0.f;
       const int64_t to = dest == kExtFinal ? at
                          : dest == kExtRows ? static_cast<int64_t>(it.slot) * A.n_tokens * A.hq + at
-                                            : static_cast<int64_t>(it.slot) * A.slot_rows + tk * A.hb + head;
-      float* fo = (dest == kExtRows ? A.row_o : A.part_o) + to * DH;
+                                            : static_cast<int64_t>(it.slot) * A.part[kExtMany].rows + tk * A.hb + head;
+      float* fo = (dest == kExtRows ? A.row_o : A.part[kExtMany].o) + to * DH;
       __nv_bfloat16* bo = static_cast<__nv_bfloat16*>(A.out) + to * DH;
       const bool lead = two ? hf == 0 : hf == 0 && t == 0;
       if (valid && lead) {
         if (dest == kExtFinal) A.lse[at] = L > 0.f ? (M + lg2(L)) * 0.69314718055994531f : -INFINITY;
-        else (dest == kExtRows ? A.row_ml : A.part_ml)[to] = make_float2(M, L);
+        else (dest == kExtRows ? A.row_ml : A.part[kExtMany].ml)[to] = make_float2(M, L);
       }
       if (two) {
 #pragma unroll
@@ -612,7 +613,7 @@ cudaError_t launch(const ExtArgs& A, const ExtMaps& maps, cudaStream_t st) {
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(A.most_ctas);
+  cfg.gridDim = dim3(A.part[kExtMany].most_ctas);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kSmemBytes;
   cfg.stream = st;
@@ -632,7 +633,7 @@ cudaError_t make_extend_maps(ExtMaps* maps, const ra_paged_cache* c, ExtArgs* A)
     const uint64_t dims[4] = {dh, static_cast<uint64_t>(A->group), static_cast<uint64_t>(A->hkv),
                               static_cast<uint64_t>(A->n_tokens)};
     const uint64_t strides[3] = {row, row * A->group, row * A->hq};
-    const uint32_t box[4] = {64, static_cast<uint32_t>(A->hb), 1, static_cast<uint32_t>(A->sh.half)};
+    const uint32_t box[4] = {64, static_cast<uint32_t>(A->hb), 1, static_cast<uint32_t>(A->sh[kExtMany].half)};
     const cudaError_t e = make_tmap_bf16(&maps->q, A->q, 4, dims, strides, box);
     if (e != cudaSuccess) return e;
   }
