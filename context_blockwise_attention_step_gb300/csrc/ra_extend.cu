@@ -58,6 +58,7 @@ __device__ __forceinline__ Tokens tokens_of(const ExtArgs& A, int b) {
 __global__ void __launch_bounds__(kPlanThreads) extend_plan(const __grid_constant__ ExtArgs A) {
   __shared__ int64_t scan_units[2][32];
   __shared__ int scan_blocks[32];
+  __shared__ int64_t first_units[2][kPlanThreads];  // of the first segments
   __shared__ int group_keys[kPlanThreads];  // of the first groups: the keys that are shared, 0: none
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const ExtShape& s = A.sh[kExtMany];
@@ -184,19 +185,50 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan(const __grid_constan
       e.blocks0 = done_blocks + before_blocks + y - blocks;
       A.segs[i] = e;
     }
+    if (i0 == 0) {
+      first_units[0][tid] = e.unit0[0];
+      first_units[1][tid] = e.unit0[1];
+    }
     done[0] += p0;
     done[1] += p1;
     done_blocks += pb;
   }
+  int ctas[2];
+  for (int c = 0; c < 2; ++c) ctas[c] = ext_ctas(done[c], A.part[c].most_ctas, A.sh[c].wide);
   if (tid == 0) {
     ExtHead h;
     for (int c = 0; c < 2; ++c) {
       h.units[c] = done[c];
-      h.ctas[c] = ext_ctas(done[c], A.part[c].most_ctas, A.sh[c].wide);
+      h.ctas[c] = ctas[c];
     }
     h.segs = segs;
     h.own_blocks = done_blocks;
     *A.head = h;
+  }
+  __syncthreads();
+  // where each CTA begins
+  for (int k = tid; k < ctas[0] + ctas[1]; k += kPlanThreads) {
+    const int c = k < ctas[0] ? 0 : 1, cta = c == 0 ? k : k - ctas[0];
+    ExtStart t;
+    t.u0 = ext_first(done[c], ctas[c], cta);
+    t.u1 = ext_first(done[c], ctas[c], cta + 1);
+    int lo = 0, hi = segs - 1;  // the last segment that begins at u0 or before
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if ((mid < kPlanThreads ? first_units[c][mid] : A.segs[mid].unit0[c]) <= t.u0) lo = mid; else hi = mid - 1;
+    }
+    t.seg = lo;
+    t.g = A.segs[lo];
+    const int64_t r = t.u0 - t.g.unit0[c];
+    // (in 32 bits where they do)
+    const int pair = static_cast<int>(r >> 32 == 0 && t.g.units >> 32 == 0
+                                          ? static_cast<uint32_t>(r) / static_cast<uint32_t>(t.g.units)
+                                          : r / t.g.units);
+    t.blk = ext_block_of(A.sh[c], t.g, r - pair * t.g.units);
+    t.base = t.g.unit0[c] + pair * t.g.units + ext_units_before(A.sh[c], t.g, t.blk);
+    t.hk = pair / A.blocks_per_kv;
+    t.hblk = pair - t.hk * A.blocks_per_kv;
+    A.starts[c][cta] = t;
   }
 }
 
@@ -650,7 +682,7 @@ int few_rows_of(const ra_paged_cache* c, bool decode, int n_tokens, int hq) {
 
 // The workspace's regions, one after the other.
 struct Regions {
-  size_t segs, part_o[2], part_ml[2], row_o, row_ml, total;
+  size_t segs, starts[2], part_o[2], part_ml[2], row_o, row_ml, total;
   int rows[2], ctas[2];  // of the parts of each class
 };
 Regions regions_of(const ra_paged_cache* c, int n_groups, int n_tokens, int hq) {
@@ -667,6 +699,8 @@ Regions regions_of(const ra_paged_cache* c, int n_groups, int n_tokens, int hq) 
   r.segs = 256;
   size_t at = r.segs + up((static_cast<size_t>(n_groups) + c->n_seqs) * sizeof(ExtSeg));
   for (int k = 0; k < 2; ++k) {
+    r.starts[k] = at;
+    at += up(r.ctas[k] * sizeof(ExtStart));
     const size_t parts = static_cast<size_t>(r.ctas[k]) * 2 * r.rows[k];
     r.part_o[k] = at;
     r.part_ml[k] = r.part_o[k] + up(parts * c->head_dim * 4);
@@ -783,9 +817,11 @@ extern "C" int ra_paged_attn_extend(const ra_paged_cache* c, const ra_shared_pre
   char* ws = static_cast<char*>(workspace);
   A.head = reinterpret_cast<ExtHead*>(ws);
   A.segs = reinterpret_cast<ExtSeg*>(ws + at.segs);
-  for (int k = 0; k < 2; ++k)
+  for (int k = 0; k < 2; ++k) {
+    A.starts[k] = reinterpret_cast<ExtStart*>(ws + at.starts[k]);
     A.part[k] = {reinterpret_cast<float*>(ws + at.part_o[k]), reinterpret_cast<float2*>(ws + at.part_ml[k]),
                  k == kExtFew ? A.few_rows : at.rows[k], at.ctas[k] / kExtSms * sms};
+  }
   A.row_o = reinterpret_cast<float*>(ws + at.row_o);
   A.row_ml = reinterpret_cast<float2*>(ws + at.row_ml);
   A.out = out;
@@ -800,8 +836,8 @@ extern "C" int ra_paged_attn_extend(const ra_paged_cache* c, const ra_shared_pre
   // unless a K/V head has many query heads
   const bool many = A.few_rows == 0 || (static_cast<int64_t>(n_tokens) * A.group > A.few_rows &&
                                         (cu_new != nullptr || n_groups > 0 || A.group > A.few_rows));
-  if (e == cudaSuccess && many) e = c->dtype == RA_BF16 ? launch_extend_tc(A, maps, st) : launch_extend_simt(A, st);
   if (e == cudaSuccess && A.few_rows > 0) e = launch_extend_few(A, st);
+  if (e == cudaSuccess && many) e = c->dtype == RA_BF16 ? launch_extend_tc(A, maps, st) : launch_extend_simt(A, st);
   if (e == cudaSuccess) {
     // at most one block of a sequence has fewer tokens than the others
     int64_t blocks = static_cast<int64_t>(n_tokens / A.sh[kExtMany].bt) + c->n_seqs;

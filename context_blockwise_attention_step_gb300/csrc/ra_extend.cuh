@@ -45,6 +45,7 @@ struct ExtArgs {
   uint64_t timeout_ns;
   ExtHead* head;
   ExtSeg* segs;
+  ExtStart* starts[2];         // of each class's CTAs
   float* row_o;                // results like a part's, of whole blocks that are joined: [2][n_tokens][hq][dh]
   float2* row_ml;
   void* out;
@@ -70,35 +71,21 @@ template <int CLS>
 struct ExtCursor {
   int64_t u0, u1, base;
   ExtSeg g;
-  int cta, segs, seg, pair, blk, blocks;
+  int cta, seg, hk, hblk, blk, blocks;
 
   __device__ __forceinline__ bool begin(const ExtArgs& A, int which) {
-    const int64_t units = A.head->units[CLS];
-    const int ctas = A.head->ctas[CLS];
-    segs = A.head->segs;
+    if (which >= A.head->ctas[CLS]) return false;
+    const ExtStart& s = A.starts[CLS][which];
     cta = which;
-    if (which >= ctas) return false;
-    u0 = ext_first(units, ctas, which);
-    u1 = ext_first(units, ctas, which + 1);
-    // the last segment that begins at u0 or before: 32 places at a time
-    const int lane = threadIdx.x & 31;
-    int lo = 0, n = segs;
-    while (n > 1) {
-      const int step = (n + 31) / 32, at = lo + lane * step;
-      const bool before = at < lo + n && A.segs[at].unit0[CLS] <= u0;
-      const int k = __popc(__ballot_sync(0xffffffffu, before)) - 1;
-      const int next = lo + k * step;
-      n = min(step, lo + n - next);
-      lo = next;
-    }
-    seg = lo;
-    g = A.segs[seg];
-    int64_t r = u0 - g.unit0[CLS];
-    pair = static_cast<int>(r / g.units);
-    r -= pair * g.units;
+    u0 = s.u0;
+    u1 = s.u1;
+    base = s.base;
+    seg = s.seg;
+    hk = s.hk;
+    hblk = s.hblk;
+    blk = s.blk;
+    g = s.g;
     blocks = ext_blocks(A.sh[CLS], g.n);
-    blk = ext_block_of(A.sh[CLS], g, r);
-    base = g.unit0[CLS] + pair * g.units + ext_units_before(A.sh[CLS], g, blk);
     return true;
   }
 
@@ -109,14 +96,14 @@ struct ExtCursor {
       const int weight = ext_weight(sh, g, blk);
       const int j0 = ext_tile_from(base, weight, w.count, u0), j1 = ext_tile_from(base, weight, w.count, u1);
       if (j0 < j1) {
-        const int a = blk * sh.bt, hblk = pair % A.blocks_per_kv;
+        const int a = blk * sh.bt;
         it.walk = w;
         it.j0 = j0;
         it.tiles = j1 - j0;
         it.tok0 = g.t0 + a;
         it.ntok = min(sh.bt, g.n - a);
         it.two = it.ntok > sh.half;
-        it.hk = pair / A.blocks_per_kv;
+        it.hk = hk;
         it.g0 = hblk * A.hb;
         it.heads = min(A.hb, A.group - it.g0);
         it.shared = g.shared;
@@ -131,14 +118,14 @@ struct ExtCursor {
       base += static_cast<int64_t>(w.count) * weight;
       if (++blk == blocks) {
         blk = 0;
-        if (++pair == A.hkv * A.blocks_per_kv) {
-          pair = 0;
-          do {
-            if (++seg >= segs) {
-              base = u1;
-              break;
-            }
-            g = A.segs[seg];
+        if (++hblk == A.blocks_per_kv) {
+          hblk = 0;
+          ++hk;
+        }
+        if (hk == A.hkv && base < u1) {
+          hk = 0;
+          do {  // (units are left, so there is one)
+            g = A.segs[++seg];
           } while (g.units == 0 || g.cls != CLS);
           blocks = ext_blocks(sh, g.n);
         }

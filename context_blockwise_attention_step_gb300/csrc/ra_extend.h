@@ -45,6 +45,13 @@ struct ExtSeg {
   int32_t cls;
 };
 
+// Where the share of a CTA begins and ends, and the block that its first unit falls to.
+struct ExtStart {
+  int64_t u0, u1, base;  // base: the block's first unit
+  int32_t seg, hk, hblk, blk;
+  ExtSeg g;
+};
+
 // Tiles of a block: walk index j is tile j for j < ns (first tokens before the window), else
 // first + j - ns.
 struct ExtWalk {
@@ -154,7 +161,7 @@ RA_HD int ext_cta_of(int64_t units, int ctas, int64_t u) {
 // is not before unit u.
 RA_HD int ext_tile_from(int64_t base, int weight, int count, int64_t u) {
   if (u <= base) return 0;
-  const int64_t j = (u - base + weight - 1) / weight;
+  const int64_t j = (u - base + weight - 1) >> (weight - 1);  // weight is 1 or 2
   return j < count ? static_cast<int>(j) : count;
 }
 

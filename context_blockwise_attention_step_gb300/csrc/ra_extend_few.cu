@@ -79,6 +79,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DH>::CTAS) extend_few(const __gr
   // the load side: rows of the next tile's keys (lane i: key i; -1: no tile), then its copies
   Tiles load;
   load.begin(A);
+  Tiles at = load;  // the side that computes
   int64_t row = -1;
   auto look_up = [&]() {
     row = -1;
@@ -115,8 +116,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<DH>::CTAS) extend_few(const __gr
   }
 
   int stage = 0;
-  Tiles at;
-  at.begin(A);
   while (at.more) {
     const ExtItem& it = at.it;
     const int rows = it.ntok * it.heads, heads = it.heads;
