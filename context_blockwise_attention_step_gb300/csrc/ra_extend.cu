@@ -25,7 +25,7 @@ static __device__ unsigned int g_status_extend;  // an index outside the cache
 namespace {
 
 // ---------------------------------------------------------------- planning
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 512, kPlanWarps = kPlanThreads / 32;
 
 struct Tokens {
   int t0, n, len;
@@ -56,8 +56,8 @@ __device__ __forceinline__ Tokens tokens_of(const ExtArgs& A, int b) {
 }
 
 __global__ void __launch_bounds__(kPlanThreads) extend_plan(const __grid_constant__ ExtArgs A) {
-  __shared__ int64_t scan_units[2][32];
-  __shared__ int scan_blocks[32];
+  __shared__ int64_t scan_units[2][kPlanWarps];
+  __shared__ int scan_blocks[kPlanWarps];
   __shared__ int64_t first_units[2][kPlanThreads];  // of the first segments
   __shared__ int group_keys[kPlanThreads];  // of the first groups: the keys that are shared, 0: none
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan(const __grid_constan
   launch_dependents();
   auto class_of = [&](int n) { return n * int64_t(A.group) <= A.few_rows ? kExtFew : kExtMany; };
   // groups, a warp each: whether the prefix lies before every new token, and whether sharing it pays
-  for (int g = warp; g < A.n_groups; g += 32) {
+  for (int g = warp; g < A.n_groups; g += kPlanWarps) {
     const int b0 = bounded(A.cu_groups[g], A.n_seqs), b1 = bounded(A.cu_groups[g + 1], A.n_seqs);
     const int64_t cap = static_cast<int64_t>(A.max_pages) * A.page_size;
     int p = A.prefix_lens[g];
@@ -166,8 +166,9 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan(const __grid_constan
     }
     __syncthreads();
     // each warp sums the warps before it, a lane a warp
-    int64_t p0 = scan_units[0][lane], p1 = scan_units[1][lane];
-    int pb = scan_blocks[lane];
+    const bool there = lane < kPlanWarps;
+    int64_t p0 = there ? scan_units[0][lane] : 0, p1 = there ? scan_units[1][lane] : 0;
+    int pb = there ? scan_blocks[lane] : 0;
     int64_t before[2] = {lane < warp ? p0 : 0, lane < warp ? p1 : 0};
     int before_blocks = lane < warp ? pb : 0;
 #pragma unroll
@@ -194,7 +195,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan(const __grid_constan
     done_blocks += pb;
   }
   int ctas[2];
-  for (int c = 0; c < 2; ++c) ctas[c] = ext_ctas(done[c], A.part[c].most_ctas, A.sh[c].wide);
+  for (int c = 0; c < 2; ++c) ctas[c] = ext_ctas(A.sh[c], done[c], A.part[c].most_ctas);
   if (tid == 0) {
     ExtHead h;
     for (int c = 0; c < 2; ++c) {
@@ -207,28 +208,27 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan(const __grid_constan
   }
   __syncthreads();
   // where each CTA begins
-  for (int k = tid; k < ctas[0] + ctas[1]; k += kPlanThreads) {
-    const int c = k < ctas[0] ? 0 : 1, cta = c == 0 ? k : k - ctas[0];
-    ExtStart t;
-    t.u0 = ext_first(done[c], ctas[c], cta);
-    t.u1 = ext_first(done[c], ctas[c], cta + 1);
+  for (int k = tid; k < ctas[0] + ctas[1] + 2; k += kPlanThreads) {
+    const int c = k <= ctas[0] ? 0 : 1, cta = c == 0 ? k : k - ctas[0] - 1;
+    ExtStart& to = A.starts[c][cta];
+    const int64_t u0 = cta < ctas[c] ? ext_first(done[c], ctas[c], cta) : done[c];
+    to.u0 = u0;
+    if (cta == ctas[c]) continue;
     int lo = 0, hi = segs - 1;  // the last segment that begins at u0 or before
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if ((mid < kPlanThreads ? first_units[c][mid] : A.segs[mid].unit0[c]) <= t.u0) lo = mid; else hi = mid - 1;
+      if ((mid < kPlanThreads ? first_units[c][mid] : A.segs[mid].unit0[c]) <= u0) lo = mid; else hi = mid - 1;
     }
-    t.seg = lo;
-    t.g = A.segs[lo];
-    const int64_t r = t.u0 - t.g.unit0[c];
-    // (in 32 bits where they do)
-    const int pair = static_cast<int>(r >> 32 == 0 && t.g.units >> 32 == 0
-                                          ? static_cast<uint32_t>(r) / static_cast<uint32_t>(t.g.units)
-                                          : r / t.g.units);
-    t.blk = ext_block_of(A.sh[c], t.g, r - pair * t.g.units);
-    t.base = t.g.unit0[c] + pair * t.g.units + ext_units_before(A.sh[c], t.g, t.blk);
-    t.hk = pair / A.blocks_per_kv;
-    t.hblk = pair - t.hk * A.blocks_per_kv;
-    A.starts[c][cta] = t;
+    const ExtSeg g = A.segs[lo];
+    const int64_t r = u0 - g.unit0[c];
+    const int pair = static_cast<int>(ext_div(r, g.units));
+    const int blk = ext_block_of(A.sh[c], g, r - pair * g.units);
+    to.base = g.unit0[c] + pair * g.units + ext_units_before(A.sh[c], g, blk);
+    to.seg = lo;
+    to.hk = pair / A.blocks_per_kv;
+    to.hblk = pair - to.hk * A.blocks_per_kv;
+    to.blk = blk;
+    to.g = g;
   }
 }
 
@@ -458,7 +458,7 @@ __device__ __forceinline__ Cut cut_of(const ExtArgs& A, const ExtSeg& g, int pai
   c.cls = g.cls;
   c.tok0 = g.t0 + blk * sh.bt;
   c.c0 = ext_cta_of(units, ctas, base);
-  c.c1 = ext_cta_of(units, ctas, base + static_cast<int64_t>(ext_walk(sh, g, blk).count - 1) * ext_weight(sh, g, blk));
+  c.c1 = ext_cta_of(units, ctas, ext_tile_unit(sh, base, ext_weight(sh, g, blk), ext_walk(sh, g, blk).count - 1));
   return c;
 }
 
@@ -665,6 +665,7 @@ ExtShape shape_of(int dtype, int hb, int window, int sinks) {
   s.half = (dtype == RA_BF16 ? 128 : kSimtRows) / hb;
   s.bt = dtype == RA_BF16 ? 2 * s.half : s.half;
   s.wide = dtype == RA_BF16 ? 2 : 1;
+  s.lead = 1;
   s.shift = dtype == RA_BF16 ? 7 : 6;
   s.window = window;
   s.sinks = sinks;
@@ -700,7 +701,7 @@ Regions regions_of(const ra_paged_cache* c, int n_groups, int n_tokens, int hq) 
   size_t at = r.segs + up((static_cast<size_t>(n_groups) + c->n_seqs) * sizeof(ExtSeg));
   for (int k = 0; k < 2; ++k) {
     r.starts[k] = at;
-    at += up(r.ctas[k] * sizeof(ExtStart));
+    at += up((r.ctas[k] + 1) * sizeof(ExtStart));
     const size_t parts = static_cast<size_t>(r.ctas[k]) * 2 * r.rows[k];
     r.part_o[k] = at;
     r.part_ml[k] = r.part_o[k] + up(parts * c->head_dim * 4);
@@ -810,7 +811,7 @@ extern "C" int ra_paged_attn_extend(const ra_paged_cache* c, const ra_shared_pre
   head_blocks(A.group, c->dtype == RA_BF16 ? 128 : kSimtRows, &A.hb, &A.blocks_per_kv);
   A.sh[kExtMany] = shape_of(c->dtype, A.hb, window, window > 0 ? sinks : 0);
   A.few_rows = few_rows_of(c, cu_new == nullptr, n_tokens, hq);
-  A.sh[kExtFew] = {16, 16, 1, 6, window, window > 0 ? sinks : 0};  // one block, tiles of 64 keys
+  A.sh[kExtFew] = {16, 16, 1, 1, 6, window, window > 0 ? sinks : 0};  // one block, tiles of 64 keys
   const int sms = n_sm < kExtSms ? n_sm : kExtSms;
   A.scale_log2 = (scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(c->head_dim))) * 1.4426950408889634f;
   A.timeout_ns = kDefaultTimeoutNs;

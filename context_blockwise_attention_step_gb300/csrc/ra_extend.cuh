@@ -45,7 +45,7 @@ struct ExtArgs {
   uint64_t timeout_ns;
   ExtHead* head;
   ExtSeg* segs;
-  ExtStart* starts[2];         // of each class's CTAs
+  ExtStart* starts[2];         // of each class's CTAs, and of one behind the last (u0 alone)
   float* row_o;                // results like a part's, of whole blocks that are joined: [2][n_tokens][hq][dh]
   float2* row_ml;
   void* out;
@@ -78,7 +78,7 @@ struct ExtCursor {
     const ExtStart& s = A.starts[CLS][which];
     cta = which;
     u0 = s.u0;
-    u1 = s.u1;
+    u1 = (&s + 1)->u0;
     base = s.base;
     seg = s.seg;
     hk = s.hk;
@@ -94,7 +94,8 @@ struct ExtCursor {
     while (base < u1) {
       const ExtWalk w = ext_walk(sh, g, blk);
       const int weight = ext_weight(sh, g, blk);
-      const int j0 = ext_tile_from(base, weight, w.count, u0), j1 = ext_tile_from(base, weight, w.count, u1);
+      const int j0 = ext_tile_from(sh, base, weight, w.count, u0);
+      const int j1 = ext_tile_from(sh, base, weight, w.count, u1);
       if (j0 < j1) {
         const int a = blk * sh.bt;
         it.walk = w;
@@ -115,7 +116,7 @@ struct ExtCursor {
         it.dest = !whole ? kExtPart : joined ? kExtRows : kExtFinal;
         it.slot = !whole ? cta * 2 + (j0 > 0 ? 0 : 1) : g.shared ? 0 : 1;
       }
-      base += static_cast<int64_t>(w.count) * weight;
+      base += ext_units(sh, w.count, weight);
       if (++blk == blocks) {
         blk = 0;
         if (++hblk == A.blocks_per_kv) {

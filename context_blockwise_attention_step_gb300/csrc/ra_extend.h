@@ -9,10 +9,11 @@
 //                   the last `window` of these and the first `sinks`
 // k0 and k1 are whole key tiles. A segment's tokens are cut into blocks of `bt`; a block walks the
 // key tiles that one of its rows sees. A tile of a block costs a unit if the block has at most
-// `half` tokens, else `wide` units, and every CTA gets the same share of all units, in the
-// order segment, pair (K/V head and block of its query heads), block, tile. A tile belongs to the
-// CTA that its first unit falls to; with shares of `wide` units at least, each CTA between the first
-// and the last of a block has a tile of it.
+// `half` tokens, else `wide` units, a block `lead` units more (its start and end, counted with its first
+// tile), and every CTA gets the same share of all units, in the order segment, pair (K/V head and
+// block of its query heads), block, tile. A tile belongs to the CTA that its first unit falls to; with
+// shares of lead + wide units at least, each CTA between the first and the last of a block has a tile
+// of it.
 //
 // Segments are of two classes, each with a kernel, a shape and shares of its own: those of few rows
 // (at most 16 a K/V head, all in one block), and the others.
@@ -27,7 +28,8 @@ enum : int { kExtMany = 0, kExtFew = 1 };
 
 struct ExtShape {
   int32_t bt, half;  // tokens of a block, and of one that costs one unit a tile
-  int32_t wide;      // units of a tile of a larger block
+  int32_t wide;      // units of a tile of a larger block: 1 or 2
+  int32_t lead;      // units of a block beside its tiles'
   int32_t shift;     // log2 of a tile's keys
   int32_t window, sinks;
 };
@@ -45,9 +47,14 @@ struct ExtSeg {
   int32_t cls;
 };
 
-// Where the share of a CTA begins and ends, and the block that its first unit falls to.
+// a / b. (In 32 bits where they do: a division of 64 takes a hundred instructions.)
+RA_HD int64_t ext_div(int64_t a, int64_t b) {
+  return (a | b) >> 31 == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+}
+
+// Where the share of a CTA begins, and the block that its first unit falls to.
 struct ExtStart {
-  int64_t u0, u1, base;  // base: the block's first unit
+  int64_t u0, base;  // base: the block's first unit (u1 is the next CTA's u0)
   int32_t seg, hk, hblk, blk;
   ExtSeg g;
 };
@@ -127,41 +134,55 @@ RA_HD int64_t ext_tiles_before(const ExtShape& s, const ExtSeg& g, int64_t i) {
   return sum;
 }
 
-// Units of a tile of block i, and of the blocks before block i <= blocks (of one pair).
+// Units of a tile of block i, of the block, and of the blocks before block i <= blocks (of one pair).
 RA_HD int ext_weight(const ExtShape& s, const ExtSeg& g, int i) {
   return g.n - static_cast<int64_t>(i) * s.bt > s.half ? s.wide : 1;
 }
+RA_HD int64_t ext_units(const ExtShape& s, int count, int weight) { return s.lead + static_cast<int64_t>(count) * weight; }
 RA_HD int64_t ext_units_before(const ExtShape& s, const ExtSeg& g, int i) {
   const int nb = ext_blocks(s, g.n);
   if (i <= 0 || nb == 0) return 0;
-  if (i < nb) return ext_tiles_before(s, g, i) * s.wide;
-  return ext_tiles_before(s, g, nb - 1) * s.wide +
-         static_cast<int64_t>(ext_walk(s, g, nb - 1).count) * ext_weight(s, g, nb - 1);
+  const int whole = i < nb ? i : nb - 1;  // blocks that are certainly whole
+  const int64_t units = whole == 0 ? 0 : ext_tiles_before(s, g, whole) * s.wide + static_cast<int64_t>(whole) * s.lead;
+  return i < nb ? units : units + ext_units(s, ext_walk(s, g, nb - 1).count, ext_weight(s, g, nb - 1));
 }
 // The block that unit u of a pair falls to.
-RA_HD int ext_block_of(const ExtShape& s, const ExtSeg& g, int64_t u) {
+RA_HD int ext_block_among(const ExtShape& s, const ExtSeg& g, int64_t u) {
   int lo = 0, hi = ext_blocks(s, g.n) - 1;
+  if (g.shared) {  // all blocks alike but the last
+    const int64_t i = ext_div(u, ext_units(s, ext_walk(s, g, 0).count, s.wide));
+    return i < hi ? static_cast<int>(i) : hi;
+  }
   while (lo < hi) {
     const int mid = lo + (hi - lo + 1) / 2;
     if (ext_units_before(s, g, mid) <= u) lo = mid; else hi = mid - 1;
   }
   return lo;
 }
+RA_HD int ext_block_of(const ExtShape& s, const ExtSeg& g, int64_t u) {
+  return g.n <= s.bt ? 0 : ext_block_among(s, g, u);
+}
 
 // Shares: of `units` units CTA i of `ctas` has [ext_first(i), ext_first(i + 1)).
-RA_HD int ext_ctas(int64_t units, int most, int wide) {
-  const int64_t c = units / wide;
-  return static_cast<int>(c < 1 ? (units > 0 ? 1 : 0) : c < most ? c : most);
+RA_HD int ext_ctas(const ExtShape& s, int64_t units, int most) {
+  const int64_t least = s.wide + s.lead;
+  if (units >= most * least) return most;
+  const int64_t c = units / least;
+  return static_cast<int>(c < 1 ? (units > 0 ? 1 : 0) : c);
 }
-RA_HD int64_t ext_first(int64_t units, int ctas, int i) { return units * i / ctas; }
+RA_HD int64_t ext_first(int64_t units, int ctas, int i) { return ext_div(units * i, ctas); }
 RA_HD int ext_cta_of(int64_t units, int ctas, int64_t u) {
-  return static_cast<int>(((u + 1) * ctas - 1) / units);
+  return static_cast<int>(ext_div((u + 1) * ctas - 1, units));
 }
-// The first tile of a block (its first unit `base`, `count` tiles of `weight` units) whose first unit
-// is not before unit u.
-RA_HD int ext_tile_from(int64_t base, int weight, int count, int64_t u) {
+// The first unit of tile j of a block (its own first unit is `base`), and the first tile of a block of
+// `count` tiles of `weight` units whose first unit is not before unit u.
+RA_HD int64_t ext_tile_unit(const ExtShape& s, int64_t base, int weight, int j) {
+  return j == 0 ? base : base + s.lead + static_cast<int64_t>(j) * weight;
+}
+RA_HD int ext_tile_from(const ExtShape& s, int64_t base, int weight, int count, int64_t u) {
   if (u <= base) return 0;
-  const int64_t j = (u - base + weight - 1) >> (weight - 1);  // weight is 1 or 2
+  const int64_t past = u - base - s.lead;
+  const int64_t j = past <= weight ? 1 : (past + weight - 1) >> (weight - 1);  // weight is 1 or 2
   return j < count ? static_cast<int>(j) : count;
 }
 

@@ -100,8 +100,7 @@ __device__ __forceinline__ void store_cols(__nv_bfloat16* dst, const float (&v)[
 template <int N>
 __device__ __forceinline__ void store_cols(float* dst, const float (&v)[N]) {
 #pragma unroll
-  for (int q = 0; q < N / 4; ++q)
-    reinterpret_cast<float4*>(dst)[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+  for (int q = 0; q < N / 8; ++q) st_global_v8(dst + 8 * q, v + 8 * q);
 }
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2,

@@ -362,6 +362,13 @@ __device__ __forceinline__ uint64_t f2_of_f16x2(uint32_t v) {
   return f2(lo, hi);
 }
 
+// Eight floats (32-byte aligned) in one store: a whole sector of a thread.
+__device__ __forceinline__ void st_global_v8(float* dst, const float* v) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
 // Fire-and-forget vector reduction into global memory (four f32 adds, 16-byte aligned).
 __device__ __forceinline__ void red_add_v4(float* dst, float a, float b, float c, float d) {
   asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(dst), "f"(a), "f"(b), "f"(c),

@@ -40,6 +40,7 @@ int main() {
     s.shift = keys == 128 ? 7 : 6;
     s.half = keys / heads;
     s.wide = keys == 128 ? 2 : 1;
+    s.lead = rand() % 3;
     s.bt = s.wide * s.half;
     s.window = rand() % 2 ? 1 + rand() % 1500 : 0;
     s.sinks = s.window && rand() % 3 ? rand() % 129 : 0;
@@ -69,50 +70,53 @@ int main() {
         if (seen[t]) want.push_back(static_cast<int>(t));
       for (int j = 0; j < w.count; ++j) got.push_back(ext_tile(w, j));
       if (got != want) bad("the tiles of a block", s, g, i);
-      const int weight = ext_weight(s, g, i);
-      for (int64_t x : {int64_t(0), int64_t(w.count) * weight - 1})
+      const int64_t all = s.lead + int64_t(w.count) * ext_weight(s, g, i);
+      for (int64_t x : {int64_t(0), all - 1})
         if (ext_block_of(s, g, units + x) != i) bad("the block of a unit", s, g, i);
-      units += int64_t(w.count) * weight;
+      units += all;
     }
     if (ext_units_before(s, g, nb) != units) bad("all units", s, g, nb);
   }
   // every tile belongs to one CTA, and the CTAs of a block are neighbours: none between has no part
   for (int it = 0; it < 20000; ++it) {
-    const ExtShape none = {};
     const ExtSeg seg = {};
-    const int wide = 1 + rand() % 2, nb = 1 + rand() % 40;
+    const int nb = 1 + rand() % 40;
+    ExtShape s = {};
+    s.wide = 1 + rand() % 2;
+    s.lead = rand() % 3;
     std::vector<int> count, weight;
     int64_t units = 0;
     for (int i = 0; i < nb; ++i) {
       count.push_back(1 + rand() % 30);
-      weight.push_back(wide == 2 && rand() % 2 ? 2 : 1);
-      units += count[i] * weight[i];
+      weight.push_back(s.wide == 2 && rand() % 2 ? 2 : 1);
+      units += ext_units(s, count[i], weight[i]);
     }
-    const int ctas = ext_ctas(units, 1 + rand() % 152, wide);
+    const int ctas = ext_ctas(s, units, 1 + rand() % 152);
     std::vector<std::vector<int>> owner(nb);
     for (int c = 0; c < ctas; ++c) {
       const int64_t u0 = ext_first(units, ctas, c), u1 = ext_first(units, ctas, c + 1);
       int64_t base = 0;
-      for (int i = 0; i < nb; base += int64_t(count[i]) * weight[i], ++i)
-        for (int j = ext_tile_from(base, weight[i], count[i], u0); j < ext_tile_from(base, weight[i], count[i], u1); ++j) {
+      for (int i = 0; i < nb; base += ext_units(s, count[i], weight[i]), ++i)
+        for (int j = ext_tile_from(s, base, weight[i], count[i], u0); j < ext_tile_from(s, base, weight[i], count[i], u1);
+             ++j) {
           owner[i].push_back(c);
-          if (ext_cta_of(units, ctas, base + int64_t(j) * weight[i]) != c) bad("the CTA of a tile", none, seg, i);
+          if (ext_cta_of(units, ctas, ext_tile_unit(s, base, weight[i], j)) != c) bad("the CTA of a tile", s, seg, i);
         }
     }
     for (int i = 0; i < nb; ++i) {
-      if (static_cast<int>(owner[i].size()) != count[i]) bad("tiles without a CTA", none, seg, i);
+      if (static_cast<int>(owner[i].size()) != count[i]) bad("tiles without a CTA", s, seg, i);
       for (size_t j = 1; j < owner[i].size(); ++j)
-        if (owner[i][j] < owner[i][j - 1] || owner[i][j] > owner[i][j - 1] + 1) bad("a CTA without a part", none, seg, i);
+        if (owner[i][j] < owner[i][j - 1] || owner[i][j] > owner[i][j - 1] + 1) bad("a CTA without a part", s, seg, i);
     }
   }
   // far positions: in 64 bits
   {
-    ExtShape s = {2, 1, 2, 7, 0, 0};
+    ExtShape s = {2, 1, 2, 1, 7, 0, 0};
     ExtSeg g = {};
     g.n = 1000;
     g.base = 2147483584 - 1000;
     int64_t sum = 0;
-    for (int i = 0; i < ext_blocks(s, g.n); ++i) sum += int64_t(ext_walk(s, g, i).count) * ext_weight(s, g, i);
+    for (int i = 0; i < ext_blocks(s, g.n); ++i) sum += ext_units(s, ext_walk(s, g, i).count, ext_weight(s, g, i));
     if (sum != ext_units_before(s, g, ext_blocks(s, g.n))) bad("far positions", s, g, 0);
     s.window = 2147483647;
     if (sum != ext_units_before(s, g, ext_blocks(s, g.n))) bad("a window over everything", s, g, 0);
