@@ -349,8 +349,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float sl2 = A.scale_log2;
     const uint64_t sl2x2 = f2(sl2, sl2);
     const int tok = row / A.hb, head = row - tok * A.hb;  // of a query tile
-    uint32_t s_phase = 0, od_phase[2] = {0, 0}, sums_phase = 0, xm_phase[2] = {0, 0};
-    int xn = 0;  // max exchanges done (slot = xn & 1)
+    uint32_t tiles = 0;    // of this team so far: the phases of S and of the exchanges of maxima
+    uint32_t od1_phase = 0;
     int kv = 0;
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, tmo, status));
@@ -370,26 +370,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       // row of a product depends on another): it sees everything, so that it asks for no mask.
       const int hi = !valid ? 0x7fffffff : it.shared ? it.end : it.base + tk + 1;
       const int lo = valid && A.sh[kExtMany].window > 0 ? max(0, hi - A.sh[kExtMany].window) : 0;
+      // tiles full_from .. full_to - 1 are seen whole by every row of the warp
+      const int full_from = (__reduce_max_sync(0xffffffffu, lo) + 127) >> 7, full_to = __reduce_min_sync(0xffffffffu, hi) >> 7;
       float m = -INFINITY, l = 0.f;
       bool ok = true;
       for (int k = 0; k < mine; ++k) {
-        const int n = two ? k : 2 * k + t, j = it.j0 + n, k0 = ext_tile(it.walk, j) * 128;
-        if (!(ok = wait(&sh.s_full[t], s_phase))) break;
-        s_phase ^= 1;
+        const int n = two ? k : 2 * k + t, j = it.j0 + n, tile = ext_tile(it.walk, j), k0 = tile * 128;
+        if (!(ok = wait(&sh.s_full[t], tiles & 1))) break;
         tc_fence_after();
+        const uint32_t xs = tiles & 1, xs_phase = (tiles >> 1) & 1;
+        ++tiles;
         if (idle) {  // no rows in this warp: its products are not looked at
-          const int xs = xn & 1;
           mbar_arrive(&sh.xmax_bar[t][xs]);
-          xm_phase[xs] ^= 1;
-          ++xn;
         } else {
-          const int cnt = min(max(hi - k0, 0), 128);
-          const int lo_t = lo - k0, sk_t = A.sh[kExtMany].window > 0 && k0 == 0 ? A.sh[kExtMany].sinks : 0;
-          const bool full = __all_sync(0xffffffffu, cnt == 128 && lo_t <= sk_t);  // no mask needed
+          const bool full = tile >= full_from && tile < full_to;  // no mask needed
           uint32_t vis[2] = {0xffffffffu, 0xffffffffu};
           if (!full) {
-            vis[0] = visible_bits(c0, cnt, lo_t, sk_t);
-            vis[1] = visible_bits(c0 + 32, cnt, lo_t, sk_t);
+            const int cnt = min(max(hi - k0, 0), 128), sk_t = A.sh[kExtMany].window > 0 && k0 == 0 ? A.sh[kExtMany].sinks : 0;
+            vis[0] = visible_bits(c0, cnt, lo - k0, sk_t);
+            vis[1] = visible_bits(c0 + 32, cnt, lo - k0, sk_t);
           }
           // pass 1: partial row max over this half's visible columns, then both halves'
           uint32_t r2[2][32];
@@ -419,13 +418,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mx = fmaxf(max3(mq[0], mq[1], mq[2]), mq[3]);
           }
           {
-            const int xs = xn & 1;
             sh.xmax[t][xs][hf][row] = mx;
             mbar_arrive(&sh.xmax_bar[t][xs]);
-            if (!(ok = wait(&sh.xmax_bar[t][xs], xm_phase[xs]))) break;
-            xm_phase[xs] ^= 1;
+            if (!(ok = wait(&sh.xmax_bar[t][xs], xs_phase))) break;
             mx = fmaxf(mx, sh.xmax[t][xs][hf ^ 1][row]);
-            ++xn;
           }
           mx *= sl2;
           const float m_new = fmaxf(m, mx);
@@ -489,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // values of keys that no row of the block sees: 0 (the other team's product with this tile
         // comes after this one's)
-        if (!two || t == 0) {
+        if ((!two || t == 0) && (k0 < it.low || k0 + 128 > it.end)) {
           const TileKeys seen = tile_keys(A, it, j);
           if (!seen.whole()) {
             const int c = kv + n, st = c % C::kStages;
@@ -515,13 +511,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       sh.sum[par][t][hf][row] = l;
       if (hf == 0) sh.max[par][t][row] = m;
       mbar_arrive(&sh.sums_bar);
-      if (!wait(&sh.sums_bar, sums_phase)) break;
-      sums_phase ^= 1;
-      if (!wait(&sh.o_done[0], od_phase[0])) break;
-      od_phase[0] ^= 1;
+      if (!wait(&sh.sums_bar, par)) break;
+      if (!wait(&sh.o_done[0], par)) break;
       if (count1 > 0) {
-        if (!wait(&sh.o_done[1], od_phase[1])) break;
-        od_phase[1] ^= 1;
+        if (!wait(&sh.o_done[1], od1_phase)) break;
+        od1_phase ^= 1;
       }
       tc_fence_after();
       float M, L, f0 = 1.f, f1 = 0.f;
