@@ -8,10 +8,10 @@
 //
 //   M = max m_i,  l = sum 2^(m_i - M) l_i,  out = sum 2^(m_i - M) o_i / l,  lse = (M + log2 l) ln 2
 //
-// Three launches, the second and the third while the one before still runs (programmatic dependent
-// launch): the planning kernel reads the lengths and lists the segments (ra_extend.h); the main kernel
-// (ra_extend_tc.cu for bf16) deals them out evenly to its CTAs; the join works on the blocks that need
-// it. The host need not know a length.
+// Three or four launches, each while the one before still runs (programmatic dependent launch): the
+// planning kernel reads the lengths and lists the segments (ra_extend.h); the main kernels, for many
+// rows (ra_extend_tc.cu, float32 here) and for few (ra_extend_few.cu), deal them out evenly to their
+// CTAs; the join works on the blocks that need it. The host need not know a length.
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -63,6 +63,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan(const __grid_constan
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const ExtShape& s = A.sh[kExtMany];
   launch_dependents();
+  if (tid == 0) A.head->ready = 0;
   auto class_of = [&](int n) { return n * int64_t(A.group) <= A.few_rows ? kExtFew : kExtMany; };
   // groups, a warp each: whether the prefix lies before every new token, and whether sharing it pays
   for (int g = warp; g < A.n_groups; g += kPlanWarps) {
@@ -204,6 +205,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan(const __grid_constan
     }
     h.segs = segs;
     h.own_blocks = done_blocks;
+    h.ready = 0;
     *A.head = h;
   }
   __syncthreads();
@@ -230,6 +232,8 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan(const __grid_constan
     to.blk = blk;
     to.g = g;
   }
+  __syncthreads();
+  if (tid == 0) ext_publish(A.head);
 }
 
 // ---------------------------------------------------------------- float32
@@ -728,15 +732,16 @@ int check_extend(const ra_paged_cache* c, int n_groups, int n_tokens, int hq) {
 
 cudaError_t extend_status(unsigned int value[2], bool reset) {
   unsigned int index = 0;
-  unsigned int few = 0;
+  unsigned int few[2] = {0, 0};
   cudaError_t e = extend_tc_status(value, reset);
-  if (e == cudaSuccess) e = extend_few_status(&few, reset);
+  if (e == cudaSuccess) e = extend_few_status(few, reset);
   if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&index, g_status_extend, sizeof index);
   if (e == cudaSuccess && reset) {
     const unsigned int zero = 0;
     e = cudaMemcpyToSymbol(g_status_extend, &zero, sizeof zero);
   }
-  value[1] |= index | few;
+  value[0] |= few[0];
+  value[1] |= index | few[1];
   return e;
 }
 
@@ -831,14 +836,15 @@ extern "C" int ra_paged_attn_extend(const ra_paged_cache* c, const ra_shared_pre
   ExtMaps maps;
   if (c->dtype == RA_BF16 && (e = make_extend_maps(&maps, c, &A)) != cudaSuccess)
     return record_error(RA_ERR_UNSUPPORTED, "the pages' strides do not fit a tensor map");
-  extend_plan<<<1, kPlanThreads, 0, st>>>(A);
-  e = cudaGetLastError();
   // the kernels that can have work: one new token of every sequence and nothing shared is few rows
   // unless a K/V head has many query heads
   const bool many = A.few_rows == 0 || (static_cast<int64_t>(n_tokens) * A.group > A.few_rows &&
                                         (cu_new != nullptr || n_groups > 0 || A.group > A.few_rows));
-  if (e == cudaSuccess && A.few_rows > 0) e = launch_extend_few(A, st);
+  A.both = many;
+  extend_plan<<<1, kPlanThreads, 0, st>>>(A);
+  e = cudaGetLastError();
   if (e == cudaSuccess && many) e = c->dtype == RA_BF16 ? launch_extend_tc(A, maps, st) : launch_extend_simt(A, st);
+  if (e == cudaSuccess && A.few_rows > 0) e = launch_extend_few(A, st);
   if (e == cudaSuccess) {
     // at most one block of a sequence has fewer tokens than the others
     int64_t blocks = static_cast<int64_t>(n_tokens / A.sh[kExtMany].bt) + c->n_seqs;

@@ -16,7 +16,32 @@ constexpr int kExtSms = 152;
 struct ExtHead {
   int64_t units[2];
   int32_t ctas[2], segs, own_blocks;
+  uint32_t ready;  // set when the rest and the segments are there
 };
+
+// The kernels of a call and what they wait for. The planning kernel comes first. Of the two main
+// kernels the one for many rows waits for its end, and only then lets the one for few rows start,
+// which has the plan too, then, and need not wait for the other to end: it takes the SMs that the
+// other leaves free. (The flag that it reads first orders its reads of the plan behind the plan's
+// writes.) It ends after the other one has ended, so that the join, which waits for its end, has
+// both kernels' results.
+__device__ __forceinline__ void ext_publish(ExtHead* h) {
+  __threadfence();
+  asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(&h->ready), "r"(1u) : "memory");
+}
+// False if the plan does not come (the wait has a limit).
+__device__ __forceinline__ bool ext_acquire(const ExtHead* h, uint64_t timeout_ns, unsigned int* status) {
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+    uint32_t ready;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(ready) : "l"(&h->ready) : "memory");
+    if (ready == 1u) return true;
+    if (globaltimer_ns() - t0 > timeout_ns) {
+      atomicOr(status, 1u);
+      return false;
+    }
+  }
+}
 // The parts of the blocks of a class that are cut between CTAs: [CTA][2][rows], and [dh].
 struct ExtParts {
   float* o;    // sums, not divided by l
@@ -39,6 +64,7 @@ struct ExtArgs {
   int32_t hb, blocks_per_kv;   // query heads of a block (the last one may have fewer), blocks of a K/V head
   int32_t box_rows, ord[3];    // tensor-core kernel: keys of a copy; places of head, slot, page in the map
   ExtShape sh[2];              // of each class
+  int32_t both;                // the kernel for many rows runs before the one for few
   int32_t few_rows;            // most rows a K/V head of a segment of few rows; 0: that class is not used
   ExtParts part[2];
   float scale_log2;
@@ -156,6 +182,6 @@ cudaError_t extend_tc_status(unsigned int value[2], bool reset);  // as extend_s
 // The kernel of the segments of few rows, bf16.
 int extend_few_ctas(int head_dim);  // most CTAs
 cudaError_t launch_extend_few(const ExtArgs& A, cudaStream_t st);
-cudaError_t extend_few_status(unsigned int* value, bool reset);
+cudaError_t extend_few_status(unsigned int value[2], bool reset);
 
 }  // namespace ra

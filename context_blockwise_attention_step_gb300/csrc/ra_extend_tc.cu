@@ -210,8 +210,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  launch_dependents();
   wait_for_previous();  // the planning kernel
+  launch_dependents();  // (after it: the kernel for few rows relies on that)
   const uint32_t tmem = sh.tmem_base;
 
   if (warp == 2) {
