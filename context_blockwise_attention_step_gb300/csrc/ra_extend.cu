@@ -840,11 +840,12 @@ extern "C" int ra_paged_attn_extend(const ra_paged_cache* c, const ra_shared_pre
   // unless a K/V head has many query heads
   const bool many = A.few_rows == 0 || (static_cast<int64_t>(n_tokens) * A.group > A.few_rows &&
                                         (cu_new != nullptr || n_groups > 0 || A.group > A.few_rows));
-  A.both = many;
+  const bool few = A.few_rows > 0;
+  A.first = few ? kExtFew : kExtMany;
   extend_plan<<<1, kPlanThreads, 0, st>>>(A);
   e = cudaGetLastError();
+  if (e == cudaSuccess && few) e = launch_extend_few(A, st);
   if (e == cudaSuccess && many) e = c->dtype == RA_BF16 ? launch_extend_tc(A, maps, st) : launch_extend_simt(A, st);
-  if (e == cudaSuccess && A.few_rows > 0) e = launch_extend_few(A, st);
   if (e == cudaSuccess) {
     // at most one block of a sequence has fewer tokens than the others
     int64_t blocks = static_cast<int64_t>(n_tokens / A.sh[kExtMany].bt) + c->n_seqs;

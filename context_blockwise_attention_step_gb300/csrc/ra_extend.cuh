@@ -20,11 +20,10 @@ struct ExtHead {
 };
 
 // The kernels of a call and what they wait for. The planning kernel comes first. Of the two main
-// kernels the one for many rows waits for its end, and only then lets the one for few rows start,
-// which has the plan too, then, and need not wait for the other to end: it takes the SMs that the
-// other leaves free. (The flag that it reads first orders its reads of the plan behind the plan's
-// writes.) It ends after the other one has ended, so that the join, which waits for its end, has
-// both kernels' results.
+// kernels the first one waits for its end, and only then lets the other one start, which has the plan
+// too, then, and need not wait for the first to end: it takes the SMs that the first leaves free. (The
+// flag that it reads first orders its reads of the plan behind the plan's writes.) It ends after the
+// first has ended, so that the join, which waits for its end, has both kernels' results.
 __device__ __forceinline__ void ext_publish(ExtHead* h) {
   __threadfence();
   asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(&h->ready), "r"(1u) : "memory");
@@ -64,7 +63,7 @@ struct ExtArgs {
   int32_t hb, blocks_per_kv;   // query heads of a block (the last one may have fewer), blocks of a K/V head
   int32_t box_rows, ord[3];    // tensor-core kernel: keys of a copy; places of head, slot, page in the map
   ExtShape sh[2];              // of each class
-  int32_t both;                // the kernel for many rows runs before the one for few
+  int32_t first;               // the class whose kernel comes first
   int32_t few_rows;            // most rows a K/V head of a segment of few rows; 0: that class is not used
   ExtParts part[2];
   float scale_log2;

@@ -66,8 +66,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<DH>::CTAS) extend_few(const __gr
   constexpr int NS = C::STAGES;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float sm_m[4][16], sm_l[4][16];
+  if (A.first == kExtFew) wait_for_previous();
   launch_dependents();
-  if (!A.both) wait_for_previous();
   if (!ext_acquire(A.head, A.timeout_ns, g_status_few) || static_cast<int>(blockIdx.x) >= A.head->ctas[kExtFew]) {
     wait_for_previous();
     return;

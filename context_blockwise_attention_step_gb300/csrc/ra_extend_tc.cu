@@ -210,14 +210,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  wait_for_previous();  // the planning kernel
-  launch_dependents();  // (after it: the kernel for few rows relies on that)
+  if (A.first == kExtMany) wait_for_previous();
+  launch_dependents();
   const uint32_t tmem = sh.tmem_base;
 
   if (warp == 2) {
     // ------------------------------------------------------------------ the walk
     ExtCursor<kExtMany> cur;
-    bool more = cur.begin(A, blockIdx.x);
+    bool more = __all_sync(0xffffffffu, ext_acquire(A.head, tmo, status)) && cur.begin(A, blockIdx.x);
     for (int kq = 0;; ++kq) {
       const int slot = kq % kItems;
       const bool ok = mbar_wait(&sh.item_empty[slot], ((kq / kItems) & 1) ^ 1, abort_flag, tmo, status);
@@ -594,6 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
   }
+  wait_for_previous();  // what follows in the stream waits for this kernel alone
 }
 
 template <int DH>
