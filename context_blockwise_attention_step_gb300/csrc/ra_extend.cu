@@ -14,6 +14,7 @@
 // CTAs; the join works on the blocks that need it. The host need not know a length.
 #include <cuda_bf16.h>
 
+#include <atomic>
 #include <cmath>
 
 #include "ra_extend.cuh"
@@ -55,7 +56,7 @@ __device__ __forceinline__ Tokens tokens_of(const ExtArgs& A, int b) {
   return t;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) extend_plan(const __grid_constant__ ExtArgs A) {
+__global__ void __launch_bounds__(kPlanThreads, 1) extend_plan(const __grid_constant__ ExtArgs A) {
   __shared__ int64_t scan_units[2][kPlanWarps];
   __shared__ int scan_blocks[kPlanWarps];
   __shared__ int64_t first_units[2][kPlanThreads];  // of the first segments
@@ -211,21 +212,22 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan(const __grid_constan
   __syncthreads();
   // where each CTA begins
   for (int k = tid; k < ctas[0] + ctas[1] + 2; k += kPlanThreads) {
-    const int c = k <= ctas[0] ? 0 : 1, cta = c == 0 ? k : k - ctas[0] - 1;
+    const int c = k <= ctas[0] ? 0 : 1, cta = c == 0 ? k : k - ctas[0] - 1, n = c == 0 ? ctas[0] : ctas[1];
+    const int64_t all = c == 0 ? done[0] : done[1];
     ExtStart& to = A.starts[c][cta];
-    const int64_t u0 = cta < ctas[c] ? ext_first(done[c], ctas[c], cta) : done[c];
+    const int64_t u0 = cta < n ? ext_first(all, n, cta) : all;
     to.u0 = u0;
-    if (cta == ctas[c]) continue;
+    if (cta == n) continue;
     int lo = 0, hi = segs - 1;  // the last segment that begins at u0 or before
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if ((mid < kPlanThreads ? first_units[c][mid] : A.segs[mid].unit0[c]) <= u0) lo = mid; else hi = mid - 1;
     }
     const ExtSeg g = A.segs[lo];
-    const int64_t r = u0 - g.unit0[c];
+    const int64_t unit0 = ext_unit0(g, c), r = u0 - unit0;
     const int pair = static_cast<int>(ext_div(r, g.units));
     const int blk = ext_block_of(A.sh[c], g, r - pair * g.units);
-    to.base = g.unit0[c] + pair * g.units + ext_units_before(A.sh[c], g, blk);
+    to.base = unit0 + pair * g.units + ext_units_before(A.sh[c], g, blk);
     to.seg = lo;
     to.hk = pair / A.blocks_per_kv;
     to.hblk = pair - to.hk * A.blocks_per_kv;
@@ -457,7 +459,7 @@ __device__ __forceinline__ Cut cut_of(const ExtArgs& A, const ExtSeg& g, int pai
   const ExtShape& sh = A.sh[g.cls];
   const int64_t units = A.head->units[g.cls];
   const int ctas = A.head->ctas[g.cls];
-  const int64_t base = g.unit0[g.cls] + pair * g.units + ext_units_before(sh, g, blk);
+  const int64_t base = ext_unit0(g, g.cls) + pair * g.units + ext_units_before(sh, g, blk);
   Cut c;
   c.cls = g.cls;
   c.tok0 = g.t0 + blk * sh.bt;
@@ -477,9 +479,12 @@ template <> __device__ __forceinline__ void put4<__nv_bfloat16>(__nv_bfloat16* p
 // A block for the rows of a block of one sequence's tokens (x: block and pair): nothing to do where one
 // CTA had it whole and no prefix is shared; 0 and -inf where nothing is seen. A warp takes a row, or
 // where there are few rows a share of its parts: a lane has a part's state, all lanes its sums, four
-// columns each (QUADS), or every 32nd. Sums are taken in a fixed order.
-template <typename T, bool QUADS>
-__global__ void __launch_bounds__(kJoinThreads) extend_join(const __grid_constant__ ExtArgs A) {
+// columns each (QUADS), or every 32nd. BULK: where there are more than eight rows, which have few parts
+// each, a warp takes four rows at once, part by part (16 questions of 500 tokens behind 16384 shared
+// keys, 32/8 heads: 40 us, was 77; its registers leave half the blocks on an SM, which decoding steps
+// would pay for: 64 sequences 19 us in place of 13). Sums are taken in a fixed order.
+template <typename T, bool QUADS, bool BULK>
+__global__ void __launch_bounds__(kJoinThreads, BULK ? 2 : 4) extend_join(const __grid_constant__ ExtArgs A) {
   __shared__ Cut sh_cut[3];  // own, the prefix's block of the first token, the next one
   __shared__ ExtSeg sh_seg;
   __shared__ int sh_blk;
@@ -525,30 +530,117 @@ __global__ void __launch_bounds__(kJoinThreads) extend_join(const __grid_constan
   if (!empty && !joined && own.c0 == own.c1) return;
   const int hk = pair / A.blocks_per_kv, g0 = pair % A.blocks_per_kv * A.hb, heads = min(A.hb, A.group - g0);
   const int tok0 = g.t0 + sh_blk * bt, rows = min(bt, g.n - sh_blk * bt) * heads;
+  // the parts of a row, and the row of part i: in the row buffers, or among its class's parts
+  struct Row {
+    int pre;  // which of sh_cut
+    int n0, n, tok, h;
+    int64_t at;
+  };
+  auto row_of = [&](int r) {
+    Row w;
+    w.tok = r / heads;
+    w.h = r - w.tok * heads;
+    w.at = static_cast<int64_t>(tok0 + w.tok) * A.hq + hk * A.group + g0 + w.h;
+    w.pre = tok0 + w.tok - sh_cut[1].tok0 < A.sh[sh_cut[1].cls].bt ? 1 : 2;  // (without a prefix both are empty)
+    w.n0 = own.c1 - own.c0 + 1;
+    w.n = w.n0 + sh_cut[w.pre].c1 - sh_cut[w.pre].c0 + 1;
+    return w;
+  };
+  auto place = [&](const Row& w, int i, const float2** ml, const float** o) {
+    const bool mine = i < w.n0;
+    const Cut& c = sh_cut[mine ? 0 : w.pre];
+    if (!mine) i -= w.n0;
+    const bool whole = c.c0 == c.c1, few = c.cls == kExtFew;
+    const int64_t row = whole ? (mine ? static_cast<int64_t>(A.n_tokens) * A.hq : 0) + w.at
+                              : (static_cast<int64_t>(c.c0 + i) * 2 + (i == 0 ? 1 : 0)) * (few ? A.part[1].rows : A.part[0].rows) +
+                                    (tok0 + w.tok - c.tok0) * A.hb + w.h;
+    *ml = (whole ? A.row_ml : few ? A.part[1].ml : A.part[0].ml) + row;
+    *o = (whole ? A.row_o : few ? A.part[1].o : A.part[0].o) + row * dh;
+  };
+  auto store = [&](int64_t at, float mx, float l, float (&x)[4]) {
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] *= inv;
+    T* out = static_cast<T*>(A.out) + at * dh;
+    if constexpr (QUADS) {
+      if (4 * lane < dh) put4<T>(out + 4 * lane, x);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (lane + 32 * e < dh) out[lane + 32 * e] = static_cast<T>(x[e]);
+    }
+    if (lane == 0) A.lse[at] = l > 0.f ? (mx + log2f(l)) * 0.69314718055994531f : -INFINITY;
+  };
+  auto fetch = [&](const float* o, float (&v)[4]) {
+    if constexpr (QUADS) {
+      if (4 * lane < dh) {
+        const float4 q = *reinterpret_cast<const float4*>(o + 4 * lane);
+        v[0] = q.x;
+        v[1] = q.y;
+        v[2] = q.z;
+        v[3] = q.w;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (lane + 32 * e < dh) v[e] = o[lane + 32 * e];
+    }
+  };
+  if (BULK && rows > kJoinWarps) {
+    constexpr int U = 4;
+    for (int r0 = warp * U; r0 < rows; r0 += kJoinWarps * U) {
+      float x[U][4] = {}, l[U] = {}, mx[U];
+      int64_t at[U];
+      int most = 0;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        mx[u] = -INFINITY;
+        const Row w = row_of(min(r0 + u, rows - 1));
+        at[u] = w.at;
+        most = max(most, w.n);
+      }
+      for (int i = 0; i < most; ++i) {
+        float2 s[U];
+        float v[U][4];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const Row w = row_of(min(r0 + u, rows - 1));
+          const float2* ml;
+          const float* o;
+          s[u] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[u][e] = 0.f;
+          if (i < w.n) {
+            place(w, i, &ml, &o);
+            s[u] = *ml;
+            fetch(o, v[u]);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const float top = fmaxf(mx[u], s[u].x), ref = top == -INFINITY ? 0.f : top;
+          const float a = exp2f(mx[u] - ref), f = exp2f(s[u].x - ref);
+          mx[u] = top;
+          l[u] = a * l[u] + f * s[u].y;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[u][e] = a * x[u][e] + f * v[u][e];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (r0 + u < rows) store(at[u], mx[u], l[u], x[u]);
+    }
+    return;
+  }
   int split = 1;  // warps of a row
   while (split < kJoinWarps && 2 * split * rows <= kJoinWarps) split *= 2;
   const int share = warp % split, at_once = kJoinWarps / split;
   for (int r = warp / split; r < (rows + at_once - 1) / at_once * at_once; r += at_once) {
     const bool on = r < rows;
-    const int tok = on ? r / heads : 0, h = on ? r - tok * heads : 0;
-    const int64_t at = static_cast<int64_t>(tok0 + tok) * A.hq + hk * A.group + g0 + h;
+    const Row w = row_of(on ? r : 0);
     float x[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f, mx = -INFINITY;
-    if (on && !empty) {
-      Cut pre = {0, -1, 0, 0};
-      if (joined) pre = tok0 + tok - sh_cut[1].tok0 < A.sh[sh_cut[1].cls].bt ? sh_cut[1] : sh_cut[2];
-      const int n0 = own.c1 - own.c0 + 1, n = n0 + pre.c1 - pre.c0 + 1;
-      // the row of part i: in the row buffers, or among its class's parts
-      auto place = [&](int i, const float2** ml, const float** o) {
-        const bool mine = i < n0;
-        const Cut& c = mine ? own : pre;
-        if (!mine) i -= n0;
-        const bool whole = c.c0 == c.c1;
-        const int64_t row = whole ? (mine ? static_cast<int64_t>(A.n_tokens) * A.hq : 0) + at
-                                  : (static_cast<int64_t>(c.c0 + i) * 2 + (i == 0 ? 1 : 0)) * A.part[c.cls].rows +
-                                        (tok0 + tok - c.tok0) * A.hb + h;
-        *ml = (whole ? A.row_ml : A.part[c.cls].ml) + row;
-        *o = (whole ? A.row_o : A.part[c.cls].o) + row * dh;
-      };
+    if (on) {
+      const int n = w.n;
       // 32 parts of this warp at a time: their states, then their sums
       for (int i0 = share; i0 < n; i0 += 32 * split) {
         const int i = i0 + lane * split;
@@ -556,18 +648,18 @@ __global__ void __launch_bounds__(kJoinThreads) extend_join(const __grid_constan
         const float* o = nullptr;
         float2 s = make_float2(-INFINITY, 0.f);
         if (i < n) {
-          place(i, &ml, &o);
+          place(w, i, &ml, &o);
           s = *ml;
         }
         float top = s.x;
 #pragma unroll
-        for (int w = 16; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
         top = fmaxf(top, mx);
         const float ref = top == -INFINITY ? 0.f : top, alpha = exp2f(mx - ref), f = exp2f(s.x - ref);
         mx = top;
         float part_l = f * s.y;
 #pragma unroll
-        for (int w = 16; w > 0; w >>= 1) part_l += __shfl_xor_sync(0xffffffffu, part_l, w);
+        for (int d = 16; d > 0; d >>= 1) part_l += __shfl_xor_sync(0xffffffffu, part_l, d);
         l = l * alpha + part_l;
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[e] *= alpha;
@@ -576,19 +668,10 @@ __global__ void __launch_bounds__(kJoinThreads) extend_join(const __grid_constan
         for (int k = 0; k < count; ++k) {
           const float fk = __shfl_sync(0xffffffffu, f, k);
           const float* ok = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(o), k));
-          if constexpr (QUADS) {
-            if (4 * lane < dh) {
-              const float4 v = *reinterpret_cast<const float4*>(ok + 4 * lane);
-              x[0] += fk * v.x;
-              x[1] += fk * v.y;
-              x[2] += fk * v.z;
-              x[3] += fk * v.w;
-            }
-          } else {
+          float v[4] = {0.f, 0.f, 0.f, 0.f};
+          fetch(ok, v);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (lane + 32 * e < dh) x[e] += fk * ok[lane + 32 * e];
-          }
+          for (int e = 0; e < 4; ++e) x[e] += fk * v[e];
         }
       }
     }
@@ -614,19 +697,7 @@ __global__ void __launch_bounds__(kJoinThreads) extend_join(const __grid_constan
         for (int e = 0; e < 4; ++e) x[e] += sums[warp + k][QUADS ? (4 * lane + e) : (lane + 32 * e)];
       }
     }
-    if (!on) continue;
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] *= inv;
-    T* out = static_cast<T*>(A.out) + at * dh;
-    if constexpr (QUADS) {
-      if (4 * lane < dh) put4<T>(out + 4 * lane, x);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (lane + 32 * e < dh) out[lane + 32 * e] = x[e];
-    }
-    if (lane == 0) A.lse[at] = l > 0.f ? (mx + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    if (on) store(w.at, mx, l, x);
   }
 }
 
@@ -643,6 +714,21 @@ cudaError_t launch_after(const void* kernel, unsigned grid, unsigned threads, si
   cfg.attrs = &early;
   cfg.numAttrs = 1;
   return cudaLaunchKernelExC(&cfg, kernel, args);
+}
+
+template <typename T, bool QUADS>
+const void* join_of(bool bulk) {
+  return bulk ? reinterpret_cast<const void*>(extend_join<T, QUADS, true>)
+              : reinterpret_cast<const void*>(extend_join<T, QUADS, false>);
+}
+
+// The SMs of a device, looked up once.
+cudaError_t sm_count_of(int dev, int* n_sm) {
+  static std::atomic<int> known[kExtDevices];
+  if (dev < kExtDevices && (*n_sm = known[dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+  const cudaError_t e = cudaDeviceGetAttribute(n_sm, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess && dev < kExtDevices) known[dev].store(*n_sm, std::memory_order_relaxed);
+  return e;
 }
 
 cudaError_t launch_extend_simt(ExtArgs& A, cudaStream_t st) {
@@ -788,7 +874,7 @@ extern "C" int ra_paged_attn_extend(const ra_paged_cache* c, const ra_shared_pre
   }
   int dev = 0, n_sm = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) e = sm_count_of(dev, &n_sm);
   if (e != cudaSuccess) return record_error(RA_ERR_CUDA, "device query: %s", cudaGetErrorString(e));
   ExtArgs A = {};
   A.q = q;
@@ -851,10 +937,11 @@ extern "C" int ra_paged_attn_extend(const ra_paged_cache* c, const ra_shared_pre
     int64_t blocks = static_cast<int64_t>(n_tokens / A.sh[kExtMany].bt) + c->n_seqs;
     if (blocks > n_tokens) blocks = n_tokens;
     void* args[] = {&A};
-    const void* kernel = c->dtype == RA_BF16 ? reinterpret_cast<const void*>(extend_join<__nv_bfloat16, true>)
-                         : A.dh % 4 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0
-                             ? reinterpret_cast<const void*>(extend_join<float, true>)
-                             : reinterpret_cast<const void*>(extend_join<float, false>);
+    const bool quads = A.dh % 4 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0;  // (bf16 always)
+    const bool bulk = static_cast<int64_t>(n_tokens) * A.group > static_cast<int64_t>(kJoinWarps) * c->n_seqs;
+    const void* kernel = c->dtype == RA_BF16 ? join_of<__nv_bfloat16, true>(bulk)
+                         : quads              ? join_of<float, true>(bulk)
+                                              : join_of<float, false>(bulk);
     e = launch_after(kernel, static_cast<unsigned>(blocks * A.hkv * A.blocks_per_kv), kJoinThreads, 0, st, args);
   }
   if (e != cudaSuccess) return record_error(RA_ERR_CUDA, "extend attention launch: %s", cudaGetErrorString(e));

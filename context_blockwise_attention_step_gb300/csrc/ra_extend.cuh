@@ -4,6 +4,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "ra_extend.h"
 #include "ra_internal.h"
 #include "ra_ptx.cuh"
@@ -11,6 +13,7 @@
 namespace ra {
 
 constexpr int kExtSms = 152;
+constexpr int kExtDevices = 64;  // whose properties and kernel attributes are looked up and set once
 
 // What the planning kernel finds out, at the beginning of the workspace; the segments follow.
 struct ExtHead {
@@ -168,6 +171,17 @@ __device__ __forceinline__ int ext_page(const ExtArgs& A, int seq, int page, uns
   if (at >= 0 && at < A.n_pages) return at;
   atomicOr(status, 1u);
   return 0;
+}
+
+// Allows a kernel its dynamic shared memory, once on each device (`done`: a flag of the kernel's for each).
+template <typename K>
+cudaError_t ext_allow_smem(K kernel, int bytes, std::atomic<bool>* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < kExtDevices && done[dev].load(std::memory_order_acquire))) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < kExtDevices) done[dev].store(true, std::memory_order_release);
+  return e;
 }
 
 // The tensor-core kernel: its tensor maps (they also fill in box_rows and ord), and its launch.

@@ -47,6 +47,8 @@ struct ExtSeg {
   int32_t cls;
 };
 
+RA_HD int64_t ext_unit0(const ExtSeg& g, int cls) { return cls == kExtMany ? g.unit0[kExtMany] : g.unit0[kExtFew]; }
+
 // a / b. (In 32 bits where they do: a division of 64 takes a hundred instructions.)
 RA_HD int64_t ext_div(int64_t a, int64_t b) {
   return (a | b) >> 31 == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;

@@ -303,7 +303,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<DH>::CTAS) extend_few(const __gr
 template <int DH, bool WIDE>
 cudaError_t launch(const ExtArgs& A, cudaStream_t st) {
   auto kernel = extend_few<DH, WIDE>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<DH>::SMEM);
+  static std::atomic<bool> done[kExtDevices];
+  const cudaError_t e = ext_allow_smem(kernel, Cfg<DH>::SMEM, done);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute early;
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -601,7 +601,8 @@ template <int DH>
 cudaError_t launch(const ExtArgs& A, const ExtMaps& maps, cudaStream_t st) {
   using C = Cfg<DH>;
   auto kernel = extend_tc_kernel<DH>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  static std::atomic<bool> done[kExtDevices];
+  const cudaError_t e = ext_allow_smem(kernel, C::kSmemBytes, done);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute early;
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -185,9 +185,13 @@ def _positions(rope, positions, rows: int, dev: int):
         return False, 0
     if positions is None:
         raise ValueError("a rotation on several axes wants positions")
+    n = rope.n_axes
     if positions.dim() not in (2, 3):
-        raise ValueError(f"positions must be [rows, {rope.n_axes}] or [B, S, {rope.n_axes}]")
-    return True, _rows(positions.unsqueeze(-2), "positions", torch.int32, rows, 1, rope.n_axes, dev)
+        raise ValueError(f"positions must be [rows, {n}] or [B, S, {n}]")
+    if (positions.dtype == torch.int32 and positions.is_contiguous() and positions.get_device() == dev
+            and positions.shape[-1] == n and positions.numel() == rows * n):
+        return True, n
+    return True, _rows(positions.unsqueeze(-2), "positions", torch.int32, rows, 1, n, dev)
 
 
 def qk_norm_rope_fwd(q, k, prob: Problem, q_weight=None, k_weight=None, rope: Rope | AxisRope | None = None,
