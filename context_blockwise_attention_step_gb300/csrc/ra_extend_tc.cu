@@ -8,8 +8,9 @@
 //   S = Q K^T          tcgen05.mma; the rows of Q, (token, head) with the heads of a group next to
 //                      each other, come by TMA, those of K and V page by page, in boxes of as many
 //                      keys as divide a page and a tile
-//   online softmax     as in the ring's forward: two threads a row, O rescaled only when a row's
-//                      maximum grows by more than 2^8, P = 2^(S scale log2 e - m) as bf16 into TMEM
+//   online softmax     a thread a row, whose 128 scores it holds in registers from one read of TMEM on; O
+//                      rescaled only when a row's maximum grows by more than 2^8, as in the ring's
+//                      forward; P = 2^(S scale log2 e - m) as bf16 into TMEM
 //   O += P V           A = P from TMEM, V from shared memory
 //
 // Two teams of softmax warps, each with a score tile and an accumulator in TMEM, keep the tensor core
@@ -22,8 +23,9 @@
 // Keys that no row of a block sees are not read, and their values in a tile are made 0 before the
 // product (what lies in a page behind a sequence's end may be NaN); their scores are masked.
 //
-// Warp roles (640 threads): 0 = TMA of Q and K (a lane a box), 3 = TMA of V, 1 = TMEM and MMA, 2 = the
-// walk over the pieces, four ahead of the others, 4-11 and 12-19 = the softmax teams.
+// Warp roles (384 threads, so that a thread may have 168 registers): 0 = TMA of Q and K (a lane a box), 3 =
+// TMA of V, 1 = TMEM and MMA, 2 = the walk over the pieces, four ahead of the others, 4-7 and 8-11 = the
+// softmax teams.
 #include "ra_extend.cuh"
 #include "ra_window.cuh"
 
@@ -33,7 +35,7 @@ static __device__ unsigned int g_status_tc[2];  // a wait that ran out; an index
 
 namespace {
 
-constexpr int kThreads = 640;
+constexpr int kThreads = 384;
 constexpr int kSubBytes = 128 * 128;  // 128 rows x 64 bf16: one 128B-swizzled sub-tile
 constexpr int kItems = 4;             // slots of the queue of pieces
 
@@ -47,7 +49,7 @@ struct Cfg {
   static constexpr int kSmemBytes = kOffV + kStages * kTileBytes + 1024;
   static constexpr int kKSteps = DH / 16;
   static constexpr uint32_t kTmemCols = 512;
-  // TMEM columns: S0 | S1 | O0 | O1 (P of team t overwrites columns 32..95 of S_t)
+  // TMEM columns: S0 | S1 | O0 | O1 (P of team t overwrites the first 64 columns of S_t)
   __device__ static constexpr uint32_t col_s(int t) { return t ? 128u : 0u; }
   __device__ static constexpr uint32_t col_o(int t) { return t ? 256u + DH : 256u; }
 };
@@ -56,15 +58,12 @@ struct Shared {
   uint64_t q_full[2], q_empty[2];
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
   uint64_t s_full[2], p_full[2], o_done[2], o_free;
-  uint64_t drain;
-  uint64_t xmax_bar[2][2], sums_bar;
+  uint64_t drain, sums_bar;
   uint64_t item_full[kItems], item_empty[kItems];
   ExtItem item[kItems];  // tiles 0: the end
   uint32_t tmem_base;
   int abort_flag;
-  float xmax[2][2][2][128];      // [team][slot][half][row]: partial row maxima
-  float sum[2][2][2][128];       // [item parity][team][half][row]: partial row sums
-  float max[2][2][128];          // [item parity][team][row]
+  float sum[2][2][128], max[2][2][128];  // [item parity][team][row]: the rows' states, for the other team
 };
 
 // What of key tile `tile` a block sees: keys [0, sinks) and [from, to) of the tile.
@@ -82,25 +81,22 @@ __device__ __forceinline__ TileKeys tile_keys(const ExtArgs& A, const ExtItem& i
   return t;
 }
 
-template <int N>
-__device__ __forceinline__ void tmem_ld_cols(uint32_t addr, float (&v)[N]) {
-  uint32_t r[N];
-  if constexpr (N == 32) tmem_ld32(addr, r); else tmem_ld16(addr, r);
+__device__ __forceinline__ void tmem_ld_cols(uint32_t addr, float (&v)[32]) {
+  uint32_t r[32];
+  tmem_ld32(addr, r);
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
-template <int N>
-__device__ __forceinline__ void store_cols(__nv_bfloat16* dst, const float (&v)[N]) {
+__device__ __forceinline__ void store_cols(__nv_bfloat16* dst, const float (&v)[32]) {
 #pragma unroll
-  for (int q = 0; q < N / 8; ++q)
+  for (int q = 0; q < 4; ++q)
     reinterpret_cast<uint4*>(dst)[q] =
         make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]), pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
                    pack_bf16x2(v[8 * q + 4], v[8 * q + 5]), pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
 }
-template <int N>
-__device__ __forceinline__ void store_cols(float* dst, const float (&v)[N]) {
+__device__ __forceinline__ void store_cols(float* dst, const float (&v)[32]) {
 #pragma unroll
-  for (int q = 0; q < N / 8; ++q) st_global_v8(dst + 8 * q, v + 8 * q);
+  for (int q = 0; q < 4; ++q) st_global_v8(dst + 8 * q, v + 8 * q);
 }
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2,
@@ -177,10 +173,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh.q_full[i], 1);
       mbar_init(&sh.q_empty[i], 1);
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_full[i], 256);
+      mbar_init(&sh.p_full[i], 128);
       mbar_init(&sh.o_done[i], 1);
-      mbar_init(&sh.xmax_bar[i][0], 256);
-      mbar_init(&sh.xmax_bar[i][1], 256);
     }
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&sh.k_full[i], 1);
@@ -188,12 +182,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh.v_full[i], 1);
       mbar_init(&sh.v_empty[i], 1);
     }
-    mbar_init(&sh.o_free, 512);
-    mbar_init(&sh.sums_bar, 512);
+    mbar_init(&sh.o_free, 256);
+    mbar_init(&sh.sums_bar, 256);
     mbar_init(&sh.drain, 1);
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&sh.item_full[i], 1);
-      mbar_init(&sh.item_empty[i], 3 + 512);  // producers, MMA thread, softmax threads
+      mbar_init(&sh.item_empty[i], 3 + 256);  // producers, MMA thread, softmax threads
     }
     sh.abort_flag = 0;
     fence_mbar_init();
@@ -306,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint32_t va = sV + st * C::kTileBytes;
 #pragma unroll
               for (int s = 0; s < 8; ++s)
-                mma_ts(tmem + C::col_o(t), tmem + C::col_s(t) + 32 + 8 * s, sdesc_sw128(va + s * 2048, kSubBytes, 1024),
+                mma_ts(tmem + C::col_o(t), tmem + C::col_s(t) + 8 * s, sdesc_sw128(va + s * 2048, kSubBytes, 1024),
                        idO, (k > 1 || s > 0) ? 1u : 0u);
               if (k == count[t]) tc_commit(&sh.o_done[t]);
               if (!two || t == 1) tc_commit(&sh.v_empty[st]);
@@ -338,18 +332,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------------ softmax + epilogue
-    const int t = (warp - 4) >> 3;
-    const int hf = ((warp - 4) >> 2) & 1;
-    const int quarter = warp & 3;
-    const int row = quarter * 32 + lane;
-    const int c0 = hf * 64;
-    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const int t = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_off + C::col_s(t);
     const uint32_t tO = tmem + lane_off + C::col_o(t);
     const float sl2 = A.scale_log2;
     const uint64_t sl2x2 = f2(sl2, sl2);
     const int tok = row / A.hb, head = row - tok * A.hb;  // of a query tile
-    uint32_t tiles = 0;    // of this team so far: the phases of S and of the exchanges of maxima
+    uint32_t tiles = 0;  // of this team so far: the phase of S
     uint32_t od1_phase = 0;
     int kv = 0;
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
@@ -378,110 +368,79 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = two ? k : 2 * k + t, j = it.j0 + n, tile = ext_tile(it.walk, j), k0 = tile * 128;
         if (!(ok = wait(&sh.s_full[t], tiles & 1))) break;
         tc_fence_after();
-        const uint32_t xs = tiles & 1, xs_phase = (tiles >> 1) & 1;
         ++tiles;
-        if (idle) {  // no rows in this warp: its products are not looked at
-          mbar_arrive(&sh.xmax_bar[t][xs]);
-        } else {
+        if (!idle) {  // (the products of a warp without rows are not looked at)
           const bool full = tile >= full_from && tile < full_to;  // no mask needed
-          uint32_t vis[2] = {0xffffffffu, 0xffffffffu};
+          uint32_t r[4][32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32_nowait(tS + 32 * c, r[c]);
+          tmem_wait_ld();
           if (!full) {
             const int cnt = min(max(hi - k0, 0), 128), sk_t = A.sh[kExtMany].window > 0 && k0 == 0 ? A.sh[kExtMany].sinks : 0;
-            vis[0] = visible_bits(c0, cnt, lo - k0, sk_t);
-            vis[1] = visible_bits(c0 + 32, cnt, lo - k0, sk_t);
-          }
-          // pass 1: partial row max over this half's visible columns, then both halves'
-          uint32_t r2[2][32];
-          tmem_ld32_nowait(tS + c0, r2[0]);
-          tmem_ld32_nowait(tS + c0 + 32, r2[1]);
-          tmem_wait_ld();
-          float mx;
-          {
-            float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            if (full) {
 #pragma unroll
-              for (int h = 0; h < 2; ++h)
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t vis = visible_bits(32 * c, cnt, lo - k0, sk_t);
 #pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                  mq[2 * h] = max3(mq[2 * h], __uint_as_float(r2[h][i]), __uint_as_float(r2[h][i + 1]));
-                  mq[2 * h + 1] = max3(mq[2 * h + 1], __uint_as_float(r2[h][i + 2]), __uint_as_float(r2[h][i + 3]));
-                }
-            } else {
-#pragma unroll
-              for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                  const float v = (vis[h] >> i) & 1u ? __uint_as_float(r2[h][i]) : -INFINITY;
-                  mq[2 * h + (i & 1)] = fmaxf(mq[2 * h + (i & 1)], v);
-                }
+              for (int i = 0; i < 32; ++i)
+                if (!((vis >> i) & 1u)) r[c][i] = 0xff800000u;  // -inf
             }
-            mx = fmaxf(max3(mq[0], mq[1], mq[2]), mq[3]);
           }
-          {
-            sh.xmax[t][xs][hf][row] = mx;
-            mbar_arrive(&sh.xmax_bar[t][xs]);
-            if (!(ok = wait(&sh.xmax_bar[t][xs], xs_phase))) break;
-            mx = fmaxf(mx, sh.xmax[t][xs][hf ^ 1][row]);
+          float mx;
+          {  // independent chains (one chain of dependent max operations is slow)
+            float mq[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              uint32_t (&v)[32] = r[q >> 1];
+              const int i0 = (q & 1) * 16;
+              mq[q] = fmaxf(__uint_as_float(v[i0]), __uint_as_float(v[i0 + 1]));
+#pragma unroll
+              for (int i = 2; i < 16; i += 2) mq[q] = max3(mq[q], __uint_as_float(v[i0 + i]), __uint_as_float(v[i0 + i + 1]));
+            }
+            mx = max3(max3(mq[0], mq[1], mq[2]), max3(mq[3], mq[4], mq[5]), fmaxf(mq[6], mq[7]));
           }
           mx *= sl2;
           const float m_new = fmaxf(m, mx);
           const bool grow = m_new > m + 8.f;  // also true for the first visible key
           const bool need = grow && k > 0 && m != -INFINITY;
-          if (__any_sync(0xffffffffu, need)) {  // rescale this half's output columns
+          if (__any_sync(0xffffffffu, need)) {  // rescale the output so far
             const float alpha = need ? ex2(m - m_new) : 1.f;
 #pragma unroll
-            for (int c = 0; c < DH / 64; ++c) {
-              uint32_t r[32];
-              tmem_ld32(tO + hf * (DH / 2) + c * 32, r);
+            for (int c = 0; c < DH / 16; ++c) {
+              uint32_t o[16];
+              tmem_ld16(tO + c * 16, o);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
-              tmem_st32(tO + hf * (DH / 2) + c * 32, r);
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st16(tO + c * 16, o);
             }
             if (need) l *= alpha;
           }
           if (grow) m = m_new;
           const float mref = (m == -INFINITY) ? 0.f : m;
-          // pass 2: P = 2^(S*scale*log2e - m) as bf16 pairs into S columns [32 + c0/2, +32)
+          // P = 2^(S*scale*log2e - m) as bf16 pairs over the first columns of S, 32 keys at a time: every FMA, then
+          // every exponential, then packing and the sums
           const uint64_t nm2 = f2(-mref, -mref);
-          uint64_t l2 = f2(0.f, 0.f);
-          uint32_t rr[2][32];
-          tmem_ld32_nowait(tS + c0, rr[0]);
-          tmem_ld32_nowait(tS + c0 + 32, rr[1]);
-          tmem_wait_ld();
+          uint64_t la = f2(0.f, 0.f), lb = f2(0.f, 0.f);
 #pragma unroll
-          for (int ch = 0; ch < 2; ++ch) {
-            uint32_t (&r)[32] = rr[ch];
-            uint32_t pk[16];
+          for (int c = 0; c < 4; ++c) {
             uint64_t xv[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-              xv[i] = fma2(f2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), sl2x2, nm2);
-            float ev[32];
+              xv[i] = fma2(f2(__uint_as_float(r[c][2 * i]), __uint_as_float(r[c][2 * i + 1])), sl2x2, nm2);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const float2 e = f2_split(xv[i]);
-              ev[2 * i] = ex2(e.x);
-              ev[2 * i + 1] = ex2(e.y);
+              xv[i] = f2(ex2(e.x), ex2(e.y));
             }
-            if (!full) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!((vis[ch] >> i) & 1u)) ev[i] = 0.f;
-            }
-            uint64_t la = f2(0.f, 0.f);
+            uint32_t pk[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const uint64_t p2 = f2(ev[2 * i], ev[2 * i + 1]);
-              if (i & 1) la = add2(la, p2); else l2 = add2(l2, p2);
-              pk[i] = bf16x2_of(p2);
+              if (i & 1) la = add2(la, xv[i]); else lb = add2(lb, xv[i]);
+              pk[i] = bf16x2_of(xv[i]);
             }
-            l2 = add2(l2, la);
-            tmem_st16(tS + 32 + c0 / 2 + 16 * ch, pk);
+            tmem_st16(tS + 16 * c, pk);
           }
-          {
-            const float2 ls = f2_split(l2);
-            l += ls.x + ls.y;
-          }
+          const float2 ls = f2_split(add2(la, lb));
+          l += ls.x + ls.y;
         }
         // values of keys that no row of the block sees: 0 (the other team's product with this tile
         // comes after this one's)
@@ -493,9 +452,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint8_t* v = smem + C::kOffV + st * C::kTileBytes;
             if (row >= seen.sinks && (row < seen.from || row >= seen.to)) {
 #pragma unroll
-              for (int i = 0; i < DH / 16; ++i)  // this half's 16-byte pieces of the row
-                *reinterpret_cast<uint4*>(v + (DH == 128 ? hf : i / 8) * kSubBytes + row * 128 +
-                                          (DH == 128 ? i : hf * 4 + (i & 3)) * 16) = make_uint4(0u, 0u, 0u, 0u);
+              for (int i = 0; i < DH / 8; ++i)  // 16-byte pieces of the row
+                *reinterpret_cast<uint4*>(v + (i / 8) * kSubBytes + row * 128 + (i % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
             }
             fence_proxy_async_smem();
           }
@@ -508,8 +466,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       kv += N;
       // epilogue: the rows' sums and maxima to everyone
       const int par = kq & 1;
-      sh.sum[par][t][hf][row] = l;
-      if (hf == 0) sh.max[par][t][row] = m;
+      sh.sum[par][t][row] = l;
+      sh.max[par][t][row] = m;
       mbar_arrive(&sh.sums_bar);
       if (!wait(&sh.sums_bar, par)) break;
       if (!wait(&sh.o_done[0], par)) break;
@@ -521,14 +479,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       float M, L, f0 = 1.f, f1 = 0.f;
       if (two) {
         M = m;
-        L = l + sh.sum[par][t][hf ^ 1][row];
+        L = l;
       } else {
         const float m0 = sh.max[par][0][row], m1 = sh.max[par][1][row];
         M = fmaxf(m0, m1);
         const float ref = M == -INFINITY ? 0.f : M;
         f0 = ex2(m0 - ref);
         f1 = ex2(m1 - ref);
-        L = f0 * (sh.sum[par][0][0][row] + sh.sum[par][0][1][row]) + f1 * (sh.sum[par][1][0][row] + sh.sum[par][1][1][row]);
+        L = f0 * sh.sum[par][0][row] + f1 * sh.sum[par][1][row];
       }
       const int dest = it.dest;
       const int64_t at = static_cast<int64_t>(it.tok0 + tk) * A.hq + it.hk * A.group + it.g0 + head;  // (token, head)
@@ -538,47 +496,50 @@ __global__ void __launch_bounds__(kThreads, 1)
                                             : static_cast<int64_t>(it.slot) * A.part[kExtMany].rows + tk * A.hb + head;
       float* fo = (dest == kExtRows ? A.row_o : A.part[kExtMany].o) + to * DH;
       __nv_bfloat16* bo = static_cast<__nv_bfloat16*>(A.out) + to * DH;
-      const bool lead = two ? hf == 0 : hf == 0 && t == 0;
+      const bool lead = two || t == 0;
       if (valid && lead) {
         if (dest == kExtFinal) A.lse[at] = L > 0.f ? (M + lg2(L)) * 0.69314718055994531f : -INFINITY;
         else (dest == kExtRows ? A.row_ml : A.part[kExtMany].ml)[to] = make_float2(M, L);
       }
       if (two) {
 #pragma unroll
-        for (int c = 0; c < DH / 64; ++c) {
-          const int col = hf * (DH / 2) + c * 32;
+        for (int c = 0; c < DH / 32; ++c) {
+          const int col = c * 32;
           float v[32];
-          tmem_ld_cols<32>(tO + col, v);
+          tmem_ld_cols(tO + col, v);
           if (valid) {
             if (dest == kExtFinal) {
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] *= inv;
-              store_cols<32>(bo + col, v);
+              store_cols(bo + col, v);
             } else {
-              store_cols<32>(fo + col, v);
+              store_cols(fo + col, v);
             }
           }
         }
       } else {
-        constexpr int W = DH / 4;  // columns of a thread
-        const int col = (2 * t + hf) * W;
-        float v[W];
-        tmem_ld_cols<W>(tmem + lane_off + C::col_o(0) + col, v);
+        // half the columns each
 #pragma unroll
-        for (int i = 0; i < W; ++i) v[i] *= f0;
-        if (count1 > 0) {
-          float u[W];
-          tmem_ld_cols<W>(tmem + lane_off + C::col_o(1) + col, u);
+        for (int c = 0; c < DH / 64; ++c) {
+          const int col = t * (DH / 2) + c * 32;
+          float v[32];
+          tmem_ld_cols(tmem + lane_off + C::col_o(0) + col, v);
 #pragma unroll
-          for (int i = 0; i < W; ++i) v[i] += f1 * u[i];
-        }
-        if (valid) {
-          if (dest == kExtFinal) {
+          for (int i = 0; i < 32; ++i) v[i] *= f0;
+          if (count1 > 0) {
+            float u[32];
+            tmem_ld_cols(tmem + lane_off + C::col_o(1) + col, u);
 #pragma unroll
-            for (int i = 0; i < W; ++i) v[i] *= inv;
-            store_cols<W>(bo + col, v);
-          } else {
-            store_cols<W>(fo + col, v);
+            for (int i = 0; i < 32; ++i) v[i] += f1 * u[i];
+          }
+          if (valid) {
+            if (dest == kExtFinal) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] *= inv;
+              store_cols(bo + col, v);
+            } else {
+              store_cols(fo + col, v);
+            }
           }
         }
       }
