@@ -369,6 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = wait(&sh.s_full[t], tiles & 1))) break;
         tc_fence_after();
         ++tiles;
+        uint64_t sum = f2(0.f, 0.f);
         if (!idle) {  // (the products of a warp without rows are not looked at)
           const bool full = tile >= full_from && tile < full_to;  // no mask needed
           uint32_t r[4][32];
@@ -405,12 +406,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (__any_sync(0xffffffffu, need)) {  // rescale the output so far
             const float alpha = need ? ex2(m - m_new) : 1.f;
 #pragma unroll
-            for (int c = 0; c < DH / 16; ++c) {
-              uint32_t o[16];
-              tmem_ld16(tO + c * 16, o);
+            for (int c = 0; c < DH / 8; ++c) {  // (in pieces that leave the scores their registers)
+              uint32_t o[8];
+              tmem_ld8(tO + c * 8, o);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-              tmem_st16(tO + c * 16, o);
+              for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st8(tO + c * 8, o);
             }
             if (need) l *= alpha;
           }
@@ -439,8 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tmem_st16(tS + 16 * c, pk);
           }
-          const float2 ls = f2_split(add2(la, lb));
-          l += ls.x + ls.y;
+          sum = add2(la, lb);
         }
         // values of keys that no row of the block sees: 0 (the other team's product with this tile
         // comes after this one's)
@@ -461,6 +461,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&sh.p_full[t]);
+        const float2 s2 = f2_split(sum);
+        l += s2.x + s2.y;
       }
       if (!ok) break;
       kv += N;
