@@ -66,6 +66,12 @@ struct Shared {
   float sum[2][2][128], max[2][2][128];  // [item parity][team][row]: the rows' states, for the other team
 };
 
+__device__ __forceinline__ bool elect_one() {
+  uint32_t x;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(x));
+  return x != 0;
+}
+
 // What of key tile `tile` a block sees: keys [0, sinks) and [from, to) of the tile.
 struct TileKeys {
   int sinks, from, to;
@@ -163,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Shared sh;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // (the same in a warp's lanes)
   volatile int* abort_flag = &sh.abort_flag;
   unsigned int* status = g_status_tc;
   const uint64_t tmo = A.timeout_ns;
@@ -264,58 +270,67 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      int kv = 0, qt = 0;
-      uint32_t p_phase[2] = {0, 0}, of_phase = 0;
-      const uint32_t idS = idesc_bf16_f32(128, 128, 0, 0);
-      const uint32_t idO = idesc_bf16_f32(128, DH, 0, 1);
-      const uint32_t sQ = smem_u32(smem), sK = smem_u32(smem + C::kOffK), sV = smem_u32(smem + C::kOffV);
-      auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return mbar_wait(bar, parity, abort_flag, tmo, status); };
-      bool ok = true;
-      for (int kq = 0; ok; ++kq) {
-        const int slot = kq % kItems;
-        if (!(ok = wait(&sh.item_full[slot], (kq / kItems) & 1))) break;
-        const int N = sh.item[slot].tiles;
-        const bool two = sh.item[slot].two != 0;
-        mbar_arrive(&sh.item_empty[slot]);
-        if (N == 0) break;
-        for (int t = 0; t < (two ? 2 : 1) && ok; ++t) ok = wait(&sh.q_full[(qt + t) & 1], ((qt + t) >> 1) & 1);
-        if (!ok) break;
-        tc_fence_after();
-        // team t's k-th key tile is n; O_t(k-1) before S_t(k)
-        const int count[2] = {two ? N : (N + 1) / 2, two ? N : N / 2};
-        for (int k = 0; k <= count[0] && ok; ++k) {
-          for (int t = 0; t < 2; ++t) {
-            if (k >= 1 && k - 1 < count[t]) {
-              const int n = two ? k - 1 : 2 * (k - 1) + t, c = kv + n, st = c % C::kStages;
-              if (!two || t == 0)
-                if (!(ok = wait(&sh.v_full[st], (c / C::kStages) & 1))) break;
-              if (!(ok = wait(&sh.p_full[t], p_phase[t]))) break;
-              p_phase[t] ^= 1;
-              if (k == 1 && t == 0) {  // both accumulators have been read
-                if (!(ok = wait(&sh.o_free, of_phase ^ 1))) break;
-                of_phase ^= 1;
-              }
-              tc_fence_after();
-              const uint32_t va = sV + st * C::kTileBytes;
+    // The whole warp walks, with values that are the same in all lanes (they stay in uniform registers,
+    // where the products want their descriptors), and one lane issues.
+    const bool leader = elect_one();
+    int kv = 0, qt = 0;
+    uint32_t p_phase[2] = {0, 0}, of_phase = 0;
+    const uint32_t idS = idesc_bf16_f32(128, 128, 0, 0);
+    const uint32_t idO = idesc_bf16_f32(128, DH, 0, 1);
+    const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint64_t dQ = sdesc_sw128(smem_u32(smem), 16, 1024), dK = sdesc_sw128(smem_u32(smem + C::kOffK), 16, 1024),
+                   dV = sdesc_sw128(smem_u32(smem + C::kOffV), kSubBytes, 1024);
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, tmo, status));
+    };
+    bool ok = true;
+    for (int kq = 0; ok; ++kq) {
+      const int slot = kq % kItems;
+      if (!(ok = wait(&sh.item_full[slot], (kq / kItems) & 1))) break;
+      const int N = __shfl_sync(0xffffffffu, sh.item[slot].tiles, 0);
+      const bool two = __shfl_sync(0xffffffffu, sh.item[slot].two, 0) != 0;
+      if (leader) mbar_arrive(&sh.item_empty[slot]);
+      if (N == 0) break;
+      for (int t = 0; t < (two ? 2 : 1) && ok; ++t) ok = wait(&sh.q_full[(qt + t) & 1], ((qt + t) >> 1) & 1);
+      if (!ok) break;
+      tc_fence_after();
+      // team t's k-th key tile is n; O_t(k-1) before S_t(k)
+      const int count0 = two ? N : (N + 1) / 2, count1 = two ? N : N / 2;
+      for (int k = 0; k <= count0 && ok; ++k) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int count = t ? count1 : count0;
+          if (ok && k >= 1 && k - 1 < count) {
+            const int n = two ? k - 1 : 2 * (k - 1) + t, c = kv + n, st = c % C::kStages;
+            if (!two || t == 0) ok = wait(&sh.v_full[st], (c / C::kStages) & 1);
+            ok = ok && wait(&sh.p_full[t], p_phase[t]);
+            p_phase[t] ^= 1;
+            if (t == 0 && k == 1) {  // both accumulators have been read
+              ok = ok && wait(&sh.o_free, of_phase ^ 1);
+              of_phase ^= 1;
+            }
+            tc_fence_after();
+            if (ok && leader) {
+              const uint64_t dv = dV + st * (C::kTileBytes >> 4);
 #pragma unroll
               for (int s = 0; s < 8; ++s)
-                mma_ts(tmem + C::col_o(t), tmem + C::col_s(t) + 8 * s, sdesc_sw128(va + s * 2048, kSubBytes, 1024),
-                       idO, (k > 1 || s > 0) ? 1u : 0u);
-              if (k == count[t]) tc_commit(&sh.o_done[t]);
+                mma_ts(base + C::col_o(t), base + C::col_s(t) + 8 * s, dv + s * (2048 >> 4), idO,
+                       (k > 1 || s > 0) ? 1u : 0u);
+              if (k == count) tc_commit(&sh.o_done[t]);
               if (!two || t == 1) tc_commit(&sh.v_empty[st]);
             }
-            if (k < count[t]) {
-              const int n = two ? k : 2 * k + t, c = kv + n, st = c % C::kStages;
-              if (!two || t == 0)
-                if (!(ok = wait(&sh.k_full[st], (c / C::kStages) & 1))) break;
-              tc_fence_after();
+          }
+          if (ok && k < count) {
+            const int n = two ? k : 2 * k + t, c = kv + n, st = c % C::kStages;
+            if (!two || t == 0) ok = wait(&sh.k_full[st], (c / C::kStages) & 1);
+            tc_fence_after();
+            if (ok && leader) {
               const int qs = (qt + (two ? t : 0)) & 1;
-              const uint32_t qa = sQ + qs * C::kTileBytes, ka = sK + st * C::kTileBytes;
+              const uint64_t dq = dQ + qs * (C::kTileBytes >> 4), dk = dK + st * (C::kTileBytes >> 4);
 #pragma unroll
               for (int s = 0; s < C::kKSteps; ++s) {
-                const uint32_t off = (s >> 2) * kSubBytes + (s & 3) * 32;
-                mma_ss(tmem + C::col_s(t), sdesc_sw128(qa + off, 16, 1024), sdesc_sw128(ka + off, 16, 1024), idS, s > 0);
+                const int off = ((s >> 2) * kSubBytes + (s & 3) * 32) >> 4;
+                mma_ss(base + C::col_s(t), dq + off, dk + off, idS, s > 0);
               }
               tc_commit(&sh.s_full[t]);
               if (!two || t == 1) tc_commit(&sh.k_empty[st]);
@@ -323,13 +338,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        kv += N;
-        qt += two ? 2 : 1;
       }
-      // let every MMA issued so far finish before TMEM is released
+      kv += N;
+      qt += two ? 2 : 1;
+    }
+    // let every MMA issued so far finish before TMEM is released
+    if (leader) {
       tc_commit(&sh.drain);
       mbar_wait(&sh.drain, 0, abort_flag, tmo, status);
     }
+    __syncwarp();
   } else if (warp >= 4) {
     // ------------------------------------------------------------------ softmax + epilogue
     const int t = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
