@@ -771,6 +771,16 @@ int few_rows_of(const ra_paged_cache* c, bool decode, int n_tokens, int hq) {
   return rows <= 8 ? 8 : 16;
 }
 
+// One new token of every sequence, and so small a cache that the attention of one token (ra_decode.cu),
+// which reads every sequence's keys by itself and has half the launches, is faster, whatever the
+// sequences share. Measured with one prefix (32/8 heads of 128, bf16; us apart and shared): 16 sequences of
+// 2048 keys, 138 MB, 28 and 39; 16 of 4096, 273 MB, 39 and 37; 32 of 4096, 545 MB, 68 and 39. float32, 16/4
+// heads of 64: 32 of 2048, 138 MB, 39 and 45; 32 of 4096, 273 MB, 61 and 57.
+bool read_apart(const ra_paged_cache* c) {
+  const double keys = static_cast<double>(c->n_seqs) * c->max_pages * c->page_size;
+  return keys * c->hkv * c->head_dim * (c->dtype == RA_BF16 ? 2 : 4) * 2 <= 256e6;
+}
+
 // The workspace's regions, one after the other.
 struct Regions {
   size_t segs, starts[2], part_o[2], part_ml[2], row_o, row_ml, total;
@@ -800,6 +810,8 @@ Regions regions_of(const ra_paged_cache* c, int n_groups, int n_tokens, int hq) 
   r.row_o = at;
   r.row_ml = r.row_o + up(rows * c->head_dim * 4);
   r.total = r.row_ml + up(rows * 8);
+  const size_t apart = ra_paged_workspace_bytes(c, hq);  // (see read_apart)
+  if (r.total < apart) r.total = apart;
   return r;
 }
 
@@ -865,6 +877,8 @@ extern "C" int ra_paged_attn_extend(const ra_paged_cache* c, const ra_shared_pre
   if (workspace == nullptr || reinterpret_cast<uintptr_t>(workspace) % 256)
     return record_error(RA_ERR_INVALID_ARG, "workspace must be a 256-byte aligned device pointer");
   if (!some) return record_error(RA_OK, "%s", "");
+  if (cu_new == nullptr && (n_groups == 0 || read_apart(c)))
+    return ra_paged_attn_decode(c, hq, scale, window, sinks, q, seq_lens, out, lse, workspace, workspace_bytes, stream);
   if (c->dtype == RA_BF16) {
     const uintptr_t p = reinterpret_cast<uintptr_t>(c->k_pages) | reinterpret_cast<uintptr_t>(c->v_pages) |
                         reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out);
@@ -922,10 +936,8 @@ extern "C" int ra_paged_attn_extend(const ra_paged_cache* c, const ra_shared_pre
   ExtMaps maps;
   if (c->dtype == RA_BF16 && (e = make_extend_maps(&maps, c, &A)) != cudaSuccess)
     return record_error(RA_ERR_UNSUPPORTED, "the pages' strides do not fit a tensor map");
-  // the kernels that can have work: one new token of every sequence and nothing shared is few rows
-  // unless a K/V head has many query heads
-  const bool many = A.few_rows == 0 || (static_cast<int64_t>(n_tokens) * A.group > A.few_rows &&
-                                        (cu_new != nullptr || n_groups > 0 || A.group > A.few_rows));
+  // the kernels that can have work
+  const bool many = A.few_rows == 0 || static_cast<int64_t>(n_tokens) * A.group > A.few_rows;
   const bool few = A.few_rows > 0;
   A.first = few ? kExtFew : kExtMany;
   extend_plan<<<1, kPlanThreads, 0, st>>>(A);

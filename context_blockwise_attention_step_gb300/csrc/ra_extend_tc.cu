@@ -57,7 +57,7 @@ struct Cfg {
 struct Shared {
   uint64_t q_full[2], q_empty[2];
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
-  uint64_t s_full[2], p_full[2], o_done[2], o_free;
+  uint64_t s_full[2], p_part[2], p_full[2], o_done[2], o_free;  // p_part: three quarters of P
   uint64_t drain, sums_bar;
   uint64_t item_full[kItems], item_empty[kItems];
   ExtItem item[kItems];  // tiles 0: the end
@@ -171,6 +171,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                                              ~static_cast<uintptr_t>(1023));
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // (the same in a warp's lanes)
   volatile int* abort_flag = &sh.abort_flag;
+  if (A.first == kExtFew) {  // the plan is there: a CTA without work has nothing to set up
+    launch_dependents();
+    if (!ext_acquire(A.head, A.timeout_ns, g_status_tc) || static_cast<int>(blockIdx.x) >= A.head->ctas[kExtMany]) {
+      wait_for_previous();
+      return;
+    }
+  }
   unsigned int* status = g_status_tc;
   const uint64_t tmo = A.timeout_ns;
 
@@ -179,6 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh.q_full[i], 1);
       mbar_init(&sh.q_empty[i], 1);
       mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_part[i], 128);
       mbar_init(&sh.p_full[i], 128);
       mbar_init(&sh.o_done[i], 1);
     }
@@ -210,8 +218,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (A.first == kExtMany) wait_for_previous();
-  launch_dependents();
+  if (A.first == kExtMany) {
+    wait_for_previous();
+    launch_dependents();
+  }
   const uint32_t tmem = sh.tmem_base;
 
   if (warp == 2) {
@@ -303,8 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ok && k >= 1 && k - 1 < count) {
             const int n = two ? k - 1 : 2 * (k - 1) + t, c = kv + n, st = c % C::kStages;
             if (!two || t == 0) ok = wait(&sh.v_full[st], (c / C::kStages) & 1);
-            ok = ok && wait(&sh.p_full[t], p_phase[t]);
-            p_phase[t] ^= 1;
+            ok = ok && wait(&sh.p_part[t], p_phase[t]);
             if (t == 0 && k == 1) {  // both accumulators have been read
               ok = ok && wait(&sh.o_free, of_phase ^ 1);
               of_phase ^= 1;
@@ -313,9 +322,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok && leader) {
               const uint64_t dv = dV + st * (C::kTileBytes >> 4);
 #pragma unroll
-              for (int s = 0; s < 8; ++s)
+              for (int s = 0; s < 6; ++s)
                 mma_ts(base + C::col_o(t), base + C::col_s(t) + 8 * s, dv + s * (2048 >> 4), idO,
                        (k > 1 || s > 0) ? 1u : 0u);
+            }
+            ok = ok && wait(&sh.p_full[t], p_phase[t]);
+            p_phase[t] ^= 1;
+            tc_fence_after();
+            if (ok && leader) {
+              const uint64_t dv = dV + st * (C::kTileBytes >> 4);
+#pragma unroll
+              for (int s = 6; s < 8; ++s)
+                mma_ts(base + C::col_o(t), base + C::col_s(t) + 8 * s, dv + s * (2048 >> 4), idO, 1u);
               if (k == count) tc_commit(&sh.o_done[t]);
               if (!two || t == 1) tc_commit(&sh.v_empty[st]);
             }
@@ -387,6 +405,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = wait(&sh.s_full[t], tiles & 1))) break;
         tc_fence_after();
         ++tiles;
+        // values of keys that no row of the block sees: 0 (the other team's product with this tile
+        // comes after this one's)
+        if ((!two || t == 0) && (k0 < it.low || k0 + 128 > it.end)) {
+          const TileKeys seen = tile_keys(A, it, j);
+          if (!seen.whole()) {
+            const int c = kv + n, st = c % C::kStages;
+            if (!(ok = wait(&sh.v_full[st], (c / C::kStages) & 1))) break;
+            uint8_t* v = smem + C::kOffV + st * C::kTileBytes;
+            if (row >= seen.sinks && (row < seen.from || row >= seen.to)) {
+#pragma unroll
+              for (int i = 0; i < DH / 8; ++i)  // 16-byte pieces of the row
+                *reinterpret_cast<uint4*>(v + (i / 8) * kSubBytes + row * 128 + (i % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+          }
+        }
         uint64_t sum = f2(0.f, 0.f);
         if (!idle) {  // (the products of a warp without rows are not looked at)
           const bool full = tile >= full_from && tile < full_to;  // no mask needed
@@ -457,24 +491,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               pk[i] = bf16x2_of(xv[i]);
             }
             tmem_st16(tS + 16 * c, pk);
+            if (c == 2) {  // the product with these keys may begin (2 % of the whole)
+              tmem_st_wait();
+              tc_fence_before();
+              mbar_arrive(&sh.p_part[t]);
+            }
           }
           sum = add2(la, lb);
-        }
-        // values of keys that no row of the block sees: 0 (the other team's product with this tile
-        // comes after this one's)
-        if ((!two || t == 0) && (k0 < it.low || k0 + 128 > it.end)) {
-          const TileKeys seen = tile_keys(A, it, j);
-          if (!seen.whole()) {
-            const int c = kv + n, st = c % C::kStages;
-            if (!(ok = wait(&sh.v_full[st], (c / C::kStages) & 1))) break;
-            uint8_t* v = smem + C::kOffV + st * C::kTileBytes;
-            if (row >= seen.sinks && (row < seen.from || row >= seen.to)) {
-#pragma unroll
-              for (int i = 0; i < DH / 8; ++i)  // 16-byte pieces of the row
-                *reinterpret_cast<uint4*>(v + (i / 8) * kSubBytes + row * 128 + (i % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
-            }
-            fence_proxy_async_smem();
-          }
+        } else {
+          mbar_arrive(&sh.p_part[t]);
         }
         tmem_st_wait();
         tc_fence_before();

@@ -18,6 +18,7 @@ from oracle import heads as H
 pytestmark = pytest.mark.gpu
 
 BF16, F32 = torch.bfloat16, torch.float32
+BIG = 260_000_000  # bytes: no small cache
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -35,16 +36,18 @@ class Batch:
     """Sequences in a paged cache. news, lens: new tokens and lengths with them; groups: list of
     (number of sequences, prefix length): their first tokens are equal, and in the same pages as far as
     these are whole. NaN wherever nobody may look: behind a sequence's end, in pages of nobody, and
-    (with a window) in pages that no row sees."""
+    (with a window) in pages that no row sees. capacity: rows of the block table that make the cache this many
+    bytes at most (a small one is read sequence by sequence in decoding steps)."""
 
     def __init__(self, seed, dtype, hq, hkv, dh, page, lens, news=None, groups=(), order="pshd", window=0, sinks=0,
-                 scale=1.0):
+                 scale=1.0, capacity=0):
         self.rng = rng = np.random.default_rng(seed)
         self.dtype, self.hq, self.hkv, self.dh, self.page = dtype, hq, hkv, dh, page
         self.lens, self.news = list(lens), [1] * len(lens) if news is None else list(news)
         self.window, self.sinks = window, sinks
         n_seqs = len(lens)
         width = max(1, max(-(-n // page) for n in lens)) + 1
+        width = max(width, -(-capacity // (n_seqs * page * hkv * dh * 2 * (2 if dtype == BF16 else 4))) + 1)
         table = np.full((n_seqs, width), 1 << 30, np.int64)  # a bad page: entries that nobody may look at
         kv = [(self._randn(max(n, 1), hkv, dh), self._randn(max(n, 1), hkv, dh)) for n in lens]
         self.cu_groups, self.prefix_lens, at = [0], [], 0
@@ -193,7 +196,7 @@ def test_shared_prefixes(case):
     dt, hq, hkv, dh, page, groups, own, news = case
     prefix = [p for m, p in groups for _ in range(m)]
     lens = [p + n if n else 0 for p, n in zip(prefix, own)]
-    b = Batch(2, dt, hq, hkv, dh, page, lens, news, groups=groups)
+    b = Batch(2, dt, hq, hkv, dh, page, lens, news, groups=groups, capacity=BIG)
     ref = b.reference()
     how = {} if news else {"cu_new": None}
     out, lse = b.run(**how)
@@ -201,5 +204,9 @@ def test_shared_prefixes(case):
     again = b.run(**how)
     assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
     b.check(*b.run(shared=None, **how), ref, "nothing shared")
-    if not news:  # one token each: the decode call's own form
+    if not news:
+        if all(own):  # (offsets give an idle sequence no row)
+            b.check(*b.run(shared=None), ref, "one token each, by offsets")
         b.check(*ra.paged_attn_decode(b.q, b.cache, b.seq_lens, shared=b.shared), ref, "decode")
+        small = Batch(2, dt, hq, hkv, dh, page, lens, news, groups=groups)
+        b.check(*ra.paged_attn_decode(small.q, small.cache, small.seq_lens, shared=small.shared), ref, "a small cache")
