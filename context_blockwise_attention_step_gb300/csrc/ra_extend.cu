@@ -26,7 +26,7 @@ static __device__ unsigned int g_status_extend;  // an index outside the cache
 namespace {
 
 // ---------------------------------------------------------------- planning
-constexpr int kPlanThreads = 512, kPlanWarps = kPlanThreads / 32;
+constexpr int kPlanThreads = 640, kPlanWarps = kPlanThreads / 32;
 
 struct Tokens {
   int t0, n, len;
@@ -214,10 +214,13 @@ __global__ void __launch_bounds__(kPlanThreads, 1) extend_plan(const __grid_cons
   for (int k = tid; k < ctas[0] + ctas[1] + 2; k += kPlanThreads) {
     const int c = k <= ctas[0] ? 0 : 1, cta = c == 0 ? k : k - ctas[0] - 1, n = c == 0 ? ctas[0] : ctas[1];
     const int64_t all = c == 0 ? done[0] : done[1];
-    ExtStart& to = A.starts[c][cta];
+    ExtStart to = {};
     const int64_t u0 = cta < n ? ext_first(all, n, cta) : all;
     to.u0 = u0;
-    if (cta == n) continue;
+    if (cta == n) {
+      A.starts[c][cta] = to;
+      continue;
+    }
     int lo = 0, hi = segs - 1;  // the last segment that begins at u0 or before
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -232,7 +235,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) extend_plan(const __grid_cons
     to.hk = pair / A.blocks_per_kv;
     to.hblk = pair - to.hk * A.blocks_per_kv;
     to.blk = blk;
-    to.g = g;
+    A.starts[c][cta] = to;
   }
   __syncthreads();
   if (tid == 0) ext_publish(A.head);

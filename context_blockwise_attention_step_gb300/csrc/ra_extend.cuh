@@ -112,7 +112,7 @@ struct ExtCursor {
     hk = s.hk;
     hblk = s.hblk;
     blk = s.blk;
-    g = s.g;
+    g = A.segs[seg];
     blocks = ext_blocks(A.sh[CLS], g.n);
     return true;
   }

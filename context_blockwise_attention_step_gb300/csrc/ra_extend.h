@@ -58,7 +58,6 @@ RA_HD int64_t ext_div(int64_t a, int64_t b) {
 struct ExtStart {
   int64_t u0, base;  // base: the block's first unit (u1 is the next CTA's u0)
   int32_t seg, hk, hblk, blk;
-  ExtSeg g;
 };
 
 // Tiles of a block: walk index j is tile j for j < ns (first tokens before the window), else
