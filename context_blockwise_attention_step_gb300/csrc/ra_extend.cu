@@ -211,13 +211,14 @@ __global__ void __launch_bounds__(kPlanThreads, 1) extend_plan(const __grid_cons
   }
   __syncthreads();
   // where each CTA begins
-  for (int k = tid; k < ctas[0] + ctas[1] + 2; k += kPlanThreads) {
-    const int c = k <= ctas[0] ? 0 : 1, cta = c == 0 ? k : k - ctas[0] - 1, n = c == 0 ? ctas[0] : ctas[1];
+  const int most = A.part[0].most_ctas;
+  for (int k = tid; k < most + A.part[1].most_ctas + 2; k += kPlanThreads) {
+    const int c = k <= most ? 0 : 1, cta = c == 0 ? k : k - most - 1, n = c == 0 ? ctas[0] : ctas[1];
     const int64_t all = c == 0 ? done[0] : done[1];
     ExtStart to = {};
     const int64_t u0 = cta < n ? ext_first(all, n, cta) : all;
     to.u0 = u0;
-    if (cta == n) {
+    if (cta >= n) {
       A.starts[c][cta] = to;
       continue;
     }
@@ -458,10 +459,10 @@ struct Cut {
   int c0, c1, cls;
   int tok0;  // token row of its first row
 };
-__device__ __forceinline__ Cut cut_of(const ExtArgs& A, const ExtSeg& g, int pair, int blk) {
+__device__ __forceinline__ Cut cut_of(const ExtArgs& A, const ExtHead& head, const ExtSeg& g, int pair, int blk) {
   const ExtShape& sh = A.sh[g.cls];
-  const int64_t units = A.head->units[g.cls];
-  const int ctas = A.head->ctas[g.cls];
+  const int64_t units = g.cls == kExtMany ? head.units[0] : head.units[1];
+  const int ctas = g.cls == kExtMany ? head.ctas[0] : head.ctas[1];
   const int64_t base = ext_unit0(g, g.cls) + pair * g.units + ext_units_before(sh, g, blk);
   Cut c;
   c.cls = g.cls;
@@ -496,11 +497,12 @@ __global__ void __launch_bounds__(kJoinThreads, BULK ? 2 : 4) extend_join(const 
   const int pairs = A.hkv * A.blocks_per_kv, block = blockIdx.x / pairs, pair = blockIdx.x - block * pairs;
   wait_for_previous();
   if (warp == 0) {
+    const ExtHead head = *A.head;
     int lo = A.n_groups, n = A.n_seqs, blk = -1;
     if (A.cu_new == nullptr) {
       lo += block;  // a block is a sequence
       blk = 0;
-    } else if (block < A.head->own_blocks) {
+    } else if (block < head.own_blocks) {
       // the last segment that begins at the block or before: 32 places at a time
       while (n > 1) {
         const int step = (n + 31) / 32, at = lo + lane * step;
@@ -514,11 +516,11 @@ __global__ void __launch_bounds__(kJoinThreads, BULK ? 2 : 4) extend_join(const 
     if (blk >= 0 && lane < 3) {
       const ExtSeg g = A.segs[lo];
       Cut c = {0, -1, 0, 0};
-      if (lane == 0 && g.units > 0) c = cut_of(A, g, pair, g.cls == kExtFew ? 0 : blk);
+      if (lane == 0 && g.units > 0) c = cut_of(A, head, g, pair, g.cls == kExtFew ? 0 : blk);
       if (lane > 0 && g.prefix >= 0) {
         const ExtSeg p = A.segs[g.prefix];
         const int i = (g.t0 + blk * bt - p.t0) / A.sh[p.cls].bt + lane - 1;
-        if (i < ext_blocks(A.sh[p.cls], p.n)) c = cut_of(A, p, pair, i);
+        if (i < ext_blocks(A.sh[p.cls], p.n)) c = cut_of(A, head, p, pair, i);
       }
       sh_cut[lane] = c;
       if (lane == 0) sh_seg = g;
@@ -833,16 +835,15 @@ int check_extend(const ra_paged_cache* c, int n_groups, int n_tokens, int hq) {
 
 cudaError_t extend_status(unsigned int value[2], bool reset) {
   unsigned int index = 0;
-  unsigned int few[2] = {0, 0};
+  unsigned int few = 0;
   cudaError_t e = extend_tc_status(value, reset);
-  if (e == cudaSuccess) e = extend_few_status(few, reset);
+  if (e == cudaSuccess) e = extend_few_status(&few, reset);
   if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&index, g_status_extend, sizeof index);
   if (e == cudaSuccess && reset) {
     const unsigned int zero = 0;
     e = cudaMemcpyToSymbol(g_status_extend, &zero, sizeof zero);
   }
-  value[0] |= few[0];
-  value[1] |= index | few[1];
+  value[1] |= index | few;
   return e;
 }
 
@@ -941,11 +942,9 @@ extern "C" int ra_paged_attn_extend(const ra_paged_cache* c, const ra_shared_pre
     return record_error(RA_ERR_UNSUPPORTED, "the pages' strides do not fit a tensor map");
   // the kernels that can have work
   const bool many = A.few_rows == 0 || static_cast<int64_t>(n_tokens) * A.group > A.few_rows;
-  const bool few = A.few_rows > 0;
-  A.first = few ? kExtFew : kExtMany;
   extend_plan<<<1, kPlanThreads, 0, st>>>(A);
   e = cudaGetLastError();
-  if (e == cudaSuccess && few) e = launch_extend_few(A, st);
+  if (e == cudaSuccess && A.few_rows > 0) e = launch_extend_few(A, st);
   if (e == cudaSuccess && many) e = c->dtype == RA_BF16 ? launch_extend_tc(A, maps, st) : launch_extend_simt(A, st);
   if (e == cudaSuccess) {
     // at most one block of a sequence has fewer tokens than the others

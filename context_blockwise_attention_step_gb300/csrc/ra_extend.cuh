@@ -22,11 +22,12 @@ struct ExtHead {
   uint32_t ready;  // set when the rest and the segments are there
 };
 
-// The kernels of a call and what they wait for. The planning kernel comes first. Of the two main
-// kernels the first one waits for its end, and only then lets the other one start, which has the plan
-// too, then, and need not wait for the first to end: it takes the SMs that the first leaves free. (The
-// flag that it reads first orders its reads of the plan behind the plan's writes.) It ends after the
-// first has ended, so that the join, which waits for its end, has both kernels' results.
+// The kernels of a call and what they wait for. The planning kernel comes first. The kernel for few rows
+// waits for its end, and only then lets the one for many rows start, which has the plan too, then, and
+// need not wait for the other to end: it takes the SMs that the other leaves free. (The flag that it
+// reads first orders its reads of the plan behind the plan's writes.) It ends after the other has
+// ended, so that the join, which waits for its end, has both kernels' results. A kernel that is alone
+// waits for the plan.
 __device__ __forceinline__ void ext_publish(ExtHead* h) {
   __threadfence();
   asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(&h->ready), "r"(1u) : "memory");
@@ -66,14 +67,13 @@ struct ExtArgs {
   int32_t hb, blocks_per_kv;   // query heads of a block (the last one may have fewer), blocks of a K/V head
   int32_t box_rows, ord[3];    // tensor-core kernel: keys of a copy; places of head, slot, page in the map
   ExtShape sh[2];              // of each class
-  int32_t first;               // the class whose kernel comes first
-  int32_t few_rows;            // most rows a K/V head of a segment of few rows; 0: that class is not used
+  int32_t few_rows;            // most rows a K/V head of a segment of few rows; 0: that kernel does not run
   ExtParts part[2];
   float scale_log2;
   uint64_t timeout_ns;
   ExtHead* head;
   ExtSeg* segs;
-  ExtStart* starts[2];         // of each class's CTAs, and of one behind the last (u0 alone)
+  ExtStart* starts[2];         // of each class's most_ctas CTAs (u0 alone without work), and of one behind the last
   float* row_o;                // results like a part's, of whole blocks that are joined: [2][n_tokens][hq][dh]
   float2* row_ml;
   void* out;
@@ -101,12 +101,13 @@ struct ExtCursor {
   ExtSeg g;
   int cta, seg, hk, hblk, blk, blocks;
 
+  // False for a CTA without work.
   __device__ __forceinline__ bool begin(const ExtArgs& A, int which) {
-    if (which >= A.head->ctas[CLS]) return false;
-    const ExtStart& s = A.starts[CLS][which];
+    const ExtStart s = A.starts[CLS][which];
     cta = which;
     u0 = s.u0;
-    u1 = (&s + 1)->u0;
+    u1 = A.starts[CLS][which + 1].u0;
+    if (u0 == u1) return false;
     base = s.base;
     seg = s.seg;
     hk = s.hk;
@@ -195,6 +196,6 @@ cudaError_t extend_tc_status(unsigned int value[2], bool reset);  // as extend_s
 // The kernel of the segments of few rows, bf16.
 int extend_few_ctas(int head_dim);  // most CTAs
 cudaError_t launch_extend_few(const ExtArgs& A, cudaStream_t st);
-cudaError_t extend_few_status(unsigned int value[2], bool reset);
+cudaError_t extend_few_status(unsigned int* value, bool reset);
 
 }  // namespace ra

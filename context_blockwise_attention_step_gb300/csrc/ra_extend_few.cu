@@ -16,7 +16,7 @@
 
 namespace ra {
 
-static __device__ unsigned int g_status_few[2];  // a wait that ran out; an index outside the cache
+static __device__ unsigned int g_status_few;  // an index outside the cache
 
 namespace {
 
@@ -66,12 +66,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<DH>::CTAS) extend_few(const __gr
   constexpr int NS = C::STAGES;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float sm_m[4][16], sm_l[4][16];
-  if (A.first == kExtFew) wait_for_previous();
-  launch_dependents();
-  if (!ext_acquire(A.head, A.timeout_ns, g_status_few) || static_cast<int>(blockIdx.x) >= A.head->ctas[kExtFew]) {
-    wait_for_previous();
-    return;
-  }
+  wait_for_previous();
+  launch_dependents();  // (after it: the kernel for many rows relies on that)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
   const uint32_t ring = smem_u32(smem) + warp * NS * C::STAGE;
   float* joined = reinterpret_cast<float*>(smem + C::RING);  // [4][CHUNK][DH]
@@ -94,7 +90,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DH>::CTAS) extend_few(const __gr
       int key = key0 + (lane & 15);  // a key that is not seen: one that is, in its place
       if (key >= sinks) key = load.j < it.walk.ns ? sinks - 1 : min(max(key, it.low), it.end - 1);
       const int page = key / A.page_size;
-      row = (ext_page(A, it.seq, page, g_status_few + 1) * A.page_stride +
+      row = (ext_page(A, it.seq, page, &g_status_few) * A.page_stride +
              static_cast<int64_t>(key - page * A.page_size) * A.slot_stride + it.hk * A.head_stride) * 2;
     }
     if (load.last()) load.next_item(A); else ++load.j;
@@ -297,7 +293,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<DH>::CTAS) extend_few(const __gr
     }
     at.next_item(A);
   }
-  wait_for_previous();  // what follows in the stream waits for this kernel alone
 }
 
 template <int DH, bool WIDE>
@@ -323,11 +318,11 @@ cudaError_t launch(const ExtArgs& A, cudaStream_t st) {
 
 int extend_few_ctas(int head_dim) { return (head_dim == 128 ? Cfg<128>::CTAS : Cfg<64>::CTAS) * kExtSms; }
 
-cudaError_t extend_few_status(unsigned int value[2], bool reset) {
+cudaError_t extend_few_status(unsigned int* value, bool reset) {
   cudaError_t e = cudaMemcpyFromSymbol(value, g_status_few, sizeof g_status_few);
   if (e == cudaSuccess && reset) {
-    const unsigned int zero[2] = {0, 0};
-    e = cudaMemcpyToSymbol(g_status_few, zero, sizeof zero);
+    const unsigned int zero = 0;
+    e = cudaMemcpyToSymbol(g_status_few, &zero, sizeof zero);
   }
   return e;
 }

@@ -171,9 +171,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                                              ~static_cast<uintptr_t>(1023));
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // (the same in a warp's lanes)
   volatile int* abort_flag = &sh.abort_flag;
-  if (A.first == kExtFew) {  // the plan is there: a CTA without work has nothing to set up
+  if (A.few_rows > 0) {  // the plan is there: a CTA without work has nothing to set up
     launch_dependents();
-    if (!ext_acquire(A.head, A.timeout_ns, g_status_tc) || static_cast<int>(blockIdx.x) >= A.head->ctas[kExtMany]) {
+    if (!ext_acquire(A.head, A.timeout_ns, g_status_tc) ||
+        A.starts[kExtMany][blockIdx.x].u0 == A.starts[kExtMany][blockIdx.x + 1].u0) {
       wait_for_previous();
       return;
     }
@@ -218,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (A.first == kExtMany) {
+  if (A.few_rows == 0) {
     wait_for_previous();
     launch_dependents();
   }
@@ -227,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 2) {
     // ------------------------------------------------------------------ the walk
     ExtCursor<kExtMany> cur;
-    bool more = __all_sync(0xffffffffu, ext_acquire(A.head, tmo, status)) && cur.begin(A, blockIdx.x);
+    bool more = cur.begin(A, blockIdx.x);
     for (int kq = 0;; ++kq) {
       const int slot = kq % kItems;
       const bool ok = mbar_wait(&sh.item_empty[slot], ((kq / kItems) & 1) ^ 1, abort_flag, tmo, status);
