@@ -14,6 +14,7 @@
 // CTAs; the join works on the blocks that need it. The host need not know a length.
 #include <cuda_bf16.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 
@@ -484,7 +485,7 @@ template <> __device__ __forceinline__ void put4<__nv_bfloat16>(__nv_bfloat16* p
 // CTA had it whole and no prefix is shared; 0 and -inf where nothing is seen. A warp takes a row, or
 // where there are few rows a share of its parts: a lane has a part's state, all lanes its sums, four
 // columns each (QUADS), or every 32nd. BULK: where there are more than eight rows, which have few parts
-// each, a warp takes four rows at once, part by part (16 questions of 500 tokens behind 16384 shared
+// each, a warp takes four rows at once, part by part, and few blocks are shared out (y) (16 questions of 500 tokens behind 16384 shared
 // keys, 32/8 heads: 40 us, was 77; its registers leave half the blocks on an SM, which decoding steps
 // would pay for: 64 sequences 19 us in place of 13). Sums are taken in a fixed order.
 template <typename T, bool QUADS, bool BULK>
@@ -593,7 +594,7 @@ __global__ void __launch_bounds__(kJoinThreads, BULK ? 2 : 4) extend_join(const 
   };
   if (BULK && rows > kJoinWarps) {
     constexpr int U = 4;
-    for (int r0 = warp * U; r0 < rows; r0 += kJoinWarps * U) {
+    for (int r0 = (blockIdx.y * kJoinWarps + warp) * U; r0 < rows; r0 += gridDim.y * kJoinWarps * U) {
       float x[U][4] = {}, l[U] = {}, mx[U];
       int64_t at[U];
       int most = 0;
@@ -637,6 +638,7 @@ __global__ void __launch_bounds__(kJoinThreads, BULK ? 2 : 4) extend_join(const 
     }
     return;
   }
+  if (BULK && blockIdx.y > 0) return;
   int split = 1;  // warps of a row
   while (split < kJoinWarps && 2 * split * rows <= kJoinWarps) split *= 2;
   const int share = warp % split, at_once = kJoinWarps / split;
@@ -707,12 +709,12 @@ __global__ void __launch_bounds__(kJoinThreads, BULK ? 2 : 4) extend_join(const 
 }
 
 // ---------------------------------------------------------------- host
-cudaError_t launch_after(const void* kernel, unsigned grid, unsigned threads, size_t smem, cudaStream_t st, void** args) {
+cudaError_t launch_after(const void* kernel, dim3 grid, unsigned threads, size_t smem, cudaStream_t st, void** args) {
   cudaLaunchAttribute early;
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -745,7 +747,7 @@ cudaError_t launch_extend_simt(ExtArgs& A, cudaStream_t st) {
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   void* args[] = {&A, &vec};
-  return launch_after(kernel, A.part[kExtMany].most_ctas, kSimtThreads, smem, st, args);
+  return launch_after(kernel, dim3(A.part[kExtMany].most_ctas), kSimtThreads, smem, st, args);
 }
 
 // Blocks of query heads of one K/V head, as even as can be.
@@ -956,7 +958,10 @@ extern "C" int ra_paged_attn_extend(const ra_paged_cache* c, const ra_shared_pre
     const void* kernel = c->dtype == RA_BF16 ? join_of<__nv_bfloat16, true>(bulk)
                          : quads              ? join_of<float, true>(bulk)
                                               : join_of<float, false>(bulk);
-    e = launch_after(kernel, static_cast<unsigned>(blocks * A.hkv * A.blocks_per_kv), kJoinThreads, 0, st, args);
+    // (two blocks an SM; more, of rows that mostly need no join, would take longer to start than they save)
+    const int64_t all = blocks * A.hkv * A.blocks_per_kv, most_y = (A.part[kExtMany].rows + 31) / 32;
+    const int64_t y = bulk ? std::max<int64_t>(1, std::min<int64_t>(most_y, 4 * sms / all)) : 1;
+    e = launch_after(kernel, dim3(static_cast<unsigned>(all), static_cast<unsigned>(y)), kJoinThreads, 0, st, args);
   }
   if (e != cudaSuccess) return record_error(RA_ERR_CUDA, "extend attention launch: %s", cudaGetErrorString(e));
   return record_error(RA_OK, "%s", "");
