@@ -247,27 +247,27 @@ __global__ void __launch_bounds__(kPlanThreads, 1) extend_plan(const __grid_cons
 // 64 rows against tiles of 64 keys on the CUDA cores, 256 threads: thread (y, x) works out the scores
 // of rows 4y .. 4y+3 and keys x, x + 16, x + 32, x + 48, sixteen lanes have a row's scores, and of the
 // result rows 4y .. and the columns 4x .. 4x+3, and 64 + 4x .. What bounds it: 2 dh FMAs a row and key
-// and product; four FMAs a 16-byte word of shared memory.
-constexpr int kSimtThreads = 256, kSimtRows = 64, kSimtKeys = 64;
+// and product; eight FMAs a 16-byte word of shared memory. The next tile's keys come by asynchronous
+// copies meanwhile, their places in the table are looked up a tile earlier still; one barrier a tile.
+constexpr int kSimtThreads = 256, kSimtRows = 64, kSimtKeys = 64, kSimtPitchP = kSimtKeys + 4;
 __host__ __device__ constexpr int simt_pitch(int dh) { return (dh + 3) / 4 * 4 + 4; }
-constexpr int simt_smem(int dh) {
-  const int keys = kSimtKeys * simt_pitch(dh), weights = kSimtRows * (kSimtKeys + 4);
-  return (kSimtRows * simt_pitch(dh) + (keys > weights ? keys : weights) + keys) * 4;
-}
+// Q, two stages of K and V, the weights; floats. Two CTAs an SM for heads of up to 64.
+__host__ __device__ constexpr int simt_floats(int dh) { return (kSimtRows + 4 * kSimtKeys) * simt_pitch(dh) + kSimtRows * kSimtPitchP; }
+constexpr int simt_ctas(int dh) { return dh > 64 ? 1 : 2; }
 
 // COLS: groups of 64 columns of the head.
 template <int COLS>
-__global__ void __launch_bounds__(kSimtThreads, 2) extend_simt(const __grid_constant__ ExtArgs A, int vec) {
+__global__ void __launch_bounds__(kSimtThreads, COLS == 1 ? 2 : 1) extend_simt(const __grid_constant__ ExtArgs A, int vec) {
   extern __shared__ __align__(16) float sm[];
   __shared__ ExtItem sh_it;
-  __shared__ int64_t sh_at[kSimtKeys];  // of the tile's keys: where they are (-1: not read)
+  __shared__ int64_t sh_at[2][kSimtKeys];  // of a tile's keys: where they are (-1: not read)
   const int dh = A.dh, pitch = simt_pitch(dh), d4 = (dh + 3) / 4;
-  float* sq = sm;                                 // [64][pitch], times scale * log2(e)
-  float* sk = sm + kSimtRows * pitch;             // [64][pitch], then the weights [64][68]
-  float* sv = sm + simt_smem(dh) / 4 - kSimtKeys * pitch;
+  float* sq = sm;                                              // [64][pitch], times scale * log2(e)
+  float* stage = sm + kSimtRows * pitch;                       // [2][K, V][64][pitch]
+  float* weights = stage + 4 * kSimtKeys * pitch;              // [64][68]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, x = tid & 15, y = tid >> 4;
-  launch_dependents();
   wait_for_previous();
+  launch_dependents();
   ExtCursor<kExtMany> cur;
   bool more = false;
   if (warp == 0) more = cur.begin(A, blockIdx.x);
@@ -282,8 +282,9 @@ __global__ void __launch_bounds__(kSimtThreads, 2) extend_simt(const __grid_cons
     __syncthreads();
     const ExtItem it = sh_it;
     if (it.tiles == 0) break;
-    const int rows = it.ntok * A.hb;
-    // a row of 4 elements, of memory whose rows need not be aligned
+    const int rows = it.ntok * A.hb, j1 = it.j0 + it.tiles;
+    const int sinks = A.sh[kExtMany].window > 0 ? min(A.sh[kExtMany].sinks, it.end) : 0;
+    // a row's four elements, of memory whose rows need not be aligned
     auto copy_row4 = [&](const float* src, float* dst, int d, bool on, float mul) {
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (on) {
@@ -298,12 +299,45 @@ __global__ void __launch_bounds__(kSimtThreads, 2) extend_simt(const __grid_cons
       }
       *reinterpret_cast<float4*>(dst + d) = make_float4(v.x * mul, v.y * mul, v.z * mul, v.w * mul);
     };
+    // where the keys of walk index j are that some row sees, by the first threads; what is not seen is 0
+    auto look_up = [&](int j) {
+      if (tid >= kSimtKeys || j >= j1) return;
+      const int key = ext_tile(it.walk, j) * kSimtKeys + tid;
+      int64_t at = -1;
+      if (key < sinks || (key >= it.low && key < it.end)) {
+        const int page = key / A.page_size;
+        at = ext_page(A, it.seq, page, &g_status_extend) * A.page_stride +
+             static_cast<int64_t>(key - page * A.page_size) * A.slot_stride + it.hk * A.head_stride;
+      }
+      sh_at[j & 1][tid] = at;
+    };
+    auto load = [&](int j) {
+      if (j >= j1) return;
+      float* k = stage + (j & 1) * 2 * kSimtKeys * pitch;
+      float* v = k + kSimtKeys * pitch;
+      for (int i = tid; i < kSimtKeys * d4; i += kSimtThreads) {
+        const int r = i / d4, d = (i - r * d4) * 4;
+        const int64_t at = sh_at[j & 1][r];
+        if (vec && at >= 0) {
+          cp_async16(smem_u32(k + r * pitch + d), static_cast<const float*>(A.k_pages) + at + d);
+          cp_async16(smem_u32(v + r * pitch + d), static_cast<const float*>(A.v_pages) + at + d);
+        } else {
+          copy_row4(static_cast<const float*>(A.k_pages) + (at < 0 ? 0 : at), k + r * pitch, d, at >= 0, 1.f);
+          copy_row4(static_cast<const float*>(A.v_pages) + (at < 0 ? 0 : at), v + r * pitch, d, at >= 0, 1.f);
+        }
+      }
+    };
+    look_up(it.j0);
     for (int i = tid; i < kSimtRows * d4; i += kSimtThreads) {
       const int r = i / d4, d = (i - r * d4) * 4, tok = r / A.hb, h = r - tok * A.hb;
       const bool on = r < rows && h < it.heads;
       const int64_t at = static_cast<int64_t>(it.tok0 + tok) * A.hq + it.hk * A.group + it.g0 + h;
       copy_row4(static_cast<const float*>(A.q) + (on ? at * dh : 0), sq + r * pitch, d, on, A.scale_log2);
     }
+    __syncthreads();
+    load(it.j0);
+    cp_async_commit();
+    look_up(it.j0 + 1);
     int hi[4], lo[4];
     bool valid[4];
     float m[4], l[4], o[4][COLS][4];
@@ -320,109 +354,84 @@ __global__ void __launch_bounds__(kSimtThreads, 2) extend_simt(const __grid_cons
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[r][c][e] = 0.f;
     }
-    const bool idle = 8 * warp >= rows;  // a warp without rows helps with the copies only
-    for (int j = it.j0; j < it.j0 + it.tiles; ++j) {
-      const int k0 = ext_tile(it.walk, j) * kSimtKeys;
-      const int sinks = A.sh[kExtMany].window > 0 ? min(A.sh[kExtMany].sinks, it.end) : 0;
-      // keys that some row sees; the rest of the tile is 0
-      if (tid < kSimtKeys) {
-        const int key = k0 + tid;
-        int64_t at = -1;
-        if (key < sinks || (key >= it.low && key < it.end)) {
-          const int page = key / A.page_size;
-          at = ext_page(A, it.seq, page, &g_status_extend) * A.page_stride +
-               static_cast<int64_t>(key - page * A.page_size) * A.slot_stride + it.hk * A.head_stride;
-        }
-        sh_at[tid] = at;
-      }
-      __syncthreads();  // the tile before has been read
-      for (int i = tid; i < kSimtKeys * d4; i += kSimtThreads) {
-        const int r = i / d4, d = (i - r * d4) * 4;
-        const int64_t at = sh_at[r];
-        if (vec && at >= 0) {
-          cp_async16(smem_u32(sk + r * pitch + d), static_cast<const float*>(A.k_pages) + at + d);
-          cp_async16(smem_u32(sv + r * pitch + d), static_cast<const float*>(A.v_pages) + at + d);
-        } else {
-          copy_row4(static_cast<const float*>(A.k_pages) + (at < 0 ? 0 : at), sk + r * pitch, d, at >= 0, 1.f);
-          copy_row4(static_cast<const float*>(A.v_pages) + (at < 0 ? 0 : at), sv + r * pitch, d, at >= 0, 1.f);
-        }
-      }
-      cp_async_commit();
+    for (int j = it.j0; j < j1; ++j) {
       cp_async_wait<0>();
-      __syncthreads();
+      __syncthreads();  // tile j is there, everyone has done with the one before, and the next one's places are known
+      load(j + 1);
+      cp_async_commit();
+      look_up(j + 2);
+      if (8 * warp >= rows) continue;  // (a warp without rows helps with the copies only)
+      const int k0 = ext_tile(it.walk, j) * kSimtKeys;
+      const float* sk = stage + (j & 1) * 2 * kSimtKeys * pitch;
+      const float* sv = sk + kSimtKeys * pitch;
       float s[4][4] = {};
-      if (!idle) {
-        for (int d = 0; d < d4; ++d) {
-          float4 q[4], k[4];
+      for (int d = 0; d < d4; ++d) {
+        float4 q[4], k[4];
 #pragma unroll
-          for (int r = 0; r < 4; ++r) q[r] = *reinterpret_cast<const float4*>(sq + (4 * y + r) * pitch + 4 * d);
+        for (int r = 0; r < 4; ++r) q[r] = *reinterpret_cast<const float4*>(sq + (4 * y + r) * pitch + 4 * d);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) k[c] = *reinterpret_cast<const float4*>(sk + (x + 16 * c) * pitch + 4 * d);
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              s[r][c] += q[r].x * k[c].x;
-              s[r][c] += q[r].y * k[c].y;
-              s[r][c] += q[r].z * k[c].z;
-              s[r][c] += q[r].w * k[c].w;
-            }
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          float mx = m[r];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int key = k0 + x + 16 * c;
-            if (!(key < hi[r] && (key >= lo[r] || key < A.sh[kExtMany].sinks))) s[r][c] = -INFINITY;
-            mx = fmaxf(mx, s[r][c]);
-          }
-#pragma unroll
-          for (int w = 8; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-          const float ref = mx == -INFINITY ? 0.f : mx, alpha = exp2f(m[r] - ref);
-          float sum = 0.f;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            s[r][c] = exp2f(s[r][c] - ref);
-            sum += s[r][c];
-          }
-#pragma unroll
-          for (int w = 8; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-          m[r] = mx;
-          l[r] = l[r] * alpha + sum;
-#pragma unroll
-          for (int c = 0; c < COLS; ++c)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[r][c][e] *= alpha;
-        }
-      }
-      __syncthreads();  // the keys have been read: the weights go there
-      if (!idle) {
-        float* p = sk;
+        for (int c = 0; c < 4; ++c) k[c] = *reinterpret_cast<const float4*>(sk + (x + 16 * c) * pitch + 4 * d);
 #pragma unroll
         for (int r = 0; r < 4; ++r)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) p[(4 * y + r) * (kSimtKeys + 4) + x + 16 * c] = s[r][c];
-        __syncwarp();  // a row's weights are its own warp's
-        for (int k = 0; k < kSimtKeys; k += 4) {
-          float4 w[4];
+          for (int c = 0; c < 4; ++c) {
+            s[r][c] += q[r].x * k[c].x;
+            s[r][c] += q[r].y * k[c].y;
+            s[r][c] += q[r].z * k[c].z;
+            s[r][c] += q[r].w * k[c].w;
+          }
+      }
 #pragma unroll
-          for (int r = 0; r < 4; ++r) w[r] = *reinterpret_cast<const float4*>(p + (4 * y + r) * (kSimtKeys + 4) + k);
+      for (int r = 0; r < 4; ++r) {
+        float mx = m[r];
 #pragma unroll
-          for (int c = 0; c < COLS; ++c) {
-            const int d = 64 * c + 4 * x;
-            if (d >= 4 * d4) continue;
+        for (int c = 0; c < 4; ++c) {
+          const int key = k0 + x + 16 * c;
+          if (!(key < hi[r] && (key >= lo[r] || key < A.sh[kExtMany].sinks))) s[r][c] = -INFINITY;
+          mx = fmaxf(mx, s[r][c]);
+        }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float4 v = *reinterpret_cast<const float4*>(sv + (k + i) * pitch + d);
+        for (int w = 8; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+        const float ref = mx == -INFINITY ? 0.f : mx, alpha = exp2f(m[r] - ref);
+        float sum = 0.f;
 #pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                const float pw = i == 0 ? w[r].x : i == 1 ? w[r].y : i == 2 ? w[r].z : w[r].w;
-                o[r][c][0] += pw * v.x;
-                o[r][c][1] += pw * v.y;
-                o[r][c][2] += pw * v.z;
-                o[r][c][3] += pw * v.w;
-              }
+        for (int c = 0; c < 4; ++c) {
+          s[r][c] = exp2f(s[r][c] - ref);
+          sum += s[r][c];
+        }
+#pragma unroll
+        for (int w = 8; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+        m[r] = mx;
+        l[r] = l[r] * alpha + sum;
+#pragma unroll
+        for (int c = 0; c < COLS; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[r][c][e] *= alpha;
+      }
+      __syncwarp();  // the weights of the tile before have been read (a row's are its own warp's)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) weights[(4 * y + r) * kSimtPitchP + x + 16 * c] = s[r][c];
+      __syncwarp();
+      for (int k = 0; k < kSimtKeys; k += 4) {
+        float4 w[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) w[r] = *reinterpret_cast<const float4*>(weights + (4 * y + r) * kSimtPitchP + k);
+#pragma unroll
+        for (int c = 0; c < COLS; ++c) {
+          const int d = 64 * c + 4 * x;
+          if (d >= 4 * d4) continue;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 v = *reinterpret_cast<const float4*>(sv + (k + i) * pitch + d);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float pw = i == 0 ? w[r].x : i == 1 ? w[r].y : i == 2 ? w[r].z : w[r].w;
+              o[r][c][0] += pw * v.x;
+              o[r][c][1] += pw * v.y;
+              o[r][c][2] += pw * v.z;
+              o[r][c][3] += pw * v.w;
             }
           }
         }
@@ -448,7 +457,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) extend_simt(const __grid_cons
         else (it.dest == kExtRows ? A.row_ml : A.part[kExtMany].ml)[to] = make_float2(m[r], l[r]);
       }
     }
-    __syncthreads();
+    __syncthreads();  // the item, its rows and its last tile have been read
   }
 }
 
@@ -743,8 +752,10 @@ cudaError_t launch_extend_simt(ExtArgs& A, cudaStream_t st) {
                       reinterpret_cast<uintptr_t>(A.v_pages);
   int vec = p % 16 == 0 && A.dh % 4 == 0 && A.page_stride % 4 == 0 && A.slot_stride % 4 == 0 && A.head_stride % 4 == 0;
   const void* kernel = A.dh > 64 ? reinterpret_cast<const void*>(extend_simt<2>) : reinterpret_cast<const void*>(extend_simt<1>);
-  const int smem = simt_smem(A.dh);
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // (more than any head size needs, so that it is allowed once)
+  const int smem = simt_floats(A.dh) * 4;
+  static std::atomic<bool> done[2][kExtDevices];
+  const cudaError_t e = ext_allow_smem(kernel, simt_floats(A.dh > 64 ? 128 : 64) * 4, done[A.dh > 64 ? 1 : 0]);
   if (e != cudaSuccess) return e;
   void* args[] = {&A, &vec};
   return launch_after(kernel, dim3(A.part[kExtMany].most_ctas), kSimtThreads, smem, st, args);
@@ -799,7 +810,7 @@ Regions regions_of(const ra_paged_cache* c, int n_groups, int n_tokens, int hq) 
   head_blocks(hq / c->hkv, c->dtype == RA_BF16 ? 128 : kSimtRows, &hb, &blocks);
   const ExtShape s = shape_of(c->dtype, hb, 0, 0);
   Regions r;
-  r.ctas[kExtMany] = (c->dtype == RA_BF16 ? 1 : 2) * kExtSms;
+  r.ctas[kExtMany] = (c->dtype == RA_BF16 ? 1 : simt_ctas(c->head_dim)) * kExtSms;
   r.rows[kExtMany] = (n_tokens < s.bt ? n_tokens : s.bt) * hb;
   r.ctas[kExtFew] = c->dtype == RA_BF16 ? extend_few_ctas(c->head_dim) : 0;
   r.rows[kExtFew] = r.ctas[kExtFew] > 0 ? 16 : 0;
