@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++tiles;
         // values of keys that no row of the block sees: 0 (the other team's product with this tile
         // comes after this one's)
-        if ((!two || t == 0) && (k0 < it.low || k0 + 128 > it.end)) {
+        if ((!two || t == 0) && (k0 < it.low || it.end - k0 < 128)) {
           const TileKeys seen = tile_keys(A, it, j);
           if (!seen.whole()) {
             const int c = kv + n, st = c % C::kStages;
