@@ -464,10 +464,12 @@ __global__ void __launch_bounds__(kSimtThreads, COLS == 1 ? 2 : 1) extend_simt(c
 // ---------------------------------------------------------------- the join
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 
-// The parts of a block: CTAs c0 .. c1 of its class (c0 == c1: it is whole, in the row buffers).
+// The parts of a block: CTA c0 of its class, and c0 + skip + 1 .. c1 (c0 == c1: it is whole, in the row
+// buffers).
 struct Cut {
-  int c0, c1, cls;
+  int c0, skip, c1, cls;
   int tok0;  // token row of its first row
+  __device__ __forceinline__ int parts() const { return c1 - c0 - skip + 1; }
 };
 __device__ __forceinline__ Cut cut_of(const ExtArgs& A, const ExtHead& head, const ExtSeg& g, int pair, int blk) {
   const ExtShape& sh = A.sh[g.cls];
@@ -478,7 +480,9 @@ __device__ __forceinline__ Cut cut_of(const ExtArgs& A, const ExtHead& head, con
   c.cls = g.cls;
   c.tok0 = g.t0 + blk * sh.bt;
   c.c0 = ext_cta_of(units, ctas, base);
-  c.c1 = ext_cta_of(units, ctas, ext_tile_unit(sh, base, ext_weight(sh, g, blk), ext_walk(sh, g, blk).count - 1));
+  const int weight = ext_weight(sh, g, blk), count = ext_walk(sh, g, blk).count;
+  c.c1 = ext_cta_of(units, ctas, ext_tile_unit(sh, base, weight, count - 1));
+  c.skip = count < 2 ? 0 : max(0, ext_cta_of(units, ctas, ext_tile_unit(sh, base, weight, 1)) - c.c0 - 1);
   return c;
 }
 
@@ -525,7 +529,7 @@ __global__ void __launch_bounds__(kJoinThreads, BULK ? 2 : 4) extend_join(const 
     }
     if (blk >= 0 && lane < 3) {
       const ExtSeg g = A.segs[lo];
-      Cut c = {0, -1, 0, 0};
+      Cut c = {0, 0, -1, 0, 0};
       if (lane == 0 && g.units > 0) c = cut_of(A, head, g, pair, g.cls == kExtFew ? 0 : blk);
       if (lane > 0 && g.prefix >= 0) {
         const ExtSeg p = A.segs[g.prefix];
@@ -557,8 +561,8 @@ __global__ void __launch_bounds__(kJoinThreads, BULK ? 2 : 4) extend_join(const 
     w.h = r - w.tok * heads;
     w.at = static_cast<int64_t>(tok0 + w.tok) * A.hq + hk * A.group + g0 + w.h;
     w.pre = tok0 + w.tok - sh_cut[1].tok0 < A.sh[sh_cut[1].cls].bt ? 1 : 2;  // (without a prefix both are empty)
-    w.n0 = own.c1 - own.c0 + 1;
-    w.n = w.n0 + sh_cut[w.pre].c1 - sh_cut[w.pre].c0 + 1;
+    w.n0 = own.parts();
+    w.n = w.n0 + sh_cut[w.pre].parts();
     return w;
   };
   auto place = [&](const Row& w, int i, const float2** ml, const float** o) {
@@ -567,7 +571,7 @@ __global__ void __launch_bounds__(kJoinThreads, BULK ? 2 : 4) extend_join(const 
     if (!mine) i -= w.n0;
     const bool whole = c.c0 == c.c1, few = c.cls == kExtFew;
     const int64_t row = whole ? (mine ? static_cast<int64_t>(A.n_tokens) * A.hq : 0) + w.at
-                              : (static_cast<int64_t>(c.c0 + i) * 2 + (i == 0 ? 1 : 0)) * (few ? A.part[1].rows : A.part[0].rows) +
+                              : (static_cast<int64_t>(i == 0 ? c.c0 : c.c0 + c.skip + i) * 2 + (i == 0 ? 1 : 0)) * (few ? A.part[1].rows : A.part[0].rows) +
                                     (tok0 + w.tok - c.tok0) * A.hb + w.h;
     *ml = (whole ? A.row_ml : few ? A.part[1].ml : A.part[0].ml) + row;
     *o = (whole ? A.row_o : few ? A.part[1].o : A.part[0].o) + row * dh;
@@ -773,7 +777,15 @@ ExtShape shape_of(int dtype, int hb, int window, int sinks) {
   s.half = (dtype == RA_BF16 ? 128 : kSimtRows) / hb;
   s.bt = dtype == RA_BF16 ? 2 * s.half : s.half;
   s.wide = dtype == RA_BF16 ? 2 : 1;
-  s.lead = 1;
+  // what a block takes beside its tiles: its rows and first keys come from memory, its sums go there. bf16:
+  // about four whole tiles (16 questions of up to 300 tokens behind 16384 shared keys, 32/8 heads of 128,
+  // the prefix shared: 1287 us at 1 unit, 761 at 4, 661 at 8; 12 and 16 no faster). float32: little of a
+  // tile, which is ten times longer (16 sequences of up to 16 tokens, 16/16 heads of 64: 39 us at 0, 43 at 1,
+  // 45 at 2; a prompt of 695 tokens, 32/8 heads of 48: 111, 111 and 119).
+  s.lead = dtype == RA_BF16 ? 8 : 0;
+  // (8 prompts of up to 30 tokens, 32/8 heads of 128: 31 us at 2, 24 at 3, from 4 the same; one of 200 behind
+  // 500: 39, 39, 41 at 4, 45 at 8)
+  s.least = dtype == RA_BF16 ? 3 : 1;
   s.shift = dtype == RA_BF16 ? 7 : 6;
   s.window = window;
   s.sinks = sinks;
@@ -933,7 +945,7 @@ extern "C" int ra_paged_attn_extend(const ra_paged_cache* c, const ra_shared_pre
   head_blocks(A.group, c->dtype == RA_BF16 ? 128 : kSimtRows, &A.hb, &A.blocks_per_kv);
   A.sh[kExtMany] = shape_of(c->dtype, A.hb, window, window > 0 ? sinks : 0);
   A.few_rows = few_rows_of(c, cu_new == nullptr, n_tokens, hq);
-  A.sh[kExtFew] = {16, 16, 1, 1, 6, window, window > 0 ? sinks : 0};  // one block, tiles of 64 keys
+  A.sh[kExtFew] = {16, 16, 1, 1, 2, 6, window, window > 0 ? sinks : 0};  // one block, tiles of 64 keys
   const int sms = n_sm < kExtSms ? n_sm : kExtSms;
   A.scale_log2 = (scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(c->head_dim))) * 1.4426950408889634f;
   A.timeout_ns = kDefaultTimeoutNs;

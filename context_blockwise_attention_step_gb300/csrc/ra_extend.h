@@ -12,8 +12,8 @@
 // `half` tokens, else `wide` units, a block `lead` units more (its start and end, counted with its first
 // tile), and every CTA gets the same share of all units, in the order segment, pair (K/V head and
 // block of its query heads), block, tile. A tile belongs to the CTA that its first unit falls to; with
-// shares of lead + wide units at least, each CTA between the first and the last of a block has a tile
-// of it.
+// shares of `least` >= `wide` units, each CTA between that of a block's second tile and its last one's
+// has a tile of it. (Between the first tile's and the second's there can be some whose share is all lead.)
 //
 // Segments are of two classes, each with a kernel, a shape and shares of its own: those of few rows
 // (at most 16 a K/V head, all in one block), and the others.
@@ -30,6 +30,7 @@ struct ExtShape {
   int32_t bt, half;  // tokens of a block, and of one that costs one unit a tile
   int32_t wide;      // units of a tile of a larger block: 1 or 2
   int32_t lead;      // units of a block beside its tiles'
+  int32_t least;     // units of a CTA's share at least: `wide` or more
   int32_t shift;     // log2 of a tile's keys
   int32_t window, sinks;
 };
@@ -166,9 +167,8 @@ RA_HD int ext_block_of(const ExtShape& s, const ExtSeg& g, int64_t u) {
 
 // Shares: of `units` units CTA i of `ctas` has [ext_first(i), ext_first(i + 1)).
 RA_HD int ext_ctas(const ExtShape& s, int64_t units, int most) {
-  const int64_t least = s.wide + s.lead;
-  if (units >= most * least) return most;
-  const int64_t c = units / least;
+  if (units >= static_cast<int64_t>(most) * s.least) return most;
+  const int64_t c = units / s.least;
   return static_cast<int>(c < 1 ? (units > 0 ? 1 : 0) : c);
 }
 RA_HD int64_t ext_first(int64_t units, int ctas, int i) { return ext_div(units * i, ctas); }
@@ -187,16 +187,20 @@ RA_HD int ext_tile_from(const ExtShape& s, int64_t base, int weight, int count, 
   return j < count ? static_cast<int>(j) : count;
 }
 
-// Units a prefix of `tiles` key tiles costs a group's sequences, each by itself (w: the units of a tile
-// of their blocks) or together; whether to share it. Sharing leaves two float parts of every row in
-// memory, written and read once, about what six tiles of the row's block take.
+// The units that a tile of a prefix costs the blocks of n tokens, and whether to share a prefix of `tiles`
+// tiles that cost a group's sequences, each by itself, `apart` units a tile, and all together `together`.
+// Sharing leaves two float parts of every row in memory, written and read once, and makes two blocks of
+// one: it has to save a dozen tiles of the row's block. (us shared and apart, bf16, behind the tiles that
+// each of the blocks together saves: 32/8 heads of 128, 16 questions of up to 100 tokens behind 4096 keys, 9.9: 117 and 108; of 300 behind 16384,
+// 10: 661 and 615; 8 of 40 behind 16384, 107: 84 and 156. 8/8 heads of 64, 4 of 1000 behind 16384, 8.5: 209
+// and 207; 16 of 500, 21: 252 and 254; 8 of 40 behind 1024, 24: 38 and 43; 16 of 300, 39: 172 and 240.)
 RA_HD int64_t ext_block_units(const ExtShape& s, int64_t n) {
   if (n <= 0) return 0;
   const int64_t nb = (n - 1) / s.bt + 1;
   return (nb - 1) * s.wide + (n - (nb - 1) * s.bt > s.half ? s.wide : 1);
 }
 RA_HD bool ext_worth_sharing(int64_t tiles, int64_t apart, int64_t together) {
-  return tiles > 0 && tiles * (apart - together) > 6 * together;
+  return tiles > 0 && tiles * (apart - together) > 12 * together;
 }
 
 }  // namespace ra
