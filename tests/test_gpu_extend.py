@@ -188,6 +188,11 @@ SHARED = [
     (F32, 8, 2, 64, 16, [(5, 700), (3, 333)], [3, 40, 0, 7, 9, 5, 1, 1], None),
     (F32, 6, 1, 40, 7, [(4, 500)], [50, 20, 3, 9], [50, 12, 3, 1]),
     (F32, 16, 1, 128, 64, [(9, 600)], [2] * 9, None),
+    # several tokens each behind a prefix long enough to be shared
+    (BF16, 8, 2, 128, 64, [(6, 5000)], [50, 20, 3, 9, 60, 7], [50, 12, 3, 1, 40, 2]),
+    (BF16, 12, 4, 64, 32, [(3, 1700), (4, 2600)], [10, 30, 2, 9, 9, 9, 100], [10, 1, 2, 0, 9, 4, 90]),
+    (BF16, 4, 4, 64, 64, [(5, 6000)], [300, 257, 200, 9, 40], [300, 257, 100, 1, 40]),
+    (F32, 6, 1, 40, 7, [(6, 2000)], [12, 20, 3, 9, 5, 1], [12, 3, 1, 2, 5, 1]),
 ]
 
 
