@@ -166,7 +166,7 @@ class RingSelfAttention(torch.nn.Module):
 
     def _attend(self, q, k, v, prob, positions):
         """Norm, rotation and attention of shard-major q, k, v -> (out, the k that was attended to)."""
-        if self.q_norm is not None or self.rope is not None:
+        if self.q_norm is not None or self.rope is not None or positions is not None:
             q, k = qk_norm_rope(q, k, prob, self.q_norm, self.k_norm, self.rope, self.eps, positions)
         out, _ = ring_attention(q.contiguous(), k.contiguous(), v.contiguous(), prob, self.window, self.sinks)
         return out, k

@@ -164,6 +164,13 @@ def test_what_may_not_be_followed_is_recorded():
         ra.paged_attn_extend(b.q.transpose(0, 1).contiguous().transpose(0, 1), b.cache, b.seq_lens, b.cu_new)
 
 
+def test_layer_refuses_positions_without_axes():
+    x, at = torch.zeros(1, 64, 32, device="cuda", dtype=BF16), torch.zeros(1, 64, 2, device="cuda", dtype=torch.int32)
+    for kw in (dict(), dict(rope=ra.make_rope(64)), dict(qk_norm=True)):
+        with pytest.raises(ValueError):
+            ra.RingSelfAttention(32, 2, 1, 64, D=1, layout="basic", device="cuda", **kw)(x, at)
+
+
 def dense(b, rows, seq, first):
     """out and lse of some rows of sequence `seq`, in float64 on the GPU."""
     n = first + (rows.stop - rows.start)
