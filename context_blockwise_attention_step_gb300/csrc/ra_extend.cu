@@ -23,6 +23,7 @@
 namespace ra {
 
 static __device__ unsigned int g_status_extend;  // an index outside the cache
+static __device__ unsigned int g_status_plan;    // a plan that did not come
 
 namespace {
 
@@ -509,11 +510,13 @@ __global__ void __launch_bounds__(kJoinThreads, BULK ? 2 : 4) extend_join(const 
   __shared__ float sums[kJoinWarps][128], sum_l[kJoinWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, dh = A.dh, bt = A.sh[kExtMany].bt;
   const int pairs = A.hkv * A.blocks_per_kv, block = blockIdx.x / pairs, pair = blockIdx.x - block * pairs;
-  wait_for_previous();
+  // the block's parts by the plan, which is there when this kernel may start, then the results
   if (warp == 0) {
+    const bool planned = __all_sync(0xffffffffu, ext_acquire(A.head, A.timeout_ns, &g_status_plan));
     const ExtHead head = *A.head;
     int lo = A.n_groups, n = A.n_seqs, blk = -1;
-    if (A.cu_new == nullptr) {
+    if (!planned) {
+    } else if (A.cu_new == nullptr) {
       lo += block;  // a block is a sequence
       blk = 0;
     } else if (block < head.own_blocks) {
@@ -541,6 +544,7 @@ __global__ void __launch_bounds__(kJoinThreads, BULK ? 2 : 4) extend_join(const 
     }
     if (lane == 0) sh_blk = blk;
   }
+  wait_for_previous();  // in every block: what follows in the stream waits for this kernel alone
   __syncthreads();
   if (sh_blk < 0) return;
   const ExtSeg& g = sh_seg;
@@ -859,15 +863,17 @@ int check_extend(const ra_paged_cache* c, int n_groups, int n_tokens, int hq) {
 }  // namespace
 
 cudaError_t extend_status(unsigned int value[2], bool reset) {
-  unsigned int index = 0;
-  unsigned int few = 0;
+  unsigned int index = 0, plan = 0, few = 0;
   cudaError_t e = extend_tc_status(value, reset);
   if (e == cudaSuccess) e = extend_few_status(&few, reset);
   if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&index, g_status_extend, sizeof index);
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&plan, g_status_plan, sizeof plan);
   if (e == cudaSuccess && reset) {
     const unsigned int zero = 0;
     e = cudaMemcpyToSymbol(g_status_extend, &zero, sizeof zero);
+    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_status_plan, &zero, sizeof zero);
   }
+  value[0] |= plan;
   value[1] |= index | few;
   return e;
 }
@@ -945,7 +951,10 @@ extern "C" int ra_paged_attn_extend(const ra_paged_cache* c, const ra_shared_pre
   head_blocks(A.group, c->dtype == RA_BF16 ? 128 : kSimtRows, &A.hb, &A.blocks_per_kv);
   A.sh[kExtMany] = shape_of(c->dtype, A.hb, window, window > 0 ? sinks : 0);
   A.few_rows = few_rows_of(c, cu_new == nullptr, n_tokens, hq);
-  A.sh[kExtFew] = {16, 16, 1, 1, 2, 6, window, window > 0 ? sinks : 0};  // one block, tiles of 64 keys
+// one block, tiles of 64 keys; its start and end take about three of them (64 sequences of up to 4 new
+  // tokens and 8000 keys, 32/8 heads of 128: 250 us at 1, 225 at 2, 213 from 3 on; 100 of 2 and 3000,
+  // window 300: 37, 37, 39)
+  A.sh[kExtFew] = {16, 16, 1, 3, 2, 6, window, window > 0 ? sinks : 0};
   const int sms = n_sm < kExtSms ? n_sm : kExtSms;
   A.scale_log2 = (scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(c->head_dim))) * 1.4426950408889634f;
   A.timeout_ns = kDefaultTimeoutNs;

@@ -27,7 +27,8 @@ struct ExtHead {
 // need not wait for the other to end: it takes the SMs that the other leaves free. (The flag that it
 // reads first orders its reads of the plan behind the plan's writes.) It ends after the other has
 // ended, so that the join, which waits for its end, has both kernels' results. A kernel that is alone
-// waits for the plan.
+// waits for the plan. So the plan is there when the join may start, too: it finds its blocks' parts while
+// the last CTAs still work.
 __device__ __forceinline__ void ext_publish(ExtHead* h) {
   __threadfence();
   asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(&h->ready), "r"(1u) : "memory");
