@@ -40,13 +40,13 @@ FALLBACK_PEAKS = {"hbm_gbs": 6800.0, "bf16_tflops": 1900.0, "bf16_tflops_sustain
 # null until re-measured.
 TRAFFIC = {
     ("ring_bwd_tc (K/V-tile pass)", "long_s131072_gqa32x8_dh128_D16_zigzag"):
-        {"bytes": 54702025472 + 542446080, "source_sha": "1566ad716793696f"},
+        {"bytes": 55603560960 + 541387520, "source_sha": "9fc7ba99b74a32b4"},
     ("ring_fwd_tc", "long_s131072_gqa32x8_dh128_D16_zigzag"):
-        {"bytes": 119668151552 + 1258698496, "source_sha": "7ab6baf4dd53997c"},
+        {"bytes": 119212401920 + 1257649664, "source_sha": "ca4f86c8ac0036aa"},
     ("ring_bwd_dq_tc (dq pass)", "long_s131072_gqa32x8_dh128_D16_zigzag"):
-        {"bytes": 16150972416 + 1060189440, "source_sha": "3de0e3344efe6290"},
+        {"bytes": 16189123840 + 1059769600, "source_sha": "21c6c61076108643"},
     ("merge_kernel", "long_s131072_gqa32x8_dh128_D16_zigzag"):
-        {"bytes": 3256050432 + 2109006336, "source_sha": "407e400454aef449"},
+        {"bytes": 3255874304 + 2109215488, "source_sha": "603b14226947c0b3"},
 }
 
 

@@ -11,7 +11,9 @@
 // Three or four launches, each while the one before still runs (programmatic dependent launch): the
 // planning kernel reads the lengths and lists the segments (ra_extend.h); the main kernels, for many
 // rows (ra_extend_tc.cu, float32 here) and for few (ra_extend_few.cu), deal them out evenly to their
-// CTAs; the join works on the blocks that need it. The host need not know a length.
+// CTAs; the join works on the blocks that need it. The host need not know a length. By themselves the plan takes
+// 10-16 us (a chain of reads and of sums over the segments, one block), the join 10-15 us for decoding steps
+// and 42 where every CTA leaves two parts of 256 rows (38 MB).
 #include <cuda_bf16.h>
 
 #include <algorithm>

@@ -9,6 +9,10 @@
 // numbers (2^-16). What is added are masks by row: a row at position p sees the keys up to p, and
 // with a window those from p - window + 1 on and the first few. Keys that no row sees are not read.
 //
+// What bounds it: the start, about 6 us from the plan over the block table to the first keys, then memory: 33
+// sequences of up to 4 drafted tokens, window 1024 + 4, 8 heads of 64, 70 MB in 23 us; 64 sequences' own keys
+// behind a shared prefix, 32/8 heads of 128, 63 MB in 27 us.
+//
 // WIDE: more than 8 rows in some segment (else the second numbers of P take the product's empty rows).
 #include <cuda_bf16.h>
 

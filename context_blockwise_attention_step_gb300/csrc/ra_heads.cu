@@ -18,6 +18,8 @@
 // and angles stay in registers. 131072 tokens, 32/8 heads of 128, bf16, on GB300: forward 440 us
 // (6.10 TB/s), backward 669 us (6.02 TB/s); 16 prompts of up to 8192 tokens into a cache 260 us
 // (6.2 TB/s); 2 x 4096 tokens, 8 heads of 64: 11 and 16 us, four new tokens 4 us, which is latency.
+// Positions on three axes cost 12 bytes a token and a load beside each angle, of a line that is in L1: 1112
+// us forward and backward of the first (1109 by place), 267 us the second.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
