@@ -187,6 +187,19 @@ RA_HD int ext_tile_from(const ExtShape& s, int64_t base, int weight, int count, 
   return j < count ? static_cast<int>(j) : count;
 }
 
+// The CTAs that have tiles of a block: c0, and c0 + skip + 1 .. c1.
+struct ExtCtas {
+  int32_t c0, skip, c1;
+};
+RA_HD ExtCtas ext_ctas_of(const ExtShape& s, int64_t units, int ctas, int64_t base, int weight, int count) {
+  ExtCtas c;
+  c.c0 = ext_cta_of(units, ctas, base);
+  c.c1 = ext_cta_of(units, ctas, ext_tile_unit(s, base, weight, count - 1));
+  const int second = count < 2 ? c.c0 : ext_cta_of(units, ctas, ext_tile_unit(s, base, weight, 1));
+  c.skip = second > c.c0 ? second - c.c0 - 1 : 0;
+  return c;
+}
+
 // The units that a tile of a prefix costs the blocks of n tokens, and whether to share a prefix of `tiles`
 // tiles that cost a group's sequences, each by itself, `apart` units a tile, and all together `together`.
 // Sharing leaves two float parts of every row in memory, written and read once, and makes two blocks of

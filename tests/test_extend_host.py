@@ -105,10 +105,16 @@ int main() {
           if (ext_cta_of(units, ctas, ext_tile_unit(s, base, weight[i], j)) != c) bad("the CTA of a tile", s, seg, i);
         }
     }
-    for (int i = 0; i < nb; ++i) {
+    for (int64_t i = 0, base = 0; i < nb; base += ext_units(s, count[i], weight[i]), ++i) {
       if (static_cast<int>(owner[i].size()) != count[i]) bad("tiles without a CTA", s, seg, i);
       for (size_t j = 1; j < owner[i].size(); ++j)
         if (owner[i][j] < owner[i][j - 1] || (j > 1 && owner[i][j] > owner[i][j - 1] + 1)) bad("a CTA without a part", s, seg, i);
+      // the CTAs that the join looks for a block's parts at
+      const ExtCtas of = ext_ctas_of(s, units, ctas, base, weight[i], count[i]);
+      std::vector<int> at = {of.c0}, have = owner[i];
+      for (int c = of.c0 + of.skip + 1; c <= of.c1; ++c) at.push_back(c);
+      have.erase(std::unique(have.begin(), have.end()), have.end());
+      if (at != have) bad("the CTAs of a block", s, seg, static_cast<int>(i));
     }
   }
   // far positions: in 64 bits
