@@ -193,6 +193,10 @@ SHARED = [
     (BF16, 12, 4, 64, 32, [(3, 1700), (4, 2600)], [10, 30, 2, 9, 9, 9, 100], [10, 1, 2, 0, 9, 4, 90]),
     (BF16, 4, 4, 64, 64, [(5, 6000)], [300, 257, 200, 9, 40], [300, 257, 100, 1, 40]),
     (F32, 6, 1, 40, 7, [(6, 2000)], [12, 20, 3, 9, 5, 1], [12, 3, 1, 2, 5, 1]),
+    # more heads a K/V head than the kernel for few rows takes; more than rows of a tile
+    (BF16, 48, 1, 64, 64, [(5, 3000)], [12, 1, 3, 9, 70], [12, 1, 3, 2, 66]),
+    (BF16, 130, 1, 128, 32, [(4, 2500)], [2, 1, 3, 2], [2, 1, 3, 1]),
+    (BF16, 34, 2, 64, 64, [(7, 1000)], [2, 1, 0, 3, 2, 5, 1], None),
 ]
 
 
