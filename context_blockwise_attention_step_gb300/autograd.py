@@ -174,6 +174,8 @@ class RingSelfAttention(torch.nn.Module):
     def forward(self, x, positions=None):
         b, s, _ = x.shape
         prob = self.problem(b, s)
+        if positions is not None and positions.device != x.device:
+            raise ValueError(f"positions must be on {x.device}, where x is, got {positions.device}")
         q, k, v = self._qkv(x)
         if not self.shard_major:
             q, k, v = shard(q, prob), shard(k, prob), shard(v, prob)

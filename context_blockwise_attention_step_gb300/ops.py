@@ -216,9 +216,15 @@ def ring_attn_bwd_noalloc(dout, q, k, v, out, lse, prob: Problem, dq, dk, dv, st
     return dq, dk, dv
 
 
+def _on_gpu(x: torch.Tensor, out: torch.Tensor):
+    if not x.is_cuda or out.device != x.device:
+        raise ValueError(f"x and out must be on one CUDA device, got {x.device} and {out.device}")
+
+
 def shard_tokens(x: torch.Tensor, prob: Problem, out=None, stream=None):
     """Natural order -> shard-major (bit-exact copy)."""
     out = torch.empty_like(x) if out is None else out
+    _on_gpu(x, out)
     row_bytes = x.numel() * x.element_size() // prob.rows
     check(lib().ra_shard_tokens(prob.ptr, 0, _p(x), _p(out), row_bytes, _stream(stream)))
     return out
@@ -227,6 +233,7 @@ def shard_tokens(x: torch.Tensor, prob: Problem, out=None, stream=None):
 def unshard_tokens(x: torch.Tensor, prob: Problem, out=None, stream=None):
     """Shard-major -> natural order (bit-exact copy)."""
     out = torch.empty_like(x) if out is None else out
+    _on_gpu(x, out)
     row_bytes = x.numel() * x.element_size() // prob.rows
     check(lib().ra_shard_tokens(prob.ptr, 1, _p(x), _p(out), row_bytes, _stream(stream)))
     return out
