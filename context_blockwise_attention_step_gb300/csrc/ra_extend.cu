@@ -70,9 +70,13 @@ __global__ void __launch_bounds__(kPlanThreads, 1) extend_plan(const __grid_cons
   launch_dependents();
   if (tid == 0) A.head->ready = 0;
   auto class_of = [&](int n) { return n * int64_t(A.group) <= A.few_rows ? kExtFew : kExtMany; };
-  // groups, a warp each: whether the prefix lies before every new token, and whether sharing it pays
+  // groups, a warp each: whether the prefix lies before every new token, and whether sharing it pays.
+  // Offsets out of order or range share nothing in the whole call: groups that overlap would give a row
+  // two prefixes, whose results go to the same place.
+  bool disorder = false;
   for (int g = warp; g < A.n_groups; g += kPlanWarps) {
     const int b0 = bounded(A.cu_groups[g], A.n_seqs), b1 = bounded(A.cu_groups[g + 1], A.n_seqs);
+    disorder = disorder || b0 != A.cu_groups[g] || b1 != A.cu_groups[g + 1] || b0 > b1;
     const int64_t cap = static_cast<int64_t>(A.max_pages) * A.page_size;
     int p = A.prefix_lens[g];
     if (p > cap) p = static_cast<int>(cap);
@@ -112,7 +116,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) extend_plan(const __grid_cons
       if (g < kPlanThreads) group_keys[g] = e.k1;
     }
   }
-  __syncthreads();
+  disorder = __syncthreads_or(disorder);
+  if (disorder && tid == 0) atomicOr(&g_status_extend, 1u);
   // all segments in order, a thread each
   const int segs = A.n_groups + A.n_seqs, pairs = A.hkv * A.blocks_per_kv;
   int64_t done[2] = {0, 0};
@@ -123,6 +128,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) extend_plan(const __grid_cons
     int blocks = 0;
     if (i < A.n_groups) {
       e = A.segs[i];
+      if (disorder) e.units = 0;
     } else if (i < segs) {
       const int b = i - A.n_groups;
       const Tokens t = tokens_of(A, b);
@@ -134,7 +140,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) extend_plan(const __grid_cons
       e.seq = b;
       e.prefix = -1;
       e.cls = class_of(t.n);
-      if (A.n_groups > 0 && t.live) {
+      if (A.n_groups > 0 && t.live && !disorder) {
         int lo = 0, hi = A.n_groups - 1;  // the last group that begins at b or before
         while (lo < hi) {
           const int mid = (lo + hi + 1) >> 1;
