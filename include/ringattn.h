@@ -379,7 +379,7 @@ size_t ra_paged_workspace_bytes(const ra_paged_cache* c, int hq);
  * arrays, cu_groups [n_groups + 1] non-decreasing within 0 .. n_seqs, prefix_lens [n_groups].
  * Sharing changes how the keys are read, not the result: the whole key tiles (128 keys, in float32
  * 64) of a prefix are read once for the group, by the block table row of its first sequence that has
- * tokens, where that saves work, and where every sequence of the group has the prefix before its
+ * new tokens, where that saves work, and where every sequence of the group has the prefix before its
  * new tokens; else each sequence reads its own. Offsets that decrease or leave 0 .. n_seqs are
  * recorded in the device status (RA_ERR_CACHE_INDEX) where the call looks at them (a decoding step
  * over a small cache does not), and then nothing is shared. */
