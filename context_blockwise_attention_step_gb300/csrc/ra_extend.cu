@@ -83,21 +83,24 @@ __global__ void __launch_bounds__(kPlanThreads, 1) extend_plan(const __grid_cons
     const int tiles = p > 0 ? p >> s.shift : 0;
     int64_t apart = 0;
     int first = A.n_seqs, ok = 1;
+    int balance = 0;  // tokens of sequences of few rows, less the others
     for (int b = b0 + lane; b < b1; b += 32) {
       const Tokens t = tokens_of(A, b);
       if (t.bad) ok = 0;
       if (!t.live) continue;
       if (t.len - t.n < tiles << s.shift) ok = 0;
       apart += ext_block_units(s, t.n);
+      balance += ext_few(t.n, A.group) ? t.n : -t.n;
       first = min(first, b);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) apart += __shfl_xor_sync(0xffffffffu, apart, o);
     first = __reduce_min_sync(0xffffffffu, first);
     ok = __reduce_min_sync(0xffffffffu, ok);
+    balance = __reduce_add_sync(0xffffffffu, balance);
     if (lane == 0) {
       ExtSeg e = {};
-      e.shared = 1;
+      e.shared = balance >= 0 ? 2 : 1;
       e.prefix = -1;
       if (b0 < b1 && first < A.n_seqs && ok) {
         const Tokens a = tokens_of(A, b0), z = tokens_of(A, b1 - 1);
@@ -808,9 +811,9 @@ ExtShape shape_of(int dtype, int hb, int window, int sinks) {
 // sequences have no more than that on average and the kernel for 8 rows, which is faster, will do.
 int few_rows_of(const ra_paged_cache* c, bool decode, int n_tokens, int hq) {
   const int group = hq / c->hkv;
-  if (c->dtype != RA_BF16 || group > 16 || c->n_seqs == 0) return 0;
+  if (c->dtype != RA_BF16 || group > kExtFewRows || c->n_seqs == 0) return 0;
   const int64_t rows = (decode ? 1 : (static_cast<int64_t>(n_tokens) + c->n_seqs - 1) / c->n_seqs) * group;
-  return rows <= 8 ? 8 : 16;
+  return rows <= 8 ? 8 : kExtFewRows;
 }
 
 // One new token of every sequence, and so small a cache that the attention of one token (ra_decode.cu),

@@ -91,6 +91,7 @@ struct ExtItem {
   int32_t tok0, ntok, two;     // token row of the block's first row, tokens; more than `half`
   int32_t hk, g0, heads;       // K/V head, first query head of its group, heads
   int32_t base, shared;        // position of tok0; prefix: every row sees keys 0 .. end - 1
+  int32_t fine;                // the weights as two bf16 numbers (tensor-core kernel)
   int32_t low, end;            // keys of the block: low .. end - 1, and with a window sinks
   int32_t seq, dest, slot;     // kExtPart: which part; kExtRows: 0 prefix, 1 own
 };
@@ -138,6 +139,7 @@ struct ExtCursor {
         it.g0 = hblk * A.hb;
         it.heads = min(A.hb, A.group - it.g0);
         it.shared = g.shared;
+        it.fine = A.cu_new == nullptr || (g.shared ? g.shared == 2 : ext_few(g.n, A.group));
         it.base = g.base + a;
         it.low = g.shared ? 0 : static_cast<int>(ext_low(sh, g, blk));
         it.end = g.shared ? g.k1 : it.base + it.ntok;

@@ -25,6 +25,8 @@
 namespace ra {
 
 enum : int { kExtMany = 0, kExtFew = 1 };
+constexpr int kExtFewRows = 16;  // a K/V head
+RA_HD bool ext_few(int n, int group) { return n * static_cast<int64_t>(group) <= kExtFewRows; }
 
 struct ExtShape {
   int32_t bt, half;  // tokens of a block, and of one that costs one unit a tile
@@ -44,7 +46,7 @@ struct ExtSeg {
   int32_t seq;     // row of the block table
   int32_t blocks0; // own blocks before this segment
   int32_t prefix;  // own: the prefix segment that has the keys before k0, or -1
-  int32_t shared;  // 1: a prefix segment
+  int32_t shared;  // a prefix segment: 1, or 2 where at least half of its rows are of sequences with few rows
   int32_t cls;
 };
 

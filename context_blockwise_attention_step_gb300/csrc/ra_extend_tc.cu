@@ -23,18 +23,27 @@
 // Keys that no row of a block sees are not read, and their values in a tile are made 0 before the
 // product (what lies in a page behind a sequence's end may be NaN); their scores are masked.
 //
-// P is rounded to bf16, as in the ring's forward: the weights' errors, of up to 2^-8 each, partly average out over
-// the keys, and `out` is 0.0023 from the definition in relative L2, of which its own rounding is 0.0017.
+// P enters its product as one bf16 number, as in the ring's forward: the weights' errors, of up to 2^-8 each, partly
+// average out over the keys, and `out` is 0.0023 from the definition in relative L2, of which its own rounding is
+// 0.0017. Where the rows are few and the keys' bytes count, P goes in as two bf16 numbers (2^-16; a second product
+// with the same V), so that a step that is given shared prefixes is as exact as one that reads each sequence
+// apart with the kernel for few rows or the decode attention: in decoding steps, for sequences of at most 16 rows a K/V
+// head, and, in calls of no more than that a sequence on average, for prefixes of whose rows at least half are
+// of such sequences. (64 sequences' last tokens behind 32768 shared keys 38 us with one number, 48 with two. For
+// prefixes of many rows, which the products bound, one number: 16 questions of up to 300 tokens behind 16384, 8/8 heads
+// of 64, 184 us, and 274 with two.)
 //
 // What bounds it: a chunk of 4096 tokens behind 28672 others, 32/8 heads of 128, 1347 us, 1.53 PFLOP/s, 0.81
 // of the measured burst rate; the tensor pipe is active 66 % of the time, the softmax warps issue in 37 %
 // of the cycles, and neither hides the hand-over of S and P between them. 16 questions of up to 500
-// tokens behind 16384: 855 us, 0.75 (they leave half tiles). Where rows are few, a tile's latency counts: 64
-// sequences' last tokens behind 32768 shared keys 38 us for 135 MB, 14 tiles a CTA and 10 us of start and end.
+// tokens behind 16384: 864 us, 0.75 (they leave half tiles). Where rows are few, a tile's latency counts: 64
+// sequences' last tokens behind 32768 shared keys 48 us for 135 MB, 14 tiles a CTA and 10 us of start and end.
 //
 // Warp roles (384 threads, so that a thread may have 168 registers): 0 = TMA of Q and K (a lane a box), 3 =
 // TMA of V, 1 = TMEM and MMA, 2 = the walk over the pieces, four ahead of the others, 4-7 and 8-11 = the
 // softmax teams.
+#include <type_traits>
+
 #include "ra_extend.cuh"
 #include "ra_window.cuh"
 
@@ -58,8 +67,10 @@ struct Cfg {
   static constexpr int kSmemBytes = kOffV + kStages * kTileBytes + 1024;
   static constexpr int kKSteps = DH / 16;
   static constexpr uint32_t kTmemCols = 512;
-  // TMEM columns: S0 | S1 | O0 | O1 (P of team t overwrites the first 64 columns of S_t)
+  // TMEM columns: S0 | S1 | O0 | O1 (P of team t overwrites the first 64 columns of S_t, its second
+  // numbers the others)
   __device__ static constexpr uint32_t col_s(int t) { return t ? 128u : 0u; }
+  __device__ static constexpr uint32_t col_rest(int t) { return col_s(t) + 64u; }
   __device__ static constexpr uint32_t col_o(int t) { return t ? 256u + DH : 256u; }
 };
 
@@ -169,7 +180,9 @@ __device__ __forceinline__ void load_boxes(const ExtArgs& A, const Boxes& b, con
   }
 }
 
-template <int DH>
+// FINE: some pieces may want weights of two numbers. (This form is slower on pieces that do not: 16 questions of up to 500
+// tokens behind 16384 keys, 32/8 heads of 128, 909 us and 925, 8/8 heads of 64 behind 32768 420 and 456.)
+template <int DH, bool FINE>
 __global__ void __launch_bounds__(kThreads, 1)
     extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ ExtArgs A) {
@@ -309,63 +322,82 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(ok = wait(&sh.item_full[slot], (kq / kItems) & 1))) break;
       const int N = __shfl_sync(0xffffffffu, sh.item[slot].tiles, 0);
       const bool two = __shfl_sync(0xffffffffu, sh.item[slot].two, 0) != 0;
+      const bool fine = FINE && __shfl_sync(0xffffffffu, sh.item[slot].fine, 0) != 0;
       if (leader) mbar_arrive(&sh.item_empty[slot]);
       if (N == 0) break;
       for (int t = 0; t < (two ? 2 : 1) && ok; ++t) ok = wait(&sh.q_full[(qt + t) & 1], ((qt + t) >> 1) & 1);
       if (!ok) break;
       tc_fence_after();
-      // team t's k-th key tile is n; O_t(k-1) before S_t(k)
-      const int count0 = two ? N : (N + 1) / 2, count1 = two ? N : N / 2;
-      for (int k = 0; k <= count0 && ok; ++k) {
+      auto products = [&](auto with_rest) {
+        constexpr bool REST = decltype(with_rest)::value;
+        // team t's k-th key tile is n; O_t(k-1) before S_t(k)
+        const int count0 = two ? N : (N + 1) / 2, count1 = two ? N : N / 2;
+        for (int k = 0; k <= count0 && ok; ++k) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int count = t ? count1 : count0;
-          if (ok && k >= 1 && k - 1 < count) {
-            const int n = two ? k - 1 : 2 * (k - 1) + t, c = kv + n, st = c % C::kStages;
-            if (!two || t == 0) ok = wait(&sh.v_full[st], (c / C::kStages) & 1);
-            ok = ok && wait(&sh.p_part[t], p_phase[t]);
-            if (t == 0 && k == 1) {  // both accumulators have been read
-              ok = ok && wait(&sh.o_free, of_phase ^ 1);
-              of_phase ^= 1;
-            }
-            tc_fence_after();
-            if (ok && leader) {
-              const uint64_t dv = dV + st * (C::kTileBytes >> 4);
-#pragma unroll
-              for (int s = 0; s < 6; ++s)
-                mma_ts(base + C::col_o(t), base + C::col_s(t) + 8 * s, dv + s * (2048 >> 4), idO,
-                       (k > 1 || s > 0) ? 1u : 0u);
-            }
-            ok = ok && wait(&sh.p_full[t], p_phase[t]);
-            p_phase[t] ^= 1;
-            tc_fence_after();
-            if (ok && leader) {
-              const uint64_t dv = dV + st * (C::kTileBytes >> 4);
-#pragma unroll
-              for (int s = 6; s < 8; ++s)
-                mma_ts(base + C::col_o(t), base + C::col_s(t) + 8 * s, dv + s * (2048 >> 4), idO, 1u);
-              if (k == count) tc_commit(&sh.o_done[t]);
-              if (!two || t == 1) tc_commit(&sh.v_empty[st]);
-            }
-          }
-          if (ok && k < count) {
-            const int n = two ? k : 2 * k + t, c = kv + n, st = c % C::kStages;
-            if (!two || t == 0) ok = wait(&sh.k_full[st], (c / C::kStages) & 1);
-            tc_fence_after();
-            if (ok && leader) {
-              const int qs = (qt + (two ? t : 0)) & 1;
-              const uint64_t dq = dQ + qs * (C::kTileBytes >> 4), dk = dK + st * (C::kTileBytes >> 4);
-#pragma unroll
-              for (int s = 0; s < C::kKSteps; ++s) {
-                const int off = ((s >> 2) * kSubBytes + (s & 3) * 32) >> 4;
-                mma_ss(base + C::col_s(t), dq + off, dk + off, idS, s > 0);
+          for (int t = 0; t < 2; ++t) {
+            const int count = t ? count1 : count0;
+            if (ok && k >= 1 && k - 1 < count) {
+              const int n = two ? k - 1 : 2 * (k - 1) + t, c = kv + n, st = c % C::kStages;
+              if (!two || t == 0) ok = wait(&sh.v_full[st], (c / C::kStages) & 1);
+              ok = ok && wait(&sh.p_part[t], p_phase[t]);
+              if (t == 0 && k == 1) {  // both accumulators have been read
+                ok = ok && wait(&sh.o_free, of_phase ^ 1);
+                of_phase ^= 1;
               }
-              tc_commit(&sh.s_full[t]);
-              if (!two || t == 1) tc_commit(&sh.k_empty[st]);
-              if (two ? k == N - 1 : n == N - 1) tc_commit(&sh.q_empty[qs]);
+              tc_fence_after();
+              if (ok && leader) {
+                const uint64_t dv = dV + st * (C::kTileBytes >> 4);
+#pragma unroll
+                for (int s = 0; s < 6; ++s)
+                  mma_ts(base + C::col_o(t), base + C::col_s(t) + 8 * s, dv + s * (2048 >> 4), idO,
+                         (k > 1 || s > 0) ? 1u : 0u);
+                if constexpr (REST) {
+#pragma unroll
+                  for (int s = 0; s < 6; ++s)
+                    mma_ts(base + C::col_o(t), base + C::col_rest(t) + 8 * s, dv + s * (2048 >> 4), idO, 1u);
+                }
+              }
+              ok = ok && wait(&sh.p_full[t], p_phase[t]);
+              p_phase[t] ^= 1;
+              tc_fence_after();
+              if (ok && leader) {
+                const uint64_t dv = dV + st * (C::kTileBytes >> 4);
+#pragma unroll
+                for (int s = 6; s < 8; ++s)
+                  mma_ts(base + C::col_o(t), base + C::col_s(t) + 8 * s, dv + s * (2048 >> 4), idO, 1u);
+                if constexpr (REST) {
+#pragma unroll
+                  for (int s = 6; s < 8; ++s)
+                    mma_ts(base + C::col_o(t), base + C::col_rest(t) + 8 * s, dv + s * (2048 >> 4), idO, 1u);
+                }
+                if (k == count) tc_commit(&sh.o_done[t]);
+                if (!two || t == 1) tc_commit(&sh.v_empty[st]);
+              }
+            }
+            if (ok && k < count) {
+              const int n = two ? k : 2 * k + t, c = kv + n, st = c % C::kStages;
+              if (!two || t == 0) ok = wait(&sh.k_full[st], (c / C::kStages) & 1);
+              tc_fence_after();
+              if (ok && leader) {
+                const int qs = (qt + (two ? t : 0)) & 1;
+                const uint64_t dq = dQ + qs * (C::kTileBytes >> 4), dk = dK + st * (C::kTileBytes >> 4);
+#pragma unroll
+                for (int s = 0; s < C::kKSteps; ++s) {
+                  const int off = ((s >> 2) * kSubBytes + (s & 3) * 32) >> 4;
+                  mma_ss(base + C::col_s(t), dq + off, dk + off, idS, s > 0);
+                }
+                tc_commit(&sh.s_full[t]);
+                if (!two || t == 1) tc_commit(&sh.k_empty[st]);
+                if (two ? k == N - 1 : n == N - 1) tc_commit(&sh.q_empty[qs]);
+              }
             }
           }
         }
+      };
+      if constexpr (FINE) {
+        if (fine) products(std::true_type{}); else products(std::false_type{});
+      } else {
+        products(std::false_type{});
       }
       kv += N;
       qt += two ? 2 : 1;
@@ -483,29 +515,42 @@ __global__ void __launch_bounds__(kThreads, 1)
           // every exponential, then packing and the sums
           const uint64_t nm2 = f2(-mref, -mref);
           uint64_t la = f2(0.f, 0.f), lb = f2(0.f, 0.f);
+          auto weights = [&](auto with_rest) {
+            constexpr bool REST = decltype(with_rest)::value;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint64_t xv[16];
+            for (int c = 0; c < 4; ++c) {
+              uint64_t xv[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              xv[i] = fma2(f2(__uint_as_float(r[c][2 * i]), __uint_as_float(r[c][2 * i + 1])), sl2x2, nm2);
+              for (int i = 0; i < 16; ++i)
+                xv[i] = fma2(f2(__uint_as_float(r[c][2 * i]), __uint_as_float(r[c][2 * i + 1])), sl2x2, nm2);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float2 e = f2_split(xv[i]);
-              xv[i] = f2(ex2(e.x), ex2(e.y));
+              for (int i = 0; i < 16; ++i) {
+                const float2 e = f2_split(xv[i]);
+                xv[i] = f2(ex2(e.x), ex2(e.y));
+              }
+              uint32_t pk[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                if (i & 1) la = add2(la, xv[i]); else lb = add2(lb, xv[i]);
+                pk[i] = bf16x2_of(xv[i]);
+              }
+              tmem_st16(tS + 16 * c, pk);
+              if constexpr (REST) {  // what the rounding left
+#pragma unroll
+                for (int i = 0; i < 16; ++i) pk[i] = bf16x2_of(sub2(xv[i], f2_of_bf16x2(pk[i])));
+                tmem_st16(tS + 64 + 16 * c, pk);
+              }
+              if (c == 2) {  // the product with these keys may begin (2 % of the whole)
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(&sh.p_part[t]);
+              }
             }
-            uint32_t pk[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              if (i & 1) la = add2(la, xv[i]); else lb = add2(lb, xv[i]);
-              pk[i] = bf16x2_of(xv[i]);
-            }
-            tmem_st16(tS + 16 * c, pk);
-            if (c == 2) {  // the product with these keys may begin (2 % of the whole)
-              tmem_st_wait();
-              tc_fence_before();
-              mbar_arrive(&sh.p_part[t]);
-            }
+          };
+          if constexpr (FINE) {
+            if (it.fine) weights(std::true_type{}); else weights(std::false_type{});
+          } else {
+            weights(std::false_type{});
           }
           sum = add2(la, lb);
         } else {
@@ -613,10 +658,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   wait_for_previous();  // what follows in the stream waits for this kernel alone
 }
 
-template <int DH>
+template <int DH, bool FINE>
 cudaError_t launch(const ExtArgs& A, const ExtMaps& maps, cudaStream_t st) {
   using C = Cfg<DH>;
-  auto kernel = extend_tc_kernel<DH>;
+  auto kernel = extend_tc_kernel<DH, FINE>;
   static std::atomic<bool> done[kExtDevices];
   const cudaError_t e = ext_allow_smem(kernel, C::kSmemBytes, done);
   if (e != cudaSuccess) return e;
@@ -686,7 +731,9 @@ cudaError_t extend_tc_status(unsigned int value[2], bool reset) {
 }
 
 cudaError_t launch_extend_tc(const ExtArgs& A, const ExtMaps& maps, cudaStream_t st) {
-  return A.dh == 128 ? launch<128>(A, maps, st) : launch<64>(A, maps, st);
+  const bool fine = A.cu_new == nullptr || static_cast<int64_t>(A.n_tokens) * A.group <= static_cast<int64_t>(kExtFewRows) * A.n_seqs;
+  if (A.dh == 128) return fine ? launch<128, true>(A, maps, st) : launch<128, false>(A, maps, st);
+  return fine ? launch<64, true>(A, maps, st) : launch<64, false>(A, maps, st);
 }
 
 }  // namespace ra

@@ -395,7 +395,7 @@ def paged_attn_decode(q, cache: PagedCache, seq_lens, window: int = 0, sinks: in
     [n_seqs, hq, head_dim], lse [n_seqs, hq] float32 (natural log). With ``window`` > 0 only the
     last ``window`` and the first ``sinks`` of the seq_lens[b] keys are seen. A sequence of
     length 0 gets out = 0, lse = -inf. With ``shared`` the keys that groups of sequences have in
-    common are read once for the group. The workspace (``paged_workspace_bytes``, with ``shared``
+    common are read once for the group, as exactly as apart. The workspace (``paged_workspace_bytes``, with ``shared``
     ``paged_extend_workspace_bytes``) is allocated when not given."""
     if shared is not None:
         return paged_attn_extend(q, cache, seq_lens, None, shared, window, sinks, scale, out, lse, workspace, stream)
@@ -459,7 +459,8 @@ def paged_attn_extend(q, cache: PagedCache, seq_lens, cu_new=None, shared: Share
     are. Without ``cu_new`` every sequence has one new token, or is idle (length 0: out = 0, lse =
     -inf). The row at position p sees the keys k <= p, with ``window`` > 0 those with k > p -
     window or k < sinks. With ``shared`` (not with a window) the keys that groups of sequences have
-    in common are read once for the group where that saves work. The workspace
+    in common are read once for the group where that saves work. In bf16 the weights of rows that are few
+    are two bf16 numbers, of others one (include/ringattn.h has the rule). The workspace
     (``paged_extend_workspace_bytes``) is allocated when not given."""
     dt, dev = cache.dtype, cache.device_index
     if q.dim() != 3:

@@ -377,8 +377,8 @@ size_t ra_paged_workspace_bytes(const ra_paged_cache* c, int hq);
  * their keys and values there are equal; as a rule their rows of the block table name the same
  * pages. Sequences of no group, or with a prefix_lens of 0, share nothing. Both arrays are DEVICE
  * arrays, cu_groups [n_groups + 1] non-decreasing within 0 .. n_seqs, prefix_lens [n_groups].
- * Sharing changes how the keys are read, not the result: the whole key tiles (128 keys, in float32
- * 64) of a prefix are read once for the group, by the block table row of its first sequence that has
+ * Sharing changes how the keys are read, and the result by no more than its roundings (see
+ * ra_paged_attn_extend on the weights): the whole key tiles (128 keys, in float32 64) of a prefix are read once for the group, by the block table row of its first sequence that has
  * new tokens, where that saves work, and where every sequence of the group has the prefix before its
  * new tokens; else each sequence reads its own. Offsets that decrease or leave 0 .. n_seqs are
  * recorded in the device status (RA_ERR_CACHE_INDEX) where the call looks at them (a decoding step
@@ -403,10 +403,15 @@ typedef struct ra_shared_prefix {
  * 1/sqrt(head_dim). A sequence with more new tokens than its length, offsets that decrease or pass
  * n_tokens, or a page index outside the cache is recorded in the device status
  * (RA_ERR_CACHE_INDEX), and never followed. bf16 wants q, out and the pages 16-byte aligned, and
- * strides that are multiples of 8 elements. Run-to-run bit-identical. The workspace (device, >=
- * ra_paged_extend_workspace_bytes, 256-byte aligned) is overwritten; nothing in it is kept from
- * call to call, so calls and captured graphs may share it as long as they do not run at the same
- * time. */
+ * strides that are multiples of 8 elements. In bf16 the softmax's weights, float32 numbers, go into the
+ * product with v as two bf16 numbers (2^-16) in steps of one new token (cu_new NULL), for sequences of
+ * at most 16 rows (new tokens x query heads of a K/V head), and, in calls of at most 16 rows a sequence on
+ * average, for shared prefixes of whose rows at least half are of such sequences: out is then as far from
+ * the definition as its own rounding, 0.0017 in relative L2. Elsewhere they go in as one (2^-8, as in
+ * ra_ring_attn_fwd): 0.0023. Run-to-run
+ * bit-identical. The workspace (device, >= ra_paged_extend_workspace_bytes, 256-byte aligned) is
+ * overwritten; nothing in it is kept from call to call, so calls and captured graphs may share it as
+ * long as they do not run at the same time. */
 int ra_paged_attn_extend(const ra_paged_cache* c, const ra_shared_prefix* shared, int n_tokens, int hq,
                          float scale, int window, int sinks, const void* q, const int32_t* seq_lens,
                          const int32_t* cu_new, void* out, float* lse, void* workspace,
