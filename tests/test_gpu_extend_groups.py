@@ -54,3 +54,33 @@ def test_offsets_that_do_not_go_together_share_nothing(dtype, dh, news):
         ra.check_device_status()
     for cu in ([0, 0, 6, 6], [6, 6, 6, 6], [0, 3, 3, 6]):  # in order: groups may be empty, and need not be all
         check(b, b.run(shared=ra.SharedPrefix(ints(cu), ints([4000] * 3))), ref, str(cu))
+
+
+@pytest.mark.parametrize("dtype,dh,news", [(BF16, 64, None), (BF16, 64, [1, 3, 0, 2]), (F32, 8, [2, 1, 0, 1])], ids=str)
+def test_more_segments_than_the_plan_has_threads(dtype, dh, news):
+    """1500 sequences, 700 groups among them, of which every 50th has a prefix long enough to be shared: the
+    plan takes them in several rounds. Every 13th sequence is idle, or has no new token."""
+    tile = 128 if dtype == BF16 else 64
+    n, m = 1500, 700
+    groups = [(2, 14 * tile + 5 if i % 50 == 0 else tile + i % 40) for i in range(m)]
+    own = [0 if i % 13 == 5 and news is None else 5 + i % 7 for i in range(n)]
+    new = None if news is None else [0 if i % 13 == 5 else news[i % 4] for i in range(n)]
+    b = Prefixed(2, dtype, 4, 1, dh, 16, groups, own, new, lead=n - 2 * m, hide=False)
+    ref = b.reference()
+    got = b.run()
+    check(b, got, ref)
+    assert all(torch.equal(x, y) for x, y in zip(got, b.run()))
+    check(b, b.run(shared=None), ref, "apart")
+    one = ra.SharedPrefix(ints([0, 0] + [n] * 3), ints([7, 0, 0, 0]))  # groups of all, and of none
+    check(b, b.run(shared=one), ref, "one group")
+
+
+@pytest.mark.parametrize("dtype,dh", [(BF16, 128), (F32, 64)], ids=str)
+def test_no_new_tokens_at_all(dtype, dh):
+    """Offsets that give no sequence a row: nothing is written, and it is no error."""
+    b = Prefixed(3, dtype, 8, 2, dh, 16, [(3, 4000)], [5, 7, 9], [1, 2, 1])
+    out, lse = torch.full_like(b.q, 7.0), torch.full(b.q.shape[:2], 7.0, device="cuda")
+    for at in (0, 2, 4):
+        b.run(cu_new=ints([at] * 4), out=out, lse=lse)
+    assert ra.check_device_status() == _abi.RA_OK, ra.last_error()
+    assert (out == 7).all() and (lse == 7).all()
