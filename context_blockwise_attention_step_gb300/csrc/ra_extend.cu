@@ -13,7 +13,8 @@
 // rows (ra_extend_tc.cu, float32 here) and for few (ra_extend_few.cu), deal them out evenly to their
 // CTAs; the join works on the blocks that need it. The host need not know a length. By themselves the plan takes
 // 10-16 us (a chain of reads and of sums over the segments, one block), the join 10-15 us for decoding steps
-// and 42 where every CTA leaves two parts of 256 rows (38 MB).
+// and 42 where every CTA leaves two parts of 256 rows (38 MB). The plan grows with the sequences: a call of one
+// token each of 64, 512, 2048 and 8192 sequences of 100 keys, 8/1 heads of 64, takes 25, 29, 66 and 219 us.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -771,9 +772,8 @@ cudaError_t launch_extend_simt(ExtArgs& A, cudaStream_t st) {
                       reinterpret_cast<uintptr_t>(A.v_pages);
   int vec = p % 16 == 0 && A.dh % 4 == 0 && A.page_stride % 4 == 0 && A.slot_stride % 4 == 0 && A.head_stride % 4 == 0;
   const void* kernel = A.dh > 64 ? reinterpret_cast<const void*>(extend_simt<2>) : reinterpret_cast<const void*>(extend_simt<1>);
-  // (more than any head size needs, so that it is allowed once)
   const int smem = simt_floats(A.dh) * 4;
-  static std::atomic<bool> done[2][kExtDevices];
+  static std::atomic<bool> done[2][kExtDevices];  // (allowed once, for the largest head of each kernel)
   const cudaError_t e = ext_allow_smem(kernel, simt_floats(A.dh > 64 ? 128 : 64) * 4, done[A.dh > 64 ? 1 : 0]);
   if (e != cudaSuccess) return e;
   void* args[] = {&A, &vec};
@@ -818,9 +818,12 @@ int few_rows_of(const ra_paged_cache* c, bool decode, int n_tokens, int hq) {
 
 // One new token of every sequence, and so small a cache that the attention of one token (ra_decode.cu),
 // which reads every sequence's keys by itself and has half the launches, is faster, whatever the
-// sequences share. Measured with one prefix (32/8 heads of 128, bf16; us apart and shared): 16 sequences of
-// 2048 keys, 138 MB, 28 and 39; 16 of 4096, 273 MB, 39 and 37; 32 of 4096, 545 MB, 68 and 39. float32, 16/4
-// heads of 64: 32 of 2048, 138 MB, 39 and 45; 32 of 4096, 273 MB, 61 and 57.
+// sequences share. It is what the block table has room for that decides, as the lengths are on the
+// device: with a table much wider than the sequences are long, steps that would be faster apart are
+// not read apart. Measured with tables of the sequences' lengths and one prefix (us apart and shared), 32/8 heads of
+// 128, bf16: 16 sequences of 2048 keys, 138 MB, 28 and 39; 16 of 4096, 273 MB, 41 and 36; 32 of 4096,
+// 545 MB, 68 and 39. 8/8 heads of 64: 32 of 4096, 273 MB, 43 and 35. float32, 16/4 heads of 64: 32 of 2048, 138 MB,
+// 39 and 45; 32 of 4096, 273 MB, 61 and 51.
 bool read_apart(const ra_paged_cache* c) {
   const double keys = static_cast<double>(c->n_seqs) * c->max_pages * c->page_size;
   return keys * c->hkv * c->head_dim * (c->dtype == RA_BF16 ? 2 : 4) * 2 <= 256e6;
@@ -962,7 +965,7 @@ extern "C" int ra_paged_attn_extend(const ra_paged_cache* c, const ra_shared_pre
   head_blocks(A.group, c->dtype == RA_BF16 ? 128 : kSimtRows, &A.hb, &A.blocks_per_kv);
   A.sh[kExtMany] = shape_of(c->dtype, A.hb, window, window > 0 ? sinks : 0);
   A.few_rows = few_rows_of(c, cu_new == nullptr, n_tokens, hq);
-// one block, tiles of 64 keys; its start and end take about three of them (64 sequences of up to 4 new
+  // one block, tiles of 64 keys; its start and end take about three of them (64 sequences of up to 4 new
   // tokens and 8000 keys, 32/8 heads of 128: 250 us at 1, 225 at 2, 213 from 3 on; 100 of 2 and 3000,
   // window 300: 37, 37, 39)
   A.sh[kExtFew] = {16, 16, 1, 3, 2, 6, window, window > 0 ? sinks : 0};

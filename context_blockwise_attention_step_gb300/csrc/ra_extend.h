@@ -94,8 +94,9 @@ RA_HD ExtWalk ext_walk(const ExtShape& s, const ExtSeg& g, int i) {
   return w;
 }
 
-// sum over i < n of floor((a i + b) / 2^shift); a >= 1, b >= 0 (the Euclid-like reduction of a
-// floor sum: take out the whole parts, then count lattice points by the other axis)
+// sum over i < n of floor((a i + b) / 2^shift); a >= 1, b >= 0: take out the whole parts, then count the
+// lattice points below the line by the other axis, as Euclid's algorithm would go on (the reciprocity of
+// such sums: Graham, Knuth, Patashnik, Concrete Mathematics, section 3.5)
 RA_HD int64_t ext_floor_sum(int64_t n, int shift, int64_t a, int64_t b) {
   int64_t m = int64_t(1) << shift, sum = 0;
   while (n > 0) {
@@ -207,8 +208,8 @@ RA_HD ExtCtas ext_ctas_of(const ExtShape& s, int64_t units, int ctas, int64_t ba
 // Sharing leaves two float parts of every row in memory, written and read once, and makes two blocks of
 // one: it has to save a dozen tiles of the row's block. (us shared and apart, bf16, behind the tiles that
 // each of the blocks together saves: 32/8 heads of 128, 16 questions of up to 100 tokens behind 4096 keys, 9.9: 117 and 108; of 300 behind 16384,
-// 10: 661 and 615; 8 of 40 behind 16384, 107: 84 and 156. 8/8 heads of 64, 4 of 1000 behind 16384, 8.5: 209
-// and 207; 16 of 500, 21: 252 and 254; 8 of 40 behind 1024, 24: 38 and 43; 16 of 300, 39: 172 and 240.)
+// 10: 661 and 615; 8 of 40 behind 16384, 107: 84 and 154. 8/8 heads of 64, 4 of 1000 behind 16384, 8.5: 209
+// and 209; 16 of 500, 21: 252 and 258; 8 of 40 behind 1024, 24: 37 and 40; 16 of 300, 39: 186 and 236.)
 RA_HD int64_t ext_block_units(const ExtShape& s, int64_t n) {
   if (n <= 0) return 0;
   const int64_t nb = (n - 1) / s.bt + 1;

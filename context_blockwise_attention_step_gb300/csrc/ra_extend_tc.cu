@@ -36,7 +36,7 @@
 // What bounds it: a chunk of 4096 tokens behind 28672 others, 32/8 heads of 128, 1347 us, 1.53 PFLOP/s, 0.81
 // of the measured burst rate; the tensor pipe is active 66 % of the time, the softmax warps issue in 37 %
 // of the cycles, and neither hides the hand-over of S and P between them. 16 questions of up to 500
-// tokens behind 16384: 864 us, 0.75 (they leave half tiles). Where rows are few, a tile's latency counts: 64
+// tokens behind 16384: 855 us, 0.75 (they leave half tiles). Where rows are few, a tile's latency counts: 64
 // sequences' last tokens behind 32768 shared keys 48 us for 135 MB, 14 tiles a CTA and 10 us of start and end.
 //
 // Warp roles (384 threads, so that a thread may have 168 registers): 0 = TMA of Q and K (a lane a box), 3 =

@@ -86,7 +86,9 @@ def make_axis_rope(rotary_dim: int, axis, base: float = 10000.0, inv_freq=None,
 def axis_sections(sections, cyclic: bool = False) -> list:
     """The axis of every pair for ``make_axis_rope``: the first sections[0] pairs on axis 0, the next
     sections[1] on axis 1, and so on; or, ``cyclic``, the axes in turn (pair i on axis i % n as long
-    as that axis has pairs left by its section: i < n * sections[i % n], else on axis 0)."""
+    as that axis has pairs left by its section: i < n * sections[i % n], else on axis 0). The turns end
+    with the pairs: where a + n * (sections[a] - 1) is not below their number, axis a > 0 gets fewer than
+    its section ([10, 20, 20] gives 17, 17 and 16)."""
     sections = [int(x) for x in sections]
     n = len(sections)
     if not cyclic:

@@ -381,8 +381,9 @@ size_t ra_paged_workspace_bytes(const ra_paged_cache* c, int hq);
  * ra_paged_attn_extend on the weights): the whole key tiles (128 keys, in float32 64) of a prefix are read once for the group, by the block table row of its first sequence that has
  * new tokens, where that saves work, and where every sequence of the group has the prefix before its
  * new tokens; else each sequence reads its own. Offsets that decrease or leave 0 .. n_seqs are
- * recorded in the device status (RA_ERR_CACHE_INDEX) where the call looks at them (a decoding step
- * over a small cache does not), and then nothing is shared. */
+ * recorded in the device status (RA_ERR_CACHE_INDEX) where the call looks at them, and then nothing is
+ * shared. A decoding step over a cache whose block table has room for no more than 256 MB of keys and
+ * values (n_seqs * max_pages pages) does not look: it reads every sequence apart, which is faster. */
 typedef struct ra_shared_prefix {
   int32_t n_groups; /* <= n_seqs; 0: none */
   const int32_t* cu_groups;
